@@ -512,6 +512,190 @@ ds4a_status ds4a_compress_append(int32_t width, int32_t ratio, int32_t n_state, 
                                  int64_t state_row_stride, void *out, int64_t out_row_stride, ds4a_stream_t stream);
 
 /*
+ * Paged K/V rows of a batch of sequences, for a serving program that keeps
+ * many sequences of different lengths in one cache ([P2] "KV Cache Design":
+ * raw rows and compressed rows per layer; page 4 of the sources: serving many
+ * requests in parallel).  The rows live in a pool of n_pages pages of
+ * page_rows rows; a table names, per sequence, the page that holds its rows
+ * 0 .. page_rows-1, the page of its next page_rows rows, and so on:
+ *     row i of sequence b = page table[b][i / page_rows], slot i % page_rows
+ *     row s of page p at base + p * page_stride + s * row_stride (bytes).
+ * A table entry outside [0, n_pages) names no page: its rows are invisible to
+ * every call (weight 0), and are neither read nor written.  A page may appear
+ * in several tables, or twice in one, for calls that only read it.
+ * Rows that no token sees (pages of other sequences, the rest of a sequence's
+ * last page) are never read: they may hold anything.
+ *   k, v        fp16 [n_pages][page_rows][512], or E4M3 codes (uint8) when
+ *               scales are given; may be the same pool (one row serving as K
+ *               and V).  Strides as elsewhere: multiples of 16 bytes,
+ *               row_stride of at least a row, page_stride of at least
+ *               page_rows rows.
+ *   k_scale, v_scale  fp32 [n_pages][page_rows] row scales of an E4M3 pool in
+ *               the format of ds4a_quantize_kv_fp8 (finite, >= 0), or both
+ *               NULL: fp16 rows.
+ *   table       device int32 [n_seq][max_pages] at table_stride bytes per
+ *               sequence (a multiple of 4, >= 4 * max_pages).
+ *   max_pages   entries per sequence; max_pages == 0: a segment without rows
+ *               (the other fields are then ignored).
+ */
+typedef struct {
+  const void *k, *v;
+  int64_t row_stride, page_stride;
+  int32_t page_rows, n_pages;
+  const float *k_scale, *v_scale;
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t max_pages;
+} ds4a_paged_rows;
+
+/*
+ * ds4a_attn_decode_paged - one decode step for n_seq sequences, as
+ * ds4a_attn_decode_batch, over paged rows: sequence b's result is that of
+ * ds4a_attn_decode on its own layout and rows (rows of absent pages left
+ * out).  A sequence that sees no row gets o = 0 and lse = -inf.
+ *   shape       ratio, window and scale shared by the batch (other fields are
+ *               ignored).
+ *   seq_geom    device int32 [n_seq][4], 16-byte aligned: per sequence
+ *               (q_pos, n_raw, raw_pos0, n_comp); the row counts are clamped
+ *               to the rows the tables can name.  Read on the device.
+ *   X->raw, X->comp  the two segments.  Segments with rows have one format:
+ *               both fp16 or both E4M3.
+ *   X->q, X->o  fp16 [n_seq][64][512]; X->lse fp32 [n_seq][64] or NULL.
+ *   workspace   as in ds4a_attn_decode, of at least
+ *               ds4a_attn_decode_paged_workspace_size(n_seq) bytes (which
+ *               depends on the current device's SM count).
+ * The 128-row tiles of all sequences together are shared out evenly among the
+ * SMs, whatever the lengths; a sequence whose tiles fall to several SMs is
+ * joined by its log-sum-exps.  The same call gives the same bits every time.
+ */
+typedef struct {
+  const void *q;
+  int64_t q_seq_stride;
+  ds4a_paged_rows raw, comp;
+  void *o;
+  int64_t o_seq_stride;
+  float *lse;
+} ds4a_paged_batch;
+
+size_t ds4a_attn_decode_paged_workspace_size(int32_t n_seq);
+ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
+                                   const ds4a_paged_batch *X, void *workspace, size_t workspace_bytes,
+                                   ds4a_stream_t stream);
+
+/*
+ * ds4a_attn_weights_paged - the attention weight each compressed row received
+ * in a decode step, summed over the heads and added to what it received
+ * before (what an eviction policy ranks rows by):
+ *     out[b][c] = decay * weights[b][c] + sum_h exp(scale * q[b][h].k_c - lse[b][h])
+ * for the compressed rows c that sequence b's token sees (c < n_comp and
+ * (c + 1) * ratio <= q_pos + 1); other entries of out are left as they were.
+ * A row of an absent page, and every row where lse[b][h] = -inf, receives 0
+ * (from that head).  lse is the one ds4a_attn_decode_paged returned.
+ *   X           q, comp and lse (read here) are used; comp.v, X->raw, X->o are
+ *               ignored.
+ *   weights     fp32 [n_seq][max_pages * page_rows] at weight_stride bytes, or
+ *               NULL: all 0.
+ *   out         fp32, same shape, at out_stride bytes; may be weights itself
+ *               (same pointer and stride), else must not overlap an input.
+ *   decay       finite.
+ */
+ds4a_status ds4a_attn_weights_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
+                                    const ds4a_paged_batch *X, const float *weights, int64_t weight_stride,
+                                    float decay, float *out, int64_t out_stride, ds4a_stream_t stream);
+
+/*
+ * ds4a_evict_paged - keeps the n_keep compressed rows of each sequence that
+ * received the most attention weight, and closes the gaps.  Sequence b has
+ * n = n_comp rows (seq_geom, clamped to the table); n' = min(n, n_keep) stay.
+ *   Order: protected rows first, then larger weights; equal ranks go to the
+ *   lower slot.  A NaN weight ranks as -inf and -0 as +0.  Row j is protected
+ *   when its id is below n_first, or at least
+ *   floor((q_pos + 1) / ratio) - n_recent (its span is among the last
+ *   n_recent that have ended).  ids[b][j] is the span the row in slot j was
+ *   pooled from; without ids it is j.
+ *   Moves: kept rows in slots below n' stay where they are; the h-th freed
+ *   slot below n' takes the h-th kept row at or above n' (both in ascending
+ *   order).  So a call moves only as many rows as it has gaps to close; the
+ *   rows' order in the cache carries no meaning (their ids do).
+ *   K and V rows and, in an E4M3 pool, their scales are moved in place.  A
+ *   move from or to an absent page copies no row.  Slots n' .. n-1 keep what
+ *   they held.  The pages of these sequences must be theirs alone: each page
+ *   in one table, once.
+ *   rows        the compressed segment (k and v are written).
+ *   weights     fp32 [n_seq][max_pages * page_rows] at weight_stride bytes.
+ *   ids         int32, same shape, at id_stride bytes, or NULL.
+ *   n_keep      >= 1;  n_first, n_recent >= 0.
+ *   kept        int32 [n_seq][n_keep] out at kept_stride bytes: the former slot
+ *               of the row now in slot i < n', -1 from n' on.
+ *   weights_out, ids_out  what the rows now in slots < n' have (slots from n' on
+ *               are left as they were); each may be its input itself (same
+ *               pointer and stride) or NULL (weights_out: not wanted;
+ *               ids_out: required exactly when ids is given).
+ *   n_out       int32 out, n' of sequence b at byte b * n_out_stride (a multiple
+ *               of 4): &seq_geom[0][3] with stride 16 updates the geometry in
+ *               place.
+ *   workspace   256-byte aligned, at least ds4a_evict_paged_workspace_size()
+ *               bytes; need not be initialised; not shared by calls in flight
+ *               at the same time.
+ * All integer results are exact.
+ */
+size_t ds4a_evict_paged_workspace_size(int32_t n_seq, int32_t n_keep);
+ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
+                             const ds4a_paged_rows *rows, const float *weights, int64_t weight_stride,
+                             const int32_t *ids, int64_t id_stride, int32_t n_keep, int32_t n_first,
+                             int32_t n_recent, int32_t *kept, int64_t kept_stride, float *weights_out,
+                             int64_t weight_out_stride, int32_t *ids_out, int64_t id_out_stride, int32_t *n_out,
+                             int64_t n_out_stride, void *workspace, size_t workspace_bytes, ds4a_stream_t stream);
+
+/*
+ * ds4a_append_paged - writes new K/V rows into a pool, quantising them (the
+ * format of ds4a_quantize_kv_fp8, bit for bit) when it is an E4M3 pool.
+ *   rows        the pool (table, table_stride and max_pages are ignored).
+ *   k, v        fp16 [n][512] at new_row_stride bytes.  For a pool whose k and
+ *               v are the same, v may be NULL; if given it is ignored.
+ *   slots       device int32 [n], 4-byte aligned: row i goes to slot
+ *               slots[i] % page_rows of page slots[i] / page_rows.  Entries
+ *               outside the pool (such as -1: a padded batch) write nothing.
+ *               No slot may be named twice.
+ */
+ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void *k, const void *v,
+                              int64_t new_row_stride, const int32_t *slots, ds4a_stream_t stream);
+
+/*
+ * ds4a_rmsnorm_fp8 - root-mean-square norm of a row, with the residual's
+ * addition, quantised to E4M3 for the product that follows ([P2]
+ * "Whole-Model Graph Execution": Q/K/V projections with a fused RMS norm, and
+ * K/V rows quantised to FP8 before they are stored):
+ *     h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight,
+ *     code = E4M3(y * (448 / m)), scale = m / 448, m = the largest |y| of the group,
+ * the format of ds4a_quantize_kv_fp8 with a scale per `group` values (group
+ * 0: one per row).  h stays in fp32 for the norm and is rounded once into
+ * residual_out.  A group whose m is 0 (or below 2^-100) gets scale 0 and
+ * codes 0.
+ *   n, width    rows; values per row, a multiple of 8, 8 .. 32768.
+ *   x_fp32      0: x, residual and residual_out are fp16; 1: fp32.  Finite values.
+ *   x, residual, residual_out  [n][width] at their strides (multiples of 16
+ *               bytes), 16-byte aligned.  residual may be NULL (h = x);
+ *               residual_out is required with a residual, else must be NULL.
+ *               It may be x or residual itself (same pointer and stride).
+ *   weight      fp32 [width], 16-byte aligned.
+ *   eps         > 0 (a normal fp32 number), finite.
+ *   group       0, 32, 64, 128 or 256 (the last group of a row may be short).
+ *   codes       uint8 [n][width] at code_stride bytes (a multiple of 8), 8-byte
+ *               aligned, or NULL.
+ *   scales      fp32 [n][groups] at scale_stride bytes (a multiple of 4), 4-byte
+ *               aligned; NULL exactly when codes is.
+ *   y           fp16 [n][width] at y_stride bytes (a multiple of 16), 16-byte
+ *               aligned: y rounded to fp16; or NULL.  codes or y is given.
+ * Outputs must not overlap inputs (but for the above) nor each other.
+ */
+ds4a_status ds4a_rmsnorm_fp8(int32_t n, int32_t width, int32_t x_fp32, const void *x, int64_t x_stride,
+                             const void *residual, int64_t residual_stride, void *residual_out,
+                             int64_t residual_out_stride, const float *weight, float eps, int32_t group,
+                             uint8_t *codes, int64_t code_stride, float *scales, int64_t scale_stride, void *y,
+                             int64_t y_stride, ds4a_stream_t stream);
+
+/*
  * ds4a_device_status - synchronises `stream`, then reports the device error
  * word the kernels set when a bounded wait runs out (DS4A_ERR_TIMEOUT) or
  * DS4A_OK.  clear != 0 resets the word.  A CUDA error from the

@@ -12,7 +12,9 @@
 #include <new>
 
 #include "ds4a.h"
+#include "host.h"
 #include "internal.h"
+#include "paged_params.h"
 
 // Device error word: set by a kernel whose bounded wait ran out.  Its address
 // is looked up once per device and handed to the kernels as a parameter.
@@ -79,6 +81,8 @@ ds4a_status current_device(DeviceState **out) {
     if (d.supported) {
       DS4A_CUDA_TRY(ds4a::prepare_attn_kernel());
       DS4A_CUDA_TRY(ds4a::prepare_pair_kernel());
+      DS4A_CUDA_TRY(ds4a::prepare_paged_kernels());
+      DS4A_CUDA_TRY(ds4a::prepare_cache_kernels());
       DS4A_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void **>(&d.err), g_ds4a_device_error));
       DS4A_CUDA_TRY(cudaGetSymbolAddress(&d.scratch, g_decode_scratch));
       if (g_encode == nullptr) {
@@ -298,6 +302,25 @@ ds4a_status prefill_pairs(const ds4a_layout *L, const ds4a_tensors *X, DeviceSta
 }
 
 }  // namespace
+
+namespace ds4a {
+
+ds4a_status host_device(HostDevice *out) {
+  DeviceState *d = nullptr;
+  const ds4a_status st = current_device(&d);
+  if (st != DS4A_OK) return st;
+  out->sm_count = d->sm_count;
+  out->err = d->err;
+  return DS4A_OK;
+}
+
+ds4a_status host_launched(cudaError_t e) { return launched(e); }
+
+ds4a_status host_encode_q(CUtensorMap *m, const void *base, int n, int64_t stride) {
+  return encode_q_blocks(m, base, n, stride);
+}
+
+}  // namespace ds4a
 
 extern "C" {
 
@@ -1143,6 +1166,7 @@ ds4a_status ds4a_graph_begin(ds4a_stream_t stream) {
       DS4A_CUDA_TRY(ds4a::preload_aux_kernels());
       DS4A_CUDA_TRY(ds4a::preload_indexer_kernels());
       DS4A_CUDA_TRY(ds4a::preload_compressor_kernels());
+      DS4A_CUDA_TRY(ds4a::preload_norm_kernels());
       d->loaded = true;
     }
   }

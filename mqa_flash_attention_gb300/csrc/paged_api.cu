@@ -1,0 +1,390 @@
+// C ABI of the paged cache and of the norm (declared in include/ds4a.h):
+// argument checks, work splitting and launches.  No device memory is
+// allocated here; every buffer belongs to the caller.
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "ds4a.h"
+#include "host.h"
+#include "internal.h"
+#include "paged_params.h"
+
+namespace {
+
+using ds4a::HostDevice;
+using ds4a::PagedSeg;
+
+constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
+constexpr int64_t kMostBytes = 1LL << 39;  // of any stride
+constexpr int32_t kMostRows = 1 << 30;     // rows of a sequence
+
+cudaStream_t as_cuda(ds4a_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool stride_ok(int64_t s, int64_t least, int64_t step) { return s >= least && s % step == 0 && s < kMostBytes; }
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Byte range [lo, hi) of `rows` rows of `row_bytes` at `stride`.
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span(const void *p, int64_t rows, int64_t stride, int64_t row_bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Span{lo, p != nullptr && rows > 0 ? lo + (uintptr_t)((rows - 1) * stride + row_bytes) : lo};
+}
+bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+// A written range against one read: the same range at the same stride, or apart.
+bool same_or_apart(Span a, int64_t stride_a, Span b, int64_t stride_b) {
+  return !meet(a, b) || (a.lo == b.lo && stride_a == stride_b);
+}
+
+bool has_rows(const ds4a_paged_rows *r) { return r->max_pages > 0; }
+
+// The pool of a segment (not its table).
+bool pool_ok(const ds4a_paged_rows *r, bool need_v) {
+  const bool e4m3 = r->k_scale != nullptr || r->v_scale != nullptr;
+  const int64_t row = e4m3 ? DS4A_HEAD_DIM : DS4A_ROW_BYTES;
+  if (r->page_rows < 1 || r->n_pages < 1 || r->page_rows > kMostRows) return false;
+  if (r->k == nullptr || !aligned(r->k, 16)) return false;
+  if (need_v && (r->v == nullptr || !aligned(r->v, 16))) return false;
+  if (!stride_ok(r->row_stride, row, 16)) return false;
+  // A page's rows lie within the page.
+  if (r->page_stride % 16 != 0 || r->page_stride >= kMostBytes ||
+      r->page_stride < (int64_t)(r->page_rows - 1) * r->row_stride + row)
+    return false;
+  if (e4m3 && (r->k_scale == nullptr || !aligned(r->k_scale, 4))) return false;
+  if (e4m3 && need_v && (r->v_scale == nullptr || !aligned(r->v_scale, 4))) return false;
+  return true;
+}
+
+bool table_ok(const ds4a_paged_rows *r) {
+  if (r->table == nullptr || !aligned(r->table, 4)) return false;
+  if (!stride_ok(r->table_stride, 4LL * r->max_pages, 4)) return false;
+  return (int64_t)r->max_pages * r->page_rows <= kMostRows;
+}
+
+PagedSeg seg_of(const ds4a_paged_rows *r) {
+  PagedSeg s;
+  std::memset(&s, 0, sizeof(s));
+  s.page_rows = 1;
+  s.k = static_cast<const uint8_t *>(r->k);
+  s.v = static_cast<const uint8_t *>(r->v);
+  s.row_stride = r->row_stride;
+  s.page_stride = r->page_stride;
+  s.page_rows = r->page_rows;
+  s.n_pages = r->n_pages;
+  s.k_scale = r->k_scale;
+  s.v_scale = r->v_scale;
+  s.table = r->table;
+  s.table_stride = r->table_stride / 4;
+  s.max_rows = r->max_pages * r->page_rows;
+  return s;
+}
+
+PagedSeg no_rows() {
+  PagedSeg s;
+  std::memset(&s, 0, sizeof(s));
+  s.page_rows = 1;
+  return s;
+}
+
+ds4a_status check_batch(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom) {
+  if (shape->window < 1 || !std::isfinite(shape->scale) || shape->ratio < 1) return DS4A_ERR_INVALID_ARG;
+  if (seq_geom == nullptr || !aligned(seq_geom, 16)) return DS4A_ERR_INVALID_ARG;
+  return n_seq > (1 << 20) ? DS4A_ERR_INVALID_ARG : DS4A_OK;
+}
+
+bool q_ok(const void *q, int64_t stride) {
+  return q != nullptr && aligned(q, 16) && stride_ok(stride, 64LL * DS4A_ROW_BYTES, 16);
+}
+
+int64_t tiles_of(int64_t rows) { return (rows + 127) / 128; }
+
+// CTAs a decode step of n_seq sequences may use.
+int decode_ctas(int sm_count) { return sm_count; }
+
+size_t decode_workspace(int32_t n_seq, int ctas) {
+  const size_t slots = (size_t)n_seq + ctas;
+  return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(__half) + sizeof(float2)) + (size_t)n_seq * sizeof(int2);
+}
+
+int device_sms() {
+  int sms = 152, dev = -1, v = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+    sms = v;
+  return sms;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ds4a_attn_decode_paged_workspace_size(int32_t n_seq) {
+  if (n_seq <= 0) return 0;
+  return decode_workspace(n_seq, decode_ctas(device_sms()));
+}
+
+ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
+                                   const ds4a_paged_batch *X, void *workspace, size_t workspace_bytes,
+                                   ds4a_stream_t stream) {
+  if (n_seq < 0 || shape == nullptr || X == nullptr) return DS4A_ERR_INVALID_ARG;
+  if (n_seq == 0) return DS4A_OK;
+  ds4a_status st = check_batch(n_seq, shape, seq_geom);
+  if (st != DS4A_OK) return st;
+  if (!q_ok(X->q, X->q_seq_stride) || !q_ok(X->o, X->o_seq_stride)) return DS4A_ERR_INVALID_ARG;
+  if (X->lse != nullptr && !aligned(X->lse, 4)) return DS4A_ERR_INVALID_ARG;
+  bool e4m3 = false, any = false;
+  int64_t most = 0;  // rows a token can see
+  for (const ds4a_paged_rows *r : {&X->raw, &X->comp}) {
+    if (r->max_pages < 0) return DS4A_ERR_INVALID_ARG;
+    if (!has_rows(r)) continue;
+    if (!pool_ok(r, true) || !table_ok(r)) return DS4A_ERR_INVALID_ARG;
+    const bool f8 = r->k_scale != nullptr;
+    if (any && f8 != e4m3) return DS4A_ERR_INVALID_ARG;  // one format for both segments
+    e4m3 = f8;
+    any = true;
+    const int64_t rows = (int64_t)r->max_pages * r->page_rows;
+    most += r == &X->raw && rows > shape->window ? shape->window : rows;
+  }
+  const int64_t tiles = n_seq * tiles_of(most);
+  if (tiles > (1 << 29)) return DS4A_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < ds4a_attn_decode_paged_workspace_size(n_seq))
+    return DS4A_ERR_WORKSPACE;
+  HostDevice d;
+  st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::PagedAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = ds4a::host_encode_q(&p.tm_q, X->q, n_seq, X->q_seq_stride);
+  if (st != DS4A_OK) return st;
+  p.seg[0] = has_rows(&X->raw) ? seg_of(&X->raw) : no_rows();
+  p.seg[1] = has_rows(&X->comp) ? seg_of(&X->comp) : no_rows();
+  p.geom = reinterpret_cast<const int4 *>(seq_geom);
+  p.n_seq = n_seq;
+  p.ratio = shape->ratio;
+  p.window = shape->window;
+  p.scale_log2 = shape->scale * 1.4426950408889634f;
+  p.o = static_cast<__half *>(X->o);
+  p.o_stride = X->o_seq_stride / 2;
+  p.lse = X->lse;
+  const int ctas = decode_ctas(d.sm_count);
+  const size_t slots = (size_t)n_seq + ctas;
+  p.ws_o = static_cast<__half *>(workspace);
+  p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + slots * DS4A_HEADS * DS4A_HEAD_DIM);
+  p.ws_plan = reinterpret_cast<int2 *>(p.ws_ml + slots * DS4A_HEADS);
+  p.timeout_ns = kTimeoutNs;
+  p.err = d.err;
+  const int grid = (int)(tiles < 1 ? 1 : tiles < ctas ? tiles : ctas);
+  st = ds4a::host_launched(ds4a::launch_paged_decode(p, e4m3, grid, as_cuda(stream)));
+  if (st != DS4A_OK) return st;
+  return ds4a::host_launched(ds4a::launch_paged_merge(p, as_cuda(stream)));
+}
+
+ds4a_status ds4a_attn_weights_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
+                                    const ds4a_paged_batch *X, const float *weights, int64_t weight_stride,
+                                    float decay, float *out, int64_t out_stride, ds4a_stream_t stream) {
+  if (n_seq < 0 || shape == nullptr || X == nullptr) return DS4A_ERR_INVALID_ARG;
+  if (n_seq == 0) return DS4A_OK;
+  ds4a_status st = check_batch(n_seq, shape, seq_geom);
+  if (st != DS4A_OK) return st;
+  if (!std::isfinite(decay) || X->comp.max_pages < 0) return DS4A_ERR_INVALID_ARG;
+  if (!has_rows(&X->comp)) return DS4A_OK;
+  if (!q_ok(X->q, X->q_seq_stride) || X->lse == nullptr || !aligned(X->lse, 4)) return DS4A_ERR_INVALID_ARG;
+  ds4a_paged_rows rows = X->comp;
+  rows.v = rows.k;
+  rows.v_scale = rows.k_scale;
+  if (!pool_ok(&rows, false) || !table_ok(&rows)) return DS4A_ERR_INVALID_ARG;
+  const int64_t cols = (int64_t)rows.max_pages * rows.page_rows;
+  if (out == nullptr || !aligned(out, 4) || !stride_ok(out_stride, 4 * cols, 4)) return DS4A_ERR_INVALID_ARG;
+  if (weights != nullptr) {
+    if (!aligned(weights, 4) || !stride_ok(weight_stride, 4 * cols, 4)) return DS4A_ERR_INVALID_ARG;
+    if (!same_or_apart(span(out, n_seq, out_stride, 4 * cols), out_stride,
+                       span(weights, n_seq, weight_stride, 4 * cols), weight_stride))
+      return DS4A_ERR_INVALID_ARG;
+  }
+  const int64_t tiles = n_seq * tiles_of(cols);
+  if (tiles > (1 << 29)) return DS4A_ERR_INVALID_ARG;
+  HostDevice d;
+  st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::PagedAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = ds4a::host_encode_q(&p.tm_q, X->q, n_seq, X->q_seq_stride);
+  if (st != DS4A_OK) return st;
+  p.seg[0] = no_rows();
+  p.seg[1] = seg_of(&rows);
+  p.geom = reinterpret_cast<const int4 *>(seq_geom);
+  p.n_seq = n_seq;
+  p.ratio = shape->ratio;
+  p.window = shape->window;
+  p.scale_log2 = shape->scale * 1.4426950408889634f;
+  p.lse_in = X->lse;
+  p.acc_in = weights;
+  p.acc_in_stride = weights != nullptr ? weight_stride / 4 : 0;
+  p.acc_out = out;
+  p.acc_out_stride = out_stride / 4;
+  p.decay = decay;
+  p.timeout_ns = kTimeoutNs;
+  p.err = d.err;
+  const int grid = (int)(tiles < d.sm_count ? tiles : d.sm_count);
+  return ds4a::host_launched(ds4a::launch_paged_weights(p, rows.k_scale != nullptr, grid, as_cuda(stream)));
+}
+
+size_t ds4a_evict_paged_workspace_size(int32_t n_seq, int32_t n_keep) {
+  if (n_seq <= 0 || n_keep <= 0) return 0;
+  return align256(4 * (size_t)n_seq) + 8 * (size_t)n_seq * (size_t)n_keep;
+}
+
+ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
+                             const ds4a_paged_rows *rows, const float *weights, int64_t weight_stride,
+                             const int32_t *ids, int64_t id_stride, int32_t n_keep, int32_t n_first,
+                             int32_t n_recent, int32_t *kept, int64_t kept_stride, float *weights_out,
+                             int64_t weight_out_stride, int32_t *ids_out, int64_t id_out_stride, int32_t *n_out,
+                             int64_t n_out_stride, void *workspace, size_t workspace_bytes, ds4a_stream_t stream) {
+  if (n_seq < 0 || shape == nullptr || rows == nullptr) return DS4A_ERR_INVALID_ARG;
+  if (n_seq == 0) return DS4A_OK;
+  if (n_keep < 1 || n_keep > kMostRows || n_first < 0 || n_recent < 0 || shape->ratio < 1 || n_seq > (1 << 20))
+    return DS4A_ERR_INVALID_ARG;
+  if (seq_geom == nullptr || !aligned(seq_geom, 16)) return DS4A_ERR_INVALID_ARG;
+  if (rows->max_pages < 1 || !pool_ok(rows, true) || !table_ok(rows)) return DS4A_ERR_INVALID_ARG;
+  const int64_t cols = (int64_t)rows->max_pages * rows->page_rows;
+  if (weights == nullptr || !aligned(weights, 4) || !stride_ok(weight_stride, 4 * cols, 4))
+    return DS4A_ERR_INVALID_ARG;
+  if ((ids == nullptr) != (ids_out == nullptr)) return DS4A_ERR_INVALID_ARG;
+  if (kept == nullptr || !aligned(kept, 4) || !stride_ok(kept_stride, 4LL * n_keep, 4)) return DS4A_ERR_INVALID_ARG;
+  if (n_out == nullptr || !aligned(n_out, 4) || !stride_ok(n_out_stride, 4, 4)) return DS4A_ERR_INVALID_ARG;
+  const Span in_w = span(weights, n_seq, weight_stride, 4 * cols);
+  if (weights_out != nullptr &&
+      (!aligned(weights_out, 4) || !stride_ok(weight_out_stride, 4 * cols, 4) ||
+       !same_or_apart(span(weights_out, n_seq, weight_out_stride, 4 * cols), weight_out_stride, in_w, weight_stride)))
+    return DS4A_ERR_INVALID_ARG;
+  if (ids != nullptr &&
+      (!aligned(ids, 4) || !stride_ok(id_stride, 4 * cols, 4) || !aligned(ids_out, 4) ||
+       !stride_ok(id_out_stride, 4 * cols, 4) ||
+       !same_or_apart(span(ids_out, n_seq, id_out_stride, 4 * cols), id_out_stride,
+                      span(ids, n_seq, id_stride, 4 * cols), id_stride)))
+    return DS4A_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < ds4a_evict_paged_workspace_size(n_seq, n_keep))
+    return DS4A_ERR_WORKSPACE;
+  if (n_seq * ((cols + 7) / 8) > INT32_MAX) return DS4A_ERR_INVALID_ARG;  // blocks of the move kernel
+  HostDevice d;
+  const ds4a_status st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::EvictParams p;
+  p.geom = reinterpret_cast<const int4 *>(seq_geom);
+  p.n_seq = n_seq;
+  p.ratio = shape->ratio;
+  p.rows = seg_of(rows);
+  p.weights = weights;
+  p.weight_stride = weight_stride / 4;
+  p.ids = ids;
+  p.id_stride = ids != nullptr ? id_stride / 4 : 0;
+  p.n_keep = n_keep;
+  p.n_first = n_first;
+  p.n_recent = n_recent;
+  p.kept = kept;
+  p.kept_stride = kept_stride / 4;
+  p.weights_out = weights_out;
+  p.weight_out_stride = weights_out != nullptr ? weight_out_stride / 4 : 0;
+  p.ids_out = ids_out;
+  p.id_out_stride = ids_out != nullptr ? id_out_stride / 4 : 0;
+  p.n_out = reinterpret_cast<uint8_t *>(n_out);
+  p.n_out_stride = n_out_stride;
+  p.n_moves = static_cast<int32_t *>(workspace);
+  p.from = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + align256(4 * (size_t)n_seq));
+  p.to = p.from + (size_t)n_seq * n_keep;
+  p.cached = ds4a::evict_cached_keys(p.rows.max_rows, ds4a::evict_cluster(p.rows.max_rows));
+  return ds4a::host_launched(ds4a::launch_evict(p, as_cuda(stream)));
+}
+
+ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void *k, const void *v,
+                              int64_t new_row_stride, const int32_t *slots, ds4a_stream_t stream) {
+  if (n < 0 || rows == nullptr) return DS4A_ERR_INVALID_ARG;
+  if (n == 0) return DS4A_OK;
+  if (!pool_ok(rows, true)) return DS4A_ERR_INVALID_ARG;
+  const bool one = rows->v == rows->k;
+  if (k == nullptr || !aligned(k, 16) || !stride_ok(new_row_stride, DS4A_ROW_BYTES, 16)) return DS4A_ERR_INVALID_ARG;
+  if (!one && (v == nullptr || !aligned(v, 16))) return DS4A_ERR_INVALID_ARG;
+  if (slots == nullptr || !aligned(slots, 4)) return DS4A_ERR_INVALID_ARG;
+  const int64_t row = rows->k_scale != nullptr ? DS4A_HEAD_DIM : DS4A_ROW_BYTES;
+  const int64_t page = (int64_t)(rows->page_rows - 1) * rows->row_stride + row;
+  for (const void *pool : {rows->k, rows->v})
+    for (const void *in : {k, one ? k : v})
+      if (meet(span(pool, rows->n_pages, rows->page_stride, page), span(in, n, new_row_stride, DS4A_ROW_BYTES)))
+        return DS4A_ERR_INVALID_ARG;
+  HostDevice d;
+  const ds4a_status st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::AppendParams p;
+  p.rows = seg_of(rows);
+  p.k = static_cast<const uint8_t *>(k);
+  p.v = static_cast<const uint8_t *>(one ? k : v);
+  p.new_stride = new_row_stride;
+  p.slots = slots;
+  p.n = n;
+  return ds4a::host_launched(ds4a::launch_append(p, as_cuda(stream)));
+}
+
+ds4a_status ds4a_rmsnorm_fp8(int32_t n, int32_t width, int32_t x_fp32, const void *x, int64_t x_stride,
+                             const void *residual, int64_t residual_stride, void *residual_out,
+                             int64_t residual_out_stride, const float *weight, float eps, int32_t group,
+                             uint8_t *codes, int64_t code_stride, float *scales, int64_t scale_stride, void *y,
+                             int64_t y_stride, ds4a_stream_t stream) {
+  if (n < 0 || width < 8 || width > 32768 || width % 8 != 0) return DS4A_ERR_INVALID_ARG;
+  if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256) return DS4A_ERR_INVALID_ARG;
+  if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return DS4A_ERR_INVALID_ARG;
+  if (codes == nullptr && y == nullptr) return DS4A_ERR_INVALID_ARG;
+  if ((codes == nullptr) != (scales == nullptr)) return DS4A_ERR_INVALID_ARG;
+  if ((residual == nullptr) != (residual_out == nullptr)) return DS4A_ERR_INVALID_ARG;
+  if (n == 0) return DS4A_OK;
+  const int64_t row = (x_fp32 ? 4LL : 2LL) * width, groups = group == 0 ? 1 : (width + group - 1) / group;
+  if (x == nullptr || !aligned(x, 16) || !stride_ok(x_stride, row, 16)) return DS4A_ERR_INVALID_ARG;
+  if (weight == nullptr || !aligned(weight, 16)) return DS4A_ERR_INVALID_ARG;
+  if (residual != nullptr && (!aligned(residual, 16) || !stride_ok(residual_stride, row, 16) ||
+                              !aligned(residual_out, 16) || !stride_ok(residual_out_stride, row, 16)))
+    return DS4A_ERR_INVALID_ARG;
+  if (codes != nullptr && (!aligned(codes, 8) || !stride_ok(code_stride, width, 8) || !aligned(scales, 4) ||
+                           !stride_ok(scale_stride, 4 * groups, 4)))
+    return DS4A_ERR_INVALID_ARG;
+  if (y != nullptr && (!aligned(y, 16) || !stride_ok(y_stride, 2LL * width, 16))) return DS4A_ERR_INVALID_ARG;
+  const Span in[3] = {span(x, n, x_stride, row), span(residual, n, residual_stride, row), span(weight, 1, 0, 4LL * width)};
+  const Span out[4] = {span(residual_out, n, residual_out_stride, row), span(codes, n, code_stride, width),
+                       span(scales, n, scale_stride, 4 * groups), span(y, n, y_stride, 2LL * width)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      const bool in_place = i == 0 && j < 2 && out[0].lo == in[j].lo &&
+                            residual_out_stride == (j == 0 ? x_stride : residual_stride);
+      if (!in_place && meet(out[i], in[j])) return DS4A_ERR_INVALID_ARG;
+    }
+    for (int j = i + 1; j < 4; ++j)
+      if (meet(out[i], out[j])) return DS4A_ERR_INVALID_ARG;
+  }
+  HostDevice d;
+  const ds4a_status st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::NormParams p;
+  p.n = n;
+  p.width = width;
+  p.x = static_cast<const uint8_t *>(x);
+  p.x_stride = x_stride;
+  p.res = static_cast<const uint8_t *>(residual);
+  p.res_stride = residual_stride;
+  p.res_out = static_cast<uint8_t *>(residual_out);
+  p.res_out_stride = residual_out_stride;
+  p.weight = weight;
+  p.eps = eps;
+  p.group = group;
+  p.codes = codes;
+  p.code_stride = code_stride;
+  p.scales = scales;
+  p.scale_stride = codes != nullptr ? scale_stride / 4 : 0;
+  p.y = static_cast<uint8_t *>(y);
+  p.y_stride = y_stride;
+  return ds4a::host_launched(ds4a::launch_norm(p, x_fp32 != 0, as_cuda(stream)));
+}
+
+}  // extern "C"

@@ -56,6 +56,20 @@ class BatchTensors(ctypes.Structure):
                 ("o", ctypes.c_void_p), ("o_seq_stride", ctypes.c_int64), ("lse", ctypes.c_void_p)]
 
 
+class PagedSegment(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("row_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_rows", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_seq_stride", ctypes.c_int64),
+                ("raw", PagedSegment), ("comp", PagedSegment),
+                ("o", ctypes.c_void_p), ("o_seq_stride", ctypes.c_int64), ("lse", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -128,6 +142,23 @@ def lib() -> ctypes.CDLL:
         L.ds4a_compress_append.argtypes = [i32, i32, i32, vp, vp, i64, i32, vp, vp, i64, vp, i64, vp]
         L.ds4a_indexer_topk.restype = st
         L.ds4a_indexer_topk.argtypes = [PL, vp, i64, i32, vp, i64, vp]
+        PP, PB, f32, sz = ctypes.POINTER(PagedSegment), ctypes.POINTER(PagedBatch), ctypes.c_float, ctypes.c_size_t
+        L.ds4a_attn_decode_paged_workspace_size.restype = sz
+        L.ds4a_attn_decode_paged_workspace_size.argtypes = [i32]
+        L.ds4a_attn_decode_paged.restype = st
+        L.ds4a_attn_decode_paged.argtypes = [i32, PL, vp, PB, vp, sz, vp]
+        L.ds4a_attn_weights_paged.restype = st
+        L.ds4a_attn_weights_paged.argtypes = [i32, PL, vp, PB, vp, i64, f32, vp, i64, vp]
+        L.ds4a_evict_paged_workspace_size.restype = sz
+        L.ds4a_evict_paged_workspace_size.argtypes = [i32, i32]
+        L.ds4a_evict_paged.restype = st
+        L.ds4a_evict_paged.argtypes = [i32, PL, vp, PP, vp, i64, vp, i64, i32, i32, i32, vp, i64, vp, i64, vp, i64,
+                                       vp, i64, vp, sz, vp]
+        L.ds4a_append_paged.restype = st
+        L.ds4a_append_paged.argtypes = [PP, i32, vp, vp, i64, vp, vp]
+        L.ds4a_rmsnorm_fp8.restype = st
+        L.ds4a_rmsnorm_fp8.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, f32, i32, vp, i64, vp, i64, vp,
+                                       i64, vp]
         L.ds4a_device_status.restype = st
         L.ds4a_device_status.argtypes = [vp, ctypes.c_int]
         L.ds4a_device_error_word.restype = st
@@ -375,7 +406,7 @@ class PreparedCall:
     def __call__(self) -> None:
         st = self._fn(*self._args)
         if st != OK:
-            raise Ds4aError(st, self._name)
+            _check(st, self._name)
 
 
 class Graph:
@@ -809,6 +840,313 @@ def compress_append(kv, score, state_kv, state_score, n_state, ratio, *, out=Non
     _check(lib().ds4a_compress_append(width, ratio, n_state, kp, sp, ks, n_new, stp, scp, sts, _ptr(out),
                                       out.stride(0) * 2, _stream(stream)), "ds4a_compress_append")
     return out[:n_out], (n_state + n_new) % ratio
+
+
+# ------------------------------------------------------------------ paged cache
+
+class PagedRows:
+    """One segment of a paged cache: the pools of K and V rows and the page table.
+
+    ``k``, ``v``: fp16 [n_pages, page_rows, 512], or E4M3 codes (uint8) with
+    ``k_scale`` / ``v_scale`` fp32 [n_pages, page_rows]; ``v=None`` (or ``k``
+    itself): one row serves as K and V.  ``table``: int32 [n_seq, max_pages],
+    the page of each sequence's rows ``i * page_rows ..``; entries outside
+    ``[0, n_pages)`` name no page.  :func:`append_paged` needs no table.
+    The tensors are kept alive by the object."""
+
+    def __init__(self, k, v=None, table=None, *, k_scale=None, v_scale=None):
+        import torch
+        if v is None:
+            v = k
+        if v is k and v_scale is None:
+            v_scale = k_scale
+        want = torch.uint8 if k_scale is not None or v_scale is not None else torch.float16
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype != want or t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1:
+                raise ValueError(f"{name} must be {'uint8 codes' if want == torch.uint8 else 'fp16'} "
+                                 "[n_pages, page_rows, 512] with contiguous rows")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must share shape and strides")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if want == torch.uint8 and (t is None or t.dtype != torch.float32 or t.shape != k.shape[:2]
+                                        or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous fp32 {tuple(k.shape[:2])}")
+        if table is not None and (table.dtype != torch.int32 or table.dim() != 2
+                                  or (table.shape[1] > 1 and table.stride(1) != 1)):
+            raise ValueError("table must be int32 [n_seq, max_pages] with contiguous rows")
+        self.k, self.v, self.table, self.k_scale, self.v_scale = k, v, table, k_scale, v_scale
+        size = k.element_size()
+        self.page_rows = k.shape[1]
+        self.max_pages = 0 if table is None else table.shape[1]
+        self.capacity = self.max_pages * self.page_rows  # rows a sequence can have
+        self._c = PagedSegment(k.data_ptr(), v.data_ptr(), k.stride(1) * size, k.stride(0) * size, k.shape[1],
+                               k.shape[0], None if k_scale is None else k_scale.data_ptr(),
+                               None if v_scale is None else v_scale.data_ptr(),
+                               None if table is None else table.data_ptr(),
+                               0 if table is None else max(table.stride(0), table.shape[1]) * 4, self.max_pages)
+
+    def _check(self, name, n_seq=None):
+        """Devices, and a table for at least ``n_seq`` sequences (None: none needed)."""
+        _on_device(**{f"{name}.k": self.k, f"{name}.v": self.v, f"{name}.k_scale": self.k_scale,
+                      f"{name}.v_scale": self.v_scale, f"{name}.table": self.table})
+        if n_seq is None:
+            return
+        if self.table is None:
+            raise ValueError(f"{name} has no page table")
+        if self.table.shape[0] < n_seq:
+            raise ValueError(f"{name}.table has {self.table.shape[0]} sequences, the batch has {n_seq}")
+        if self.table.shape[0] > 1 and self.table.stride(0) < self.table.shape[1]:
+            raise ValueError(f"{name}.table must not repeat rows by stride")
+
+
+_NO_ROWS = PagedSegment(None, None, 0, 0, 1, 1, None, None, None, 0, 0)
+
+
+def _paged_geom(seq_geom, n_seq):
+    import torch
+    if seq_geom.dtype != torch.int32 or seq_geom.dim() != 2 or tuple(seq_geom.shape) != (n_seq, 4) \
+            or not seq_geom.is_contiguous():
+        raise ValueError(f"seq_geom must be contiguous int32 [{n_seq}, 4]")
+    _on_device(seq_geom=seq_geom)
+
+
+def _per_row(t, name, n_seq, cols, dtype):
+    """A [n_seq, >= cols] tensor with contiguous rows -> (pointer, byte stride)."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] < n_seq or t.shape[1] < cols \
+            or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must be {dtype} [>= {n_seq}, >= {cols}] with contiguous rows")
+    _on_device(**{name: t})
+    return _ptr(t), max(t.stride(0), cols) * t.element_size()
+
+
+def _bytes_of(workspace, need, q):
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _on_device(workspace=workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def decode_paged_workspace_bytes(n_seq: int, shape=None, raw=None, comp=None) -> int:
+    """Workspace bytes of :func:`attn_decode_paged` for a batch (of any lengths)."""
+    return int(lib().ds4a_attn_decode_paged_workspace_size(int(n_seq)))
+
+
+def prepare_decode_paged(shape, seq_geom, q, raw, comp=None, *, workspace=None, out, lse=None,
+                         stream=None) -> PreparedCall:
+    """:func:`attn_decode_paged` on fixed buffers, as a :class:`PreparedCall`."""
+    S, B = make_layout(shape), q.shape[0]
+    qp, qs = _tokens(q, "q")
+    op, os_ = _tokens(out, "out", B)
+    _lse_ok(lse, B)
+    _on_device(q=q, out=out, lse=lse)
+    _paged_geom(seq_geom, B)
+    for seg, name in ((raw, "raw"), (comp, "comp")):
+        if seg is not None:
+            seg._check(name, B)
+    workspace, nbytes = _bytes_of(workspace, decode_paged_workspace_bytes(B), q)
+    X = PagedBatch(qp, qs, _NO_ROWS if raw is None else raw._c, _NO_ROWS if comp is None else comp._c, op, os_,
+                   _ptr(lse))
+    args = (B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(X), _ptr(workspace), nbytes, _stream(stream))
+    return PreparedCall(lib().ds4a_attn_decode_paged, "ds4a_attn_decode_paged", args,
+                        (S, X, seq_geom, q, raw, comp, workspace, out, lse, stream))
+
+
+def attn_decode_paged(shape, seq_geom, q, raw, comp=None, *, workspace=None, out=None, lse=None, want_lse=False,
+                      stream=None):
+    """One decode step for B sequences over paged rows: q fp16 [B, 64, 512];
+    ``raw`` and ``comp`` :class:`PagedRows` (either may be None) of one format;
+    seq_geom int32 [B, 4] on the device: (q_pos, n_raw, raw_pos0, n_comp)."""
+    out, lse = _outputs(q, out, lse, want_lse)
+    prepare_decode_paged(shape, seq_geom, q, raw, comp, workspace=workspace, out=out, lse=lse, stream=stream)()
+    return (out, lse) if (want_lse or lse is not None) else out
+
+
+def prepare_weights_paged(shape, seq_geom, q, comp, lse, *, weights=None, decay=1.0, out, stream=None) -> PreparedCall:
+    """:func:`attn_weights_paged` on fixed buffers, as a :class:`PreparedCall`."""
+    import torch
+    S, B = make_layout(shape), q.shape[0]
+    qp, qs = _tokens(q, "q")
+    if lse is None:
+        raise ValueError("lse is missing")
+    _lse_ok(lse, B)
+    _on_device(q=q, lse=lse)
+    _paged_geom(seq_geom, B)
+    comp._check("comp", B)
+    wp, wst = _per_row(weights, "weights", B, comp.capacity, torch.float32)
+    op, ost = _per_row(out, "out", B, comp.capacity, torch.float32)
+    X = PagedBatch(qp, qs, _NO_ROWS, comp._c, None, 0, _ptr(lse))
+    args = (B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(X), wp, wst, float(decay), op, ost, _stream(stream))
+    return PreparedCall(lib().ds4a_attn_weights_paged, "ds4a_attn_weights_paged", args,
+                        (S, X, seq_geom, q, comp, lse, weights, out, stream))
+
+
+def attn_weights_paged(shape, seq_geom, q, comp, lse, *, weights=None, decay=1.0, out=None, stream=None):
+    """The attention weight each compressed row received in a decode step,
+    summed over heads, plus ``decay * weights`` (None: 0): fp32 [B, capacity].
+    ``lse`` is what :func:`attn_decode_paged` returned; ``out`` may be
+    ``weights``.  Entries of rows a token does not see are not written (0 in an
+    ``out`` made here)."""
+    import torch
+    if out is None:
+        out = torch.zeros((q.shape[0], comp.capacity), dtype=torch.float32, device=q.device)
+    prepare_weights_paged(shape, seq_geom, q, comp, lse, weights=weights, decay=decay, out=out, stream=stream)()
+    return out
+
+
+def evict_paged_workspace_bytes(n_seq: int, n_keep: int) -> int:
+    return int(lib().ds4a_evict_paged_workspace_size(int(n_seq), int(n_keep)))
+
+
+def prepare_evict_paged(shape, seq_geom, rows, weights, n_keep, *, n_first=0, n_recent=0, ids=None, kept,
+                        weights_out=None, ids_out=None, n_out, workspace=None, stream=None) -> PreparedCall:
+    """:func:`evict_paged` on fixed buffers, as a :class:`PreparedCall`."""
+    import torch
+    S, B, n_keep = make_layout(shape), seq_geom.shape[0], int(n_keep)
+    _paged_geom(seq_geom, B)
+    rows._check("rows", B)
+    wp, wst = _per_row(weights, "weights", B, rows.capacity, torch.float32)
+    if weights is None:
+        raise ValueError("weights are missing")
+    if (ids is None) != (ids_out is None):
+        raise ValueError("ids and ids_out go together")
+    ip, ist = _per_row(ids, "ids", B, rows.capacity, torch.int32)
+    kp, kst = _per_row(kept, "kept", B, n_keep, torch.int32)
+    wop, wost = _per_row(weights_out, "weights_out", B, rows.capacity, torch.float32)
+    iop, iost = _per_row(ids_out, "ids_out", B, rows.capacity, torch.int32)
+    if n_out.dtype != torch.int32 or n_out.dim() != 1 or n_out.shape[0] < B or (B > 1 and n_out.stride(0) < 1):
+        raise ValueError(f"n_out must be int32 [>= {B}]")
+    _on_device(n_out=n_out)
+    workspace, nbytes = _bytes_of(workspace, evict_paged_workspace_bytes(B, n_keep), weights)
+    args = (B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(rows._c), wp, wst, ip, ist, n_keep, int(n_first),
+            int(n_recent), kp, kst, wop, wost, iop, iost, _ptr(n_out), max(n_out.stride(0), 1) * 4, _ptr(workspace),
+            nbytes, _stream(stream))
+    return PreparedCall(lib().ds4a_evict_paged, "ds4a_evict_paged", args,
+                        (S, seq_geom, rows, weights, ids, kept, weights_out, ids_out, n_out, workspace, stream))
+
+
+def evict_paged(shape, seq_geom, rows, weights, n_keep, *, n_first=0, n_recent=0, ids=None, kept=None,
+                weights_out=None, ids_out=None, n_out=None, workspace=None, stream=None):
+    """Keeps the ``n_keep`` compressed rows of each sequence with the largest
+    ``weights`` fp32 [B, capacity] (the ``n_first`` first and ``n_recent`` latest
+    by ``ids`` ahead of all others) and moves kept rows into the freed slots.
+    ``weights`` and ``ids`` are updated in place unless ``weights_out`` /
+    ``ids_out`` are given.  Returns (kept int32 [B, n_keep]: the former slot of
+    the row in each slot, -1 beyond; n_out int32 [B]).  ``n_out=seq_geom[:, 3]``
+    updates the geometry on the device."""
+    import torch
+    B, dev = seq_geom.shape[0], weights.device
+    if kept is None:
+        kept = torch.empty((B, int(n_keep)), dtype=torch.int32, device=dev)
+    if n_out is None:
+        n_out = torch.empty((B,), dtype=torch.int32, device=dev)
+    prepare_evict_paged(shape, seq_geom, rows, weights, n_keep, n_first=n_first, n_recent=n_recent, ids=ids,
+                        kept=kept, weights_out=weights if weights_out is None else weights_out,
+                        ids_out=ids if ids_out is None else ids_out, n_out=n_out, workspace=workspace,
+                        stream=stream)()
+    return kept, n_out
+
+
+def prepare_append_paged(rows, k, v, slots, *, stream=None) -> PreparedCall:
+    """:func:`append_paged` on fixed buffers, as a :class:`PreparedCall`."""
+    import torch
+    rows._check("rows")
+    n = k.shape[0]
+    kp, ks = _rows(k, "k")
+    if rows.v is not rows.k:
+        if v is None:
+            raise ValueError("v is missing: the pool keeps K and V apart")
+        vp, vs = _rows(v, "v", n)
+        if n > 1 and vs != ks:
+            raise ValueError("k and v must share the row stride")
+    else:
+        v, vp = None, None
+    if slots.dtype != torch.int32 or slots.dim() != 1 or slots.shape[0] != n or (n > 1 and slots.stride(0) != 1):
+        raise ValueError(f"slots must be contiguous int32 [{n}]")
+    _on_device(k=k, v=v, slots=slots)
+    args = (ctypes.byref(rows._c), n, kp, vp, max(ks, ROW_BYTES), _ptr(slots), _stream(stream))
+    return PreparedCall(lib().ds4a_append_paged, "ds4a_append_paged", args, (rows, k, v, slots, stream))
+
+
+def append_paged(rows, k, v, slots, *, stream=None) -> None:
+    """Writes the rows k / v fp16 [n, 512] into the slots ``slots`` int32 [n] of
+    a pool (slot = page * page_rows + row in page; entries outside the pool
+    write nothing), quantised when it is an E4M3 pool."""
+    prepare_append_paged(rows, k, v, slots, stream=stream)()
+
+
+# ------------------------------------------------------------------ norm
+
+def _norm_rows(t, name, n, width, dtype):
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] < n or t.shape[1] != width or t.stride(1) != 1 \
+            or (t.shape[0] > 1 and t.stride(0) < width):
+        raise ValueError(f"{name} must be {dtype} [>= {n}, {width}] with contiguous rows")
+    _on_device(**{name: t})
+    # a single row's stride says nothing; the library wants whole 16-byte steps
+    st = t.stride(0) * t.element_size() if t.shape[0] > 1 else -(-width * t.element_size() // 16) * 16
+    return _ptr(t), st
+
+
+def prepare_rmsnorm_fp8(x, weight, *, eps=1e-6, residual=None, residual_out=None, group=0, codes=None, scales=None,
+                        y=None, stream=None) -> PreparedCall:
+    """:func:`rmsnorm_fp8` on fixed buffers, as a :class:`PreparedCall`."""
+    import torch
+    if x.dim() != 2 or x.dtype not in (torch.float16, torch.float32):
+        raise ValueError("x must be fp16 or fp32 [n, width]")
+    n, width = x.shape
+    xp, xs = _norm_rows(x, "x", n, width, x.dtype)
+    rp, rs = _norm_rows(residual, "residual", n, width, x.dtype)
+    rop, ros = _norm_rows(residual_out, "residual_out", n, width, x.dtype)
+    if weight.dtype != torch.float32 or tuple(weight.shape) != (width,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous fp32 [{width}]")
+    groups = 1 if group == 0 else -(-width // int(group))
+    cp, cs = _norm_rows(codes, "codes", n, width, torch.uint8)
+    yp, ys = _norm_rows(y, "y", n, width, torch.float16)
+    sp, ss = None, 0
+    if scales is not None:
+        if scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] < n or scales.shape[1] != groups \
+                or (groups > 1 and scales.stride(1) != 1) or (n > 1 and scales.stride(0) < groups):
+            raise ValueError(f"scales must be fp32 [>= {n}, {groups}] with contiguous rows")
+        _on_device(scales=scales)
+        sp, ss = _ptr(scales), max(scales.stride(0), groups) * 4
+    _on_device(weight=weight)
+    args = (n, width, 1 if x.dtype == torch.float32 else 0, xp, xs, rp, rs, rop, ros, _ptr(weight), float(eps),
+            int(group), cp, cs, sp, ss, yp, ys, _stream(stream))
+    return PreparedCall(lib().ds4a_rmsnorm_fp8, "ds4a_rmsnorm_fp8", args,
+                        (x, weight, residual, residual_out, codes, scales, y, stream))
+
+
+def rmsnorm_fp8(x, weight, *, eps=1e-6, residual=None, residual_out=None, group=0, codes=None, scales=None, y=None,
+                want_y=False, stream=None):
+    """Root-mean-square norm of ``x`` (+ ``residual``), fp16 or fp32 [n, width],
+    quantised to E4M3 with a scale per ``group`` values (0: per row).  Returns
+    (codes uint8 [n, width], scales fp32 [n, groups]), then x + residual when a
+    residual is given (``residual_out``; new when None), then y in fp16 with
+    ``want_y``."""
+    import torch
+    n, width = x.shape
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    if codes is None:
+        codes = torch.empty((n, -(-width // 8) * 8), dtype=torch.uint8, device=x.device)[:, :width]
+    if scales is None:
+        scales = torch.empty((n, 1 if group == 0 else -(-width // int(group))), dtype=torch.float32, device=x.device)
+    if y is None and want_y:
+        y = torch.empty((n, width), dtype=torch.float16, device=x.device)
+    prepare_rmsnorm_fp8(x, weight, eps=eps, residual=residual, residual_out=residual_out, group=group, codes=codes,
+                        scales=scales, y=y, stream=stream)()
+    out = [codes, scales]
+    if residual is not None:
+        out.append(residual_out)
+    if y is not None:
+        out.append(y)
+    return tuple(out)
 
 
 def device_status(clear: bool = True, stream=None) -> int:
