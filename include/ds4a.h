@@ -639,13 +639,26 @@ ds4a_status ds4a_attn_weights_paged(int32_t n_seq, const ds4a_layout *shape, con
  *               at the same time.
  * All integer results are exact.
  */
+typedef struct {
+  const float *weights;
+  int64_t weight_stride;
+  const int32_t *ids;
+  int64_t id_stride;
+  int32_t n_keep, n_first, n_recent;
+  int32_t *kept;
+  int64_t kept_stride;
+  float *weights_out;
+  int64_t weight_out_stride;
+  int32_t *ids_out;
+  int64_t id_out_stride;
+  int32_t *n_out;
+  int64_t n_out_stride;
+} ds4a_eviction;
+
 size_t ds4a_evict_paged_workspace_size(int32_t n_seq, int32_t n_keep);
 ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
-                             const ds4a_paged_rows *rows, const float *weights, int64_t weight_stride,
-                             const int32_t *ids, int64_t id_stride, int32_t n_keep, int32_t n_first,
-                             int32_t n_recent, int32_t *kept, int64_t kept_stride, float *weights_out,
-                             int64_t weight_out_stride, int32_t *ids_out, int64_t id_out_stride, int32_t *n_out,
-                             int64_t n_out_stride, void *workspace, size_t workspace_bytes, ds4a_stream_t stream);
+                             const ds4a_paged_rows *rows, const ds4a_eviction *E, void *workspace,
+                             size_t workspace_bytes, ds4a_stream_t stream);
 
 /*
  * ds4a_append_paged - writes new K/V rows into a pool, quantising them (the
@@ -687,13 +700,28 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
  *               aligned; NULL exactly when codes is.
  *   y           fp16 [n][width] at y_stride bytes (a multiple of 16), 16-byte
  *               aligned: y rounded to fp16; or NULL.  codes or y is given.
- * Outputs must not overlap inputs (but for the above) nor each other.
+ * The byte range of an output, from its first to its last byte, must not meet
+ * that of an input (but for the above) nor of another output.
  */
-ds4a_status ds4a_rmsnorm_fp8(int32_t n, int32_t width, int32_t x_fp32, const void *x, int64_t x_stride,
-                             const void *residual, int64_t residual_stride, void *residual_out,
-                             int64_t residual_out_stride, const float *weight, float eps, int32_t group,
-                             uint8_t *codes, int64_t code_stride, float *scales, int64_t scale_stride, void *y,
-                             int64_t y_stride, ds4a_stream_t stream);
+typedef struct {
+  int32_t n, width, x_fp32, group;
+  const void *x;
+  int64_t x_stride;
+  const void *residual;
+  int64_t residual_stride;
+  void *residual_out;
+  int64_t residual_out_stride;
+  const float *weight;
+  float eps;
+  uint8_t *codes;
+  int64_t code_stride;
+  float *scales;
+  int64_t scale_stride;
+  void *y;
+  int64_t y_stride;
+} ds4a_norm;
+
+ds4a_status ds4a_rmsnorm_fp8(const ds4a_norm *N, ds4a_stream_t stream);
 
 /*
  * ds4a_device_status - synchronises `stream`, then reports the device error

@@ -99,6 +99,26 @@ bool q_ok(const void *q, int64_t stride) {
   return q != nullptr && aligned(q, 16) && stride_ok(stride, 64LL * DS4A_ROW_BYTES, 16);
 }
 
+// Rows of a run that TMA copies at once: the largest power of two that divides
+// a page's rows, 128 at most; 0 (all rows gathered) below 8.
+int run_rows_of(int page_rows) {
+  const int run = page_rows & -page_rows;
+  return run > 128 ? 128 : run < 8 ? 0 : run;
+}
+
+// The tensor maps of the compressed rows, when their pages allow them.
+ds4a_status encode_comp(ds4a::PagedAttnParams &p, const ds4a_paged_rows *r, bool need_v) {
+  p.run_rows = has_rows(r) ? run_rows_of(r->page_rows) : 0;
+  if (p.run_rows == 0) return DS4A_OK;
+  const bool e4m3 = r->k_scale != nullptr;
+  ds4a_status st = ds4a::host_encode_pages(&p.tm_k, r->k, e4m3, r->page_rows, r->n_pages, r->row_stride,
+                                           r->page_stride, p.run_rows);
+  if (st == DS4A_OK && need_v)
+    st = ds4a::host_encode_pages(&p.tm_v, r->v, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride,
+                                 p.run_rows);
+  return st;
+}
+
 int64_t tiles_of(int64_t rows) { return (rows + 127) / 128; }
 
 // CTAs a decode step of n_seq sequences may use.
@@ -106,7 +126,7 @@ int decode_ctas(int sm_count) { return sm_count; }
 
 size_t decode_workspace(int32_t n_seq, int ctas) {
   const size_t slots = (size_t)n_seq + ctas;
-  return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(__half) + sizeof(float2)) + (size_t)n_seq * sizeof(int2);
+  return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(float) + sizeof(float2)) + (size_t)n_seq * sizeof(int2);
 }
 
 int device_sms() {
@@ -160,6 +180,8 @@ ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, cons
   std::memset(&p, 0, sizeof(p));
   st = ds4a::host_encode_q(&p.tm_q, X->q, n_seq, X->q_seq_stride);
   if (st != DS4A_OK) return st;
+  st = encode_comp(p, &X->comp, true);
+  if (st != DS4A_OK) return st;
   p.seg[0] = has_rows(&X->raw) ? seg_of(&X->raw) : no_rows();
   p.seg[1] = has_rows(&X->comp) ? seg_of(&X->comp) : no_rows();
   p.geom = reinterpret_cast<const int4 *>(seq_geom);
@@ -172,7 +194,7 @@ ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, cons
   p.lse = X->lse;
   const int ctas = decode_ctas(d.sm_count);
   const size_t slots = (size_t)n_seq + ctas;
-  p.ws_o = static_cast<__half *>(workspace);
+  p.ws_o = static_cast<float *>(workspace);
   p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + slots * DS4A_HEADS * DS4A_HEAD_DIM);
   p.ws_plan = reinterpret_cast<int2 *>(p.ws_ml + slots * DS4A_HEADS);
   p.timeout_ns = kTimeoutNs;
@@ -214,6 +236,8 @@ ds4a_status ds4a_attn_weights_paged(int32_t n_seq, const ds4a_layout *shape, con
   std::memset(&p, 0, sizeof(p));
   st = ds4a::host_encode_q(&p.tm_q, X->q, n_seq, X->q_seq_stride);
   if (st != DS4A_OK) return st;
+  st = encode_comp(p, &rows, false);
+  if (st != DS4A_OK) return st;
   p.seg[0] = no_rows();
   p.seg[1] = seg_of(&rows);
   p.geom = reinterpret_cast<const int4 *>(seq_geom);
@@ -239,36 +263,36 @@ size_t ds4a_evict_paged_workspace_size(int32_t n_seq, int32_t n_keep) {
 }
 
 ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
-                             const ds4a_paged_rows *rows, const float *weights, int64_t weight_stride,
-                             const int32_t *ids, int64_t id_stride, int32_t n_keep, int32_t n_first,
-                             int32_t n_recent, int32_t *kept, int64_t kept_stride, float *weights_out,
-                             int64_t weight_out_stride, int32_t *ids_out, int64_t id_out_stride, int32_t *n_out,
-                             int64_t n_out_stride, void *workspace, size_t workspace_bytes, ds4a_stream_t stream) {
-  if (n_seq < 0 || shape == nullptr || rows == nullptr) return DS4A_ERR_INVALID_ARG;
+                             const ds4a_paged_rows *rows, const ds4a_eviction *E, void *workspace,
+                             size_t workspace_bytes, ds4a_stream_t stream) {
+  if (n_seq < 0 || shape == nullptr || rows == nullptr || E == nullptr) return DS4A_ERR_INVALID_ARG;
   if (n_seq == 0) return DS4A_OK;
-  if (n_keep < 1 || n_keep > kMostRows || n_first < 0 || n_recent < 0 || shape->ratio < 1 || n_seq > (1 << 20))
+  if (E->n_keep < 1 || E->n_keep > kMostRows || E->n_first < 0 || E->n_recent < 0 || shape->ratio < 1 ||
+      n_seq > (1 << 20))
     return DS4A_ERR_INVALID_ARG;
   if (seq_geom == nullptr || !aligned(seq_geom, 16)) return DS4A_ERR_INVALID_ARG;
   if (rows->max_pages < 1 || !pool_ok(rows, true) || !table_ok(rows)) return DS4A_ERR_INVALID_ARG;
   const int64_t cols = (int64_t)rows->max_pages * rows->page_rows;
-  if (weights == nullptr || !aligned(weights, 4) || !stride_ok(weight_stride, 4 * cols, 4))
+  if (E->weights == nullptr || !aligned(E->weights, 4) || !stride_ok(E->weight_stride, 4 * cols, 4))
     return DS4A_ERR_INVALID_ARG;
-  if ((ids == nullptr) != (ids_out == nullptr)) return DS4A_ERR_INVALID_ARG;
-  if (kept == nullptr || !aligned(kept, 4) || !stride_ok(kept_stride, 4LL * n_keep, 4)) return DS4A_ERR_INVALID_ARG;
-  if (n_out == nullptr || !aligned(n_out, 4) || !stride_ok(n_out_stride, 4, 4)) return DS4A_ERR_INVALID_ARG;
-  const Span in_w = span(weights, n_seq, weight_stride, 4 * cols);
-  if (weights_out != nullptr &&
-      (!aligned(weights_out, 4) || !stride_ok(weight_out_stride, 4 * cols, 4) ||
-       !same_or_apart(span(weights_out, n_seq, weight_out_stride, 4 * cols), weight_out_stride, in_w, weight_stride)))
+  if ((E->ids == nullptr) != (E->ids_out == nullptr)) return DS4A_ERR_INVALID_ARG;
+  if (E->kept == nullptr || !aligned(E->kept, 4) || !stride_ok(E->kept_stride, 4LL * E->n_keep, 4))
     return DS4A_ERR_INVALID_ARG;
-  if (ids != nullptr &&
-      (!aligned(ids, 4) || !stride_ok(id_stride, 4 * cols, 4) || !aligned(ids_out, 4) ||
-       !stride_ok(id_out_stride, 4 * cols, 4) ||
-       !same_or_apart(span(ids_out, n_seq, id_out_stride, 4 * cols), id_out_stride,
-                      span(ids, n_seq, id_stride, 4 * cols), id_stride)))
+  if (E->n_out == nullptr || !aligned(E->n_out, 4) || !stride_ok(E->n_out_stride, 4, 4)) return DS4A_ERR_INVALID_ARG;
+  const Span in_w = span(E->weights, n_seq, E->weight_stride, 4 * cols);
+  if (E->weights_out != nullptr &&
+      (!aligned(E->weights_out, 4) || !stride_ok(E->weight_out_stride, 4 * cols, 4) ||
+       !same_or_apart(span(E->weights_out, n_seq, E->weight_out_stride, 4 * cols), E->weight_out_stride, in_w,
+                      E->weight_stride)))
+    return DS4A_ERR_INVALID_ARG;
+  if (E->ids != nullptr &&
+      (!aligned(E->ids, 4) || !stride_ok(E->id_stride, 4 * cols, 4) || !aligned(E->ids_out, 4) ||
+       !stride_ok(E->id_out_stride, 4 * cols, 4) ||
+       !same_or_apart(span(E->ids_out, n_seq, E->id_out_stride, 4 * cols), E->id_out_stride,
+                      span(E->ids, n_seq, E->id_stride, 4 * cols), E->id_stride)))
     return DS4A_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256) ||
-      workspace_bytes < ds4a_evict_paged_workspace_size(n_seq, n_keep))
+      workspace_bytes < ds4a_evict_paged_workspace_size(n_seq, E->n_keep))
     return DS4A_ERR_WORKSPACE;
   if (n_seq * ((cols + 7) / 8) > INT32_MAX) return DS4A_ERR_INVALID_ARG;  // blocks of the move kernel
   HostDevice d;
@@ -279,24 +303,24 @@ ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int3
   p.n_seq = n_seq;
   p.ratio = shape->ratio;
   p.rows = seg_of(rows);
-  p.weights = weights;
-  p.weight_stride = weight_stride / 4;
-  p.ids = ids;
-  p.id_stride = ids != nullptr ? id_stride / 4 : 0;
-  p.n_keep = n_keep;
-  p.n_first = n_first;
-  p.n_recent = n_recent;
-  p.kept = kept;
-  p.kept_stride = kept_stride / 4;
-  p.weights_out = weights_out;
-  p.weight_out_stride = weights_out != nullptr ? weight_out_stride / 4 : 0;
-  p.ids_out = ids_out;
-  p.id_out_stride = ids_out != nullptr ? id_out_stride / 4 : 0;
-  p.n_out = reinterpret_cast<uint8_t *>(n_out);
-  p.n_out_stride = n_out_stride;
+  p.weights = E->weights;
+  p.weight_stride = E->weight_stride / 4;
+  p.ids = E->ids;
+  p.id_stride = E->ids != nullptr ? E->id_stride / 4 : 0;
+  p.n_keep = E->n_keep;
+  p.n_first = E->n_first;
+  p.n_recent = E->n_recent;
+  p.kept = E->kept;
+  p.kept_stride = E->kept_stride / 4;
+  p.weights_out = E->weights_out;
+  p.weight_out_stride = E->weights_out != nullptr ? E->weight_out_stride / 4 : 0;
+  p.ids_out = E->ids_out;
+  p.id_out_stride = E->ids_out != nullptr ? E->id_out_stride / 4 : 0;
+  p.n_out = reinterpret_cast<uint8_t *>(E->n_out);
+  p.n_out_stride = E->n_out_stride;
   p.n_moves = static_cast<int32_t *>(workspace);
   p.from = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + align256(4 * (size_t)n_seq));
-  p.to = p.from + (size_t)n_seq * n_keep;
+  p.to = p.from + (size_t)n_seq * E->n_keep;
   p.cached = ds4a::evict_cached_keys(p.rows.max_rows, ds4a::evict_cluster(p.rows.max_rows));
   return ds4a::host_launched(ds4a::launch_evict(p, as_cuda(stream)));
 }
@@ -329,35 +353,38 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
   return ds4a::host_launched(ds4a::launch_append(p, as_cuda(stream)));
 }
 
-ds4a_status ds4a_rmsnorm_fp8(int32_t n, int32_t width, int32_t x_fp32, const void *x, int64_t x_stride,
-                             const void *residual, int64_t residual_stride, void *residual_out,
-                             int64_t residual_out_stride, const float *weight, float eps, int32_t group,
-                             uint8_t *codes, int64_t code_stride, float *scales, int64_t scale_stride, void *y,
-                             int64_t y_stride, ds4a_stream_t stream) {
-  if (n < 0 || width < 8 || width > 32768 || width % 8 != 0) return DS4A_ERR_INVALID_ARG;
-  if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256) return DS4A_ERR_INVALID_ARG;
-  if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return DS4A_ERR_INVALID_ARG;
-  if (codes == nullptr && y == nullptr) return DS4A_ERR_INVALID_ARG;
-  if ((codes == nullptr) != (scales == nullptr)) return DS4A_ERR_INVALID_ARG;
-  if ((residual == nullptr) != (residual_out == nullptr)) return DS4A_ERR_INVALID_ARG;
-  if (n == 0) return DS4A_OK;
-  const int64_t row = (x_fp32 ? 4LL : 2LL) * width, groups = group == 0 ? 1 : (width + group - 1) / group;
-  if (x == nullptr || !aligned(x, 16) || !stride_ok(x_stride, row, 16)) return DS4A_ERR_INVALID_ARG;
-  if (weight == nullptr || !aligned(weight, 16)) return DS4A_ERR_INVALID_ARG;
-  if (residual != nullptr && (!aligned(residual, 16) || !stride_ok(residual_stride, row, 16) ||
-                              !aligned(residual_out, 16) || !stride_ok(residual_out_stride, row, 16)))
+ds4a_status ds4a_rmsnorm_fp8(const ds4a_norm *N, ds4a_stream_t stream) {
+  if (N == nullptr) return DS4A_ERR_INVALID_ARG;
+  if (N->n < 0 || N->width < 8 || N->width > 32768 || N->width % 8 != 0) return DS4A_ERR_INVALID_ARG;
+  if (N->group != 0 && N->group != 32 && N->group != 64 && N->group != 128 && N->group != 256)
     return DS4A_ERR_INVALID_ARG;
-  if (codes != nullptr && (!aligned(codes, 8) || !stride_ok(code_stride, width, 8) || !aligned(scales, 4) ||
-                           !stride_ok(scale_stride, 4 * groups, 4)))
+  if (!(N->eps >= FLT_MIN) || !std::isfinite(N->eps)) return DS4A_ERR_INVALID_ARG;
+  if (N->codes == nullptr && N->y == nullptr) return DS4A_ERR_INVALID_ARG;
+  if ((N->codes == nullptr) != (N->scales == nullptr)) return DS4A_ERR_INVALID_ARG;
+  if ((N->residual == nullptr) != (N->residual_out == nullptr)) return DS4A_ERR_INVALID_ARG;
+  if (N->n == 0) return DS4A_OK;
+  const int64_t row = (N->x_fp32 ? 4LL : 2LL) * N->width;
+  const int64_t groups = N->group == 0 ? 1 : (N->width + N->group - 1) / N->group;
+  if (N->x == nullptr || !aligned(N->x, 16) || !stride_ok(N->x_stride, row, 16)) return DS4A_ERR_INVALID_ARG;
+  if (N->weight == nullptr || !aligned(N->weight, 16)) return DS4A_ERR_INVALID_ARG;
+  if (N->residual != nullptr && (!aligned(N->residual, 16) || !stride_ok(N->residual_stride, row, 16) ||
+                                 !aligned(N->residual_out, 16) || !stride_ok(N->residual_out_stride, row, 16)))
     return DS4A_ERR_INVALID_ARG;
-  if (y != nullptr && (!aligned(y, 16) || !stride_ok(y_stride, 2LL * width, 16))) return DS4A_ERR_INVALID_ARG;
-  const Span in[3] = {span(x, n, x_stride, row), span(residual, n, residual_stride, row), span(weight, 1, 0, 4LL * width)};
-  const Span out[4] = {span(residual_out, n, residual_out_stride, row), span(codes, n, code_stride, width),
-                       span(scales, n, scale_stride, 4 * groups), span(y, n, y_stride, 2LL * width)};
+  if (N->codes != nullptr && (!aligned(N->codes, 8) || !stride_ok(N->code_stride, N->width, 8) ||
+                              !aligned(N->scales, 4) || !stride_ok(N->scale_stride, 4 * groups, 4)))
+    return DS4A_ERR_INVALID_ARG;
+  if (N->y != nullptr && (!aligned(N->y, 16) || !stride_ok(N->y_stride, 2LL * N->width, 16)))
+    return DS4A_ERR_INVALID_ARG;
+  const Span in[3] = {span(N->x, N->n, N->x_stride, row), span(N->residual, N->n, N->residual_stride, row),
+                      span(N->weight, 1, 0, 4LL * N->width)};
+  const Span out[4] = {span(N->residual_out, N->n, N->residual_out_stride, row),
+                       span(N->codes, N->n, N->code_stride, N->width),
+                       span(N->scales, N->n, N->scale_stride, 4 * groups),
+                       span(N->y, N->n, N->y_stride, 2LL * N->width)};
   for (int i = 0; i < 4; ++i) {
     for (int j = 0; j < 3; ++j) {
       const bool in_place = i == 0 && j < 2 && out[0].lo == in[j].lo &&
-                            residual_out_stride == (j == 0 ? x_stride : residual_stride);
+                            N->residual_out_stride == (j == 0 ? N->x_stride : N->residual_stride);
       if (!in_place && meet(out[i], in[j])) return DS4A_ERR_INVALID_ARG;
     }
     for (int j = i + 1; j < 4; ++j)
@@ -367,24 +394,24 @@ ds4a_status ds4a_rmsnorm_fp8(int32_t n, int32_t width, int32_t x_fp32, const voi
   const ds4a_status st = ds4a::host_device(&d);
   if (st != DS4A_OK) return st;
   ds4a::NormParams p;
-  p.n = n;
-  p.width = width;
-  p.x = static_cast<const uint8_t *>(x);
-  p.x_stride = x_stride;
-  p.res = static_cast<const uint8_t *>(residual);
-  p.res_stride = residual_stride;
-  p.res_out = static_cast<uint8_t *>(residual_out);
-  p.res_out_stride = residual_out_stride;
-  p.weight = weight;
-  p.eps = eps;
-  p.group = group;
-  p.codes = codes;
-  p.code_stride = code_stride;
-  p.scales = scales;
-  p.scale_stride = codes != nullptr ? scale_stride / 4 : 0;
-  p.y = static_cast<uint8_t *>(y);
-  p.y_stride = y_stride;
-  return ds4a::host_launched(ds4a::launch_norm(p, x_fp32 != 0, as_cuda(stream)));
+  p.n = N->n;
+  p.width = N->width;
+  p.x = static_cast<const uint8_t *>(N->x);
+  p.x_stride = N->x_stride;
+  p.res = static_cast<const uint8_t *>(N->residual);
+  p.res_stride = N->residual_stride;
+  p.res_out = static_cast<uint8_t *>(N->residual_out);
+  p.res_out_stride = N->residual_out_stride;
+  p.weight = N->weight;
+  p.eps = N->eps;
+  p.group = N->group;
+  p.codes = N->codes;
+  p.code_stride = N->code_stride;
+  p.scales = N->scales;
+  p.scale_stride = N->codes != nullptr ? N->scale_stride / 4 : 0;
+  p.y = static_cast<uint8_t *>(N->y);
+  p.y_stride = N->y_stride;
+  return ds4a::host_launched(ds4a::launch_norm(p, N->x_fp32 != 0, as_cuda(stream)));
 }
 
 }  // extern "C"

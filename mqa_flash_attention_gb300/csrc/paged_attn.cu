@@ -9,30 +9,43 @@
 // Flash Inference Engine", sections "Fixed Model Shape", "Layer Compression"
 // and "KV Cache Design"; the visibility rule is that of attn_kernel.cuh.)
 //
-// Work.  A sequence's visible rows, raw then compressed, form one list, cut
+// Work.  A sequence's visible rows, compressed then raw, form one list, cut
 // into tiles of 128 rows; row j of the list is found through the page table,
 // so pages of any size, tiles that span pages and pages that end inside a tile
 // are all alike.  The tiles of all sequences are numbered through and CTA i
 // takes ceil(total / CTAs) of them in a row: the load is even whatever the
 // lengths.  A CTA's tiles of one sequence are an item.  An item that holds
 // the whole sequence writes its output; otherwise it leaves its normalised
-// output (fp16) and (m, l) in slot (CTA + sequence) of the workspace (unique,
+// output (fp32) and (m, l) in slot (CTA + sequence) of the workspace (unique,
 // since along the tiles either number grows), and the merge kernel joins the
 // slots of a sequence.
 //
 // Per tile, as in attn_kernel.cuh, the rows are on the M side of every MMA:
 //   S^T[128 rows][64 heads]  = K_tile[128][512] . Q^T
 //   O^T[512 dims][64 heads] += V_tile^T . P^T
-// with S^T and O^T in TMEM.  An absent row's K and V are zero-filled in shared
-// memory (cp.async with no source bytes), so nothing a page holds beyond the
-// rows in use can reach a product, not even as 0 * NaN.
+// with S^T and O^T in TMEM.
+//
+// Loads.  A stage of the ring holds 128 dims of a tile.  A tile of 128
+// compressed rows whose pages all exist is loaded by TMA, one copy per run of
+// rows that one page holds (the largest power of two that divides the page's
+// rows, 8 at least and 128 at most), issued by the loader warps in turn: a
+// thread's bulk copies start some 700 cycles apart.  Every other tile (a sequence's last rows, the window rows, absent
+// pages, pages of odd sizes) is gathered with 16-byte cp.async by all loader
+// threads, an absent row zero-filled (a copy with no source bytes): nothing a
+// page holds beyond the rows in use can reach a product, not even as 0 * NaN.
 //
 // Warps (512 threads, one CTA per SM): 0-7 softmax and epilogue, 8-14 loaders,
-// 15 TMEM allocation and MMA issue.  The loaders copy the rows with 16-byte
-// cp.async in the 128-byte swizzled layout; in ring order K(0), then K(j+1)
-// and V(j) for each tile j, so the next scores are computed while the softmax
-// works.  With E4M3 rows, warps 8, 13 and 14 copy codes into the upper half of
-// a stage and warps 9-12 widen them in place, exactly.
+// 15 TMEM allocation and MMA issue.  Ring order: K(0), then K(j+1) and V(j) for
+// each tile j, so the next scores are computed while the softmax works.  With
+// E4M3 rows, warps 8, 13 and 14 load codes into the upper half of a stage and
+// warps 9-12 widen them in place, exactly.
+//
+// A stage's fp16 layout is rows in groups of 8: [16 groups][2 blocks of 64
+// dims][8 rows][128 bytes], 128-byte swizzle: a TMA box of any number of
+// 8-row groups lands contiguously, and the distance between row groups
+// is one constant for the MMA descriptors.  With E4M3 rows it is [2 blocks][128
+// rows][128 bytes], where a row's codes sit in bytes that only its own values
+// replace.
 //
 // E4M3 scales.  K's multiplies the scores.  V's scale c_j is folded into the
 // exponent: p'_j = 2^(s_j + log2 c_j - m') with m' the running maximum of that
@@ -50,6 +63,12 @@ namespace {
 constexpr int kLists = 4;  // row lists in flight
 constexpr float kLeastLog2Scale = -40.f;  // V scales below 2^-40 count as 0: such rows round to 0 in fp16
 
+// Low bits of a list entry (rows are 16-byte aligned).  A slot without a row
+// holds the address of a row that exists, copied with no source bytes.
+constexpr unsigned long long kSegBit = 1, kNoRow = 2;
+// A tile within its item (the CTA's tiles of one sequence).
+constexpr int kFirst = 1, kLast = 2, kWhole = 4;  // kWhole: the item holds all tiles of the sequence
+
 // Wait sites of this kernel.
 enum : unsigned int {
   PSITE_Q_EMPTY = 0x60, PSITE_KV_EMPTY, PSITE_Q_FULL, PSITE_S_EMPTY, PSITE_KV_FULL, PSITE_P_FULL, PSITE_O_EMPTY,
@@ -57,10 +76,11 @@ enum : unsigned int {
 };
 
 struct PMisc {
-  alignas(16) unsigned long long row[kLists][kTile];  // K address | segment; 0: no row
+  alignas(16) unsigned long long row[kLists][kTile];  // K address | kSegBit | kNoRow
   alignas(16) float ksc[kLists][kTile];   // E4M3: scale * log2(e) * K scale
   alignas(16) float lvs[kLists][kTile];   // E4M3: log2 of the V scale (of 2^-40 at least)
   alignas(16) float ivs[kLists][kTile];   // E4M3: 2^-lvs
+  int2 box[kLists][kTile / 8];            // (page, slot) of the runs of a tile that TMA loads
   alignas(16) float red[4][kH];
   alignas(16) float m_use[kH];
   alignas(16) float alpha[kH];
@@ -68,19 +88,27 @@ struct PMisc {
   alignas(8) uint64_t q_full, q_empty;
   uint64_t kv_full[kStages], kv_empty[kStages], code_full[kStages];
   uint64_t list_full[kLists], list_empty[kLists];
+  int gathered[kLists];  // of the lists' tiles: rows come by cp.async
+  int seq[kLists], flags[kLists], base[kLists], end[kLists];  // of the lists' tiles: sequence, kFirst | ..,
+                                                              // first row of the tile, rows of the sequence
   uint64_t s_full[2], s_empty[2];
   uint64_t o_full[4];
   uint64_t p_full, p_empty, o_empty, mma_done;
   unsigned scan[kThreads / 32];
   int first_seq, first_tile;  // where this CTA's tiles start: sequence, tile within it
   int n_tiles;                // tiles of this CTA
-  int per_cta;                // tiles of a full CTA
   uint32_t tmem_base;
   int abort_flag;
   int resc_flag[2];
 };
 constexpr uint32_t kPagedSmem = kOffMisc + ((sizeof(PMisc) + 127) / 128) * 128 + 1024;
 static_assert(kPagedSmem <= 232448, "shared memory of one CTA");
+
+// Bytes between 8-row groups and between the two 64-dim blocks of a stage.
+template <bool FP8>
+__host__ __device__ constexpr uint32_t group_stride() { return FP8 ? 1024u : 2048u; }
+template <bool FP8>
+__host__ __device__ constexpr uint32_t block_stride() { return FP8 ? kBoxBytes : 1024u; }
 
 template <bool FP8>
 __host__ __device__ constexpr int loader_threads() { return FP8 ? kLoaderThreads - kTile : kLoaderThreads; }
@@ -97,8 +125,27 @@ struct StageRing {
   }
 };
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void bar_sync_id(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, int32_t c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
 }
 // 16 bytes global -> shared; `bytes` of 0 writes zeros and reads nothing.
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t bytes) {
@@ -147,8 +194,8 @@ __device__ __forceinline__ float reduce_heads(const float (&s)[32], int lane) {
 
 // ------------------------------------------------------------------ plan
 
-// The rows sequence b's token sees: raw rows [raw_lo, raw_lo + nr), then
-// compressed rows [0, nc).  The weights need the compressed ones only.
+// The rows sequence b's token sees: compressed rows [0, nc), then raw rows
+// [raw_lo, raw_lo + nr).  The weights need the compressed ones only.
 struct SeqRows {
   int raw_lo, nr, nc;
   __device__ __forceinline__ int tiles() const { return (nr + nc + kTile - 1) / kTile; }
@@ -201,45 +248,63 @@ struct Walk {
     }
     last = j == n - 1 || left == 1;
   }
-  // Whole sequence in this item (asked at its last tile): it began here, at tile 0.
-  __device__ __forceinline__ bool whole(int first_j) const { return first_j == 0 && j == n - 1; }
+  __device__ __forceinline__ int flags() {
+    if (first) first_j = j;
+    return (first ? kFirst : 0) | (last ? kLast : 0) | (last && first_j == 0 && j == n - 1 ? kWhole : 0);
+  }
+  int first_j;   // tile the item began with
 };
 
 // Block-wide: where this CTA starts and how many tiles it has; CTA 0 also
-// writes each sequence's slots for the merge.
+// writes each sequence's slots for the merge.  Thread t counts sequence t of
+// every round of 512; with one round (the usual batch) the tiles are counted
+// once.
 template <bool WEIGHTS>
 __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool once = p.n_seq <= kThreads;
+  auto tiles_of_seq = [&](int b) { return b < p.n_seq ? seq_rows<WEIGHTS>(p, b).tiles() : 0; };
+  auto before_warp = [&](int inc, int &all) {  // tiles of the warps before this one, and of all
+    __syncthreads();
+    if (lane == 31) ms.scan[warp] = inc;
+    __syncthreads();
+    int v = lane < kThreads / 32 ? ms.scan[lane] : 0, x = v;
+#pragma unroll
+    for (int o = 1; o < kThreads / 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += t;
+    }
+    all = __shfl_sync(0xffffffffu, x, kThreads / 32 - 1);
+    return __shfl_sync(0xffffffffu, x - v, warp);
+  };
+  auto scan = [&](int n) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += t;
+    }
+    return n;
+  };
   int mine = 0;
-  for (int b = tid; b < p.n_seq; b += kThreads) mine += seq_rows<WEIGHTS>(p, b).tiles();
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) ms.scan[warp] = mine;
-  __syncthreads();
-  int total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) total += ms.scan[i];
+  for (int b = tid; b < p.n_seq; b += kThreads) mine += tiles_of_seq(b);
+  int inc = scan(mine), total;
+  int before = before_warp(inc, total);
   const int G = gridDim.x, per = (total + G - 1) / G;
   const int g0 = min(total, (int)blockIdx.x * per), g1 = min(total, g0 + per);
   if (tid == 0) {
     ms.n_tiles = g1 - g0;
-    ms.per_cta = per;
     ms.first_seq = ms.first_tile = 0;
   }
+  __syncthreads();
   int carry = 0;
   for (int b0 = 0; b0 < p.n_seq; b0 += kThreads) {
     const int b = b0 + tid;
-    const int n = b < p.n_seq ? seq_rows<WEIGHTS>(p, b).tiles() : 0;
-    int inc = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    __syncthreads();  // the previous use of scan[] is over
-    if (lane == 31) ms.scan[warp] = inc;
-    __syncthreads();
-    int before = carry;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += ms.scan[i];
-      carry += ms.scan[i];
+    int n = mine, all = 0;
+    if (!once) {
+      n = tiles_of_seq(b);
+      inc = scan(n);
+      before = carry + before_warp(inc, all);
+      carry += all;
     }
     const int at = before + inc - n;  // tiles before sequence b
     if (n > 0 && at <= g0 && g0 < at + n && g1 > g0) {
@@ -255,89 +320,181 @@ __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
 
 // ------------------------------------------------------------------ loaders
 
+// Lists run ahead of the copies: while the rows of tiles g + 1 and g are
+// issued, the page ids of tile g + 3 and the scales of tile g + 2 are on their
+// way in registers, so neither latency stands between tiles.
 template <bool FP8, bool WEIGHTS>
 __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sbase, PMisc &ms, int ltid) {
   constexpr int kGroup = loader_threads<FP8>();
-  constexpr int kRowStep = kGroup / 8;
+  constexpr int kRowStep = kGroup / 8, kWarps = kGroup / 32;
+  constexpr int kMine = (kTile + kGroup - 1) / kGroup;  // list rows of a thread
   volatile int *abrt = &ms.abort_flag;
   const int gtid = (FP8 && ltid >= 32) ? ltid - kTile : ltid;  // 0 .. kGroup - 1
   const int c8 = gtid & 7, rsub = gtid >> 3;
   const uint32_t b_q_full = smem_u32(&ms.q_full), b_q_empty = smem_u32(&ms.q_empty);
-  const long long vdelta[2] = {p.seg[0].v - p.seg[0].k, p.seg[1].v - p.seg[1].k};
+  const long long vdelta0 = p.seg[0].v - p.seg[0].k, vdelta1 = p.seg[1].v - p.seg[1].k;
+  const int pad_seg = p.seg[1].max_rows > 0 ? 1 : 0;
+  const unsigned long long pad_row = reinterpret_cast<unsigned long long>(p.seg[pad_seg].k) | pad_seg | kNoRow;
   StageRing ring;
   bool ok = true;
   bool q_issued = false;
   uint32_t n_item = 0, q_par = 0;
+  uint32_t filled = 0, last_par = 0;  // TMA stages this thread issued, and their phases
+  int turn = 0;                       // warp of the next part's first run
   const int nt = ms.n_tiles;
 
-  // The rows of tile `w` into list `g % kLists`.
-  auto make_list = [&](const Walk<WEIGHTS> &w, int g) {
+  Walk<WEIGHTS> w;     // at the tile whose page ids are fetched next
+  w.start(p, ms);
+  // Tile whose page ids are in flight, then tile whose scales are.
+  int a_row[kMine], a_page[kMine], a_seq = 0, a_flags = 0, a_base = 0, a_end = 0;
+  bool a_full = false, b_full = false;  // 128 compressed rows in runs that TMA can copy
+  unsigned long long b_at[kMine];
+  int b_page[kMine], b_slot[kMine];
+  float b_ks[kMine], b_vs[kMine];
+  int b_seq = 0, b_flags = 0, b_base = 0, b_end = 0;
+
+  auto fetch_pages = [&]() {
+    a_seq = w.b;
+    a_flags = w.flags();
+    a_base = w.j * kTile;
+    a_end = w.rows.nc + w.rows.nr;
+    a_full = p.run_rows > 0 && a_base + kTile <= w.rows.nc;
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int r = gtid + u * kGroup, x = a_base + r;
+      a_row[u] = -1;
+      a_page[u] = -1;
+      if (r < kTile && x < a_end) {
+        const int sg = x < w.rows.nc ? 1 : 0;
+        const PagedSeg &s = p.seg[sg];
+        const int row = sg == 0 ? w.rows.raw_lo + x - w.rows.nc : x;
+        const int pi = row / s.page_rows;
+        a_page[u] = __ldg(s.table + w.b * s.table_stride + pi);
+        a_row[u] = 2 * (row - pi * s.page_rows) + sg;
+      }
+    }
+    w.next(p);
+  };
+  auto fetch_scales = [&]() {
+    b_seq = a_seq;
+    b_flags = a_flags;
+    b_base = a_base;
+    b_end = a_end;
+    b_full = a_full;
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      b_at[u] = pad_row;
+      b_page[u] = a_page[u];
+      b_slot[u] = a_row[u] >> 1;
+      b_ks[u] = 0.f;
+      b_vs[u] = 1.f;
+      const PagedSeg &s = p.seg[a_row[u] & 1];
+      if (a_row[u] >= 0 && (unsigned)a_page[u] < (unsigned)s.n_pages) {
+        const int slot = a_row[u] >> 1;
+        b_at[u] = reinterpret_cast<unsigned long long>(s.k + a_page[u] * s.page_stride + slot * s.row_stride) |
+                  (a_row[u] & 1);
+        if (FP8) {
+          const long long sr = (long long)a_page[u] * s.page_rows + slot;
+          b_ks[u] = __ldg(s.k_scale + sr);
+          if (!WEIGHTS) b_vs[u] = __ldg(s.v_scale + sr);
+        }
+      }
+    }
+  };
+  // The list of tile g, complete for the whole group; all go on or none.
+  // Returns whether TMA loads the tile.
+  auto store_list = [&](int g) -> bool {
     const int buf = g % kLists;
+    const bool full = b_full;
+    bool absent = false;
     if (ok && !mbar_wait(smem_u32(&ms.list_empty[buf]), ((g / kLists) & 1) ^ 1, abrt, p.timeout_ns, p.err,
                          PSITE_LIST_EMPTY))
       ok = false;
     if (ok) {
-      for (int r = gtid; r < kTile; r += kGroup) {
-        const int x = w.j * kTile + r;
-        const int sg = x < w.rows.nr ? 0 : 1;
-        const int row = sg == 0 ? w.rows.raw_lo + x : x - w.rows.nr;
-        unsigned long long at = 0;
-        float ksc = 0.f, lvs = 0.f, ivs = 1.f;
-        if (x < w.rows.nr + w.rows.nc) {
-          const PagedSeg &s = p.seg[sg];
-          const int pi = row / s.page_rows, slot = row - pi * s.page_rows;
-          const int page = __ldg(s.table + w.b * s.table_stride + pi);
-          if ((unsigned)page < (unsigned)s.n_pages) {
-            at = reinterpret_cast<unsigned long long>(s.k + page * s.page_stride + slot * s.row_stride) | sg;
-            if (FP8) {
-              const long long sr = (long long)page * s.page_rows + slot;
-              ksc = p.scale_log2 * __ldg(s.k_scale + sr);
-              if (!WEIGHTS) {
-                lvs = fmaxf(__log2f(__ldg(s.v_scale + sr)), kLeastLog2Scale);
-                ivs = exp2f(-lvs);
-              }
+#pragma unroll
+      for (int u = 0; u < kMine; ++u) {
+        const int r = gtid + u * kGroup;
+        if (r < kTile) {
+          ms.row[buf][r] = b_at[u];
+          absent = absent || (b_at[u] & kNoRow);
+          if (full && (r & (p.run_rows - 1)) == 0) ms.box[buf][r / p.run_rows] = make_int2(b_page[u], b_slot[u]);
+          if (FP8) {
+            ms.ksc[buf][r] = p.scale_log2 * b_ks[u];
+            if (!WEIGHTS) {
+              const float lv = fmaxf(__log2f(b_vs[u]), kLeastLog2Scale);
+              ms.lvs[buf][r] = lv;
+              ms.ivs[buf][r] = exp2f(-lv);
             }
           }
         }
-        ms.row[buf][r] = at;
-        if (FP8) {
-          ms.ksc[buf][r] = ksc;
-          if (!WEIGHTS) {
-            ms.lvs[buf][r] = lvs;
-            ms.ivs[buf][r] = ivs;
-          }
-        }
+      }
+      if (gtid == 0) {
+        ms.seq[buf] = b_seq;
+        ms.flags[buf] = b_flags;
+        ms.base[buf] = b_base;
+        ms.end[buf] = b_end;
       }
     }
+    __syncwarp();  // the barrier below is one of whole warps
+    const bool odd = bar_red_or(2, kGroup, !ok || (full && absent));
+    if (odd) ok = !bar_red_or(2, kGroup, !ok);
+    const bool tma = full && !odd;
+    if (gtid == 0 && ok) ms.gathered[buf] = !tma;
     mbar_arrive(smem_u32(&ms.list_full[buf]));
-    ok = !bar_red_or(2, kGroup, !ok);  // the list is complete; all go on or none
+    return tma;
   };
   // One part of tile g into the next stage (parts 0-3: K dims 128 part .., 4-7: V).
-  auto emit = [&](int g, int part) -> bool {
-    if (!mbar_wait(smem_u32(&ms.kv_empty[ring.st]), ring.ph ^ 1, abrt, p.timeout_ns, p.err, PSITE_KV_EMPTY))
-      return false;
+  auto emit = [&](int g, int part, bool tma) -> bool {
     const uint32_t stage = sbase + kOffKV + ring.st * kStageBytes;
+    const uint32_t b_full_bar = smem_u32(FP8 ? &ms.code_full[ring.st] : &ms.kv_full[ring.st]);
+    const uint32_t b_empty = smem_u32(&ms.kv_empty[ring.st]), ph = ring.ph ^ 1, st_bit = 1u << ring.st;
+    ring.advance();
+    // Every thread waits for every fill of a stage, whoever loads it: a parity
+    // wait is only right for a thread that has seen the phase before.
+    if (!mbar_wait(b_empty, ph, abrt, p.timeout_ns, p.err, PSITE_KV_EMPTY)) return false;
+    if (tma) {
+      // Run i of a part goes to one lane of warp (turn + i) % warps, so that
+      // the warps share the copies of a part and of successive parts; lane 0
+      // of each warp arrives for all its lanes.
+      const int lane = ltid & 31, runs = kTile / p.run_rows;
+      const int first = gtid / 32 - turn, i = (first < 0 ? first + kWarps : first) + lane * kWarps;
+      turn = (turn + runs) % kWarps;
+      if (lane == 0) {
+        if (gtid == 0) mbar_arrive_expect_tx(b_full_bar, FP8 ? kBoxBytes : kStageBytes);
+        mbar_arrive_cnt(b_full_bar, gtid == 0 ? 31 : 32);
+      }
+      if (i < runs) {
+        filled |= st_bit;
+        last_par = ph ? last_par & ~st_bit : last_par | st_bit;
+        const uint32_t at = i * p.run_rows * (FP8 ? 128u : 256u);
+        const CUtensorMap *m = part >= 4 ? &p.tm_v : &p.tm_k;
+        const int2 x = ms.box[g % kLists][i];
+        if (FP8)
+          tma_load_3d(stage + kBoxBytes + at, m, b_full_bar, 128 * (part & 3), x.y, x.x);
+        else
+          tma_load_5d(stage + at, m, b_full_bar, 0, 0, 2 * (part & 3), x.y >> 3, x.x);
+      }
+      return true;
+    }
     const unsigned long long *list = ms.row[g % kLists];
+    const int dim = (FP8 ? 128 : 256) * (part & 3) + 16 * c8;  // bytes
+    const long long off0 = part >= 4 ? vdelta0 + dim : dim, off1 = part >= 4 ? vdelta1 + dim : dim;
 #pragma unroll
     for (int it = 0; it < (kTile + kRowStep - 1) / kRowStep; ++it) {
       const int row = kRowStep * it + rsub;
       if (kTile % kRowStep != 0 && row >= kTile) break;
       const unsigned long long e = list[row];
-      const uint32_t n = e != 0 ? 16u : 0u;
-      const uint8_t *src = e != 0 ? reinterpret_cast<const uint8_t *>(e & ~15ull) : reinterpret_cast<const uint8_t *>(p.geom);
-      if (part >= 4 && e != 0) src += vdelta[e & 1];
+      const uint32_t n = (e & kNoRow) ? 0u : 16u;
+      const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBit) ? off1 : off0);
       if (FP8) {
-        if (e != 0) src += 128 * (part & 3) + 16 * c8;
         cp_async16z(stage + kBoxBytes + row * 128 + 16 * c8, src, n);
       } else {
-        if (e != 0) src += 256 * (part & 3) + 16 * c8;
-        const uint32_t dst = stage + row * 128 + ((c8 ^ (row & 7)) << 4);
-        cp_async16z(dst, src, n);                                // dims 0-63 of the part
-        cp_async16z(dst + kBoxBytes, e != 0 ? src + 128 : src, n);  // dims 64-127
+        const uint32_t dst = stage + (row >> 3) * group_stride<FP8>() + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4);
+        cp_async16z(dst, src, n);                              // dims 0-63 of the part
+        cp_async16z(dst + block_stride<FP8>(), src + 128, n);  // dims 64-127
       }
     }
-    cp_async_arrive(smem_u32(FP8 ? &ms.code_full[ring.st] : &ms.kv_full[ring.st]));
-    ring.advance();
+    cp_async_arrive(b_full_bar);
     return true;
   };
   auto load_q = [&](int b) {
@@ -354,30 +511,41 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
     ++n_item;
   };
 
-  Walk<WEIGHTS> w;
-  w.start(p, ms);
   if (nt > 0) {
     load_q(w.b);
-    make_list(w, 0);
-    for (int part = 0; part < 4 && ok; ++part) ok = emit(0, part);
+    fetch_pages();
+    fetch_scales();
+    if (nt > 1) fetch_pages();
+    bool tma = store_list(0), tma_next = false;
+    if (nt > 1) fetch_scales();
+    if (nt > 2) fetch_pages();
+    for (int part = 0; part < 4 && ok; ++part) ok = emit(0, part, tma);
     for (int g = 0; g < nt; ++g) {
       if (g + 1 < nt) {
-        w.next(p);
-        if (w.first) load_q(w.b);
-        make_list(w, g + 1);
-        for (int part = 0; part < 4 && ok; ++part) ok = emit(g + 1, part);
+        tma_next = store_list(g + 1);
+        if (g + 2 < nt) fetch_scales();
+        if (g + 3 < nt) fetch_pages();
+        if (ms.flags[(g + 1) % kLists] & kFirst) load_q(ms.seq[(g + 1) % kLists]);
+        for (int part = 0; part < 4 && ok; ++part) ok = emit(g + 1, part, tma_next);
       } else {
+        __syncwarp();
         ok = !bar_red_or(2, kGroup, !ok);
       }
       if (!WEIGHTS)
-        for (int part = 4; part < 8 && ok; ++part) ok = emit(g, part);
+        for (int part = 4; part < 8 && ok; ++part) ok = emit(g, part, tma);
+      tma = tma_next;
     }
   }
-  cp_async_done();  // no copy may still be landing at exit
-  if (ltid == 0 && q_issued) {
-    volatile int never = 0;
-    mbar_wait(b_q_full, q_par, &never, 100000000ull, p.err, PSITE_DRAIN);
-  }
+  // No copy may still be landing at exit.  (When every wait succeeded the MMA
+  // thread has seen all stages land.)
+  cp_async_done();
+  volatile int never = 0;
+  if (*abrt != 0)
+    for (int st = 0; st < kStages; ++st)
+      if (filled & (1u << st))
+        mbar_wait(smem_u32(FP8 ? &ms.code_full[st] : &ms.kv_full[st]), (last_par >> st) & 1, &never, 100000000ull,
+                  p.err, PSITE_DRAIN);
+  if (ltid == 0 && q_issued) mbar_wait(b_q_full, q_par, &never, 100000000ull, p.err, PSITE_DRAIN);
 }
 
 // Warps 9-12 with E4M3 rows: every stage's codes (upper half), one row per
@@ -422,48 +590,60 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams &p, uint32_t 
 
 // ------------------------------------------------------------------ MMA issue
 
+// The whole warp walks the tiles, so that descriptors are warp-uniform values,
+// and one elected lane issues (42 cycles per 128 x 64 x 16 MMA; 61 when a
+// single lane runs the role).  Waits are joined over the warp: all lanes go
+// on or none.
 template <bool FP8, bool WEIGHTS>
-__device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_t sbase, uint32_t tmem, PMisc &ms,
-                                               int lane) {
-  if (lane == 0) {
-    volatile int *abrt = &ms.abort_flag;
-    constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
-    constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
-    const uint64_t k_desc = sdesc_sw128(sbase + kOffKV, 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(sbase + kOffKV, kBoxBytes, 1024);
-    const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
-    const uint64_t p_desc = sdesc_sw128(sbase + kOffP, 16, 1024);
-    StageRing ring;
-    const int nt = ms.n_tiles;
-    uint32_t q_item = 0, o_item = 0;
-    bool ok = true;
-    // Rows copied by cp.async are generic-proxy writes; the fence makes the
-    // landed stage visible to the tensor core.
-    auto stage_ready = [&]() -> bool {
-      if (!mbar_wait(smem_u32(&ms.kv_full[ring.st]), ring.ph, abrt, p.timeout_ns, p.err, PSITE_KV_FULL)) return false;
-      if (!FP8) fence_proxy_async_smem();
-      tc_fence_after();
-      return true;
-    };
-    auto qk = [&](int g, bool first, bool last) -> bool {
-      if (first) {
-        if (!mbar_wait(smem_u32(&ms.q_full), q_item & 1, abrt, p.timeout_ns, p.err, PSITE_Q_FULL)) return false;
-        ++q_item;
-      }
-      const uint32_t sb = g & 1;
-      if (!mbar_wait(smem_u32(&ms.s_empty[sb]), ((g >> 1) & 1) ^ 1, abrt, p.timeout_ns, p.err, PSITE_S_EMPTY))
-        return false;
-      tc_fence_after();
-      const uint32_t d_s = tmem + kTmemS + 64 * sb;
-      for (int c = 0; c < 4; ++c) {
-        if (!stage_ready()) return false;
-        const uint64_t a0 = sdesc_add(k_desc, ring.st * kStageBytes);
-        const uint64_t b0 = sdesc_add(q_desc, 2 * c * kQBoxBytes);
+__device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_t sbase, uint32_t tmem, PMisc &ms) {
+  volatile int *abrt = &ms.abort_flag;
+  constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
+  constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
+  // K tiles and Q: K-major.  V tiles: MN-major, LBO = distance of the 64-dim
+  // blocks, SBO = distance of 8-row groups.  P^T: one 64-head MN atom.
+  constexpr uint32_t kGrp = group_stride<FP8>(), kBlk = block_stride<FP8>();
+  const uint64_t k_desc = sdesc_sw128(sbase + kOffKV, 16, kGrp);
+  const uint64_t v_desc = sdesc_sw128(sbase + kOffKV, kBlk, kGrp);
+  const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
+  const uint64_t p_desc = sdesc_sw128(sbase + kOffP, 16, 1024);
+  StageRing ring;
+  const int nt = ms.n_tiles;
+  uint32_t q_item = 0, o_item = 0;
+  bool ok = true;
+  auto wait = [&](uint64_t &bar, uint32_t parity, unsigned int site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abrt, p.timeout_ns, p.err, site));
+  };
+  auto commit = [&](uint64_t &bar) {
+    if (elect_lane()) umma_commit(smem_u32(&bar));
+  };
+  // Gathered rows (cp.async) are generic-proxy writes: the fence makes the
+  // landed stage visible to the tensor core.  TMA writes, and the widened
+  // rows (fenced by the converters), need none.
+  auto stage_ready = [&](int g) -> bool {
+    if (!wait(ms.kv_full[ring.st], ring.ph, PSITE_KV_FULL)) return false;
+    if (!FP8 && ms.gathered[g % kLists]) fence_proxy_async_smem();
+    tc_fence_after();
+    return true;
+  };
+  auto qk = [&](int g, bool first, bool last) -> bool {
+    if (first) {
+      if (!wait(ms.q_full, q_item & 1, PSITE_Q_FULL)) return false;
+      ++q_item;
+    }
+    const uint32_t sb = g & 1;
+    if (!wait(ms.list_full[g % kLists], (g / kLists) & 1, PSITE_LIST_FULL)) return false;
+    if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, PSITE_S_EMPTY)) return false;
+    const uint32_t d_s = tmem + kTmemS + 64 * sb;
+    for (int c = 0; c < 4; ++c) {
+      if (!stage_ready(g)) return false;
+      const uint64_t a0 = sdesc_add(k_desc, ring.st * kStageBytes);
+      const uint64_t b0 = sdesc_add(q_desc, 2 * c * kQBoxBytes);
+      if (elect_lane()) {
 #pragma unroll
         for (int b2 = 0; b2 < 2; ++b2) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t a = sdesc_add(a0, b2 * kBoxBytes + ks * 32);
+            const uint64_t a = sdesc_add(a0, b2 * kBlk + ks * 32);
             const uint64_t b = sdesc_add(b0, b2 * kQBoxBytes + ks * 32);
             if (b2 == 0 && ks == 0)
               umma_f16(d_s, a, b, kIdescQK, c != 0 ? 1u : 0u);
@@ -472,26 +652,27 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
           }
         }
         umma_commit(smem_u32(&ms.kv_empty[ring.st]));
-        ring.advance();
+        if (c == 3) umma_commit(smem_u32(&ms.s_full[sb]));
+        if (c == 3 && last) umma_commit(smem_u32(&ms.q_empty));
       }
-      umma_commit(smem_u32(&ms.s_full[sb]));
-      if (last) umma_commit(smem_u32(&ms.q_empty));
-      return true;
-    };
-    auto pv = [&](int g, bool first, bool last) -> bool {
-      if (!mbar_wait(smem_u32(&ms.p_full), g & 1, abrt, p.timeout_ns, p.err, PSITE_P_FULL)) return false;
-      if (first) {
-        if (!mbar_wait(smem_u32(&ms.o_empty), (o_item & 1) ^ 1, abrt, p.timeout_ns, p.err, PSITE_O_EMPTY))
-          return false;
-        ++o_item;
-      }
-      tc_fence_after();
-      for (int m = 0; m < 4; ++m) {
-        if (!stage_ready()) return false;
-        const uint64_t a0 = sdesc_add(v_desc, ring.st * kStageBytes);
+      __syncwarp();
+      ring.advance();
+    }
+    return true;
+  };
+  auto pv = [&](int g, bool first, bool last) -> bool {
+    if (!wait(ms.p_full, g & 1, PSITE_P_FULL)) return false;
+    if (first) {
+      if (!wait(ms.o_empty, (o_item & 1) ^ 1, PSITE_O_EMPTY)) return false;
+      ++o_item;
+    }
+    for (int m = 0; m < 4; ++m) {
+      if (!stage_ready(g)) return false;
+      const uint64_t a0 = sdesc_add(v_desc, ring.st * kStageBytes);
+      if (elect_lane()) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const uint64_t a = sdesc_add(a0, ks * 2048);
+          const uint64_t a = sdesc_add(a0, ks * 2 * kGrp);
           const uint64_t b = sdesc_add(p_desc, ks * 2048);
           if (ks == 0)
             umma_f16(tmem + 64 * m, a, b, kIdescPV, first ? 0u : 1u);
@@ -500,26 +681,27 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
         }
         umma_commit(smem_u32(&ms.kv_empty[ring.st]));
         if (last) umma_commit(smem_u32(&ms.o_full[m]));
-        ring.advance();
+        if (m == 3) umma_commit(smem_u32(&ms.p_empty));
       }
-      umma_commit(smem_u32(&ms.p_empty));
-      return true;
-    };
-    Walk<WEIGHTS> w;
-    w.start(p, ms);
-    if (nt > 0) ok = qk(0, true, w.last);
-    for (int g = 0; g < nt && ok; ++g) {
-      const bool first = w.first, last = w.last;
-      if (g + 1 < nt) {
-        w.next(p);
-        ok = qk(g + 1, w.first, w.last);
-      }
-      if (!WEIGHTS) ok = ok && pv(g, first, last);
+      __syncwarp();
+      ring.advance();
     }
-    umma_commit(smem_u32(&ms.mma_done));
-    volatile int never = 0;
-    mbar_wait(smem_u32(&ms.mma_done), 0, &never, 100000000ull, p.err, PSITE_DRAIN);
+    return true;
+  };
+  Walk<WEIGHTS> w;
+  w.start(p, ms);
+  if (nt > 0) ok = qk(0, true, w.last);
+  for (int g = 0; g < nt && ok; ++g) {
+    const bool first = w.first, last = w.last;
+    if (g + 1 < nt) {
+      w.next(p);
+      ok = qk(g + 1, w.first, w.last);
+    }
+    if (!WEIGHTS) ok = ok && pv(g, first, last);
   }
+  commit(ms.mma_done);
+  volatile int never = 0;
+  mbar_wait(smem_u32(&ms.mma_done), 0, &never, 100000000ull, p.err, PSITE_DRAIN);
   __syncwarp();
 }
 
@@ -539,21 +721,17 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
   uint32_t n_item = 0;
   float m_ref = -INFINITY;  // reference of head `tid` (threads < 64), log2 units
   float lpart[32];
-  int first_j = 0;
-  Walk<false> w;
-  w.start(p, ms);
   for (int g = 0; g < nt; ++g) {
-    if (g > 0) w.next(p);
-    if (w.first) {
-      first_j = w.j;
+    const int buf = g % kLists;
+    const uint32_t sb = g & 1;
+    bad = bad || !mbar_wait(smem_u32(&ms.list_full[buf]), (g / kLists) & 1, abrt, p.timeout_ns, p.err, PSITE_LIST_FULL);
+    const int flags = ms.flags[buf], seq = ms.seq[buf];
+    if (flags & kFirst) {
       m_ref = -INFINITY;
 #pragma unroll
       for (int h = 0; h < 32; ++h) lpart[h] = 0.f;
     }
-    const int buf = g % kLists;
-    const uint32_t sb = g & 1;
-    bad = bad || !mbar_wait(smem_u32(&ms.list_full[buf]), (g / kLists) & 1, abrt, p.timeout_ns, p.err, PSITE_LIST_FULL);
-    const bool vis = ms.row[buf][r] != 0;
+    const bool vis = (ms.row[buf][r] & kNoRow) == 0;
     const float sl2 = FP8 ? ms.ksc[buf][r] : p.scale_log2;
     const float lvs = FP8 ? ms.lvs[buf][r] : 0.f;
     const float ivs = FP8 ? ms.ivs[buf][r] : 1.f;
@@ -587,12 +765,6 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
     const int resc = ms.resc_flag[g & 1];
     if (tid == 0) ms.resc_flag[(g + 1) & 1] = 0;
     bad = bad || !mbar_wait(smem_u32(&ms.p_empty), (g & 1) ^ 1, abrt, p.timeout_ns, p.err, PSITE_P_EMPTY);
-    if (resc) {
-      float al[32];
-      load_row32(ms.alpha + col0, al);
-#pragma unroll
-      for (int h = 0; h < 32; ++h) lpart[h] *= al[h];
-    }
     {
       // P^T row r: heads 32hh .. +31 are 16-byte chunks 4hh .. 4hh+3 of its
       // 128 bytes, chunk c at c ^ (r & 7).  P is rounded once to fp16 for the
@@ -605,6 +777,13 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
         const float4 m0 = reinterpret_cast<const float4 *>(ms.m_use + col0)[2 * c];
         const float4 m1 = reinterpret_cast<const float4 *>(ms.m_use + col0)[2 * c + 1];
         const float mu[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+        if (resc) {
+          const float4 a0 = reinterpret_cast<const float4 *>(ms.alpha + col0)[2 * c];
+          const float4 a1 = reinterpret_cast<const float4 *>(ms.alpha + col0)[2 * c + 1];
+          const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) lpart[8 * c + i] *= al[i];
+        }
         uint32_t w4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -618,9 +797,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
         *reinterpret_cast<uint4 *>(prow + (((4 * hh + c) ^ (r & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
       }
     }
-    if (resc && !w.first) {
-      float al[32];
-      load_row32(ms.alpha + col0, al);
+    if (resc && !(flags & kFirst)) {
       tc_fence_after();
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
@@ -628,7 +805,13 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
         tmem_ld32(tmem + 64 * m + col0 + lane_base, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 32; ++h) o[h] *= al[h];
+        for (int c = 0; c < 8; ++c) {
+          const float4 a = reinterpret_cast<const float4 *>(ms.alpha + col0)[c];
+          o[4 * c] *= a.x;
+          o[4 * c + 1] *= a.y;
+          o[4 * c + 2] *= a.z;
+          o[4 * c + 3] *= a.w;
+        }
         tmem_st32(tmem + 64 * m + col0 + lane_base, o);
       }
       tmem_wait_st();
@@ -636,11 +819,13 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
     fence_proxy_async_smem();
     tc_fence_before();
     mbar_arrive(smem_u32(&ms.p_full));
-    if (!w.last) continue;
+    if (!(flags & kLast)) continue;
 
-    // End of an item: row sums, then o block by block as the last PV finishes them.
-    const bool whole = w.whole(first_j);
-    const long long slot = (long long)blockIdx.x + w.b;
+    // End of an item: row sums, then o block by block as the last PV finishes
+    // them: fp16 and normalised for a whole sequence, else fp32 and normalised
+    // by the item's own sum.
+    const bool whole = flags & kWhole;
+    const long long slot = (long long)blockIdx.x + seq;
     ms.red[q][col0 + l] = reduce_heads<false>(lpart, l);
     if (bar_red_or(1, kComputeThreads, bad)) break;
     if (tid < kH) {
@@ -649,15 +834,12 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
       if (!whole) {
         p.ws_ml[slot * kH + tid] = make_float2(lsum > 0.f ? m_ref : -INFINITY, lsum);
       } else if (p.lse != nullptr) {
-        p.lse[(long long)w.b * kH + tid] = lsum > 0.f ? (m_ref + log2f(lsum)) * kLn2 : -INFINITY;
+        p.lse[(long long)seq * kH + tid] = lsum > 0.f ? (m_ref + log2f(lsum)) * kLn2 : -INFINITY;
       }
     }
     bar_sync_id(1, kComputeThreads);
     float inv[32];
     load_row32(ms.inv_l + col0, inv);
-    const bool odd = l & 1;
-    __half *obase = whole ? p.o + w.b * p.o_stride + (long long)col0 * kD + (r & ~1)
-                          : p.ws_o + (slot * kH + col0) * kD + (r & ~1);
 #pragma unroll 1
     for (int m = 0; m < 4; ++m) {
       bad = bad || !mbar_wait(smem_u32(&ms.o_full[m]), n_item & 1, abrt, p.timeout_ns, p.err, PSITE_O_FULL);
@@ -665,12 +847,21 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
       float o[32];
       tmem_ld32(tmem + 64 * m + col0 + lane_base, o);
       tmem_wait_ld();
+      if (whole) {
+        // Lanes 2k and 2k + 1 hold adjacent dims: they swap one value per pair
+        // of heads and write half2.
+        const bool odd = l & 1;
+        __half *at = p.o + seq * p.o_stride + (long long)(col0 + (odd ? 1 : 0)) * kD + 128 * m + (r & ~1);
 #pragma unroll
-      for (int h = 0; h < 32; h += 2) {
-        const float a = o[h] * inv[h], c = o[h + 1] * inv[h + 1];
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-        const __half2 v = odd ? __floats2half2_rn(got, c) : __floats2half2_rn(a, got);
-        *reinterpret_cast<__half2 *>(obase + (h + (odd ? 1 : 0)) * kD + 128 * m) = v;
+        for (int h = 0; h < 32; h += 2) {
+          const float a = o[h] * inv[h], c = o[h + 1] * inv[h + 1];
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+          *reinterpret_cast<__half2 *>(at + h * kD) = odd ? __floats2half2_rn(got, c) : __floats2half2_rn(a, got);
+        }
+      } else {
+        float *at = p.ws_o + (slot * kH + col0) * kD + 128 * m + r;
+#pragma unroll
+        for (int h = 0; h < 32; ++h) at[h * kD] = o[h] * inv[h];
       }
     }
     tc_fence_before();
@@ -693,26 +884,23 @@ __device__ __forceinline__ void weights_role(const PagedAttnParams &p, uint32_t 
   const int nt = ms.n_tiles;
   bool bad = false;
   float *part = &ms.red[0][0];  // [2][128] by tile parity (256 floats)
-  Walk<true> w;
-  w.start(p, ms);
   for (int g = 0; g < nt; ++g) {
-    if (g > 0) w.next(p);
-    if (w.first) {
+    const int buf = g % kLists;
+    const uint32_t sb = g & 1;
+    bad = bad || !mbar_wait(smem_u32(&ms.list_full[buf]), (g / kLists) & 1, abrt, p.timeout_ns, p.err, PSITE_LIST_FULL);
+    const int seq = ms.seq[buf], c = ms.base[buf] + r;
+    const bool mine = hh == 0 && c < ms.end[buf];
+    const float before = mine && p.acc_in != nullptr ? p.acc_in[seq * p.acc_in_stride + c] : 0.f;
+    if (ms.flags[buf] & kFirst) {
       // 2^(s - lse log2 e); a head whose lse is -inf gave no weight to anything.
       bar_sync_id(1, kComputeThreads);
       if (tid < kH) {
-        const float v = p.lse_in[(long long)w.b * kH + tid];
+        const float v = p.lse_in[(long long)seq * kH + tid];
         ms.m_use[tid] = v == -INFINITY ? INFINITY : v * kLog2e;
       }
       bar_sync_id(1, kComputeThreads);
     }
-    const int buf = g % kLists;
-    const uint32_t sb = g & 1;
-    const int c = w.j * kTile + r;
-    const bool mine = hh == 0 && c < w.rows.nc;
-    const float before = mine && p.acc_in != nullptr ? p.acc_in[w.b * p.acc_in_stride + c] : 0.f;
-    bad = bad || !mbar_wait(smem_u32(&ms.list_full[buf]), (g / kLists) & 1, abrt, p.timeout_ns, p.err, PSITE_LIST_FULL);
-    const bool vis = ms.row[buf][r] != 0;
+    const bool vis = (ms.row[buf][r] & kNoRow) == 0;
     const float sl2 = FP8 ? ms.ksc[buf][r] : p.scale_log2;
     mbar_arrive(smem_u32(&ms.list_empty[buf]));
     bad = bad || !mbar_wait(smem_u32(&ms.s_full[sb]), (g >> 1) & 1, abrt, p.timeout_ns, p.err, PSITE_S_FULL);
@@ -731,7 +919,7 @@ __device__ __forceinline__ void weights_role(const PagedAttnParams &p, uint32_t 
     if (bar_red_or(1, kComputeThreads, bad)) break;
     if (mine) {
       const float got = vis ? sum + part[128 * (g & 1) + r] : 0.f;
-      p.acc_out[w.b * p.acc_out_stride + c] = fmaf(p.decay, before, got);
+      p.acc_out[seq * p.acc_out_stride + c] = fmaf(p.decay, before, got);
     }
   }
 }
@@ -744,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   PMisc &ms = *reinterpret_cast<PMisc *>(smem + kOffMisc);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ms.q_full), 1);
     mbar_init(smem_u32(&ms.q_empty), 1);
@@ -770,6 +958,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     ms.resc_flag[0] = ms.resc_flag[1] = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.tm_q);
+    if (p.run_rows > 0) {
+      tma_prefetch_desc(&p.tm_k);
+      if (!WEIGHTS) tma_prefetch_desc(&p.tm_v);
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&ms.tmem_base), kTmemCols);
@@ -788,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     else
       softmax_role<FP8>(p, smem, tmem, ms, threadIdx.x);
   } else if (warp == kMmaWarp) {
-    mma_role_paged<FP8, WEIGHTS>(p, sbase, tmem, ms, lane);
+    mma_role_paged<FP8, WEIGHTS>(p, sbase, tmem, ms);
   } else {
     const int ltid = threadIdx.x - 32 * kLoaderWarp0;
     if (FP8 && ltid >= 32 && ltid < 32 + kTile)
@@ -803,57 +995,108 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ merge
-// One block per (sequence, head): with M = max_s m_s and W_s = 2^(m_s - M) l_s,
+// With M = max_s m_s and W_s = 2^(m_s - M) l_s over the slots of a sequence:
 //   o = sum_s W_s o_s / L,  L = sum_s W_s,  lse = (M + log2 L) ln 2.
-// A sequence one CTA finished alone (one slot) is left alone; one without
-// rows (no slot) gets o = 0 and lse = -inf.  Eight threads of 16 bytes cover 64
-// dims, the block 512 dims of four slots at a time.
+// A sequence that one CTA finished (one slot) is left alone; one without rows
+// (no slot) gets o = 0 and lse = -inf.  A block takes 128 VEC dims of one head
+// of one sequence, its warps share the slots (warp w: w, w + WARPS, ..), a lane
+// holds VEC float4, and the warps meet in shared memory.  A warp's first slots are
+// loaded together with their (m, l), before the weights are known.  Two
+// shapes: VEC = 4, 4 warps (64 small blocks a sequence, for batches, where a
+// sequence has a few slots), VEC = 1, 8 warps (256 blocks a sequence, for a few
+// long sequences with up to one slot per SM).
 
-constexpr int kMergeThreads = 256;
+constexpr int kMergeLoads = 8;  // float4 in flight per lane
 
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p) {
-  __shared__ float part[kMergeThreads / 64][kD];
+template <int VEC, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) paged_merge_kernel(const PagedAttnParams p) {
+  constexpr int kChunks = kD / (128 * VEC), kRound = kMergeLoads / VEC;  // slots per warp and round
+  __shared__ float2 wl[WARPS];          // (M, L) of each warp's slots
+  __shared__ float4 part[WARPS][32 * VEC];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int b = blockIdx.x / kH, h = blockIdx.x - b * kH;
-  const int tid = threadIdx.x, grp = tid >> 6, v = tid & 63;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int item = blockIdx.x / kChunks, chunk = blockIdx.x - item * kChunks;
+  const int b = item / kH, h = item - b * kH;
   const int2 plan = __ldg(p.ws_plan + b);
-  if (plan.y == 1) return;
-  const long long base = plan.x;
-  float M = -INFINITY;
-  for (int s = 0; s < plan.y; ++s) M = fmaxf(M, p.ws_ml[(base + s) * kH + h].x);
-  float L = 0.f;
-  float acc[8];
+  const int n = plan.y;
+  if (n == 1) return;
+  const float2 *ml = p.ws_ml + (long long)plan.x * kH + h;
+  const float4 *src =
+      reinterpret_cast<const float4 *>(p.ws_o + ((long long)plan.x * kH + h) * kD + 128 * VEC * chunk) + lane;
+  constexpr long long kStep = (long long)kH * kD / 4;  // one slot, in float4
+  float4 acc[VEC];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (int s = 0; s < plan.y; ++s) {
-    const float2 ml = p.ws_ml[(base + s) * kH + h];
-    const float wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M) * ml.y;
-    L += wgt;
-    if ((s & 3) == grp) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.ws_o + ((base + s) * kH + h) * kD) + v);
-      const __half2 *h2 = reinterpret_cast<const __half2 *>(&x);
+  for (int e = 0; e < VEC; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, L = 0.f;  // of this warp's slots so far
+  for (int s0 = warp; s0 < n; s0 += WARPS * kRound) {
+    float4 x[kRound][VEC];
+    float2 q[kRound];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(h2[e]);
-        acc[2 * e] = fmaf(wgt, f.x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(wgt, f.y, acc[2 * e + 1]);
+    for (int k = 0; k < kRound; ++k) {
+      const int s = s0 + k * WARPS;
+      q[k] = s < n ? __ldg(ml + s * kH) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        x[k][e] = s < n ? __ldg(src + s * kStep + 32 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) top = fmaxf(top, q[k].x);
+    if (top == -INFINITY) continue;
+    const float old = exp2f(M - top);  // 0 while nothing has been added
+    M = top;
+    L *= old;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      acc[e].x *= old;
+      acc[e].y *= old;
+      acc[e].z *= old;
+      acc[e].w *= old;
+    }
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) {
+      const float t = exp2f(q[k].x - top) * q[k].y;
+      L += t;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        acc[e].x = fmaf(t, x[k][e].x, acc[e].x);
+        acc[e].y = fmaf(t, x[k][e].y, acc[e].y);
+        acc[e].z = fmaf(t, x[k][e].z, acc[e].z);
+        acc[e].w = fmaf(t, x[k][e].w, acc[e].w);
       }
     }
   }
+  if (lane == 0) wl[warp] = make_float2(M, L);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) part[grp][8 * v + e] = acc[e];
+  for (int e = 0; e < VEC; ++e) part[warp][lane + 32 * e] = acc[e];
   __syncthreads();
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  float2 o = make_float2(0.f, 0.f);
+  M = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kMergeThreads / 64; ++i) {
-    o.x += part[i][2 * tid];
-    o.y += part[i][2 * tid + 1];
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, wl[w].x);
+  L = 0.f;
+  float t[WARPS];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    t[w] = M == -INFINITY ? 0.f : exp2f(wl[w].x - M);
+    L = fmaf(t[w], wl[w].y, L);
   }
-  *reinterpret_cast<__half2 *>(p.o + b * p.o_stride + (long long)h * kD + 2 * tid) =
-      __floats2half2_rn(o.x * inv, o.y * inv);
-  if (p.lse != nullptr && tid == 0)
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  for (int v = threadIdx.x; v < 32 * VEC; v += 32 * WARPS) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float4 y = part[w][v];
+      o.x = fmaf(t[w], y.x, o.x);
+      o.y = fmaf(t[w], y.y, o.y);
+      o.z = fmaf(t[w], y.z, o.z);
+      o.w = fmaf(t[w], y.w, o.w);
+    }
+    const __half2 a = __floats2half2_rn(o.x * inv, o.y * inv), c = __floats2half2_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2 *>(p.o + b * p.o_stride + (long long)h * kD + 128 * VEC * chunk + 4 * v) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+  }
+  if (p.lse != nullptr && chunk == 0 && threadIdx.x == 0)
     p.lse[(long long)b * kH + h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
@@ -880,7 +1123,8 @@ cudaError_t launch_paged_decode(const PagedAttnParams &p, bool e4m3, int grid, c
 }
 
 cudaError_t launch_paged_merge(const PagedAttnParams &p, cudaStream_t s) {
-  return launch_pdl((const void *)paged_merge_kernel, p, p.n_seq * kH, kMergeThreads, 0, s);
+  if (p.n_seq <= 8) return launch_pdl((const void *)paged_merge_kernel<1, 8>, p, p.n_seq * kH * 4, 256, 0, s);
+  return launch_pdl((const void *)paged_merge_kernel<4, 4>, p, p.n_seq * kH, 128, 0, s);
 }
 
 cudaError_t launch_paged_weights(const PagedAttnParams &p, bool e4m3, int grid, cudaStream_t s) {
@@ -895,7 +1139,8 @@ cudaError_t prepare_paged_kernels() {
     if (e != cudaSuccess) return e;
   }
   cudaFuncAttributes a;
-  return cudaFuncGetAttributes(&a, (const void *)paged_merge_kernel);
+  const cudaError_t e = cudaFuncGetAttributes(&a, (const void *)paged_merge_kernel<1, 8>);
+  return e != cudaSuccess ? e : cudaFuncGetAttributes(&a, (const void *)paged_merge_kernel<4, 4>);
 }
 
 }  // namespace ds4a

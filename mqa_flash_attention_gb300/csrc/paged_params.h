@@ -22,6 +22,11 @@ struct PagedSeg {
 
 struct PagedAttnParams {
   CUtensorMap tm_q;        // 4-D {64, 64 heads, n_seq, 8 dim blocks}, box {64, 64, 1, 8}
+  // Compressed rows by runs of run_rows rows: fp16 5-D {64 dims, 8 rows, 8
+  // blocks, page_rows / 8, pages}, box {64, 8, 2, run_rows / 8, 1}; codes 3-D
+  // {512, page_rows, pages}, box {128, run_rows, 1}.
+  CUtensorMap tm_k, tm_v;
+  int run_rows;            // 8 .. 128, a power of two; 0: no TMA loads
   PagedSeg seg[2];         // raw, compressed
   const int4 *geom;        // (q_pos, n_raw, raw_pos0, n_comp) per sequence
   int n_seq, ratio, window;
@@ -29,7 +34,7 @@ struct PagedAttnParams {
   __half *o;
   long long o_stride;      // elements
   float *lse;              // decode: written, or NULL
-  __half *ws_o;            // [slots][64][512] normalised partial outputs
+  float *ws_o;             // [slots][64][512] normalised partial outputs
   float2 *ws_ml;           // [slots][64] (m in log2 units, l)
   int2 *ws_plan;           // [n_seq] (first slot, slots) of the sequences split over several CTAs
   const float *lse_in;     // weights: [n_seq][64]

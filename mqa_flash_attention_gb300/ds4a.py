@@ -70,6 +70,28 @@ class PagedBatch(ctypes.Structure):
                 ("o", ctypes.c_void_p), ("o_seq_stride", ctypes.c_int64), ("lse", ctypes.c_void_p)]
 
 
+class Eviction(ctypes.Structure):
+    _fields_ = [("weights", ctypes.c_void_p), ("weight_stride", ctypes.c_int64),
+                ("ids", ctypes.c_void_p), ("id_stride", ctypes.c_int64),
+                ("n_keep", ctypes.c_int32), ("n_first", ctypes.c_int32), ("n_recent", ctypes.c_int32),
+                ("kept", ctypes.c_void_p), ("kept_stride", ctypes.c_int64),
+                ("weights_out", ctypes.c_void_p), ("weight_out_stride", ctypes.c_int64),
+                ("ids_out", ctypes.c_void_p), ("id_out_stride", ctypes.c_int64),
+                ("n_out", ctypes.c_void_p), ("n_out_stride", ctypes.c_int64)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("width", ctypes.c_int32), ("x_fp32", ctypes.c_int32),
+                ("group", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("residual_out", ctypes.c_void_p), ("residual_out_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("codes", ctypes.c_void_p), ("code_stride", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -152,13 +174,11 @@ def lib() -> ctypes.CDLL:
         L.ds4a_evict_paged_workspace_size.restype = sz
         L.ds4a_evict_paged_workspace_size.argtypes = [i32, i32]
         L.ds4a_evict_paged.restype = st
-        L.ds4a_evict_paged.argtypes = [i32, PL, vp, PP, vp, i64, vp, i64, i32, i32, i32, vp, i64, vp, i64, vp, i64,
-                                       vp, i64, vp, sz, vp]
+        L.ds4a_evict_paged.argtypes = [i32, PL, vp, PP, ctypes.POINTER(Eviction), vp, sz, vp]
         L.ds4a_append_paged.restype = st
         L.ds4a_append_paged.argtypes = [PP, i32, vp, vp, i64, vp, vp]
         L.ds4a_rmsnorm_fp8.restype = st
-        L.ds4a_rmsnorm_fp8.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, f32, i32, vp, i64, vp, i64, vp,
-                                       i64, vp]
+        L.ds4a_rmsnorm_fp8.argtypes = [ctypes.POINTER(Norm), vp]
         L.ds4a_device_status.restype = st
         L.ds4a_device_status.argtypes = [vp, ctypes.c_int]
         L.ds4a_device_error_word.restype = st
@@ -1022,11 +1042,12 @@ def prepare_evict_paged(shape, seq_geom, rows, weights, n_keep, *, n_first=0, n_
         raise ValueError(f"n_out must be int32 [>= {B}]")
     _on_device(n_out=n_out)
     workspace, nbytes = _bytes_of(workspace, evict_paged_workspace_bytes(B, n_keep), weights)
-    args = (B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(rows._c), wp, wst, ip, ist, n_keep, int(n_first),
-            int(n_recent), kp, kst, wop, wost, iop, iost, _ptr(n_out), max(n_out.stride(0), 1) * 4, _ptr(workspace),
-            nbytes, _stream(stream))
+    E = Eviction(wp, wst, ip, ist, n_keep, int(n_first), int(n_recent), kp, kst, wop, wost, iop, iost, _ptr(n_out),
+                 max(n_out.stride(0), 1) * 4)
+    args = (B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(rows._c), ctypes.byref(E), _ptr(workspace), nbytes,
+            _stream(stream))
     return PreparedCall(lib().ds4a_evict_paged, "ds4a_evict_paged", args,
-                        (S, seq_geom, rows, weights, ids, kept, weights_out, ids_out, n_out, workspace, stream))
+                        (S, E, seq_geom, rows, weights, ids, kept, weights_out, ids_out, n_out, workspace, stream))
 
 
 def evict_paged(shape, seq_geom, rows, weights, n_keep, *, n_first=0, n_recent=0, ids=None, kept=None,
@@ -1116,10 +1137,10 @@ def prepare_rmsnorm_fp8(x, weight, *, eps=1e-6, residual=None, residual_out=None
         _on_device(scales=scales)
         sp, ss = _ptr(scales), max(scales.stride(0), groups) * 4
     _on_device(weight=weight)
-    args = (n, width, 1 if x.dtype == torch.float32 else 0, xp, xs, rp, rs, rop, ros, _ptr(weight), float(eps),
-            int(group), cp, cs, sp, ss, yp, ys, _stream(stream))
-    return PreparedCall(lib().ds4a_rmsnorm_fp8, "ds4a_rmsnorm_fp8", args,
-                        (x, weight, residual, residual_out, codes, scales, y, stream))
+    N = Norm(n, width, 1 if x.dtype == torch.float32 else 0, int(group), xp, xs, rp, rs, rop, ros, _ptr(weight),
+             float(eps), cp, cs, sp, ss, yp, ys)
+    return PreparedCall(lib().ds4a_rmsnorm_fp8, "ds4a_rmsnorm_fp8", (ctypes.byref(N), _stream(stream)),
+                        (N, x, weight, residual, residual_out, codes, scales, y, stream))
 
 
 def rmsnorm_fp8(x, weight, *, eps=1e-6, residual=None, residual_out=None, group=0, codes=None, scales=None, y=None,

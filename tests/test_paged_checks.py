@@ -3,6 +3,7 @@ rejects bad arguments before touching CUDA (an unsupported device or a CUDA
 error is what a call with good ones answers here), and the binding rejects
 tensors that do not fit."""
 
+import concurrent.futures as cf
 import ctypes
 import math
 
@@ -41,8 +42,14 @@ def batch(raw=None, comp=None, **kw):
 def decode(lib, X, n=2, shape=None, geom=7 * AT, ws=1 << 30, nbytes=None):
     S = ds4a.make_layout(dict(SHAPE, **(shape or {})))
     need = lib.ds4a_attn_decode_paged_workspace_size(n)
-    return lib.ds4a_attn_decode_paged(n, ctypes.byref(S), geom, ctypes.byref(X), ws, need if nbytes is None else nbytes,
-                                      None)
+    return elsewhere(lib.ds4a_attn_decode_paged, n, ctypes.byref(S), geom, ctypes.byref(X), ws,
+                     need if nbytes is None else nbytes, None)
+
+
+def elsewhere(fn, *args):
+    """A call on a thread of its own: the CUDA error text is kept per thread."""
+    with cf.ThreadPoolExecutor(1) as ex:
+        return ex.submit(fn, *args).result()
 
 
 def passes(status):
@@ -102,8 +109,8 @@ def test_bad_decode_calls_are_refused(lib):
 
 def weights(lib, X=None, acc=8 * AT, acc_stride=512, decay=1.0, out=9 * AT, out_stride=512, n=2):
     S = ds4a.make_layout(SHAPE)
-    return lib.ds4a_attn_weights_paged(n, ctypes.byref(S), 7 * AT, ctypes.byref(X or batch()), acc, acc_stride, decay,
-                                       out, out_stride, None)
+    return elsewhere(lib.ds4a_attn_weights_paged, n, ctypes.byref(S), 7 * AT, ctypes.byref(X or batch()), acc,
+                     acc_stride, decay, out, out_stride, None)
 
 
 @needs_no_gpu
@@ -123,9 +130,10 @@ def evict(lib, rows=None, n=2, keep=100, first=0, recent=0, w=8 * AT, ws=512, id
           kept_stride=400, wo=None, wo_stride=0, io=None, io_stride=0, n_out=10 * AT, no_stride=4, work=1 << 30,
           nbytes=1 << 20, geom=7 * AT):
     S = ds4a.make_layout(SHAPE)
-    return lib.ds4a_evict_paged(n, ctypes.byref(S), geom, ctypes.byref(rows or seg()), w, ws, ids, ids_stride, keep,
-                                first, recent, kept, kept_stride, wo, wo_stride, io, io_stride, n_out, no_stride, work,
-                                nbytes, None)
+    E = ds4a.Eviction(w, ws, ids, ids_stride, keep, first, recent, kept, kept_stride, wo, wo_stride, io, io_stride,
+                      n_out, no_stride)
+    return elsewhere(lib.ds4a_evict_paged, n, ctypes.byref(S), geom, ctypes.byref(rows or seg()), ctypes.byref(E), work,
+                     nbytes, None)
 
 
 @needs_no_gpu
@@ -149,7 +157,7 @@ def test_evict_arguments_are_checked(lib):
 
 
 def append(lib, rows=None, n=4, k=8 * AT, v=9 * AT, stride=1024, slots=10 * AT):
-    return lib.ds4a_append_paged(ctypes.byref(rows or seg()), n, k, v, stride, slots, None)
+    return elsewhere(lib.ds4a_append_paged, ctypes.byref(rows or seg()), n, k, v, stride, slots, None)
 
 
 @needs_no_gpu
@@ -166,7 +174,8 @@ def test_append_arguments_are_checked(lib):
 
 def norm(lib, n=3, width=64, f32=0, x=AT, xs=128, r=None, rs=0, ro=None, ros=0, w=2 * AT, eps=1e-6, group=0, c=3 * AT,
          cs=64, s=4 * AT, ss=4, y=None, ys=0):
-    return lib.ds4a_rmsnorm_fp8(n, width, f32, x, xs, r, rs, ro, ros, w, eps, group, c, cs, s, ss, y, ys, None)
+    N = ds4a.Norm(n, width, f32, group, x, xs, r, rs, ro, ros, w, eps, c, cs, s, ss, y, ys)
+    return elsewhere(lib.ds4a_rmsnorm_fp8, ctypes.byref(N), None)
 
 
 @needs_no_gpu
