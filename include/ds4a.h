@@ -683,8 +683,9 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
  *     code = E4M3(y * (448 / m)), scale = m / 448, m = the largest |y| of the group,
  * the format of ds4a_quantize_kv_fp8 with a scale per `group` values (group
  * 0: one per row).  h stays in fp32 for the norm and is rounded once into
- * residual_out.  A group whose m is 0 (or below 2^-100) gets scale 0 and
- * codes 0.
+ * residual_out.  A group whose m is 0 gets scale 0 and codes 0; one whose m
+ * is below 2^-100 may.  The sum of a row's squares is an fp32 number: a row
+ * where it overflows (values near 2^60) has y = 0.
  *   n, width    rows; values per row, a multiple of 8, 8 .. 32768.
  *   x_fp32      0: x, residual and residual_out are fp16; 1: fp32.  Finite values.
  *   x, residual, residual_out  [n][width] at their strides (multiples of 16

@@ -26,6 +26,9 @@ SOURCES = ["attn.cu", "attn_pair.cu", "aux.cu", "indexer.cu", "compressor.cu", "
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--use_fast_math", "-Xcompiler", "-fPIC,-O2",
          "-Xptxas", "-v", f"-I{INCLUDE}", f"-I{CSRC}"]
+# The norm keeps fp32 subnormals: a row may hold them and still have an
+# ordinary norm (the other sources take fp16 values or weights).
+FILE_FLAGS = {"norm.cu": ["-ftz=false"]}
 
 
 def nvcc() -> str:
@@ -43,7 +46,7 @@ def _newest_input_mtime() -> float:
 
 def _compile(src: str) -> tuple[str, str]:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [nvcc(), *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [nvcc(), *ARCH, *FLAGS, *FILE_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")

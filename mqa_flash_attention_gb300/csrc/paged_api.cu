@@ -259,7 +259,8 @@ ds4a_status ds4a_attn_weights_paged(int32_t n_seq, const ds4a_layout *shape, con
 
 size_t ds4a_evict_paged_workspace_size(int32_t n_seq, int32_t n_keep) {
   if (n_seq <= 0 || n_keep <= 0) return 0;
-  return align256(4 * (size_t)n_seq) + 8 * (size_t)n_seq * (size_t)n_keep;
+  const size_t words = ((size_t)n_keep + 31) / 32;
+  return align256(8 * (size_t)n_seq) + 4 * (size_t)n_seq * (2 * (size_t)n_keep + words);
 }
 
 ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
@@ -294,7 +295,8 @@ ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int3
   if (workspace == nullptr || !aligned(workspace, 256) ||
       workspace_bytes < ds4a_evict_paged_workspace_size(n_seq, E->n_keep))
     return DS4A_ERR_WORKSPACE;
-  if (n_seq * ((cols + 7) / 8) > INT32_MAX) return DS4A_ERR_INVALID_ARG;  // blocks of the move kernel
+  if (n_seq * ((cols + 7) / 8) > INT32_MAX || n_seq * ((E->n_keep + 255LL) / 256) > INT32_MAX)
+    return DS4A_ERR_INVALID_ARG;  // blocks of the move kernel
   HostDevice d;
   const ds4a_status st = ds4a::host_device(&d);
   if (st != DS4A_OK) return st;
@@ -318,9 +320,11 @@ ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int3
   p.id_out_stride = E->ids_out != nullptr ? E->id_out_stride / 4 : 0;
   p.n_out = reinterpret_cast<uint8_t *>(E->n_out);
   p.n_out_stride = E->n_out_stride;
-  p.n_moves = static_cast<int32_t *>(workspace);
-  p.from = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + align256(4 * (size_t)n_seq));
+  p.n_moves = static_cast<int2 *>(workspace);
+  p.from = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + align256(8 * (size_t)n_seq));
   p.to = p.from + (size_t)n_seq * E->n_keep;
+  p.stay_words = (E->n_keep + 31) / 32;
+  p.stay = reinterpret_cast<uint32_t *>(p.to + (size_t)n_seq * E->n_keep);
   p.cached = ds4a::evict_cached_keys(p.rows.max_rows, ds4a::evict_cluster(p.rows.max_rows));
   return ds4a::host_launched(ds4a::launch_evict(p, as_cuda(stream)));
 }
@@ -404,6 +408,7 @@ ds4a_status ds4a_rmsnorm_fp8(const ds4a_norm *N, ds4a_stream_t stream) {
   p.res_out_stride = N->residual_out_stride;
   p.weight = N->weight;
   p.eps = N->eps;
+  p.inv_width = 1.0f / (float)N->width;
   p.group = N->group;
   p.codes = N->codes;
   p.code_stride = N->code_stride;
@@ -411,7 +416,7 @@ ds4a_status ds4a_rmsnorm_fp8(const ds4a_norm *N, ds4a_stream_t stream) {
   p.scale_stride = N->codes != nullptr ? N->scale_stride / 4 : 0;
   p.y = static_cast<uint8_t *>(N->y);
   p.y_stride = N->y_stride;
-  return ds4a::host_launched(ds4a::launch_norm(p, N->x_fp32 != 0, as_cuda(stream)));
+  return ds4a::host_launched(ds4a::launch_norm(p, N->x_fp32 != 0, d.sm_count, as_cuda(stream)));
 }
 
 }  // extern "C"

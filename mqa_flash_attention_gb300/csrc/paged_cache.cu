@@ -2,6 +2,8 @@
 // eviction of the rows that received the least attention weight.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "paged_params.h"
 #include "ptx.cuh"
@@ -71,239 +73,314 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_paged_kernel(const A
 }
 
 // ------------------------------------------------------------------ eviction: choosing the rows
-// A cluster of CTAs per sequence; each CTA owns a contiguous range of slots
-// and each of its warps a contiguous part of that.  An exact radix select
-// over order-preserving 32-bit keys, four digits of 8 bits from the top, finds
-// the smallest kept key and how many rows of that key stay (the lowest slots);
-// the cluster adds its histograms through distributed shared memory.  Three
-// walks of the keys follow: equal keys per warp; with their prefix every row
-// knows whether it stays, so kept rows at or above n' and freed slots below it
-// are counted; with the prefix of those each row writes its own entry.  The
-// h-th of either list pairs up in the move kernel.  All integer work: the
-// result does not depend on any order of execution.
+// A cluster of CTAs per sequence (one CTA for up to 8192 rows, eight for up to
+// 65536, else sixteen);
+// each CTA owns a contiguous range of slots and each of its warps a contiguous
+// part of that.  An exact radix select over order-preserving 32-bit keys, in
+// digits of 11, 11 and 10 bits (the first spans sign, exponent and two mantissa
+// bits, so that rows of like weight still spread over bins and the shared
+// atomics rarely collide), finds the smallest kept key T and how many rows of
+// that key stay (the lowest slots).  CTAs of a cluster add their histograms
+// through distributed shared memory.  One walk
+// then counts, per warp and apart below and above n', the rows over T and at
+// T; their prefixes give every warp its first entry of the two lists (kept rows
+// at or above n', freed slots below), and a last walk writes them, and a bit
+// per slot below n' that tells whether its row stays there.  The h-th of either
+// list pairs up in the move kernel.  All integer work: the result does not
+// depend on any order of execution.
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 256;
-constexpr int kMaxCachedKeys = 49152;  // 192 KB of keys beside the histogram
+constexpr int kBins = 2048;
+constexpr int kMaxCachedKeys = 45056;  // 176 KB of keys beside the histograms
+constexpr int kBatch = 8;              // rows of a thread (or a warp's steps) loaded ahead
+
+struct Counts {  // rows over T and at T, in slots below n' and from n' on
+  unsigned gt_lo, eq_lo, gt_hi, eq_hi;
+};
 
 struct SelShared {
-  unsigned hist[kBins];
+  unsigned hist[kBins];    // of this CTA's keys
   unsigned warp_sum[kSelWarps];
-  unsigned warp_sum2[kSelWarps];
-  unsigned total[3];  // this CTA's counts, read by the other CTAs
+  Counts warp[kSelWarps];
   unsigned digit, left;
+};
+struct ClusterShared : SelShared {
+  unsigned sum[3][kBins];  // of the cluster's keys, by digit
+  Counts cta[16];          // every CTA's counts
 };
 
 // Order-preserving key: larger weight, larger key; NaN as -inf, -0 as +0.
 // Protected rows come above every weight.
 __device__ __forceinline__ uint32_t evict_key(float x, bool safe) {
   if (safe) return 0xFFFFFFFFu;
-  if (x != x) x = -INFINITY;
   uint32_t u = __float_as_uint(x);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0xFF800000u;
   if (u == 0x80000000u) u = 0u;
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix over the block's warps of a per-warp count; total = sum.
-__device__ __forceinline__ unsigned warps_before(unsigned mine, unsigned *sums, int warp, int lane, unsigned &total) {
-  __syncthreads();
-  if (lane == 0) sums[warp] = mine;
-  __syncthreads();
-  const unsigned v = sums[lane];
-  unsigned inc = v;
+__device__ __forceinline__ unsigned warp_add(unsigned v) { return __reduce_add_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ unsigned scan_lanes(unsigned v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
+    const unsigned t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
   }
-  total = __shfl_sync(0xffffffffu, inc, 31);
-  return __shfl_sync(0xffffffffu, inc - v, warp);
+  return v;
 }
 
+// Of rows over / at T, how many of those at T are taken when `seen` rows at T
+// come before and `left` are taken in all.
+__device__ __forceinline__ unsigned taken(unsigned eq, unsigned seen, unsigned left) {
+  return seen >= left ? 0u : min(eq, left - seen);
+}
+
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
   extern __shared__ uint32_t keys[];
-  __shared__ SelShared sh;
+  __shared__ typename std::conditional<CLUSTER, ClusterShared, SelShared>::type sh;
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int C = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / C;
+  for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+  if constexpr (CLUSTER) {
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) sh.sum[0][i] = 0;
+    cluster.sync();  // clear before any CTA adds to them
+  }
+  grid_launch_dependents();
   grid_dependency_wait();
   const int4 g = __ldg(p.geom + b);
   const int n = min(max(g.w, 0), p.rows.max_rows);
   const int n_out = min(n, p.n_keep);
   const float *w = p.weights + b * p.weight_stride;
   const int32_t *ids = p.ids != nullptr ? p.ids + b * p.id_stride : nullptr;
-  int32_t *kept = p.kept + b * p.kept_stride;
-  float *w_out = p.weights_out != nullptr ? p.weights_out + b * p.weight_out_stride : nullptr;
-  int32_t *ids_out = p.ids_out != nullptr ? p.ids_out + b * p.id_out_stride : nullptr;
+  uint32_t *stay = p.stay + (long long)b * p.stay_words;
   const int per = ((n + C - 1) / C + 31) / 32 * 32;
   const int lo = min(n, rank * per), hi = min(n, lo + per);
-  for (int i = n_out + rank * kSelThreads + tid; i < p.n_keep; i += C * kSelThreads) kept[i] = -1;
   if (n == n_out) {  // everything stays
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      kept[j] = j;
-      if (w_out != nullptr) w_out[j] = w[j];
-      if (ids_out != nullptr) ids_out[j] = ids[j];
-    }
+    for (int i = lo / 32 + tid; 32 * i < hi; i += kSelThreads) stay[i] = 0xFFFFFFFFu;
     if (rank == 0 && tid == 0) {
-      p.n_moves[b] = 0;
+      p.n_moves[b] = make_int2(0, n_out);
       *reinterpret_cast<int32_t *>(p.n_out + b * p.n_out_stride) = n_out;
     }
     return;
   }
-  const long long recent = ((long long)max(g.x, 0) + 1) / p.ratio - p.n_recent;
+  // Ids over `old` are protected; it lies in -2^31 .. 2^31 - 1.
+  const int old = (int)(((long long)max(g.x, 0) + 1) / p.ratio - p.n_recent - 1);
   auto key_at = [&](int j) -> uint32_t {
     const int id = ids != nullptr ? ids[j] : j;
-    return evict_key(w[j], id < p.n_first || id >= recent);
+    return evict_key(w[j], id < p.n_first || id > old);
   };
-  if (p.cached > 0)
-    for (int j = lo + tid; j < hi; j += kSelThreads) keys[j - lo] = key_at(j);
   auto key = [&](int j) -> uint32_t { return p.cached > 0 ? keys[j - lo] : key_at(j); };
+  if (p.cached > 0) {  // kBatch loads of a thread in flight at a time
+    for (int base = lo + tid; base < hi; base += kBatch * kSelThreads) {
+      float x[kBatch];
+      int id[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = base + i * kSelThreads;
+        x[i] = j < hi ? w[j] : 0.f;
+        id[i] = j < hi && ids != nullptr ? ids[j] : j;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = base + i * kSelThreads;
+        if (j < hi) keys[j - lo] = evict_key(x[i], id[i] < p.n_first || id[i] > old);
+      }
+    }
+  }
 
   // The n'-th largest key, digit by digit.
   uint32_t prefix = 0, mask = 0;
   unsigned left = (unsigned)n_out;  // rows still to take among those that match the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < kBins) sh.hist[tid] = 0;
-    __syncthreads();
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    const uint32_t digits = (1u << bits) - 1u;
+    __syncthreads();  // the histogram is clear
     for (int base = lo; base < hi; base += kSelThreads) {
       const int j = base + tid;
       uint32_t k = 0;
-      const bool in = j < hi && (((k = key(j)) ^ prefix) & mask) == 0;
-      const unsigned who = __ballot_sync(0xffffffffu, in);
-      if (who == 0) continue;
-      const uint32_t d = (k >> shift) & 0xFFu;
+      bool in = j < hi;
+      if (in) {
+        k = key(j);
+        in = ((k ^ prefix) & mask) == 0;
+      }
+      if (!__any_sync(0xffffffffu, in)) continue;
+      const uint32_t d = (k >> shift) & digits, d0 = __shfl_sync(0xffffffffu, d, 0);
       // Rows of one digit (all-equal weights) are added once per warp.
-      int same = 0;
-      if (who == 0xffffffffu) __match_all_sync(0xffffffffu, d, &same);
-      if (same) {
+      if (__all_sync(0xffffffffu, in && d == d0)) {
         if (lane == 0) atomicAdd(&sh.hist[d], 32u);
       } else if (in) {
         atomicAdd(&sh.hist[d], 1u);
       }
     }
-    cluster.sync();
-    unsigned c = 0, above = 0;
-    if (tid < kBins) {  // thread t: the bin t from the top
-      const int bin = kBins - 1 - tid;
-      for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(sh.hist, r)[bin];
-      unsigned inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += t;
-      }
-      if (lane == 31) sh.warp_sum[warp] = inc;
-      above = inc - c;
-    }
     __syncthreads();
-    if (tid < kBins) {
-      for (int i = 0; i < warp; ++i) above += sh.warp_sum[i];
-      if (above < left && left <= above + c) {  // exactly one thread
-        sh.digit = kBins - 1 - tid;
-        sh.left = left - above;
+    if constexpr (CLUSTER) {
+      // The bins that this CTA's keys fall into, added to the sums of every
+      // CTA: few of them in any pass, and one cluster barrier per digit.
+#pragma unroll
+      for (int u = 0; u < kBins / kSelThreads; ++u) {
+        const int bin = tid + u * kSelThreads;
+        const unsigned v = sh.hist[bin];
+        if (v != 0)
+          for (int r = 0; r < C; ++r) atomicAdd(cluster.map_shared_rank(&sh.sum[pass][bin], (rank + r) % C), v);
       }
+      cluster.sync();
     }
-    cluster.sync();  // every CTA has read the histograms; digit and left are set
+    // Thread t: the two bins 2t, 2t + 1 counted from the top.
+    const unsigned *total = sh.hist;
+    if constexpr (CLUSTER) total = sh.sum[pass];
+    const int top = kBins - 1 - 2 * tid;
+    const unsigned c0 = total[top], c1 = total[top - 1];
+    const unsigned inc = scan_lanes(c0 + c1, lane);
+    if (lane == 31) sh.warp_sum[warp] = inc;
+    __syncthreads();
+    const unsigned before = warp_add(lane < warp ? sh.warp_sum[lane] : 0u);
+    const unsigned above0 = before + inc - c0 - c1, above1 = above0 + c0;
+    if (above0 < left && left <= above1) {  // one thread of one of the two lines
+      sh.digit = top;
+      sh.left = left - above0;
+    } else if (above1 < left && left <= above1 + c1) {
+      sh.digit = top - 1;
+      sh.left = left - above1;
+    }
+    sh.hist[2 * tid] = sh.hist[2 * tid + 1] = 0;
+    __syncthreads();
     prefix |= sh.digit << shift;
-    mask |= 0xFFu << shift;
+    mask |= digits << shift;
     left = sh.left;
   }
   const uint32_t T = prefix;  // rows above T stay, and the first `left` of T
 
   const int sub = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int w0 = min(hi, lo + warp * sub), w1 = min(hi, w0 + sub);
-  unsigned eq = 0;
-  for (int base = w0; base < w1; base += 32) {
-    const int j = base + lane;
-    eq += __popc(__ballot_sync(0xffffffffu, j < w1 && key(j) == T));
+  Counts c = {0u, 0u, 0u, 0u};
+  for (int j = w0 + lane; j < w1; j += 32) {
+    const uint32_t k = key(j);
+    const unsigned gt = k > T, eq = k == T, low = j < n_out;
+    c.gt_lo += gt & low;
+    c.eq_lo += eq & low;
+    c.gt_hi += gt & ~low & 1u;
+    c.eq_hi += eq & ~low & 1u;
   }
-  unsigned total;
-  unsigned eq_before = warps_before(eq, sh.warp_sum, warp, lane, total);
-  if (tid == 0) sh.total[0] = total;
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) eq_before += *cluster.map_shared_rank(&sh.total[0], r);
-
-  const unsigned below = (1u << lane) - 1u;
-  auto stays = [&](int j, unsigned &seen) -> bool {  // `seen`: equal keys before this step's 32 rows
-    const uint32_t k = j < w1 ? key(j) : 0u;
-    const bool is_eq = j < w1 && k == T;
-    const unsigned bal = __ballot_sync(0xffffffffu, is_eq);
-    const bool in = j < w1 && (k > T || (is_eq && seen + __popc(bal & below) < left));
-    seen += __popc(bal);
-    return in;
+  c.gt_lo = warp_add(c.gt_lo);
+  c.eq_lo = warp_add(c.eq_lo);
+  c.gt_hi = warp_add(c.gt_hi);
+  c.eq_hi = warp_add(c.eq_hi);
+  if (lane == 0) sh.warp[warp] = c;
+  __syncthreads();
+  // Lane l: warp l's counts, its rows at T before it in this CTA.
+  const Counts wc = sh.warp[lane];
+  const unsigned wc_eq = wc.eq_lo + wc.eq_hi;
+  const unsigned eq_inc = scan_lanes(wc_eq, lane);
+  if constexpr (CLUSTER) {
+    if (warp == 0) {
+      const Counts t = {warp_add(wc.gt_lo), warp_add(wc.eq_lo), warp_add(wc.gt_hi), warp_add(wc.eq_hi)};
+      if (lane < C) *cluster.map_shared_rank(&sh.cta[rank], lane) = t;
+    }
+    cluster.sync();
+  }
+  // Entries of the lists, and rows at T, of the CTAs before this one.
+  unsigned eq_before = 0, m_before = 0, h_before = 0, m_all = 0;
+  auto lists_of = [&](const Counts &x, int slots_lo, unsigned seen, unsigned &movers, unsigned &holes) {
+    holes = slots_lo - x.gt_lo - taken(x.eq_lo, seen, left);
+    movers = x.gt_hi + taken(x.eq_hi, seen + x.eq_lo, left);
   };
-  unsigned movers = 0, holes = 0, seen = eq_before;
-  for (int base = w0; base < w1; base += 32) {
-    const int j = base + lane;
-    const bool in = stays(j, seen);
-    movers += __popc(__ballot_sync(0xffffffffu, in && j >= n_out));
-    holes += __popc(__ballot_sync(0xffffffffu, !in && j < w1 && j < n_out));
-  }
-  unsigned tm, th;
-  unsigned m_at = warps_before(movers, sh.warp_sum, warp, lane, tm);
-  unsigned h_at = warps_before(holes, sh.warp_sum2, warp, lane, th);
-  if (tid == 0) {
-    sh.total[1] = tm;
-    sh.total[2] = th;
-  }
-  cluster.sync();
-  unsigned all = 0;
-  for (int r = 0; r < C; ++r) {
-    const unsigned t1 = *cluster.map_shared_rank(&sh.total[1], r);
-    all += t1;
-    if (r < rank) {
-      m_at += t1;
-      h_at += *cluster.map_shared_rank(&sh.total[2], r);
+  if constexpr (CLUSTER) {
+    unsigned seen = 0;
+    for (int r = 0; r < C; ++r) {
+      const Counts x = sh.cta[r];
+      const int r0 = min(n, r * per), r1 = min(n, r0 + per);
+      unsigned m, h;
+      lists_of(x, min(max(n_out - r0, 0), r1 - r0), seen, m, h);
+      if (r < rank) {
+        m_before += m;
+        h_before += h;
+        eq_before = seen + x.eq_lo + x.eq_hi;
+      }
+      m_all += m;
+      seen += x.eq_lo + x.eq_hi;
     }
   }
+  // The same for the warps of this CTA (lane l: warp l).
+  unsigned m_mine, h_mine;
+  {
+    const int r0 = min(hi, lo + lane * sub), r1 = min(hi, r0 + sub);
+    lists_of(wc, min(max(n_out - r0, 0), r1 - r0), eq_before + eq_inc - wc_eq, m_mine, h_mine);
+  }
+  const unsigned m_inc = scan_lanes(m_mine, lane), h_inc = scan_lanes(h_mine, lane);
+  if (!CLUSTER) m_all = __shfl_sync(0xffffffffu, m_inc, 31);
+  unsigned m_at = m_before + __shfl_sync(0xffffffffu, m_inc - m_mine, warp);
+  unsigned h_at = h_before + __shfl_sync(0xffffffffu, h_inc - h_mine, warp);
+  unsigned seen = eq_before + __shfl_sync(0xffffffffu, eq_inc - wc_eq, warp);
+  const unsigned below = (1u << lane) - 1u;
   int32_t *from = p.from + (long long)b * p.n_keep, *to = p.to + (long long)b * p.n_keep;
-  seen = eq_before;
   for (int base = w0; base < w1; base += 32) {
     const int j = base + lane;
-    const bool in = stays(j, seen);
-    const bool mover = in && j >= n_out, hole = !in && j < w1 && j < n_out;
-    const unsigned bm = __ballot_sync(0xffffffffu, mover), bh = __ballot_sync(0xffffffffu, hole);
-    if (mover) from[m_at + __popc(bm & below)] = j;
-    if (hole) to[h_at + __popc(bh & below)] = j;
-    if (in && j < n_out) {
-      kept[j] = j;
-      if (w_out != nullptr) w_out[j] = w[j];
-      if (ids_out != nullptr) ids_out[j] = ids[j];
-    }
+    const uint32_t k = j < w1 ? key(j) : 0u;
+    const bool eq = j < w1 && k == T;
+    const unsigned be = __ballot_sync(0xffffffffu, eq);
+    const bool in = j < w1 && (k > T || (eq && seen + __popc(be & below) < left));
+    const bool low = j < n_out;
+    const unsigned bm = __ballot_sync(0xffffffffu, in && !low);
+    const unsigned bh = __ballot_sync(0xffffffffu, !in && j < w1 && low);
+    if (lane == 0 && base < n_out) stay[base >> 5] = ~bh;
+    if ((bm >> lane) & 1u) from[m_at + __popc(bm & below)] = j;
+    if ((bh >> lane) & 1u) to[h_at + __popc(bh & below)] = j;
+    seen += __popc(be);
     m_at += __popc(bm);
     h_at += __popc(bh);
   }
   if (rank == 0 && tid == 0) {
-    p.n_moves[b] = (int)all;
+    p.n_moves[b] = make_int2((int)m_all, n_out);
     *reinterpret_cast<int32_t *>(p.n_out + b * p.n_out_stride) = n_out;
   }
-  cluster.sync();  // no CTA leaves while another reads its counts
 }
 
 // ------------------------------------------------------------------ eviction: moving the rows
 // One warp per move: the K and the V row (and the scales of an E4M3 pool) of
 // the h-th kept row above n' into the h-th freed slot below it.  Sources and
-// destinations never meet, so the moves need no order.  Bound by memory: two
-// rows read and two written per move.
+// destinations never meet, so the moves need no order.  The blocks of a
+// sequence first share out its slots: kept, weights and ids of the rows that
+// stay.  Bound by memory: two rows read and two written per move.
 
 constexpr int kMoveWarps = 8;
+constexpr int kMoveSlots = 32 * kMoveWarps;  // slots of a block, one per thread
 
 __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const EvictParams p, int blocks_per_seq) {
-  const int b = blockIdx.x / blocks_per_seq, lane = threadIdx.x & 31;
-  const int h = (blockIdx.x - b * blocks_per_seq) * kMoveWarps + (threadIdx.x >> 5);
+  const int b = blockIdx.x / blocks_per_seq, part = blockIdx.x - b * blocks_per_seq, lane = threadIdx.x & 31;
+  const int h = part * kMoveWarps + (threadIdx.x >> 5);
+  grid_launch_dependents();
   grid_dependency_wait();
-  if (h >= p.n_moves[b]) return;
+  const int2 plan = p.n_moves[b];  // (moves, n')
+  int32_t *kept = p.kept + b * p.kept_stride;
+  const float *w = p.weights + b * p.weight_stride;
+  float *w_out = p.weights_out != nullptr ? p.weights_out + b * p.weight_out_stride : nullptr;
+  const int32_t *ids = p.ids != nullptr ? p.ids + b * p.id_stride : nullptr;
+  int32_t *ids_out = p.ids_out != nullptr ? p.ids_out + b * p.id_out_stride : nullptr;
+  const int j = part * kMoveSlots + threadIdx.x;
+  if (j < p.n_keep) {
+    if (j >= plan.y) {
+      kept[j] = -1;
+    } else if ((__ldg(p.stay + (long long)b * p.stay_words + (j >> 5)) >> (j & 31)) & 1u) {
+      kept[j] = j;
+      if (w_out != nullptr) w_out[j] = w[j];
+      if (ids_out != nullptr) ids_out[j] = ids[j];
+    }
+  }
+  if (h >= plan.x) return;
   const int src = p.from[(long long)b * p.n_keep + h], dst = p.to[(long long)b * p.n_keep + h];
   const PagedSeg &s = p.rows;
   const int32_t *table = s.table + b * s.table_stride;
   const int sp = src / s.page_rows, dp = dst / s.page_rows;
   const int from_page = __ldg(table + sp), to_page = __ldg(table + dp);
-  if (lane == 0) p.kept[b * p.kept_stride + dst] = src;
-  if (lane == 1 && p.weights_out != nullptr)
-    p.weights_out[b * p.weight_out_stride + dst] = p.weights[b * p.weight_stride + src];
-  if (lane == 2 && p.ids_out != nullptr) p.ids_out[b * p.id_out_stride + dst] = p.ids[b * p.id_stride + src];
+  if (lane == 0) kept[dst] = src;
+  if (lane == 1 && w_out != nullptr) w_out[dst] = w[src];
+  if (lane == 2 && ids_out != nullptr) ids_out[dst] = ids[src];
   if ((unsigned)from_page >= (unsigned)s.n_pages || (unsigned)to_page >= (unsigned)s.n_pages) return;
   const int ss = src - sp * s.page_rows, ds = dst - dp * s.page_rows;
   const long long so = from_page * s.page_stride + ss * s.row_stride, d = to_page * s.page_stride + ds * s.row_stride;
@@ -337,7 +414,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const Evict
 
 }  // namespace
 
-int evict_cluster(int max_rows) { return max_rows <= 8192 ? 1 : 8; }
+int evict_cluster(int max_rows) { return max_rows <= 8192 ? 1 : max_rows <= 65536 ? 8 : 16; }
 
 int evict_cached_keys(int max_rows, int cluster) {
   const long long per = (((long long)max_rows + cluster - 1) / cluster + 31) / 32 * 32;
@@ -358,13 +435,14 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
   attr[1].val.clusterDim.x = C;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  const cudaError_t e = C > 1 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p)
+                              : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
   if (e != cudaSuccess) return e;
   const int spare = p.rows.max_rows - p.n_keep;  // kept rows above n' are at most this many
-  const int moves = spare < p.n_keep ? spare : p.n_keep;
-  if (moves <= 0) return cudaSuccess;
-  const int blocks = (moves + kMoveWarps - 1) / kMoveWarps;
+  const int moves = spare < 0 ? 0 : spare < p.n_keep ? spare : p.n_keep;
+  const int move_blocks = (moves + kMoveWarps - 1) / kMoveWarps, slot_blocks = (p.n_keep + kMoveSlots - 1) / kMoveSlots;
+  const int blocks = move_blocks > slot_blocks ? move_blocks : slot_blocks;
   cfg.gridDim = dim3(p.n_seq * blocks);
   cfg.blockDim = dim3(32 * kMoveWarps);
   cfg.dynamicSmemBytes = 0;
@@ -388,10 +466,13 @@ cudaError_t launch_append(const AppendParams &p, cudaStream_t s) {
 
 // The shared-memory opt-in of the selection, and the code of every kernel here.
 cudaError_t prepare_cache_kernels() {
-  cudaError_t e = cudaFuncSetAttribute((const void *)evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       4 * kMaxCachedKeys);
-  for (const void *f : {(const void *)append_paged_kernel, (const void *)evict_select_kernel,
-                        (const void *)evict_move_kernel}) {
+  cudaError_t e = cudaSuccess;
+  for (const void *f : {(const void *)evict_select_kernel<false>, (const void *)evict_select_kernel<true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMaxCachedKeys);
+  if (e == cudaSuccess)  // clusters of sixteen
+    e = cudaFuncSetAttribute((const void *)evict_select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (const void *f : {(const void *)append_paged_kernel, (const void *)evict_select_kernel<false>,
+                        (const void *)evict_select_kernel<true>, (const void *)evict_move_kernel}) {
     cudaFuncAttributes a;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, f);
   }

@@ -68,7 +68,9 @@ struct EvictParams {
   long long id_out_stride;
   uint8_t *n_out;
   long long n_out_stride;  // bytes
-  int32_t *n_moves;        // workspace: [n_seq]
+  int2 *n_moves;           // workspace: [n_seq] (rows moved, n')
+  uint32_t *stay;          // workspace: [n_seq][stay_words] a bit per slot below n': its row stays
+  int stay_words;          // ceil(n_keep / 32)
   int32_t *from, *to;      // workspace: [n_seq][n_keep] slots of the moved rows, and the freed slots they take
   int cached;              // keys of a CTA's rows kept in shared memory (0: recomputed from the weights)
 };
@@ -92,7 +94,7 @@ struct NormParams {
   uint8_t *res_out;
   long long x_stride, res_stride, res_out_stride;  // bytes
   const float *weight;
-  float eps;
+  float eps, inv_width;
   int group;   // values per scale, 0: the row
   uint8_t *codes;
   long long code_stride;
@@ -101,7 +103,7 @@ struct NormParams {
   uint8_t *y;
   long long y_stride;
 };
-cudaError_t launch_norm(const NormParams &p, bool fp32, cudaStream_t s);
+cudaError_t launch_norm(const NormParams &p, bool fp32, int sm_count, cudaStream_t s);
 cudaError_t preload_norm_kernels();
 
 }  // namespace ds4a

@@ -437,6 +437,19 @@ def test_evict_protects_by_id(torch, ds4a, in_place):
     run_evict(torch, ds4a, rng, rows, 32, 450, first=2, recent=10 ** 6, in_place=in_place)
 
 
+def test_evict_at_the_ends_of_the_integers(torch, ds4a):
+    """The last position an int32 holds, ids at both ends, and the largest n_recent."""
+    w = np.arange(64, dtype=np.float32)[None]
+    ids = np.linspace(-2 ** 31, 2 ** 31 - 1, 64).astype(np.int64).astype(np.int32)[None]
+    seg = make(np.random.default_rng(0), 1, [64], 16)
+    for pos, recent, first in ((2 ** 31 - 1, 0, 0), (2 ** 31 - 1, 2 ** 31 - 1, 0), (0, 2 ** 31 - 1, 2 ** 31 - 1), (5, 3, 0)):
+        geom = [(pos, 0, 0, 64)]
+        kept, n_out = ds4a.evict_paged(shape_of(1), up(torch, np.array(geom, dtype=np.int32)), rows_on(torch, ds4a, seg),
+                                       up(torch, w), 20, n_first=first, n_recent=recent, ids=up(torch, ids))
+        (no, kp), = paged.evict(dict(ratio=1), geom, w, ids, 20, first, recent, 64)
+        assert host(n_out)[0] == no and np.array_equal(host(kept)[0], kp), (pos, recent)
+
+
 @pytest.mark.parametrize("kind", ["equal", "zeros", "nan", "inf", "subnormal", "negative"])
 def test_evict_weights_of_every_kind(torch, ds4a, kind):
     rng = np.random.default_rng(42)
@@ -486,6 +499,27 @@ def test_evict_long_sequences(torch, ds4a, rows, keep):
         t = seg.table[b].long()
         assert torch.equal(k[t[dst // page], dst % page], k0[t[src // page], src % page])
         assert torch.equal(ks[t[dst // page], dst % page], ks0[t[src // page], src % page])
+
+
+def test_evict_the_longest_lists(torch, ds4a):
+    """More keys than a cluster's shared memory holds: ranks are taken from the weights each time."""
+    n, page = 850000, 512
+    pages = -(-n // page)
+    k = torch.zeros((pages, page, D), dtype=torch.uint8, device="cuda")
+    ks = torch.arange(pages * page, dtype=torch.float32, device="cuda").view(pages, page)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    g = torch.tensor([[4 * n, 0, 0, n]], dtype=torch.int32, device="cuda")
+    w = torch.randint(0, 1000, (1, pages * page), device="cuda").float()
+    keep = 500000
+    want = torch.sort(w[0, :n], descending=True, stable=True).indices[:keep].sort().values
+    w0 = w.clone()
+    kept, n_out = ds4a.evict_paged(shape_of(), g, ds4a.PagedRows(k, None, table, k_scale=ks), w, keep)
+    assert n_out.item() == keep
+    assert torch.equal(kept[0].long().sort().values, want)
+    stay = want[want < keep]
+    assert torch.equal(kept[0, stay].long(), stay)
+    assert torch.equal(w[0, :keep], w0[0, kept[0].long()])
+    assert torch.equal(ks.view(-1)[:keep], kept[0].float())
 
 
 def test_evict_absent_pages_move_nothing(torch, ds4a):
@@ -551,6 +585,29 @@ def test_norm_matches_the_oracle(torch, ds4a, f32, residual, n, width, group):
     z = y / np.maximum(np.repeat(want_s, group or width, axis=1)[:, :width], 1e-300)
     off = np.abs(fp8.decode_table()[codes] - z)
     assert (off <= 0.5 * paged.e4m3_step(z) * (1 + 1e-9) + np.abs(z) * 2.0 ** -17).all()
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e-25, 1e-12, 1e12, 1e18])
+def test_norm_of_rows_of_any_size(torch, ds4a, size):
+    """fp32 rows from 1e-36 to 1e12, and one tiny group beside ordinary ones; rows of zeros; rows of 1e18, whose
+    squares add up to more than fp32 holds (512e36 > 3.4e38), have y = 0."""
+    rng = np.random.default_rng(72)
+    x = (rng.standard_normal((3, 512)) * size).astype(np.float32)
+    x[1] = 0
+    x[2, :128] *= np.float32(1e-6)
+    w = np.ones(512, dtype=np.float32)
+    codes, scales, y = ds4a.rmsnorm_fp8(up(torch, x), up(torch, w), eps=1e-37, group=128, want_y=True)
+    _, want = paged.rmsnorm(x, w, 1e-37)
+    with np.errstate(over="ignore"):
+        want[np.isinf(np.square(x).sum(1))] = 0
+    want_s = paged.group_scales(want, 128)
+    got_s = host(scales)
+    keep = want_s * 448 >= 2.0 ** -100
+    assert (np.abs(got_s - want_s) <= want_s * 2.0 ** -18)[keep].all() and (got_s[1] == 0).all()
+    z = want / np.maximum(np.repeat(want_s, 128, axis=1), 1e-300)
+    off = np.abs(fp8.decode_table()[host(codes)] - z)
+    ok = off <= 0.5 * paged.e4m3_step(z) * (1 + 1e-9) + np.abs(z) * 2.0 ** -17
+    assert ok[np.repeat(keep, 128, axis=1)].all() and (host(codes)[got_s.max(1) == 0] == 0).all()
 
 
 def test_norm_strides_in_place_and_parts(torch, ds4a):
