@@ -618,11 +618,12 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
   };
   // Gathered rows (cp.async) are generic-proxy writes: the fence makes the
   // landed stage visible to the tensor core.  TMA writes, and the widened
-  // rows (fenced by the converters), need none.
+  // rows (fenced by the converters), need none.  No tcgen05 fence here: it is
+  // for TMEM that other threads read or wrote, and costs the time the MMAs
+  // in flight still take (some 500 cycles per stage).
   auto stage_ready = [&](int g) -> bool {
     if (!wait(ms.kv_full[ring.st], ring.ph, PSITE_KV_FULL)) return false;
     if (!FP8 && ms.gathered[g % kLists]) fence_proxy_async_smem();
-    tc_fence_after();
     return true;
   };
   auto qk = [&](int g, bool first, bool last) -> bool {
@@ -633,6 +634,7 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
     const uint32_t sb = g & 1;
     if (!wait(ms.list_full[g % kLists], (g / kLists) & 1, PSITE_LIST_FULL)) return false;
     if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, PSITE_S_EMPTY)) return false;
+    tc_fence_after();
     const uint32_t d_s = tmem + kTmemS + 64 * sb;
     for (int c = 0; c < 4; ++c) {
       if (!stage_ready(g)) return false;
@@ -666,6 +668,7 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
       if (!wait(ms.o_empty, (o_item & 1) ^ 1, PSITE_O_EMPTY)) return false;
       ++o_item;
     }
+    tc_fence_after();
     for (int m = 0; m < 4; ++m) {
       if (!stage_ready(g)) return false;
       const uint64_t a0 = sdesc_add(v_desc, ring.st * kStageBytes);
