@@ -75,6 +75,13 @@ enum : unsigned int {
   PSITE_S_FULL, PSITE_P_EMPTY, PSITE_O_FULL, PSITE_DRAIN, PSITE_CODE_FULL, PSITE_LIST_FULL, PSITE_LIST_EMPTY
 };
 
+// The rows sequence b's token sees: compressed rows [0, nc), then raw rows
+// [raw_lo, raw_lo + nr).  The weights need the compressed ones only.
+struct SeqRows {
+  int raw_lo, nr, nc;
+  __device__ __forceinline__ int tiles() const { return (nr + nc + kTile - 1) / kTile; }
+};
+
 struct PMisc {
   alignas(16) unsigned long long row[kLists][kTile];  // K address | kSegBit | kNoRow
   alignas(16) float ksc[kLists][kTile];   // E4M3: scale * log2(e) * K scale
@@ -96,6 +103,7 @@ struct PMisc {
   uint64_t p_full, p_empty, o_empty, mma_done;
   unsigned scan[kThreads / 32];
   int first_seq, first_tile;  // where this CTA's tiles start: sequence, tile within it
+  SeqRows first_rows;
   int n_tiles;                // tiles of this CTA
   uint32_t tmem_base;
   int abort_flag;
@@ -194,13 +202,6 @@ __device__ __forceinline__ float reduce_heads(const float (&s)[32], int lane) {
 
 // ------------------------------------------------------------------ plan
 
-// The rows sequence b's token sees: compressed rows [0, nc), then raw rows
-// [raw_lo, raw_lo + nr).  The weights need the compressed ones only.
-struct SeqRows {
-  int raw_lo, nr, nc;
-  __device__ __forceinline__ int tiles() const { return (nr + nc + kTile - 1) / kTile; }
-};
-
 template <bool WEIGHTS>
 __device__ __forceinline__ SeqRows seq_rows(const PagedAttnParams &p, int b) {
   const int4 g = __ldg(p.geom + b);
@@ -214,7 +215,7 @@ __device__ __forceinline__ SeqRows seq_rows(const PagedAttnParams &p, int b) {
     s.raw_lo = (int)min(lo, (long long)n_raw);
     s.nr = hi > lo ? (int)(hi - lo) : 0;
   }
-  s.nc = (int)min((long long)n_comp, ((long long)pos + 1) / p.ratio);
+  s.nc = (int)min((unsigned)n_comp, ((unsigned)pos + 1u) / (unsigned)p.ratio);
   return s;
 }
 
@@ -230,7 +231,7 @@ struct Walk {
     j = ms.first_tile;
     left = ms.n_tiles;
     if (left <= 0) return;
-    rows = seq_rows<WEIGHTS>(p, b);
+    rows = ms.first_rows;
     n = rows.tiles();
     first = true;
     last = j == n - 1 || left == 1;
@@ -258,26 +259,12 @@ struct Walk {
 // Block-wide: where this CTA starts and how many tiles it has; CTA 0 also
 // writes each sequence's slots for the merge.  Thread t counts sequence t of
 // every round of 512; with one round (the usual batch) the tiles are counted
-// once.
+// once and one barrier lies between.  The caller's barrier publishes the result.
 template <bool WEIGHTS>
 __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool once = p.n_seq <= kThreads;
-  auto tiles_of_seq = [&](int b) { return b < p.n_seq ? seq_rows<WEIGHTS>(p, b).tiles() : 0; };
-  auto before_warp = [&](int inc, int &all) {  // tiles of the warps before this one, and of all
-    __syncthreads();
-    if (lane == 31) ms.scan[warp] = inc;
-    __syncthreads();
-    int v = lane < kThreads / 32 ? ms.scan[lane] : 0, x = v;
-#pragma unroll
-    for (int o = 1; o < kThreads / 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += t;
-    }
-    all = __shfl_sync(0xffffffffu, x, kThreads / 32 - 1);
-    return __shfl_sync(0xffffffffu, x - v, warp);
-  };
-  auto scan = [&](int n) {
+  const SeqRows none = {0, 0, 0};
+  auto scan_warp = [&](int n) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, n, o);
@@ -285,24 +272,31 @@ __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
     }
     return n;
   };
-  int mine = 0;
-  for (int b = tid; b < p.n_seq; b += kThreads) mine += tiles_of_seq(b);
-  int inc = scan(mine), total;
+  // Tiles of the warps before this one, and of all; inc: this warp's inclusive scan.
+  auto before_warp = [&](int inc, int &all) {
+    if (lane == 31) ms.scan[warp] = inc;
+    __syncthreads();
+    const int v = lane < kThreads / 32 ? (int)ms.scan[lane] : 0;
+    all = __reduce_add_sync(0xffffffffu, v);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+  };
+  SeqRows rows = tid < p.n_seq ? seq_rows<WEIGHTS>(p, tid) : none;
+  int n = rows.tiles(), mine = n;
+  for (int b = tid + kThreads; b < p.n_seq; b += kThreads) mine += seq_rows<WEIGHTS>(p, b).tiles();
+  int inc = scan_warp(mine), total;
   int before = before_warp(inc, total);
   const int G = gridDim.x, per = (total + G - 1) / G;
   const int g0 = min(total, (int)blockIdx.x * per), g1 = min(total, g0 + per);
-  if (tid == 0) {
-    ms.n_tiles = g1 - g0;
-    ms.first_seq = ms.first_tile = 0;
-  }
-  __syncthreads();
+  if (tid == 0) ms.n_tiles = g1 - g0;
   int carry = 0;
   for (int b0 = 0; b0 < p.n_seq; b0 += kThreads) {
     const int b = b0 + tid;
-    int n = mine, all = 0;
-    if (!once) {
-      n = tiles_of_seq(b);
-      inc = scan(n);
+    if (p.n_seq > kThreads) {  // several rounds: scan each by itself
+      rows = b < p.n_seq ? seq_rows<WEIGHTS>(p, b) : none;
+      n = rows.tiles();
+      inc = scan_warp(n);
+      int all;
+      __syncthreads();
       before = carry + before_warp(inc, all);
       carry += all;
     }
@@ -310,6 +304,7 @@ __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
     if (n > 0 && at <= g0 && g0 < at + n && g1 > g0) {
       ms.first_seq = b;
       ms.first_tile = g0 - at;
+      ms.first_rows = rows;
     }
     if (!WEIGHTS && blockIdx.x == 0 && b < p.n_seq) {
       const int c0 = n > 0 ? at / per : 0, c1 = n > 0 ? (at + n - 1) / per : -1;
@@ -591,8 +586,8 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams &p, uint32_t 
 // ------------------------------------------------------------------ MMA issue
 
 // The whole warp walks the tiles, so that descriptors are warp-uniform values,
-// and one elected lane issues (42 cycles per 128 x 64 x 16 MMA; 61 when a
-// single lane runs the role).  Waits are joined over the warp: all lanes go
+// and one elected lane issues (47 cycles per 128 x 64 x 16 MMA in a row; 61
+// when a single lane runs the role).  Waits are joined over the warp: all lanes go
 // on or none.
 template <bool FP8, bool WEIGHTS>
 __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_t sbase, uint32_t tmem, PMisc &ms) {
@@ -619,10 +614,14 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
   // Gathered rows (cp.async) are generic-proxy writes: the fence makes the
   // landed stage visible to the tensor core.  TMA writes, and the widened
   // rows (fenced by the converters), need none.  No tcgen05 fence here: it is
-  // for TMEM that other threads read or wrote, and costs the time the MMAs
-  // in flight still take (some 500 cycles per stage).
-  auto stage_ready = [&](int g) -> bool {
-    if (!wait(ms.kv_full[ring.st], ring.ph, PSITE_KV_FULL)) return false;
+  // for TMEM that other threads read or wrote.  fp16 stages are waited for two
+  // at a time: behind the eight MMAs of one the warp would stand still until
+  // they are done.  (E4M3 stages come one by one from the converters.)
+  constexpr int kStep = FP8 ? 1 : 2;
+  auto stages_ready = [&](int g) -> bool {
+#pragma unroll
+    for (int u = 0; u < kStep; ++u)
+      if (!wait(ms.kv_full[ring.st + u], ring.ph, PSITE_KV_FULL)) return false;
     if (!FP8 && ms.gathered[g % kLists]) fence_proxy_async_smem();
     return true;
   };
@@ -636,29 +635,33 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
     if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, PSITE_S_EMPTY)) return false;
     tc_fence_after();
     const uint32_t d_s = tmem + kTmemS + 64 * sb;
-    for (int c = 0; c < 4; ++c) {
-      if (!stage_ready(g)) return false;
+    for (int c = 0; c < 4; c += kStep) {
+      if (!stages_ready(g)) return false;
       const uint64_t a0 = sdesc_add(k_desc, ring.st * kStageBytes);
       const uint64_t b0 = sdesc_add(q_desc, 2 * c * kQBoxBytes);
       if (elect_lane()) {
 #pragma unroll
-        for (int b2 = 0; b2 < 2; ++b2) {
+        for (int u = 0; u < kStep; ++u) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t a = sdesc_add(a0, b2 * kBlk + ks * 32);
-            const uint64_t b = sdesc_add(b0, b2 * kQBoxBytes + ks * 32);
-            if (b2 == 0 && ks == 0)
-              umma_f16(d_s, a, b, kIdescQK, c != 0 ? 1u : 0u);
-            else
-              umma_f16_acc(d_s, a, b, kIdescQK);
+          for (int b2 = 0; b2 < 2; ++b2) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint64_t a = sdesc_add(a0, u * kStageBytes + b2 * kBlk + ks * 32);
+              const uint64_t b = sdesc_add(b0, (2 * u + b2) * kQBoxBytes + ks * 32);
+              if (u == 0 && b2 == 0 && ks == 0)
+                umma_f16(d_s, a, b, kIdescQK, c != 0 ? 1u : 0u);
+              else
+                umma_f16_acc(d_s, a, b, kIdescQK);
+            }
           }
+          umma_commit(smem_u32(&ms.kv_empty[ring.st + u]));
         }
-        umma_commit(smem_u32(&ms.kv_empty[ring.st]));
-        if (c == 3) umma_commit(smem_u32(&ms.s_full[sb]));
-        if (c == 3 && last) umma_commit(smem_u32(&ms.q_empty));
+        if (c + kStep == 4) umma_commit(smem_u32(&ms.s_full[sb]));
+        if (c + kStep == 4 && last) umma_commit(smem_u32(&ms.q_empty));
       }
       __syncwarp();
-      ring.advance();
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) ring.advance();
     }
     return true;
   };
@@ -669,25 +672,29 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
       ++o_item;
     }
     tc_fence_after();
-    for (int m = 0; m < 4; ++m) {
-      if (!stage_ready(g)) return false;
+    for (int m = 0; m < 4; m += kStep) {
+      if (!stages_ready(g)) return false;
       const uint64_t a0 = sdesc_add(v_desc, ring.st * kStageBytes);
       if (elect_lane()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint64_t a = sdesc_add(a0, ks * 2 * kGrp);
-          const uint64_t b = sdesc_add(p_desc, ks * 2048);
-          if (ks == 0)
-            umma_f16(tmem + 64 * m, a, b, kIdescPV, first ? 0u : 1u);
-          else
-            umma_f16_acc(tmem + 64 * m, a, b, kIdescPV);
+        for (int u = 0; u < kStep; ++u) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint64_t a = sdesc_add(a0, u * kStageBytes + ks * 2 * kGrp);
+            const uint64_t b = sdesc_add(p_desc, ks * 2048);
+            if (ks == 0)
+              umma_f16(tmem + 64 * (m + u), a, b, kIdescPV, first ? 0u : 1u);
+            else
+              umma_f16_acc(tmem + 64 * (m + u), a, b, kIdescPV);
+          }
+          umma_commit(smem_u32(&ms.kv_empty[ring.st + u]));
+          if (last) umma_commit(smem_u32(&ms.o_full[m + u]));
         }
-        umma_commit(smem_u32(&ms.kv_empty[ring.st]));
-        if (last) umma_commit(smem_u32(&ms.o_full[m]));
-        if (m == 3) umma_commit(smem_u32(&ms.p_empty));
+        if (m + kStep == 4) umma_commit(smem_u32(&ms.p_empty));
       }
       __syncwarp();
-      ring.advance();
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) ring.advance();
     }
     return true;
   };
@@ -1001,106 +1008,141 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 // With M = max_s m_s and W_s = 2^(m_s - M) l_s over the slots of a sequence:
 //   o = sum_s W_s o_s / L,  L = sum_s W_s,  lse = (M + log2 L) ln 2.
 // A sequence that one CTA finished (one slot) is left alone; one without rows
-// (no slot) gets o = 0 and lse = -inf.  A block takes 128 VEC dims of one head
-// of one sequence, its warps share the slots (warp w: w, w + WARPS, ..), a lane
-// holds VEC float4, and the warps meet in shared memory.  A warp's first slots are
-// loaded together with their (m, l), before the weights are known.  Two
-// shapes: VEC = 4, 4 warps (64 small blocks a sequence, for batches, where a
-// sequence has a few slots), VEC = 1, 8 warps (256 blocks a sequence, for a few
-// long sequences with up to one slot per SM).
+// (no slot) gets o = 0 and lse = -inf.  A lane holds VEC float4 of a head
+// (128 VEC dims a warp) and has kMergeLoads of them in flight; a warp's slots are
+// loaded together with their (m, l), before the weights are known.
 
-constexpr int kMergeLoads = 8;  // float4 in flight per lane
+constexpr int kMergeLoads = 8;
 
-template <int VEC, int WARPS>
+template <int VEC>
+struct Merged {
+  float M, L;  // largest reference and sum of weights (relative to it) so far
+  float4 acc[VEC];
+};
+
+// Slots first, first + step, .. below n of one head.
+template <int VEC>
+__device__ __forceinline__ Merged<VEC> merge_slots(const float2 *ml, const float4 *src, int n, int first, int step) {
+  constexpr int kRound = kMergeLoads / VEC;
+  constexpr long long kSlot = (long long)kH * kD / 4;  // float4 of a slot
+  Merged<VEC> r;
+  r.M = -INFINITY;
+  r.L = 0.f;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) r.acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = first; s0 < n; s0 += step * kRound) {
+    float4 x[kRound][VEC];
+    float2 q[kRound];
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) {
+      const int s = s0 + k * step;
+      q[k] = s < n ? __ldg(ml + (long long)s * kH) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        x[k][e] = s < n ? __ldcs(src + s * kSlot + 32 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float top = r.M;
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) top = fmaxf(top, q[k].x);
+    if (top == -INFINITY) continue;
+    const float old = exp2f(r.M - top);  // 0 while nothing has been added
+    r.M = top;
+    r.L *= old;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      r.acc[e].x *= old;
+      r.acc[e].y *= old;
+      r.acc[e].z *= old;
+      r.acc[e].w *= old;
+    }
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) {
+      const float t = exp2f(q[k].x - top) * q[k].y;
+      r.L += t;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        r.acc[e].x = fmaf(t, x[k][e].x, r.acc[e].x);
+        r.acc[e].y = fmaf(t, x[k][e].y, r.acc[e].y);
+        r.acc[e].z = fmaf(t, x[k][e].z, r.acc[e].z);
+        r.acc[e].w = fmaf(t, x[k][e].w, r.acc[e].w);
+      }
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store_half4(__half *at, const float4 &o, float f) {
+  const __half2 a = __floats2half2_rn(o.x * f, o.y * f), c = __floats2half2_rn(o.z * f, o.w * f);
+  *reinterpret_cast<uint2 *>(at) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+}
+
+// A block takes HEADS heads of one sequence, 128 VEC dims of each.  With HEADS
+// = WARPS a warp joins a head by itself when the sequence has few slots (a
+// batch: no barrier, every load in one or two rounds); otherwise, and with
+// HEADS = 1 (few long sequences, up to a slot per SM), the warps share the
+// slots of each head and meet in shared memory.
+template <int VEC, int WARPS, int HEADS>
 __global__ void __launch_bounds__(32 * WARPS) paged_merge_kernel(const PagedAttnParams p) {
-  constexpr int kChunks = kD / (128 * VEC), kRound = kMergeLoads / VEC;  // slots per warp and round
-  __shared__ float2 wl[WARPS];          // (M, L) of each warp's slots
+  constexpr int kChunks = kD / (128 * VEC), kGroups = kH / HEADS;
+  __shared__ float2 wl[WARPS];  // (M, L) of each warp's slots
   __shared__ float4 part[WARPS][32 * VEC];
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int item = blockIdx.x / kChunks, chunk = blockIdx.x - item * kChunks;
-  const int b = item / kH, h = item - b * kH;
+  const int b = item / kGroups, h0 = (item - b * kGroups) * HEADS;
   const int2 plan = __ldg(p.ws_plan + b);
   const int n = plan.y;
   if (n == 1) return;
-  const float2 *ml = p.ws_ml + (long long)plan.x * kH + h;
-  const float4 *src =
-      reinterpret_cast<const float4 *>(p.ws_o + ((long long)plan.x * kH + h) * kD + 128 * VEC * chunk) + lane;
-  constexpr long long kStep = (long long)kH * kD / 4;  // one slot, in float4
-  float4 acc[VEC];
+  auto ml_of = [&](int h) { return p.ws_ml + (long long)plan.x * kH + h; };
+  auto src_of = [&](int h) {
+    return reinterpret_cast<const float4 *>(p.ws_o + ((long long)plan.x * kH + h) * kD + 128 * VEC * chunk) + lane;
+  };
+  auto out_of = [&](int h) { return p.o + b * p.o_stride + (long long)h * kD + 128 * VEC * chunk; };
+  auto put_lse = [&](int h, float M, float L) {
+    if (p.lse != nullptr && chunk == 0) p.lse[(long long)b * kH + h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  };
+  if (HEADS == WARPS && n <= 4 * kMergeLoads / VEC) {
+    const int h = h0 + warp;
+    const Merged<VEC> r = merge_slots<VEC>(ml_of(h), src_of(h), n, 0, 1);
+    const float inv = r.L > 0.f ? 1.f / r.L : 0.f;
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float M = -INFINITY, L = 0.f;  // of this warp's slots so far
-  for (int s0 = warp; s0 < n; s0 += WARPS * kRound) {
-    float4 x[kRound][VEC];
-    float2 q[kRound];
-#pragma unroll
-    for (int k = 0; k < kRound; ++k) {
-      const int s = s0 + k * WARPS;
-      q[k] = s < n ? __ldg(ml + s * kH) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        x[k][e] = s < n ? __ldg(src + s * kStep + 32 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float top = M;
-#pragma unroll
-    for (int k = 0; k < kRound; ++k) top = fmaxf(top, q[k].x);
-    if (top == -INFINITY) continue;
-    const float old = exp2f(M - top);  // 0 while nothing has been added
-    M = top;
-    L *= old;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      acc[e].x *= old;
-      acc[e].y *= old;
-      acc[e].z *= old;
-      acc[e].w *= old;
-    }
-#pragma unroll
-    for (int k = 0; k < kRound; ++k) {
-      const float t = exp2f(q[k].x - top) * q[k].y;
-      L += t;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        acc[e].x = fmaf(t, x[k][e].x, acc[e].x);
-        acc[e].y = fmaf(t, x[k][e].y, acc[e].y);
-        acc[e].z = fmaf(t, x[k][e].z, acc[e].z);
-        acc[e].w = fmaf(t, x[k][e].w, acc[e].w);
-      }
-    }
+    for (int e = 0; e < VEC; ++e) store_half4(out_of(h) + 4 * (lane + 32 * e), r.acc[e], inv);
+    if (lane == 0) put_lse(h, r.M, r.L);
+    return;
   }
-  if (lane == 0) wl[warp] = make_float2(M, L);
+  for (int h = h0; h < h0 + HEADS; ++h) {
+    const Merged<VEC> r = merge_slots<VEC>(ml_of(h), src_of(h), n, warp, WARPS);
+    if (HEADS > 1) __syncthreads();  // the previous head has been read
+    if (lane == 0) wl[warp] = make_float2(r.M, r.L);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) part[warp][lane + 32 * e] = acc[e];
-  __syncthreads();
-  M = -INFINITY;
+    for (int e = 0; e < VEC; ++e) part[warp][lane + 32 * e] = r.acc[e];
+    __syncthreads();
+    float M = -INFINITY, L = 0.f;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, wl[w].x);
-  L = 0.f;
-  float t[WARPS];
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    t[w] = M == -INFINITY ? 0.f : exp2f(wl[w].x - M);
-    L = fmaf(t[w], wl[w].y, L);
-  }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  for (int v = threadIdx.x; v < 32 * VEC; v += 32 * WARPS) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, wl[w].x);
+    float t[WARPS];
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      const float4 y = part[w][v];
-      o.x = fmaf(t[w], y.x, o.x);
-      o.y = fmaf(t[w], y.y, o.y);
-      o.z = fmaf(t[w], y.z, o.z);
-      o.w = fmaf(t[w], y.w, o.w);
+      t[w] = M == -INFINITY ? 0.f : exp2f(wl[w].x - M);
+      L = fmaf(t[w], wl[w].y, L);
     }
-    const __half2 a = __floats2half2_rn(o.x * inv, o.y * inv), c = __floats2half2_rn(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2 *>(p.o + b * p.o_stride + (long long)h * kD + 128 * VEC * chunk + 4 * v) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    for (int v = threadIdx.x; v < 32 * VEC; v += 32 * WARPS) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float4 y = part[w][v];
+        o.x = fmaf(t[w], y.x, o.x);
+        o.y = fmaf(t[w], y.y, o.y);
+        o.z = fmaf(t[w], y.z, o.z);
+        o.w = fmaf(t[w], y.w, o.w);
+      }
+      store_half4(out_of(h) + 4 * v, o, inv);
+    }
+    if (threadIdx.x == 0) put_lse(h, M, L);
   }
-  if (p.lse != nullptr && chunk == 0 && threadIdx.x == 0)
-    p.lse[(long long)b * kH + h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 cudaError_t launch_pdl(const void *f, const PagedAttnParams &p, int grid, int threads, size_t smem, cudaStream_t s) {
@@ -1125,9 +1167,12 @@ cudaError_t launch_paged_decode(const PagedAttnParams &p, bool e4m3, int grid, c
                     p, grid, kThreads, kPagedSmem, s);
 }
 
+// By the slots a sequence has on average, (CTAs + sequences) / sequences: four
+// at most, a warp per head; up to twenty, a block per head; more, four.
 cudaError_t launch_paged_merge(const PagedAttnParams &p, cudaStream_t s) {
-  if (p.n_seq <= 8) return launch_pdl((const void *)paged_merge_kernel<1, 8>, p, p.n_seq * kH * 4, 256, 0, s);
-  return launch_pdl((const void *)paged_merge_kernel<4, 4>, p, p.n_seq * kH, 128, 0, s);
+  if (p.n_seq <= 8) return launch_pdl((const void *)paged_merge_kernel<1, 8, 1>, p, p.n_seq * kH * 4, 256, 0, s);
+  if (p.n_seq < 48) return launch_pdl((const void *)paged_merge_kernel<4, 4, 1>, p, p.n_seq * kH, 128, 0, s);
+  return launch_pdl((const void *)paged_merge_kernel<4, 4, 4>, p, p.n_seq * kH / 4, 128, 0, s);
 }
 
 cudaError_t launch_paged_weights(const PagedAttnParams &p, bool e4m3, int grid, cudaStream_t s) {
@@ -1141,9 +1186,13 @@ cudaError_t prepare_paged_kernels() {
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPagedSmem);
     if (e != cudaSuccess) return e;
   }
-  cudaFuncAttributes a;
-  const cudaError_t e = cudaFuncGetAttributes(&a, (const void *)paged_merge_kernel<1, 8>);
-  return e != cudaSuccess ? e : cudaFuncGetAttributes(&a, (const void *)paged_merge_kernel<4, 4>);
+  for (const void *f : {(const void *)paged_merge_kernel<1, 8, 1>, (const void *)paged_merge_kernel<4, 4, 1>,
+                        (const void *)paged_merge_kernel<4, 4, 4>}) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, f);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace ds4a
