@@ -12,13 +12,19 @@
 // Work.  A sequence's visible rows, compressed then raw, form one list, cut
 // into tiles of 128 rows; row j of the list is found through the page table,
 // so pages of any size, tiles that span pages and pages that end inside a tile
-// are all alike.  The tiles of all sequences are numbered through and CTA i
-// takes ceil(total / CTAs) of them in a row: the load is even whatever the
-// lengths.  A CTA's tiles of one sequence are an item.  An item that holds
-// the whole sequence writes its output; otherwise it leaves its normalised
-// output (fp32) and (m, l) in slot (CTA + sequence) of the workspace (unique,
-// since along the tiles either number grows), and the merge kernel joins the
-// slots of a sequence.
+// are all alike.  A CTA's tiles of one sequence are an item.  With c the least
+// number for which the items ceil(tiles / c) of all sequences number at most
+// the CTAs, each CTA gets one item of at most c tiles.  Where there is no such
+// c near the average (more sequences than CTAs), the tiles of all sequences
+// are numbered through instead and CTA i takes ceil(total / CTAs) of them in a
+// row, several items.  Either way the load is even whatever the lengths; one
+// item per CTA costs one drain of the pipeline and fewer partial results (64
+// sequences of 8 to 21 tiles: 36 us in the slowest CTA with items cut at even
+// tile numbers, 30 us so).  An item that holds the whole sequence
+// writes its output; otherwise it leaves its normalised output (fp32) and
+// (m, l) in a slot of the workspace, slot CTA, or CTA + sequence with several
+// items per CTA (unique, since along the tiles either number grows), and the
+// merge kernel joins the slots of a sequence.
 //
 // Per tile, as in attn_kernel.cuh, the rows are on the M side of every MMA:
 //   S^T[128 rows][64 heads]  = K_tile[128][512] . Q^T
@@ -105,6 +111,8 @@ struct PMisc {
   int first_seq, first_tile;  // where this CTA's tiles start: sequence, tile within it
   SeqRows first_rows;
   int n_tiles;                // tiles of this CTA
+  int slot_step;              // slot of an item: CTA + slot_step * sequence
+  int fits[kThreads / 32];
   uint32_t tmem_base;
   int abort_flag;
   int resc_flag[2];
@@ -257,12 +265,14 @@ struct Walk {
 };
 
 // Block-wide: where this CTA starts and how many tiles it has; CTA 0 also
-// writes each sequence's slots for the merge.  Thread t counts sequence t of
-// every round of 512; with one round (the usual batch) the tiles are counted
-// once and one barrier lies between.  The caller's barrier publishes the result.
+// writes each sequence's slots for the merge.  Thread t counts sequence t (of
+// every round of 512).  The caller's barrier publishes the result.  `counts`:
+// 512 ints of shared memory, free until then.
 template <bool WEIGHTS>
-__device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
+__device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms, int *counts) {
+  constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = gridDim.x, cta = blockIdx.x;
   const SeqRows none = {0, 0, 0};
   auto scan_warp = [&](int n) {
 #pragma unroll
@@ -272,22 +282,52 @@ __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
     }
     return n;
   };
-  // Tiles of the warps before this one, and of all; inc: this warp's inclusive scan.
+  // Sum over the warps before this one, and over all, of `inc` in lane 31.
   auto before_warp = [&](int inc, int &all) {
     if (lane == 31) ms.scan[warp] = inc;
     __syncthreads();
-    const int v = lane < kThreads / 32 ? (int)ms.scan[lane] : 0;
+    const int v = lane < kWarps ? (int)ms.scan[lane] : 0;
     all = __reduce_add_sync(0xffffffffu, v);
     return __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
   };
   SeqRows rows = tid < p.n_seq ? seq_rows<WEIGHTS>(p, tid) : none;
-  int n = rows.tiles(), mine = n;
+  int n = rows.tiles(), mine = n, total;
   for (int b = tid + kThreads; b < p.n_seq; b += kThreads) mine += seq_rows<WEIGHTS>(p, b).tiles();
-  int inc = scan_warp(mine), total;
+  counts[tid] = n;
+  int inc = scan_warp(mine);
   int before = before_warp(inc, total);
-  const int G = gridDim.x, per = (total + G - 1) / G;
-  const int g0 = min(total, (int)blockIdx.x * per), g1 = min(total, g0 + per);
-  if (tid == 0) ms.n_tiles = g1 - g0;
+  const int per = (total + G - 1) / G;
+  if (p.n_seq <= kThreads && total > 0) {
+    // One item per CTA: warp w tries c = per + w.
+    int items = 0;
+    for (int b = lane; b < p.n_seq; b += 32) items += (counts[b] + per + warp - 1) / (per + warp);
+    items = __reduce_add_sync(0xffffffffu, items);
+    if (lane == 0) ms.fits[warp] = items <= G;
+    __syncthreads();
+    const unsigned fit = __ballot_sync(0xffffffffu, lane < kWarps && ms.fits[lane < kWarps ? lane : 0]);
+    if (fit != 0) {
+      const int c = per + __ffs(fit) - 1, k = (n + c - 1) / c;
+      int all;
+      inc = scan_warp(k);
+      const int first = before_warp(inc, all) + inc - k;  // CTA of the sequence's first item
+      if (tid == 0) ms.slot_step = 0;
+      if (cta >= all && tid == 0) ms.n_tiles = 0;
+      if (k > 0 && first <= cta && cta < first + k) {
+        const int i = cta - first, j0 = (int)((long long)i * n / k), j1 = (int)((long long)(i + 1) * n / k);
+        ms.first_seq = tid;
+        ms.first_tile = j0;
+        ms.first_rows = rows;
+        ms.n_tiles = j1 - j0;
+      }
+      if (!WEIGHTS && cta == 0 && tid < p.n_seq) p.ws_plan[tid] = make_int2(first, k);
+      return;
+    }
+  }
+  const int g0 = min(total, cta * per), g1 = min(total, g0 + per);
+  if (tid == 0) {
+    ms.n_tiles = g1 - g0;
+    ms.slot_step = 1;
+  }
   int carry = 0;
   for (int b0 = 0; b0 < p.n_seq; b0 += kThreads) {
     const int b = b0 + tid;
@@ -306,11 +346,25 @@ __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms) {
       ms.first_tile = g0 - at;
       ms.first_rows = rows;
     }
-    if (!WEIGHTS && blockIdx.x == 0 && b < p.n_seq) {
+    if (!WEIGHTS && cta == 0 && b < p.n_seq) {
       const int c0 = n > 0 ? at / per : 0, c1 = n > 0 ? (at + n - 1) / per : -1;
       p.ws_plan[b] = make_int2(c0 + b, c1 - c0 + 1);
     }
   }
+}
+
+// The geometry and the page tables, into L2 while the previous kernel still
+// runs: each CTA a part of them.  (Only L2: what they hold then does not matter.)
+template <bool WEIGHTS>
+__device__ __forceinline__ void prefetch_tables(const PagedAttnParams &p) {
+  auto lines = [&](const void *at, long long bytes, long long line) {
+    if (line * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(at) + line * 128));
+  };
+  lines(p.geom, 16ll * p.n_seq, threadIdx.x);
+  const long long line = (long long)blockIdx.x * kThreads + threadIdx.x;
+#pragma unroll
+  for (int i = WEIGHTS ? 1 : 0; i < 2; ++i)
+    if (p.seg[i].max_rows > 0) lines(p.seg[i].table, 4ll * p.seg[i].table_stride * (p.n_seq - 1) + 4, line);
 }
 
 // ------------------------------------------------------------------ loaders
@@ -510,11 +564,11 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
     load_q(w.b);
     fetch_pages();
     fetch_scales();
-    if (nt > 1) fetch_pages();
     bool tma = store_list(0), tma_next = false;
+    for (int part = 0; part < 4 && ok; ++part) ok = emit(0, part, tma);
+    if (nt > 1) fetch_pages();
     if (nt > 1) fetch_scales();
     if (nt > 2) fetch_pages();
-    for (int part = 0; part < 4 && ok; ++part) ok = emit(0, part, tma);
     for (int g = 0; g < nt; ++g) {
       if (g + 1 < nt) {
         tma_next = store_list(g + 1);
@@ -835,7 +889,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
     // them: fp16 and normalised for a whole sequence, else fp32 and normalised
     // by the item's own sum.
     const bool whole = flags & kWhole;
-    const long long slot = (long long)blockIdx.x + seq;
+    const long long slot = (long long)blockIdx.x + (long long)ms.slot_step * seq;
     ms.red[q][col0 + l] = reduce_heads<false>(lpart, l);
     if (bar_red_or(1, kComputeThreads, bad)) break;
     if (tid < kH) {
@@ -978,8 +1032,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     tmem_relinquish();
   }
   grid_launch_dependents();
+  prefetch_tables<WEIGHTS>(p);
   grid_dependency_wait();  // the plan reads the sequences' geometry
-  plan_cta<WEIGHTS>(p, ms);
+  plan_cta<WEIGHTS>(p, ms, reinterpret_cast<int *>(smem + kOffKV));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
