@@ -155,7 +155,7 @@ ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, cons
   if (st != DS4A_OK) return st;
   if (!q_ok(X->q, X->q_seq_stride) || !q_ok(X->o, X->o_seq_stride)) return DS4A_ERR_INVALID_ARG;
   if (X->lse != nullptr && !aligned(X->lse, 4)) return DS4A_ERR_INVALID_ARG;
-  bool e4m3 = false, any = false;
+  bool e4m3 = false, any = false, shared = true;
   int64_t most = 0;  // rows a token can see
   for (const ds4a_paged_rows *r : {&X->raw, &X->comp}) {
     if (r->max_pages < 0) return DS4A_ERR_INVALID_ARG;
@@ -165,6 +165,7 @@ ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, cons
     if (any && f8 != e4m3) return DS4A_ERR_INVALID_ARG;  // one format for both segments
     e4m3 = f8;
     any = true;
+    shared = shared && r->k == r->v && r->k_scale == r->v_scale;
     const int64_t rows = (int64_t)r->max_pages * r->page_rows;
     most += r == &X->raw && rows > shape->window ? shape->window : rows;
   }
@@ -200,7 +201,7 @@ ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, cons
   p.timeout_ns = kTimeoutNs;
   p.err = d.err;
   const int grid = (int)(tiles < 1 ? 1 : tiles < ctas ? tiles : ctas);
-  st = ds4a::host_launched(ds4a::launch_paged_decode(p, e4m3, grid, as_cuda(stream)));
+  st = ds4a::host_launched(ds4a::launch_paged_decode(p, e4m3, any && shared, grid, as_cuda(stream)));
   if (st != DS4A_OK) return st;
   return ds4a::host_launched(ds4a::launch_paged_merge(p, as_cuda(stream)));
 }

@@ -167,6 +167,10 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// Starts bringing `bytes` (a multiple of 16) at a 16-byte aligned address into L2.
+__device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrives (as one of the expected arrivals) when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -372,7 +376,7 @@ __device__ __forceinline__ void prefetch_tables(const PagedAttnParams &p) {
 // Lists run ahead of the copies: while the rows of tiles g + 1 and g are
 // issued, the page ids of tile g + 3 and the scales of tile g + 2 are on their
 // way in registers, so neither latency stands between tiles.
-template <bool FP8, bool WEIGHTS>
+template <bool FP8, bool WEIGHTS, bool SHARED>
 __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sbase, PMisc &ms, int ltid) {
   constexpr int kGroup = loader_threads<FP8>();
   constexpr int kRowStep = kGroup / 8, kWarps = kGroup / 32;
@@ -442,6 +446,9 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
         const int slot = a_row[u] >> 1;
         b_at[u] = reinterpret_cast<unsigned long long>(s.k + a_page[u] * s.page_stride + slot * s.row_stride) |
                   (a_row[u] & 1);
+        if (SHARED && a_full && ((gtid + u * kGroup) & (p.run_rows - 1)) == 0)
+          l2_prefetch(reinterpret_cast<const void *>(b_at[u] & ~15ull),
+                      (p.run_rows - 1) * (uint32_t)s.row_stride + (FP8 ? 512u : 1024u));
         if (FP8) {
           const long long sr = (long long)a_page[u] * s.page_rows + slot;
           b_ks[u] = __ldg(s.k_scale + sr);
@@ -570,17 +577,18 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
     if (nt > 1) fetch_scales();
     if (nt > 2) fetch_pages();
     for (int g = 0; g < nt; ++g) {
+      if (!WEIGHTS && !SHARED && g + 1 == nt) {
+        __syncwarp();
+        ok = !bar_red_or(2, kGroup, !ok);
+      }
       if (g + 1 < nt) {
         tma_next = store_list(g + 1);
         if (g + 2 < nt) fetch_scales();
         if (g + 3 < nt) fetch_pages();
         if (ms.flags[(g + 1) % kLists] & kFirst) load_q(ms.seq[(g + 1) % kLists]);
         for (int part = 0; part < 4 && ok; ++part) ok = emit(g + 1, part, tma_next);
-      } else {
-        __syncwarp();
-        ok = !bar_red_or(2, kGroup, !ok);
       }
-      if (!WEIGHTS)
+      if (!WEIGHTS && !SHARED)
         for (int part = 4; part < 8 && ok; ++part) ok = emit(g, part, tma);
       tma = tma_next;
     }
@@ -600,11 +608,11 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
 // Warps 9-12 with E4M3 rows: every stage's codes (upper half), one row per
 // thread, widened exactly to fp16 in the swizzled layout.  Row r's values
 // overwrite only row r's own codes, which its thread has read first.
-template <bool WEIGHTS>
+template <int PARTS>
 __device__ __forceinline__ void convert_role(const PagedAttnParams &p, uint32_t sbase, PMisc &ms, int row) {
   volatile int *abrt = &ms.abort_flag;
   StageRing ring;
-  const long long parts = (long long)ms.n_tiles * (WEIGHTS ? 4 : 8);
+  const long long parts = (long long)ms.n_tiles * PARTS;
   for (long long i = 0; i < parts; ++i) {
     if (!mbar_wait(smem_u32(&ms.code_full[ring.st]), ring.ph, abrt, p.timeout_ns, p.err, PSITE_CODE_FULL)) return;
     const uint32_t stage = sbase + kOffKV + ring.st * kStageBytes;
@@ -643,7 +651,7 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams &p, uint32_t 
 // and one elected lane issues (47 cycles per 128 x 64 x 16 MMA in a row; 61
 // when a single lane runs the role).  Waits are joined over the warp: all lanes go
 // on or none.
-template <bool FP8, bool WEIGHTS>
+template <bool FP8, bool WEIGHTS, bool SHARED>
 __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_t sbase, uint32_t tmem, PMisc &ms) {
   volatile int *abrt = &ms.abort_flag;
   constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
@@ -708,7 +716,7 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
                 umma_f16_acc(d_s, a, b, kIdescQK);
             }
           }
-          umma_commit(smem_u32(&ms.kv_empty[ring.st + u]));
+          if (!SHARED) umma_commit(smem_u32(&ms.kv_empty[ring.st + u]));
         }
         if (c + kStep == 4) umma_commit(smem_u32(&ms.s_full[sb]));
         if (c + kStep == 4 && last) umma_commit(smem_u32(&ms.q_empty));
@@ -727,8 +735,10 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
     }
     tc_fence_after();
     for (int m = 0; m < 4; m += kStep) {
-      if (!stages_ready(g)) return false;
-      const uint64_t a0 = sdesc_add(v_desc, ring.st * kStageBytes);
+      // Shared rows: part m still lies in stage m, where QK^T read it.
+      if (!SHARED && !stages_ready(g)) return false;
+      const int st = SHARED ? m : (int)ring.st;
+      const uint64_t a0 = sdesc_add(v_desc, st * kStageBytes);
       if (elect_lane()) {
 #pragma unroll
         for (int u = 0; u < kStep; ++u) {
@@ -741,14 +751,15 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
             else
               umma_f16_acc(tmem + 64 * (m + u), a, b, kIdescPV);
           }
-          umma_commit(smem_u32(&ms.kv_empty[ring.st + u]));
+          umma_commit(smem_u32(&ms.kv_empty[st + u]));
           if (last) umma_commit(smem_u32(&ms.o_full[m + u]));
         }
         if (m + kStep == 4) umma_commit(smem_u32(&ms.p_empty));
       }
       __syncwarp();
+      if (!SHARED)
 #pragma unroll
-      for (int u = 0; u < kStep; ++u) ring.advance();
+        for (int u = 0; u < kStep; ++u) ring.advance();
     }
     return true;
   };
@@ -757,11 +768,12 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
   if (nt > 0) ok = qk(0, true, w.last);
   for (int g = 0; g < nt && ok; ++g) {
     const bool first = w.first, last = w.last;
-    if (g + 1 < nt) {
+    if (SHARED) ok = pv(g, first, last);  // frees the stages of the next tile
+    if (ok && g + 1 < nt) {
       w.next(p);
       ok = qk(g + 1, w.first, w.last);
     }
-    if (!WEIGHTS) ok = ok && pv(g, first, last);
+    if (!WEIGHTS && !SHARED) ok = ok && pv(g, first, last);
   }
   commit(ms.mma_done);
   volatile int never = 0;
@@ -990,7 +1002,8 @@ __device__ __forceinline__ void weights_role(const PagedAttnParams &p, uint32_t 
 
 // ------------------------------------------------------------------ kernel
 
-template <bool FP8, bool WEIGHTS>
+// SHARED: K and V are the same rows, loaded once.
+template <bool FP8, bool WEIGHTS, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1045,13 +1058,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     else
       softmax_role<FP8>(p, smem, tmem, ms, threadIdx.x);
   } else if (warp == kMmaWarp) {
-    mma_role_paged<FP8, WEIGHTS>(p, sbase, tmem, ms);
+    mma_role_paged<FP8, WEIGHTS, SHARED>(p, sbase, tmem, ms);
   } else {
     const int ltid = threadIdx.x - 32 * kLoaderWarp0;
     if (FP8 && ltid >= 32 && ltid < 32 + kTile)
-      convert_role<WEIGHTS>(p, sbase, ms, ltid - 32);
+      convert_role<(WEIGHTS || SHARED) ? 4 : 8>(p, sbase, ms, ltid - 32);
     else
-      load_role<FP8, WEIGHTS>(p, sbase, ms, ltid);
+      load_role<FP8, WEIGHTS, SHARED>(p, sbase, ms, ltid);
   }
   tc_fence_before();
   __syncthreads();
@@ -1217,9 +1230,12 @@ cudaError_t launch_pdl(const void *f, const PagedAttnParams &p, int grid, int th
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const PagedAttnParams &p, bool e4m3, int grid, cudaStream_t s) {
-  return launch_pdl(e4m3 ? (const void *)paged_attn_kernel<true, false> : (const void *)paged_attn_kernel<false, false>,
-                    p, grid, kThreads, kPagedSmem, s);
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool e4m3, bool shared, int grid, cudaStream_t s) {
+  const void *f = e4m3 ? (shared ? (const void *)paged_attn_kernel<true, false, true>
+                                 : (const void *)paged_attn_kernel<true, false, false>)
+                       : (shared ? (const void *)paged_attn_kernel<false, false, true>
+                                 : (const void *)paged_attn_kernel<false, false, false>);
+  return launch_pdl(f, p, grid, kThreads, kPagedSmem, s);
 }
 
 // By the slots a sequence has on average, (CTAs + sequences) / sequences: four
@@ -1231,13 +1247,16 @@ cudaError_t launch_paged_merge(const PagedAttnParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_paged_weights(const PagedAttnParams &p, bool e4m3, int grid, cudaStream_t s) {
-  return launch_pdl(e4m3 ? (const void *)paged_attn_kernel<true, true> : (const void *)paged_attn_kernel<false, true>,
+  return launch_pdl(e4m3 ? (const void *)paged_attn_kernel<true, true, false>
+                         : (const void *)paged_attn_kernel<false, true, false>,
                     p, grid, kThreads, kPagedSmem, s);
 }
 
 cudaError_t prepare_paged_kernels() {
-  for (const void *f : {(const void *)paged_attn_kernel<false, false>, (const void *)paged_attn_kernel<true, false>,
-                        (const void *)paged_attn_kernel<false, true>, (const void *)paged_attn_kernel<true, true>}) {
+  for (const void *f :
+       {(const void *)paged_attn_kernel<false, false, false>, (const void *)paged_attn_kernel<true, false, false>,
+        (const void *)paged_attn_kernel<false, false, true>, (const void *)paged_attn_kernel<true, false, true>,
+        (const void *)paged_attn_kernel<false, true, false>, (const void *)paged_attn_kernel<true, true, false>}) {
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPagedSmem);
     if (e != cudaSuccess) return e;
   }

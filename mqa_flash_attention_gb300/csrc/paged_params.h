@@ -47,7 +47,7 @@ struct PagedAttnParams {
   unsigned int *err;
 };
 cudaError_t prepare_paged_kernels();  // shared-memory opt-in and code of the paged attention kernels
-cudaError_t launch_paged_decode(const PagedAttnParams &p, bool e4m3, int grid, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool e4m3, bool shared, int grid, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedAttnParams &p, cudaStream_t s);
 cudaError_t launch_paged_weights(const PagedAttnParams &p, bool e4m3, int grid, cudaStream_t s);
 
