@@ -64,6 +64,13 @@ bool table_ok(const ds4a_paged_rows *r) {
   return (int64_t)r->max_pages * r->page_rows <= kMostRows;
 }
 
+// The exponent of a power of two, -1 otherwise.
+int log2_of(int n) {
+  for (int i = 0; i < 31; ++i)
+    if (n == 1 << i) return i;
+  return -1;
+}
+
 PagedSeg seg_of(const ds4a_paged_rows *r) {
   PagedSeg s;
   std::memset(&s, 0, sizeof(s));
@@ -73,6 +80,7 @@ PagedSeg seg_of(const ds4a_paged_rows *r) {
   s.row_stride = r->row_stride;
   s.page_stride = r->page_stride;
   s.page_rows = r->page_rows;
+  s.page_shift = log2_of(r->page_rows);
   s.n_pages = r->n_pages;
   s.k_scale = r->k_scale;
   s.v_scale = r->v_scale;
@@ -110,6 +118,7 @@ int run_rows_of(int page_rows) {
 ds4a_status encode_comp(ds4a::PagedAttnParams &p, const ds4a_paged_rows *r, bool need_v) {
   p.run_rows = has_rows(r) ? run_rows_of(r->page_rows) : 0;
   if (p.run_rows == 0) return DS4A_OK;
+  p.run_shift = log2_of(p.run_rows);
   const bool e4m3 = r->k_scale != nullptr;
   ds4a_status st = ds4a::host_encode_pages(&p.tm_k, r->k, e4m3, r->page_rows, r->n_pages, r->row_stride,
                                            r->page_stride, p.run_rows);

@@ -88,6 +88,13 @@ struct SeqRows {
   __device__ __forceinline__ int tiles() const { return (nr + nc + kTile - 1) / kTile; }
 };
 
+// A CTA's tiles: n of them, from tile `tile` of sequence `seq` on.  The slot of
+// an item is CTA + slot_step * sequence.
+struct CtaPlan {
+  int n, seq, tile, slot_step;
+  SeqRows rows;  // of sequence `seq`
+};
+
 struct PMisc {
   alignas(16) unsigned long long row[kLists][kTile];  // K address | kSegBit | kNoRow
   alignas(16) float ksc[kLists][kTile];   // E4M3: scale * log2(e) * K scale
@@ -108,10 +115,7 @@ struct PMisc {
   uint64_t o_full[4];
   uint64_t p_full, p_empty, o_empty, mma_done;
   unsigned scan[kThreads / 32];
-  int first_seq, first_tile;  // where this CTA's tiles start: sequence, tile within it
-  SeqRows first_rows;
-  int n_tiles;                // tiles of this CTA
-  int slot_step;              // slot of an item: CTA + slot_step * sequence
+  CtaPlan plan;
   int fits[kThreads / 32];
   uint32_t tmem_base;
   int abort_flag;
@@ -238,12 +242,12 @@ struct Walk {
   SeqRows rows;
   bool first, last;  // of this CTA's tiles of the sequence (an item)
   int left;      // tiles of the CTA from this one on
-  __device__ __forceinline__ void start(const PagedAttnParams &p, const PMisc &ms) {
-    b = ms.first_seq;
-    j = ms.first_tile;
-    left = ms.n_tiles;
+  __device__ __forceinline__ void start(const CtaPlan &cp) {
+    b = cp.seq;
+    j = cp.tile;
+    left = cp.n;
     if (left <= 0) return;
-    rows = ms.first_rows;
+    rows = cp.rows;
     n = rows.tiles();
     first = true;
     last = j == n - 1 || left == 1;
@@ -268,24 +272,100 @@ struct Walk {
   int first_j;   // tile the item began with
 };
 
-// Block-wide: where this CTA starts and how many tiles it has; CTA 0 also
-// writes each sequence's slots for the merge.  Thread t counts sequence t (of
-// every round of 512).  The caller's barrier publishes the result.  `counts`:
-// 512 ints of shared memory, free until then.
+__device__ __forceinline__ int scan_warp(int n, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) n += t;
+  }
+  return n;
+}
+
+constexpr int kTries = 16;       // item sizes tried from the average up
+
+// The plan of this CTA, by one warp alone: lane l has kMost sequences in a
+// row.  Every warp computes it for itself (no block barrier stands between the
+// geometry and the first load); `writes`: this one writes each sequence's slots
+// for the merge.
+template <bool WEIGHTS, int kMost>
+__device__ __forceinline__ CtaPlan plan_warp(const PagedAttnParams &p, int lane, bool writes) {
+  const int G = gridDim.x, cta = blockIdx.x;
+  const SeqRows none = {0, 0, 0};
+  SeqRows rows[kMost];
+  int n[kMost], sum = 0;
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    const int b = lane * kMost + u;
+    rows[u] = b < p.n_seq ? seq_rows<WEIGHTS>(p, b) : none;
+    n[u] = rows[u].tiles();
+    sum += n[u];
+  }
+  const int total = __reduce_add_sync(0xffffffffu, sum), per = (total + G - 1) / G;
+  int c = per, items = G + 1;
+  for (int t = 0; t < kTries && total > 0; ++t, ++c) {
+    int k = 0;
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) k += (unsigned)(n[u] + c - 1) / (unsigned)c;
+    items = __reduce_add_sync(0xffffffffu, k);
+    if (items <= G) break;
+  }
+  const bool one = items <= G;  // one item per CTA
+  int count[kMost], mine = 0;   // of the unit that is dealt out: items, or tiles
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    count[u] = one ? (int)((unsigned)(n[u] + c - 1) / (unsigned)c) : n[u];
+    mine += count[u];
+  }
+  int at = scan_warp(mine, lane) - mine;  // items or tiles before this lane's sequences
+  const int g0 = one ? cta : min(total, cta * per), g1 = one ? cta + 1 : min(total, g0 + per);
+  CtaPlan cp = {0, 0, 0, one ? 0 : 1, none};
+  bool found = false;
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    const int b = lane * kMost + u;
+    if (count[u] > 0 && at <= g0 && g0 < at + count[u] && g1 > g0) {
+      found = true;
+      cp.seq = b;
+      cp.rows = rows[u];
+      if (one) {
+        const unsigned i = g0 - at, k = count[u];
+        cp.tile = (int)(i * (unsigned)n[u] / k);
+        cp.n = (int)((i + 1) * (unsigned)n[u] / k) - cp.tile;
+      } else {
+        cp.tile = g0 - at;
+        cp.n = g1 - g0;
+      }
+    }
+    if (writes && b < p.n_seq) {
+      int2 slots = make_int2(at, count[u]);
+      if (!one) {
+        const int c0 = n[u] > 0 ? at / per : 0, c1 = n[u] > 0 ? (at + n[u] - 1) / per : -1;
+        slots = make_int2(c0 + b, c1 - c0 + 1);
+      }
+      p.ws_plan[b] = slots;
+    }
+    at += count[u];
+  }
+  const unsigned who = __ballot_sync(0xffffffffu, found);
+  const int src = who != 0 ? __ffs(who) - 1 : 0;
+  cp.n = __shfl_sync(0xffffffffu, cp.n, src);
+  cp.seq = __shfl_sync(0xffffffffu, cp.seq, src);
+  cp.tile = __shfl_sync(0xffffffffu, cp.tile, src);
+  cp.rows.raw_lo = __shfl_sync(0xffffffffu, cp.rows.raw_lo, src);
+  cp.rows.nr = __shfl_sync(0xffffffffu, cp.rows.nr, src);
+  cp.rows.nc = __shfl_sync(0xffffffffu, cp.rows.nc, src);
+  return cp;
+}
+
+// The same for more sequences, by the whole block: thread t counts sequence t
+// of every round of 512.  `counts`: 512 ints of shared memory, free until the
+// caller's barrier, which publishes the result (ms.plan).
 template <bool WEIGHTS>
-__device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms, int *counts) {
+__device__ __forceinline__ void plan_block(const PagedAttnParams &p, PMisc &ms, int *counts) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = gridDim.x, cta = blockIdx.x;
   const SeqRows none = {0, 0, 0};
-  auto scan_warp = [&](int n) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, n, o);
-      if (lane >= o) n += t;
-    }
-    return n;
-  };
   // Sum over the warps before this one, and over all, of `inc` in lane 31.
   auto before_warp = [&](int inc, int &all) {
     if (lane == 31) ms.scan[warp] = inc;
@@ -298,11 +378,11 @@ __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms, in
   int n = rows.tiles(), mine = n, total;
   for (int b = tid + kThreads; b < p.n_seq; b += kThreads) mine += seq_rows<WEIGHTS>(p, b).tiles();
   counts[tid] = n;
-  int inc = scan_warp(mine);
+  int inc = scan_warp(mine, lane);
   int before = before_warp(inc, total);
   const int per = (total + G - 1) / G;
   if (p.n_seq <= kThreads && total > 0) {
-    // One item per CTA: warp w tries c = per + w.
+    static_assert(kTries == kWarps, "a warp per item size");
     int items = 0;
     for (int b = lane; b < p.n_seq; b += 32) items += (counts[b] + per + warp - 1) / (per + warp);
     items = __reduce_add_sync(0xffffffffu, items);
@@ -312,44 +392,34 @@ __device__ __forceinline__ void plan_cta(const PagedAttnParams &p, PMisc &ms, in
     if (fit != 0) {
       const int c = per + __ffs(fit) - 1, k = (n + c - 1) / c;
       int all;
-      inc = scan_warp(k);
+      inc = scan_warp(k, lane);
       const int first = before_warp(inc, all) + inc - k;  // CTA of the sequence's first item
-      if (tid == 0) ms.slot_step = 0;
-      if (cta >= all && tid == 0) ms.n_tiles = 0;
+      if (cta >= all && tid == 0) ms.plan.n = 0;
       if (k > 0 && first <= cta && cta < first + k) {
-        const int i = cta - first, j0 = (int)((long long)i * n / k), j1 = (int)((long long)(i + 1) * n / k);
-        ms.first_seq = tid;
-        ms.first_tile = j0;
-        ms.first_rows = rows;
-        ms.n_tiles = j1 - j0;
+        const unsigned i = cta - first;
+        const int j0 = (int)(i * (unsigned)n / (unsigned)k);
+        ms.plan = CtaPlan{(int)((i + 1) * (unsigned)n / (unsigned)k) - j0, tid, j0, 0, rows};
       }
       if (!WEIGHTS && cta == 0 && tid < p.n_seq) p.ws_plan[tid] = make_int2(first, k);
       return;
     }
   }
   const int g0 = min(total, cta * per), g1 = min(total, g0 + per);
-  if (tid == 0) {
-    ms.n_tiles = g1 - g0;
-    ms.slot_step = 1;
-  }
+  if (tid == 0 && g1 == g0) ms.plan.n = 0;
   int carry = 0;
   for (int b0 = 0; b0 < p.n_seq; b0 += kThreads) {
     const int b = b0 + tid;
     if (p.n_seq > kThreads) {  // several rounds: scan each by itself
       rows = b < p.n_seq ? seq_rows<WEIGHTS>(p, b) : none;
       n = rows.tiles();
-      inc = scan_warp(n);
+      inc = scan_warp(n, lane);
       int all;
       __syncthreads();
       before = carry + before_warp(inc, all);
       carry += all;
     }
     const int at = before + inc - n;  // tiles before sequence b
-    if (n > 0 && at <= g0 && g0 < at + n && g1 > g0) {
-      ms.first_seq = b;
-      ms.first_tile = g0 - at;
-      ms.first_rows = rows;
-    }
+    if (n > 0 && at <= g0 && g0 < at + n && g1 > g0) ms.plan = CtaPlan{g1 - g0, b, g0 - at, 1, rows};
     if (!WEIGHTS && cta == 0 && b < p.n_seq) {
       const int c0 = n > 0 ? at / per : 0, c1 = n > 0 ? (at + n - 1) / per : -1;
       p.ws_plan[b] = make_int2(c0 + b, c1 - c0 + 1);
@@ -377,7 +447,8 @@ __device__ __forceinline__ void prefetch_tables(const PagedAttnParams &p) {
 // issued, the page ids of tile g + 3 and the scales of tile g + 2 are on their
 // way in registers, so neither latency stands between tiles.
 template <bool FP8, bool WEIGHTS, bool SHARED>
-__device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sbase, PMisc &ms, int ltid) {
+__device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPlan &cp, uint32_t sbase, PMisc &ms,
+                                          int ltid) {
   constexpr int kGroup = loader_threads<FP8>();
   constexpr int kRowStep = kGroup / 8, kWarps = kGroup / 32;
   constexpr int kMine = (kTile + kGroup - 1) / kGroup;  // list rows of a thread
@@ -390,14 +461,14 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
   const unsigned long long pad_row = reinterpret_cast<unsigned long long>(p.seg[pad_seg].k) | pad_seg | kNoRow;
   StageRing ring;
   bool ok = true;
-  bool q_issued = false;
-  uint32_t n_item = 0, q_par = 0;
+  bool q_issued = cp.n > 0;  // (the first Q by the kernel's thread 0)
+  uint32_t n_item = 1, q_par = 0;
   uint32_t filled = 0, last_par = 0;  // TMA stages this thread issued, and their phases
   int turn = 0;                       // warp of the next part's first run
-  const int nt = ms.n_tiles;
+  const int nt = cp.n;
 
   Walk<WEIGHTS> w;     // at the tile whose page ids are fetched next
-  w.start(p, ms);
+  w.start(cp);
   // Tile whose page ids are in flight, then tile whose scales are.
   int a_row[kMine], a_page[kMine], a_seq = 0, a_flags = 0, a_base = 0, a_end = 0;
   bool a_full = false, b_full = false;  // 128 compressed rows in runs that TMA can copy
@@ -421,14 +492,14 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
         const int sg = x < w.rows.nc ? 1 : 0;
         const PagedSeg &s = p.seg[sg];
         const int row = sg == 0 ? w.rows.raw_lo + x - w.rows.nc : x;
-        const int pi = row / s.page_rows;
+        const int pi = s.page_shift >= 0 ? row >> s.page_shift : row / s.page_rows;
         a_page[u] = __ldg(s.table + w.b * s.table_stride + pi);
         a_row[u] = 2 * (row - pi * s.page_rows) + sg;
       }
     }
     w.next(p);
   };
-  auto fetch_scales = [&]() {
+  auto fetch_scales = [&](bool ahead) {
     b_seq = a_seq;
     b_flags = a_flags;
     b_base = a_base;
@@ -446,7 +517,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
         const int slot = a_row[u] >> 1;
         b_at[u] = reinterpret_cast<unsigned long long>(s.k + a_page[u] * s.page_stride + slot * s.row_stride) |
                   (a_row[u] & 1);
-        if (SHARED && a_full && ((gtid + u * kGroup) & (p.run_rows - 1)) == 0)
+        if (SHARED && ahead && a_full && ((gtid + u * kGroup) & (p.run_rows - 1)) == 0)
           l2_prefetch(reinterpret_cast<const void *>(b_at[u] & ~15ull),
                       (p.run_rows - 1) * (uint32_t)s.row_stride + (FP8 ? 512u : 1024u));
         if (FP8) {
@@ -473,7 +544,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
         if (r < kTile) {
           ms.row[buf][r] = b_at[u];
           absent = absent || (b_at[u] & kNoRow);
-          if (full && (r & (p.run_rows - 1)) == 0) ms.box[buf][r / p.run_rows] = make_int2(b_page[u], b_slot[u]);
+          if (full && (r & (p.run_rows - 1)) == 0) ms.box[buf][r >> p.run_shift] = make_int2(b_page[u], b_slot[u]);
           if (FP8) {
             ms.ksc[buf][r] = p.scale_log2 * b_ks[u];
             if (!WEIGHTS) {
@@ -512,7 +583,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
       // Run i of a part goes to one lane of warp (turn + i) % warps, so that
       // the warps share the copies of a part and of successive parts; lane 0
       // of each warp arrives for all its lanes.
-      const int lane = ltid & 31, runs = kTile / p.run_rows;
+      const int lane = ltid & 31, runs = kTile >> p.run_shift;
       const int first = gtid / 32 - turn, i = (first < 0 ? first + kWarps : first) + lane * kWarps;
       turn = (turn + runs) % kWarps;
       if (lane == 0) {
@@ -522,7 +593,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
       if (i < runs) {
         filled |= st_bit;
         last_par = ph ? last_par & ~st_bit : last_par | st_bit;
-        const uint32_t at = i * p.run_rows * (FP8 ? 128u : 256u);
+        const uint32_t at = (i << p.run_shift) * (FP8 ? 128u : 256u);
         const CUtensorMap *m = part >= 4 ? &p.tm_v : &p.tm_k;
         const int2 x = ms.box[g % kLists][i];
         if (FP8)
@@ -568,13 +639,12 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
   };
 
   if (nt > 0) {
-    load_q(w.b);
     fetch_pages();
-    fetch_scales();
+    fetch_scales(false);
     bool tma = store_list(0), tma_next = false;
     for (int part = 0; part < 4 && ok; ++part) ok = emit(0, part, tma);
     if (nt > 1) fetch_pages();
-    if (nt > 1) fetch_scales();
+    if (nt > 1) fetch_scales(true);
     if (nt > 2) fetch_pages();
     for (int g = 0; g < nt; ++g) {
       if (!WEIGHTS && !SHARED && g + 1 == nt) {
@@ -583,7 +653,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
       }
       if (g + 1 < nt) {
         tma_next = store_list(g + 1);
-        if (g + 2 < nt) fetch_scales();
+        if (g + 2 < nt) fetch_scales(true);
         if (g + 3 < nt) fetch_pages();
         if (ms.flags[(g + 1) % kLists] & kFirst) load_q(ms.seq[(g + 1) % kLists]);
         for (int part = 0; part < 4 && ok; ++part) ok = emit(g + 1, part, tma_next);
@@ -609,10 +679,11 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, uint32_t sba
 // thread, widened exactly to fp16 in the swizzled layout.  Row r's values
 // overwrite only row r's own codes, which its thread has read first.
 template <int PARTS>
-__device__ __forceinline__ void convert_role(const PagedAttnParams &p, uint32_t sbase, PMisc &ms, int row) {
+__device__ __forceinline__ void convert_role(const PagedAttnParams &p, const CtaPlan &cp, uint32_t sbase, PMisc &ms,
+                                             int row) {
   volatile int *abrt = &ms.abort_flag;
   StageRing ring;
-  const long long parts = (long long)ms.n_tiles * PARTS;
+  const long long parts = (long long)cp.n * PARTS;
   for (long long i = 0; i < parts; ++i) {
     if (!mbar_wait(smem_u32(&ms.code_full[ring.st]), ring.ph, abrt, p.timeout_ns, p.err, PSITE_CODE_FULL)) return;
     const uint32_t stage = sbase + kOffKV + ring.st * kStageBytes;
@@ -652,7 +723,8 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams &p, uint32_t 
 // when a single lane runs the role).  Waits are joined over the warp: all lanes go
 // on or none.
 template <bool FP8, bool WEIGHTS, bool SHARED>
-__device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_t sbase, uint32_t tmem, PMisc &ms) {
+__device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const CtaPlan &cp, uint32_t sbase,
+                                               uint32_t tmem, PMisc &ms) {
   volatile int *abrt = &ms.abort_flag;
   constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
   constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
@@ -664,7 +736,7 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
   const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
   const uint64_t p_desc = sdesc_sw128(sbase + kOffP, 16, 1024);
   StageRing ring;
-  const int nt = ms.n_tiles;
+  const int nt = cp.n;
   uint32_t q_item = 0, o_item = 0;
   bool ok = true;
   auto wait = [&](uint64_t &bar, uint32_t parity, unsigned int site) -> bool {
@@ -764,7 +836,7 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
     return true;
   };
   Walk<WEIGHTS> w;
-  w.start(p, ms);
+  w.start(cp);
   if (nt > 0) ok = qk(0, true, w.last);
   for (int g = 0; g < nt && ok; ++g) {
     const bool first = w.first, last = w.last;
@@ -784,15 +856,15 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, uint32_
 // ------------------------------------------------------------------ softmax and epilogue
 
 template <bool FP8>
-__device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *smem, uint32_t tmem, PMisc &ms,
-                                             int tid) {
+__device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const CtaPlan &cp, uint8_t *smem, uint32_t tmem,
+                                             PMisc &ms, int tid) {
   volatile int *abrt = &ms.abort_flag;
   const int wq = tid >> 5, l = tid & 31;
   const int q = wq & 3, hh = wq >> 2;  // TMEM lane quarter, head half
   const int r = 32 * q + l;            // row of the tile, or dim of a 128-dim block
   const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
   const uint32_t col0 = 32 * hh;
-  const int nt = ms.n_tiles;
+  const int nt = cp.n;
   bool bad = false;
   uint32_t n_item = 0;
   float m_ref = -INFINITY;  // reference of head `tid` (threads < 64), log2 units
@@ -901,7 +973,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
     // them: fp16 and normalised for a whole sequence, else fp32 and normalised
     // by the item's own sum.
     const bool whole = flags & kWhole;
-    const long long slot = (long long)blockIdx.x + (long long)ms.slot_step * seq;
+    const long long slot = (long long)blockIdx.x + (long long)cp.slot_step * seq;
     ms.red[q][col0 + l] = reduce_heads<false>(lpart, l);
     if (bar_red_or(1, kComputeThreads, bad)) break;
     if (tid < kH) {
@@ -950,14 +1022,15 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, uint8_t *
 // Weights: row r of a tile is TMEM lane r; each head half adds its 32 heads'
 // exponentials in registers and the halves meet in shared memory.
 template <bool FP8>
-__device__ __forceinline__ void weights_role(const PagedAttnParams &p, uint32_t tmem, PMisc &ms, int tid) {
+__device__ __forceinline__ void weights_role(const PagedAttnParams &p, const CtaPlan &cp, uint32_t tmem, PMisc &ms,
+                                             int tid) {
   volatile int *abrt = &ms.abort_flag;
   const int wq = tid >> 5, l = tid & 31;
   const int q = wq & 3, hh = wq >> 2;
   const int r = 32 * q + l;
   const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
   const uint32_t col0 = 32 * hh;
-  const int nt = ms.n_tiles;
+  const int nt = cp.n;
   bool bad = false;
   float *part = &ms.red[0][0];  // [2][128] by tile parity (256 floats)
   for (int g = 0; g < nt; ++g) {
@@ -1044,27 +1117,43 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     tmem_alloc(smem_u32(&ms.tmem_base), kTmemCols);
     tmem_relinquish();
   }
-  grid_launch_dependents();
   prefetch_tables<WEIGHTS>(p);
-  grid_dependency_wait();  // the plan reads the sequences' geometry
-  plan_cta<WEIGHTS>(p, ms, reinterpret_cast<int *>(smem + kOffKV));
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // barriers and TMEM are ready
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
+  grid_launch_dependents();
+  grid_dependency_wait();  // the plan reads the sequences' geometry
+  CtaPlan cp;
+  const bool writes = !WEIGHTS && blockIdx.x == 0 && warp == 0;
+  if (p.n_seq <= 32) {
+    cp = plan_warp<WEIGHTS, 1>(p, threadIdx.x & 31, writes);
+  } else if (p.n_seq <= 64) {
+    cp = plan_warp<WEIGHTS, 2>(p, threadIdx.x & 31, writes);
+  } else {
+    plan_block<WEIGHTS>(p, ms, reinterpret_cast<int *>(smem + kOffKV));
+    __syncthreads();
+    cp = ms.plan;
+  }
+  // The first item's Q, by a thread of the compute warps (which wait for it);
+  // the loaders issue those of further items.
+  if (threadIdx.x == 0 && cp.n > 0) {
+    mbar_arrive_expect_tx(smem_u32(&ms.q_full), kQBytes);
+    tma_load_4d(sbase + kOffQ, &p.tm_q, smem_u32(&ms.q_full), 0, 0, cp.seq, 0);
+  }
   if (warp < kComputeWarps) {
     if (WEIGHTS)
-      weights_role<FP8>(p, tmem, ms, threadIdx.x);
+      weights_role<FP8>(p, cp, tmem, ms, threadIdx.x);
     else
-      softmax_role<FP8>(p, smem, tmem, ms, threadIdx.x);
+      softmax_role<FP8>(p, cp, smem, tmem, ms, threadIdx.x);
   } else if (warp == kMmaWarp) {
-    mma_role_paged<FP8, WEIGHTS, SHARED>(p, sbase, tmem, ms);
+    mma_role_paged<FP8, WEIGHTS, SHARED>(p, cp, sbase, tmem, ms);
   } else {
     const int ltid = threadIdx.x - 32 * kLoaderWarp0;
     if (FP8 && ltid >= 32 && ltid < 32 + kTile)
-      convert_role<(WEIGHTS || SHARED) ? 4 : 8>(p, sbase, ms, ltid - 32);
+      convert_role<(WEIGHTS || SHARED) ? 4 : 8>(p, cp, sbase, ms, ltid - 32);
     else
-      load_role<FP8, WEIGHTS, SHARED>(p, sbase, ms, ltid);
+      load_role<FP8, WEIGHTS, SHARED>(p, cp, sbase, ms, ltid);
   }
   tc_fence_before();
   __syncthreads();

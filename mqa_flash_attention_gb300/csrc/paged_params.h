@@ -14,6 +14,7 @@ struct PagedSeg {
   const uint8_t *k, *v;
   long long row_stride, page_stride;
   int page_rows, n_pages;
+  int page_shift;                  // log2 of page_rows, or -1
   const float *k_scale, *v_scale;  // E4M3 rows: [n_pages][page_rows]
   const int32_t *table;
   long long table_stride;          // elements
@@ -26,7 +27,7 @@ struct PagedAttnParams {
   // blocks, page_rows / 8, pages}, box {64, 8, 2, run_rows / 8, 1}; codes 3-D
   // {512, page_rows, pages}, box {128, run_rows, 1}.
   CUtensorMap tm_k, tm_v;
-  int run_rows;            // 8 .. 128, a power of two; 0: no TMA loads
+  int run_rows, run_shift; // 8 .. 128, a power of two, and its log2; 0: no TMA loads
   PagedSeg seg[2];         // raw, compressed
   const int4 *geom;        // (q_pos, n_raw, raw_pos0, n_comp) per sequence
   int n_seq, ratio, window;
