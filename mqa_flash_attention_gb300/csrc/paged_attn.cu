@@ -102,7 +102,8 @@ struct PMisc {
   alignas(16) float ivs[kLists][kTile];   // E4M3: 2^-lvs
   int2 box[kLists][kTile / 8];            // (page, slot) of the runs of a tile that TMA loads
   alignas(16) float red[4][kH];
-  alignas(16) float m_use[kH];
+  alignas(16) float m_use[kH];  // reference of each head (weights: its lse), log2 units
+  alignas(16) float m_lim[kH];  // m_use + kTau
   alignas(16) float alpha[kH];
   alignas(16) float inv_l[kH];
   alignas(8) uint64_t q_full, q_empty;
@@ -119,7 +120,6 @@ struct PMisc {
   int fits[kThreads / 32];
   uint32_t tmem_base;
   int abort_flag;
-  int resc_flag[2];
 };
 constexpr uint32_t kPagedSmem = kOffMisc + ((sizeof(PMisc) + 127) / 128) * 128 + 1024;
 static_assert(kPagedSmem <= 232448, "shared memory of one CTA");
@@ -474,6 +474,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
   bool a_full = false, b_full = false;  // 128 compressed rows in runs that TMA can copy
   unsigned long long b_at[kMine];
   int b_page[kMine], b_slot[kMine];
+  bool b_tma = false;
   float b_ks[kMine], b_vs[kMine];
   int b_seq = 0, b_flags = 0, b_base = 0, b_end = 0;
 
@@ -528,12 +529,13 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
       }
     }
   };
-  // The list of tile g, complete for the whole group; all go on or none.
+  // The rows of tile g, complete for the whole group; all go on or none.
   // Returns whether TMA loads the tile.
   auto store_list = [&](int g) -> bool {
     const int buf = g % kLists;
     const bool full = b_full;
     bool absent = false;
+    b_tma = false;
     if (ok && !mbar_wait(smem_u32(&ms.list_empty[buf]), ((g / kLists) & 1) ^ 1, abrt, p.timeout_ns, p.err,
                          PSITE_LIST_EMPTY))
       ok = false;
@@ -545,7 +547,24 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
           ms.row[buf][r] = b_at[u];
           absent = absent || (b_at[u] & kNoRow);
           if (full && (r & (p.run_rows - 1)) == 0) ms.box[buf][r >> p.run_shift] = make_int2(b_page[u], b_slot[u]);
-          if (FP8) {
+        }
+      }
+    }
+    __syncwarp();  // the barrier below is one of whole warps
+    const bool odd = bar_red_or(2, kGroup, !ok || (full && absent));
+    if (odd) ok = !bar_red_or(2, kGroup, !ok);
+    b_tma = full && !odd;
+    return b_tma;
+  };
+  // The rest of it, once its rows are on their way: what the other warps need.
+  auto finish_list = [&](int g) {
+    const int buf = g % kLists;
+    if (ok) {
+      if (FP8) {
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+          const int r = gtid + u * kGroup;
+          if (r < kTile) {
             ms.ksc[buf][r] = p.scale_log2 * b_ks[u];
             if (!WEIGHTS) {
               const float lv = fmaxf(__log2f(b_vs[u]), kLeastLog2Scale);
@@ -556,19 +575,14 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
         }
       }
       if (gtid == 0) {
+        ms.gathered[buf] = !b_tma;
         ms.seq[buf] = b_seq;
         ms.flags[buf] = b_flags;
         ms.base[buf] = b_base;
         ms.end[buf] = b_end;
       }
     }
-    __syncwarp();  // the barrier below is one of whole warps
-    const bool odd = bar_red_or(2, kGroup, !ok || (full && absent));
-    if (odd) ok = !bar_red_or(2, kGroup, !ok);
-    const bool tma = full && !odd;
-    if (gtid == 0 && ok) ms.gathered[buf] = !tma;
     mbar_arrive(smem_u32(&ms.list_full[buf]));
-    return tma;
   };
   // One part of tile g into the next stage (parts 0-3: K dims 128 part .., 4-7: V).
   auto emit = [&](int g, int part, bool tma) -> bool {
@@ -643,6 +657,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
     fetch_scales(false);
     bool tma = store_list(0), tma_next = false;
     for (int part = 0; part < 4 && ok; ++part) ok = emit(0, part, tma);
+    finish_list(0);
     if (nt > 1) fetch_pages();
     if (nt > 1) fetch_scales(true);
     if (nt > 2) fetch_pages();
@@ -653,10 +668,14 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
       }
       if (g + 1 < nt) {
         tma_next = store_list(g + 1);
-        if (g + 2 < nt) fetch_scales(true);
-        if (g + 3 < nt) fetch_pages();
-        if (ms.flags[(g + 1) % kLists] & kFirst) load_q(ms.seq[(g + 1) % kLists]);
+        if (b_flags & kFirst) load_q(b_seq);
+        if (SHARED) finish_list(g + 1);  // (the next rows are prefetched before these copies wait for their stages)
+        if (SHARED && g + 2 < nt) fetch_scales(true);
+        if (SHARED && g + 3 < nt) fetch_pages();
         for (int part = 0; part < 4 && ok; ++part) ok = emit(g + 1, part, tma_next);
+        if (!SHARED) finish_list(g + 1);
+        if (!SHARED && g + 2 < nt) fetch_scales(true);
+        if (!SHARED && g + 3 < nt) fetch_pages();
       }
       if (!WEIGHTS && !SHARED)
         for (int part = 4; part < 8 && ok; ++part) ok = emit(g, part, tma);
@@ -855,6 +874,13 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const C
 
 // ------------------------------------------------------------------ softmax and epilogue
 
+// The reference of a head is a value its scores stay within 2^kTau of, so P
+// fits fp16; it moves only when a score passes that.  While it holds (nearly
+// always after a sequence's first tile) a tile needs no maximum over its rows:
+// one vote of the block that no score is over.  kNoRef stands for no reference
+// yet: any score passes it, and absent rows (-inf) get weight 0 under it.
+constexpr float kNoRef = -1e30f;
+
 template <bool FP8>
 __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const CtaPlan &cp, uint8_t *smem, uint32_t tmem,
                                              PMisc &ms, int tid) {
@@ -867,15 +893,16 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
   const int nt = cp.n;
   bool bad = false;
   uint32_t n_item = 0;
-  float m_ref = -INFINITY;  // reference of head `tid` (threads < 64), log2 units
+  float m_ref = kNoRef;  // reference of head `tid` (threads < 64), log2 units
   float lpart[32];
+  if (tid < kH) ms.m_use[tid] = ms.m_lim[tid] = kNoRef;
+  bar_sync_id(1, kComputeThreads);
   for (int g = 0; g < nt; ++g) {
     const int buf = g % kLists;
     const uint32_t sb = g & 1;
     bad = bad || !mbar_wait(smem_u32(&ms.list_full[buf]), (g / kLists) & 1, abrt, p.timeout_ns, p.err, PSITE_LIST_FULL);
     const int flags = ms.flags[buf], seq = ms.seq[buf];
     if (flags & kFirst) {
-      m_ref = -INFINITY;
 #pragma unroll
       for (int h = 0; h < 32; ++h) lpart[h] = 0.f;
     }
@@ -891,27 +918,36 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
     tmem_wait_ld();
     tc_fence_before();
     mbar_arrive(smem_u32(&ms.s_empty[sb]));
+    bool over = false;
 #pragma unroll
-    for (int h = 0; h < 32; ++h) s[h] = vis ? fmaf(s[h], sl2, lvs) : -INFINITY;
-
-    ms.red[q][col0 + l] = reduce_heads<true>(s, l);
-    if (bar_red_or(1, kComputeThreads, bad)) break;
-    if (tid < kH) {
-      const float tmax = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid]));
-      float alpha = 1.f;
-      if (m_ref == -INFINITY) {
-        m_ref = tmax;
-      } else if (tmax > m_ref + kTau) {  // the reference moves only when P would pass 2^8
-        alpha = exp2f(m_ref - tmax);
-        m_ref = tmax;
+    for (int c = 0; c < 8; ++c) {
+      const float4 lim = reinterpret_cast<const float4 *>(ms.m_lim + col0)[c];
+      const float li[4] = {lim.x, lim.y, lim.z, lim.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[4 * c + i] = vis ? fmaf(s[4 * c + i], sl2, lvs) : -INFINITY;
+        over = over || s[4 * c + i] > li[i];
       }
-      ms.m_use[tid] = m_ref == -INFINITY ? 0.f : m_ref;
-      ms.alpha[tid] = alpha;
-      if (alpha != 1.f) ms.resc_flag[g & 1] = 1;
     }
-    bar_sync_id(1, kComputeThreads);
-    const int resc = ms.resc_flag[g & 1];
-    if (tid == 0) ms.resc_flag[(g + 1) & 1] = 0;
+    bool resc = false;
+    if (bar_red_or(1, kComputeThreads, over || bad)) {
+      // Some head's reference moves: the tile's maxima over the rows.
+      ms.red[q][col0 + l] = reduce_heads<true>(s, l);
+      if (bar_red_or(1, kComputeThreads, bad)) break;
+      if (tid < kH) {
+        const float tmax = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid]));
+        float alpha = 1.f;
+        if (tmax > m_ref + kTau) {
+          alpha = exp2f(m_ref - tmax);  // 0 while there was none
+          m_ref = tmax;
+        }
+        ms.m_use[tid] = m_ref;
+        ms.m_lim[tid] = m_ref + kTau;
+        ms.alpha[tid] = alpha;
+      }
+      bar_sync_id(1, kComputeThreads);
+      resc = true;
+    }
     bad = bad || !mbar_wait(smem_u32(&ms.p_empty), (g & 1) ^ 1, abrt, p.timeout_ns, p.err, PSITE_P_EMPTY);
     {
       // P^T row r: heads 32hh .. +31 are 16-byte chunks 4hh .. 4hh+3 of its
@@ -1015,6 +1051,8 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
     tc_fence_before();
     mbar_arrive(smem_u32(&ms.o_empty));
     ++n_item;
+    m_ref = kNoRef;
+    if (tid < kH) ms.m_use[tid] = ms.m_lim[tid] = kNoRef;
     if (bar_red_or(1, kComputeThreads, bad)) break;
   }
 }
@@ -1105,7 +1143,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     mbar_init(smem_u32(&ms.o_empty), kComputeThreads);
     mbar_init(smem_u32(&ms.mma_done), 1);
     ms.abort_flag = 0;
-    ms.resc_flag[0] = ms.resc_flag[1] = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.tm_q);
     if (p.run_rows > 0) {
