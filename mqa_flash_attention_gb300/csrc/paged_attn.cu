@@ -357,6 +357,21 @@ __device__ __forceinline__ CtaPlan plan_warp(const PagedAttnParams &p, int lane,
   return cp;
 }
 
+// The same for a single sequence: nothing to add up.
+template <bool WEIGHTS>
+__device__ __forceinline__ CtaPlan plan_one(const PagedAttnParams &p, bool writes) {
+  const SeqRows rows = seq_rows<WEIGHTS>(p, 0);
+  const unsigned n = rows.tiles(), G = gridDim.x, i = blockIdx.x;
+  const unsigned c = (n + G - 1) / G, k = n > 0 ? (n + c - 1) / c : 0;  // tiles of an item, items
+  CtaPlan cp = {0, 0, 0, 0, rows};
+  if (i < k) {
+    cp.tile = (int)(i * n / k);
+    cp.n = (int)((i + 1) * n / k) - cp.tile;
+  }
+  if (writes && threadIdx.x == 0) p.ws_plan[0] = make_int2(0, (int)k);
+  return cp;
+}
+
 // The same for more sequences, by the whole block: thread t counts sequence t
 // of every round of 512.  `counts`: 512 ints of shared memory, free until the
 // caller's barrier, which publishes the result (ms.plan).
@@ -1163,7 +1178,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   grid_dependency_wait();  // the plan reads the sequences' geometry
   CtaPlan cp;
   const bool writes = !WEIGHTS && blockIdx.x == 0 && warp == 0;
-  if (p.n_seq <= 32) {
+  if (p.n_seq == 1) {
+    cp = plan_one<WEIGHTS>(p, writes);
+  } else if (p.n_seq <= 32) {
     cp = plan_warp<WEIGHTS, 1>(p, threadIdx.x & 31, writes);
   } else if (p.n_seq <= 64) {
     cp = plan_warp<WEIGHTS, 2>(p, threadIdx.x & 31, writes);
