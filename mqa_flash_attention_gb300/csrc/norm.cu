@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) rmsnorm_fp8_kernel(
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[i][e] = 0.f;
     if (vec < vecs) {
-      const float4 a = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * vec);
-      const float4 b = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * vec + 1);
+      const float4 a = reinterpret_cast<const float4 *>(p.weight)[2 * vec];
+      const float4 b = reinterpret_cast<const float4 *>(p.weight)[2 * vec + 1];
       w[i][0] = a.x; w[i][1] = a.y; w[i][2] = a.z; w[i][3] = a.w;
       w[i][4] = b.x; w[i][5] = b.y; w[i][6] = b.z; w[i][7] = b.w;
     }
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) rmsnorm_fp8_kernel(
       }
       if (p.codes != nullptr) {
         const bool some = m[i] > kLeastMax && rs > 0.f;  // (rs is 0 when the sum of squares overflowed)
-        const float inv = __fdividef(448.f, m[i]);
+        const float inv = __fdiv_rn(448.f, m[i]);  // exactly rounded: an error here moves codes that lie near a tie
         uint32_t out[2] = {0u, 0u};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
