@@ -567,6 +567,9 @@ typedef struct {
  * The 128-row tiles of all sequences together are shared out evenly among the
  * SMs, whatever the lengths; a sequence whose tiles fall to several SMs is
  * joined by its log-sum-exps.  The same call gives the same bits every time.
+ * A sequence's table may name 2^30 rows at most (the window's and all
+ * compressed ones together).  Where K and V are the same pool in both segments
+ * (and, in E4M3, the same scales), each row is read once for both products.
  */
 typedef struct {
   const void *q;
@@ -686,7 +689,7 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
  * residual_out.  A group whose m is 0 gets scale 0 and codes 0; one whose m
  * is below 2^-100 may.  The sum of a row's squares is an fp32 number: a row
  * where it overflows (values near 2^60) has y = 0.
- *   n, width    rows; values per row, a multiple of 8, 8 .. 32768.
+ *   n, width    rows, 0 .. 2^30; values per row, a multiple of 8, 8 .. 32768.
  *   x_fp32      0: x, residual and residual_out are fp16; 1: fp32.  Finite values.
  *   x, residual, residual_out  [n][width] at their strides (multiples of 16
  *               bytes), 16-byte aligned.  residual may be NULL (h = x);
@@ -744,7 +747,11 @@ ds4a_status ds4a_device_status(ds4a_stream_t stream, int clear);
  * 0x28 draining copies, 0x29 extra-row scores ready, 0x2A extra-row buffer or
  * Q box free, 0x2B row statistics ready, 0x2C row statistics read.  Indexer
  * scores: 0x40 q free, 0x41 k stage free, 0x42 q loaded, 0x43 accumulator
- * free, 0x44 k stage loaded, 0x45 accumulator complete, 0x46 draining.
+ * free, 0x44 k stage loaded, 0x45 accumulator complete, 0x46 draining.  Paged
+ * attention: 0x60 Q buffer free, 0x61 K/V stage free, 0x62 Q loaded, 0x63 S
+ * buffer free, 0x64 K/V stage loaded, 0x65 P written, 0x66 O read, 0x67 S
+ * computed, 0x68 P consumed, 0x69 O complete, 0x6A draining copies, 0x6B E4M3
+ * codes loaded, 0x6C row list written, 0x6D row list read.
  * clear != 0 resets the word.
  */
 ds4a_status ds4a_device_error_word(ds4a_stream_t stream, uint32_t *word, int clear);

@@ -120,6 +120,10 @@ ds4a_status encode_comp(ds4a::PagedAttnParams &p, const ds4a_paged_rows *r, bool
   if (p.run_rows == 0) return DS4A_OK;
   p.run_shift = log2_of(p.run_rows);
   const bool e4m3 = r->k_scale != nullptr;
+  // Rows further apart (one layer of a pool that interleaves several): a run's
+  // block would bring more of other rows than of these.
+  const int64_t row = e4m3 ? DS4A_HEAD_DIM : DS4A_ROW_BYTES;
+  if (r->row_stride <= 2 * row) p.run_bytes = (uint32_t)((p.run_rows - 1) * r->row_stride + row);
   ds4a_status st = ds4a::host_encode_pages(&p.tm_k, r->k, e4m3, r->page_rows, r->n_pages, r->row_stride,
                                            r->page_stride, p.run_rows);
   if (st == DS4A_OK && need_v)
@@ -179,7 +183,7 @@ ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, cons
     most += r == &X->raw && rows > shape->window ? shape->window : rows;
   }
   const int64_t tiles = n_seq * tiles_of(most);
-  if (tiles > (1 << 29)) return DS4A_ERR_INVALID_ARG;
+  if (most > kMostRows || tiles > (1 << 29)) return DS4A_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256) ||
       workspace_bytes < ds4a_attn_decode_paged_workspace_size(n_seq))
     return DS4A_ERR_WORKSPACE;
@@ -358,7 +362,9 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
   const ds4a_status st = ds4a::host_device(&d);
   if (st != DS4A_OK) return st;
   ds4a::AppendParams p;
-  p.rows = seg_of(rows);
+  ds4a_paged_rows pool = *rows;
+  pool.max_pages = 0;
+  p.rows = seg_of(&pool);
   p.k = static_cast<const uint8_t *>(k);
   p.v = static_cast<const uint8_t *>(one ? k : v);
   p.new_stride = new_row_stride;
@@ -369,7 +375,7 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
 
 ds4a_status ds4a_rmsnorm_fp8(const ds4a_norm *N, ds4a_stream_t stream) {
   if (N == nullptr) return DS4A_ERR_INVALID_ARG;
-  if (N->n < 0 || N->width < 8 || N->width > 32768 || N->width % 8 != 0) return DS4A_ERR_INVALID_ARG;
+  if (N->n < 0 || N->n > kMostRows || N->width < 8 || N->width > 32768 || N->width % 8 != 0) return DS4A_ERR_INVALID_ARG;
   if (N->group != 0 && N->group != 32 && N->group != 64 && N->group != 128 && N->group != 256)
     return DS4A_ERR_INVALID_ARG;
   if (!(N->eps >= FLT_MIN) || !std::isfinite(N->eps)) return DS4A_ERR_INVALID_ARG;

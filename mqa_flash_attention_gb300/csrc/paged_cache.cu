@@ -31,8 +31,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_paged_kernel(const A
   const bool is_v = i >= p.n;
   const int r = (int)(is_v ? i - p.n : i);
   const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + r * p.new_stride) + 2 * lane;
-  const int slot = __ldg(p.slots + r);
-  const uint4 a = __ldg(src), b = __ldg(src + 1);
+  const int slot = p.slots[r];
+  const uint4 a = src[0], b = src[1];
   if (slot < 0) return;
   const int page = slot / p.rows.page_rows, row = slot - page * p.rows.page_rows;
   if (page >= p.rows.n_pages) return;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  const int4 g = __ldg(p.geom + b);
+  const int4 g = p.geom[b];
   const int n = min(max(g.w, 0), p.rows.max_rows);
   const int n_out = min(n, p.n_keep);
   const float *w = p.weights + b * p.weight_stride;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const Evict
   if (j < p.n_keep) {
     if (j >= plan.y) {
       kept[j] = -1;
-    } else if ((__ldg(p.stay + (long long)b * p.stay_words + (j >> 5)) >> (j & 31)) & 1u) {
+    } else if ((p.stay[(long long)b * p.stay_words + (j >> 5)] >> (j & 31)) & 1u) {
       kept[j] = j;
       if (w_out != nullptr) w_out[j] = w[j];
       if (ids_out != nullptr) ids_out[j] = ids[j];
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const Evict
   const PagedSeg &s = p.rows;
   const int32_t *table = s.table + b * s.table_stride;
   const int sp = src / s.page_rows, dp = dst / s.page_rows;
-  const int from_page = __ldg(table + sp), to_page = __ldg(table + dp);
+  const int from_page = table[sp], to_page = table[dp];
   if (lane == 0) kept[dst] = src;
   if (lane == 1 && w_out != nullptr) w_out[dst] = w[src];
   if (lane == 2 && ids_out != nullptr) ids_out[dst] = ids[src];

@@ -28,6 +28,7 @@ struct PagedAttnParams {
   // {512, page_rows, pages}, box {128, run_rows, 1}.
   CUtensorMap tm_k, tm_v;
   int run_rows, run_shift; // 8 .. 128, a power of two, and its log2; 0: no TMA loads
+  uint32_t run_bytes;      // of a run, first row to last, or 0: not worth a prefetch as one block
   PagedSeg seg[2];         // raw, compressed
   const int4 *geom;        // (q_pos, n_raw, raw_pos0, n_comp) per sequence
   int n_seq, ratio, window;

@@ -262,6 +262,49 @@ def test_decode_one_segment_only(torch, ds4a):
         check_decode(host(o), host(lse), paged.decode(shape, geom, q, r, c), [278, 131])
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("n", [2, 31, 32, 33, 64, 65, 100, 153, 512, 513])
+def test_decode_batches_of_every_plan(torch, ds4a, n, f8):
+    """Batches on both sides of each way of sharing out the tiles, with empty sequences first, between and last."""
+    rng = np.random.default_rng(60 + n)
+    comp_rows = [int(x) for x in rng.integers(0, 500 if n < 60 else 150, n)]
+    geom, q, raw, comp = case(rng, comp_rows, 4, 8, f8, True, window=16)
+    for b in {0, n // 2, n - 1} if n > 2 else {1}:
+        geom[b] = (geom[b][0], 0, 0, 0)
+    shape = shape_of(4, 16)
+    o, lse = ds4a.attn_decode_paged(shape, up(torch, np.array(geom, dtype=np.int32)), up(torch, q),
+                                    rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp), want_lse=True)
+    check_decode(host(o), host(lse), paged.decode(shape, geom, q, raw, comp), [c + 16 for c in comp_rows])
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("pad_row", [D, 4 * D])
+def test_decode_rows_of_interleaved_layers(torch, ds4a, pad_row, f8):
+    """Rows far apart (a pool that holds several layers' rows side by side), NaN between them."""
+    rng = np.random.default_rng(61)
+    comp_rows = [1500, 700, 140]
+    geom, q, raw, comp = case(rng, comp_rows, 4, 64, f8, True)
+    shape = shape_of()
+    o, lse = ds4a.attn_decode_paged(shape, up(torch, np.array(geom, dtype=np.int32)), up(torch, q),
+                                    rows_on(torch, ds4a, raw, pad_row=pad_row),
+                                    rows_on(torch, ds4a, comp, pad_row=pad_row), want_lse=True)
+    check_decode(host(o), host(lse), paged.decode(shape, geom, q, raw, comp), [c + 128 for c in comp_rows])
+
+
+@pytest.mark.parametrize("scale", [1e25, 1e33])
+def test_decode_of_one_row_is_its_value(torch, ds4a, scale):
+    """However low the row's score: a softmax over one row is 1."""
+    rng = np.random.default_rng(62)
+    seg = make(rng, 1, [1], 16)
+    q = torch.from_numpy(-np.repeat(seg["k"][seg["table"][0, 0], 0][None, None], H, 1)).cuda()
+    geom = torch.tensor([[7, 0, 0, 1]], dtype=torch.int32, device="cuda")
+    o, lse = ds4a.attn_decode_paged(shape_of(scale=scale), geom, q, None, rows_on(torch, ds4a, seg), want_lse=True)
+    want = seg["v"][seg["table"][0, 0], 0]
+    assert np.array_equal(host(o)[0], np.repeat(want[None], H, 0))
+    k = seg["k"][seg["table"][0, 0], 0].astype(np.float64)
+    assert np.abs(host(lse)[0] / (-float(np.float32(scale)) * (k * k).sum()) - 1).max() <= 516 * 2.0 ** -23  # products and sums, and eight roundings
+
+
 def test_decode_pages_past_32_bit_offsets(torch, ds4a):
     """A 5 GB pool whose used pages lie at its end, read through both tables by two sequences (shared pages)."""
     rng = np.random.default_rng(12)

@@ -99,6 +99,10 @@ def test_bad_decode_calls_are_refused(lib):
         S.ratio = shape.get("ratio", 4)
         assert lib.ds4a_attn_decode_paged(2, ctypes.byref(S), 7 * AT, ctypes.byref(X), AT, 1 << 40, None) == \
             ds4a.ERR_INVALID_ARG
+    # The window's rows and the compressed ones together: 2^30 at most.
+    most = seg(page_rows=1 << 27, n_pages=8, page_stride=1 << 37, table_stride=32, max_pages=8)
+    assert decode(lib, batch(comp=most)) == ds4a.ERR_INVALID_ARG
+    assert passes(decode(lib, batch(raw=seg(max_pages=0), comp=most)))
     assert decode(lib, X, geom=None) == ds4a.ERR_INVALID_ARG
     assert decode(lib, X, geom=AT + 4) == ds4a.ERR_INVALID_ARG
     assert decode(lib, X, ws=None) == ds4a.ERR_WORKSPACE
@@ -185,7 +189,7 @@ def test_norm_arguments_are_checked(lib):
     assert passes(norm(lib, r=5 * AT, rs=128, ro=AT, ros=128))
     assert passes(norm(lib, c=None, s=None, y=6 * AT, ys=128))
     assert passes(norm(lib, group=32, ss=8))
-    for bad in (dict(n=-1), dict(width=4), dict(width=60), dict(width=32776, xs=1 << 17, cs=32776), dict(group=16),
+    for bad in (dict(n=-1), dict(n=(1 << 30) + 1), dict(width=4), dict(width=60), dict(width=32776, xs=1 << 17, cs=32776), dict(group=16),
                 dict(group=-32), dict(eps=0.0), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(eps=1e-40),
                 dict(x=None), dict(x=AT + 8), dict(xs=120), dict(xs=136), dict(f32=1), dict(w=None), dict(w=AT + 4),
                 dict(r=5 * AT, rs=128), dict(ro=5 * AT, ros=128), dict(r=5 * AT, rs=128, ro=5 * AT + 16, ros=128),
