@@ -461,9 +461,11 @@ __device__ __forceinline__ void prefetch_tables(const PagedAttnParams &p) {
 
 // ------------------------------------------------------------------ loaders
 
-// Lists run ahead of the copies: while the rows of tiles g + 1 and g are
-// issued, the page ids of tile g + 3 and the scales of tile g + 2 are on their
-// way in registers, so neither latency stands between tiles.
+// Lists run ahead of the copies: while the rows of tile g are issued, its scales
+// and the page ids of tile g + 1 are on their way in registers, so neither
+// latency stands between tiles.  One loop holds the code of every step once, in
+// the order in which the first tile runs through it: the code is cold when a CTA
+// starts, and each further copy of a step in its way cost some 1,000 cycles.
 template <bool FP8, bool WEIGHTS, bool SHARED>
 __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPlan &cp, uint32_t sbase, PMisc &ms,
                                           int ltid) {
@@ -496,6 +498,10 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
   float b_ks[kMine], b_vs[kMine];
   int b_seq = 0, b_flags = 0, b_base = 0, b_end = 0;
 
+  // A field of segment sg: a choice of two constants.  (Indexed loads of the
+  // parameters made the list of an E4M3 tile, two rows a thread, take 3,000 cycles
+  // and not 1,100: weights of 16 sequences 32 us and not 26.)
+  auto of = [&](int sg, auto field) { return sg != 0 ? p.seg[1].*field : p.seg[0].*field; };
   auto fetch_pages = [&]() {
     a_seq = w.b;
     a_flags = w.flags();
@@ -508,12 +514,12 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
       a_row[u] = -1;
       a_page[u] = -1;
       if (r < kTile && x < a_end) {
-        const int sg = x < w.rows.nc ? 1 : 0;
-        const PagedSeg &s = p.seg[sg];
+        const int sg = WEIGHTS || x < w.rows.nc ? 1 : 0;
         const int row = sg == 0 ? w.rows.raw_lo + x - w.rows.nc : x;
-        const int pi = s.page_shift >= 0 ? row >> s.page_shift : row / s.page_rows;
-        a_page[u] = s.table[w.b * s.table_stride + pi];
-        a_row[u] = 2 * (row - pi * s.page_rows) + sg;
+        const int shift = of(sg, &PagedSeg::page_shift), per = of(sg, &PagedSeg::page_rows);
+        const int pi = shift >= 0 ? row >> shift : row / per;
+        a_page[u] = of(sg, &PagedSeg::table)[w.b * of(sg, &PagedSeg::table_stride) + pi];
+        a_row[u] = 2 * (row - pi * per) + sg;
       }
     }
     w.next(p);
@@ -531,17 +537,18 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
       b_slot[u] = a_row[u] >> 1;
       b_ks[u] = 0.f;
       b_vs[u] = 1.f;
-      const PagedSeg &s = p.seg[a_row[u] & 1];
-      if (a_row[u] >= 0 && (unsigned)a_page[u] < (unsigned)s.n_pages) {
+      const int sg = WEIGHTS ? 1 : a_row[u] & 1;
+      if (a_row[u] >= 0 && (unsigned)a_page[u] < (unsigned)of(sg, &PagedSeg::n_pages)) {
         const int slot = a_row[u] >> 1;
-        b_at[u] = reinterpret_cast<unsigned long long>(s.k + a_page[u] * s.page_stride + slot * s.row_stride) |
-                  (a_row[u] & 1);
+        b_at[u] = reinterpret_cast<unsigned long long>(of(sg, &PagedSeg::k) + a_page[u] * of(sg, &PagedSeg::page_stride) +
+                                                       slot * of(sg, &PagedSeg::row_stride)) |
+                  sg;
         if (SHARED && ahead && a_full && p.run_bytes > 0 && ((gtid + u * kGroup) & (p.run_rows - 1)) == 0)
           l2_prefetch(reinterpret_cast<const void *>(b_at[u] & ~15ull), p.run_bytes);
         if (FP8) {
-          const long long sr = (long long)a_page[u] * s.page_rows + slot;
-          b_ks[u] = s.k_scale[sr];
-          if (!WEIGHTS) b_vs[u] = s.v_scale[sr];
+          const long long sr = (long long)a_page[u] * of(sg, &PagedSeg::page_rows) + slot;
+          b_ks[u] = of(sg, &PagedSeg::k_scale)[sr];
+          if (!WEIGHTS) b_vs[u] = of(sg, &PagedSeg::v_scale)[sr];
         }
       }
     }
@@ -669,35 +676,28 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
     ++n_item;
   };
 
-  if (nt > 0) {
-    fetch_pages();
-    fetch_scales(false);
-    bool tma = store_list(0), tma_next = false;
-    for (int part = 0; part < 4 && ok; ++part) ok = emit(0, part, tma);
-    finish_list(0);
-    if (nt > 1) fetch_pages();
-    if (nt > 1) fetch_scales(true);
-    if (nt > 2) fetch_pages();
-    for (int g = 0; g < nt; ++g) {
-      if (!WEIGHTS && !SHARED && g + 1 == nt) {
-        __syncwarp();
-        ok = !bar_red_or(2, kGroup, !ok);
-      }
-      if (g + 1 < nt) {
-        tma_next = store_list(g + 1);
-        if (b_flags & kFirst) load_q(b_seq);
-        if (SHARED) finish_list(g + 1);  // (the next rows are prefetched before these copies wait for their stages)
-        if (SHARED && g + 2 < nt) fetch_scales(true);
-        if (SHARED && g + 3 < nt) fetch_pages();
-        for (int part = 0; part < 4 && ok; ++part) ok = emit(g + 1, part, tma_next);
-        if (!SHARED) finish_list(g + 1);
-        if (!SHARED && g + 2 < nt) fetch_scales(true);
-        if (!SHARED && g + 3 < nt) fetch_pages();
-      }
-      if (!WEIGHTS && !SHARED)
-        for (int part = 4; part < 8 && ok; ++part) ok = emit(g, part, tma);
-      tma = tma_next;
+  if (nt > 0) fetch_pages();
+  bool tma = false, tma_v;  // whether TMA loads tile g, and tile g - 1
+  for (int g = 0; nt > 0 && (g < nt || (!WEIGHTS && !SHARED && g == nt)); ++g) {
+    tma_v = tma;
+    if (g < nt) {
+      // The first tile's rows before the prefetch of the second's: every SM wants
+      // its first tile at the same time.
+      if (SHARED && g == 1)
+        mbar_wait(smem_u32(FP8 ? &ms.code_full[kStages - 1] : &ms.kv_full[kStages - 1]), 0, abrt, p.timeout_ns, p.err,
+                  FP8 ? PSITE_CODE_FULL : PSITE_KV_FULL);
+      fetch_scales(g > 0);
+      if (g + 1 < nt) fetch_pages();
+      tma = store_list(g);
+      if (g > 0 && (b_flags & kFirst)) load_q(b_seq);
+      for (int part = 0; part < 4 && ok; ++part) ok = emit(g, part, tma);
+      finish_list(g);
+    } else {
+      __syncwarp();
+      ok = !bar_red_or(2, kGroup, !ok);
     }
+    if (!WEIGHTS && !SHARED && g > 0)
+      for (int part = 4; part < 8 && ok; ++part) ok = emit(g - 1, part, tma_v);
   }
   // No copy may still be landing at exit.  (When every wait succeeded the MMA
   // thread has seen all stages land.)
@@ -746,7 +746,6 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams &p, const Cta
       sts_v4(drow + ((col ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
       sts_v4(drow + (((col + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
     }
-    fence_proxy_async_smem();
     mbar_arrive(smem_u32(&ms.kv_full[ring.st]));
     ring.advance();
   }
@@ -781,9 +780,9 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const C
   auto commit = [&](uint64_t &bar) {
     if (elect_lane()) umma_commit(smem_u32(&bar));
   };
-  // Gathered rows (cp.async) are generic-proxy writes: the fence makes the
-  // landed stage visible to the tensor core.  TMA writes, and the widened
-  // rows (fenced by the converters), need none.  No tcgen05 fence here: it is
+  // Gathered rows (cp.async) and widened ones are generic-proxy writes: the fence
+  // makes the landed stage visible to the tensor core (here one warp's, which took
+  // 2% less of E4M3 decodes than one by every converter).  TMA writes need none.  No tcgen05 fence here: it is
   // for TMEM that other threads read or wrote.  fp16 stages are waited for two
   // at a time: behind the eight MMAs of one the warp would stand still until
   // they are done.  (E4M3 stages come one by one from the converters.)
@@ -792,7 +791,7 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const C
 #pragma unroll
     for (int u = 0; u < kStep; ++u)
       if (!wait(ms.kv_full[ring.st + u], ring.ph, PSITE_KV_FULL)) return false;
-    if (!FP8 && ms.gathered[g % kLists]) fence_proxy_async_smem();
+    if (FP8 || ms.gathered[g % kLists]) fence_proxy_async_smem();
     return true;
   };
   auto qk = [&](int g, bool first, bool last) -> bool {
@@ -801,7 +800,7 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const C
       ++q_item;
     }
     const uint32_t sb = g & 1;
-    if (!wait(ms.list_full[g % kLists], (g / kLists) & 1, PSITE_LIST_FULL)) return false;
+    if (!FP8 && !wait(ms.list_full[g % kLists], (g / kLists) & 1, PSITE_LIST_FULL)) return false;
     if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, PSITE_S_EMPTY)) return false;
     tc_fence_after();
     const uint32_t d_s = tmem + kTmemS + 64 * sb;
