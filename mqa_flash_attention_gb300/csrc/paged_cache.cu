@@ -138,10 +138,8 @@ __device__ __forceinline__ unsigned taken(unsigned eq, unsigned seen, unsigned l
   return seen >= left ? 0u : min(eq, left - seen);
 }
 
-template <bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys[];
-  __shared__ typename std::conditional<CLUSTER, ClusterShared, SelShared>::type sh;
+template <bool CLUSTER, typename Shared>
+__device__ __forceinline__ void select_rows(const EvictParams &p, uint32_t *keys, Shared &sh) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -368,43 +366,30 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 // ------------------------------------------------------------------ eviction: moving the rows
 // One warp per move: the K and the V row (and the scales of an E4M3 pool) of
 // the h-th kept row above n' into the h-th freed slot below it.  Sources and
-// destinations never meet, so the moves need no order.  The blocks of a
-// sequence first share out its slots: kept, weights and ids of the rows that
-// stay.  Bound by memory: two rows read and two written per move.
+// destinations never meet, so the moves need no order.  One thread per slot
+// below n_keep: kept, weights and ids of the row that stays in it.
 
-constexpr int kMoveWarps = 8;
-constexpr int kMoveSlots = 32 * kMoveWarps;  // slots of a block, one per thread
-
-__global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const EvictParams p, int blocks_per_seq) {
-  const int b = blockIdx.x / blocks_per_seq, part = blockIdx.x - b * blocks_per_seq, lane = threadIdx.x & 31;
-  const int h = part * kMoveWarps + (threadIdx.x >> 5);
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int2 plan = p.n_moves[b];  // (moves, n')
+__device__ __forceinline__ void keep_slot(const EvictParams &p, int b, int j, int n_out) {
   int32_t *kept = p.kept + b * p.kept_stride;
-  const float *w = p.weights + b * p.weight_stride;
-  float *w_out = p.weights_out != nullptr ? p.weights_out + b * p.weight_out_stride : nullptr;
-  const int32_t *ids = p.ids != nullptr ? p.ids + b * p.id_stride : nullptr;
-  int32_t *ids_out = p.ids_out != nullptr ? p.ids_out + b * p.id_out_stride : nullptr;
-  const int j = part * kMoveSlots + threadIdx.x;
-  if (j < p.n_keep) {
-    if (j >= plan.y) {
-      kept[j] = -1;
-    } else if ((p.stay[(long long)b * p.stay_words + (j >> 5)] >> (j & 31)) & 1u) {
-      kept[j] = j;
-      if (w_out != nullptr) w_out[j] = w[j];
-      if (ids_out != nullptr) ids_out[j] = ids[j];
-    }
+  if (j >= n_out) {
+    kept[j] = -1;
+  } else if ((p.stay[(long long)b * p.stay_words + (j >> 5)] >> (j & 31)) & 1u) {
+    kept[j] = j;
+    if (p.weights_out != nullptr) p.weights_out[b * p.weight_out_stride + j] = p.weights[b * p.weight_stride + j];
+    if (p.ids_out != nullptr) p.ids_out[b * p.id_out_stride + j] = p.ids[b * p.id_stride + j];
   }
-  if (h >= plan.x) return;
+}
+
+__device__ __forceinline__ void move_row(const EvictParams &p, int b, int h, int lane) {
   const int src = p.from[(long long)b * p.n_keep + h], dst = p.to[(long long)b * p.n_keep + h];
   const PagedSeg &s = p.rows;
   const int32_t *table = s.table + b * s.table_stride;
   const int sp = src / s.page_rows, dp = dst / s.page_rows;
   const int from_page = table[sp], to_page = table[dp];
-  if (lane == 0) kept[dst] = src;
-  if (lane == 1 && w_out != nullptr) w_out[dst] = w[src];
-  if (lane == 2 && ids_out != nullptr) ids_out[dst] = ids[src];
+  if (lane == 0) p.kept[b * p.kept_stride + dst] = src;
+  if (lane == 1 && p.weights_out != nullptr)
+    p.weights_out[b * p.weight_out_stride + dst] = p.weights[b * p.weight_stride + src];
+  if (lane == 2 && p.ids_out != nullptr) p.ids_out[b * p.id_out_stride + dst] = p.ids[b * p.id_stride + src];
   if ((unsigned)from_page >= (unsigned)s.n_pages || (unsigned)to_page >= (unsigned)s.n_pages) return;
   const int ss = src - sp * s.page_rows, ds = dst - dp * s.page_rows;
   const long long so = from_page * s.page_stride + ss * s.row_stride, d = to_page * s.page_stride + ds * s.row_stride;
@@ -436,6 +421,35 @@ __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const Evict
   }
 }
 
+// With few rows to move (p.move_here) the CTA that chose them moves them too.
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ typename std::conditional<CLUSTER, ClusterShared, SelShared>::type sh;
+  select_rows<CLUSTER>(p, keys, sh);
+  if (CLUSTER || !p.move_here) return;
+  const int b = blockIdx.x;
+  __syncthreads();  // its lists are written
+  const int2 plan = p.n_moves[b];
+  for (int h = threadIdx.x >> 5; h < plan.x; h += kSelWarps) move_row(p, b, h, threadIdx.x & 31);
+  for (int j = threadIdx.x; j < p.n_keep; j += kSelThreads) keep_slot(p, b, j, plan.y);
+}
+
+// Bound by memory: two rows read and two written per move.  The blocks of a
+// sequence share out its slots, too.
+constexpr int kMoveWarps = 8;
+constexpr int kMoveSlots = 32 * kMoveWarps;  // slots of a block, one per thread
+
+__global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const EvictParams p, int blocks_per_seq) {
+  const int b = blockIdx.x / blocks_per_seq, part = blockIdx.x - b * blocks_per_seq;
+  const int h = part * kMoveWarps + (threadIdx.x >> 5), j = part * kMoveSlots + threadIdx.x;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int2 plan = p.n_moves[b];  // (moves, n')
+  if (j < p.n_keep) keep_slot(p, b, j, plan.y);
+  if (h < plan.x) move_row(p, b, h, threadIdx.x & 31);
+}
+
 }  // namespace
 
 int evict_cluster(int max_rows) { return max_rows <= 8192 ? 1 : max_rows <= 65536 ? 8 : 16; }
@@ -445,8 +459,18 @@ int evict_cached_keys(int max_rows, int cluster) {
   return per <= kMaxCachedKeys ? (int)per : 0;
 }
 
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
+// With up to so many rows that a table can name beyond n_keep (as many can have
+// to move; a page of 64, say) the CTA of a sequence moves the rows itself.  64
+// sequences that lose 1, 16 or 64 rows of 1,088: 7.5, 8.2 and 11.4 us, with a
+// second kernel 9.5, 10.5 and 11.9; one sequence that loses 64: 11.2 us, and 9.4;
+// 64 sequences with 128 rows beyond: 15.6, and 13.3.
+constexpr int kMovesHere = 64, kSlotsHere = 8192;
+
+cudaError_t launch_evict(EvictParams p, cudaStream_t s) {
   const int C = evict_cluster(p.rows.max_rows);
+  const int spare = p.rows.max_rows - p.n_keep;  // kept rows above n' are at most this many
+  const int moves = spare < 0 ? 0 : spare < p.n_keep ? spare : p.n_keep;
+  p.move_here = C == 1 && moves <= kMovesHere && p.n_keep <= kSlotsHere;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.n_seq * C);
   cfg.blockDim = dim3(kSelThreads);
@@ -462,9 +486,7 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
   cfg.numAttrs = C > 1 ? 2 : 1;
   const cudaError_t e = C > 1 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p)
                               : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
-  if (e != cudaSuccess) return e;
-  const int spare = p.rows.max_rows - p.n_keep;  // kept rows above n' are at most this many
-  const int moves = spare < 0 ? 0 : spare < p.n_keep ? spare : p.n_keep;
+  if (e != cudaSuccess || p.move_here) return e;
   const int move_blocks = (moves + kMoveWarps - 1) / kMoveWarps, slot_blocks = (p.n_keep + kMoveSlots - 1) / kMoveSlots;
   const int blocks = move_blocks > slot_blocks ? move_blocks : slot_blocks;
   cfg.gridDim = dim3(p.n_seq * blocks);

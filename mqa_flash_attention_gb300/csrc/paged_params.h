@@ -75,10 +75,11 @@ struct EvictParams {
   int stay_words;          // ceil(n_keep / 32)
   int32_t *from, *to;      // workspace: [n_seq][n_keep] slots of the moved rows, and the freed slots they take
   int cached;              // keys of a CTA's rows kept in shared memory (0: recomputed from the weights)
+  int move_here;           // set by launch_evict: the selection moves the rows, too
 };
 int evict_cluster(int max_rows);
 int evict_cached_keys(int max_rows, int cluster);
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
+cudaError_t launch_evict(EvictParams p, cudaStream_t s);
 cudaError_t prepare_cache_kernels();
 
 struct AppendParams {
