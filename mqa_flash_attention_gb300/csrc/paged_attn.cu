@@ -19,7 +19,7 @@
 // are numbered through instead and CTA i takes ceil(total / CTAs) of them in a
 // row, several items.  Either way the load is even whatever the lengths; one
 // item per CTA costs one drain of the pipeline and fewer partial results (64
-// sequences of 8 to 21 tiles: 36 us in the slowest CTA with items cut at even
+// sequences of 5 to 17 tiles: 36 us in the slowest CTA with items cut at even
 // tile numbers, 30 us so).  An item that holds the whole sequence
 // writes its output; otherwise it leaves its normalised output (fp32) and
 // (m, l) in a slot of the workspace, slot CTA, or CTA + sequence with several
@@ -45,8 +45,9 @@
 // each tile j, so the next scores are computed while the softmax works.  Where K
 // and V are the same rows, a tile is loaded once: its four parts stay in the four
 // stages from QK^T to PV, and the next tile, whose rows are in L2 by then, follows
-// as each PV frees its stage (64 sequences of 8 to 21 E4M3 tiles: 46 us, 52 us
-// with the rows loaded twice).  With E4M3 rows, warps 8, 13 and 14 load codes into
+// as each PV frees its stage (24 sequences of 17 to 65 E4M3 tiles: 46 us, 52 us
+// with the rows loaded twice).  Half tiles, two of them in the ring, took 49 us: a
+// product of 64 rows costs the tensor core as much as one of 128.  With E4M3 rows, warps 8, 13 and 14 load codes into
 // the upper half of a stage and warps 9-12 widen them in place, exactly.
 //
 // A stage's fp16 layout is rows in groups of 8: [16 groups][2 blocks of 64
@@ -60,6 +61,15 @@
 // exponent: p'_j = 2^(s_j + log2 c_j - m') with m' the running maximum of that
 // sum, so the fp16 p' that feeds the MMA has full precision whatever the size
 // of the scales; the sum of weights adds p'_j / c_j.
+//
+// What bounds it.  One sequence of 262,144 fp16 rows: HBM (537 MB in 95 us with the
+// merge, 83% of the measured copy rate).  Batches with K = V: the chain of a tile,
+// some 7,600 cycles from one tile's first load to the next's: 1,100 until the first
+// part is there and 2,200 for 128 KB at the 64 bytes a clock of an SM's port to
+// L2, the last part's QK^T 630, softmax 1,800, PV 430 to the first freed stage; 64
+// sequences take 41 us, 24 of E4M3 rows 44 us, where widening (read once, written
+// twice as wide) and the products' operands share the bandwidth of shared memory.
+// Weights of 16 sequences of E4M3 rows, 88 MB: 26 us, bound by the same.
 #include "attn_params.h"
 #include "internal.h"
 #include "paged_params.h"
