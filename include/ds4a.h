@@ -554,7 +554,7 @@ typedef struct {
  * ds4a_attn_decode on its own layout and rows (rows of absent pages left
  * out).  A sequence that sees no row gets o = 0 and lse = -inf.
  *   shape       ratio, window and scale shared by the batch (other fields are
- *               ignored).
+ *               ignored); scale below 2.3e38 in size.
  *   seq_geom    device int32 [n_seq][4], 16-byte aligned: per sequence
  *               (q_pos, n_raw, raw_pos0, n_comp); the row counts are clamped
  *               to the rows the tables can name.  Read on the device.
@@ -622,8 +622,9 @@ ds4a_status ds4a_attn_weights_paged(int32_t n_seq, const ds4a_layout *shape, con
  *   rows' order in the cache carries no meaning (their ids do).
  *   K and V rows and, in an E4M3 pool, their scales are moved in place.  A
  *   move from or to an absent page copies no row.  Slots n' .. n-1 keep what
- *   they held.  The pages of these sequences must be theirs alone: each page
- *   in one table, once.
+ *   they held, and their weights too: the caller sets the weight (0, say) that a
+ *   row appended there starts from.  The pages of these sequences must be theirs
+ *   alone: each page in one table, once.
  *   rows        the compressed segment (k and v are written).
  *   weights     fp32 [n_seq][max_pages * page_rows] at weight_stride bytes.
  *   ids         int32, same shape, at id_stride bytes, or NULL.

@@ -19,6 +19,7 @@ using ds4a::PagedSeg;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int64_t kMostBytes = 1LL << 39;  // of any stride
 constexpr int32_t kMostRows = 1 << 30;     // rows of a sequence
+constexpr float kLog2e = 1.4426950408889634f;
 
 cudaStream_t as_cuda(ds4a_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -98,7 +99,7 @@ PagedSeg no_rows() {
 }
 
 ds4a_status check_batch(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom) {
-  if (shape->window < 1 || !std::isfinite(shape->scale) || shape->ratio < 1) return DS4A_ERR_INVALID_ARG;
+  if (shape->window < 1 || !std::isfinite(shape->scale * kLog2e) || shape->ratio < 1) return DS4A_ERR_INVALID_ARG;
   if (seq_geom == nullptr || !aligned(seq_geom, 16)) return DS4A_ERR_INVALID_ARG;
   return n_seq > (1 << 20) ? DS4A_ERR_INVALID_ARG : DS4A_OK;
 }
@@ -134,9 +135,7 @@ ds4a_status encode_comp(ds4a::PagedAttnParams &p, const ds4a_paged_rows *r, bool
 
 int64_t tiles_of(int64_t rows) { return (rows + 127) / 128; }
 
-// CTAs a decode step of n_seq sequences may use.
-int decode_ctas(int sm_count) { return sm_count; }
-
+// A slot per CTA and one more per sequence, and the plan of the merge.
 size_t decode_workspace(int32_t n_seq, int ctas) {
   const size_t slots = (size_t)n_seq + ctas;
   return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(float) + sizeof(float2)) + (size_t)n_seq * sizeof(int2);
@@ -156,7 +155,7 @@ extern "C" {
 
 size_t ds4a_attn_decode_paged_workspace_size(int32_t n_seq) {
   if (n_seq <= 0) return 0;
-  return decode_workspace(n_seq, decode_ctas(device_sms()));
+  return decode_workspace(n_seq, device_sms());
 }
 
 ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, const int32_t *seq_geom,
@@ -202,11 +201,11 @@ ds4a_status ds4a_attn_decode_paged(int32_t n_seq, const ds4a_layout *shape, cons
   p.n_seq = n_seq;
   p.ratio = shape->ratio;
   p.window = shape->window;
-  p.scale_log2 = shape->scale * 1.4426950408889634f;
+  p.scale_log2 = shape->scale * kLog2e;
   p.o = static_cast<__half *>(X->o);
   p.o_stride = X->o_seq_stride / 2;
   p.lse = X->lse;
-  const int ctas = decode_ctas(d.sm_count);
+  const int ctas = d.sm_count;
   const size_t slots = (size_t)n_seq + ctas;
   p.ws_o = static_cast<float *>(workspace);
   p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + slots * DS4A_HEADS * DS4A_HEAD_DIM);
@@ -258,7 +257,7 @@ ds4a_status ds4a_attn_weights_paged(int32_t n_seq, const ds4a_layout *shape, con
   p.n_seq = n_seq;
   p.ratio = shape->ratio;
   p.window = shape->window;
-  p.scale_log2 = shape->scale * 1.4426950408889634f;
+  p.scale_log2 = shape->scale * kLog2e;
   p.lse_in = X->lse;
   p.acc_in = weights;
   p.acc_in_stride = weights != nullptr ? weight_stride / 4 : 0;

@@ -94,7 +94,7 @@ def test_bad_batches_are_refused(lib, bad):
 def test_bad_decode_calls_are_refused(lib):
     X = batch()
     assert decode(lib, X, n=-1) == ds4a.ERR_INVALID_ARG
-    for shape in (dict(window=0), dict(ratio=0), dict(scale=math.inf), dict(scale=math.nan)):
+    for shape in (dict(window=0), dict(ratio=0), dict(scale=math.inf), dict(scale=math.nan), dict(scale=3e38)):
         S = ds4a.make_layout(dict(SHAPE, **shape))
         S.ratio = shape.get("ratio", 4)
         assert lib.ds4a_attn_decode_paged(2, ctypes.byref(S), 7 * AT, ctypes.byref(X), AT, 1 << 40, None) == \
