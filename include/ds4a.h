@@ -668,6 +668,9 @@ ds4a_status ds4a_evict_paged(int32_t n_seq, const ds4a_layout *shape, const int3
  * ds4a_append_paged - writes new K/V rows into a pool, quantising them (the
  * format of ds4a_quantize_kv_fp8, bit for bit) when it is an E4M3 pool.
  *   rows        the pool (table, table_stride and max_pages are ignored).
+ *               An E4M3 pool whose k and v are the same may have one scale array
+ *               or two (each gets the row's scale); one whose k and v differ has
+ *               two, which must not overlap.
  *   k, v        fp16 [n][512] at new_row_stride bytes.  For a pool whose k and
  *               v are the same, v may be NULL; if given it is ignored.
  *   slots       device int32 [n], 4-byte aligned: row i goes to slot

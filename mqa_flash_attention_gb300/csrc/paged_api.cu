@@ -353,6 +353,11 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
   if (slots == nullptr || !aligned(slots, 4)) return DS4A_ERR_INVALID_ARG;
   const int64_t row = rows->k_scale != nullptr ? DS4A_HEAD_DIM : DS4A_ROW_BYTES;
   const int64_t page = (int64_t)(rows->page_rows - 1) * rows->row_stride + row;
+  // A row's K and V have a scale each, unless they are one row.
+  const int64_t scales = 4LL * rows->page_rows;
+  const Span ks = span(rows->k_scale, rows->n_pages, scales, scales);
+  const Span vs = span(rows->v_scale, rows->n_pages, scales, scales);
+  if (meet(ks, vs) && !(one && rows->k_scale == rows->v_scale)) return DS4A_ERR_INVALID_ARG;
   for (const void *pool : {rows->k, rows->v})
     for (const void *in : {k, one ? k : v})
       if (meet(span(pool, rows->n_pages, rows->page_stride, page), span(in, n, new_row_stride, DS4A_ROW_BYTES)))

@@ -67,9 +67,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_paged_kernel(const A
     }
   }
   reinterpret_cast<uint4 *>(dst)[lane] = make_uint4(out[0], out[1], out[2], out[3]);
-  if (lane == 0)
-    const_cast<float *>(is_v ? p.rows.v_scale : p.rows.k_scale)[(long long)page * p.rows.page_rows + row] =
-        amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
+  // Rows that serve as K and V may have a scale array for each: both get this row's.
+  const float *scales = is_v || (lane == 1 && pools == 1) ? p.rows.v_scale : p.rows.k_scale;
+  if (lane <= (pools == 1 && p.rows.v_scale != p.rows.k_scale))
+    const_cast<float *>(scales)[(long long)page * p.rows.page_rows + row] = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
 }
 
 // ------------------------------------------------------------------ eviction: choosing the rows

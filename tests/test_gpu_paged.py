@@ -601,6 +601,33 @@ def test_append_matches_the_oracle(torch, ds4a, f8, shared, n, page, pages):
             assert np.array_equal(host(getattr(dev, name + "_scale")), seg[name + "_scale"])
 
 
+def test_append_to_one_row_pool_with_two_scale_arrays(torch, ds4a):
+    """K = V rows with a scale array each: both get the new row's scale, and a decode that reads them sees it."""
+    rng = np.random.default_rng(57)
+    page, pages = 4, 3
+    seg = make(rng, 1, [page * pages], page, True, True)
+    seg["v_scale"] = seg["k_scale"] * np.float32(3)
+    k = up(torch, seg["k"])
+    dev = ds4a.PagedRows(k, k, up(torch, seg["table"]), k_scale=up(torch, seg["k_scale"]),
+                         v_scale=up(torch, seg["v_scale"]))
+    new = (5 * rng.standard_normal((5, D))).astype(np.float16)
+    new[2] = 0
+    slots = np.array([0, 7, 11, -1, 4])
+    ds4a.append_paged(dev, up(torch, new), None, up(torch, slots.astype(np.int32)))
+    codes, scale = fp8.quantize_rows(new)
+    for i, s in enumerate(slots):
+        if s >= 0:
+            at = (s // page, s % page)
+            seg["k"][at], seg["k_scale"][at], seg["v_scale"][at] = codes[i], scale[i], scale[i]
+    for name in ("k", "k_scale", "v_scale"):
+        assert np.array_equal(host(getattr(dev, name)), seg[name]), name
+    geom, q = [(4 * 12, 0, 0, 12)], rng.standard_normal((1, H, D)).astype(np.float16)
+    seg["v"] = seg["k"]
+    o, lse = ds4a.attn_decode_paged(shape_of(), up(torch, np.array(geom, dtype=np.int32)), up(torch, q), None, dev,
+                                    want_lse=True)
+    check_decode(host(o), host(lse), paged.decode(shape_of(), geom, q, None, seg), [12])
+
+
 # ------------------------------------------------------------------ norm
 
 @pytest.mark.parametrize("f32", [False, True])

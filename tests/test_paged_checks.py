@@ -176,6 +176,19 @@ def test_append_arguments_are_checked(lib):
     assert append(lib, n=0) == ds4a.OK
 
 
+@needs_no_gpu
+def test_append_refuses_one_scale_for_two_rows(lib):
+    """K and V rows apart need a scale array each (4 * 16 scales a page, 8 pages: 512 bytes)."""
+    f8 = dict(row_stride=512, page_stride=8192)
+    assert passes(append(lib, seg(k_scale=11 * AT, v_scale=12 * AT, **f8)))
+    assert passes(append(lib, seg(k_scale=11 * AT, v_scale=11 * AT + 512, **f8)))
+    assert passes(append(lib, seg(v=AT, k_scale=11 * AT, v_scale=11 * AT, **f8), v=None))
+    assert passes(append(lib, seg(v=AT, k_scale=11 * AT, v_scale=12 * AT, **f8), v=None))
+    for bad in (seg(k_scale=11 * AT, v_scale=11 * AT, **f8), seg(k_scale=11 * AT, v_scale=11 * AT + 508, **f8),
+                seg(v=AT, k_scale=11 * AT, v_scale=11 * AT + 4, **f8)):
+        assert append(lib, bad) == ds4a.ERR_INVALID_ARG
+
+
 def norm(lib, n=3, width=64, f32=0, x=AT, xs=128, r=None, rs=0, ro=None, ros=0, w=2 * AT, eps=1e-6, group=0, c=3 * AT,
          cs=64, s=4 * AT, ss=4, y=None, ys=0):
     N = ds4a.Norm(n, width, f32, group, x, xs, r, rs, ro, ros, w, eps, c, cs, s, ss, y, ys)
