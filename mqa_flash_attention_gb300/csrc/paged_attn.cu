@@ -1101,12 +1101,14 @@ __device__ __forceinline__ void weights_role(const PagedAttnParams &p, const Cta
     const int buf = g % kLists;
     const uint32_t sb = g & 1;
     bad = bad || !mbar_wait(smem_u32(&ms.list_full[buf]), (g / kLists) & 1, abrt, p.timeout_ns, p.err, PSITE_LIST_FULL);
+    // All go on or none: without the list its flags and sequence are what an
+    // earlier kernel left here, and lead to barriers and addresses of their own.
+    if (bar_red_or(1, kComputeThreads, bad)) break;
     const int seq = ms.seq[buf], c = ms.base[buf] + r;
     const bool mine = hh == 0 && c < ms.end[buf];
     const float before = mine && p.acc_in != nullptr ? p.acc_in[seq * p.acc_in_stride + c] : 0.f;
     if (ms.flags[buf] & kFirst) {
       // 2^(s - lse log2 e); a head whose lse is -inf gave no weight to anything.
-      bar_sync_id(1, kComputeThreads);
       if (tid < kH) {
         const float v = p.lse_in[(long long)seq * kH + tid];
         ms.m_use[tid] = v == -INFINITY ? INFINITY : v * kLog2e;

@@ -6,6 +6,8 @@ tensors that do not fit."""
 import concurrent.futures as cf
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -109,6 +111,35 @@ def test_bad_decode_calls_are_refused(lib):
     assert decode(lib, X, ws=AT + 128) == ds4a.ERR_WORKSPACE
     assert decode(lib, X, nbytes=lib.ds4a_attn_decode_paged_workspace_size(2) - 1) == ds4a.ERR_WORKSPACE
     assert lib.ds4a_attn_decode_paged(2, None, 7 * AT, ctypes.byref(X), AT, 1 << 40, None) == ds4a.ERR_INVALID_ARG
+
+
+def source_of(function):
+    """The body of a __device__ function of paged_attn.cu, comments taken out."""
+    with open(os.path.join(ds4a_build.CSRC, "paged_attn.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    at = text.index(function + "(const PagedAttnParams &p")
+    start, depth = text.index("{", at), 0
+    for i in range(start, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[start:i]
+    raise AssertionError(function)
+
+
+@pytest.mark.parametrize("role", ["softmax_role", "weights_role"])
+def test_compute_roles_vote_after_a_wait(role):
+    """A wait may run out in some threads of a block and not in others.  What follows it and needs all
+    threads (a plain barrier), or depends on what was waited for (addresses), comes after a vote."""
+    voted, seen = True, set()
+    for m in re.finditer(r"mbar_wait\(|bar_red_or\(|bar_sync_id\(|p\.(?:acc_in|lse_in|acc_out|lse|ws_ml)\[", source_of(role)):
+        seen.add(m.group())
+        if m.group() == "mbar_wait(":
+            voted = False
+        elif m.group() == "bar_red_or(":
+            voted = True
+        else:
+            assert voted, f"{role}: {m.group()} after a wait without a vote"
+    assert {"mbar_wait(", "bar_red_or(", "bar_sync_id("} <= seen and voted
 
 
 def weights(lib, X=None, acc=8 * AT, acc_stride=512, decay=1.0, out=9 * AT, out_stride=512, n=2):
