@@ -1198,7 +1198,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   } else if (p.n_seq <= 64) {
     cp = plan_warp<WEIGHTS, 2>(p, threadIdx.x & 31, writes);
   } else {
-    plan_block<WEIGHTS>(p, ms, reinterpret_cast<int *>(smem + kOffKV));
+    // P's bytes: ordinary stores there are followed by ordinary stores only (the
+    // ring's and Q's by TMA, whose writes a block barrier does not order after them).
+    plan_block<WEIGHTS>(p, ms, reinterpret_cast<int *>(smem + kOffP));
     __syncthreads();
     cp = ms.plan;
   }

@@ -142,6 +142,17 @@ def test_compute_roles_vote_after_a_wait(role):
     assert {"mbar_wait(", "bar_red_or(", "bar_sync_id("} <= seen and voted
 
 
+def test_plan_counts_lie_where_no_bulk_copy_writes():
+    """Block-wide plans store counts with ordinary stores; a TMA copy into the same bytes is not ordered after
+    them by a block barrier, so they stay out of what TMA fills (Q and the K/V ring)."""
+    with open(os.path.join(ds4a_build.CSRC, "paged_attn.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    at = re.findall(r"plan_block<WEIGHTS>\(p, ms, reinterpret_cast<int \*>\(smem \+ (\w+)\)\)", text)
+    filled = set(re.findall(r"tma_load_4d\(sbase \+ (\w+)", text)) | \
+        set(re.findall(r"const uint32_t stage = sbase \+ (\w+)", text))
+    assert filled == {"kOffQ", "kOffKV"} and at == ["kOffP"]
+
+
 def weights(lib, X=None, acc=8 * AT, acc_stride=512, decay=1.0, out=9 * AT, out_stride=512, n=2):
     S = ds4a.make_layout(SHAPE)
     return elsewhere(lib.ds4a_attn_weights_paged, n, ctypes.byref(S), 7 * AT, ctypes.byref(X or batch()), acc,
