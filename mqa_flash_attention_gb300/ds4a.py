@@ -231,6 +231,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on_stream(stream):
+    """The context in which a call issued on ``stream`` makes its own tensors:
+    their fills run there, before the call's kernels, and their memory goes
+    back to that stream's pool, behind them."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -1013,7 +1022,8 @@ def attn_weights_paged(shape, seq_geom, q, comp, lse, *, weights=None, decay=1.0
     ``out`` made here)."""
     import torch
     if out is None:
-        out = torch.zeros((q.shape[0], comp.capacity), dtype=torch.float32, device=q.device)
+        with _on_stream(stream):
+            out = torch.zeros((q.shape[0], comp.capacity), dtype=torch.float32, device=q.device)
     prepare_weights_paged(shape, seq_geom, q, comp, lse, weights=weights, decay=decay, out=out, stream=stream)()
     return out
 

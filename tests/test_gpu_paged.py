@@ -831,6 +831,25 @@ def test_two_streams_at_once(torch, ds4a):
         check_decode(host(o), host(lse), paged.decode(shape, geom, q, raw, comp), [1028, 170])
 
 
+def test_weights_on_a_side_stream_while_the_current_one_is_busy(torch, ds4a):
+    """The output made by the call is zeroed on the call's stream, before its kernel, not when the current stream
+    gets to it."""
+    rng = np.random.default_rng(92)
+    rows = [300, 77]
+    geom = geometry(rows, 4, 16)
+    comp = make(rng, 2, rows, 16)
+    shape, g, q, seg = shape_of(), up(torch, np.array(geom, dtype=np.int32)), up(torch, rng.standard_normal(
+        (2, H, D)).astype(np.float16)), rows_on(torch, ds4a, comp)
+    _, lse = ds4a.attn_decode_paged(shape, g, q, None, seg, want_lse=True)
+    want = ds4a.attn_weights_paged(shape, g, q, seg, lse)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)  # some 10 ms of the current stream
+    got = ds4a.attn_weights_paged(shape, g, q, seg, lse, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and got.sum() > 100
+
+
 def test_a_bad_call_records_nothing(torch, ds4a):
     rng = np.random.default_rng(91)
     seg = make(rng, 1, [20], 4)

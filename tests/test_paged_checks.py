@@ -343,3 +343,50 @@ def test_sizes_are_refused_before_devices(call, monkeypatch):
         raises("weight", ds4a.rmsnorm_fp8, x, one.half())
     else:
         raises("residual", ds4a.rmsnorm_fp8, x, one, residual=x.float())
+
+
+# ------------------------------------------------------------------ streams
+
+class Streams:
+    """Stands in for torch's current stream: which stream was current at each allocation."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.made = None, []
+        outer = self
+
+        class On:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                self.before, outer.current = outer.current, self.stream
+
+            def __exit__(self, *exc):
+                outer.current = self.before
+
+        monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(ds4a, "_on_device", lambda **kw: None)
+        monkeypatch.setattr(ds4a, "_stream", lambda s: ctypes.c_void_p(0))
+        for name in ("empty", "zeros", "empty_like"):
+            def make(*a, real=getattr(torch, name), name=name, **kw):
+                self.made.append((name, self.current))
+                return real(*a, **kw)
+            monkeypatch.setattr(torch, name, make)
+
+
+class Library:
+    """Every call succeeds; every size is 4096."""
+
+    def __getattr__(self, name):
+        return lambda *a: 4096 if "size" in name or "splits" in name else ds4a.OK
+
+
+def test_weights_fill_their_output_on_the_stream_of_the_call(monkeypatch):
+    rows = ds4a.PagedRows(torch.zeros((4, 8, D), dtype=F16), None, torch.zeros((2, 3), dtype=I32))
+    q, geom, lse = torch.zeros((2, H, D), dtype=F16), torch.zeros((2, 4), dtype=I32), torch.zeros((2, H))
+    monkeypatch.setattr(ds4a, "_lib", Library())
+    s = Streams(monkeypatch)
+    for stream in (None, "side"):
+        s.made.clear()
+        ds4a.attn_weights_paged(SHAPE, geom, q, rows, lse, stream=stream)
+        assert s.made == [("zeros", stream)] and s.current is None
