@@ -4,6 +4,10 @@ Argument marshalling only: every step of the attention path runs in the
 library's CUDA kernels.  PyTorch supplies device memory and the current
 stream.  There is no fallback: if the library is missing, importing the
 functions raises.
+
+A call runs on the current stream, or on ``stream``; the outputs and workspaces
+it makes belong to that stream (as tensors made in ``with
+torch.cuda.stream(stream)`` do).
 """
 
 from __future__ import annotations
@@ -231,13 +235,16 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _on_stream(stream):
-    """The context in which a call issued on ``stream`` makes its own tensors:
-    their fills run there, before the call's kernels, and their memory goes
-    back to that stream's pool, behind them."""
-    import contextlib
+def _new(stream, make, *args, **kw):
+    """A tensor that a call on ``stream`` makes for itself or its caller
+    (``make``: torch.empty and the like), made as in ``with
+    torch.cuda.stream(stream)``: a fill runs there, before the call's kernels,
+    and the memory goes back to that stream's pool, behind them."""
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 
 def _ptr(t):
@@ -333,12 +340,12 @@ def _status_ok(L, status, q_tile, name):
         raise ValueError(f"{name} must be contiguous uint8 {want}")
 
 
-def _outputs(q, out, lse, want_lse):
+def _outputs(q, out, lse, want_lse, stream):
     import torch
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     if lse is None and want_lse:
-        lse = torch.empty((q.shape[0], H), dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, (q.shape[0], H), dtype=torch.float32, device=q.device)
     return out, lse
 
 
@@ -351,7 +358,7 @@ def pad_kv(src, n_rows: int | None = None, dst=None, stream=None):
     n = src.shape[0] if n_rows is None else int(n_rows)
     n_pad = -(-n // BLOCK_ROWS) * BLOCK_ROWS
     if dst is None:
-        dst = torch.empty((n_pad, D), dtype=torch.float16, device=src.device)
+        dst = _new(stream, torch.empty, (n_pad, D), dtype=torch.float16, device=src.device)
     sp, ss = _rows(src, "src", n)
     dp, ds = _rows(dst, "dst", n_pad)
     _on_device(src=src, dst=dst)
@@ -372,7 +379,7 @@ def block_mask(layout, q_tile: int, mask=None, out=None, stream=None):
     nb = _n_blocks(L)
     _mask_ok(L, mask)
     if out is None:
-        out = torch.empty((-(-L.T // q_tile), nb), dtype=torch.uint8, device="cuda")
+        out = _new(stream, torch.empty, (-(-L.T // q_tile), nb), dtype=torch.uint8, device="cuda")
     _status_ok(L, out, q_tile, "out")
     _on_device(mask=mask, out=out)
     ms = 0 if mask is None else mask.stride(0) * 2
@@ -389,7 +396,7 @@ def attn_prefill(layout, q, k_raw, v_raw, k_comp=None, v_comp=None, *, mask=None
         if mask is None:
             raise ValueError("status bytes are read only with a dense mask")
         _status_ok(L, status, q_tile, "status")
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     X = _tensors(L, q, k_raw, v_raw, k_comp, v_comp, out, lse)
     _on_device(mask=mask, status=status)
     ms = 0 if mask is None else mask.stride(0) * 2
@@ -410,11 +417,11 @@ def attn_decode(layout, q, k_raw, v_raw, k_comp=None, v_comp=None, *, n_splits=0
                 lse=None, want_lse=False, stream=None):
     import torch
     L = make_layout(layout)
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     X = _tensors(L, q, k_raw, v_raw, k_comp, v_comp, out, lse)
     need = decode_workspace_bytes(L, n_splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 256), dtype=torch.uint8, device=q.device)
     _on_device(workspace=workspace)
     _check(lib().ds4a_attn_decode(ctypes.byref(L), ctypes.byref(X), int(n_splits), _ptr(workspace),
                                   workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -512,7 +519,7 @@ def attn_decode_fp8(layout, q, k_raw, v_raw, k_codes, k_scale, v_codes, v_scale,
     fp32 row scales [n], as made by :func:`quantize_kv_fp8`)."""
     import torch
     L = make_layout(layout)
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     L0 = make_layout(layout)
     L0.n_comp = 0
     X = _tensors(L0, q, k_raw, v_raw, None, None, out, lse, check_device=False)
@@ -531,7 +538,7 @@ def attn_decode_fp8(layout, q, k_raw, v_raw, k_codes, k_scale, v_codes, v_scale,
     X.k_comp, X.v_comp, X.comp_row_stride = k_codes.data_ptr(), v_codes.data_ptr(), k_codes.stride(0)
     need = decode_workspace_bytes(L, n_splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 256), dtype=torch.uint8, device=q.device)
     _on_device(workspace=workspace)
     _check(lib().ds4a_attn_decode_fp8(ctypes.byref(L), ctypes.byref(X), _ptr(k_scale), _ptr(v_scale), int(n_splits),
                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -592,12 +599,12 @@ def attn_decode_fp8kv(layout, q, k_raw, v_raw, k_comp, v_comp, *, k_comp_scale, 
     scales are given, else fp16 [n_raw, 512]."""
     import torch
     L = make_layout(layout)
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     X, S = _fp8kv(L, q, k_raw, v_raw, k_comp, v_comp, out, lse, k_raw_scale, v_raw_scale, k_comp_scale,
                   v_comp_scale)
     need = decode_workspace_bytes(L, n_splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 256), dtype=torch.uint8, device=q.device)
     _on_device(workspace=workspace)
     _check(lib().ds4a_attn_decode_fp8kv(ctypes.byref(L), ctypes.byref(X), ctypes.byref(S), int(n_splits),
                                         _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -621,7 +628,7 @@ def attn_prefill_fp8kv(layout, q, k_raw, v_raw, k_comp=None, v_comp=None, *, k_c
     one-token kernel without a workspace."""
     import torch
     L = make_layout(layout)
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     X, S = _fp8kv(L, q, k_raw, v_raw, k_comp, v_comp, out, lse, k_raw_scale, v_raw_scale, k_comp_scale,
                   v_comp_scale)
     if workspace is False:
@@ -630,7 +637,7 @@ def attn_prefill_fp8kv(layout, q, k_raw, v_raw, k_comp=None, v_comp=None, *, k_c
     else:
         need = lib().ds4a_attn_prefill_fp8kv_workspace_size(ctypes.byref(L)) if k_raw_scale is not None else 0
         if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _new(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
         wp, wb = None, 0
         if workspace is not None:
             _on_device(workspace=workspace)
@@ -650,7 +657,7 @@ def attn_decode_batch(shape, seq_geom, q, k_raw, v_raw, k_comp=None, v_comp=None
     B = q.shape[0]
     if seq_geom.dtype != torch.int32 or tuple(seq_geom.shape) != (B, 4) or not seq_geom.is_contiguous():
         raise ValueError("seq_geom must be contiguous int32 [B, 4]")
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     qp, qs = _tokens(q, "q")
     op, os_ = _tokens(out, "out", B)
     _lse_ok(lse, B)
@@ -673,7 +680,7 @@ def attn_decode_batch(shape, seq_geom, q, k_raw, v_raw, k_comp=None, v_comp=None
         n_splits = lib().ds4a_attn_decode_batch_default_splits(B, ctypes.byref(S), rr, cr)
     need = lib().ds4a_attn_decode_batch_workspace_size(B, int(n_splits))
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 256), dtype=torch.uint8, device=q.device)
     _on_device(workspace=workspace)
     _check(lib().ds4a_attn_decode_batch(B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(X), int(n_splits),
                                         _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -688,7 +695,8 @@ def attn_decode_partials(layout, q, k_raw, v_raw, k_comp=None, v_comp=None, *, n
     L = make_layout(layout)
     X = _tensors(L, q, k_raw, v_raw, k_comp, v_comp, None, None)
     if workspace is None:
-        workspace = torch.empty(max(decode_workspace_bytes(L, n_splits), 256), dtype=torch.uint8, device=q.device)
+        need = decode_workspace_bytes(L, n_splits)
+        workspace = _new(stream, torch.empty, max(need, 256), dtype=torch.uint8, device=q.device)
     _on_device(workspace=workspace)
     _check(lib().ds4a_attn_decode_partials(ctypes.byref(L), ctypes.byref(X), int(n_splits), _ptr(workspace),
                                            workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -714,7 +722,7 @@ def attn_decode_noalloc(layout, q, k_raw, v_raw, k_comp=None, v_comp=None, *, n_
     """:func:`attn_decode` without a workspace: the library's own 8 MiB scratch
     array holds the split partials (for callers that cannot allocate)."""
     L = make_layout(layout)
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     X = _tensors(L, q, k_raw, v_raw, k_comp, v_comp, out, lse)
     _check(lib().ds4a_attn_decode_noalloc(ctypes.byref(L), ctypes.byref(X), int(n_splits), _stream(stream)),
            "ds4a_attn_decode_noalloc")
@@ -728,7 +736,7 @@ def attn_indexed(layout, q, k_raw, v_raw, k_comp, v_comp, idx, *, out=None, lse=
         raise ValueError("idx must be int32 [T, top_k] with contiguous rows")
     if idx.shape[0] < L.T:
         raise ValueError(f"idx has {idx.shape[0]} lists, the layout has T = {L.T}")
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     X = _tensors(L, q, k_raw, v_raw, k_comp, v_comp, out, lse)
     _on_device(idx=idx)
     _check(lib().ds4a_attn_indexed(ctypes.byref(L), ctypes.byref(X), _ptr(idx), idx.stride(0) * 4, idx.shape[1],
@@ -747,7 +755,7 @@ def attn_indexed_fp8kv(layout, q, k_raw, v_raw, k_comp, v_comp, idx, *, k_comp_s
         raise ValueError("idx must be int32 [T, top_k] with contiguous rows")
     if idx.shape[0] < L.T:
         raise ValueError(f"idx has {idx.shape[0]} lists, the layout has T = {L.T}")
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     X, S = _fp8kv(L, q, k_raw, v_raw, k_comp, v_comp, out, lse, k_raw_scale, v_raw_scale, k_comp_scale,
                   v_comp_scale)
     _on_device(idx=idx)
@@ -779,7 +787,7 @@ def indexer_scores(layout, q_idx, k_idx, head_weights, *, scale, relu=True, out=
         raise ValueError(f"k_idx holds {k_idx.shape[0]} rows, the layout needs {n_comp}")
     if out is None:
         stride = (n_comp + 3) // 4 * 4
-        out = torch.empty((T, stride), dtype=torch.float32, device=q_idx.device)[:, :n_comp]
+        out = _new(stream, torch.empty, (T, stride), dtype=torch.float32, device=q_idx.device)[:, :n_comp]
     if out.dtype != torch.float32 or out.dim() != 2 or out.stride(1) != 1 or out.shape[0] < T or \
             out.shape[1] < n_comp:
         raise ValueError(f"out must be fp32 [>= {T}, >= {n_comp}] with contiguous rows")
@@ -801,7 +809,7 @@ def indexer_topk(layout, scores, top_k, *, out=None, stream=None):
         raise ValueError(f"scores is {tuple(scores.shape)}, the layout needs at least ({L.T}, {L.n_comp})")
     if out is None:
         stride = (top_k + 3) // 4 * 4
-        out = torch.empty((T, stride), dtype=torch.int32, device=scores.device)[:, :top_k]
+        out = _new(stream, torch.empty, (T, stride), dtype=torch.int32, device=scores.device)[:, :top_k]
     if out.dtype != torch.int32 or out.dim() != 2 or out.stride(1) != 1 or out.shape[0] < L.T or \
             out.shape[1] < top_k:
         raise ValueError(f"out must be int32 [>= {L.T}, >= {top_k}] with contiguous rows")
@@ -817,9 +825,9 @@ def quantize_kv_fp8(rows, *, codes=None, scales=None, stream=None):
     ptr, stride = _rows(rows, "rows")
     n = rows.shape[0]
     if codes is None:
-        codes = torch.empty((n, 512), dtype=torch.uint8, device=rows.device)
+        codes = _new(stream, torch.empty, (n, 512), dtype=torch.uint8, device=rows.device)
     if scales is None:
-        scales = torch.empty((n,), dtype=torch.float32, device=rows.device)
+        scales = _new(stream, torch.empty, (n,), dtype=torch.float32, device=rows.device)
     if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.stride(1) != 1 or codes.shape[1] != 512 or \
             codes.shape[0] < n:
         raise ValueError(f"codes must be uint8 [>= {n}, 512] with contiguous rows")
@@ -861,7 +869,7 @@ def compress_append(kv, score, state_kv, state_score, n_state, ratio, *, out=Non
     if sts != scs or state_kv.shape[0] < ratio - 1 or state_score.shape[0] < ratio - 1:
         raise ValueError("the state tensors must hold ratio - 1 rows at one row stride")
     if out is None:
-        out = torch.empty((n_out, width), dtype=torch.float16, device=kv.device)
+        out = _new(stream, torch.empty, (n_out, width), dtype=torch.float16, device=kv.device)
     if out.dtype != torch.float16 or out.dim() != 2 or out.shape[0] < n_out or out.shape[1] != width or \
             out.stride(1) != 1:
         raise ValueError("out must be fp16 [>= n_out, width] with contiguous rows")
@@ -950,10 +958,10 @@ def _per_row(t, name, n_seq, cols, dtype):
     return _ptr(t), max(t.stride(0), cols) * t.element_size()
 
 
-def _bytes_of(workspace, need, q):
+def _bytes_of(workspace, need, q, stream):
     import torch
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 256), dtype=torch.uint8, device=q.device)
     _on_device(workspace=workspace)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -977,7 +985,7 @@ def prepare_decode_paged(shape, seq_geom, q, raw, comp=None, *, workspace=None, 
     for seg, name in ((raw, "raw"), (comp, "comp")):
         if seg is not None:
             seg._check(name, B)
-    workspace, nbytes = _bytes_of(workspace, decode_paged_workspace_bytes(B), q)
+    workspace, nbytes = _bytes_of(workspace, decode_paged_workspace_bytes(B), q, stream)
     X = PagedBatch(qp, qs, _NO_ROWS if raw is None else raw._c, _NO_ROWS if comp is None else comp._c, op, os_,
                    _ptr(lse))
     args = (B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(X), _ptr(workspace), nbytes, _stream(stream))
@@ -990,7 +998,7 @@ def attn_decode_paged(shape, seq_geom, q, raw, comp=None, *, workspace=None, out
     """One decode step for B sequences over paged rows: q fp16 [B, 64, 512];
     ``raw`` and ``comp`` :class:`PagedRows` (either may be None) of one format;
     seq_geom int32 [B, 4] on the device: (q_pos, n_raw, raw_pos0, n_comp)."""
-    out, lse = _outputs(q, out, lse, want_lse)
+    out, lse = _outputs(q, out, lse, want_lse, stream)
     prepare_decode_paged(shape, seq_geom, q, raw, comp, workspace=workspace, out=out, lse=lse, stream=stream)()
     return (out, lse) if (want_lse or lse is not None) else out
 
@@ -1022,8 +1030,7 @@ def attn_weights_paged(shape, seq_geom, q, comp, lse, *, weights=None, decay=1.0
     ``out`` made here)."""
     import torch
     if out is None:
-        with _on_stream(stream):
-            out = torch.zeros((q.shape[0], comp.capacity), dtype=torch.float32, device=q.device)
+        out = _new(stream, torch.zeros, (q.shape[0], comp.capacity), dtype=torch.float32, device=q.device)
     prepare_weights_paged(shape, seq_geom, q, comp, lse, weights=weights, decay=decay, out=out, stream=stream)()
     return out
 
@@ -1051,7 +1058,7 @@ def prepare_evict_paged(shape, seq_geom, rows, weights, n_keep, *, n_first=0, n_
     if n_out.dtype != torch.int32 or n_out.dim() != 1 or n_out.shape[0] < B or (B > 1 and n_out.stride(0) < 1):
         raise ValueError(f"n_out must be int32 [>= {B}]")
     _on_device(n_out=n_out)
-    workspace, nbytes = _bytes_of(workspace, evict_paged_workspace_bytes(B, n_keep), weights)
+    workspace, nbytes = _bytes_of(workspace, evict_paged_workspace_bytes(B, n_keep), weights, stream)
     E = Eviction(wp, wst, ip, ist, n_keep, int(n_first), int(n_recent), kp, kst, wop, wost, iop, iost, _ptr(n_out),
                  max(n_out.stride(0), 1) * 4)
     args = (B, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(rows._c), ctypes.byref(E), _ptr(workspace), nbytes,
@@ -1072,9 +1079,9 @@ def evict_paged(shape, seq_geom, rows, weights, n_keep, *, n_first=0, n_recent=0
     import torch
     B, dev = seq_geom.shape[0], weights.device
     if kept is None:
-        kept = torch.empty((B, int(n_keep)), dtype=torch.int32, device=dev)
+        kept = _new(stream, torch.empty, (B, int(n_keep)), dtype=torch.int32, device=dev)
     if n_out is None:
-        n_out = torch.empty((B,), dtype=torch.int32, device=dev)
+        n_out = _new(stream, torch.empty, (B,), dtype=torch.int32, device=dev)
     prepare_evict_paged(shape, seq_geom, rows, weights, n_keep, n_first=n_first, n_recent=n_recent, ids=ids,
                         kept=kept, weights_out=weights if weights_out is None else weights_out,
                         ids_out=ids if ids_out is None else ids_out, n_out=n_out, workspace=workspace,
@@ -1163,13 +1170,14 @@ def rmsnorm_fp8(x, weight, *, eps=1e-6, residual=None, residual_out=None, group=
     import torch
     n, width = x.shape
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _new(stream, torch.empty_like, residual)
     if codes is None:
-        codes = torch.empty((n, -(-width // 8) * 8), dtype=torch.uint8, device=x.device)[:, :width]
+        codes = _new(stream, torch.empty, (n, -(-width // 8) * 8), dtype=torch.uint8, device=x.device)[:, :width]
     if scales is None:
-        scales = torch.empty((n, 1 if group == 0 else -(-width // int(group))), dtype=torch.float32, device=x.device)
+        groups = 1 if group == 0 else -(-width // int(group))
+        scales = _new(stream, torch.empty, (n, groups), dtype=torch.float32, device=x.device)
     if y is None and want_y:
-        y = torch.empty((n, width), dtype=torch.float16, device=x.device)
+        y = _new(stream, torch.empty, (n, width), dtype=torch.float16, device=x.device)
     prepare_rmsnorm_fp8(x, weight, eps=eps, residual=residual, residual_out=residual_out, group=group, codes=codes,
                         scales=scales, y=y, stream=stream)()
     out = [codes, scales]

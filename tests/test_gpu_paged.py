@@ -831,6 +831,49 @@ def test_two_streams_at_once(torch, ds4a):
         check_decode(host(o), host(lse), paged.decode(shape, geom, q, raw, comp), [1028, 170])
 
 
+def test_two_streams_without_workspaces_of_the_callers(torch, ds4a):
+    """Decodes in flight on two streams, their outputs and workspaces made by the calls, nothing waited for between
+    them: each call has its own, and a job's results are the same bits every time."""
+    rng = np.random.default_rng(93)
+    shape = shape_of()
+    jobs = []
+    for k in range(2):
+        geom, q, raw, comp = case(rng, [4000 + k, 2500], 4, 16, bool(k), True)
+        jobs.append((geom, q, raw, comp, up(torch, np.array(geom, dtype=np.int32)), up(torch, q),
+                     rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[ds4a.attn_decode_paged(shape, j[4], j[5], j[6], j[7], want_lse=True, stream=j[8]) for j in jobs]
+            for _ in range(20)]
+    torch.cuda.synchronize()
+    for k, (geom, q, raw, comp, *_) in enumerate(jobs):
+        check_decode(host(outs[0][k][0]), host(outs[0][k][1]), paged.decode(shape, geom, q, raw, comp), [4129, 2628])
+        for o in outs[1:]:
+            assert torch.equal(o[k][0], outs[0][k][0]) and torch.equal(o[k][1], outs[0][k][1])
+
+
+def test_two_streams_with_workspaces_held(torch, ds4a):
+    """The same with a workspace each that lives as long as the calls use it."""
+    rng = np.random.default_rng(94)
+    shape = shape_of()
+    jobs = []
+    for k in range(2):
+        geom, q, raw, comp = case(rng, [3000, 800 + k], 4, 16, bool(k), True)
+        o, lse = torch.empty((2, H, D), dtype=torch.float16, device="cuda"), torch.empty((2, H), device="cuda")
+        ws = torch.empty(ds4a.decode_paged_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+        call = ds4a.prepare_decode_paged(shape, up(torch, np.array(geom, dtype=np.int32)), up(torch, q),
+                                         rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp), workspace=ws, out=o,
+                                         lse=lse, stream=torch.cuda.Stream())
+        jobs.append((geom, q, raw, comp, o, lse, call))
+    assert jobs[0][6]._keep[6].data_ptr() != jobs[1][6]._keep[6].data_ptr()
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for j in jobs:
+            j[6]()
+    torch.cuda.synchronize()
+    for geom, q, raw, comp, o, lse, _ in jobs:
+        check_decode(host(o), host(lse), paged.decode(shape, geom, q, raw, comp), [3128, 930])
+
+
 def test_weights_on_a_side_stream_while_the_current_one_is_busy(torch, ds4a):
     """The output made by the call is zeroed on the call's stream, before its kernel, not when the current stream
     gets to it."""

@@ -390,3 +390,53 @@ def test_weights_fill_their_output_on_the_stream_of_the_call(monkeypatch):
         s.made.clear()
         ds4a.attn_weights_paged(SHAPE, geom, q, rows, lse, stream=stream)
         assert s.made == [("zeros", stream)] and s.current is None
+
+
+def wrapper_calls():
+    """Every wrapper that makes tensors of its own, on small host tensors: (name, number of tensors, call)."""
+    q, geom = torch.zeros((2, H, D), dtype=F16), torch.zeros((2, 4), dtype=I32)
+    r, c, sc = torch.zeros((64, D), dtype=F16), torch.zeros((64, D), dtype=U8), torch.ones(64)
+    b = torch.zeros((2, 64, D), dtype=F16)
+    rows = ds4a.PagedRows(torch.zeros((4, 8, D), dtype=F16), None, torch.zeros((2, 3), dtype=I32))
+    L = ds4a.make_layout(dict(T=2, q_pos0=100, n_raw=64, raw_pos0=38, n_comp=25, ratio=4, window=128))
+    S = ds4a.make_layout(SHAPE)
+    w, lse = torch.zeros((2, 24)), torch.zeros((2, H))
+    x, one = torch.zeros((2, 64), dtype=F16), torch.ones(64)
+    idx = torch.zeros((2, 8), dtype=I32)
+    f8 = dict(k_comp_scale=sc, v_comp_scale=sc, k_raw_scale=sc, v_raw_scale=sc)
+    kv, state = torch.zeros((5, 16)), torch.zeros((3, 16))
+    qi, ki, wi, scores = torch.zeros((2, 4, 128), dtype=F16), torch.zeros((25, 128), dtype=F16), torch.ones((2, 4)), \
+        torch.zeros((2, 28))
+    return [
+        ("pad_kv", 1, lambda **k: ds4a.pad_kv(r, 33, **k)),
+        ("attn_prefill", 2, lambda **k: ds4a.attn_prefill(L, q, r, r, r, r, want_lse=True, **k)),
+        ("attn_decode", 3, lambda **k: ds4a.attn_decode(L, q, r, r, r, r, want_lse=True, **k)),
+        ("attn_decode_fp8", 2, lambda **k: ds4a.attn_decode_fp8(L, q, r, r, c, sc, c, sc, **k)),
+        ("attn_decode_fp8kv", 2, lambda **k: ds4a.attn_decode_fp8kv(L, q, c, c, c, c, **f8, **k)),
+        ("attn_prefill_fp8kv", 2, lambda **k: ds4a.attn_prefill_fp8kv(L, q, c, c, c, c, **f8, **k)),
+        ("attn_decode_batch", 2, lambda **k: ds4a.attn_decode_batch(S, geom, q, b, b, b, b, **k)),
+        ("attn_decode_partials", 1, lambda **k: ds4a.attn_decode_partials(L, q, r, r, r, r, **k)),
+        ("attn_decode_noalloc", 1, lambda **k: ds4a.attn_decode_noalloc(L, q, r, r, r, r, **k)),
+        ("attn_indexed", 1, lambda **k: ds4a.attn_indexed(L, q, r, r, r, r, idx, **k)),
+        ("attn_indexed_fp8kv", 1, lambda **k: ds4a.attn_indexed_fp8kv(L, q, c, c, c, c, idx, **f8, **k)),
+        ("indexer_scores", 1, lambda **k: ds4a.indexer_scores(L, qi, ki, wi, scale=1.0, **k)),
+        ("indexer_topk", 1, lambda **k: ds4a.indexer_topk(L, scores, 8, **k)),
+        ("compress_append", 1, lambda **k: ds4a.compress_append(kv, kv, state, state, 0, 4, **k)),
+        ("quantize_kv_fp8", 2, lambda **k: ds4a.quantize_kv_fp8(r, **k)),
+        ("attn_decode_paged", 3, lambda **k: ds4a.attn_decode_paged(SHAPE, geom, q, None, rows, want_lse=True, **k)),
+        ("prepare_decode_paged", 1, lambda **k: ds4a.prepare_decode_paged(SHAPE, geom, q, None, rows, out=q, **k)),
+        ("evict_paged", 3, lambda **k: ds4a.evict_paged(SHAPE, geom, rows, w, 10, **k)),
+        ("rmsnorm_fp8", 4, lambda **k: ds4a.rmsnorm_fp8(x, one, residual=x, want_y=True, **k)),
+    ]
+
+
+@pytest.mark.parametrize("i", range(19))
+def test_tensors_of_a_call_are_made_on_its_stream(monkeypatch, i):
+    """A workspace freed to another stream's pool could be handed out while the call's kernels still use it."""
+    name, n, call = wrapper_calls()[i]
+    monkeypatch.setattr(ds4a, "_lib", Library())
+    s = Streams(monkeypatch)
+    for stream in (None, "side"):
+        s.made.clear()
+        call(stream=stream)
+        assert [on for _, on in s.made] == [stream] * n and s.current is None, name
