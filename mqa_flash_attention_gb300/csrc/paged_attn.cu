@@ -116,7 +116,7 @@ struct PMisc {
   int2 box[kLists][kTile / 8];            // (page, slot) of the runs of a tile that TMA loads
   alignas(16) float red[4][kH];
   alignas(16) float m_use[kH];  // reference of each head (weights: its lse), log2 units
-  alignas(16) float m_lim[kH];  // m_use + kTau
+  alignas(16) float m_lim[kH];  // largest score under that reference
   alignas(16) float alpha[kH];
   alignas(16) float inv_l[kH];
   alignas(8) uint64_t q_full, q_empty;
@@ -900,11 +900,19 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const C
 
 // ------------------------------------------------------------------ softmax and epilogue
 
-// The reference of a head is a value its scores stay within 2^kTau of, so P
-// fits fp16; it moves only when a score passes that.  While it holds (nearly
-// always after a sequence's first tile) a tile needs no maximum over its rows:
-// one vote of the block that no score is over.  kNoRef stands for no reference
-// yet: any score passes it, and absent rows (-inf) get weight 0 under it.
+// The reference of a head lies kLift below the largest score of the tile that
+// set it, and moves only when a score passes it by kLift + kHold, so P is 2^15
+// at most (fp16 holds 65504) and keeps fp16's full precision for rows down to
+// 2^-(14 + kLift) of the largest weight; rows further down are off by half a
+// step, 2^-(25 + kLift) of it.  (Without the lift a row of 2^-25 counted in the
+// sum and not in the product: a long tail under one row lost 42% of its value.)
+// While the reference holds (nearly always after a sequence's first tile) a
+// tile needs no maximum over its rows: one vote of the block that no score is
+// over.  kLift and kHold share out fp16's 15 bits above 1: 64 sequences of fp16
+// and 24 of E4M3 rows take 41.3 and 43.9 us with 7 + 8, 41.5 and 44.0 with 10 +
+// 5, 43.5 and 47.0 with 12 + 3, where the reference moves often.  kNoRef stands for no reference yet: any score passes it, and absent
+// rows (-inf) get weight 0 under it.
+constexpr float kLift = 10.f, kHold = 5.f;
 constexpr float kNoRef = -3e38f;
 
 template <bool FP8>
@@ -919,7 +927,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
   const int nt = cp.n;
   bool bad = false;
   uint32_t n_item = 0;
-  float m_ref = kNoRef;  // reference of head `tid` (threads < 64), log2 units
+  float m_ref = kNoRef, m_lim = kNoRef;  // reference of head `tid` (threads < 64), log2 units, and its limit
   float lpart[32];
   if (tid < kH) ms.m_use[tid] = ms.m_lim[tid] = kNoRef;
   bar_sync_id(1, kComputeThreads);
@@ -963,12 +971,15 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
       if (tid < kH) {
         const float tmax = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid]));
         float alpha = 1.f;
-        if (tmax > m_ref + kTau) {
-          alpha = exp2f(m_ref - tmax);  // 0 while there was none
-          m_ref = tmax;
+        if (tmax > m_lim) {
+          // Rounded so that P stays within 2^15 where scores are 16 and more apart.
+          const float next = __fsub_ru(tmax, kLift);
+          alpha = exp2f(m_ref - next);  // 0 while there was none
+          m_ref = next;
+          m_lim = __fadd_rd(m_ref, kLift + kHold);
         }
         ms.m_use[tid] = m_ref;
-        ms.m_lim[tid] = m_ref + kTau;
+        ms.m_lim[tid] = m_lim;
         ms.alpha[tid] = alpha;
       }
       bar_sync_id(1, kComputeThreads);
@@ -978,8 +989,8 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
     {
       // P^T row r: heads 32hh .. +31 are 16-byte chunks 4hh .. 4hh+3 of its
       // 128 bytes, chunk c at c ^ (r & 7).  P is rounded once to fp16 for the
-      // MMA; the row sums add it unrounded, so lse keeps fp32 precision (the
-      // two differ by rounding errors that average out over the rows).
+      // MMA, to 2^-11 of a weight (below 2^-(14 + kLift) of the largest, to half
+      // a step); the row sums add it unrounded, so lse keeps fp32 precision.
       uint8_t *prow = smem + kOffP + r * 128;
       const bool dead = FP8 && lvs <= kLeastLog2Scale;  // a V scale of 0: weight, but no value
 #pragma unroll
@@ -1077,7 +1088,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
     tc_fence_before();
     mbar_arrive(smem_u32(&ms.o_empty));
     ++n_item;
-    m_ref = kNoRef;
+    m_ref = m_lim = kNoRef;
     if (tid < kH) ms.m_use[tid] = ms.m_lim[tid] = kNoRef;
     if (bar_red_or(1, kComputeThreads, bad)) break;
   }

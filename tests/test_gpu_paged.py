@@ -360,6 +360,55 @@ def test_decode_large_scores_move_the_reference(torch, ds4a):
     check_decode(host(o), host(lse), paged.decode(shape, geom, q, raw, comp), [1628])
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("n_seq", [1, 64])
+@pytest.mark.parametrize("below", [12.3, 20.7, 24.6, 25.0, 25.5, 28.3])
+def test_decode_of_a_long_tail_under_one_row(torch, ds4a, below, n_seq, f8):
+    """One row on top whose value is 0, and 65,535 rows of value 1, each with 2^-below of its weight: the output is
+    the tail's share.  Scores are single products (exact but for the rounding of the scale and of the product, 2^-23
+    of a score: 2^-18 of a weight).  A weight's rounding is at most 2^-11 of it, or half a step of fp16's smallest
+    numbers, where the largest weight counts as 2^10: 2^-35 of that one; the output is rounded (2^-11, or 2^-25)."""
+    n, page = 65536, 128
+    k = torch.zeros((n // page, page, D), dtype=torch.uint8 if f8 else torch.float16, device="cuda")
+    v = torch.full_like(k, 0x38 if f8 else 1.0)  # 0x38: the E4M3 code of 1
+    k[0, 5, 7] = 0x50 if f8 else 8.0             # 8
+    v[0, 5] = 0
+    one = torch.ones((n // page, page), device="cuda") if f8 else None
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").repeat(n_seq, 1)
+    q = torch.zeros((n_seq, H, D), dtype=torch.float16, device="cuda")
+    q[:, :, 7] = 1
+    geom = torch.tensor([[4 * n, 0, 0, n]] * n_seq, dtype=torch.int32, device="cuda")
+    shape = shape_of(scale=below * np.log(2.0) / 8)
+    o, lse = ds4a.attn_decode_paged(shape, geom, q, None, ds4a.PagedRows(k, v, table, k_scale=one, v_scale=one),
+                                    want_lse=True)
+    e = np.exp(-8 * np.float64(shape["scale"]))
+    want = (n - 1) * e / (1 + (n - 1) * e)
+    bound = want * (2.0 ** -11 + max(2.0 ** -11, 2.0 ** -35 / e) + 2.0 ** -17) + 2.0 ** -25
+    got = host(o).astype(np.float64)
+    assert np.abs(got - want).max() <= bound, f"{got.min()} .. {got.max()}, {want} +- {bound}"
+    assert np.abs(host(lse) - (8 * np.float64(shape["scale"]) + np.log1p((n - 1) * e))).max() <= \
+        (n / 128 + 40) * 2.0 ** -23 + 32 * 2.0 ** -22
+
+
+@pytest.mark.parametrize("base", range(4))
+def test_decode_scores_a_step_apart_stay_finite(torch, ds4a, base):
+    """Scores near 2^27, where fp32 numbers are 16 apart: a row one step above a tile's largest, in a later tile,
+    is the new reference, not a weight of 2^16.  (Whichever scores round alike, the output lies between the values.)"""
+    k = torch.zeros((2, 128, D), dtype=torch.float16, device="cuda")
+    v = torch.ones_like(k)
+    k[:, :, 0], k[:, :, 1] = 6144.0, float(base)  # 2048 * 6144 + base
+    k[1, 9, 1] = base + 1.0
+    v[1, 9] = 2.0
+    q = torch.zeros((8, H, D), dtype=torch.float16, device="cuda")
+    q[:, :, 0], q[:, :, 1] = 2048.0, 1.0
+    table = torch.arange(2, dtype=torch.int32, device="cuda").repeat(8, 1)
+    geom = torch.tensor([[1024, 0, 0, 256]] * 8, dtype=torch.int32, device="cuda")
+    o, lse = ds4a.attn_decode_paged(shape_of(scale=16 * np.log(2.0)), geom, q, None, ds4a.PagedRows(k, v, table),
+                                    want_lse=True)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert (o >= 1).all() and (o <= 2).all()
+
+
 def test_decode_equals_batched_decode_and_itself(torch, ds4a):
     """The batched decode over the same rows, gathered; the same call twice, bit for bit, on a dirty workspace."""
     rng = np.random.default_rng(15)
