@@ -564,9 +564,10 @@ typedef struct {
  *   workspace   as in ds4a_attn_decode, of at least
  *               ds4a_attn_decode_paged_workspace_size(n_seq) bytes (which
  *               depends on the current device's SM count).
- * The 128-row tiles of all sequences together are shared out evenly among the
- * SMs, whatever the lengths; a sequence whose tiles fall to several SMs is
- * joined by its log-sum-exps.  The same call gives the same bits every time.
+ * The 128-row tiles of all sequences together are shared out among the SMs,
+ * whatever the lengths: none has more than the average (rounded up) and two
+ * tiles.  A sequence whose tiles fall to several SMs is joined by its
+ * log-sum-exps.  The same call gives the same bits every time.
  * A sequence's table may name 2^30 rows at most (the window's and all
  * compressed ones together).  Where K and V are the same pool in both segments
  * (and, in E4M3, the same scales), each row is read once for both products.

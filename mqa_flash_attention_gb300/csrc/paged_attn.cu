@@ -14,13 +14,17 @@
 // so pages of any size, tiles that span pages and pages that end inside a tile
 // are all alike.  A CTA's tiles of one sequence are an item.  With c the least
 // number for which the items ceil(tiles / c) of all sequences number at most
-// the CTAs, each CTA gets one item of at most c tiles.  Where there is no such
-// c near the average (more sequences than CTAs), the tiles of all sequences
-// are numbered through instead and CTA i takes ceil(total / CTAs) of them in a
-// row, several items.  Either way the load is even whatever the lengths; one
-// item per CTA costs one drain of the pipeline and fewer partial results (64
-// sequences of 5 to 17 tiles: 36 us in the slowest CTA with items cut at even
-// tile numbers, 30 us so).  An item that holds the whole sequence
+// the CTAs, each CTA gets one item of at most c tiles.  Where c would be over
+// a + min(2, a - 1), with a the average ceil(total / CTAs), or there is none
+// (more sequences than CTAs), the tiles of all sequences are numbered through
+// instead and CTA i takes a of them in a row, several items.  So no CTA has more
+// than the average and two tiles, whatever the lengths; one item per CTA costs one
+// drain of the pipeline and fewer partial results.  Averages of 3 to 12 tiles,
+// fp16: items one tile above the average 28.5 and 32.0 us, numbered 28.6 and
+// 34.3; two above 34.3 to 51.9, numbered 36.8 to 51.3; four above 37.7 to 74.9,
+// numbered 32.0 to 67.4; an average of 2, items of 4: 29.1, numbered 26.0; 149
+// sequences of one tile and one of 48, items of 16: 69.4, numbered 25.7.
+// An item that holds the whole sequence
 // writes its output; otherwise it leaves its normalised output (fp32) and
 // (m, l) in a slot of the workspace, slot CTA, or CTA + sequence with several
 // items per CTA (unique, since along the tiles either number grows), and the
@@ -80,6 +84,7 @@ namespace ds4a {
 namespace {
 
 constexpr int kLists = 4;  // row lists in flight
+constexpr int kTries = 3;  // sizes tried for one item per CTA: the average number of tiles, one and two more
 constexpr float kLeastLog2Scale = -40.f;  // V scales below 2^-40 count as 0: such rows round to 0 in fp16
 
 // Low bits of a list entry (rows are 16-byte aligned).  A slot without a row
@@ -130,7 +135,7 @@ struct PMisc {
   uint64_t p_full, p_empty, o_empty, mma_done;
   unsigned scan[kThreads / 32];
   CtaPlan plan;
-  int fits[kThreads / 32];
+  int fits[kTries];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -294,7 +299,6 @@ __device__ __forceinline__ int scan_warp(int n, int lane) {  // inclusive
   return n;
 }
 
-constexpr int kTries = 16;       // item sizes tried from the average up
 
 // The plan of this CTA, by one warp alone: lane l has kMost sequences in a
 // row.  Every warp computes it for itself (no block barrier stands between the
@@ -315,7 +319,7 @@ __device__ __forceinline__ CtaPlan plan_warp(const PagedAttnParams &p, int lane,
   }
   const int total = __reduce_add_sync(0xffffffffu, sum), per = (total + G - 1) / G;
   int c = per, items = G + 1;
-  for (int t = 0; t < kTries && total > 0; ++t, ++c) {
+  for (int t = 0; t < kTries && t < per; ++t, ++c) {
     int k = 0;
 #pragma unroll
     for (int u = 0; u < kMost; ++u) k += (unsigned)(n[u] + c - 1) / (unsigned)c;
@@ -410,13 +414,15 @@ __device__ __forceinline__ void plan_block(const PagedAttnParams &p, PMisc &ms, 
   int before = before_warp(inc, total);
   const int per = (total + G - 1) / G;
   if (p.n_seq <= kThreads && total > 0) {
-    static_assert(kTries == kWarps, "a warp per item size");
-    int items = 0;
-    for (int b = lane; b < p.n_seq; b += 32) items += (counts[b] + per + warp - 1) / (per + warp);
-    items = __reduce_add_sync(0xffffffffu, items);
-    if (lane == 0) ms.fits[warp] = items <= G;
+    static_assert(kTries <= kWarps, "a warp per item size");
+    if (warp < kTries) {
+      int items = 0;
+      for (int b = lane; b < p.n_seq; b += 32) items += (counts[b] + per + warp - 1) / (per + warp);
+      items = __reduce_add_sync(0xffffffffu, items);
+      if (lane == 0) ms.fits[warp] = warp < per && items <= G;
+    }
     __syncthreads();
-    const unsigned fit = __ballot_sync(0xffffffffu, lane < kWarps && ms.fits[lane < kWarps ? lane : 0]);
+    const unsigned fit = __ballot_sync(0xffffffffu, lane < kTries && ms.fits[lane < kTries ? lane : 0]);
     if (fit != 0) {
       const int c = per + __ffs(fit) - 1, k = (n + c - 1) / c;
       int all;

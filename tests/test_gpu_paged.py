@@ -277,6 +277,34 @@ def test_decode_batches_of_every_plan(torch, ds4a, n, f8):
     check_decode(host(o), host(lse), paged.decode(shape, geom, q, raw, comp), [c + 16 for c in comp_rows])
 
 
+@pytest.mark.parametrize("short,long", [(149, 48), (150, 32), (60, 200), (0, 40), (7, 300), (31, 90), (400, 64)])
+def test_decode_shares_one_long_sequence_out(torch, ds4a, short, long):
+    """Many sequences of one tile and a long one: no CTA has more tiles of it than the average and two, or than
+    three where that is two.  (What a call leaves behind the partial results in its workspace: per sequence the first
+    slot and the number of slots.)"""
+    rng = np.random.default_rng(65)
+    n = short + 1
+    comp_rows = [128] * short + [128 * long]
+    comp_rows[short // 2], comp_rows[-1] = comp_rows[-1], comp_rows[short // 2]
+    pages = 16  # of 64 rows, shared by all tables
+    k = rng.standard_normal((pages, 64, D)).astype(np.float16)
+    table = rng.integers(0, pages, (n, 2 * long)).astype(np.int32)
+    geom = [(4 * c, 0, 0, c) for c in comp_rows]
+    q = rng.standard_normal((n, H, D)).astype(np.float16)
+    shape = shape_of()
+    ws = torch.zeros(ds4a.decode_paged_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+    o, lse = ds4a.attn_decode_paged(shape, up(torch, np.array(geom, dtype=np.int32)), up(torch, q), None,
+                                    ds4a.PagedRows(up(torch, k), None, up(torch, table)), want_lse=True, workspace=ws)
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    average = -(-(short + long) // ctas)
+    plan = host(ws[(n + ctas) * H * (4 * D + 8):][:8 * n].view(torch.int32)).reshape(n, 2)
+    assert -(-long // plan[short // 2, 1]) <= average + min(2, average - 1), plan[short // 2]
+    seg = dict(k=k, v=k, table=table)
+    few = sorted({0, short // 2, n - 1})
+    want = paged.decode(shape, [geom[b] for b in few], q[few], None, dict(seg, table=table[few]))
+    check_decode(host(o)[few], host(lse)[few], want, [comp_rows[b] for b in few])
+
+
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("pad_row", [D, 4 * D])
 def test_decode_rows_of_interleaved_layers(torch, ds4a, pad_row, f8):
