@@ -694,7 +694,8 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
  * residual_out.  A group whose m is 0 gets scale 0 and codes 0; one whose m
  * is below 2^-100 may.  The sum of a row's squares is an fp32 number: a row
  * where it overflows (values near 2^60) has y = 0.
- *   n, width    rows, 0 .. 2^30; values per row, a multiple of 8, 8 .. 32768.
+ *   n, width    rows, 0 .. 2^30 (0: nothing is done, whatever the pointers);
+ *               values per row, a multiple of 8, 8 .. 32768.
  *   x_fp32      0: x, residual and residual_out are fp16; 1: fp32.  Finite values.
  *   x, residual, residual_out  [n][width] at their strides (multiples of 16
  *               bytes), 16-byte aligned.  residual may be NULL (h = x);

@@ -383,10 +383,10 @@ ds4a_status ds4a_rmsnorm_fp8(const ds4a_norm *N, ds4a_stream_t stream) {
   if (N->group != 0 && N->group != 32 && N->group != 64 && N->group != 128 && N->group != 256)
     return DS4A_ERR_INVALID_ARG;
   if (!(N->eps >= FLT_MIN) || !std::isfinite(N->eps)) return DS4A_ERR_INVALID_ARG;
+  if (N->n == 0) return DS4A_OK;  // (the pointers of empty tensors say nothing)
   if (N->codes == nullptr && N->y == nullptr) return DS4A_ERR_INVALID_ARG;
   if ((N->codes == nullptr) != (N->scales == nullptr)) return DS4A_ERR_INVALID_ARG;
   if ((N->residual == nullptr) != (N->residual_out == nullptr)) return DS4A_ERR_INVALID_ARG;
-  if (N->n == 0) return DS4A_OK;
   const int64_t row = (N->x_fp32 ? 4LL : 2LL) * N->width;
   const int64_t groups = N->group == 0 ? 1 : (N->width + N->group - 1) / N->group;
   if (N->x == nullptr || !aligned(N->x, 16) || !stride_ok(N->x_stride, row, 16)) return DS4A_ERR_INVALID_ARG;

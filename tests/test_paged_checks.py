@@ -345,6 +345,33 @@ def test_sizes_are_refused_before_devices(call, monkeypatch):
         raises("residual", ds4a.rmsnorm_fp8, x, one, residual=x.float())
 
 
+@pytest.mark.parametrize("call", ["decode", "weights", "evict", "append", "norm", "norm_residual", "norm_y"])
+def test_empty_batches_do_nothing(lib, call, monkeypatch):
+    """No sequences, no rows: empty tensors have no address, and no call refuses them."""
+    monkeypatch.setattr(ds4a, "_on_device", lambda **kw: None)
+    monkeypatch.setattr(ds4a, "_stream", lambda s: ctypes.c_void_p(0))
+    rows = ds4a.PagedRows(torch.zeros((4, 8, D), dtype=F16), None, torch.zeros((0, 3), dtype=I32))
+    q, geom, x = torch.zeros((0, H, D), dtype=F16), torch.zeros((0, 4), dtype=I32), torch.zeros((0, 64), dtype=F16)
+    one = torch.ones(64)
+    if call == "decode":
+        o, lse = ds4a.attn_decode_paged(SHAPE, geom, q, rows, rows, want_lse=True)
+        assert o.shape == (0, H, D) and lse.shape == (0, H)
+    elif call == "weights":
+        assert ds4a.attn_weights_paged(SHAPE, geom, q, rows, torch.zeros((0, H))).shape == (0, 24)
+    elif call == "evict":
+        kept, n_out = ds4a.evict_paged(SHAPE, geom, rows, torch.zeros((0, 24)), 10)
+        assert kept.shape == (0, 10) and n_out.shape == (0,)
+    elif call == "append":
+        ds4a.append_paged(rows, torch.zeros((0, D), dtype=F16), None, torch.zeros(0, dtype=I32))
+    elif call == "norm":
+        codes, scales = ds4a.rmsnorm_fp8(x, one, group=32)
+        assert codes.shape == (0, 64) and scales.shape == (0, 2)
+    elif call == "norm_residual":
+        assert ds4a.rmsnorm_fp8(x, one, residual=x)[2].shape == (0, 64)
+    else:
+        ds4a.prepare_rmsnorm_fp8(x, one, y=torch.zeros((0, 64), dtype=F16))()
+
+
 # ------------------------------------------------------------------ streams
 
 class Streams:
