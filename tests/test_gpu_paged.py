@@ -678,6 +678,41 @@ def test_append_matches_the_oracle(torch, ds4a, f8, shared, n, page, pages):
             assert np.array_equal(host(getattr(dev, name + "_scale")), seg[name + "_scale"])
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("page,pages,slots", [(1, 1, [0]), (4, 2, [7]), (5, 3, [14, -1, 0, 6, 15, 5])])
+def test_append_writes_one_row_and_rows_of_zeros(torch, ds4a, f8, shared, page, pages, slots):
+    """A single row, the pool's first and last slots, and (first) a row of zeros: scale 0, codes 0 over what the slot
+    held; the other slots keep their bytes."""
+    rng = np.random.default_rng(58)
+    seg = make(rng, 1, [page * pages], page, f8, shared)
+    for zero in (False, True):
+        dev = rows_on(torch, ds4a, seg)
+        new = rng.standard_normal((len(slots), 2, D)).astype(np.float16)
+        if zero:
+            new[0] = 0
+        buf = up(torch, new)
+        before = host(dev.k).copy()
+        ds4a.append_paged(dev, buf[:, 0], buf[:, 1], up(torch, np.array(slots, dtype=np.int32)))
+        kept = [s for s in slots if 0 <= s < page * pages]
+        for i, s in enumerate(slots):
+            if s not in kept:
+                continue
+            for j, name in enumerate(("k",) if shared else ("k", "v")):
+                at, row = (s // page, s % page), new[i:i + 1, j]
+                if f8:
+                    c, sc = fp8.quantize_rows(row)
+                    seg[name][at], seg[name + "_scale"][at] = c[0], sc[0]
+                    assert not (zero and i == 0) or (sc[0] == 0 and (c == 0).all())
+                else:
+                    seg[name][at] = row[0]
+        assert len(kept) >= 1 and not np.array_equal(host(dev.k).view(np.uint8), before.view(np.uint8))
+        for name in ("k", "v"):
+            assert np.array_equal(host(getattr(dev, name)).view(np.uint8), seg[name].view(np.uint8))
+            if f8:
+                assert np.array_equal(host(getattr(dev, name + "_scale")), seg[name + "_scale"])
+
+
 def test_append_to_one_row_pool_with_two_scale_arrays(torch, ds4a):
     """K = V rows with a scale array each: both get the new row's scale, and a decode that reads them sees it."""
     rng = np.random.default_rng(57)
