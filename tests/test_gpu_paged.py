@@ -18,6 +18,9 @@ the value, one to fp32 by 2^-24):
 * whole numbers, moved rows, appended rows, residual sums: bit for bit.
 """
 
+import os
+import re
+
 import numpy as np
 import pytest
 
@@ -919,6 +922,49 @@ def test_serving_steps(torch, ds4a, f8, recorded):
         assert np.array_equal(host(dev.k).view(np.uint8), seg["k"].view(np.uint8))
     if graph is not None:
         graph.close()
+
+
+def test_the_documented_serving_step(torch, ds4a):
+    """The README's paged cache and its step, run as they stand: three steps of two sequences at the budget.  A row
+    appended after an eviction starts from weight 0 and not from what its slot's last row received."""
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    (setup,), (step,) = [b for b in blocks if "PagedRows(" in b], [b for b in blocks if "append_paged(" in b]
+    rng = np.random.default_rng(95)
+    n, budget, ratio = 2, 1024, 4
+    pages = budget // 64 + 1
+    pos = budget * ratio + 1
+    tables = rng.permutation(1024)[:n * pages].reshape(n, pages).astype(np.int32)
+    raw_rows = rng.standard_normal((4 * n, 64, D)).astype(np.float16)
+    names = dict(torch=torch, ds4a=ds4a, n_seq=n, comp_table=up(torch, tables), raw_pool=up(torch, raw_rows),
+                 raw_table=up(torch, np.arange(4 * n, dtype=np.int32).reshape(n, 4)), q_pos=pos, n_raw=192,
+                 raw_pos0=pos - 191, n_comp=budget)
+    exec(setup, names)
+    names["pool"].copy_(up(torch, rng.standard_normal((1024, 64, D)).astype(np.float16)))
+    for i in range(1, 4):
+        q, new = rng.standard_normal((n, H, D)).astype(np.float16), rng.standard_normal((n, D)).astype(np.float16)
+        names["geom"][:, 0], names["geom"][:, 2] = pos + ratio * i, pos + ratio * i - 191
+        names.update(q=up(torch, q), new_k=up(torch, new), new_ids=budget + i - 1)
+        w, ids = host(names["weights"]).copy(), host(names["ids"]).copy()
+        geom = host(names["geom"]).copy()
+        k = host(names["pool"]).copy()
+        exec(step, names)
+        assert (geom[:, 3] == budget).all() and (host(names["geom"])[:, 3] == budget).all()
+        w[:, budget], ids[:, budget] = 0, budget + i - 1
+        k[tables[:, budget // 64], budget % 64] = new
+        geom[:, 3] += 1
+        comp, raw = dict(k=k, v=k, table=tables), dict(k=raw_rows, v=raw_rows, table=host(names["raw_table"]))
+        shape = shape_of(ratio)
+        want = paged.decode(shape, geom, q, raw, comp)
+        check_decode(host(names["o"]), host(names["lse"]), want, [budget + 129] * n)
+        after = paged.weights(shape, geom, q, comp, host(names["lse"]), w, 1.0)
+        got_w, got_ids = host(names["weights"]), host(names["ids"])
+        for b in range(n):
+            weight = dict(zip(ids[b, :budget + 1].tolist(), after[b, :budget + 1]))
+            left = got_ids[b, :budget].tolist()
+            assert len(set(left)) == budget and set(left) < set(weight) and budget + i - 1 in left
+            # a score is off by 512 * 2^-23 of scale sum |q||k|, 17 here: 1.04e-3 of a weight
+            np.testing.assert_allclose(got_w[b, :budget], [weight[x] for x in left], rtol=2e-3)
 
 
 def test_two_streams_at_once(torch, ds4a):
