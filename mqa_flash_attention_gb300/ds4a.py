@@ -1106,7 +1106,9 @@ def prepare_append_paged(rows, k, v, slots, *, stream=None) -> PreparedCall:
     if slots.dtype != torch.int32 or slots.dim() != 1 or slots.shape[0] != n or (n > 1 and slots.stride(0) != 1):
         raise ValueError(f"slots must be contiguous int32 [{n}]")
     _on_device(k=k, v=v, slots=slots)
-    args = (ctypes.byref(rows._c), n, kp, vp, max(ks, ROW_BYTES), _ptr(slots), _stream(stream))
+    if n <= 1:
+        ks = ROW_BYTES  # a single row's stride says nothing
+    args = (ctypes.byref(rows._c), n, kp, vp, ks, _ptr(slots), _stream(stream))
     return PreparedCall(lib().ds4a_append_paged, "ds4a_append_paged", args, (rows, k, v, slots, stream))
 
 

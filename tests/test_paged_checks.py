@@ -345,6 +345,29 @@ def test_sizes_are_refused_before_devices(call, monkeypatch):
         raises("residual", ds4a.rmsnorm_fp8, x, one, residual=x.float())
 
 
+def test_rows_repeated_by_stride_are_refused(lib, monkeypatch):
+    """One row expanded to several, or rows that overlap, are not read as rows of their own behind it."""
+    monkeypatch.setattr(ds4a, "_on_device", lambda **kw: None)
+    monkeypatch.setattr(ds4a, "_stream", lambda s: ctypes.c_void_p(0))
+    pool, slots = torch.zeros((4, 8, D), dtype=F16), torch.arange(3, dtype=I32)
+    one, row = ds4a.PagedRows(pool), torch.zeros((1, D), dtype=F16)
+    apart = ds4a.PagedRows(pool, torch.zeros_like(pool))
+    for k in (row.expand(3, D), torch.zeros(4 * D, dtype=F16).as_strided((3, D), (256, 1))):
+        for rows, v in ((one, None), (apart, k)):
+            with pytest.raises(ds4a.Ds4aError) as e:
+                elsewhere(ds4a.append_paged, rows, k, v, slots)
+            assert e.value.status == ds4a.ERR_INVALID_ARG
+    w, geom = torch.zeros((1, 24)), torch.zeros((3, 4), dtype=I32)
+    rows = ds4a.PagedRows(pool, None, torch.zeros((3, 3), dtype=I32))
+    q, lse = torch.zeros((3, H, D), dtype=F16), torch.zeros((3, H))
+    raises("weights must be", ds4a.attn_weights_paged, SHAPE, geom, q, rows, lse, weights=w.expand(3, 24))
+    raises("out must be", ds4a.attn_weights_paged, SHAPE, geom, q, rows, lse, out=w.expand(3, 24))
+    raises("x must be", ds4a.rmsnorm_fp8, torch.zeros((1, 64), dtype=F16).expand(3, 64), torch.ones(64))
+    with pytest.raises(ds4a.Ds4aError) as e:
+        elsewhere(ds4a.attn_decode_paged, SHAPE, geom, q[:1].expand(3, H, D), None, rows)
+    assert e.value.status == ds4a.ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("call", ["decode", "weights", "evict", "append", "norm", "norm_residual", "norm_y"])
 def test_empty_batches_do_nothing(lib, call, monkeypatch):
     """No sequences, no rows: empty tensors have no address, and no call refuses them."""
