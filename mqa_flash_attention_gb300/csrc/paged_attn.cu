@@ -1057,11 +1057,13 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams &p, const Cta
     if (bar_red_or(1, kComputeThreads, bad)) break;
     if (tid < kH) {
       const float lsum = ms.red[0][tid] + ms.red[1][tid] + ms.red[2][tid] + ms.red[3][tid];
-      ms.inv_l[tid] = lsum > 0.f ? 1.f / lsum : 0.f;
+      // No weight at all: o = 0.  (A sum that is NaN is not that: it stays.)
+      const bool none = lsum == 0.f;
+      ms.inv_l[tid] = none ? 0.f : 1.f / lsum;
       if (!whole) {
-        p.ws_ml[slot * kH + tid] = make_float2(lsum > 0.f ? m_ref : -INFINITY, lsum);
+        p.ws_ml[slot * kH + tid] = make_float2(none ? -INFINITY : m_ref, lsum);
       } else if (p.lse != nullptr) {
-        p.lse[(long long)seq * kH + tid] = lsum > 0.f ? (m_ref + log2f(lsum)) * kLn2 : -INFINITY;
+        p.lse[(long long)seq * kH + tid] = none ? -INFINITY : (m_ref + log2f(lsum)) * kLn2;
       }
     }
     bar_sync_id(1, kComputeThreads);
@@ -1344,12 +1346,12 @@ __global__ void __launch_bounds__(32 * WARPS) paged_merge_kernel(const PagedAttn
   };
   auto out_of = [&](int h) { return p.o + b * p.o_stride + (long long)h * kD + 128 * VEC * chunk; };
   auto put_lse = [&](int h, float M, float L) {
-    if (p.lse != nullptr && chunk == 0) p.lse[(long long)b * kH + h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    if (p.lse != nullptr && chunk == 0) p.lse[(long long)b * kH + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   };
   if (HEADS == WARPS && n <= 4 * kMergeLoads / VEC) {
     const int h = h0 + warp;
     const Merged<VEC> r = merge_slots<VEC>(ml_of(h), src_of(h), n, 0, 1);
-    const float inv = r.L > 0.f ? 1.f / r.L : 0.f;
+    const float inv = r.L == 0.f ? 0.f : 1.f / r.L;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) store_half4(out_of(h) + 4 * (lane + 32 * e), r.acc[e], inv);
     if (lane == 0) put_lse(h, r.M, r.L);
@@ -1371,7 +1373,7 @@ __global__ void __launch_bounds__(32 * WARPS) paged_merge_kernel(const PagedAttn
       t[w] = M == -INFINITY ? 0.f : exp2f(wl[w].x - M);
       L = fmaf(t[w], wl[w].y, L);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     for (int v = threadIdx.x; v < 32 * VEC; v += 32 * WARPS) {
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

@@ -336,6 +336,49 @@ def test_decode_of_one_row_is_its_value(torch, ds4a, scale):
     assert np.abs(host(lse)[0] / (-float(np.float32(scale)) * (k * k).sum()) - 1).max() <= 516 * 2.0 ** -23  # products and sums, and eight roundings
 
 
+@pytest.mark.parametrize("rows", [[100], [4000], [100] * 200, [700] * 60, [2000] * 60, [5000] * 9])
+@pytest.mark.parametrize("f8", [False, True])
+def test_decode_hides_no_nan(torch, ds4a, rows, f8):
+    """A NaN in a head's query makes that head's output and log-sum-exp NaN, one in a row that is seen every head's,
+    whether one CTA has the whole sequence or several share it; other heads and sequences stay as they are."""
+    rng = np.random.default_rng(66)
+    n, page = len(rows), 64
+    pages = -(-max(rows) // page)
+    k = up(torch, rng.integers(0, 120, (pages + 1, page, D)).astype(np.uint8) if f8 else
+           rng.standard_normal((pages + 1, page, D)).astype(np.float16))
+    ks = torch.full((pages + 1, page), 0.01, device="cuda") if f8 else None
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(n, 1)
+    b, row = n // 2, rows[n // 2] - 30
+    k[-1] = k[row // page]
+    if ks is not None:
+        ks[-1] = ks[row // page]
+    table[b, row // page] = pages  # sequence b's alone
+    seg = ds4a.PagedRows(k, None, table, k_scale=ks)
+    geom = up(torch, np.array([(4 * r, 0, 0, r) for r in rows], dtype=np.int32))
+    q = up(torch, rng.standard_normal((n, H, D)).astype(np.float16))
+    o, lse = ds4a.attn_decode_paged(shape_of(), geom, q, None, seg, want_lse=True)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    bad = q.clone()
+    bad[b, 5, 17] = float("nan")
+    o2, lse2 = ds4a.attn_decode_paged(shape_of(), geom, bad, None, seg, want_lse=True)
+    assert torch.isnan(o2[b, 5]).all() and torch.isnan(lse2[b, 5])
+    o2[b, 5], lse2[b, 5] = o[b, 5], lse[b, 5]
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    k[-1, row % page, 9] = 0x7F if f8 else float("nan")
+    o3, lse3 = ds4a.attn_decode_paged(shape_of(), geom, q, None, seg, want_lse=True)
+    assert torch.isnan(o3[b]).all() and torch.isnan(lse3[b]).all()
+    o3[b], lse3[b] = o[b], lse[b]
+    assert torch.equal(o3, o) and torch.equal(lse3, lse)
+
+
+@pytest.mark.parametrize("n", [1, 40, 70])
+def test_decode_without_any_segment(torch, ds4a, n):
+    q = torch.ones((n, H, D), dtype=torch.float16, device="cuda")
+    geom = torch.full((n, 4), 9, dtype=torch.int32, device="cuda")
+    o, lse = ds4a.attn_decode_paged(shape_of(), geom, q, None, None, out=torch.full_like(q, 3.0), want_lse=True)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
 def test_decode_pages_past_32_bit_offsets(torch, ds4a):
     """A 5 GB pool whose used pages lie at its end, read through both tables by two sequences (shared pages)."""
     rng = np.random.default_rng(12)
