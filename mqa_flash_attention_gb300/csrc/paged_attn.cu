@@ -71,7 +71,7 @@
 // some 7,600 cycles from one tile's first load to the next's: 1,100 until the first
 // part is there and 2,200 for 128 KB at the 64 bytes a clock of an SM's port to
 // L2, the last part's QK^T 630, softmax 1,800, PV 430 to the first freed stage; 64
-// sequences take 41 us, 24 of E4M3 rows 44 us, where widening (read once, written
+// sequences take 40 us, 24 of E4M3 rows 43 us, where widening (read once, written
 // twice as wide) and the products' operands share the bandwidth of shared memory.
 // Weights of 16 sequences of E4M3 rows, 88 MB: 26 us, bound by the same.
 #include "attn_params.h"
@@ -514,9 +514,8 @@ __device__ __forceinline__ void load_role(const PagedAttnParams &p, const CtaPla
   float b_ks[kMine], b_vs[kMine];
   int b_seq = 0, b_flags = 0, b_base = 0, b_end = 0;
 
-  // A field of segment sg: a choice of two constants.  (Indexed loads of the
-  // parameters made the list of an E4M3 tile, two rows a thread, take 3,000 cycles
-  // and not 1,100: weights of 16 sequences 32 us and not 26.)
+  // A field of segment sg: a choice of two constants (weights of 16 sequences of
+  // E4M3 rows 25.7 us; the same with indexed loads of the parameters).
   auto of = [&](int sg, auto field) { return sg != 0 ? p.seg[1].*field : p.seg[0].*field; };
   auto fetch_pages = [&]() {
     a_seq = w.b;
@@ -915,8 +914,8 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const C
 // While the reference holds (nearly always after a sequence's first tile) a
 // tile needs no maximum over its rows: one vote of the block that no score is
 // over.  kLift and kHold share out fp16's 15 bits above 1: 64 sequences of fp16
-// and 24 of E4M3 rows take 41.3 and 43.9 us with 7 + 8, 41.5 and 44.0 with 10 +
-// 5, 43.5 and 47.0 with 12 + 3, where the reference moves often.  kNoRef stands for no reference yet: any score passes it, and absent
+// and 24 of E4M3 rows take 0.5% and 0.2% longer with 10 + 5 than with 7 + 8, 5%
+// and 7% longer with 12 + 3, where the reference moves often.  kNoRef stands for no reference yet: any score passes it, and absent
 // rows (-inf) get weight 0 under it.
 constexpr float kLift = 10.f, kHold = 5.f;
 constexpr float kNoRef = -3e38f;

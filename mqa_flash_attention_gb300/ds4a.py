@@ -969,7 +969,8 @@ def _bytes_of(workspace, need, q, stream):
 
 
 def decode_paged_workspace_bytes(n_seq: int, shape=None, raw=None, comp=None) -> int:
-    """Workspace bytes of :func:`attn_decode_paged` for a batch (of any lengths)."""
+    """Workspace bytes of :func:`attn_decode_paged` for ``n_seq`` sequences on the
+    current device, whatever the shape and the segments (which need not be given)."""
     return int(lib().ds4a_attn_decode_paged_workspace_size(int(n_seq)))
 
 
