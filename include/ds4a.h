@@ -552,8 +552,8 @@ typedef struct {
  * ds4a_attn_decode_paged - one decode step for n_seq sequences, as
  * ds4a_attn_decode_batch, over paged rows: sequence b's result is that of
  * ds4a_attn_decode on its own layout and rows (rows of absent pages left
- * out).  A sequence that sees no row gets o = 0 and lse = -inf; a NaN in a
- * head's query, or in a row that is seen, makes its o and lse NaN.
+ * out).  A sequence that sees no row gets o = 0 and lse = -inf.  A NaN in a
+ * head's query, or in a K row that is seen, makes the head's o and lse NaN.
  *   shape       ratio, window and scale shared by the batch (other fields are
  *               ignored); scale below 2.3e38 in size.
  *   seq_geom    device int32 [n_seq][4], 16-byte aligned: per sequence

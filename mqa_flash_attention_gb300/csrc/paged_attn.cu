@@ -915,8 +915,9 @@ __device__ __forceinline__ void mma_role_paged(const PagedAttnParams &p, const C
 // tile needs no maximum over its rows: one vote of the block that no score is
 // over.  kLift and kHold share out fp16's 15 bits above 1: 64 sequences of fp16
 // and 24 of E4M3 rows take 0.5% and 0.2% longer with 10 + 5 than with 7 + 8, 5%
-// and 7% longer with 12 + 3, where the reference moves often.  kNoRef stands for no reference yet: any score passes it, and absent
-// rows (-inf) get weight 0 under it.
+// and 7% longer with 12 + 3, where the reference moves often.  kNoRef stands for
+// no reference yet: any score passes it, and absent rows (-inf) get weight 0
+// under it.
 constexpr float kLift = 10.f, kHold = 5.f;
 constexpr float kNoRef = -3e38f;
 
