@@ -684,6 +684,106 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
                               int64_t new_row_stride, const int32_t *slots, ds4a_stream_t stream);
 
 /*
+ * A serving step with several new tokens per sequence: drafted tokens of which
+ * the model's choices accept some, or runs of prompts of different lengths. The
+ * tokens of all sequences are packed: those of sequence b are first[b] ..
+ * first[b + 1] - 1 of n_tok (device int32 [n_seq + 1], ascending; clamped to
+ * 0 .. n_tok).  The calls of a step, in order: ds4a_page_tables (room for the new
+ * rows, and their slots), ds4a_append_paged, ds4a_attn_tree_paged,
+ * ds4a_tree_accept, ds4a_commit_paged, ds4a_page_tables (gives back).  The
+ * sources define no such step: the readings are the library's own.
+ */
+
+/*
+ * ds4a_page_tables - page tables and slots from the rows that each sequence
+ * has and wants, built on the device.  In sequence b's table (in the numbering
+ * before the call) rows 0 .. have-1 are in use.  The call drops the whole pages
+ * among its first drop rows (never past have), gives back the pages behind row
+ * want - 1, and takes pages up to row want - 1; the kept entries move down by
+ * the dropped pages, so row i becomes row i - page_rows * (pages dropped).
+ *   Free list: free_pages[0 .. n_free-1].  Pages that are given back are put at
+ *   its end, by sequence, each one's dropped pages first, by entry; then pages
+ *   are taken from its end, by sequence and entry.  An entry outside
+ *   [0, n_pages) names no page and is not given back.  Where the list runs out,
+ *   the entries that got no page are -1 and n_short counts them (0 else).
+ *   Entries up to the last one used before or after that name no row now are
+ *   set to -1; those beyond are left as they were.
+ *   Slots: the new rows have .. want-1 of all sequences, packed: row j of
+ *   sequence b's is slots[first[b] + j] = page * page_rows + row in page, or -1
+ *   where it has no page; slots from first[n_seq] on are -1 (a padded batch).
+ *   New rows beyond n_slots get no slot, and first is clamped to n_slots.
+ *   X->table     device int32 [n_seq][max_pages], at table_stride bytes
+ *                (a multiple of 4, >= 4 * max_pages), read and written.
+ *   page_rows, n_pages  of the pool; page_rows * max_pages <= 2^30 and
+ *                page_rows * n_pages < 2^31.
+ *   free_pages, n_free  device int32 [n_pages] and [1], read and written.
+ *   have, want   device int32 [n_seq], clamped to 0 .. what the table can hold
+ *                (want: and what the dropped pages make room for).
+ *   drop         device int32 [n_seq], or NULL: nothing is dropped.
+ *   slots        device int32 [n_slots]; n_slots == 0: not wanted.
+ *   first        device int32 [n_seq + 1] out.   n_short  device int32 [1] out.
+ * No two of these ranges may overlap, but have, want and drop one another.
+ *   workspace    256-byte aligned, at least ds4a_page_tables_workspace_size()
+ *                bytes; need not be initialised; not shared by calls in flight
+ *                at the same time.
+ * All results are whole numbers and exact.  n_seq == 0 does nothing.
+ */
+typedef struct {
+  int32_t *table;
+  int64_t table_stride;
+  int32_t max_pages, page_rows, n_pages;
+  int32_t *free_pages, *n_free;
+  const int32_t *have, *want, *drop;
+  int32_t *slots;
+  int32_t n_slots;
+  int32_t *first, *n_short;
+} ds4a_page_lists;
+
+size_t ds4a_page_tables_workspace_size(int32_t n_seq);
+ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *workspace, size_t workspace_bytes,
+                             ds4a_stream_t stream);
+
+/*
+ * ds4a_tree_accept - the path of drafted tokens that agree with the model.
+ * Node t of a sequence (counted within it) holds token[t]; target[t] is the
+ * token chosen to follow it.  The path starts at the lowest root whose token is
+ * prev[b] (the token chosen after the cached rows; prev NULL: at the lowest
+ * root, whatever its token), and goes on, from each node, to its lowest child
+ * whose token is the node's target.
+ *   parent       device int32 [n_tok], counted within the sequence; a node
+ *                whose entry is not an earlier node (negative, or itself or later) is a
+ *                root.  NULL: each sequence is a chain.
+ *   token, target  device int32 [n_tok].   prev  device int32 [n_seq] or NULL.
+ *   path         device int32 [n_seq][width] out at path_stride bytes (a
+ *                multiple of 4): the accepted nodes, then -1.  A path ends at width nodes.
+ *   n_accepted, next  device int32 [n_seq] out: nodes accepted, and the target of
+ *                the last one (prev[b], or -1 without it, when there is none).
+ * Outputs must not overlap one another or an input.
+ */
+ds4a_status ds4a_tree_accept(int32_t n_seq, int32_t n_tok, const int32_t *first, const int32_t *parent,
+                             const int32_t *token, const int32_t *target, const int32_t *prev, int32_t *path,
+                             int64_t path_stride, int32_t width, int32_t *n_accepted, int32_t *next,
+                             ds4a_stream_t stream);
+
+/*
+ * ds4a_commit_paged - moves the rows of accepted tokens behind the cached ones,
+ * in place: row n_raw + path[b][i] of sequence b goes to row n_raw + i, for
+ * i < n_accepted[b] (with its scales in an E4M3 pool).  One call per layer.
+ *   rows         the raw segment (k and v are written).  The pages of these
+ *                sequences must be theirs alone: each page in one table, once.
+ *                A move from or to a row without a page copies nothing.
+ *   seq_geom     device int32 [n_seq][4], 16-byte aligned: n_raw (its second
+ *                number) is the one before the step; the others are ignored.
+ *   path         device int32 [n_seq][width] at path_stride bytes, as
+ *                ds4a_tree_accept gave it: ascending, path[i] >= i (an entry
+ *                path[i] <= i moves nothing).
+ *   n_accepted   device int32 [n_seq], clamped to 0 .. width.
+ */
+ds4a_status ds4a_commit_paged(int32_t n_seq, const ds4a_paged_rows *rows, const int32_t *seq_geom,
+                              const int32_t *path, int64_t path_stride, int32_t width, const int32_t *n_accepted,
+                              ds4a_stream_t stream);
+
+/*
  * ds4a_rmsnorm_fp8 - root-mean-square norm of a row, with the residual's
  * addition, quantised to E4M3 for the product that follows ([P2]
  * "Whole-Model Graph Execution": Q/K/V projections with a fused RMS norm, and

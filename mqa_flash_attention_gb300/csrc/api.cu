@@ -15,6 +15,7 @@
 #include "host.h"
 #include "internal.h"
 #include "paged_params.h"
+#include "step_params.h"
 
 // Device error word: set by a kernel whose bounded wait ran out.  Its address
 // is looked up once per device and handed to the kernels as a parameter.
@@ -1181,6 +1182,7 @@ ds4a_status ds4a_graph_begin(ds4a_stream_t stream) {
       DS4A_CUDA_TRY(ds4a::preload_indexer_kernels());
       DS4A_CUDA_TRY(ds4a::preload_compressor_kernels());
       DS4A_CUDA_TRY(ds4a::preload_norm_kernels());
+      DS4A_CUDA_TRY(ds4a::preload_step_kernels());
       d->loaded = true;
     }
   }

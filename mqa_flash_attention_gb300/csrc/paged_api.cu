@@ -10,6 +10,7 @@
 #include "host.h"
 #include "internal.h"
 #include "paged_params.h"
+#include "step_params.h"
 
 namespace {
 
@@ -19,6 +20,7 @@ using ds4a::PagedSeg;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int64_t kMostBytes = 1LL << 39;  // of any stride
 constexpr int32_t kMostRows = 1 << 30;     // rows of a sequence
+constexpr int32_t kMostSeqs = 1 << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 
 cudaStream_t as_cuda(ds4a_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -38,6 +40,19 @@ bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 // A written range against one read: the same range at the same stride, or apart.
 bool same_or_apart(Span a, int64_t stride_a, Span b, int64_t stride_b) {
   return !meet(a, b) || (a.lo == b.lo && stride_a == stride_b);
+}
+
+// n whole numbers in a row (none: a range that meets nothing).
+Span ints(const int32_t *p, int64_t n) { return p != nullptr && n > 0 ? span(p, 1, 0, 4 * n) : Span{0, 0}; }
+// Every output apart from every input and from every other output.
+bool apart(const Span *out, int n_out, const Span *in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (meet(out[i], in[j])) return false;
+    for (int j = i + 1; j < n_out; ++j)
+      if (meet(out[i], out[j])) return false;
+  }
+  return true;
 }
 
 bool has_rows(const ds4a_paged_rows *r) { return r->max_pages > 0; }
@@ -375,6 +390,122 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
   p.slots = slots;
   p.n = n;
   return ds4a::host_launched(ds4a::launch_append(p, as_cuda(stream)));
+}
+
+size_t ds4a_page_tables_workspace_size(int32_t n_seq) {
+  return n_seq <= 0 ? 0 : ((size_t)n_seq + 1) * sizeof(ds4a::PagePlan);
+}
+
+ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *workspace, size_t workspace_bytes,
+                             ds4a_stream_t stream) {
+  if (n_seq < 0 || X == nullptr) return DS4A_ERR_INVALID_ARG;
+  if (n_seq == 0) return DS4A_OK;
+  if (n_seq > kMostSeqs || X->max_pages < 1 || X->page_rows < 1 || X->n_pages < 1 || X->n_slots < 0 ||
+      (int64_t)X->max_pages * X->page_rows > kMostRows || (int64_t)X->n_pages * X->page_rows > INT32_MAX)
+    return DS4A_ERR_INVALID_ARG;
+  if (X->table == nullptr || !aligned(X->table, 4) || !stride_ok(X->table_stride, 4LL * X->max_pages, 4))
+    return DS4A_ERR_INVALID_ARG;
+  for (const int32_t *p : {(const int32_t *)X->free_pages, (const int32_t *)X->n_free, X->have, X->want,
+                           (const int32_t *)X->first, (const int32_t *)X->n_short})
+    if (p == nullptr || !aligned(p, 4)) return DS4A_ERR_INVALID_ARG;
+  if (!aligned(X->drop, 4) || !aligned(X->slots, 4) || (X->n_slots > 0 && X->slots == nullptr))
+    return DS4A_ERR_INVALID_ARG;
+  const Span out[6] = {span(X->table, n_seq, X->table_stride, 4LL * X->max_pages), ints(X->free_pages, X->n_pages),
+                       ints(X->n_free, 1), ints(X->slots, X->n_slots), ints(X->first, (int64_t)n_seq + 1),
+                       ints(X->n_short, 1)};
+  const Span in[3] = {ints(X->have, n_seq), ints(X->want, n_seq), ints(X->drop, n_seq)};
+  if (!apart(out, 6, in, 3)) return DS4A_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < ds4a_page_tables_workspace_size(n_seq))
+    return DS4A_ERR_WORKSPACE;
+  HostDevice d;
+  const ds4a_status st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::PageTablesParams p;
+  p.n_seq = n_seq;
+  p.max_pages = X->max_pages;
+  p.page_rows = X->page_rows;
+  p.n_pages = X->n_pages;
+  p.n_slots = X->n_slots;
+  p.table = X->table;
+  p.table_stride = X->table_stride / 4;
+  p.free_pages = X->free_pages;
+  p.n_free = X->n_free;
+  p.slots = X->slots;
+  p.first = X->first;
+  p.n_short = X->n_short;
+  p.have = X->have;
+  p.want = X->want;
+  p.drop = X->drop;
+  p.plan = static_cast<ds4a::PagePlan *>(workspace);
+  return ds4a::host_launched(ds4a::launch_page_tables(p, as_cuda(stream)));
+}
+
+ds4a_status ds4a_tree_accept(int32_t n_seq, int32_t n_tok, const int32_t *first, const int32_t *parent,
+                             const int32_t *token, const int32_t *target, const int32_t *prev, int32_t *path,
+                             int64_t path_stride, int32_t width, int32_t *n_accepted, int32_t *next,
+                             ds4a_stream_t stream) {
+  if (n_seq < 0 || n_tok < 0 || width < 0) return DS4A_ERR_INVALID_ARG;
+  if (n_seq == 0) return DS4A_OK;
+  if (n_seq > kMostSeqs || n_tok > kMostRows || width > kMostRows) return DS4A_ERR_INVALID_ARG;
+  for (const int32_t *p : {first, (const int32_t *)n_accepted, (const int32_t *)next})
+    if (p == nullptr || !aligned(p, 4)) return DS4A_ERR_INVALID_ARG;
+  if (n_tok > 0 && (token == nullptr || target == nullptr)) return DS4A_ERR_INVALID_ARG;
+  if (!aligned(parent, 4) || !aligned(token, 4) || !aligned(target, 4) || !aligned(prev, 4))
+    return DS4A_ERR_INVALID_ARG;
+  if (width > 0 && (path == nullptr || !aligned(path, 4) || !stride_ok(path_stride, 4LL * width, 4)))
+    return DS4A_ERR_INVALID_ARG;
+  const Span out[3] = {span(path, width > 0 ? n_seq : 0, path_stride, 4LL * width), ints(n_accepted, n_seq),
+                       ints(next, n_seq)};
+  const Span in[5] = {ints(first, (int64_t)n_seq + 1), ints(parent, n_tok), ints(token, n_tok), ints(target, n_tok),
+                      ints(prev, n_seq)};
+  if (!apart(out, 3, in, 5)) return DS4A_ERR_INVALID_ARG;
+  HostDevice d;
+  const ds4a_status st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::AcceptParams p;
+  p.n_seq = n_seq;
+  p.n_tok = n_tok;
+  p.width = width;
+  p.first = first;
+  p.parent = parent;
+  p.token = token;
+  p.target = target;
+  p.prev = prev;
+  p.path = path;
+  p.path_stride = path_stride / 4;
+  p.n_accepted = n_accepted;
+  p.next = next;
+  return ds4a::host_launched(ds4a::launch_accept(p, as_cuda(stream)));
+}
+
+ds4a_status ds4a_commit_paged(int32_t n_seq, const ds4a_paged_rows *rows, const int32_t *seq_geom,
+                              const int32_t *path, int64_t path_stride, int32_t width, const int32_t *n_accepted,
+                              ds4a_stream_t stream) {
+  if (n_seq < 0 || rows == nullptr || width < 0) return DS4A_ERR_INVALID_ARG;
+  if (n_seq == 0 || width == 0) return DS4A_OK;
+  if (n_seq > kMostSeqs || width > kMostRows) return DS4A_ERR_INVALID_ARG;
+  if (rows->max_pages < 1 || !pool_ok(rows, true) || !table_ok(rows)) return DS4A_ERR_INVALID_ARG;
+  // K and V apart have a scale array each.
+  const int64_t scales = 4LL * rows->page_rows;
+  if (rows->k != rows->v && rows->k_scale != nullptr &&
+      meet(span(rows->k_scale, rows->n_pages, scales, scales), span(rows->v_scale, rows->n_pages, scales, scales)))
+    return DS4A_ERR_INVALID_ARG;
+  if (seq_geom == nullptr || !aligned(seq_geom, 16) || n_accepted == nullptr || !aligned(n_accepted, 4))
+    return DS4A_ERR_INVALID_ARG;
+  if (path == nullptr || !aligned(path, 4) || !stride_ok(path_stride, 4LL * width, 4)) return DS4A_ERR_INVALID_ARG;
+  HostDevice d;
+  const ds4a_status st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::CommitParams p;
+  p.rows = seg_of(rows);
+  p.n_seq = n_seq;
+  p.width = width;
+  p.geom = reinterpret_cast<const int4 *>(seq_geom);
+  p.path = path;
+  p.path_stride = path_stride / 4;
+  p.n_accepted = n_accepted;
+  return ds4a::host_launched(ds4a::launch_commit(p, as_cuda(stream)));
 }
 
 ds4a_status ds4a_rmsnorm_fp8(const ds4a_norm *N, ds4a_stream_t stream) {

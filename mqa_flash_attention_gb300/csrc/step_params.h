@@ -1,0 +1,51 @@
+// Launch parameters of the kernels of a step with several new tokens per
+// sequence, shared by the host code that fills them and by the kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "paged_params.h"
+
+namespace ds4a {
+
+// Where a sequence's tables stand: pages it needs in all sequences before it,
+// and new rows there (workspace of the page tables).
+struct PagePlan {
+  long long pages, rows;
+};
+
+struct PageTablesParams {
+  int n_seq, max_pages, page_rows, n_pages, n_slots;
+  int32_t *table;
+  long long table_stride;  // elements
+  int32_t *free_pages, *n_free, *slots, *first, *n_short;
+  const int32_t *have, *want, *drop;
+  PagePlan *plan;          // workspace: [n_seq + 1]; the last one: the list's top before any page is taken, all new rows
+};
+cudaError_t launch_page_tables(const PageTablesParams &p, cudaStream_t s);
+
+struct AcceptParams {
+  int n_seq, n_tok, width;
+  const int32_t *first, *parent, *token, *target, *prev;
+  int32_t *path;
+  long long path_stride;   // elements
+  int32_t *n_accepted, *next;
+};
+cudaError_t launch_accept(const AcceptParams &p, cudaStream_t s);
+
+struct CommitParams {
+  PagedSeg rows;
+  int n_seq, width;
+  const int4 *geom;
+  const int32_t *path;
+  long long path_stride;   // elements
+  const int32_t *n_accepted;
+};
+cudaError_t launch_commit(const CommitParams &p, cudaStream_t s);
+
+cudaError_t preload_step_kernels();
+
+}  // namespace ds4a

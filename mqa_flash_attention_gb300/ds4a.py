@@ -96,6 +96,15 @@ class Norm(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64)]
 
 
+class PageLists(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+                ("page_rows", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+                ("have", ctypes.c_void_p), ("want", ctypes.c_void_p), ("drop", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int32),
+                ("first", ctypes.c_void_p), ("n_short", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -189,6 +198,14 @@ def lib() -> ctypes.CDLL:
         L.ds4a_device_error_word.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         L.ds4a_selftest_wait_timeout.restype = st
         L.ds4a_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
+        L.ds4a_page_tables_workspace_size.restype = ctypes.c_size_t
+        L.ds4a_page_tables_workspace_size.argtypes = [i32]
+        L.ds4a_page_tables.restype = st
+        L.ds4a_page_tables.argtypes = [i32, ctypes.POINTER(PageLists), vp, ctypes.c_size_t, vp]
+        L.ds4a_tree_accept.restype = st
+        L.ds4a_tree_accept.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, vp]
+        L.ds4a_commit_paged.restype = st
+        L.ds4a_commit_paged.argtypes = [i32, ctypes.POINTER(PagedSegment), vp, vp, i64, i32, vp, vp]
         L.ds4a_graph_begin.restype = st
         L.ds4a_graph_begin.argtypes = [vp]
         L.ds4a_graph_end.restype = st
@@ -1118,6 +1135,127 @@ def append_paged(rows, k, v, slots, *, stream=None) -> None:
     a pool (slot = page * page_rows + row in page; entries outside the pool
     write nothing), quantised when it is an E4M3 pool."""
     prepare_append_paged(rows, k, v, slots, stream=stream)()
+
+
+# ------------------------------------------------------------------ a step with several new tokens per sequence
+
+def _ints(t, name, n, optional=False):
+    """A contiguous int32 tensor of at least ``n`` numbers on the current device -> its pointer."""
+    import torch
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < n or (t.shape[0] > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous int32 [>= {n}]")
+    _on_device(**{name: t})
+    return _ptr(t)
+
+
+def page_tables_workspace_bytes(n_seq: int) -> int:
+    return int(lib().ds4a_page_tables_workspace_size(int(n_seq)))
+
+
+def prepare_page_tables(table, free_pages, n_free, have, want, page_rows, *, drop=None, slots, first, n_short,
+                        workspace=None, stream=None) -> PreparedCall:
+    """:func:`page_tables` on fixed buffers, as a :class:`PreparedCall`."""
+    import torch
+    B = have.shape[0]
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] < B or table.shape[1] < 1 \
+            or (table.shape[1] > 1 and table.stride(1) != 1) \
+            or (table.shape[0] > 1 and table.stride(0) < table.shape[1]):
+        raise ValueError(f"table must be int32 [>= {B}, max_pages] with contiguous rows")
+    _on_device(table=table)
+    n_pages = free_pages.shape[0]
+    X = PageLists(_ptr(table), max(table.stride(0), table.shape[1]) * 4, table.shape[1], int(page_rows), n_pages,
+                  _ints(free_pages, "free_pages", n_pages), _ints(n_free, "n_free", 1), _ints(have, "have", B),
+                  _ints(want, "want", B), _ints(drop, "drop", B, True), _ints(slots, "slots", 0, True),
+                  0 if slots is None else slots.shape[0], _ints(first, "first", B + 1), _ints(n_short, "n_short", 1))
+    workspace, nbytes = _bytes_of(workspace, page_tables_workspace_bytes(B), table, stream)
+    args = (B, ctypes.byref(X), _ptr(workspace), nbytes, _stream(stream))
+    return PreparedCall(lib().ds4a_page_tables, "ds4a_page_tables", args,
+                        (X, table, free_pages, n_free, have, want, drop, slots, first, n_short, workspace, stream))
+
+
+def page_tables(table, free_pages, n_free, have, want, page_rows, *, drop=None, slots=None, n_slots=0, first=None,
+                n_short=None, workspace=None, stream=None):
+    """Room for ``want`` rows per sequence (int32 [B]) that has ``have``: pages
+    are taken from, or given back to, the free list ``free_pages`` int32
+    [n_pages] (``n_free`` int32 [1] of it in use), the whole pages among the
+    first ``drop`` rows leave the ``table`` int32 [B, max_pages].  All four are
+    updated in place.  Returns (slots, first, n_short): the slots of the new
+    rows, packed, -1 behind them (``n_slots`` of them when made here); where each
+    sequence's begin, int32 [B + 1]; how many pages were lacking, int32 [1]."""
+    import torch
+    dev = table.device
+    if slots is None:
+        slots = _new(stream, torch.empty, (int(n_slots),), dtype=torch.int32, device=dev)
+    if first is None:
+        first = _new(stream, torch.empty, (have.shape[0] + 1,), dtype=torch.int32, device=dev)
+    if n_short is None:
+        n_short = _new(stream, torch.empty, (1,), dtype=torch.int32, device=dev)
+    prepare_page_tables(table, free_pages, n_free, have, want, page_rows, drop=drop, slots=slots, first=first,
+                        n_short=n_short, workspace=workspace, stream=stream)()
+    return slots, first, n_short
+
+
+def prepare_tree_accept(first, token, target, *, parent=None, prev=None, path, n_accepted, next_token,
+                        stream=None) -> PreparedCall:
+    """:func:`tree_accept` on fixed buffers, as a :class:`PreparedCall`."""
+    import torch
+    B, n = first.shape[0] - 1, token.shape[0]
+    if B < 0:
+        raise ValueError("first must be int32 [n_seq + 1]")
+    if path is None:
+        raise ValueError("path is missing")
+    pp, ps = _per_row(path, "path", B, path.shape[1], torch.int32)
+    args = (B, n, _ints(first, "first", B + 1), _ints(parent, "parent", n, True), _ints(token, "token", n),
+            _ints(target, "target", n), _ints(prev, "prev", B, True), pp, max(ps, path.shape[1] * 4), path.shape[1],
+            _ints(n_accepted, "n_accepted", B), _ints(next_token, "next_token", B), _stream(stream))
+    return PreparedCall(lib().ds4a_tree_accept, "ds4a_tree_accept", args,
+                        (first, token, target, parent, prev, path, n_accepted, next_token, stream))
+
+
+def tree_accept(first, token, target, *, parent=None, prev=None, width=None, path=None, n_accepted=None,
+                next_token=None, stream=None):
+    """The accepted path of each sequence's drafted tokens: nodes ``first[b] ..``
+    hold ``token`` int32 [n_tok], ``target`` is what the model chose after each,
+    ``parent`` (None: chains) counts within the sequence, ``prev`` int32 [B] is
+    what it chose after the cached rows.  Returns (path int32 [B, width], -1
+    behind it; n_accepted int32 [B]; next_token int32 [B])."""
+    import torch
+    B, dev = first.shape[0] - 1, first.device
+    if path is None:
+        path = _new(stream, torch.empty, (B, int(token.shape[0] if width is None else width)), dtype=torch.int32,
+                    device=dev)
+    if n_accepted is None:
+        n_accepted = _new(stream, torch.empty, (B,), dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = _new(stream, torch.empty, (B,), dtype=torch.int32, device=dev)
+    prepare_tree_accept(first, token, target, parent=parent, prev=prev, path=path, n_accepted=n_accepted,
+                        next_token=next_token, stream=stream)()
+    return path, n_accepted, next_token
+
+
+def prepare_commit_paged(rows, seq_geom, path, n_accepted, *, stream=None) -> PreparedCall:
+    """:func:`commit_paged` on fixed buffers, as a :class:`PreparedCall`."""
+    import torch
+    B = seq_geom.shape[0]
+    _paged_geom(seq_geom, B)
+    rows._check("rows", B)
+    if path is None:
+        raise ValueError("path is missing")
+    pp, ps = _per_row(path, "path", B, path.shape[1], torch.int32)
+    args = (B, ctypes.byref(rows._c), _ptr(seq_geom), pp, max(ps, path.shape[1] * 4), path.shape[1],
+            _ints(n_accepted, "n_accepted", B), _stream(stream))
+    return PreparedCall(lib().ds4a_commit_paged, "ds4a_commit_paged", args, (rows, seq_geom, path, n_accepted, stream))
+
+
+def commit_paged(rows, seq_geom, path, n_accepted, *, stream=None) -> None:
+    """Moves the accepted tokens' rows (raw row ``n_raw + path[b, i]``, n_raw of
+    ``seq_geom`` as before the step) behind the cached ones (to ``n_raw + i``),
+    in place; with their scales in an E4M3 pool."""
+    prepare_commit_paged(rows, seq_geom, path, n_accepted, stream=stream)()
 
 
 # ------------------------------------------------------------------ norm

@@ -1,0 +1,147 @@
+"""Refusals of the calls of a step with several new tokens, without a GPU, and
+the step's oracle by hand."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from mqa_flash_attention_gb300 import ds4a
+from oracle import step
+from test_paged_checks import AT, I32, elsewhere, lib, needs_no_gpu, passes, raises, seg  # noqa: F401
+
+
+def lists(**kw):
+    base = dict(table=AT, table_stride=32, max_pages=8, page_rows=16, n_pages=100, free_pages=2 * AT, n_free=3 * AT,
+                have=4 * AT, want=5 * AT, drop=None, slots=6 * AT, n_slots=50, first=7 * AT, n_short=8 * AT)
+    base.update(kw)
+    return ds4a.PageLists(*[base[n] for n, _ in ds4a.PageLists._fields_])
+
+
+def pages(lib, n=3, ws=1 << 30, nbytes=1 << 20, **kw):
+    return elsewhere(lib.ds4a_page_tables, n, ctypes.byref(lists(**kw)), ws, nbytes, None)
+
+
+@needs_no_gpu
+def test_page_tables_arguments_are_checked(lib):
+    assert passes(pages(lib)) and passes(pages(lib, drop=9 * AT)) and passes(pages(lib, slots=None, n_slots=0))
+    assert passes(pages(lib, want=4 * AT, drop=4 * AT))
+    assert pages(lib, n=0) == ds4a.OK
+    for bad in (dict(n=-1), dict(n=(1 << 20) + 1), dict(table=None), dict(table=AT + 2), dict(table_stride=28),
+                dict(table_stride=34), dict(max_pages=0), dict(page_rows=0), dict(n_pages=0), dict(n_slots=-1),
+                dict(max_pages=1 << 10, table_stride=1 << 12, page_rows=(1 << 20) + 1, n_pages=1),
+                dict(page_rows=1 << 16, n_pages=1 << 15), dict(free_pages=None), dict(n_free=None), dict(have=None),
+                dict(want=None), dict(first=None), dict(n_short=None), dict(slots=None), dict(have=AT * 4 + 1),
+                dict(drop=AT * 9 + 2), dict(slots=6 * AT + 1), dict(first=7 * AT + 3),
+                # ranges that overlap
+                dict(have=AT + 64), dict(slots=5 * AT + 8), dict(free_pages=6 * AT + 196), dict(n_free=2 * AT + 396),
+                dict(n_short=7 * AT + 12), dict(first=AT + 92), dict(drop=8 * AT)):
+        assert pages(lib, **bad) == ds4a.ERR_INVALID_ARG, bad
+    need = lib.ds4a_page_tables_workspace_size(3)
+    assert need > 0 and lib.ds4a_page_tables_workspace_size(0) == 0
+    for bad in (dict(ws=None), dict(ws=AT + 64), dict(nbytes=need - 1)):
+        assert pages(lib, **bad) == ds4a.ERR_WORKSPACE, bad
+
+
+def accept(lib, n=3, n_tok=20, first=AT, parent=2 * AT, token=3 * AT, target=4 * AT, prev=5 * AT, path=6 * AT, stride=40,
+           width=10, count=7 * AT, nxt=8 * AT):
+    return elsewhere(lib.ds4a_tree_accept, n, n_tok, first, parent, token, target, prev, path, stride, width, count, nxt,
+                     None)
+
+
+@needs_no_gpu
+def test_accept_arguments_are_checked(lib):
+    assert passes(accept(lib)) and passes(accept(lib, parent=None, prev=None))
+    assert passes(accept(lib, width=0, path=None, stride=0)) and passes(accept(lib, n_tok=0, token=None, target=None))
+    assert passes(accept(lib, token=4 * AT))
+    assert accept(lib, n=0) == ds4a.OK
+    for bad in (dict(n=-1), dict(n_tok=-1), dict(width=-1), dict(first=None), dict(first=AT + 2), dict(token=None),
+                dict(target=None), dict(parent=AT * 2 + 1), dict(token=AT * 3 + 2), dict(prev=5 * AT + 2),
+                dict(path=None), dict(path=6 * AT + 2), dict(stride=36), dict(stride=42), dict(count=None), dict(nxt=None),
+                dict(count=7 * AT + 1), dict(path=2 * AT + 76), dict(count=AT + 12), dict(nxt=7 * AT + 8),
+                dict(nxt=5 * AT), dict(count=6 * AT + 116), dict(n=(1 << 20) + 1)):
+        assert accept(lib, **bad) == ds4a.ERR_INVALID_ARG, bad
+
+
+def commit(lib, rows=None, n=3, geom=5 * AT, path=6 * AT, stride=40, width=10, count=7 * AT):
+    return elsewhere(lib.ds4a_commit_paged, n, ctypes.byref(rows or seg()), geom, path, stride, width, count, None)
+
+
+@needs_no_gpu
+def test_commit_arguments_are_checked(lib):
+    assert passes(commit(lib)) and passes(commit(lib, seg(v=AT)))
+    f8 = dict(row_stride=512, page_stride=8192)
+    assert passes(commit(lib, seg(k_scale=11 * AT, v_scale=12 * AT, **f8)))
+    assert commit(lib, n=0) == ds4a.OK and commit(lib, width=0, path=None) == ds4a.OK
+    for bad in (dict(n=-1), dict(width=-1), dict(geom=None), dict(geom=AT + 4), dict(path=None), dict(path=AT + 1),
+                dict(stride=36), dict(stride=41), dict(count=None), dict(count=AT + 2), dict(rows=seg(max_pages=0)),
+                dict(rows=seg(table=None)), dict(rows=seg(v=None)), dict(rows=seg(k=AT + 8)), dict(n=(1 << 20) + 1),
+                dict(rows=seg(k_scale=11 * AT, v_scale=11 * AT, **f8))):
+        assert commit(lib, **bad) == ds4a.ERR_INVALID_ARG, bad
+
+
+# ------------------------------------------------------------------ binding
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=I32)
+
+
+def test_step_calls_refuse_what_does_not_fit():
+    """Sizes, types and strides, and then that host tensors are no device tensors."""
+    good = dict(table=i32(3, 8), free_pages=i32(100), n_free=i32(1), have=i32(3), want=i32(3), page_rows=16,
+                slots=i32(9), first=i32(4), n_short=i32(1), workspace=torch.zeros(256, dtype=torch.uint8))
+    raises("CUDA tensor", ds4a.prepare_page_tables, **good)
+    for bad, match in ((dict(table=i32(2, 8)), "table"), (dict(table=i32(3)), "table"),
+                       (dict(table=torch.zeros(3, 8)), "table"), (dict(table=i32(8, 3).T), "table"),
+                       (dict(table=i32(1, 8).expand(3, 8)), "table")):
+        raises(match, ds4a.prepare_page_tables, **dict(good, **bad))
+    good = dict(first=i32(4), token=i32(20), target=i32(20), path=i32(3, 5), n_accepted=i32(3), next_token=i32(3))
+    for bad, match in ((dict(path=i32(2, 5)), "path"), (dict(path=None), "path"), (dict(path=i32(1, 5).expand(3, 5)), "path"),
+                       (dict(path=torch.zeros(3, 5)), "path"), (dict(first=i32(0)), "first")):
+        raises(match, ds4a.prepare_tree_accept, **dict(good, **bad))
+
+
+@pytest.mark.parametrize("name,bad", [("have", i32(2)), ("have", i32(6)[::2]), ("want", torch.zeros(3)),
+                                      ("first", i32(3)), ("n_short", i32(0)), ("drop", i32(2)), ("n_free", i32(1, 1))])
+def test_whole_numbers_of_the_wrong_kind_are_refused(name, bad, monkeypatch):
+    monkeypatch.setattr(ds4a, "_on_device", lambda **kw: None)
+    good = dict(table=i32(3, 8), free_pages=i32(100), n_free=i32(1), have=i32(3), want=i32(3), page_rows=16,
+                slots=i32(9), first=i32(4), n_short=i32(1), workspace=torch.zeros(256, dtype=torch.uint8))
+    if name == "have" and bad.shape[0] == 2:
+        good["table"] = i32(1, 8)
+        name, match = "have", "table"
+    else:
+        match = name
+    raises(match, ds4a.prepare_page_tables, **dict(good, **{name: bad}))
+
+
+# ------------------------------------------------------------------ the oracle by hand
+
+def test_page_tables_by_hand():
+    """Sequence 0 drops its first page and grows over a page's end; 1 gives a page back; 2 finds the list empty."""
+    table = np.array([[3, 1, -1], [0, 5, -1], [-1, -1, -1]], dtype=np.int32)
+    free = [4, -1, -1, -1, -1, -1]
+    n_free, slots, first, short = step.page_tables(table, free, 1, [7, 6, 0], [10, 3, 9], [5, 0, 0], 4, 6, 14)
+    # given back: 3, then 5 -> list 4 3 5; taken: 5 (sequence 0), then 3, 4 and none (sequence 2)
+    assert table.tolist() == [[1, 5, -1], [0, -1, -1], [3, 4, -1]]
+    assert n_free == 0 and short == 1 and first.tolist() == [0, 3, 3, 12]
+    assert slots.tolist() == [1 * 4 + 3, 5 * 4, 5 * 4 + 1] + [12, 13, 14, 15, 16, 17, 18, 19, -1] + [-1, -1]
+
+
+def test_accept_by_hand():
+    #      0 -> 1, 2;  1 -> 3;  2 -> 4, 5
+    parent = np.array([-1, 0, 0, 1, 2, 2])
+    token = np.array([7, 8, 9, 1, 2, 3])
+    target = np.array([9, 1, 3, 0, 0, 6])
+    assert step.accept([0, 6], parent, token, target, [7], 9) == ([[0, 2, 5]], [6])
+    assert step.accept([0, 6], parent, token, target, [6], 9) == ([[]], [6])
+    assert step.accept([0, 6], parent, token, target, None, 2) == ([[0, 2]], [3])
+    assert step.accept([0, 0], parent, token, target, None, 2) == ([[]], [-1])
+
+
+def test_seen_by_hand():
+    """A tree of four at position 6, rows 4 and 5 cached, window 3."""
+    shape = dict(window=3, ratio=2, scale=1.0)
+    got = step.seen(shape, (6, 2, 4, 9), np.array([-1, 0, 0, 2]), 0, 4, 100, 100)
+    assert got == [([0, 1, 2], [0, 1, 2]), ([1, 2, 3], [0, 1, 2, 3]), ([1, 2, 4], [0, 1, 2, 3]), ([2, 4, 5], [0, 1, 2, 3])]
