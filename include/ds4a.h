@@ -744,6 +744,53 @@ ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *work
                              ds4a_stream_t stream);
 
 /*
+ * ds4a_attn_tree_paged - attention of several new tokens per sequence over
+ * paged rows: a tree of drafted tokens, or (parent NULL) a run of tokens, each
+ * seeing those before it.  The new tokens' own rows lie behind the cached raw
+ * ones: token t of sequence b (counted within it) has raw row n_raw + t, written
+ * before the call.  Its position is p = q_pos + (number of its ancestors), and it
+ * sees
+ *   - cached raw row i < n_raw when p - window < raw_pos0 + i <= p;
+ *   - its own row and those of its ancestors, each fewer than window
+ *     generations above it;
+ *   - compressed row c < n_comp when (c + 1) * ratio <= p + 1.
+ * Rows of absent pages, and raw rows behind the table, are left out.  A token
+ * that sees no row gets o = 0 and lse = -inf.
+ *   n_tok       tokens of all sequences; those that first gives to no sequence
+ *               keep what o and lse held.
+ *   shape, seq_geom  as in ds4a_attn_decode_paged; q_pos is the position of a
+ *               sequence's first new token, n_raw does not count the new rows.
+ *   X->first    as above.
+ *   X->parent   device int32 [n_tok], as in ds4a_tree_accept (token t's
+ *               ancestors: its parent, the parent's parent, ..); NULL: runs.
+ *               A tree has DS4A_TREE_TOKENS tokens at most: those behind see no
+ *               row.  Runs are as long as the tables allow.
+ *   X->raw, X->comp  as in ds4a_attn_decode_paged.
+ *   X->q, X->o  fp16 [n_tok][64][512]; X->lse fp32 [n_tok][64] or NULL.
+ *   workspace   256-byte aligned, at least ds4a_attn_tree_paged_workspace_size()
+ *               bytes (which depends on the current device's SM count); need not
+ *               be initialised; not shared by calls in flight at the same time.
+ * A NaN in a head's query, or in a K row that a token sees, makes the head's o
+ * and lse NaN.  A V row that is not finite spoils the tokens that see it and no
+ * others.  The same call gives the same bits every time.
+ */
+#define DS4A_TREE_TOKENS 128
+typedef struct {
+  const void *q;
+  int64_t q_tok_stride;
+  const int32_t *first, *parent;
+  ds4a_paged_rows raw, comp;
+  void *o;
+  int64_t o_tok_stride;
+  float *lse;
+} ds4a_paged_tree;
+
+size_t ds4a_attn_tree_paged_workspace_size(int32_t n_seq, int32_t n_tok);
+ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout *shape, const int32_t *seq_geom,
+                                 const ds4a_paged_tree *X, void *workspace, size_t workspace_bytes,
+                                 ds4a_stream_t stream);
+
+/*
  * ds4a_tree_accept - the path of drafted tokens that agree with the model.
  * Node t of a sequence (counted within it) holds token[t]; target[t] is the
  * token chosen to follow it.  The path starts at the lowest root whose token is

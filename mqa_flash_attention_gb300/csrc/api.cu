@@ -84,6 +84,7 @@ ds4a_status current_device(DeviceState **out) {
       DS4A_CUDA_TRY(ds4a::prepare_pair_kernel());
       DS4A_CUDA_TRY(ds4a::prepare_paged_kernels());
       DS4A_CUDA_TRY(ds4a::prepare_cache_kernels());
+      DS4A_CUDA_TRY(ds4a::prepare_tree_kernels());
       DS4A_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void **>(&d.err), g_ds4a_device_error));
       DS4A_CUDA_TRY(cudaGetSymbolAddress(&d.scratch, g_decode_scratch));
       if (g_encode == nullptr) {

@@ -21,6 +21,7 @@ constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int64_t kMostBytes = 1LL << 39;  // of any stride
 constexpr int32_t kMostRows = 1 << 30;     // rows of a sequence
 constexpr int32_t kMostSeqs = 1 << 20;
+constexpr int32_t kMostTokens = 1 << 20;   // new tokens of a call
 constexpr float kLog2e = 1.4426950408889634f;
 
 cudaStream_t as_cuda(ds4a_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -154,6 +155,12 @@ int64_t tiles_of(int64_t rows) { return (rows + 127) / 128; }
 size_t decode_workspace(int32_t n_seq, int ctas) {
   const size_t slots = (size_t)n_seq + ctas;
   return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(float) + sizeof(float2)) + (size_t)n_seq * sizeof(int2);
+}
+
+// Partial results of two tokens, two items per CTA pair, and the plan.
+size_t tree_workspace(int32_t n_seq, int32_t n_tok, int ctas) {
+  const size_t slots = 4 * (size_t)(ctas / 2), units = ((size_t)n_tok + n_seq) / 2 + 2;
+  return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(float) + sizeof(float2)) + 16 * units + 8 * (size_t)n_seq + 256;
 }
 
 int device_sms() {
@@ -439,6 +446,61 @@ ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *work
   p.drop = X->drop;
   p.plan = static_cast<ds4a::PagePlan *>(workspace);
   return ds4a::host_launched(ds4a::launch_page_tables(p, as_cuda(stream)));
+}
+
+size_t ds4a_attn_tree_paged_workspace_size(int32_t n_seq, int32_t n_tok) {
+  if (n_seq <= 0 || n_tok <= 0) return 0;
+  return tree_workspace(n_seq, n_tok, device_sms());
+}
+
+ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout *shape, const int32_t *seq_geom,
+                                 const ds4a_paged_tree *X, void *workspace, size_t workspace_bytes,
+                                 ds4a_stream_t stream) {
+  if (n_seq < 0 || n_tok < 0 || shape == nullptr || X == nullptr) return DS4A_ERR_INVALID_ARG;
+  if (n_seq == 0 || n_tok == 0) return DS4A_OK;
+  ds4a_status st = check_batch(n_seq, shape, seq_geom);
+  if (st != DS4A_OK) return st;
+  if (n_tok > kMostTokens) return DS4A_ERR_INVALID_ARG;
+  if (!q_ok(X->q, X->q_tok_stride) || !q_ok(X->o, X->o_tok_stride)) return DS4A_ERR_INVALID_ARG;
+  if (!aligned(X->lse, 4) || X->first == nullptr || !aligned(X->first, 4) || !aligned(X->parent, 4))
+    return DS4A_ERR_INVALID_ARG;
+  bool e4m3 = false, any = false;
+  int64_t most = 0;  // rows of a sequence
+  for (const ds4a_paged_rows *r : {&X->raw, &X->comp}) {
+    if (r->max_pages < 0) return DS4A_ERR_INVALID_ARG;
+    if (!has_rows(r)) continue;
+    if (!pool_ok(r, true) || !table_ok(r)) return DS4A_ERR_INVALID_ARG;
+    const bool f8 = r->k_scale != nullptr;
+    if (any && f8 != e4m3) return DS4A_ERR_INVALID_ARG;  // one format for both segments
+    e4m3 = f8;
+    any = true;
+    most += (int64_t)r->max_pages * r->page_rows;
+  }
+  if (most > kMostRows) return DS4A_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < ds4a_attn_tree_paged_workspace_size(n_seq, n_tok))
+    return DS4A_ERR_WORKSPACE;
+  HostDevice d;
+  st = ds4a::host_device(&d);
+  if (st != DS4A_OK) return st;
+  ds4a::TreeAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.seg[0] = has_rows(&X->raw) ? seg_of(&X->raw) : no_rows();
+  p.seg[1] = has_rows(&X->comp) ? seg_of(&X->comp) : no_rows();
+  p.geom = reinterpret_cast<const int4 *>(seq_geom);
+  p.first = X->first;
+  p.parent = X->parent;
+  p.n_seq = n_seq;
+  p.n_tok = n_tok;
+  p.ratio = shape->ratio;
+  p.window = shape->window;
+  p.scale_log2 = shape->scale * kLog2e;
+  p.q = static_cast<const uint8_t *>(X->q);
+  p.q_stride = X->q_tok_stride;
+  p.o = static_cast<__half *>(X->o);
+  p.o_stride = X->o_tok_stride / 2;
+  p.lse = X->lse;
+  return ds4a::host_launched(ds4a::launch_tree_attn(p, e4m3, as_cuda(stream)));
 }
 
 ds4a_status ds4a_tree_accept(int32_t n_seq, int32_t n_tok, const int32_t *first, const int32_t *parent,

@@ -46,6 +46,23 @@ struct CommitParams {
 };
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t s);
 
+constexpr int kTreeTokens = 128;
+
+struct TreeAttnParams {
+  PagedSeg seg[2];         // raw, compressed
+  const int4 *geom;        // (q_pos, n_raw, raw_pos0, n_comp) per sequence
+  const int32_t *first, *parent;
+  int n_seq, n_tok, ratio, window;
+  float scale_log2;
+  const uint8_t *q;
+  long long q_stride;      // bytes
+  __half *o;
+  long long o_stride;      // elements
+  float *lse;
+};
+cudaError_t launch_tree_attn(const TreeAttnParams &p, bool e4m3, cudaStream_t s);
+cudaError_t prepare_tree_kernels();
+
 cudaError_t preload_step_kernels();
 
 }  // namespace ds4a

@@ -96,6 +96,13 @@ class Norm(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64)]
 
 
+class PagedTree(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_tok_stride", ctypes.c_int64),
+                ("first", ctypes.c_void_p), ("parent", ctypes.c_void_p),
+                ("raw", PagedSegment), ("comp", PagedSegment),
+                ("o", ctypes.c_void_p), ("o_tok_stride", ctypes.c_int64), ("lse", ctypes.c_void_p)]
+
+
 class PageLists(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32),
                 ("page_rows", ctypes.c_int32), ("n_pages", ctypes.c_int32),
@@ -202,6 +209,10 @@ def lib() -> ctypes.CDLL:
         L.ds4a_page_tables_workspace_size.argtypes = [i32]
         L.ds4a_page_tables.restype = st
         L.ds4a_page_tables.argtypes = [i32, ctypes.POINTER(PageLists), vp, ctypes.c_size_t, vp]
+        L.ds4a_attn_tree_paged_workspace_size.restype = ctypes.c_size_t
+        L.ds4a_attn_tree_paged_workspace_size.argtypes = [i32, i32]
+        L.ds4a_attn_tree_paged.restype = st
+        L.ds4a_attn_tree_paged.argtypes = [i32, i32, PL, vp, ctypes.POINTER(PagedTree), vp, ctypes.c_size_t, vp]
         L.ds4a_tree_accept.restype = st
         L.ds4a_tree_accept.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, vp]
         L.ds4a_commit_paged.restype = st
@@ -1197,6 +1208,51 @@ def page_tables(table, free_pages, n_free, have, want, page_rows, *, drop=None, 
     prepare_page_tables(table, free_pages, n_free, have, want, page_rows, drop=drop, slots=slots, first=first,
                         n_short=n_short, workspace=workspace, stream=stream)()
     return slots, first, n_short
+
+
+def tree_paged_workspace_bytes(n_seq: int, n_tok: int) -> int:
+    """Workspace bytes of :func:`attn_tree_paged` for ``n_tok`` tokens of
+    ``n_seq`` sequences on the current device."""
+    return int(lib().ds4a_attn_tree_paged_workspace_size(int(n_seq), int(n_tok)))
+
+
+def prepare_tree_paged(shape, seq_geom, first, q, raw, comp=None, *, parent=None, workspace=None, out, lse=None,
+                       stream=None) -> PreparedCall:
+    """:func:`attn_tree_paged` on fixed buffers, as a :class:`PreparedCall`."""
+    S, B, T = make_layout(shape), seq_geom.shape[0], q.shape[0]
+    qp, qs = _tokens(q, "q")
+    op, os_ = _tokens(out, "out", T)
+    if T > 1 and os_ < H * ROW_BYTES:
+        raise ValueError("out must not repeat tokens by stride")
+    if T <= 1:
+        qs = os_ = H * ROW_BYTES  # a single token's stride says nothing
+    _lse_ok(lse, T)
+    _on_device(q=q, out=out, lse=lse)
+    _paged_geom(seq_geom, B)
+    fp, pp = _ints(first, "first", B + 1), _ints(parent, "parent", T, True)
+    for seg, name in ((raw, "raw"), (comp, "comp")):
+        if seg is not None:
+            seg._check(name, B)
+    workspace, nbytes = _bytes_of(workspace, tree_paged_workspace_bytes(B, T), q, stream)
+    X = PagedTree(qp, qs, fp, pp, _NO_ROWS if raw is None else raw._c, _NO_ROWS if comp is None else comp._c, op, os_,
+                  _ptr(lse))
+    args = (B, T, ctypes.byref(S), _ptr(seq_geom), ctypes.byref(X), _ptr(workspace), nbytes, _stream(stream))
+    return PreparedCall(lib().ds4a_attn_tree_paged, "ds4a_attn_tree_paged", args,
+                        (S, X, seq_geom, first, parent, q, raw, comp, workspace, out, lse, stream))
+
+
+def attn_tree_paged(shape, seq_geom, first, q, raw, comp=None, *, parent=None, workspace=None, out=None, lse=None,
+                    want_lse=False, stream=None):
+    """Attention of several new tokens per sequence over paged rows: q fp16
+    [n_tok, 64, 512], those of sequence b at ``first[b] .. first[b + 1] - 1``
+    (int32 [B + 1]); ``parent`` int32 [n_tok] within the sequence, negative for
+    a root, or None: runs of tokens, causal.  Token t's own row is raw row
+    ``n_raw + t``; seq_geom int32 [B, 4]: (position of the first new token,
+    cached raw rows, raw_pos0, n_comp)."""
+    out, lse = _outputs(q, out, lse, want_lse, stream)
+    prepare_tree_paged(shape, seq_geom, first, q, raw, comp, parent=parent, workspace=workspace, out=out, lse=lse,
+                       stream=stream)()
+    return (out, lse) if (want_lse or lse is not None) else out
 
 
 def prepare_tree_accept(first, token, target, *, parent=None, prev=None, path, n_accepted, next_token,

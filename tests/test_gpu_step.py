@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 
 from oracle import paged, step
-from test_gpu_paged import device_error_word_stays_clear, ds4a, host, rows_on, torch, up  # noqa: F401
+from test_gpu_paged import (check_decode, device_error_word_stays_clear, ds4a, host, poison, rows_on, shape_of,  # noqa: F401
+                            torch, up)
 from test_paged_oracle import make
 
 pytestmark = pytest.mark.gpu
@@ -201,3 +202,268 @@ def test_commit_of_any_numbers(torch, ds4a):
     step.commit(seg, geom, [[2, 5, 9, 100, 1 << 30], [-4, -1, 2, 3, 4], [1, 2, 3, 4, 5]])
     for name in ("k", "v"):
         assert np.array_equal(host(getattr(rows, name)), seg[name])
+
+
+# ------------------------------------------------------------------ attention of several new tokens
+# Tolerances: as for one token (test_gpu_paged.py): a rounding of the weights and one of the output to fp16, the
+# scores' fp32 sums, and fp32 sums of the weights.
+
+def tree_case(rng, counts, comp_rows, ratio, page, f8=False, shared=True, window=128, absent=(), chain=False,
+              extra=1, wide=8):
+    """Sequences whose new tokens come right after the cached rows; NaN wherever no row is in use."""
+    geom, raw_rows = [], []
+    for c, n in zip(comp_rows, counts):
+        pos = c * ratio + min(extra, ratio - 1)
+        first = max(0, pos + 1 - window) // page * page
+        geom.append((pos, pos - first, first, (pos + n) // ratio if chain else c))
+        raw_rows.append(pos - first + n)
+    have_comp = [g[3] for g in geom]
+    comp = make(rng, len(counts), have_comp, page, f8, shared, absent)
+    raw = make(rng, len(counts), raw_rows, page, f8, shared)
+    poison(comp, have_comp)
+    poison(raw, raw_rows)
+    first = np.concatenate([[0], np.cumsum(counts)])
+    parent = None if chain else np.concatenate([tree_of(rng, n, False, wide) for n in counts] + [np.zeros(0, int)])
+    q = rng.standard_normal((first[-1], H, D)).astype(np.float16)
+    return geom, first, parent, q, raw, comp
+
+
+def check_tree(got_o, got_lse, want):
+    o, lse, spread, reach, count = want
+    check_decode(got_o, got_lse, (o, lse, spread, reach), count)
+
+
+def run_tree(torch, ds4a, shape, geom, first, parent, q, raw, comp, **kw):
+    i32 = lambda a: None if a is None else up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    o, lse = ds4a.attn_tree_paged(shape, i32(geom), i32(first), up(torch, q), raw, comp, parent=i32(parent),
+                                  want_lse=True, **kw)
+    return host(o), host(lse)
+
+
+TREES = [
+    # counts, compressed rows, ratio, page, f8, shared, chain, window
+    ([1], [0], 4, 16, False, True, False, 128),
+    ([2], [3], 4, 16, False, False, True, 128),
+    ([8], [256], 128, 64, False, True, False, 128),
+    ([8], [256], 128, 64, True, True, False, 128),
+    ([3, 1, 7, 0, 16], [40, 500, 0, 9, 1100], 4, 16, False, False, False, 128),
+    ([3, 1, 7, 0, 16], [40, 500, 0, 9, 1100], 4, 16, True, False, False, 128),
+    ([64, 13, 128], [700, 64, 300], 4, 32, False, True, False, 128),
+    ([64, 13, 128], [700, 64, 300], 4, 32, True, True, False, 128),
+    ([33, 20], [200, 90], 1, 24, False, True, False, 7),
+    ([40, 21], [517, 255], 1, 8, False, False, True, 128),
+    ([150, 299], [10, 40], 4, 100, False, True, True, 128),
+    ([61, 200, 5], [300, 20, 2], 4, 64, True, False, True, 33),
+    ([5, 4], [1024, 2000], 4, 128, False, False, False, 1),
+    ([17] * 20, list(range(0, 400, 20)), 4, 16, False, True, False, 128),
+    ([2] * 90, [30] * 90, 128, 7, True, True, True, 128),
+]
+
+
+@pytest.mark.parametrize("k", range(len(TREES)))
+def test_tree_matches_the_oracle(torch, ds4a, k):
+    counts, rows, ratio, page, f8, shared, chain, window = TREES[k]
+    rng = np.random.default_rng(100 + k)
+    geom, first, parent, q, raw, comp = tree_case(rng, counts, rows, ratio, page, f8, shared, window, chain=chain)
+    shape = shape_of(ratio, window)
+    want = step.attention(shape, geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape, geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_long_ragged_batches(torch, ds4a, f8, chain):
+    """Many tiles in a row, of every kind, and sequences cut over several groups of SMs."""
+    rng = np.random.default_rng(7 + f8)
+    counts, rows = [9, 2, 30, 1, 5, 12], [9000, 40, 2500, 6000, 1, 700]
+    geom, first, parent, q, raw, comp = tree_case(rng, counts, rows, 4, 64, f8, not chain, chain=chain)
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    r, c = rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp)
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, r, c)
+    check_tree(*got, want)
+    for _ in range(3):
+        again = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, r, c)
+        assert np.array_equal(again[0], got[0]) and np.array_equal(again[1], got[1])
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_tree_absent_pages(torch, ds4a, f8):
+    rng = np.random.default_rng(21)
+    geom, first, parent, q, raw, comp = tree_case(rng, [6, 9], [600, 90], 4, 32, f8, False,
+                                                  absent=((0, 0), (0, 7), (0, 8), (1, 2)))
+    raw["table"][0, 1] = -1
+    raw["table"][1, raw["table"].shape[1] - 1] = 1 << 30  # the new rows of a sequence, perhaps
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_tree_strides_and_untouched_tokens(torch, ds4a, f8):
+    """Padded pools, tokens and outputs; tokens behind the last sequence keep what they held."""
+    rng = np.random.default_rng(22)
+    geom, first, parent, q, raw, comp = tree_case(rng, [3, 10], [300, 31], 4, 16, f8, False)
+    n, T = int(first[-1]), int(first[-1]) + 5
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    big_q = torch.full((T, H * D + 24), float("nan"), dtype=torch.float16, device="cuda")
+    big_o = torch.full((T, H * D + 8), 7.0, dtype=torch.float16, device="cuda")
+    qv = big_q.as_strided((T, H, D), (H * D + 24, D, 1))
+    ov = big_o.as_strided((T, H, D), (H * D + 8, D, 1))
+    qv[:n] = up(torch, q)
+    lse = torch.full((T, H), 5.0, device="cuda")
+    i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    ds4a.attn_tree_paged(shape_of(4), i32(geom), i32(first), qv, rows_on(torch, ds4a, raw, 16, 64),
+                         rows_on(torch, ds4a, comp, 32, 128), parent=i32(np.concatenate([parent, np.zeros(5)])), out=ov,
+                         lse=lse)
+    check_tree(host(ov)[:n], host(lse)[:n], want)
+    assert (host(big_o)[n:] == 7).all() and (host(big_o)[:, H * D:] == 7).all() and (host(lse)[n:] == 5).all()
+
+
+def test_tree_of_more_nodes_than_are_seen(torch, ds4a):
+    """Nodes behind the 128th see no row; a chain of as many does."""
+    rng = np.random.default_rng(23)
+    geom, first, parent, q, raw, comp = tree_case(rng, [131, 4], [50, 6], 4, 16)
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    assert (want[0][128:131] == 0).all() and np.isneginf(want[1][128:131]).all()
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_of_any_numbers(torch, ds4a, chain):
+    """Parents that are no earlier node, new rows behind the table, ranges and geometry out of bounds, segments
+    without rows: what the oracle, which goes by the definition, says."""
+    rng = np.random.default_rng(24)
+    geom, first, parent, q, raw, comp = tree_case(rng, [12, 20, 3], [40, 90, 2], 4, 16, chain=chain)
+    if not chain:
+        parent = rng.integers(-4, 25, 35)
+        parent[5] = 1 << 30
+    geom[0] = (geom[0][0], raw["table"].shape[1] * 16 - 4, 0, 1 << 30)  # most new rows behind the table
+    geom[1] = (-5, -7, -3, -1)
+    for seg in (raw, comp):  # every row may be read now
+        seg["k"][np.isnan(seg["k"])] = 1.0
+        seg["table"][seg["table"] < 0] = 0
+    r, c = rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp)
+    for f in (first, [-9, 12, 32, 1 << 30], [0, 0, 35, 35], [12, 12, 12, 12]):
+        for rr, cc, ro, co in ((r, c, raw, comp), (r, None, raw, None), (None, c, None, comp), (None, None, None, None)):
+            want = step.attention(shape_of(4), geom, f, parent, q, ro, co)
+            mine = ~np.isnan(want[0][:, 0, 0])
+            o, lse = run_tree(torch, ds4a, shape_of(4), geom, f, parent, q, rr, cc)
+            check_tree(o[mine], lse[mine], tuple(x[mine] for x in want))
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_bad_rows_spoil_their_tokens_only(torch, ds4a, f8, chain):
+    """A row that holds NaN or infinities (as K, as V, or both) reaches the tokens that see it, and no others."""
+    rng = np.random.default_rng(25)
+    counts = [12, 40]
+    geom, first, parent, q, raw, comp = tree_case(rng, counts, [150, 300], 4 if chain else 128, 16, f8, False, chain=chain)
+    want = step.attention(shape_of(4 if chain else 128), geom, first, parent, q, raw, comp)
+    for node, which, value in ((3, "k", np.nan), (7, "v", np.nan), (11, "v", np.inf), (0, "v", -np.inf)):
+        for b, cached in ((0, False), (1, False), (1, True)):
+            seg = {k: (None if x is None else x.copy()) for k, x in raw.items()}
+            row = geom[b][1] - 100 + node if cached else geom[b][1] + node  # (a cached row leaves a run's window)
+            page, slot = seg["table"][b, row // 16], row % 16
+            bad = 0x7F if f8 else value
+            seg[which][page, slot, 5] = bad
+            seg[which][page, slot, 300] = bad
+            o, lse = run_tree(torch, ds4a, shape_of(4 if chain else 128), geom, first, parent, q,
+                              rows_on(torch, ds4a, seg), rows_on(torch, ds4a, comp))
+            views = step.seen(shape_of(4 if chain else 128), geom[b], parent, int(first[b]), counts[b], 1 << 20, 1 << 20)
+            hit = np.zeros(len(q), dtype=bool)
+            hit[first[b]:first[b + 1]] = [row in v[0] for v in views]
+            assert hit.any() and not hit.all()
+            check_tree(o[~hit], lse[~hit], tuple(x[~hit] for x in want))
+            assert not np.isfinite(o[hit][:, :, 5]).any() and not np.isfinite(o[hit][:, :, 300]).any()
+            if which == "k":
+                assert np.isnan(o[hit]).all() and np.isnan(lse[hit]).all()
+            else:
+                assert np.isfinite(lse[hit]).all()
+
+
+def test_tree_pages_past_32_bit_offsets(torch, ds4a):
+    """A pool of over 4 GB: rows at its far end."""
+    rng = np.random.default_rng(26)
+    page, n_pages = 64, 70000
+    pool = torch.zeros((n_pages, page, D), dtype=torch.float16, device="cuda")
+    counts, rows = [5, 8], [400, 130]
+    geom, first, parent, q, raw, comp = tree_case(rng, counts, rows, 4, page)
+    far = {}
+    for name, seg, base in (("raw", raw, n_pages - 40), ("comp", comp, n_pages - 80)):
+        pool[base:base + len(seg["k"])] = up(torch, seg["k"])
+        far[name] = ds4a.PagedRows(pool, None, up(torch, np.where(seg["table"] >= 0, seg["table"] + base, -1).astype(np.int32)))
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, far["raw"], far["comp"])
+    check_tree(*got, want)
+
+
+@pytest.mark.parametrize("exponent", [-60, -12, 0, 12])
+def test_tree_e4m3_scales_of_any_size(torch, ds4a, exponent):
+    """V scales far from 1: the output scales with them."""
+    rng = np.random.default_rng(27)
+    geom, first, parent, q, raw, comp = tree_case(rng, [7, 4], [300, 77], 4, 16, True, False)
+    for seg in (raw, comp):
+        live = np.isfinite(seg["v_scale"])
+        seg["v_scale"][live] *= np.float32(2.0) ** exponent
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_tree_large_scores_move_the_reference(torch, ds4a, f8):
+    """Scores that grow along the rows, by far more than an exponent holds."""
+    rng = np.random.default_rng(28)
+    geom, first, parent, q, raw, comp = tree_case(rng, [6], [3000], 4, 64, f8, False)
+    q = (q.astype(np.float32) * 2).astype(np.float16)
+    if not f8:
+        grow = np.linspace(0.1, 12, 3000)
+        for i in range(3000):
+            comp["k"][comp["table"][0, i // 64], i % 64] *= np.float16(grow[i])
+    else:
+        for i in range(3000):
+            comp["k_scale"][comp["table"][0, i // 64], i % 64] *= np.float32(0.1 + i / 250)
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
+@pytest.mark.parametrize("below", [6, 12, 18, 24])
+def test_tree_of_a_long_tail_under_one_row(torch, ds4a, below):
+    """65,000 rows 2^-below under a single one: each rounds to little, together they count."""
+    rng = np.random.default_rng(29)
+    n, page = 65000, 64
+    geom, first, parent, q, raw, comp = tree_case(rng, [2], [n], 1, page, False, False)
+    axis = np.zeros(D, dtype=np.float16)
+    axis[0] = 16.0
+    q[:] = axis
+    raw["k"][np.isfinite(raw["k"])] = 0
+    raw["k"][:, :, 0] = np.where(np.isfinite(raw["k"][:, :, 0]), -64.0, np.nan)  # far below all others
+    scale = 1.0 / np.sqrt(512.0)
+    low = -below * np.log(2.0) / (16.0 * scale)
+    comp["k"][np.isfinite(comp["k"])] = 0
+    comp["k"][:, :, 0] = np.where(np.isfinite(comp["k"][:, :, 0]), low, np.nan)
+    comp["k"][comp["table"][0, 300], 5, 0] = 0.0
+    comp["v"][np.isfinite(comp["v"])] = 1.0
+    comp["v"][comp["table"][0, 300], 5] = -1.0
+    want = step.attention(shape_of(1), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(1), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
+def test_tree_of_single_tokens_is_the_decode(torch, ds4a):
+    """One new token per sequence: the decode's result, its own row counted among the raw ones."""
+    rng = np.random.default_rng(30)
+    geom, first, parent, q, raw, comp = tree_case(rng, [1] * 5, [0, 9, 300, 77, 1500], 4, 16)
+    r, c = rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp)
+    one = [(p, n + 1, r0, nc) for p, n, r0, nc in geom]
+    want = paged.decode(shape_of(4), one, q, raw, comp)
+    rows = [n for *_, n in geom]
+    for par in (parent, None):
+        got = run_tree(torch, ds4a, shape_of(4), geom, first, par, q, r, c)
+        check_decode(*got, want, [n + 129 for n in rows])
+    i32 = up(torch, np.array(one, dtype=np.int32))
+    o, lse = ds4a.attn_decode_paged(shape_of(4), i32, up(torch, q), r, c, want_lse=True)
+    check_decode(host(o), host(lse), want, [n + 129 for n in rows])

@@ -2,6 +2,7 @@
 the step's oracle by hand."""
 
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -9,7 +10,7 @@ import torch
 
 from mqa_flash_attention_gb300 import ds4a
 from oracle import step
-from test_paged_checks import AT, I32, elsewhere, lib, needs_no_gpu, passes, raises, seg  # noqa: F401
+from test_paged_checks import AT, I32, SHAPE, elsewhere, lib, needs_no_gpu, passes, raises, seg  # noqa: F401
 
 
 def lists(**kw):
@@ -81,6 +82,42 @@ def test_commit_arguments_are_checked(lib):
         assert commit(lib, **bad) == ds4a.ERR_INVALID_ARG, bad
 
 
+def tree(lib, n=3, n_tok=20, shape=None, geom=5 * AT, ws=1 << 30, nbytes=None, **kw):
+    base = dict(q=4 * AT, q_tok_stride=65536, first=6 * AT, parent=7 * AT, raw=seg(), comp=seg(), o=8 * AT,
+                o_tok_stride=65536, lse=9 * AT)
+    base.update(kw)
+    X = ds4a.PagedTree(*[base[n] for n, _ in ds4a.PagedTree._fields_])
+    S = ds4a.make_layout(dict(SHAPE, **(shape or {})))
+    if shape and "ratio" in shape:
+        S.ratio = shape["ratio"]
+    need = lib.ds4a_attn_tree_paged_workspace_size(n, n_tok)
+    return elsewhere(lib.ds4a_attn_tree_paged, n, n_tok, ctypes.byref(S), geom, ctypes.byref(X), ws,
+                     need if nbytes is None else nbytes, None)
+
+
+@needs_no_gpu
+def test_tree_arguments_are_checked(lib):
+    f8 = dict(row_stride=512, page_stride=8192, k_scale=AT, v_scale=AT)
+    none = seg(max_pages=0, k=None)
+    assert passes(tree(lib)) and passes(tree(lib, parent=None, lse=None)) and passes(tree(lib, raw=none))
+    assert passes(tree(lib, comp=none)) and passes(tree(lib, raw=seg(**f8), comp=seg(**f8)))
+    assert passes(tree(lib, raw=none, comp=none)) and passes(tree(lib, comp=seg(page_rows=1, page_stride=1024)))
+    assert tree(lib, n=0) == ds4a.OK and tree(lib, n_tok=0) == ds4a.OK
+    big = dict(page_rows=1 << 27, n_pages=8, page_stride=1 << 37, table_stride=32, max_pages=8)
+    for bad in (dict(n=-1), dict(n_tok=-1), dict(n=(1 << 20) + 1), dict(n_tok=(1 << 20) + 1), dict(q=None), dict(q=AT + 8),
+                dict(q_tok_stride=65520), dict(q_tok_stride=65544), dict(o=None), dict(o=AT + 4), dict(o_tok_stride=0),
+                dict(lse=AT + 2), dict(first=None), dict(first=AT + 1), dict(parent=AT + 2), dict(geom=None),
+                dict(geom=AT + 8), dict(shape=dict(window=0)), dict(shape=dict(ratio=0)), dict(shape=dict(scale=math.inf)),
+                dict(shape=dict(scale=math.nan)), dict(shape=dict(scale=3e38)), dict(comp=seg(**f8)), dict(raw=seg(k=None)),
+                dict(comp=seg(v=None)), dict(raw=seg(page_rows=0)), dict(comp=seg(table=None)), dict(raw=seg(max_pages=-1)),
+                dict(raw=seg(**big), comp=seg())):
+        assert tree(lib, **bad) == ds4a.ERR_INVALID_ARG, bad
+    need = lib.ds4a_attn_tree_paged_workspace_size(3, 20)
+    assert need > 0 and lib.ds4a_attn_tree_paged_workspace_size(0, 5) == 0
+    for bad in (dict(ws=None), dict(ws=AT + 128), dict(nbytes=need - 1)):
+        assert tree(lib, **bad) == ds4a.ERR_WORKSPACE, bad
+
+
 # ------------------------------------------------------------------ binding
 
 def i32(*shape):
@@ -100,6 +137,22 @@ def test_step_calls_refuse_what_does_not_fit():
     for bad, match in ((dict(path=i32(2, 5)), "path"), (dict(path=None), "path"), (dict(path=i32(1, 5).expand(3, 5)), "path"),
                        (dict(path=torch.zeros(3, 5)), "path"), (dict(first=i32(0)), "first")):
         raises(match, ds4a.prepare_tree_accept, **dict(good, **bad))
+
+
+def test_tree_refuses_what_does_not_fit(monkeypatch):
+    def f16(*shape):
+        return torch.zeros(shape, dtype=torch.float16)
+    rows = ds4a.PagedRows(f16(4, 16, 512), None, i32(2, 3))
+    good = dict(shape=SHAPE, seq_geom=i32(2, 4), first=i32(3), q=f16(9, 64, 512), raw=rows, out=f16(9, 64, 512),
+                workspace=torch.zeros(1, dtype=torch.uint8))
+    raises("CUDA tensor", ds4a.prepare_tree_paged, **good)
+    monkeypatch.setattr(ds4a, "_on_device", lambda **kw: None)
+    for bad, match in ((dict(q=f16(9, 64, 256)), "q must"), (dict(out=f16(8, 64, 512)), "out"), (dict(first=i32(2)), "first"),
+                       (dict(out=f16(1, 64, 512).expand(9, 64, 512)), "out"), (dict(parent=i32(8)), "parent"),
+                       (dict(parent=torch.zeros(9)), "parent"), (dict(lse=torch.zeros(9, 63)), "lse"),
+                       (dict(seq_geom=i32(2, 3)), "seq_geom"), (dict(raw=ds4a.PagedRows(f16(4, 16, 512))), "page table"),
+                       (dict(comp=ds4a.PagedRows(f16(4, 16, 512), None, i32(1, 3))), "comp.table")):
+        raises(match, ds4a.prepare_tree_paged, **dict(good, **bad))
 
 
 @pytest.mark.parametrize("name,bad", [("have", i32(2)), ("have", i32(6)[::2]), ("want", torch.zeros(3)),
