@@ -323,16 +323,16 @@ ds4a_status host_encode_q(CUtensorMap *m, const void *base, int n, int64_t strid
 }
 
 ds4a_status host_encode_pages(CUtensorMap *m, const void *base, bool e4m3, int page_rows, int n_pages,
-                              int64_t row_stride, int64_t page_stride, int run_rows) {
+                              int64_t row_stride, int64_t page_stride, int run_rows, int blocks) {
   if (e4m3) {
     const cuuint64_t dims[3] = {DS4A_HEAD_DIM, (cuuint64_t)page_rows, (cuuint64_t)n_pages};
     const cuuint64_t strides[2] = {(cuuint64_t)row_stride, (cuuint64_t)page_stride};
-    const cuuint32_t box[3] = {128, (cuuint32_t)run_rows, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(64 * blocks), (cuuint32_t)run_rows, 1};
     return encode(m, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT8);
   }
   const cuuint64_t dims[5] = {64, 8, DS4A_HEAD_DIM / 64, (cuuint64_t)page_rows / 8, (cuuint64_t)n_pages};
   const cuuint64_t strides[4] = {(cuuint64_t)row_stride, 128, (cuuint64_t)row_stride * 8, (cuuint64_t)page_stride};
-  const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)run_rows / 8, 1};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)blocks, (cuuint32_t)run_rows / 8, 1};
   return encode(m, base, 5, dims, strides, box);
 }
 

@@ -157,10 +157,24 @@ size_t decode_workspace(int32_t n_seq, int ctas) {
   return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(float) + sizeof(float2)) + (size_t)n_seq * sizeof(int2);
 }
 
-// Partial results of two tokens, two items per CTA pair, and the plan.
-size_t tree_workspace(int32_t n_seq, int32_t n_tok, int ctas) {
-  const size_t slots = 4 * (size_t)(ctas / 2), units = ((size_t)n_tok + n_seq) / 2 + 2;
-  return slots * DS4A_HEADS * (DS4A_HEAD_DIM * sizeof(float) + sizeof(float2)) + 16 * units + 8 * (size_t)n_seq + 256;
+// The workspace of the attention of several new tokens: the plan, then partial
+// results of two items of two tokens per pair of CTAs.
+struct TreeSpace {
+  int clusters, max_units;
+  size_t start, unit, seq, ml, o, bytes;
+};
+TreeSpace tree_space(int32_t n_seq, int32_t n_tok, int ctas) {
+  TreeSpace t;
+  t.clusters = ctas / 2;
+  t.max_units = (int)(((int64_t)n_tok + n_seq) / 2 + 1);
+  const size_t slots = 4 * (size_t)t.clusters;
+  t.start = 256;
+  t.unit = t.start + align256(4 * ((size_t)t.clusters + 1));
+  t.seq = t.unit + align256(16 * (size_t)t.max_units);
+  t.ml = t.seq + align256(4 * (size_t)n_seq);
+  t.o = t.ml + align256(slots * DS4A_HEADS * sizeof(float2));
+  t.bytes = t.o + slots * DS4A_HEADS * DS4A_HEAD_DIM * sizeof(float);
+  return t;
 }
 
 int device_sms() {
@@ -450,7 +464,7 @@ ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *work
 
 size_t ds4a_attn_tree_paged_workspace_size(int32_t n_seq, int32_t n_tok) {
   if (n_seq <= 0 || n_tok <= 0) return 0;
-  return tree_workspace(n_seq, n_tok, device_sms());
+  return tree_space(n_seq, n_tok, device_sms()).bytes;
 }
 
 ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout *shape, const int32_t *seq_geom,
@@ -477,6 +491,8 @@ ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout
     most += (int64_t)r->max_pages * r->page_rows;
   }
   if (most > kMostRows) return DS4A_ERR_INVALID_ARG;
+  // Tiles of 256 rows, of pairs of tokens.
+  if ((((int64_t)n_tok + n_seq) / 2 + 1) * ((most + 255) / 256 + 1) > (1 << 30)) return DS4A_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256) ||
       workspace_bytes < ds4a_attn_tree_paged_workspace_size(n_seq, n_tok))
     return DS4A_ERR_WORKSPACE;
@@ -495,11 +511,39 @@ ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout
   p.ratio = shape->ratio;
   p.window = shape->window;
   p.scale_log2 = shape->scale * kLog2e;
-  p.q = static_cast<const uint8_t *>(X->q);
-  p.q_stride = X->q_tok_stride;
   p.o = static_cast<__half *>(X->o);
   p.o_stride = X->o_tok_stride / 2;
+  p.o_wide = aligned(X->o, 32) && X->o_tok_stride % 32 == 0;
   p.lse = X->lse;
+  st = ds4a::host_encode_q(&p.tm_q, X->q, n_tok, X->q_tok_stride);
+  if (st != DS4A_OK) return st;
+  if (has_rows(&X->comp)) {
+    const ds4a_paged_rows *r = &X->comp;
+    const int run = run_rows_of(r->page_rows);
+    p.run_rows = run > 64 ? 64 : run;  // (a part of V has 64 rows)
+  }
+  if (p.run_rows > 0) {
+    const ds4a_paged_rows *r = &X->comp;
+    p.run_shift = log2_of(p.run_rows);
+    st = ds4a::host_encode_pages(&p.tm_k, r->k, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride,
+                                 p.run_rows, 1);
+    if (st == DS4A_OK)
+      st = ds4a::host_encode_pages(&p.tm_v, r->v, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride,
+                                   p.run_rows, 2);
+    if (st != DS4A_OK) return st;
+  }
+  const TreeSpace t = tree_space(n_seq, n_tok, d.sm_count);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.clusters = t.clusters;
+  p.max_units = t.max_units;
+  p.ws_head = reinterpret_cast<int4 *>(ws);
+  p.ws_start = reinterpret_cast<int *>(ws + t.start);
+  p.ws_unit = reinterpret_cast<int4 *>(ws + t.unit);
+  p.ws_seq = reinterpret_cast<int *>(ws + t.seq);
+  p.ws_ml = reinterpret_cast<float2 *>(ws + t.ml);
+  p.ws_o = reinterpret_cast<float *>(ws + t.o);
+  p.timeout_ns = kTimeoutNs;
+  p.err = d.err;
   return ds4a::host_launched(ds4a::launch_tree_attn(p, e4m3, as_cuda(stream)));
 }
 

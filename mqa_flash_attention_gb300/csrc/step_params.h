@@ -49,16 +49,31 @@ cudaError_t launch_commit(const CommitParams &p, cudaStream_t s);
 constexpr int kTreeTokens = 128;
 
 struct TreeAttnParams {
+  CUtensorMap tm_q;        // 4-D {64, 64 heads, n_tok, 8 dim blocks}, box {64, 64, 1, 8}
+  // Compressed rows by runs of run_rows rows, K by 64 dims and V by 128: fp16 5-D
+  // {64 dims, 8 rows, 8 blocks, page_rows / 8, pages}, box {64, 8, 1 or 2,
+  // run_rows / 8, 1}; codes 3-D {512, page_rows, pages}, box {64 or 128, run_rows, 1}.
+  CUtensorMap tm_k, tm_v;
+  int run_rows, run_shift; // 8 .. 64, a power of two, and its log2; 0: no TMA loads
   PagedSeg seg[2];         // raw, compressed
   const int4 *geom;        // (q_pos, n_raw, raw_pos0, n_comp) per sequence
   const int32_t *first, *parent;
   int n_seq, n_tok, ratio, window;
   float scale_log2;
-  const uint8_t *q;
-  long long q_stride;      // bytes
   __half *o;
   long long o_stride;      // elements
+  int o_wide;              // o and its stride are 32-byte aligned: 32-byte stores
   float *lse;
+  int clusters, max_units;
+  // Workspace.
+  int4 *ws_head;           // (tiles, tiles of a cluster, units, -)
+  int *ws_start;           // [clusters] unit of a cluster's first tile
+  int4 *ws_unit;           // [max_units] (sequence, first token, tiles, tiles before)
+  int *ws_seq;             // [n_seq] units before
+  float2 *ws_ml;           // [4 clusters][64] (m in log2 units, l)
+  float *ws_o;             // [4 clusters][64][512] normalised partial outputs
+  unsigned long long timeout_ns;
+  unsigned int *err;
 };
 cudaError_t launch_tree_attn(const TreeAttnParams &p, bool e4m3, cudaStream_t s);
 cudaError_t prepare_tree_kernels();
