@@ -72,7 +72,7 @@ enum : int { TF_FIRST = 1, TF_LAST = 2, TF_WHOLE = 4, TF_GATHERED = 8, TF_SPOILE
 enum : unsigned int {
   TSITE_Q_EMPTY = 0x80, TSITE_KV_EMPTY, TSITE_Q_FULL, TSITE_S_EMPTY, TSITE_KV_FULL, TSITE_P_FULL, TSITE_O_EMPTY,
   TSITE_S_FULL, TSITE_P_EMPTY, TSITE_O_FULL, TSITE_DRAIN, TSITE_CODE_FULL, TSITE_LIST_FULL, TSITE_LIST_EMPTY,
-  TSITE_CODE_EMPTY, TSITE_PEER_FULL
+  TSITE_CODE_EMPTY
 };
 
 struct TMisc {
@@ -85,7 +85,7 @@ struct TMisc {
   int flags[kListsT], tok[kListsT];                    // TF_ bits; the token (-1: none)
   alignas(16) float red[4][kH];
   alignas(8) uint64_t q_full, q_empty, peer_q_full;
-  uint64_t kv_full[7], kv_empty[7], peer_full[7];
+  uint64_t kv_full[7], kv_empty[7];  // (rank 0's kv_full: of both CTAs)
   uint64_t code_full[kCodeSlots], code_empty[kCodeSlots];
   uint64_t list_full[kListsT], list_empty[kListsT];
   uint64_t s_full[2], s_empty[2], o_full[2];
@@ -494,7 +494,7 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
     // Every thread waits for every fill of a stage, whoever loads it: a parity
     // wait is only right for a thread that has seen the phase before.
     if (!(FP8 ? mbar_wait(b_empty, ph, abrt, p.timeout_ns, p.err, TSITE_CODE_EMPTY)
-              : mbar_wait_cluster(b_empty, ph, abrt, p.timeout_ns, p.err, TSITE_KV_EMPTY)))
+              : mbar_wait(b_empty, ph, abrt, p.timeout_ns, p.err, TSITE_KV_EMPTY)))
       return false;
     const bool is_v = part >= 8;
     const int nb = (part >> 2) & 1, kq = part & 3;
@@ -507,9 +507,11 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
       const int runs = (is_v ? 64 : 128) >> p.run_shift;
       const int first = gwarp - turn, i = (first < 0 ? first + kWarps : first) + lane * kWarps;
       turn = (turn + runs) % kWarps;
+      // (fp16: the bytes of both CTAs count at rank 0's barrier; here only the issue does.)
       if (lane == 0) {
-        if (gtid == 0) mbar_arrive_expect_tx(b_full_bar, FP8 ? kCodePart : kPart);
-        mbar_arrive_cnt(b_full_bar, gtid == 0 ? 31 : 32);
+        const bool expects = gtid == 0 && (FP8 || rank == 0);
+        if (expects) mbar_arrive_expect_tx(b_full_bar, FP8 ? kCodePart : 2 * kPart);
+        mbar_arrive_cnt(b_full_bar, expects ? 31 : 32);
       }
       if (i < runs) {
         filled |= st_bit;
@@ -520,7 +522,7 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
         if (FP8)
           tma_load_3d(dst, m, b_full_bar, dim0, x.y, x.x);
         else
-          tma_load_5d(dst, m, b_full_bar, 0, 0, dim0 >> 6, x.y >> 3, x.x);
+          tma_load_5d_pair(dst, m, cluster_addr(b_full_bar, 0), 0, 0, dim0 >> 6, x.y >> 3, x.x);
       }
       return true;
     }
@@ -562,7 +564,7 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
   };
   auto load_q = [&]() {
     if (gtid == 0 && ok) {
-      if (!mbar_wait_cluster(smem_u32(&ms.q_empty), (n_item & 1) ^ 1, abrt, p.timeout_ns, p.err, TSITE_Q_EMPTY)) {
+      if (!mbar_wait(smem_u32(&ms.q_empty), (n_item & 1) ^ 1, abrt, p.timeout_ns, p.err, TSITE_Q_EMPTY)) {
         ok = false;
       } else {
         mbar_arrive_expect_tx(smem_u32(&ms.q_full), kQBytes);
@@ -629,7 +631,7 @@ __device__ __forceinline__ void tree_convert_role(const TreeAttnParams &p, int n
                    : "r"(src + 16 * (ct + 128 * k)));
     __syncwarp();
     if ((ct & 31) == 0) mbar_arrive(smem_u32(&ms.code_empty[codes.st]));
-    if (!mbar_wait_cluster(smem_u32(&ms.kv_empty[ring.st]), ring.ph ^ 1, abrt, p.timeout_ns, p.err, TSITE_KV_EMPTY)) return;
+    if (!mbar_wait(smem_u32(&ms.kv_empty[ring.st]), ring.ph ^ 1, abrt, p.timeout_ns, p.err, TSITE_KV_EMPTY)) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int n = ct + 128 * k;
@@ -666,7 +668,7 @@ __device__ __forceinline__ void tree_relay_role(const TreeAttnParams &p, int nt,
     for (int i = 0; i < n; ++i) {
       if (!mbar_wait(smem_u32(&ms.kv_full[ring.st]), ring.ph, abrt, p.timeout_ns, p.err, TSITE_KV_FULL)) return false;
       fence_proxy_async_smem();
-      mbar_arrive_cluster(cluster_addr(smem_u32(&ms.peer_full[ring.st]), 0));
+      mbar_arrive_cluster(cluster_addr(smem_u32(&ms.kv_full[ring.st]), 0));
       ring.advance();
     }
     return true;
@@ -704,11 +706,10 @@ __device__ __forceinline__ void tree_mma_role(const TreeAttnParams &p, int nt, u
   Ring<kStagesT<FP8>> ring;
   uint32_t q_item = 0, o_item = 0;
   auto wait = [&](uint64_t &bar, uint32_t parity, unsigned int site) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&bar), parity, abrt, p.timeout_ns, p.err, site));
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abrt, p.timeout_ns, p.err, site));
   };
   auto stage_ready = [&](bool gathered) -> bool {
     if (!wait(ms.kv_full[ring.st], ring.ph, TSITE_KV_FULL)) return false;
-    if (!wait(ms.peer_full[ring.st], ring.ph, TSITE_PEER_FULL)) return false;
     if (FP8 || gathered) fence_proxy_async_smem();
     return true;
   };
@@ -837,7 +838,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     }
     spoiled = spoiled || (flags & TF_SPOILED);
     if (!FP8) mbar_arrive(smem_u32(&ms.list_empty[buf]));
-    bad = bad || !mbar_wait_cluster(smem_u32(&ms.s_full[sb]), (g >> 1) & 1, abrt, p.timeout_ns, p.err, TSITE_S_FULL);
+    bad = bad || !mbar_wait(smem_u32(&ms.s_full[sb]), (g >> 1) & 1, abrt, p.timeout_ns, p.err, TSITE_S_FULL);
     tc_fence_after();
     float s[64];
     tmem_ld64(tmem + kTmemTS + 128 * sb + 64 * hh + lanes, s);
@@ -887,7 +888,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       moved = true;
       lsum *= alpha;
     }
-    bad = bad || !mbar_wait_cluster(smem_u32(&ms.p_empty), (g & 1) ^ 1, abrt, p.timeout_ns, p.err, TSITE_P_EMPTY);
+    bad = bad || !mbar_wait(smem_u32(&ms.p_empty), (g & 1) ^ 1, abrt, p.timeout_ns, p.err, TSITE_P_EMPTY);
     {
       // This head's 64 weights: 16-byte chunk c of its 128 bytes at c ^ (h & 7).
       // Rounded once to fp16 for the product; the sums add them unrounded, sixteen
@@ -952,7 +953,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       else if (p.lse != nullptr)
         p.lse[(long long)tok * kH + h] = none ? -INFINITY : (m_ref + log2f(sum)) * kLn2;
     }
-    bad = bad || !mbar_wait_cluster(smem_u32(&ms.o_full[hh]), n_item & 1, abrt, p.timeout_ns, p.err, TSITE_O_FULL);
+    bad = bad || !mbar_wait(smem_u32(&ms.o_full[hh]), n_item & 1, abrt, p.timeout_ns, p.err, TSITE_O_FULL);
     tc_fence_after();
     const int dim0 = 256 * hh + 128 * half;
 #pragma unroll 1
@@ -1012,9 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     mbar_init(smem_u32(&ms.q_empty), 1);
     mbar_init(smem_u32(&ms.peer_q_full), 1);
     for (int s = 0; s < 7; ++s) {
-      mbar_init(smem_u32(&ms.kv_full[s]), FP8 ? 128 : kLoadersT<false>);
+      mbar_init(smem_u32(&ms.kv_full[s]), (FP8 ? 128 : kLoadersT<false>) + (rank == 0 ? 1 : 0));
       mbar_init(smem_u32(&ms.kv_empty[s]), 1);
-      mbar_init(smem_u32(&ms.peer_full[s]), 1);
     }
     for (int s = 0; s < kCodeSlots; ++s) {
       mbar_init(smem_u32(&ms.code_full[s]), kLoadersT<true>);
@@ -1064,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     }
     __syncwarp();
     volatile int never = 0;
-    mbar_wait_cluster(smem_u32(&ms.mma_done), 0, &never, 3 * p.timeout_ns, p.err, TSITE_DRAIN);
+    mbar_wait(smem_u32(&ms.mma_done), 0, &never, 3 * p.timeout_ns, p.err, TSITE_DRAIN);
     __syncwarp();
   } else {
     const int ltid = threadIdx.x - 32 * kLoaderWarp0;
