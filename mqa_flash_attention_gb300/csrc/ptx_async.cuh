@@ -42,6 +42,27 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// What a wait needs when it does not succeed at once, in shared memory: one copy of
+// the loop, called, keeps the code of a kernel of many waits small (inlined, the
+// waits of one kernel were a third of its 160 KB, more than the instruction cache holds).
+struct WaitBox {
+  unsigned long long timeout_ns;
+  unsigned int *err;
+  int abort_flag;
+};
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t site, WaitBox *w) {
+  return mbar_wait(bar, parity, &w->abort_flag, w->timeout_ns, w->err, site);
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32_t site, WaitBox *w) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, site, w);
+}
+
+// One arrival for a converged warp, behind what its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // ------------------------------------------------------------------ a pair of CTAs
 // Two CTAs of a cluster issue one tcgen05.mma of cta_group::2: each holds half of
 // A's rows, half of B's rows and its rows' half of D; the CTA of rank 0 issues.

@@ -43,8 +43,7 @@ namespace ds4a {
 namespace {
 
 constexpr int kRows = 256;                  // of a tile
-constexpr uint32_t kPart = 16384;           // a stage: 64 dims of 128 K rows, or 128 dims of 64 V rows
-constexpr int kParts = 16;                  // stages of a tile: 8 of K, 8 of V
+constexpr uint32_t kPart = 16384;           // a stage (a tile has 8 of K, 8 of V): 64 dims of 128 K rows, or 128 dims of 64 V rows
 constexpr uint32_t kCodePart = kPart / 2;
 constexpr uint32_t kOffTP = kQBytes;        // P: 4 boxes [64 heads][64 rows]
 constexpr uint32_t kPBox = 8192;
@@ -54,16 +53,28 @@ constexpr uint32_t kOffTMisc = kOffRing + kRingBytes;
 constexpr uint32_t kTmemTS = 256;           // S buffers at columns 256 and 384
 constexpr int kListsT = 3;
 
-// fp16 rows: seven stages.  E4M3 rows: codes land in slots of their own and are
-// widened into four stages.
+// K and V come through rings of their own, because their products are issued by
+// warps of their own.  fp16 rows: four stages of K and three of V.  E4M3 rows:
+// codes land in three slots for each and are widened into two stages for each.
 template <bool FP8>
-constexpr int kStagesT = FP8 ? 4 : 7;
-constexpr int kCodeSlots = 6;
-static_assert(kStagesT<false> * kPart <= kRingBytes && 4 * kPart + kCodeSlots * kCodePart <= kRingBytes, "stages and code slots share the ring's bytes");
+constexpr int kKStages = FP8 ? 2 : 4;
 template <bool FP8>
-constexpr int kLoadersT = FP8 ? kLoaderThreads - 128 : kLoaderThreads;
+constexpr int kVStages = FP8 ? 2 : 3;
+constexpr int kCodeSlots = 3;
+static_assert(7 * kPart <= kRingBytes && 4 * kPart + 2 * kCodeSlots * kCodePart <= kRingBytes, "shared memory of the rings");
+// Warps 0-7 softmax and epilogue; 8-10 load K and 11-12 V (E4M3: 8 loads both, 9-10
+// widen K and 11-12 V); 13 finds the rows of the tiles; 14 issues P . V, 15 Q . K (in
+// the CTA of rank 1 they report what has landed).  Every role is a loop over the
+// tiles that meets the others at mbarriers only, and its code is kept small: what
+// all roles run through in a tile has to stay in the instruction cache.
+constexpr int kKLoadWarp0 = 8, kVLoadWarp0 = 11, kWidenWarp0 = 9, kListWarp = 13, kPvWarp = 14, kQkWarp = 15;
+template <bool FP8>
+constexpr int kKLoadWarps = FP8 ? 1 : 3;
+template <bool FP8>
+constexpr int kVLoadWarps = FP8 ? 1 : 2;
 
 constexpr float kLeastLog2ScaleT = -40.f;   // V scales below 2^-40 count as 0: such rows round to 0 in fp16
+constexpr float kMostScaleInv = 1.0995e12f;      // just below 2^40
 constexpr unsigned long long kSegBitT = 1, kNoRowT = 2, kNoValue = 4;  // low bits of a list entry
 
 // Of a tile within its item (the cluster's tiles of one unit).
@@ -76,22 +87,22 @@ enum : unsigned int {
 };
 
 struct TMisc {
-  alignas(16) unsigned long long row[kListsT][kRows];  // K address | bits
+  alignas(16) unsigned long long row[kListsT][kRows];  // K address | bits (of gathered tiles)
   alignas(16) float ksc[kListsT][kRows];               // E4M3: scale * log2(e) * K scale
   alignas(16) float lvs[kListsT][kRows];               // E4M3: log2 of the V scale (of 2^-40 at least)
   alignas(16) float ivs[kListsT][kRows];               // E4M3: 2^-lvs
   int2 box[kListsT][kRows / 8];                        // (page, slot) of the runs of a tile that TMA loads
   uint32_t mask[kListsT][kRows / 32];                  // rows that this CTA's token sees
-  int flags[kListsT], tok[kListsT];                    // TF_ bits; the token (-1: none)
+  int flags[kListsT], tok[kListsT], q_tok[kListsT];    // TF_ bits; this CTA's token (-1: none); the one whose Q it loads
   alignas(16) float red[4][kH];
   alignas(8) uint64_t q_full, q_empty, peer_q_full;
-  uint64_t kv_full[7], kv_empty[7];  // (rank 0's kv_full: of both CTAs)
-  uint64_t code_full[kCodeSlots], code_empty[kCodeSlots];
+  uint64_t kv_full[7], kv_empty[7];  // K's stages, then V's (rank 0's kv_full: of both CTAs)
+  uint64_t code_full[2 * kCodeSlots], code_empty[2 * kCodeSlots];
   uint64_t list_full[kListsT], list_empty[kListsT];
   uint64_t s_full[2], s_empty[2], o_full[2];
   uint64_t p_full, p_empty, o_empty, mma_done;
+  WaitBox wait;
   uint32_t tmem_base;
-  int abort_flag;
 };
 constexpr uint32_t kTreeSmem = kOffTMisc + ((sizeof(TMisc) + 127) / 128) * 128 + 1024;
 static_assert(kTreeSmem <= 232448, "shared memory of one CTA");
@@ -212,7 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
   }
 }
 
-// ------------------------------------------------------------------ loaders
+// ------------------------------------------------------------------ lists
 
 // What token i of the unit sees of the list.
 struct View {
@@ -220,421 +231,377 @@ struct View {
   uint32_t anc[4];
 };
 
+// One warp goes ahead of all others and writes down, per tile, what is in it.  A full
+// tile (compressed rows that both tokens see, in runs that TMA can copy) is no more than
+// the pages of its runs (and E4M3 scales); of any other the address of every row.
 template <bool FP8>
-__device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, int cluster, uint32_t rank, uint32_t sbase,
-                                               TMisc &ms, int ltid) {
-  constexpr int kGroup = kLoadersT<FP8>;
-  constexpr int kRowStep = kGroup / 8, kWarps = kGroup / 32;
-  constexpr int kMine = (kRows + kGroup - 1) / kGroup;
-  constexpr int kSlots = FP8 ? kCodeSlots : kStagesT<false>;
+__device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, int cluster, uint32_t rank, TMisc &ms,
+                                               int lane) {
   if (nt <= 0) return;
-  volatile int *abrt = &ms.abort_flag;
-  const int gtid = (FP8 && ltid >= 32) ? ltid - 128 : ltid, lane = ltid & 31, gwarp = gtid >> 5;
-  const int c8 = gtid & 7, rsub = gtid >> 3;
   const bool chain = p.parent == nullptr;
   const long long vdelta0 = p.seg[0].v - p.seg[0].k, vdelta1 = p.seg[1].v - p.seg[1].k;
   const int pad_seg = p.seg[1].max_rows > 0 ? 1 : 0;
   const unsigned long long pad_row = reinterpret_cast<unsigned long long>(p.seg[pad_seg].k) | pad_seg | kNoRowT;
-  Ring<kSlots> ring;
-  bool ok = true, q_issued = false;
-  uint32_t n_item = 0, q_par = 0, filled = 0, last_par = 0;
-  int turn = 0;
+  const int n_runs = p.run_rows > 0 ? kRows >> p.run_shift : 0;  // of a tile that TMA loads
 
-  // The unit of the tile that is listed next, and what its tokens see.
   int u = p.ws_start[cluster], left = nt;
-  int4 rec = p.ws_unit[u];
-  int j = cluster * p.ws_head[0].y - rec.w, first_j = j;
-  int tok0 = 0, own_tok = 0;
+  int4 rec = p.ws_unit[u], next_rec = rec;
+  int j = cluster * p.ws_head[0].y - rec.w, first_j = j, seq = -1;
+  int4 geom;
+  Span2 span;
+  int par[4];
   UnitRows rows;
   View view[2];
-  auto enter_unit = [&]() {
-    const int4 g = p.geom[rec.x];
-    const Span2 s = tokens_of(p, rec.x);
-    const int t0 = rec.y, t1 = min(rec.y + 1, s.n - 1);
-    tok0 = s.at + t0;
-    own_tok = rank == 0 ? tok0 : t1 > t0 ? tok0 + 1 : -1;
-    rows = unit_rows(p, g, s.n, t0, t1);
-    const long long pos = max(g.x, 0), raw_pos0 = max(g.z, 0);
-    const bool dead = !chain && t0 >= kTreeTokens;
-    int par[4] = {-1, -1, -1, -1};
-    if (!chain && !dead) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (32 * k + lane < min(s.n, kTreeTokens)) par[k] = p.parent[s.at + 32 * k + lane];
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      View &v = view[i];
-      const int t = i == 0 ? t0 : t1;
-      v.nc = v.ra = v.rb = v.da = v.db = 0;
-      v.anc[0] = v.anc[1] = v.anc[2] = v.anc[3] = 0;
-      if (dead) continue;
-      int depth = 0;
-      if (chain) {
-        depth = t;
-        v.da = max(0, t - p.window + 1);
-        v.db = t + 1;
-      } else {
-        // Up to the root; every lane alike.  (Each step goes to an earlier node.)
-        for (int at = t;; ++depth) {
-          if (depth < p.window) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (at >> 5 == k) v.anc[k] |= 1u << (at & 31);
-          }
-          const int mine = at < 32 ? par[0] : at < 64 ? par[1] : at < 96 ? par[2] : par[3];
-          const int up = __shfl_sync(0xffffffffu, mine, at & 31);
-          if (up < 0 || up >= at) break;
-          at = up;
-        }
-      }
-      const long long at_pos = pos + depth;
-      v.nc = (int)min((unsigned)rows.nc, (unsigned)(at_pos + 1) / (unsigned)p.ratio);
-      v.ra = (int)min(max(at_pos - p.window + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
-      v.rb = (int)min(max(at_pos + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
-    }
-  };
-  enter_unit();
-
+  bool enter = true;
   // A field of segment sg: a choice of two constants.
   auto of = [&](int sg, auto field) { return sg != 0 ? p.seg[1].*field : p.seg[0].*field; };
-  // Tile whose page ids are in flight, then tile whose rows are known.
-  int a_row[kMine], a_page[kMine], a_seen[kMine], a_flags = 0, a_own = 0, a_tok0 = 0;
-  bool a_full = false, b_full = false, b_tma = false;
-  unsigned long long b_at[kMine];
-  int b_page[kMine], b_slot[kMine], b_seen[kMine], b_flags = 0, b_own = 0, b_tok0 = 0;
-  float b_ks[kMine], b_vs[kMine];
-
-  auto fetch_pages = [&]() {
-    const int base = j * kRows, len = rows.len();
-    const bool head = left == nt || j == 0;
-    if (head) first_j = j;
-    const bool last = j == rec.z - 1 || left == 1;
-    a_flags = (head ? TF_FIRST : 0) | (last ? TF_LAST : 0) | (last && first_j == 0 && j == rec.z - 1 ? TF_WHOLE : 0) |
-              (first_j == 0 ? TF_HEAD : 0);
-    a_own = own_tok;
-    a_tok0 = tok0;
-    a_full = p.run_rows > 0 && base + kRows <= min(view[0].nc, view[1].nc);
+  for (int g = 0; g < nt; ++g) {
+    const int buf = g % kListsT;
+    if (enter) {
+      if (rec.x != seq) {
+        seq = rec.x;
+        geom = p.geom[seq];
+        span = tokens_of(p, seq);
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int r = gtid + k * kGroup, x = base + r;
-      a_row[k] = a_page[k] = -1;
-      a_seen[k] = 0;
-      if (r < kRows && x < len) {
-        const int sg = x < rows.nc ? 1 : 0;
-        int row = x;
-        if (sg != 0) {
-          a_seen[k] = (x < view[0].nc ? 1 : 0) | (x < view[1].nc ? 2 : 0);
-        } else if (x < rows.nc + rows.nr) {
-          row = rows.r0 + (x - rows.nc);
-          a_seen[k] = (row >= view[0].ra && row < view[0].rb ? 1 : 0) | (row >= view[1].ra && row < view[1].rb ? 2 : 0);
+        for (int k = 0; k < 4; ++k)
+          par[k] = !chain && 32 * k + lane < min(span.n, kTreeTokens) ? p.parent[span.at + 32 * k + lane] : -1;
+      }
+      if (left > rec.z - j) next_rec = p.ws_unit[u + 1];
+      const int t0 = rec.y, t1 = min(rec.y + 1, span.n - 1);
+      rows = unit_rows(p, geom, span.n, t0, t1);
+      const long long pos = max(geom.x, 0), raw_pos0 = max(geom.z, 0);
+      const bool dead = !chain && t0 >= kTreeTokens;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        View &v = view[i];
+        const int t = i == 0 ? t0 : t1;
+        v.nc = v.ra = v.rb = v.da = v.db = 0;
+        v.anc[0] = v.anc[1] = v.anc[2] = v.anc[3] = 0;
+        if (dead) continue;
+        int depth = 0;
+        if (chain) {
+          depth = t;
+          v.da = max(0, t - p.window + 1);
+          v.db = t + 1;
         } else {
-          const int d = rows.d0 + (x - rows.nc - rows.nr);
-          row = rows.n_raw + d;
+          // Up to the root; every lane alike.  (Each step goes to an earlier node.)
+#pragma unroll 1
+          for (int at = t;; ++depth) {
+            if (depth < p.window) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t w = d < 32 ? view[i].anc[0] : d < 64 ? view[i].anc[1] : d < 96 ? view[i].anc[2] : view[i].anc[3];
-            const bool seen = chain ? d >= view[i].da && d < view[i].db : ((w >> (d & 31)) & 1u) != 0;
-            a_seen[k] |= seen ? 1 << i : 0;
-          }
-        }
-        const int shift = of(sg, &PagedSeg::page_shift), per = of(sg, &PagedSeg::page_rows);
-        const int pi = shift >= 0 ? row >> shift : row / per;
-        if (a_seen[k] != 0) {
-          a_page[k] = of(sg, &PagedSeg::table)[rec.x * of(sg, &PagedSeg::table_stride) + pi];
-          a_row[k] = 2 * (row - pi * per) + sg;
-        }
-      }
-    }
-    // On to the next tile.
-    --left;
-    if (left > 0 && ++j == rec.z) {
-      j = 0;
-      rec = p.ws_unit[++u];
-      enter_unit();
-    }
-  };
-  auto find_rows = [&]() {
-    b_flags = a_flags;
-    b_own = a_own;
-    b_tok0 = a_tok0;
-    b_full = a_full;
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      b_at[k] = pad_row;
-      b_page[k] = a_page[k];
-      b_slot[k] = a_row[k] >> 1;
-      b_seen[k] = 0;
-      b_ks[k] = 0.f;
-      b_vs[k] = 1.f;
-      const int sg = a_row[k] & 1;
-      if (a_row[k] >= 0 && (unsigned)a_page[k] < (unsigned)of(sg, &PagedSeg::n_pages)) {
-        const int slot = a_row[k] >> 1;
-        b_seen[k] = a_seen[k];
-        b_at[k] = reinterpret_cast<unsigned long long>(of(sg, &PagedSeg::k) + a_page[k] * of(sg, &PagedSeg::page_stride) +
-                                                       slot * of(sg, &PagedSeg::row_stride)) |
-                  sg;
-        if (FP8) {
-          const long long sr = (long long)a_page[k] * of(sg, &PagedSeg::page_rows) + slot;
-          b_ks[k] = of(sg, &PagedSeg::k_scale)[sr];
-          b_vs[k] = of(sg, &PagedSeg::v_scale)[sr];
-        }
-      }
-    }
-    // A V row that one token sees and the other does not must be finite, because
-    // its weight of 0 multiplies it all the same: the warp looks these few rows
-    // through (new rows, edges of a window).  One that is not finite is left out
-    // of the product, and the token that sees it is marked.
-    if (!b_full) {
-#pragma unroll
-      for (int k = 0; k < kMine; ++k) {
-        unsigned who = __ballot_sync(0xffffffffu, b_seen[k] == 1 || b_seen[k] == 2);
-        unsigned bad = 0;
-        while (who != 0) {
-          constexpr int kAhead = 4;
-          uint4 v[kAhead][FP8 ? 1 : 2];
-          int l[kAhead];
-#pragma unroll
-          for (int a = 0; a < kAhead; ++a) {
-            l[a] = who != 0 ? __ffs(who) - 1 : -1;
-            who &= who - 1;
-            const unsigned long long e = __shfl_sync(0xffffffffu, b_at[k], max(l[a], 0));
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? vdelta1 : vdelta0);
-#pragma unroll
-            for (int w = 0; w < (FP8 ? 1 : 2); ++w)
-              v[a][w] = l[a] >= 0 ? reinterpret_cast<const uint4 *>(src)[32 * w + lane] : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int a = 0; a < kAhead; ++a) {
-            bool odd = false;
-#pragma unroll
-            for (int w = 0; w < (FP8 ? 1 : 2); ++w) {
-              const uint32_t x[4] = {v[a][w].x, v[a][w].y, v[a][w].z, v[a][w].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (FP8) {
-                  // A code of NaN: seven ones.  (Adding 1 to each seven carries into the eighth.)
-                  odd = odd || (((x[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-                } else {
-                  // An exponent of five ones.
-                  odd = odd || (((x[i] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0;
-                }
-              }
+              for (int k = 0; k < 4; ++k)
+                if (at >> 5 == k) v.anc[k] |= 1u << (at & 31);
             }
-            if (__ballot_sync(0xffffffffu, odd) != 0 && l[a] >= 0) bad |= 1u << l[a];
+            const int mine = at < 32 ? par[0] : at < 64 ? par[1] : at < 96 ? par[2] : par[3];
+            const int up = __shfl_sync(0xffffffffu, mine, at & 31);
+            if (up < 0 || up >= at) break;
+            at = up;
           }
         }
-        if ((bad >> lane) & 1u) b_at[k] |= kNoValue;
-        if (__ballot_sync(0xffffffffu, ((bad >> lane) & 1u) != 0 && ((b_seen[k] >> rank) & 1) != 0) != 0)
-          b_flags |= TF_SPOILED;
+        const long long at_pos = pos + depth;
+        v.nc = (int)min((unsigned)rows.nc, (unsigned)(at_pos + 1) / (unsigned)p.ratio);
+        v.ra = (int)min(max(at_pos - p.window + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
+        v.rb = (int)min(max(at_pos + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
       }
+      enter = false;
     }
-  };
-  // The rows of tile g, complete for the whole group; all go on or none.
-  // Returns whether TMA loads the tile.
-  auto store_list = [&](int g) -> bool {
-    const int buf = g % kListsT;
-    const bool full = b_full;
-    bool absent = false;
-    b_tma = false;
-    if (ok && !mbar_wait(smem_u32(&ms.list_empty[buf]), ((g / kListsT) & 1) ^ 1, abrt, p.timeout_ns, p.err,
-                         TSITE_LIST_EMPTY))
-      ok = false;
+    const int base = j * kRows, len = rows.len();
+    bool tma = p.run_rows > 0 && base + kRows <= min(view[0].nc, view[1].nc), spoiled = false;
+    // (Page ids before the wait for a free list.)
+    int run_page = -1, run_slot = 0;
+    if (tma && lane < n_runs) {
+      const int row = base + (lane << p.run_shift), pi = p.seg[1].page_shift >= 0 ? row >> p.seg[1].page_shift : row / p.seg[1].page_rows;
+      run_page = p.seg[1].table[seq * p.seg[1].table_stride + pi];
+      run_slot = row - pi * p.seg[1].page_rows;
+    }
+    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_empty[buf]), ((g / kListsT) & 1) ^ 1, TSITE_LIST_EMPTY,
+                                            &ms.wait)))
+      return;
+    if (tma) {
+      tma = __all_sync(0xffffffffu, lane >= n_runs || (unsigned)run_page < (unsigned)p.seg[1].n_pages);
+      if (lane < n_runs) ms.box[buf][lane] = make_int2(run_page, run_slot);
+      if (lane < kRows / 32) ms.mask[buf][lane] = 0xFFFFFFFFu;
+    }
+    if (FP8 || !tma) {
+      uint32_t mixed[kRows / 32];  // rows that one token sees and the other does not
+      constexpr int kStep = 4;     // rows of a lane whose loads go together
+#pragma unroll 1
+      for (int k0 = 0; k0 < kRows / 32; k0 += kStep) {
+        int page[kStep], slot2[kStep], seen[kStep];  // page, 2 * slot + segment, who sees it
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int r = gtid + k * kGroup;
-      if (r < kRows) {  // whole warps
-        const unsigned seen = __ballot_sync(0xffffffffu, (b_seen[k] >> rank) & 1);
-        if (ok) {
-          ms.row[buf][r] = b_at[k];
-          if (lane == 0) ms.mask[buf][r >> 5] = seen;
-          absent = absent || (b_at[k] & kNoRowT);
-          if (full && (r & (p.run_rows - 1)) == 0) ms.box[buf][r >> p.run_shift] = make_int2(b_page[k], b_slot[k]);
+        for (int k = 0; k < kStep; ++k) {
+          const int x = base + 32 * (k0 + k) + lane;
+          page[k] = -1;
+          slot2[k] = seen[k] = 0;
+          int row = x, sg = 1;
+          if (x < rows.nc) {
+            seen[k] = (x < view[0].nc ? 1 : 0) | (x < view[1].nc ? 2 : 0);
+          } else if (x < rows.nc + rows.nr) {
+            sg = 0;
+            row = rows.r0 + (x - rows.nc);
+            seen[k] = (row >= view[0].ra && row < view[0].rb ? 1 : 0) | (row >= view[1].ra && row < view[1].rb ? 2 : 0);
+          } else if (x < len) {
+            sg = 0;
+            const int d = rows.d0 + (x - rows.nc - rows.nr);
+            row = rows.n_raw + d;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t w = d < 32 ? view[i].anc[0] : d < 64 ? view[i].anc[1] : d < 96 ? view[i].anc[2] : view[i].anc[3];
+              const bool s = chain ? d >= view[i].da && d < view[i].db : ((w >> (d & 31)) & 1u) != 0;
+              seen[k] |= s ? 1 << i : 0;
+            }
+          }
+          if (seen[k] != 0) {
+            const int shift = of(sg, &PagedSeg::page_shift), per = of(sg, &PagedSeg::page_rows);
+            const int pi = shift >= 0 ? row >> shift : row / per;
+            page[k] = of(sg, &PagedSeg::table)[seq * of(sg, &PagedSeg::table_stride) + pi];
+            slot2[k] = 2 * (row - pi * per) + sg;
+          }
         }
-      }
-    }
-    __syncwarp();  // the barrier below is one of whole warps
-    const bool odd = bar_red_or(3, kGroup, !ok || (full && absent));
-    if (odd) ok = !bar_red_or(3, kGroup, !ok);
-    b_tma = full && !odd;
-    return b_tma;
-  };
-  // The rest of it, once its rows are on their way: what the other warps need.
-  auto finish_list = [&](int g) {
-    const int buf = g % kListsT;
-    const bool spoiled = bar_red_or(3, kGroup, (b_flags & TF_SPOILED) != 0);
-    if (ok) {
-      if (FP8) {
+        float ks[kStep], vs[kStep];
+        unsigned long long at[kStep];
 #pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-          const int r = gtid + k * kGroup;
-          if (r < kRows) {
-            ms.ksc[buf][r] = p.scale_log2 * b_ks[k];
-            const float lv = fmaxf(__log2f(b_vs[k]), kLeastLog2ScaleT);
+        for (int k = 0; k < kStep; ++k) {
+          const int sg = slot2[k] & 1, slot = slot2[k] >> 1;
+          at[k] = pad_row;
+          ks[k] = 0.f;
+          vs[k] = 1.f;
+          if ((unsigned)page[k] < (unsigned)of(sg, &PagedSeg::n_pages)) {
+            at[k] = reinterpret_cast<unsigned long long>(of(sg, &PagedSeg::k) + page[k] * of(sg, &PagedSeg::page_stride) +
+                                                         slot * of(sg, &PagedSeg::row_stride)) |
+                    sg;
+            if (FP8) {
+              const long long sr = (long long)page[k] * of(sg, &PagedSeg::page_rows) + slot;
+              ks[k] = of(sg, &PagedSeg::k_scale)[sr];
+              vs[k] = of(sg, &PagedSeg::v_scale)[sr];
+            }
+          } else {
+            seen[k] = 0;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          const int r = 32 * (k0 + k) + lane;
+          const unsigned own = __ballot_sync(0xffffffffu, (seen[k] >> rank) & 1);
+          const unsigned odd = __ballot_sync(0xffffffffu, seen[k] == 1 || seen[k] == 2);
+          if (!tma) {
+            ms.row[buf][r] = at[k];
+            if (lane == 0) ms.mask[buf][k0 + k] = own;
+          }
+          if (k0 == 0) mixed[k] = odd; else mixed[kStep + k] = odd;
+          if (FP8) {
+            ms.ksc[buf][r] = p.scale_log2 * ks[k];
+            const float lv = fmaxf(__log2f(vs[k]), kLeastLog2ScaleT);
             ms.lvs[buf][r] = lv;
             ms.ivs[buf][r] = exp2f(-lv);
           }
         }
       }
-      if (gtid == 0) {
-        ms.flags[buf] = (b_flags & ~TF_SPOILED) | (spoiled ? TF_SPOILED : 0) | (b_tma ? 0 : TF_GATHERED);
-        ms.tok[buf] = b_own;
-      }
-    }
-    mbar_arrive(smem_u32(&ms.list_full[buf]));
-  };
-  // One part of tile g into the next stage: parts 0-7 dims 64 part .. of this
-  // CTA's K rows, parts 8-15 (nb, kq): dims 256 nb + 128 rank .. of V rows 64 kq ..
-  auto emit = [&](int g, int part, bool tma) -> bool {
-    const uint32_t slot = FP8 ? sbase + kOffRing + 4 * kPart + ring.st * kCodePart : sbase + kOffRing + ring.st * kPart;
-    const uint32_t b_full_bar = smem_u32(FP8 ? &ms.code_full[ring.st] : &ms.kv_full[ring.st]);
-    const uint32_t b_empty = smem_u32(FP8 ? &ms.code_empty[ring.st] : &ms.kv_empty[ring.st]);
-    const uint32_t ph = ring.ph ^ 1, st_bit = 1u << ring.st;
-    ring.advance();
-    // Every thread waits for every fill of a stage, whoever loads it: a parity
-    // wait is only right for a thread that has seen the phase before.
-    if (!(FP8 ? mbar_wait(b_empty, ph, abrt, p.timeout_ns, p.err, TSITE_CODE_EMPTY)
-              : mbar_wait(b_empty, ph, abrt, p.timeout_ns, p.err, TSITE_KV_EMPTY)))
-      return false;
-    const bool is_v = part >= 8;
-    const int nb = (part >> 2) & 1, kq = part & 3;
-    const int row0 = is_v ? 64 * kq : 128 * (int)rank;           // first row of the part within the tile
-    const int dim0 = is_v ? 256 * nb + 128 * (int)rank : 64 * part;
-    const int buf = g % kListsT;
-    if (tma) {
-      // Run i of a part goes to one lane of warp (turn + i) % warps; lane 0 of
-      // each warp arrives for all its lanes.
-      const int runs = (is_v ? 64 : 128) >> p.run_shift;
-      const int first = gwarp - turn, i = (first < 0 ? first + kWarps : first) + lane * kWarps;
-      turn = (turn + runs) % kWarps;
-      // (fp16: the bytes of both CTAs count at rank 0's barrier; here only the issue does.)
-      if (lane == 0) {
-        const bool expects = gtid == 0 && (FP8 || rank == 0);
-        if (expects) mbar_arrive_expect_tx(b_full_bar, FP8 ? kCodePart : 2 * kPart);
-        mbar_arrive_cnt(b_full_bar, expects ? 31 : 32);
-      }
-      if (i < runs) {
-        filled |= st_bit;
-        last_par = ph ? last_par & ~st_bit : last_par | st_bit;
-        const uint32_t dst = slot + (i << p.run_shift) * (is_v ? (FP8 ? 128u : 256u) : (FP8 ? 64u : 128u));
-        const CUtensorMap *m = is_v ? &p.tm_v : &p.tm_k;
-        const int2 x = ms.box[buf][(row0 >> p.run_shift) + i];
-        if (FP8)
-          tma_load_3d(dst, m, b_full_bar, dim0, x.y, x.x);
-        else
-          tma_load_5d_pair(dst, m, cluster_addr(b_full_bar, 0), 0, 0, dim0 >> 6, x.y >> 3, x.x);
-      }
-      return true;
-    }
-    const unsigned long long *list = ms.row[buf] + row0;
-    const long long off0 = (is_v ? vdelta0 : 0) + (FP8 ? dim0 : 2 * dim0), off1 = (is_v ? vdelta1 : 0) + (FP8 ? dim0 : 2 * dim0);
-    const unsigned long long skip = is_v ? kNoRowT | kNoValue : kNoRowT;
-    if (FP8) {
-      // 16 codes a copy: 4 copies a row of K, 8 of V; 512 in all.
-      for (int i = gtid; i < 512; i += kGroup) {
-        const int row = is_v ? i >> 3 : i >> 2, c = is_v ? i & 7 : i & 3;
-        const unsigned long long e = list[row];
-        cp_async16z(slot + 16 * i, reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? off1 : off0) + 16 * c,
-                    (e & skip) ? 0u : 16u);
-      }
-    } else if (!is_v) {
+      // A V row that one token sees and the other does not must be finite, because
+      // its weight of 0 multiplies it all the same: the warp looks these few rows
+      // through (new rows, edges of a window).  One that is not finite is left out
+      // of the product, and the token that sees it is marked.
+      __syncwarp();
+      unsigned any = 0;
 #pragma unroll
-      for (int it = 0; it < (128 + kRowStep - 1) / kRowStep; ++it) {
-        const int row = kRowStep * it + rsub;
-        if (row >= 128) break;
-        const unsigned long long e = list[row];
-        cp_async16z(slot + (row >> 3) * 1024 + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4),
-                    reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? off1 : off0) + 16 * c8,
-                    (e & skip) ? 0u : 16u);
-      }
-    } else {
+      for (int k = 0; k < kRows / 32; ++k) any |= mixed[k] != 0 ? 1u << k : 0;
+#pragma unroll 1
+      while (!tma && any != 0) {
+        const int k = __ffs(any) - 1;
+        any &= any - 1;
+        unsigned who = 0;
 #pragma unroll
-      for (int it = 0; it < (64 + kRowStep - 1) / kRowStep; ++it) {
-        const int row = kRowStep * it + rsub;
-        if (row >= 64) break;
-        const unsigned long long e = list[row];
-        const uint32_t dst = slot + (row >> 3) * 2048 + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4), n = (e & skip) ? 0u : 16u;
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? off1 : off0) + 16 * c8;
-        cp_async16z(dst, src, n);
-        cp_async16z(dst + 1024, src + 128, n);
+        for (int m = 0; m < kRows / 32; ++m) who = m == k ? mixed[m] : who;
+#pragma unroll 1
+        while (who != 0) {
+          constexpr int kAhead = 8, kWords = FP8 ? 1 : 2;
+          uint4 v[kAhead][kWords];
+          int r[kAhead];
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a) {
+            r[a] = who != 0 ? 32 * k + __ffs(who) - 1 : -1;
+            who &= who - 1;
+            const unsigned long long e = r[a] >= 0 ? ms.row[buf][r[a]] : 0;
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? vdelta1 : vdelta0);
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+              v[a][w] = r[a] >= 0 ? reinterpret_cast<const uint4 *>(src)[32 * w + lane] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+              const uint32_t x[4] = {v[a][w].x, v[a][w].y, v[a][w].z, v[a][w].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                odd |= FP8 ? ((x[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u   // a code of NaN: seven ones
+                           : ((x[i] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;  // an exponent of five ones
+            }
+            if (__any_sync(0xffffffffu, odd != 0)) {
+              spoiled = spoiled || ((ms.mask[buf][k] >> (r[a] & 31)) & 1u) != 0;
+              if (lane == 0) ms.row[buf][r[a]] |= kNoValue;
+            }
+          }
+        }
       }
     }
-    cp_async_arrive(b_full_bar);
-    return true;
-  };
-  auto load_q = [&]() {
-    if (gtid == 0 && ok) {
-      if (!mbar_wait(smem_u32(&ms.q_empty), (n_item & 1) ^ 1, abrt, p.timeout_ns, p.err, TSITE_Q_EMPTY)) {
-        ok = false;
-      } else {
-        mbar_arrive_expect_tx(smem_u32(&ms.q_full), kQBytes);
-        tma_load_4d(sbase, &p.tm_q, smem_u32(&ms.q_full), 0, 0, b_own >= 0 ? b_own : b_tok0, 0);
-        q_issued = true;
-        q_par = n_item & 1;
-      }
+    const bool head = g == 0 || j == 0, last = j == rec.z - 1 || left == 1;
+    if (head) first_j = j;
+    if (lane == 0) {
+      const int t = span.at + rec.y, two = rec.y + 1 < span.n;
+      ms.flags[buf] = (head ? TF_FIRST : 0) | (last ? TF_LAST : 0) | (last && first_j == 0 && j == rec.z - 1 ? TF_WHOLE : 0) |
+                      (first_j == 0 ? TF_HEAD : 0) | (tma ? 0 : TF_GATHERED) | (spoiled ? TF_SPOILED : 0);
+      ms.tok[buf] = rank == 0 ? t : two ? t + 1 : -1;
+      ms.q_tok[buf] = rank == 0 || !two ? t : t + 1;
     }
-    ++n_item;
-  };
+    warp_arrive(smem_u32(&ms.list_full[buf]));
+    --left;
+    if (++j == rec.z) {
+      j = 0;
+      ++u;
+      rec = next_rec;
+      enter = true;
+    }
+  }
+}
 
-  fetch_pages();
-  bool tma = false, tma_v;  // whether TMA loads tile g, and tile g - 1
-  for (int g = 0; g <= nt; ++g) {
-    tma_v = tma;
-    if (g < nt) {
-      find_rows();
-      if (g + 1 < nt) fetch_pages();
-      tma = store_list(g);
-      if (b_flags & TF_FIRST) load_q();
-      // The list before the last K parts: the ring holds fewer than a tile's eight,
-      // and who empties it waits for the list.
-      for (int part = 0; part < 4 && ok; ++part) ok = emit(g, part, tma);
+// ------------------------------------------------------------------ loaders
+
+// The warps of K, or of V, load part after part into their ring: by TMA, a run per lane
+// (warps in turn), or by 16-byte copies.  E4M3: one warp for both, K one tile ahead.
+template <bool FP8>
+__device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, uint32_t rank, uint32_t sbase, TMisc &ms,
+                                               bool v_warp, int tid) {
+  if (nt <= 0) return;
+  const int n_warps = v_warp ? kVLoadWarps<FP8> : kKLoadWarps<FP8>, n_threads = 32 * n_warps;
+  const int lane = tid & 31, warp = tid >> 5;
+  const long long vdelta0 = p.seg[0].v - p.seg[0].k, vdelta1 = p.seg[1].v - p.seg[1].k;
+  uint32_t st_k = 0, ph_k = 1, st_v = 0, ph_v = 1;  // next stage of either ring and the parity to wait for
+  uint32_t filled = 0, last_par = 0, n_item = 0;
+  bool ok = true, q_issued = false;
+  // Step i loads K of tile i / 2 (even) or V of the tile before (odd): warps of
+  // one kind have every other step.
+  const int steps = 2 * nt + 2;
+#pragma unroll 1
+  for (int i = FP8 ? 0 : v_warp ? 3 : 0; i < steps && ok; i += FP8 ? 1 : 2) {
+    const bool is_v = i & 1;
+    const int g = is_v ? (i >> 1) - 1 : i >> 1;
+    if (g < 0 || g >= nt) continue;
+    const int buf = g % kListsT;
+    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait))) break;
+    const int flags = ms.flags[buf];
+    if (!is_v && (flags & TF_FIRST)) {
+      if (tid == 0) {
+        if (!wait_phase(smem_u32(&ms.q_empty), (n_item & 1) ^ 1, TSITE_Q_EMPTY, &ms.wait)) {
+          ok = false;
+        } else {
+          mbar_arrive_expect_tx(smem_u32(&ms.q_full), kQBytes);
+          tma_load_4d(sbase, &p.tm_q, smem_u32(&ms.q_full), 0, 0, ms.q_tok[buf], 0);
+          q_issued = true;
+        }
+      }
+      ++n_item;
       __syncwarp();
-      finish_list(g);
-      for (int part = 4; part < 8 && ok; ++part) ok = emit(g, part, tma);
-    } else {
-      __syncwarp();
-      ok = !bar_red_or(3, kGroup, !ok);
     }
-    if (g > 0)
-      for (int part = 8; part < kParts && ok; ++part) ok = emit(g - 1, part, tma_v);
+    const bool tma = !(flags & TF_GATHERED);
+    const int runs = (is_v ? 64 : 128) >> p.run_shift;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      // Part c of K is dims 64 c .. of this CTA's rows; of V (nb, kq) dims 256 nb + 128 rank .. of rows 64 kq ..
+      const int row0 = is_v ? 64 * (c & 3) : 128 * (int)rank;
+      const int dim0 = is_v ? 256 * (c >> 2) + 128 * (int)rank : 64 * c;
+      const uint32_t st = is_v ? (FP8 ? kCodeSlots : kKStages<false>) + st_v : st_k, ph = is_v ? ph_v : ph_k;
+      const uint32_t slot = sbase + kOffRing + (FP8 ? 4 * kPart + st * kCodePart : st * kPart);
+      const uint32_t b_full = smem_u32(FP8 ? &ms.code_full[st] : &ms.kv_full[st]);
+      if (!__all_sync(0xffffffffu, wait_phase(smem_u32(FP8 ? &ms.code_empty[st] : &ms.kv_empty[st]), ph,
+                                              FP8 ? TSITE_CODE_EMPTY : TSITE_KV_EMPTY, &ms.wait))) {
+        ok = false;
+        break;
+      }
+      if (tma) {
+        // fp16: the bytes of both CTAs count at rank 0's barrier; rank 1's has the issue only.
+        if (lane == 0) {
+          const bool expects = warp == 0 && (FP8 || rank == 0);
+          if (expects) mbar_arrive_expect_tx(b_full, FP8 ? kCodePart : 2 * kPart);
+          mbar_arrive_cnt(b_full, expects ? 31 : 32);
+        }
+        const int turn = warp - c % n_warps, run = (turn < 0 ? turn + n_warps : turn) + lane * n_warps;
+        if (run < runs) {
+          const uint32_t dst = slot + (run << p.run_shift) * (is_v ? (FP8 ? 128u : 256u) : (FP8 ? 64u : 128u));
+          const CUtensorMap *m = is_v ? &p.tm_v : &p.tm_k;
+          const int2 x = ms.box[buf][(row0 >> p.run_shift) + run];
+          filled |= 1u << st;
+          last_par = ph ? last_par & ~(1u << st) : last_par | 1u << st;
+          if (FP8)
+            tma_load_3d(dst, m, b_full, dim0, x.y, x.x);
+          else
+            tma_load_5d_pair(dst, m, cluster_addr(b_full, 0), 0, 0, dim0 >> 6, x.y >> 3, x.x);
+        }
+      } else {
+        // A part's row has 8 (K) or 16 (V) copies, of E4M3 codes half as many.
+        const unsigned long long *list = ms.row[buf] + row0;
+        const long long off0 = (is_v ? vdelta0 : 0) + (FP8 ? dim0 : 2 * dim0), off1 = (is_v ? vdelta1 : 0) + (FP8 ? dim0 : 2 * dim0);
+        const unsigned long long skip = is_v ? kNoRowT | kNoValue : kNoRowT;
+        const int shift = (is_v ? 4 : 3) - (FP8 ? 1 : 0), copies = FP8 ? 512 : 1024;
+#pragma unroll 4
+        for (int k = tid; k < copies; k += n_threads) {
+          const int row = k >> shift, x = k & ((1 << shift) - 1);
+          const unsigned long long e = list[row];
+          uint32_t dst = slot + 16 * k;
+          if (!FP8)
+            dst = slot + (row & 7) * 128 + (((x & 7) ^ (row & 7)) << 4) +
+                  (is_v ? (row >> 3) * 2048 + (x >> 3) * 1024 : (row >> 3) * 1024);
+          cp_async16z(dst, reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? off1 : off0) + 16 * x,
+                      (e & skip) ? 0u : 16u);
+        }
+        cp_async_arrive(b_full);
+      }
+      if (is_v) {
+        if (++st_v == (FP8 ? kCodeSlots : kVStages<false>)) st_v = 0, ph_v ^= 1;
+      } else {
+        if (++st_k == (FP8 ? kCodeSlots : kKStages<false>)) st_k = 0, ph_k ^= 1;
+      }
+    }
     __syncwarp();
+    if (ok && (!FP8 || is_v)) warp_arrive(smem_u32(&ms.list_empty[buf]));
   }
   // No copy may still be landing at exit.  (When every wait succeeded the MMA
-  // warp has seen all stages land.)
+  // warps have seen all stages land.)
   cp_async_done();
-  volatile int never = 0;
-  if (*abrt != 0)
-    for (int st = 0; st < kSlots; ++st)
+  if (ms.wait.abort_flag != 0) {
+    volatile int never = 0;
+    for (int st = 0; st < 7; ++st)
       if (filled & (1u << st))
         mbar_wait(smem_u32(FP8 ? &ms.code_full[st] : &ms.kv_full[st]), (last_par >> st) & 1, &never, 100000000ull,
                   p.err, TSITE_DRAIN);
-  if (gtid == 0 && q_issued) mbar_wait(smem_u32(&ms.q_full), q_par, &never, 100000000ull, p.err, TSITE_DRAIN);
+    if (q_issued) mbar_wait(smem_u32(&ms.q_full), (n_item & 1) ^ 1, &never, 100000000ull, p.err, TSITE_DRAIN);
+  }
 }
 
-// Warps 9-12 with E4M3 rows: a slot's codes, 64 a thread, widened exactly into
-// the next stage in the layout that the fp16 kernel's copies have.
-__device__ __forceinline__ void tree_convert_role(const TreeAttnParams &p, int nt, uint32_t sbase, TMisc &ms, int ct) {
-  volatile int *abrt = &ms.abort_flag;
+// Warps 9 and 10 (K) or 11 and 12 (V) with E4M3 rows: a slot's codes, 128 a thread,
+// widened exactly into the next stage in the layout that the fp16 kernel's copies have.
+__device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &ms, bool is_v, int ct) {
+  const uint32_t slot0 = is_v ? kCodeSlots : 0, stage0 = is_v ? kKStages<true> : 0;
+  static_assert(kKStages<true> == kVStages<true>, "one ring length for both");
   Ring<kCodeSlots> codes;
-  Ring<kStagesT<true>> ring;
-  for (long long i = 0; i < (long long)nt * kParts; ++i) {
-    // Stages come as K(0), then K(g + 1) and V(g): the first eight, then by turns, the last eight of V.
-    const long long eighth = i >> 3, last = 2ll * nt - 1;
-    const bool is_v = eighth != 0 && (eighth == last || (eighth & 1) == 0);
-    if (!mbar_wait(smem_u32(&ms.code_full[codes.st]), codes.ph, abrt, p.timeout_ns, p.err, TSITE_CODE_FULL)) return;
-    const uint32_t src = sbase + kOffRing + 4 * kPart + codes.st * kCodePart, dst = sbase + kOffRing + ring.st * kPart;
-    uint4 raw[4];
+  Ring<kKStages<true>> ring;
+#pragma unroll 1
+  for (int i = 0; i < 8 * nt; ++i) {
+    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[slot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait))) return;
+    const uint32_t src = sbase + kOffRing + 4 * kPart + (slot0 + codes.st) * kCodePart;
+    const uint32_t dst = sbase + kOffRing + (stage0 + ring.st) * kPart;
+    uint4 raw[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 8; ++k)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(raw[k].x), "=r"(raw[k].y), "=r"(raw[k].z), "=r"(raw[k].w)
-                   : "r"(src + 16 * (ct + 128 * k)));
-    __syncwarp();
-    if ((ct & 31) == 0) mbar_arrive(smem_u32(&ms.code_empty[codes.st]));
-    if (!mbar_wait(smem_u32(&ms.kv_empty[ring.st]), ring.ph ^ 1, abrt, p.timeout_ns, p.err, TSITE_KV_EMPTY)) return;
+                   : "r"(src + 16 * (ct + 64 * k)));
+    warp_arrive(smem_u32(&ms.code_empty[slot0 + codes.st]));
+    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.kv_empty[stage0 + ring.st]), ring.ph ^ 1, TSITE_KV_EMPTY, &ms.wait))) return;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = ct + 128 * k;
+    for (int k = 0; k < 8; ++k) {
+      const int n = ct + 64 * k;
       const int row = is_v ? n >> 3 : n >> 2, c = is_v ? n & 7 : n & 3;  // 16 codes: chunks 2c, 2c + 1 of 8 values
       const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
       uint32_t h[8];
@@ -648,7 +615,7 @@ __device__ __forceinline__ void tree_convert_role(const TreeAttnParams &p, int n
       sts_v4(drow + ((col ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
       sts_v4(drow + (((col + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
     }
-    mbar_arrive(smem_u32(&ms.kv_full[ring.st]));
+    warp_arrive(smem_u32(&ms.kv_full[stage0 + ring.st]));
     codes.advance();
     ring.advance();
   }
@@ -656,136 +623,101 @@ __device__ __forceinline__ void tree_convert_role(const TreeAttnParams &p, int n
 
 // ------------------------------------------------------------------ MMA issue and relay
 
-// The CTA of rank 1 has no MMA to issue: its last warp tells the other CTA what
-// has landed here.  Gathered and widened rows are generic-proxy writes: the fence
-// makes them visible to the tensor core before the news goes out.
+// The CTA of rank 1 has no MMA to issue: these warps (one lane) tell the other CTA
+// what has landed here, stage by stage.  Gathered and widened rows are generic-proxy
+// writes: the fence makes them visible to the tensor core before the news goes out.
 template <bool FP8>
-__device__ __forceinline__ void tree_relay_role(const TreeAttnParams &p, int nt, TMisc &ms) {
-  volatile int *abrt = &ms.abort_flag;
-  Ring<kStagesT<FP8>> ring;
-  uint32_t item = 0;
-  auto parts = [&](int n) -> bool {
-    for (int i = 0; i < n; ++i) {
-      if (!mbar_wait(smem_u32(&ms.kv_full[ring.st]), ring.ph, abrt, p.timeout_ns, p.err, TSITE_KV_FULL)) return false;
-      fence_proxy_async_smem();
-      mbar_arrive_cluster(cluster_addr(smem_u32(&ms.kv_full[ring.st]), 0));
-      ring.advance();
-    }
-    return true;
-  };
-  if (nt <= 0) return;
+__device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v) {
+  const uint32_t stage0 = is_v ? kKStages<FP8> : 0, stages = is_v ? kVStages<FP8> : kKStages<FP8>;
+  uint32_t st = 0, ph = 0, item = 0;
+#pragma unroll 1
   for (int g = 0; g < nt; ++g) {
     const int buf = g % kListsT;
-    if (!mbar_wait(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, abrt, p.timeout_ns, p.err, TSITE_LIST_FULL)) return;
-    const int flags = ms.flags[buf];
-    mbar_arrive(smem_u32(&ms.list_empty[buf]));
-    if (flags & TF_FIRST) {
-      if (!mbar_wait(smem_u32(&ms.q_full), item & 1, abrt, p.timeout_ns, p.err, TSITE_Q_FULL)) return;
-      mbar_arrive_cluster(cluster_addr(smem_u32(&ms.peer_q_full), 0));
-      ++item;
+    if (!is_v) {
+      if (!wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait)) return;
+      const int flags = ms.flags[buf];
+      mbar_arrive(smem_u32(&ms.list_empty[buf]));
+      if (flags & TF_FIRST) {
+        if (!wait_phase(smem_u32(&ms.q_full), item & 1, TSITE_Q_FULL, &ms.wait)) return;
+        mbar_arrive_cluster(cluster_addr(smem_u32(&ms.peer_q_full), 0));
+        ++item;
+      }
     }
-    if (!parts(8)) return;
-    if (g > 0 && !parts(8)) return;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t bar = smem_u32(&ms.kv_full[stage0 + st]);
+      if (!wait_phase(bar, ph, TSITE_KV_FULL, &ms.wait)) return;
+      fence_proxy_async_smem();
+      mbar_arrive_cluster(cluster_addr(bar, 0));
+      if (++st == stages) st = 0, ph ^= 1;
+    }
   }
-  parts(8);
 }
 
-// The whole warp walks the tiles, so that descriptors are warp-uniform values, and
-// one elected lane issues.  Waits are joined over the warp: all lanes go on or none.
-template <bool FP8>
-__device__ __forceinline__ void tree_mma_role(const TreeAttnParams &p, int nt, uint32_t sbase, uint32_t tmem, TMisc &ms) {
-  volatile int *abrt = &ms.abort_flag;
-  constexpr uint32_t kIdescQK = idesc_f16_f32(128, 256, false, false);
-  constexpr uint32_t kIdescPV = idesc_f16_f32(128, 256, false, true);
+// Two warps issue, Q . K and P . V, each the products of its own ring: the wait for a
+// stage, the issue and the commits take a warp some 400 cycles a stage, its MMAs
+// 256; one warp for both took 6,400 cycles a tile.  The whole warp walks the tiles, so that
+// descriptors are warp-uniform values, and one elected lane issues.  Waits are
+// joined over the warp: all lanes go on or none.
+template <bool FP8, bool IS_V>
+__device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t tmem, TMisc &ms) {
+  constexpr uint32_t kIdesc = idesc_f16_f32(128, 256, false, IS_V);
+  constexpr int kStage0 = IS_V ? kKStages<FP8> : 0;
   // Q, K and P: K-major.  V: MN-major, LBO = distance of the 64-dim blocks, SBO =
   // distance of 8-row groups.
-  const uint64_t q_desc = sdesc_sw128(sbase, 16, 1024);
-  const uint64_t k_desc = sdesc_sw128(sbase + kOffRing, 16, 1024);
-  const uint64_t p_desc = sdesc_sw128(sbase + kOffTP, 16, 1024);
-  const uint64_t v_desc = sdesc_sw128(sbase + kOffRing, 1024, 2048);
-  Ring<kStagesT<FP8>> ring;
-  uint32_t q_item = 0, o_item = 0;
-  auto wait = [&](uint64_t &bar, uint32_t parity, unsigned int site) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abrt, p.timeout_ns, p.err, site));
+  const uint64_t a_desc = IS_V ? sdesc_sw128(sbase + kOffTP, 16, 1024) : sdesc_sw128(sbase, 16, 1024);
+  const uint64_t b_desc = IS_V ? sdesc_sw128(sbase + kOffRing + kStage0 * kPart, 1024, 2048)
+                               : sdesc_sw128(sbase + kOffRing, 16, 1024);
+  Ring<IS_V ? kVStages<FP8> : kKStages<FP8>> ring;
+  uint32_t item = 0;
+  auto wait = [&](uint64_t &bar, uint32_t parity, uint32_t site) -> bool {
+    return __all_sync(0xffffffffu, wait_phase(smem_u32(&bar), parity, site, &ms.wait));
   };
-  auto stage_ready = [&](bool gathered) -> bool {
-    if (!wait(ms.kv_full[ring.st], ring.ph, TSITE_KV_FULL)) return false;
-    if (FP8 || gathered) fence_proxy_async_smem();
-    return true;
-  };
-  auto qk = [&](int g, int flags) -> bool {
+#pragma unroll 1
+  for (int g = 0; g < nt; ++g) {
+    const int buf = g % kListsT;
+    if (!wait(ms.list_full[buf], (g / kListsT) & 1, TSITE_LIST_FULL)) return;
+    const int flags = ms.flags[buf];
+    warp_arrive(smem_u32(&ms.list_empty[buf]));
+    const bool first = flags & TF_FIRST, last = flags & TF_LAST, fence = FP8 || (flags & TF_GATHERED);
     const uint32_t sb = g & 1;
-    if (flags & TF_FIRST) {
-      if (!wait(ms.q_full, q_item & 1, TSITE_Q_FULL) || !wait(ms.peer_q_full, q_item & 1, TSITE_Q_FULL)) return false;
-      ++q_item;
+    if (IS_V) {
+      if (first && !wait(ms.o_empty, (item & 1) ^ 1, TSITE_O_EMPTY)) return;
+      if (!wait(ms.p_full, g & 1, TSITE_P_FULL)) return;
+    } else {
+      if (first && (!wait(ms.q_full, item & 1, TSITE_Q_FULL) || !wait(ms.peer_q_full, item & 1, TSITE_Q_FULL))) return;
+      if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, TSITE_S_EMPTY)) return;
     }
-    if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, TSITE_S_EMPTY)) return false;
+    if (first) ++item;
     tc_fence_after();
-    const uint32_t d = tmem + kTmemTS + 128 * sb;
+#pragma unroll 1
     for (int c = 0; c < 8; ++c) {
-      if (!stage_ready(flags & TF_GATHERED)) return false;
-      const uint64_t a0 = sdesc_add(q_desc, c * kQBoxBytes), b0 = sdesc_add(k_desc, ring.st * kPart);
+      if (!wait(ms.kv_full[kStage0 + ring.st], ring.ph, TSITE_KV_FULL)) return;
+      if (fence) fence_proxy_async_smem();
+      const uint64_t a0 = sdesc_add(a_desc, (IS_V ? c & 3 : c) * 8192);
+      const uint64_t b0 = sdesc_add(b_desc, ring.st * kPart);
+      const uint32_t d = IS_V ? tmem + 128 * (c >> 2) : tmem + kTmemTS + 128 * sb;
+      const bool fresh = IS_V ? first && (c & 3) == 0 : c == 0;
       if (elect_lane()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           if (ks == 0)
-            umma_pair_f16(d, a0, b0, kIdescQK, c != 0 ? 1u : 0u);
+            umma_pair_f16(d, a0, b0, kIdesc, fresh ? 0u : 1u);
           else
-            umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * 32), kIdescQK);
+            umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * (IS_V ? 4096 : 32)), kIdesc);
         }
-        umma_pair_commit(smem_u32(&ms.kv_empty[ring.st]));
-        if (c == 7) umma_pair_commit(smem_u32(&ms.s_full[sb]));
-        if (c == 7 && (flags & TF_LAST)) umma_pair_commit(smem_u32(&ms.q_empty));
+        umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + ring.st]));
+        if (IS_V) {
+          if ((c & 3) == 3 && last) umma_pair_commit(smem_u32(&ms.o_full[c >> 2]));
+          if (c == 7) umma_pair_commit(smem_u32(&ms.p_empty));
+        } else if (c == 7) {
+          umma_pair_commit(smem_u32(&ms.s_full[sb]));
+          if (last) umma_pair_commit(smem_u32(&ms.q_empty));
+        }
       }
       __syncwarp();
       ring.advance();
     }
-    return true;
-  };
-  auto pv = [&](int g, int flags) -> bool {
-    if (!wait(ms.p_full, g & 1, TSITE_P_FULL)) return false;
-    const bool first = flags & TF_FIRST;
-    if (first) {
-      if (!wait(ms.o_empty, (o_item & 1) ^ 1, TSITE_O_EMPTY)) return false;
-      ++o_item;
-    }
-    tc_fence_after();
-    for (int c = 0; c < 8; ++c) {
-      const int nb = c >> 2, kq = c & 3;
-      if (!stage_ready(flags & TF_GATHERED)) return false;
-      const uint64_t a0 = sdesc_add(p_desc, kq * kPBox), b0 = sdesc_add(v_desc, ring.st * kPart);
-      const uint32_t d = tmem + 128 * nb;
-      if (elect_lane()) {
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (ks == 0)
-            umma_pair_f16(d, a0, b0, kIdescPV, first && kq == 0 ? 0u : 1u);
-          else
-            umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * 4096), kIdescPV);
-        }
-        umma_pair_commit(smem_u32(&ms.kv_empty[ring.st]));
-        if (kq == 3 && (flags & TF_LAST)) umma_pair_commit(smem_u32(&ms.o_full[nb]));
-        if (c == 7) umma_pair_commit(smem_u32(&ms.p_empty));
-      }
-      __syncwarp();
-      ring.advance();
-    }
-    return true;
-  };
-  bool ok = true;
-  int flags = 0;
-  for (int g = 0; g <= nt && ok; ++g) {
-    const int before = flags;
-    if (g < nt) {
-      const int buf = g % kListsT;
-      ok = wait(ms.list_full[buf], (g / kListsT) & 1, TSITE_LIST_FULL);
-      if (!ok) break;
-      flags = ms.flags[buf];
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms.list_empty[buf]));
-      ok = qk(g, flags);
-    }
-    if (ok && g > 0) ok = pv(g - 1, before);
   }
 }
 
@@ -809,26 +741,28 @@ __device__ __forceinline__ void stg32(void *at, const uint32_t (&w)[8]) {
 template <bool FP8>
 __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int nt, int cluster, uint32_t rank,
                                                   uint8_t *smem, uint32_t tmem, TMisc &ms, int tid) {
-  volatile int *abrt = &ms.abort_flag;
   const int w = tid >> 5, l = tid & 31;
   const int q = w & 3, hh = w >> 2, half = q >> 1;
   const int h = 32 * (q & 1) + l, box = 2 * half + hh;
   const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
   const uint32_t group = 1 + (q & 1);
-  const uint32_t r_s_empty[2] = {cluster_addr(smem_u32(&ms.s_empty[0]), 0), cluster_addr(smem_u32(&ms.s_empty[1]), 0)};
-  const uint32_t r_p_full = cluster_addr(smem_u32(&ms.p_full), 0), r_o_empty = cluster_addr(smem_u32(&ms.o_empty), 0);
-  auto tell = [&](uint32_t bar) {  // one arrival per warp
+  auto tell = [&](uint64_t &bar) {  // one arrival per warp, at rank 0's barrier
     __syncwarp();
-    if (l == 0) mbar_arrive_cluster(bar);
+    if (l == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&bar), 0));
   };
   bool bad = false, spoiled = false;
+  auto wait = [&](uint64_t &bar, uint32_t parity, uint32_t site) {
+    bad = bad || !wait_phase(smem_u32(&bar), parity, site, &ms.wait);
+    __syncwarp();
+  };
   uint32_t n_item = 0;
   float m_ref = kNoRefT, m_lim = kNoRefT, lsum = 0.f;
   uint8_t *prow = smem + kOffTP + box * kPBox + (h >> 3) * 1024 + (h & 7) * 128;
+#pragma unroll 1
   for (int g = 0; g < nt; ++g) {
     const int buf = g % kListsT;
-    const uint32_t sb = g & 1;
-    bad = bad || !mbar_wait(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, abrt, p.timeout_ns, p.err, TSITE_LIST_FULL);
+    const uint32_t sb = g & 1, s_at = tmem + kTmemTS + 128 * sb + 64 * hh + lanes;
+    wait(ms.list_full[buf], (g / kListsT) & 1, TSITE_LIST_FULL);
     const int flags = ms.flags[buf], tok = ms.tok[buf];
     const uint32_t see0 = ms.mask[buf][2 * box], see1 = ms.mask[buf][2 * box + 1];
     if (flags & TF_FIRST) {
@@ -837,40 +771,45 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       spoiled = false;
     }
     spoiled = spoiled || (flags & TF_SPOILED);
-    if (!FP8) mbar_arrive(smem_u32(&ms.list_empty[buf]));
-    bad = bad || !mbar_wait(smem_u32(&ms.s_full[sb]), (g >> 1) & 1, abrt, p.timeout_ns, p.err, TSITE_S_FULL);
+    if (!FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
+    wait(ms.s_full[sb], (g >> 1) & 1, TSITE_S_FULL);
     tc_fence_after();
-    float s[64];
-    tmem_ld64(tmem + kTmemTS + 128 * sb + 64 * hh + lanes, s);
-    tmem_wait_ld();
-    tc_fence_before();
-    tell(r_s_empty[sb]);
-    if (FP8) {
-      const float4 *ks = reinterpret_cast<const float4 *>(ms.ksc[buf] + 64 * box);
-      const float4 *lv = reinterpret_cast<const float4 *>(ms.lvs[buf] + 64 * box);
+    // 32 scores a time, twice over: for their maximum, then for the weights.  (Held in
+    // registers for both, the code is twice as long.)
+    auto scores = [&](int c0, float (&s)[32]) {
+      tmem_ld32(s_at + c0, s);
+      tmem_wait_ld();
+      if (FP8) {
+        const float4 *ks = reinterpret_cast<const float4 *>(ms.ksc[buf] + 64 * box + c0);
+        const float4 *lv = reinterpret_cast<const float4 *>(ms.lvs[buf] + 64 * box + c0);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float4 k = ks[c], v = lv[c];
-        s[4 * c] = fmaf(s[4 * c], k.x, v.x);
-        s[4 * c + 1] = fmaf(s[4 * c + 1], k.y, v.y);
-        s[4 * c + 2] = fmaf(s[4 * c + 2], k.z, v.z);
-        s[4 * c + 3] = fmaf(s[4 * c + 3], k.w, v.w);
+        for (int c = 0; c < 8; ++c) {
+          const float4 k = ks[c], v = lv[c];
+          s[4 * c] = fmaf(s[4 * c], k.x, v.x);
+          s[4 * c + 1] = fmaf(s[4 * c + 1], k.y, v.y);
+          s[4 * c + 2] = fmaf(s[4 * c + 2], k.z, v.z);
+          s[4 * c + 3] = fmaf(s[4 * c + 3], k.w, v.w);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] *= p.scale_log2;
       }
-    } else {
+      const uint32_t see = c0 == 0 ? see0 : see1;
+      if (see != 0xFFFFFFFFu) {
 #pragma unroll
-      for (int c = 0; c < 64; ++c) s[c] *= p.scale_log2;
-    }
-    if ((see0 & see1) != 0xFFFFFFFFu) {
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        s[c] = (see0 >> c) & 1u ? s[c] : -INFINITY;
-        s[c + 32] = (see1 >> c) & 1u ? s[c + 32] : -INFINITY;
+        for (int c = 0; c < 32; ++c) s[c] = (see >> c) & 1u ? s[c] : -INFINITY;
       }
-    }
-    float mx[4] = {s[0], s[1], s[2], s[3]};
+    };
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c0 = 0; c0 < 64; c0 += 32) {
+      float s[32];
+      scores(c0, s);
+      float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      for (int c = 4; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+      top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+    }
     bool moved = false;
     float alpha = 1.f;
     if (bar_red_or(group, 128, top > m_lim || bad)) {
@@ -888,37 +827,41 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       moved = true;
       lsum *= alpha;
     }
-    bad = bad || !mbar_wait(smem_u32(&ms.p_empty), (g & 1) ^ 1, abrt, p.timeout_ns, p.err, TSITE_P_EMPTY);
-    {
-      // This head's 64 weights: 16-byte chunk c of its 128 bytes at c ^ (h & 7).
-      // Rounded once to fp16 for the product; the sums add them unrounded, sixteen
-      // at a time, so that lse keeps fp32 precision over long rows.
+    wait(ms.p_empty, (g & 1) ^ 1, TSITE_P_EMPTY);
+    // This head's 64 weights: 16-byte chunk c of its 128 bytes at c ^ (h & 7).
+    // Rounded once to fp16 for the product; the sums add them unrounded, eight at
+    // a time, so that lse keeps fp32 precision over long rows.
+#pragma unroll 1
+    for (int c0 = 0; c0 < 64; c0 += 32) {
+      float s[32];
+      scores(c0, s);
       float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t w4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int x = 8 * c + 2 * i;
           const float e0 = exp2f(s[x] - m_ref), e1 = exp2f(s[x + 1] - m_ref);
+          __half2 hp = __floats2half2_rn(e0, e1);
           if (FP8) {
-            const float2 iv = *reinterpret_cast<const float2 *>(&ms.ivs[buf][64 * box + x]);
-            const float2 lv = *reinterpret_cast<const float2 *>(&ms.lvs[buf][64 * box + x]);
+            const float2 iv = *reinterpret_cast<const float2 *>(&ms.ivs[buf][64 * box + c0 + x]);
             part[i] = fmaf(e0, iv.x, fmaf(e1, iv.y, part[i]));
             // A V scale of 0: weight, but no value.
-            const __half2 hp = __floats2half2_rn(lv.x <= kLeastLog2ScaleT ? 0.f : e0, lv.y <= kLeastLog2ScaleT ? 0.f : e1);
-            w4[i] = *reinterpret_cast<const uint32_t *>(&hp);
+            if (iv.x >= kMostScaleInv || iv.y >= kMostScaleInv)
+              hp = __floats2half2_rn(iv.x >= kMostScaleInv ? 0.f : e0, iv.y >= kMostScaleInv ? 0.f : e1);
           } else {
             part[i] += e0 + e1;
-            const __half2 hp = __floats2half2_rn(e0, e1);
-            w4[i] = *reinterpret_cast<const uint32_t *>(&hp);
           }
+          w4[i] = *reinterpret_cast<const uint32_t *>(&hp);
         }
-        *reinterpret_cast<uint4 *>(prow + ((c ^ (h & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        *reinterpret_cast<uint4 *>(prow + (((c0 / 8 + c) ^ (h & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
       }
       lsum += (part[0] + part[1]) + (part[2] + part[3]);
     }
-    if (FP8) mbar_arrive(smem_u32(&ms.list_empty[buf]));
+    tc_fence_before();
+    tell(ms.s_empty[sb]);
+    if (FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
     if (moved && !(flags & TF_FIRST)) {
       tc_fence_after();
 #pragma unroll 1
@@ -934,7 +877,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    tell(r_p_full);
+    tell(ms.p_full);
     if (!(flags & TF_LAST)) continue;
 
     // End of an item: the sum over a head's four threads, then this thread's 128
@@ -953,7 +896,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       else if (p.lse != nullptr)
         p.lse[(long long)tok * kH + h] = none ? -INFINITY : (m_ref + log2f(sum)) * kLn2;
     }
-    bad = bad || !mbar_wait(smem_u32(&ms.o_full[hh]), n_item & 1, abrt, p.timeout_ns, p.err, TSITE_O_FULL);
+    wait(ms.o_full[hh], n_item & 1, TSITE_O_FULL);
     tc_fence_after();
     const int dim0 = 256 * hh + 128 * half;
 #pragma unroll 1
@@ -991,7 +934,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       }
     }
     tc_fence_before();
-    tell(r_o_empty);
+    tell(ms.o_empty);
     ++n_item;
     if (bar_red_or(group, 128, bad)) break;  // (and the sums have been read)
   }
@@ -1013,16 +956,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     mbar_init(smem_u32(&ms.q_empty), 1);
     mbar_init(smem_u32(&ms.peer_q_full), 1);
     for (int s = 0; s < 7; ++s) {
-      mbar_init(smem_u32(&ms.kv_full[s]), (FP8 ? 128 : kLoadersT<false>) + (rank == 0 ? 1 : 0));
+      // Loader threads, or the two warps that widen; and the other CTA's report.
+      const int loaders = 32 * (s < kKStages<false> ? kKLoadWarps<false> : kVLoadWarps<false>);
+      mbar_init(smem_u32(&ms.kv_full[s]), (FP8 ? 2 : loaders) + (rank == 0 ? 1 : 0));
       mbar_init(smem_u32(&ms.kv_empty[s]), 1);
     }
-    for (int s = 0; s < kCodeSlots; ++s) {
-      mbar_init(smem_u32(&ms.code_full[s]), kLoadersT<true>);
-      mbar_init(smem_u32(&ms.code_empty[s]), 4);
+    for (int s = 0; s < 2 * kCodeSlots; ++s) {
+      mbar_init(smem_u32(&ms.code_full[s]), 32);
+      mbar_init(smem_u32(&ms.code_empty[s]), 2);
     }
     for (int s = 0; s < kListsT; ++s) {
-      mbar_init(smem_u32(&ms.list_full[s]), kLoadersT<FP8>);
-      mbar_init(smem_u32(&ms.list_empty[s]), kComputeThreads + 1);
+      mbar_init(smem_u32(&ms.list_full[s]), 1);
+      mbar_init(smem_u32(&ms.list_empty[s]), kComputeWarps + (rank == 0 ? 2 : 1) +
+                                                 (FP8 ? 1 : kKLoadWarps<false> + kVLoadWarps<false>));
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ms.s_full[s]), 1);
@@ -1032,8 +978,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     mbar_init(smem_u32(&ms.p_full), 2 * kComputeWarps);
     mbar_init(smem_u32(&ms.p_empty), 1);
     mbar_init(smem_u32(&ms.o_empty), 2 * kComputeWarps);
-    mbar_init(smem_u32(&ms.mma_done), 1);
-    ms.abort_flag = 0;
+    mbar_init(smem_u32(&ms.mma_done), 2);
+    ms.wait.timeout_ns = p.timeout_ns;
+    ms.wait.err = p.err;
+    ms.wait.abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.tm_q);
     if (p.run_rows > 0) {
@@ -1041,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       tma_prefetch_desc(&p.tm_v);
     }
   }
-  if (warp == kMmaWarp) tmem_alloc_pair(smem_u32(&ms.tmem_base), kTmemCols);
+  if (warp == kQkWarp) tmem_alloc_pair(smem_u32(&ms.tmem_base), kTmemCols);
   tc_fence_before();
   __syncthreads();
   cluster_barrier();  // both CTAs' barriers and TMEM are ready
@@ -1054,30 +1002,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const int nt = (int)max(0ll, min((long long)head.y, head.x - before));
   if (warp < kComputeWarps) {
     tree_softmax_role<FP8>(p, nt, cluster, rank, smem, tmem, ms, threadIdx.x);
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kPvWarp) {
+    const bool is_v = warp == kPvWarp, lane0 = (threadIdx.x & 31) == 0;
     if (rank == 0) {
-      tree_mma_role<FP8>(p, nt, sbase, tmem, ms);
+      if (is_v)
+        tree_mma_role<FP8, true>(nt, sbase, tmem, ms);
+      else
+        tree_mma_role<FP8, false>(nt, sbase, tmem, ms);
       __syncwarp();
       if (elect_lane()) umma_pair_commit(smem_u32(&ms.mma_done));
-    } else if ((threadIdx.x & 31) == 0) {
-      tree_relay_role<FP8>(p, nt, ms);
+    } else if (lane0) {
+      tree_relay_role<FP8>(nt, ms, is_v);
     }
     __syncwarp();
     volatile int never = 0;
     mbar_wait(smem_u32(&ms.mma_done), 0, &never, 3 * p.timeout_ns, p.err, TSITE_DRAIN);
     __syncwarp();
+  } else if (warp == kListWarp) {
+    tree_list_role<FP8>(p, nt, cluster, rank, ms, threadIdx.x & 31);
+  } else if (FP8 && warp >= kWidenWarp0) {
+    const bool is_v = warp >= kWidenWarp0 + 2;
+    tree_widen_role(nt, sbase, ms, is_v, (threadIdx.x - 32 * kWidenWarp0) & 63);
   } else {
-    const int ltid = threadIdx.x - 32 * kLoaderWarp0;
-    if (FP8 && ltid >= 32 && ltid < 160)
-      tree_convert_role(p, nt, sbase, ms, ltid - 32);
-    else
-      tree_load_role<FP8>(p, nt, cluster, rank, sbase, ms, ltid);
+    const bool is_v = !FP8 && warp >= kVLoadWarp0;
+    tree_load_role<FP8>(p, nt, rank, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kVLoadWarp0 : kKLoadWarp0));
   }
   tc_fence_before();
   __syncthreads();
   cluster_barrier();  // neither CTA leaves while the other may still arrive here, or its MMAs read
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+  if (warp == kQkWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
 // ------------------------------------------------------------------ merge
