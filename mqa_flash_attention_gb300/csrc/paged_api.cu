@@ -170,7 +170,7 @@ TreeSpace tree_space(int32_t n_seq, int32_t n_tok, int ctas) {
   const size_t slots = 4 * (size_t)t.clusters;
   t.start = 256;
   t.unit = t.start + align256(4 * ((size_t)t.clusters + 1));
-  t.seq = t.unit + align256(16 * (size_t)t.max_units);
+  t.seq = t.unit + align256(128 * (size_t)t.max_units);
   t.ml = t.seq + align256(4 * (size_t)n_seq);
   t.o = t.ml + align256(slots * DS4A_HEADS * sizeof(float2));
   t.bytes = t.o + slots * DS4A_HEADS * DS4A_HEAD_DIM * sizeof(float);
@@ -538,7 +538,7 @@ ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout
   p.max_units = t.max_units;
   p.ws_head = reinterpret_cast<int4 *>(ws);
   p.ws_start = reinterpret_cast<int *>(ws + t.start);
-  p.ws_unit = reinterpret_cast<int4 *>(ws + t.unit);
+  p.ws_unit = ws + t.unit;
   p.ws_seq = reinterpret_cast<int *>(ws + t.seq);
   p.ws_ml = reinterpret_cast<float2 *>(ws + t.ml);
   p.ws_o = reinterpret_cast<float *>(ws + t.o);

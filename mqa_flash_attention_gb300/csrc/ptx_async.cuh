@@ -57,6 +57,19 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32
   return mbar_try_wait(bar, parity) || wait_long(bar, parity, site, w);
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One arrival for a converged warp, behind what its lanes did before.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();

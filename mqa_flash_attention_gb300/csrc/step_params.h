@@ -68,7 +68,7 @@ struct TreeAttnParams {
   // Workspace.
   int4 *ws_head;           // (tiles, tiles of a cluster, units, -)
   int *ws_start;           // [clusters] unit of a cluster's first tile
-  int4 *ws_unit;           // [max_units] (sequence, first token, tiles, tiles before)
+  void *ws_unit;           // [max_units] 128 bytes each
   int *ws_seq;             // [n_seq] units before
   float2 *ws_ml;           // [4 clusters][64] (m in log2 units, l)
   float *ws_o;             // [4 clusters][64][512] normalised partial outputs

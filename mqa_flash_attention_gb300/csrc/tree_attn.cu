@@ -86,6 +86,18 @@ enum : unsigned int {
   TSITE_CODE_EMPTY
 };
 
+// What a cluster has to know of a unit, as 32 words (a warp reads one a lane).
+struct UnitRec {
+  int seq, t0, tiles, before;        // sequence, first token, tiles, tiles of all units before
+  int nc, r0, nr, d0, len, n_raw;    // the list (UnitRows)
+  int tok, two;                      // first token counted over all sequences; whether there is a second
+  int nc_of[2], ra[2], rb[2];        // what either token sees: compressed rows below nc_of, cached rows ra .. rb - 1,
+  int da[2], db[2];                  // new rows da .. db - 1 of a run,
+  uint32_t anc[2][4];                // and of a tree those with a bit set
+  int pad[2];
+};
+static_assert(sizeof(UnitRec) == 128, "a word per lane");
+
 struct TMisc {
   alignas(16) unsigned long long row[kListsT][kRows];  // K address | bits (of gathered tiles)
   alignas(16) float ksc[kListsT][kRows];               // E4M3: scale * log2(e) * K scale
@@ -102,6 +114,7 @@ struct TMisc {
   uint64_t s_full[2], s_empty[2], o_full[2];
   uint64_t p_full, p_empty, o_empty, mma_done;
   WaitBox wait;
+  UnitRec unit;   // of the tile that is listed
   uint32_t tmem_base;
 };
 constexpr uint32_t kTreeSmem = kOffTMisc + ((sizeof(TMisc) + 127) / 128) * 128 + 1024;
@@ -177,9 +190,58 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sum, int &all) {
   return v;
 }
 
+__device__ __forceinline__ void unit_record(const TreeAttnParams &p, int seq, int t0, UnitRec &r) {
+  const bool chain = p.parent == nullptr;
+  const Span2 s = tokens_of(p, seq);
+  const int4 g = p.geom[seq];
+  const int t1 = min(t0 + 1, s.n - 1);
+  const UnitRows rows = unit_rows(p, g, s.n, t0, t1);
+  const long long pos = max(g.x, 0), raw_pos0 = max(g.z, 0);
+  r.seq = seq;
+  r.t0 = t0;
+  r.tiles = rows.tiles();
+  r.nc = rows.nc;
+  r.r0 = rows.r0;
+  r.nr = rows.nr;
+  r.d0 = rows.d0;
+  r.len = rows.len();
+  r.n_raw = rows.n_raw;
+  r.tok = s.at + t0;
+  r.two = t1 > t0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = i == 0 ? t0 : t1;
+    r.nc_of[i] = r.ra[i] = r.rb[i] = r.da[i] = r.db[i] = 0;
+    r.anc[i][0] = r.anc[i][1] = r.anc[i][2] = r.anc[i][3] = 0;
+    if (!chain && t0 >= kTreeTokens) continue;  // nodes that see nothing
+    int depth = 0;
+    if (chain) {
+      depth = t;
+      r.da[i] = max(0, t - p.window + 1);
+      r.db[i] = t + 1;
+    } else {
+      for (int at = t;; ++depth) {  // up to the root, each step to an earlier node
+        if (depth < p.window) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (at >> 5 == k) r.anc[i][k] |= 1u << (at & 31);
+        }
+        const int up = p.parent[s.at + at];
+        if (up < 0 || up >= at) break;
+        at = up;
+      }
+    }
+    const long long at_pos = pos + depth;
+    r.nc_of[i] = (int)min((unsigned)rows.nc, (unsigned)(at_pos + 1) / (unsigned)p.ratio);
+    r.ra[i] = (int)min(max(at_pos - p.window + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
+    r.rb[i] = (int)min(max(at_pos + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAttnParams p) {
   __shared__ int warp_sum[32];
   const int tid = threadIdx.x;
+  UnitRec *recs = static_cast<UnitRec *>(p.ws_unit);
   grid_launch_dependents();
   grid_dependency_wait();
   int units = 0;  // of the sequences before
@@ -195,21 +257,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
   int tiles = 0;
   for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int u = u0 + tid;
-    int4 rec = make_int4(0, 0, 0, 0);
+    UnitRec rec;
+    rec.tiles = 0;
     if (u < units) {
       int lo = 0, hi = p.n_seq;  // the last sequence whose units begin at or before u
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (p.ws_seq[mid] <= u) lo = mid; else hi = mid;
       }
-      const int n = tokens_of(p, lo).n, t0 = 2 * (u - p.ws_seq[lo]);
-      rec = make_int4(lo, t0, unit_rows(p, p.geom[lo], n, t0, min(t0 + 1, n - 1)).tiles(), 0);
+      unit_record(p, lo, 2 * (u - p.ws_seq[lo]), rec);
     }
     int all;
-    const int inc = block_scan(rec.z, warp_sum, all);
+    const int inc = block_scan(rec.tiles, warp_sum, all);
     if (u < units) {
-      rec.w = tiles + inc - rec.z;
-      p.ws_unit[u] = rec;
+      rec.before = tiles + inc - rec.tiles;
+      rec.pad[0] = rec.pad[1] = 0;
+      recs[u] = rec;
     }
     tiles += all;
   }
@@ -218,18 +281,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
   __syncthreads();
   // The unit of each cluster's first tile.
   for (int u = tid; u < units; u += kPlanThreads) {
-    const int4 rec = p.ws_unit[u];
-    for (int i = (rec.w + per - 1) / per; (long long)i * per < rec.w + rec.z; ++i) p.ws_start[i] = u;
+    const int at = recs[u].before, n = recs[u].tiles;
+    for (int i = (at + per - 1) / per; (long long)i * per < at + n; ++i) p.ws_start[i] = u;
   }
 }
 
 // ------------------------------------------------------------------ lists
-
-// What token i of the unit sees of the list.
-struct View {
-  int nc, ra, rb, da, db;
-  uint32_t anc[4];
-};
 
 // One warp goes ahead of all others and writes down, per tile, what is in it.  A full
 // tile (compressed rows that both tokens see, in runs that TMA can copy) is no more than
@@ -243,75 +300,32 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
   const int pad_seg = p.seg[1].max_rows > 0 ? 1 : 0;
   const unsigned long long pad_row = reinterpret_cast<unsigned long long>(p.seg[pad_seg].k) | pad_seg | kNoRowT;
   const int n_runs = p.run_rows > 0 ? kRows >> p.run_shift : 0;  // of a tile that TMA loads
+  const int *recs = static_cast<const int *>(p.ws_unit);
 
-  int u = p.ws_start[cluster], left = nt;
-  int4 rec = p.ws_unit[u], next_rec = rec;
-  int j = cluster * p.ws_head[0].y - rec.w, first_j = j, seq = -1;
-  int4 geom;
-  Span2 span;
-  int par[4];
-  UnitRows rows;
-  View view[2];
+  int u = p.ws_start[cluster], left = nt, j = 0, first_j = 0;
+  int word = recs[32 * u + lane];  // of the unit that is entered next
   bool enter = true;
-  // A field of segment sg: a choice of two constants.
-  auto of = [&](int sg, auto field) { return sg != 0 ? p.seg[1].*field : p.seg[0].*field; };
+  UnitRec &r = ms.unit;
+  const int32_t *table0 = nullptr, *table1 = nullptr;
   for (int g = 0; g < nt; ++g) {
     const int buf = g % kListsT;
     if (enter) {
-      if (rec.x != seq) {
-        seq = rec.x;
-        geom = p.geom[seq];
-        span = tokens_of(p, seq);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          par[k] = !chain && 32 * k + lane < min(span.n, kTreeTokens) ? p.parent[span.at + 32 * k + lane] : -1;
-      }
-      if (left > rec.z - j) next_rec = p.ws_unit[u + 1];
-      const int t0 = rec.y, t1 = min(rec.y + 1, span.n - 1);
-      rows = unit_rows(p, geom, span.n, t0, t1);
-      const long long pos = max(geom.x, 0), raw_pos0 = max(geom.z, 0);
-      const bool dead = !chain && t0 >= kTreeTokens;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        View &v = view[i];
-        const int t = i == 0 ? t0 : t1;
-        v.nc = v.ra = v.rb = v.da = v.db = 0;
-        v.anc[0] = v.anc[1] = v.anc[2] = v.anc[3] = 0;
-        if (dead) continue;
-        int depth = 0;
-        if (chain) {
-          depth = t;
-          v.da = max(0, t - p.window + 1);
-          v.db = t + 1;
-        } else {
-          // Up to the root; every lane alike.  (Each step goes to an earlier node.)
-#pragma unroll 1
-          for (int at = t;; ++depth) {
-            if (depth < p.window) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (at >> 5 == k) v.anc[k] |= 1u << (at & 31);
-            }
-            const int mine = at < 32 ? par[0] : at < 64 ? par[1] : at < 96 ? par[2] : par[3];
-            const int up = __shfl_sync(0xffffffffu, mine, at & 31);
-            if (up < 0 || up >= at) break;
-            at = up;
-          }
-        }
-        const long long at_pos = pos + depth;
-        v.nc = (int)min((unsigned)rows.nc, (unsigned)(at_pos + 1) / (unsigned)p.ratio);
-        v.ra = (int)min(max(at_pos - p.window + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
-        v.rb = (int)min(max(at_pos + 1 - raw_pos0, 0ll), (long long)rows.n_raw);
-      }
+      __syncwarp();
+      reinterpret_cast<int *>(&r)[lane] = word;
+      __syncwarp();
+      j = g == 0 ? cluster * p.ws_head[0].y - r.before : 0;
+      if (left > r.tiles - j) word = recs[32 * (u + 1) + lane];
+      table0 = p.seg[0].table + r.seq * p.seg[0].table_stride;
+      table1 = p.seg[1].table + r.seq * p.seg[1].table_stride;
       enter = false;
     }
-    const int base = j * kRows, len = rows.len();
-    bool tma = p.run_rows > 0 && base + kRows <= min(view[0].nc, view[1].nc), spoiled = false;
+    const int base = j * kRows, nc = r.nc;
+    bool tma = p.run_rows > 0 && base + kRows <= min(r.nc_of[0], r.nc_of[1]), spoiled = false;
     // (Page ids before the wait for a free list.)
     int run_page = -1, run_slot = 0;
     if (tma && lane < n_runs) {
       const int row = base + (lane << p.run_shift), pi = p.seg[1].page_shift >= 0 ? row >> p.seg[1].page_shift : row / p.seg[1].page_rows;
-      run_page = p.seg[1].table[seq * p.seg[1].table_stride + pi];
+      run_page = table1[pi];
       run_slot = row - pi * p.seg[1].page_rows;
     }
     if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_empty[buf]), ((g / kListsT) & 1) ^ 1, TSITE_LIST_EMPTY,
@@ -323,77 +337,86 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
       if (lane < kRows / 32) ms.mask[buf][lane] = 0xFFFFFFFFu;
     }
     if (FP8 || !tma) {
-      uint32_t mixed[kRows / 32];  // rows that one token sees and the other does not
-      constexpr int kStep = 4;     // rows of a lane whose loads go together
+      constexpr int kStep = 8;  // rows of a lane whose loads go together
+      unsigned mixed_any = 0, mixed_of = 0;  // words with rows that one token sees and the other does not; lane k: word k
 #pragma unroll 1
       for (int k0 = 0; k0 < kRows / 32; k0 += kStep) {
-        int page[kStep], slot2[kStep], seen[kStep];  // page, 2 * slot + segment, who sees it
+        int page[kStep];
+        unsigned what[kStep];  // slot * 8 | segment * 4 | who sees it
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
           const int x = base + 32 * (k0 + k) + lane;
           page[k] = -1;
-          slot2[k] = seen[k] = 0;
-          int row = x, sg = 1;
-          if (x < rows.nc) {
-            seen[k] = (x < view[0].nc ? 1 : 0) | (x < view[1].nc ? 2 : 0);
-          } else if (x < rows.nc + rows.nr) {
+          what[k] = 0;
+          int row = x;
+          unsigned seen = 0, sg = 1;
+          if (x < nc) {
+            seen = (x < r.nc_of[0] ? 1 : 0) | (x < r.nc_of[1] ? 2 : 0);
+          } else if (x < r.len) {
             sg = 0;
-            row = rows.r0 + (x - rows.nc);
-            seen[k] = (row >= view[0].ra && row < view[0].rb ? 1 : 0) | (row >= view[1].ra && row < view[1].rb ? 2 : 0);
-          } else if (x < len) {
-            sg = 0;
-            const int d = rows.d0 + (x - rows.nc - rows.nr);
-            row = rows.n_raw + d;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t w = d < 32 ? view[i].anc[0] : d < 64 ? view[i].anc[1] : d < 96 ? view[i].anc[2] : view[i].anc[3];
-              const bool s = chain ? d >= view[i].da && d < view[i].db : ((w >> (d & 31)) & 1u) != 0;
-              seen[k] |= s ? 1 << i : 0;
+            const int at = x - nc;
+            if (at < r.nr) {
+              row = r.r0 + at;
+              seen = (row >= r.ra[0] && row < r.rb[0] ? 1 : 0) | (row >= r.ra[1] && row < r.rb[1] ? 2 : 0);
+            } else {
+              const int d = r.d0 + (at - r.nr);
+              row = r.n_raw + d;
+              if (chain)
+                seen = (d >= r.da[0] && d < r.db[0] ? 1 : 0) | (d >= r.da[1] && d < r.db[1] ? 2 : 0);
+              else
+                seen = ((r.anc[0][d >> 5] >> (d & 31)) & 1u) | (((r.anc[1][d >> 5] >> (d & 31)) & 1u) << 1);
             }
           }
-          if (seen[k] != 0) {
-            const int shift = of(sg, &PagedSeg::page_shift), per = of(sg, &PagedSeg::page_rows);
+          if (seen != 0) {
+            const int shift = sg != 0 ? p.seg[1].page_shift : p.seg[0].page_shift;
+            const int per = sg != 0 ? p.seg[1].page_rows : p.seg[0].page_rows;
             const int pi = shift >= 0 ? row >> shift : row / per;
-            page[k] = of(sg, &PagedSeg::table)[seq * of(sg, &PagedSeg::table_stride) + pi];
-            slot2[k] = 2 * (row - pi * per) + sg;
+            page[k] = (sg != 0 ? table1 : table0)[pi];
+            what[k] = (unsigned)(row - pi * per) << 3 | sg << 2 | seen;
           }
         }
-        float ks[kStep], vs[kStep];
         unsigned long long at[kStep];
+        float ks[kStep], vs[kStep];
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
-          const int sg = slot2[k] & 1, slot = slot2[k] >> 1;
+          const bool sg = what[k] & 4;
+          const int slot = (int)(what[k] >> 3);
           at[k] = pad_row;
           ks[k] = 0.f;
           vs[k] = 1.f;
-          if ((unsigned)page[k] < (unsigned)of(sg, &PagedSeg::n_pages)) {
-            at[k] = reinterpret_cast<unsigned long long>(of(sg, &PagedSeg::k) + page[k] * of(sg, &PagedSeg::page_stride) +
-                                                         slot * of(sg, &PagedSeg::row_stride)) |
-                    sg;
+          if ((unsigned)page[k] < (unsigned)(sg ? p.seg[1].n_pages : p.seg[0].n_pages)) {
+            at[k] = reinterpret_cast<unsigned long long>(sg ? p.seg[1].k : p.seg[0].k) +
+                    page[k] * (sg ? p.seg[1].page_stride : p.seg[0].page_stride) +
+                    slot * (sg ? p.seg[1].row_stride : p.seg[0].row_stride);
+            at[k] |= sg ? 1 : 0;
             if (FP8) {
-              const long long sr = (long long)page[k] * of(sg, &PagedSeg::page_rows) + slot;
-              ks[k] = of(sg, &PagedSeg::k_scale)[sr];
-              vs[k] = of(sg, &PagedSeg::v_scale)[sr];
+              const long long sr = (long long)page[k] * (sg ? p.seg[1].page_rows : p.seg[0].page_rows) + slot;
+              ks[k] = (sg ? p.seg[1].k_scale : p.seg[0].k_scale)[sr];
+              vs[k] = (sg ? p.seg[1].v_scale : p.seg[0].v_scale)[sr];
             }
           } else {
-            seen[k] = 0;
+            what[k] = 0;
           }
         }
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
-          const int r = 32 * (k0 + k) + lane;
-          const unsigned own = __ballot_sync(0xffffffffu, (seen[k] >> rank) & 1);
-          const unsigned odd = __ballot_sync(0xffffffffu, seen[k] == 1 || seen[k] == 2);
+          const int x = 32 * (k0 + k) + lane;
+          const unsigned seen = what[k] & 3;
           if (!tma) {
-            ms.row[buf][r] = at[k];
-            if (lane == 0) ms.mask[buf][k0 + k] = own;
+            const unsigned own = __ballot_sync(0xffffffffu, (seen >> rank) & 1);
+            const unsigned odd = __ballot_sync(0xffffffffu, seen == 1 || seen == 2);
+            ms.row[buf][x] = at[k];
+            if (lane == k0 + k) {
+              ms.mask[buf][lane] = own;
+              mixed_of = odd;
+            }
+            if (odd != 0) mixed_any |= 1u << (k0 + k);
           }
-          if (k0 == 0) mixed[k] = odd; else mixed[kStep + k] = odd;
           if (FP8) {
-            ms.ksc[buf][r] = p.scale_log2 * ks[k];
+            ms.ksc[buf][x] = p.scale_log2 * ks[k];
             const float lv = fmaxf(__log2f(vs[k]), kLeastLog2ScaleT);
-            ms.lvs[buf][r] = lv;
-            ms.ivs[buf][r] = exp2f(-lv);
+            ms.lvs[buf][x] = lv;
+            ms.ivs[buf][x] = exp2f(-lv);
           }
         }
       }
@@ -402,65 +425,58 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
       // through (new rows, edges of a window).  One that is not finite is left out
       // of the product, and the token that sees it is marked.
       __syncwarp();
-      unsigned any = 0;
-#pragma unroll
-      for (int k = 0; k < kRows / 32; ++k) any |= mixed[k] != 0 ? 1u << k : 0;
+      int k = 0;
+      unsigned who = 0;
 #pragma unroll 1
-      while (!tma && any != 0) {
-        const int k = __ffs(any) - 1;
-        any &= any - 1;
-        unsigned who = 0;
+      while (mixed_any != 0 || who != 0) {
+        constexpr int kAhead = 8, kWords = FP8 ? 1 : 2;
+        uint4 v[kAhead][kWords];
+        int x[kAhead];
 #pragma unroll
-        for (int m = 0; m < kRows / 32; ++m) who = m == k ? mixed[m] : who;
-#pragma unroll 1
-        while (who != 0) {
-          constexpr int kAhead = 8, kWords = FP8 ? 1 : 2;
-          uint4 v[kAhead][kWords];
-          int r[kAhead];
-#pragma unroll
-          for (int a = 0; a < kAhead; ++a) {
-            r[a] = who != 0 ? 32 * k + __ffs(who) - 1 : -1;
-            who &= who - 1;
-            const unsigned long long e = r[a] >= 0 ? ms.row[buf][r[a]] : 0;
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? vdelta1 : vdelta0);
-#pragma unroll
-            for (int w = 0; w < kWords; ++w)
-              v[a][w] = r[a] >= 0 ? reinterpret_cast<const uint4 *>(src)[32 * w + lane] : make_uint4(0, 0, 0, 0);
+        for (int a = 0; a < kAhead; ++a) {
+          if (who == 0 && mixed_any != 0) {
+            k = __ffs(mixed_any) - 1;
+            mixed_any &= mixed_any - 1;
+            who = __shfl_sync(0xffffffffu, mixed_of, k);
           }
+          x[a] = who != 0 ? 32 * k + __ffs(who) - 1 : -1;
+          who &= who - 1;
+          const unsigned long long e = x[a] >= 0 ? ms.row[buf][x[a]] : 0;
+          const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? vdelta1 : vdelta0);
 #pragma unroll
-          for (int a = 0; a < kAhead; ++a) {
-            uint32_t odd = 0;
+          for (int w = 0; w < kWords; ++w)
+            v[a][w] = x[a] >= 0 ? reinterpret_cast<const uint4 *>(src)[32 * w + lane] : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-              const uint32_t x[4] = {v[a][w].x, v[a][w].y, v[a][w].z, v[a][w].w};
+        for (int a = 0; a < kAhead; ++a) {
+          uint32_t odd = 0;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                odd |= FP8 ? ((x[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u   // a code of NaN: seven ones
-                           : ((x[i] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;  // an exponent of five ones
-            }
-            if (__any_sync(0xffffffffu, odd != 0)) {
-              spoiled = spoiled || ((ms.mask[buf][k] >> (r[a] & 31)) & 1u) != 0;
-              if (lane == 0) ms.row[buf][r[a]] |= kNoValue;
-            }
+          for (int w = 0; w < kWords; ++w) {
+            const uint32_t y[4] = {v[a][w].x, v[a][w].y, v[a][w].z, v[a][w].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              odd |= FP8 ? ((y[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u   // a code of NaN: seven ones
+                         : ((y[i] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;  // an exponent of five ones
+          }
+          if (__any_sync(0xffffffffu, odd != 0)) {
+            spoiled = spoiled || ((ms.mask[buf][x[a] >> 5] >> (x[a] & 31)) & 1u) != 0;
+            if (lane == 0) ms.row[buf][x[a]] |= kNoValue;
           }
         }
       }
     }
-    const bool head = g == 0 || j == 0, last = j == rec.z - 1 || left == 1;
+    const bool head = g == 0 || j == 0, last = j == r.tiles - 1 || left == 1;
     if (head) first_j = j;
     if (lane == 0) {
-      const int t = span.at + rec.y, two = rec.y + 1 < span.n;
-      ms.flags[buf] = (head ? TF_FIRST : 0) | (last ? TF_LAST : 0) | (last && first_j == 0 && j == rec.z - 1 ? TF_WHOLE : 0) |
+      ms.flags[buf] = (head ? TF_FIRST : 0) | (last ? TF_LAST : 0) | (last && first_j == 0 && j == r.tiles - 1 ? TF_WHOLE : 0) |
                       (first_j == 0 ? TF_HEAD : 0) | (tma ? 0 : TF_GATHERED) | (spoiled ? TF_SPOILED : 0);
-      ms.tok[buf] = rank == 0 ? t : two ? t + 1 : -1;
-      ms.q_tok[buf] = rank == 0 || !two ? t : t + 1;
+      ms.tok[buf] = rank == 0 ? r.tok : r.two ? r.tok + 1 : -1;
+      ms.q_tok[buf] = rank == 0 || !r.two ? r.tok : r.tok + 1;
     }
     warp_arrive(smem_u32(&ms.list_full[buf]));
     --left;
-    if (++j == rec.z) {
-      j = 0;
+    if (++j == r.tiles) {
       ++u;
-      rec = next_rec;
       enter = true;
     }
   }
@@ -539,21 +555,45 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
             tma_load_5d_pair(dst, m, cluster_addr(b_full, 0), 0, 0, dim0 >> 6, x.y >> 3, x.x);
         }
       } else {
-        // A part's row has 8 (K) or 16 (V) copies, of E4M3 codes half as many.
+        // 16-byte copies, eight lanes to a row (E4M3 codes of K: four).
         const unsigned long long *list = ms.row[buf] + row0;
-        const long long off0 = (is_v ? vdelta0 : 0) + (FP8 ? dim0 : 2 * dim0), off1 = (is_v ? vdelta1 : 0) + (FP8 ? dim0 : 2 * dim0);
-        const unsigned long long skip = is_v ? kNoRowT | kNoValue : kNoRowT;
-        const int shift = (is_v ? 4 : 3) - (FP8 ? 1 : 0), copies = FP8 ? 512 : 1024;
-#pragma unroll 4
-        for (int k = tid; k < copies; k += n_threads) {
-          const int row = k >> shift, x = k & ((1 << shift) - 1);
+        auto src_of = [&](int row, int byte, unsigned long long skip, uint32_t &bytes) {
           const unsigned long long e = list[row];
-          uint32_t dst = slot + 16 * k;
-          if (!FP8)
-            dst = slot + (row & 7) * 128 + (((x & 7) ^ (row & 7)) << 4) +
-                  (is_v ? (row >> 3) * 2048 + (x >> 3) * 1024 : (row >> 3) * 1024);
-          cp_async16z(dst, reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? off1 : off0) + 16 * x,
-                      (e & skip) ? 0u : 16u);
+          const long long to_v = (e & kSegBitT) ? vdelta1 : vdelta0;
+          bytes = (e & skip) ? 0u : 16u;
+          return reinterpret_cast<const uint8_t *>(e & ~15ull) + (is_v ? to_v : 0) + byte;
+        };
+        uint32_t n;
+        if (FP8) {
+          const int shift = is_v ? 3 : 2;
+#pragma unroll 8
+          for (int k = lane; k < 512; k += 32) {
+            const uint8_t *src = src_of(k >> shift, dim0 + 16 * (k & ((1 << shift) - 1)), is_v ? kNoRowT | kNoValue : kNoRowT, n);
+            cp_async16z(slot + 16 * k, src, n);
+          }
+        } else if (!is_v) {
+          constexpr int kRowsAtOnce = 4 * kKLoadWarps<false>, kTurns = (128 + kRowsAtOnce - 1) / kRowsAtOnce;
+          const int c8 = tid & 7;
+#pragma unroll
+          for (int k = 0; k < kTurns; ++k) {
+            const int row = kRowsAtOnce * k + (tid >> 3);
+            if (row < 128) {
+              const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, kNoRowT, n);
+              cp_async16z(slot + row * 128 + ((c8 ^ (row & 7)) << 4), src, n);
+            }
+          }
+        } else {
+          constexpr int kRowsAtOnce = 4 * kVLoadWarps<false>, kTurns = 64 / kRowsAtOnce;
+          static_assert(64 % kRowsAtOnce == 0, "rows of a V part");
+          const int c8 = tid & 7;
+#pragma unroll
+          for (int k = 0; k < kTurns; ++k) {
+            const int row = kRowsAtOnce * k + (tid >> 3);
+            const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, kNoRowT | kNoValue, n);
+            const uint32_t dst = slot + (row >> 3) * 2048 + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4);
+            cp_async16z(dst, src, n);
+            cp_async16z(dst + 1024, src + 128, n);
+          }
         }
         cp_async_arrive(b_full);
       }
@@ -690,12 +730,17 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
     }
     if (first) ++item;
     tc_fence_after();
+    bool ready = false;
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
-      if (!wait(ms.kv_full[kStage0 + ring.st], ring.ph, TSITE_KV_FULL)) return;
+      const uint32_t st = ring.st;
+      if (!__all_sync(0xffffffffu, ready) && !wait(ms.kv_full[kStage0 + st], ring.ph, TSITE_KV_FULL)) return;
+      ring.advance();
+      // The next stage is asked for before this one's products are issued.
+      ready = c < 7 && mbar_test(smem_u32(&ms.kv_full[kStage0 + ring.st]), ring.ph);
       if (fence) fence_proxy_async_smem();
       const uint64_t a0 = sdesc_add(a_desc, (IS_V ? c & 3 : c) * 8192);
-      const uint64_t b0 = sdesc_add(b_desc, ring.st * kPart);
+      const uint64_t b0 = sdesc_add(b_desc, st * kPart);
       const uint32_t d = IS_V ? tmem + 128 * (c >> 2) : tmem + kTmemTS + 128 * sb;
       const bool fresh = IS_V ? first && (c & 3) == 0 : c == 0;
       if (elect_lane()) {
@@ -706,7 +751,7 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
           else
             umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * (IS_V ? 4096 : 32)), kIdesc);
         }
-        umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + ring.st]));
+        umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + st]));
         if (IS_V) {
           if ((c & 3) == 3 && last) umma_pair_commit(smem_u32(&ms.o_full[c >> 2]));
           if (c == 7) umma_pair_commit(smem_u32(&ms.p_empty));
@@ -716,7 +761,6 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
         }
       }
       __syncwarp();
-      ring.advance();
     }
   }
 }
@@ -827,40 +871,42 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       moved = true;
       lsum *= alpha;
     }
-    wait(ms.p_empty, (g & 1) ^ 1, TSITE_P_EMPTY);
-    // This head's 64 weights: 16-byte chunk c of its 128 bytes at c ^ (h & 7).
-    // Rounded once to fp16 for the product; the sums add them unrounded, eight at
-    // a time, so that lse keeps fp32 precision over long rows.
-#pragma unroll 1
+    // This head's 64 weights, rounded once to fp16 for the product; the sums add them
+    // unrounded, eight at a time, so that lse keeps fp32 precision over long rows.
+    // They wait in registers for P's buffer: the next P . V waits for no more than
+    // their stores.
+    uint32_t weights[32];
+#pragma unroll
     for (int c0 = 0; c0 < 64; c0 += 32) {
       float s[32];
       scores(c0, s);
       float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w4[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = 8 * c + 2 * i;
-          const float e0 = exp2f(s[x] - m_ref), e1 = exp2f(s[x + 1] - m_ref);
-          __half2 hp = __floats2half2_rn(e0, e1);
-          if (FP8) {
-            const float2 iv = *reinterpret_cast<const float2 *>(&ms.ivs[buf][64 * box + c0 + x]);
-            part[i] = fmaf(e0, iv.x, fmaf(e1, iv.y, part[i]));
-            // A V scale of 0: weight, but no value.
-            if (iv.x >= kMostScaleInv || iv.y >= kMostScaleInv)
-              hp = __floats2half2_rn(iv.x >= kMostScaleInv ? 0.f : e0, iv.y >= kMostScaleInv ? 0.f : e1);
-          } else {
-            part[i] += e0 + e1;
-          }
-          w4[i] = *reinterpret_cast<const uint32_t *>(&hp);
+      for (int i = 0; i < 16; ++i) {
+        const int x = 2 * i;
+        const float e0 = exp2f(s[x] - m_ref), e1 = exp2f(s[x + 1] - m_ref);
+        __half2 hp = __floats2half2_rn(e0, e1);
+        if (FP8) {
+          const float2 iv = *reinterpret_cast<const float2 *>(&ms.ivs[buf][64 * box + c0 + x]);
+          part[i & 3] = fmaf(e0, iv.x, fmaf(e1, iv.y, part[i & 3]));
+          // A V scale of 0: weight, but no value.
+          if (iv.x >= kMostScaleInv || iv.y >= kMostScaleInv)
+            hp = __floats2half2_rn(iv.x >= kMostScaleInv ? 0.f : e0, iv.y >= kMostScaleInv ? 0.f : e1);
+        } else {
+          part[i & 3] += e0 + e1;
         }
-        *reinterpret_cast<uint4 *>(prow + (((c0 / 8 + c) ^ (h & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        weights[c0 / 2 + i] = *reinterpret_cast<const uint32_t *>(&hp);
       }
       lsum += (part[0] + part[1]) + (part[2] + part[3]);
     }
     tc_fence_before();
     tell(ms.s_empty[sb]);
+    wait(ms.p_empty, (g & 1) ^ 1, TSITE_P_EMPTY);
+    // 16-byte chunk c of the head's 128 bytes at c ^ (h & 7).
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4 *>(prow + ((c ^ (h & 7)) << 4)) =
+          make_uint4(weights[4 * c], weights[4 * c + 1], weights[4 * c + 2], weights[4 * c + 3]);
     if (FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
     if (moved && !(flags & TF_FIRST)) {
       tc_fence_after();
@@ -1053,12 +1099,11 @@ __global__ void __launch_bounds__(32 * kMergeHeads) tree_merge_kernel(const Tree
   const int4 head = p.ws_head[0];
   const long long at = (long long)edge * head.y;
   if (at >= head.x) return;
-  const int4 rec = p.ws_unit[p.ws_start[edge]];
-  if (rec.w >= at || at - rec.w > head.y) return;  // no cut here, or not the unit's first
-  const Span2 s = tokens_of(p, rec.x);
-  const int t = rec.y + i;
-  if (t >= s.n) return;
-  const int n = (rec.w + rec.z - 1) / head.y - (edge - 1) + 1;  // parts
+  const UnitRec &rec = static_cast<const UnitRec *>(p.ws_unit)[p.ws_start[edge]];
+  const int before = rec.before;
+  if (before >= at || at - before > head.y) return;  // no cut here, or not the unit's first
+  if (i > rec.two) return;
+  const int n = (before + rec.tiles - 1) / head.y - (edge - 1) + 1;  // parts
   auto slot = [&](int k) { return 2ll * (k == 0 ? 2 * (edge - 1) + 1 : 2 * (edge - 1 + k)) + i; };
   float M = -INFINITY, L = 0.f;
   float4 acc[4];
@@ -1100,7 +1145,7 @@ __global__ void __launch_bounds__(32 * kMergeHeads) tree_merge_kernel(const Tree
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const long long tok = s.at + t;
+  const long long tok = rec.tok + i;
   __half *o = p.o + tok * p.o_stride + (long long)h * kD;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
