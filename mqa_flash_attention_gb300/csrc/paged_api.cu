@@ -517,19 +517,33 @@ ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout
   p.lse = X->lse;
   st = ds4a::host_encode_q(&p.tm_q, X->q, n_tok, X->q_tok_stride);
   if (st != DS4A_OK) return st;
-  if (has_rows(&X->comp)) {
-    const ds4a_paged_rows *r = &X->comp;
-    const int run = run_rows_of(r->page_rows);
-    p.run_rows = run > 64 ? 64 : run;  // (a part of V has 64 rows)
-  }
-  if (p.run_rows > 0) {
-    const ds4a_paged_rows *r = &X->comp;
-    p.run_shift = log2_of(p.run_rows);
-    st = ds4a::host_encode_pages(&p.tm_k, r->k, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride,
-                                 p.run_rows, 1);
-    if (st == DS4A_OK)
-      st = ds4a::host_encode_pages(&p.tm_v, r->v, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride,
-                                   p.run_rows, 2);
+  // Rows of a copy that lies within a page: 16 or 8 of either segment, and of the
+  // compressed ones up to 64.  (Pages of other sizes are gathered row by row.)
+  int grain = 16;
+  for (const ds4a_paged_rows *r : {&X->raw, &X->comp})
+    if (has_rows(r) && run_rows_of(r->page_rows) < grain) grain = run_rows_of(r->page_rows);
+  p.grain = any ? grain : 0;
+  if (p.grain > 0) {
+    p.grain_shift = p.run_shift = log2_of(grain);
+    const ds4a_paged_rows *segs[2] = {&X->raw, &X->comp};
+    for (int i = 0; i < 2 && st == DS4A_OK; ++i) {
+      const ds4a_paged_rows *r = segs[i];
+      if (!has_rows(r)) continue;
+      st = ds4a::host_encode_pages(&p.tm_kg[i], r->k, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride,
+                                   grain, 1);
+      if (st == DS4A_OK)
+        st = ds4a::host_encode_pages(&p.tm_vg[i], r->v, e4m3, r->page_rows, r->n_pages, r->row_stride,
+                                     r->page_stride, grain, 2);
+    }
+    if (st == DS4A_OK && has_rows(&X->comp)) {
+      const ds4a_paged_rows *r = &X->comp;
+      const int run = run_rows_of(r->page_rows) > 64 ? 64 : run_rows_of(r->page_rows);  // (a part of V has 64 rows)
+      p.run_shift = log2_of(run);
+      st = ds4a::host_encode_pages(&p.tm_k, r->k, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride, run, 1);
+      if (st == DS4A_OK)
+        st = ds4a::host_encode_pages(&p.tm_v, r->v, e4m3, r->page_rows, r->n_pages, r->row_stride, r->page_stride,
+                                     run, 2);
+    }
     if (st != DS4A_OK) return st;
   }
   const TreeSpace t = tree_space(n_seq, n_tok, d.sm_count);

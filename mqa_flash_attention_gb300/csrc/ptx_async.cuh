@@ -57,6 +57,11 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32
   return mbar_try_wait(bar, parity) || wait_long(bar, parity, site, w);
 }
 
+// More bytes to come before the phase completes; no arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // Whether the phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;

@@ -50,11 +50,12 @@ constexpr int kTreeTokens = 128;
 
 struct TreeAttnParams {
   CUtensorMap tm_q;        // 4-D {64, 64 heads, n_tok, 8 dim blocks}, box {64, 64, 1, 8}
-  // Compressed rows by runs of run_rows rows, K by 64 dims and V by 128: fp16 5-D
-  // {64 dims, 8 rows, 8 blocks, page_rows / 8, pages}, box {64, 8, 1 or 2,
-  // run_rows / 8, 1}; codes 3-D {512, page_rows, pages}, box {64 or 128, run_rows, 1}.
-  CUtensorMap tm_k, tm_v;
-  int run_rows, run_shift; // 8 .. 64, a power of two, and its log2; 0: no TMA loads
+  // K by 64 dims and V by 128: fp16 5-D {64 dims, 8 rows, 8 blocks, page_rows / 8,
+  // pages}, box {64, 8, 1 or 2, rows / 8, 1}; codes 3-D {512, page_rows, pages}, box
+  // {64 or 128, rows, 1}.  Compressed rows by runs of 2^run_shift rows (at most 64),
+  // and rows of either segment by grains of 8 or 16.
+  CUtensorMap tm_k, tm_v, tm_kg[2], tm_vg[2];
+  int grain, grain_shift, run_shift;  // grain 0: pages that TMA cannot copy
   PagedSeg seg[2];         // raw, compressed
   const int4 *geom;        // (q_pos, n_raw, raw_pos0, n_comp) per sequence
   const int32_t *first, *parent;

@@ -77,8 +77,11 @@ constexpr float kLeastLog2ScaleT = -40.f;   // V scales below 2^-40 count as 0: 
 constexpr float kMostScaleInv = 1.0995e12f;      // just below 2^40
 constexpr unsigned long long kSegBitT = 1, kNoRowT = 2, kNoValue = 4;  // low bits of a list entry
 
-// Of a tile within its item (the cluster's tiles of one unit).
-enum : int { TF_FIRST = 1, TF_LAST = 2, TF_WHOLE = 4, TF_GATHERED = 8, TF_SPOILED = 16, TF_HEAD = 32 };
+// Of a tile within its item (the cluster's tiles of one unit); how its rows come; and
+// from TF_PARTS on a bit for each 64 rows of which some token sees any.  (V's stages
+// and products of the others are left out.)
+enum : int { TF_FIRST = 1, TF_LAST = 2, TF_WHOLE = 4, TF_GATHERED = 8, TF_SPOILED = 16, TF_HEAD = 32, TF_FULL = 64 };
+constexpr int TF_PARTS = 8;
 
 enum : unsigned int {
   TSITE_Q_EMPTY = 0x80, TSITE_KV_EMPTY, TSITE_Q_FULL, TSITE_S_EMPTY, TSITE_KV_FULL, TSITE_P_FULL, TSITE_O_EMPTY,
@@ -89,12 +92,12 @@ enum : unsigned int {
 // What a cluster has to know of a unit, as 32 words (a warp reads one a lane).
 struct UnitRec {
   int seq, t0, tiles, before;        // sequence, first token, tiles, tiles of all units before
-  int nc, r0, nr, d0, len, n_raw;    // the list (UnitRows)
+  int nc, raw_at, raw0, len, n_raw;  // the list (UnitRows)
   int tok, two;                      // first token counted over all sequences; whether there is a second
   int nc_of[2], ra[2], rb[2];        // what either token sees: compressed rows below nc_of, cached rows ra .. rb - 1,
   int da[2], db[2];                  // new rows da .. db - 1 of a run,
   uint32_t anc[2][4];                // and of a tree those with a bit set
-  int pad[2];
+  int pad[3];
 };
 static_assert(sizeof(UnitRec) == 128, "a word per lane");
 
@@ -103,7 +106,8 @@ struct TMisc {
   alignas(16) float ksc[kListsT][kRows];               // E4M3: scale * log2(e) * K scale
   alignas(16) float lvs[kListsT][kRows];               // E4M3: log2 of the V scale (of 2^-40 at least)
   alignas(16) float ivs[kListsT][kRows];               // E4M3: 2^-lvs
-  int2 box[kListsT][kRows / 8];                        // (page, slot) of the runs of a tile that TMA loads
+  int2 box[kListsT][kRows / 8];                        // (page, 2 * slot + segment) of the tile's grains
+  uint32_t held[kListsT], live[kListsT];               // grains that have a page; whose rows all are seen by some token
   uint32_t mask[kListsT][kRows / 32];                  // rows that this CTA's token sees
   int flags[kListsT], tok[kListsT], q_tok[kListsT];    // TF_ bits; this CTA's token (-1: none); the one whose Q it loads
   alignas(16) float red[4][kH];
@@ -141,31 +145,35 @@ __device__ __forceinline__ Span2 tokens_of(const TreeAttnParams &p, int b) {
   return Span2{at, min(max(p.first[b + 1], at), p.n_tok) - at};
 }
 
-// The rows that a unit's tokens t0 .. t1 see: compressed rows [0, nc), cached raw
-// rows [r0, r0 + nr), new rows [d0, d0 + nd).  (Of a tree, what any of its nodes
-// could see: their depths are not known here.)
+// The rows that a unit's tokens t0 .. t1 see, as a list: compressed rows [0, nc), and
+// from place raw_at on the raw rows raw0 .. (cached ones, then new ones, which follow
+// them in the table).  raw_at and raw0 are whole grains, so that a grain of the list is
+// one of a page.  (Of a tree, what any of its nodes could see: their depths are not
+// known here.)
 struct UnitRows {
-  int nc, r0, nr, d0, nd, n_raw;
-  __device__ __forceinline__ int len() const { return nc + nr + nd; }
-  __device__ __forceinline__ int tiles() const { return max(1, (len() + kRows - 1) / kRows); }
+  int nc, raw_at, raw0, len, n_raw;
+  __device__ __forceinline__ int tiles() const { return max(1, (len + kRows - 1) / kRows); }
 };
 
 __device__ __forceinline__ UnitRows unit_rows(const TreeAttnParams &p, int4 g, int n, int t0, int t1) {
   const bool chain = p.parent == nullptr;
   const long long pos = max(g.x, 0), raw_pos0 = max(g.z, 0);
-  const int n_comp = min(max(g.w, 0), p.seg[1].max_rows);
+  const int n_comp = min(max(g.w, 0), p.seg[1].max_rows), grain = max(p.grain, 1);
   UnitRows r;
   r.n_raw = min(max(g.y, 0), p.seg[0].max_rows);
-  r.nc = r.r0 = r.nr = r.d0 = r.nd = 0;
+  r.nc = r.raw_at = r.raw0 = r.len = 0;
   if (!chain && t0 >= kTreeTokens) return r;  // nodes that see nothing
   const long long lo = chain ? pos + t0 : pos, hi = chain ? pos + t1 : pos + min(n, kTreeTokens) - 1;
   r.nc = (int)min((unsigned)n_comp, (unsigned)(hi + 1) / (unsigned)p.ratio);
-  r.r0 = (int)min(max(lo - p.window + 1 - raw_pos0, 0ll), (long long)r.n_raw);
-  const int r1 = (int)min(max(hi + 1 - raw_pos0, (long long)r.r0), (long long)r.n_raw);
-  r.nr = r1 - r.r0;
-  const int d1 = min(t1 + 1, p.seg[0].max_rows - r.n_raw);
-  r.d0 = chain ? min(max(0, t0 - p.window + 1), d1) : 0;
-  r.nd = d1 - r.d0;
+  r.len = r.raw_at = (r.nc + grain - 1) / grain * grain;
+  const int r0 = (int)min(max(lo - p.window + 1 - raw_pos0, 0ll), (long long)r.n_raw);
+  const int r1 = (int)min(max(hi + 1 - raw_pos0, (long long)r0), (long long)r.n_raw);
+  const int d1 = min(t1 + 1, p.seg[0].max_rows - r.n_raw), d0 = chain ? min(max(0, t0 - p.window + 1), d1) : 0;
+  const int from = r1 > r0 ? r0 : r.n_raw + d0, to = d1 > d0 ? r.n_raw + d1 : r1;
+  if (to > from) {
+    r.raw0 = from / grain * grain;
+    r.len += to - r.raw0;
+  }
   return r;
 }
 
@@ -201,10 +209,9 @@ __device__ __forceinline__ void unit_record(const TreeAttnParams &p, int seq, in
   r.t0 = t0;
   r.tiles = rows.tiles();
   r.nc = rows.nc;
-  r.r0 = rows.r0;
-  r.nr = rows.nr;
-  r.d0 = rows.d0;
-  r.len = rows.len();
+  r.raw_at = rows.raw_at;
+  r.raw0 = rows.raw0;
+  r.len = rows.len;
   r.n_raw = rows.n_raw;
   r.tok = s.at + t0;
   r.two = t1 > t0;
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
     const int inc = block_scan(rec.tiles, warp_sum, all);
     if (u < units) {
       rec.before = tiles + inc - rec.tiles;
-      rec.pad[0] = rec.pad[1] = 0;
+      rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
       recs[u] = rec;
     }
     tiles += all;
@@ -288,9 +295,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
 
 // ------------------------------------------------------------------ lists
 
-// One warp goes ahead of all others and writes down, per tile, what is in it.  A full
-// tile (compressed rows that both tokens see, in runs that TMA can copy) is no more than
-// the pages of its runs (and E4M3 scales); of any other the address of every row.
+// One warp goes ahead of all others and writes down, per tile, what is in it.  Where the
+// pages allow TMA, a tile is a list of grains (8 or 16 rows, which one page holds): K
+// comes by TMA wherever a grain has a page, since scores of rows that nobody sees are
+// masked; V only where all rows of a grain are seen, and row by row elsewhere, zeros in
+// place of the others.  Otherwise it is a list of the rows' addresses.
 template <bool FP8>
 __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, int cluster, uint32_t rank, TMisc &ms,
                                                int lane) {
@@ -299,7 +308,8 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
   const long long vdelta0 = p.seg[0].v - p.seg[0].k, vdelta1 = p.seg[1].v - p.seg[1].k;
   const int pad_seg = p.seg[1].max_rows > 0 ? 1 : 0;
   const unsigned long long pad_row = reinterpret_cast<unsigned long long>(p.seg[pad_seg].k) | pad_seg | kNoRowT;
-  const int n_runs = p.run_rows > 0 ? kRows >> p.run_shift : 0;  // of a tile that TMA loads
+  // Without grains every lane finds the pages of its own rows, as if each were one.
+  const int grain = max(p.grain, 1), shift = p.grain > 0 ? p.grain_shift : 0;
   const int *recs = static_cast<const int *>(p.ws_unit);
 
   int u = p.ws_start[cluster], left = nt, j = 0, first_j = 0;
@@ -307,6 +317,37 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
   bool enter = true;
   UnitRec &r = ms.unit;
   const int32_t *table0 = nullptr, *table1 = nullptr;
+  // Page and 2 * slot + segment of the list's place x (page -1: none).
+  auto place = [&](int x) {
+    int2 b = make_int2(-1, 0);
+    if (x < r.len && (x < r.nc || x >= r.raw_at)) {
+      const bool sg = x < r.raw_at;
+      const int row = sg ? x : r.raw0 + (x - r.raw_at);
+      const int s = sg ? p.seg[1].page_shift : p.seg[0].page_shift, per = sg ? p.seg[1].page_rows : p.seg[0].page_rows;
+      const int pi = s >= 0 ? row >> s : row / per;
+      b.x = (sg ? table1 : table0)[pi];
+      b.y = 2 * (row - pi * per) + (sg ? 1 : 0);
+      if ((unsigned)b.x >= (unsigned)(sg ? p.seg[1].n_pages : p.seg[0].n_pages)) b.x = -1;
+    }
+    return b;
+  };
+  auto address = [&](int2 b, int more) {  // of the K row `more` rows behind a place, with its segment's bit
+    const bool sg = b.y & 1;
+    return (reinterpret_cast<unsigned long long>(sg ? p.seg[1].k : p.seg[0].k) +
+            b.x * (sg ? p.seg[1].page_stride : p.seg[0].page_stride) +
+            ((b.y >> 1) + more) * (sg ? p.seg[1].row_stride : p.seg[0].row_stride)) |
+           (sg ? kSegBitT : 0);
+  };
+  // Who sees the list's place x (1: the first token, 2: the second).
+  auto seen_by = [&](int x) -> unsigned {
+    if (x < r.raw_at) return (x < r.nc_of[0] ? 1 : 0) | (x < r.nc_of[1] ? 2 : 0);
+    if (x >= r.len) return 0;
+    const int row = r.raw0 + (x - r.raw_at), d = row - r.n_raw;
+    if (d < 0) return (row >= r.ra[0] && row < r.rb[0] ? 1 : 0) | (row >= r.ra[1] && row < r.rb[1] ? 2 : 0);
+    if (chain) return (d >= r.da[0] && d < r.db[0] ? 1 : 0) | (d >= r.da[1] && d < r.db[1] ? 2 : 0);
+    return ((r.anc[0][d >> 5] >> (d & 31)) & 1u) | (((r.anc[1][d >> 5] >> (d & 31)) & 1u) << 1);
+  };
+#pragma unroll 1
   for (int g = 0; g < nt; ++g) {
     const int buf = g % kListsT;
     if (enter) {
@@ -319,129 +360,106 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
       table1 = p.seg[1].table + r.seq * p.seg[1].table_stride;
       enter = false;
     }
-    const int base = j * kRows, nc = r.nc;
-    bool tma = p.run_rows > 0 && base + kRows <= min(r.nc_of[0], r.nc_of[1]), spoiled = false;
-    // (Page ids before the wait for a free list.)
-    int run_page = -1, run_slot = 0;
-    if (tma && lane < n_runs) {
-      const int row = base + (lane << p.run_shift), pi = p.seg[1].page_shift >= 0 ? row >> p.seg[1].page_shift : row / p.seg[1].page_rows;
-      run_page = table1[pi];
-      run_slot = row - pi * p.seg[1].page_rows;
+    const int base = j * kRows;
+    // Compressed rows that both tokens see, in grains with pages: nothing to look through.
+    bool full = p.grain > 0 && base + kRows <= min(r.nc_of[0], r.nc_of[1]), spoiled = false;
+    int2 mine = make_int2(-1, 0);  // lane i: grain i
+    unsigned held = 0, live = 0;
+    if (p.grain > 0) {
+      if (lane < kRows >> shift) mine = place(base + (lane << shift));
+      held = __ballot_sync(0xffffffffu, mine.x >= 0);
+      live = held;
+      full = full && held == (kRows >> shift == 32 ? 0xffffffffu : (1u << (kRows >> shift)) - 1);
+    }
+    float ks[FP8 ? 8 : 1], vs[FP8 ? 8 : 1];
+    if (FP8 && p.grain > 0) {
+#pragma unroll
+      for (int k = 0; k < (FP8 ? 8 : 1); ++k) {
+        const int x = 32 * k + lane;
+        const int page = __shfl_sync(0xffffffffu, mine.x, x >> shift), at = __shfl_sync(0xffffffffu, mine.y, x >> shift);
+        ks[k] = 0.f;
+        vs[k] = 1.f;
+        if (page >= 0 && (full || seen_by(base + x) != 0)) {
+          const bool sg = at & 1;
+          const long long sr = (long long)page * (sg ? p.seg[1].page_rows : p.seg[0].page_rows) + (at >> 1) + (x & (grain - 1));
+          ks[k] = (sg ? p.seg[1].k_scale : p.seg[0].k_scale)[sr];
+          vs[k] = (sg ? p.seg[1].v_scale : p.seg[0].v_scale)[sr];
+        }
+      }
     }
     if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_empty[buf]), ((g / kListsT) & 1) ^ 1, TSITE_LIST_EMPTY,
                                             &ms.wait)))
       return;
-    if (tma) {
-      tma = __all_sync(0xffffffffu, lane >= n_runs || (unsigned)run_page < (unsigned)p.seg[1].n_pages);
-      if (lane < n_runs) ms.box[buf][lane] = make_int2(run_page, run_slot);
+    unsigned parts = 15;
+    if (full) {
       if (lane < kRows / 32) ms.mask[buf][lane] = 0xFFFFFFFFu;
-    }
-    if (FP8 || !tma) {
-      constexpr int kStep = 8;  // rows of a lane whose loads go together
-      unsigned mixed_any = 0, mixed_of = 0;  // words with rows that one token sees and the other does not; lane k: word k
+    } else {
+      parts = 0;
+      unsigned any_of = 0, one_of = 0, one_any = 0;  // lane k, rows 32 k ..: seen by some token, by one; words of the latter
 #pragma unroll 1
-      for (int k0 = 0; k0 < kRows / 32; k0 += kStep) {
-        int page[kStep];
-        unsigned what[kStep];  // slot * 8 | segment * 4 | who sees it
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          const int x = base + 32 * (k0 + k) + lane;
-          page[k] = -1;
-          what[k] = 0;
-          int row = x;
-          unsigned seen = 0, sg = 1;
-          if (x < nc) {
-            seen = (x < r.nc_of[0] ? 1 : 0) | (x < r.nc_of[1] ? 2 : 0);
-          } else if (x < r.len) {
-            sg = 0;
-            const int at = x - nc;
-            if (at < r.nr) {
-              row = r.r0 + at;
-              seen = (row >= r.ra[0] && row < r.rb[0] ? 1 : 0) | (row >= r.ra[1] && row < r.rb[1] ? 2 : 0);
-            } else {
-              const int d = r.d0 + (at - r.nr);
-              row = r.n_raw + d;
-              if (chain)
-                seen = (d >= r.da[0] && d < r.db[0] ? 1 : 0) | (d >= r.da[1] && d < r.db[1] ? 2 : 0);
-              else
-                seen = ((r.anc[0][d >> 5] >> (d & 31)) & 1u) | (((r.anc[1][d >> 5] >> (d & 31)) & 1u) << 1);
-            }
-          }
-          if (seen != 0) {
-            const int shift = sg != 0 ? p.seg[1].page_shift : p.seg[0].page_shift;
-            const int per = sg != 0 ? p.seg[1].page_rows : p.seg[0].page_rows;
-            const int pi = shift >= 0 ? row >> shift : row / per;
-            page[k] = (sg != 0 ? table1 : table0)[pi];
-            what[k] = (unsigned)(row - pi * per) << 3 | sg << 2 | seen;
-          }
+      for (int k = 0; k < kRows / 32; ++k) {
+        const int x = 32 * k + lane;
+        int2 at = mine;
+        if (p.grain > 0) {
+          at.x = __shfl_sync(0xffffffffu, mine.x, x >> shift);
+        } else {
+          at = place(base + x);
+          ms.row[buf][x] = pad_row;
         }
-        unsigned long long at[kStep];
-        float ks[kStep], vs[kStep];
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          const bool sg = what[k] & 4;
-          const int slot = (int)(what[k] >> 3);
-          at[k] = pad_row;
-          ks[k] = 0.f;
-          vs[k] = 1.f;
-          if ((unsigned)page[k] < (unsigned)(sg ? p.seg[1].n_pages : p.seg[0].n_pages)) {
-            at[k] = reinterpret_cast<unsigned long long>(sg ? p.seg[1].k : p.seg[0].k) +
-                    page[k] * (sg ? p.seg[1].page_stride : p.seg[0].page_stride) +
-                    slot * (sg ? p.seg[1].row_stride : p.seg[0].row_stride);
-            at[k] |= sg ? 1 : 0;
-            if (FP8) {
-              const long long sr = (long long)page[k] * (sg ? p.seg[1].page_rows : p.seg[0].page_rows) + slot;
-              ks[k] = (sg ? p.seg[1].k_scale : p.seg[0].k_scale)[sr];
-              vs[k] = (sg ? p.seg[1].v_scale : p.seg[0].v_scale)[sr];
-            }
-          } else {
-            what[k] = 0;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          const int x = 32 * (k0 + k) + lane;
-          const unsigned seen = what[k] & 3;
-          if (!tma) {
-            const unsigned own = __ballot_sync(0xffffffffu, (seen >> rank) & 1);
-            const unsigned odd = __ballot_sync(0xffffffffu, seen == 1 || seen == 2);
-            ms.row[buf][x] = at[k];
-            if (lane == k0 + k) {
-              ms.mask[buf][lane] = own;
-              mixed_of = odd;
-            }
-            if (odd != 0) mixed_any |= 1u << (k0 + k);
-          }
+        const unsigned seen = at.x >= 0 ? seen_by(base + x) : 0;
+        if (p.grain == 0 && seen != 0) {
+          ms.row[buf][x] = address(at, 0);
           if (FP8) {
-            ms.ksc[buf][x] = p.scale_log2 * ks[k];
-            const float lv = fmaxf(__log2f(vs[k]), kLeastLog2ScaleT);
-            ms.lvs[buf][x] = lv;
-            ms.ivs[buf][x] = exp2f(-lv);
+            const bool sg = at.y & 1;
+            const long long sr = (long long)at.x * (sg ? p.seg[1].page_rows : p.seg[0].page_rows) + (at.y >> 1);
+            const float kk = (sg ? p.seg[1].k_scale : p.seg[0].k_scale)[sr], vv = (sg ? p.seg[1].v_scale : p.seg[0].v_scale)[sr];
+            ms.ksc[buf][x] = kk;
+            ms.lvs[buf][x] = vv;
           }
+        } else if (FP8 && p.grain == 0) {
+          ms.ksc[buf][x] = 0.f;
+          ms.lvs[buf][x] = 1.f;
         }
+        const unsigned own = __ballot_sync(0xffffffffu, (seen >> rank) & 1), some = __ballot_sync(0xffffffffu, seen != 0);
+        const unsigned one = __ballot_sync(0xffffffffu, seen == 1 || seen == 2);
+        if (lane == k) {
+          ms.mask[buf][k] = own;
+          any_of = some;
+          one_of = one;
+        }
+        if (one != 0) one_any |= 1u << k;
+        if (some != 0) parts |= 1u << (k >> 1);
       }
       // A V row that one token sees and the other does not must be finite, because
       // its weight of 0 multiplies it all the same: the warp looks these few rows
       // through (new rows, edges of a window).  One that is not finite is left out
       // of the product, and the token that sees it is marked.
       __syncwarp();
+      unsigned bad_of = 0, who = 0;
       int k = 0;
-      unsigned who = 0;
 #pragma unroll 1
-      while (mixed_any != 0 || who != 0) {
+      while (one_any != 0 || who != 0) {
         constexpr int kAhead = 8, kWords = FP8 ? 1 : 2;
         uint4 v[kAhead][kWords];
         int x[kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-          if (who == 0 && mixed_any != 0) {
-            k = __ffs(mixed_any) - 1;
-            mixed_any &= mixed_any - 1;
-            who = __shfl_sync(0xffffffffu, mixed_of, k);
+          if (who == 0 && one_any != 0) {
+            k = __ffs(one_any) - 1;
+            one_any &= one_any - 1;
+            who = __shfl_sync(0xffffffffu, one_of, k);
           }
           x[a] = who != 0 ? 32 * k + __ffs(who) - 1 : -1;
           who &= who - 1;
-          const unsigned long long e = x[a] >= 0 ? ms.row[buf][x[a]] : 0;
+          unsigned long long e = 0;
+          if (x[a] >= 0) {
+            if (p.grain > 0) {
+              const int2 b = make_int2(__shfl_sync(0xffffffffu, mine.x, x[a] >> shift), __shfl_sync(0xffffffffu, mine.y, x[a] >> shift));
+              e = address(b, x[a] & (grain - 1));
+            } else {
+              e = ms.row[buf][x[a]];
+            }
+          }
           const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? vdelta1 : vdelta0);
 #pragma unroll
           for (int w = 0; w < kWords; ++w)
@@ -460,16 +478,50 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
           }
           if (__any_sync(0xffffffffu, odd != 0)) {
             spoiled = spoiled || ((ms.mask[buf][x[a] >> 5] >> (x[a] & 31)) & 1u) != 0;
-            if (lane == 0) ms.row[buf][x[a]] |= kNoValue;
+            if (lane == x[a] >> 5) bad_of |= 1u << (x[a] & 31);
           }
         }
       }
+      if (p.grain > 0) {
+        // Grains of which every row is seen and fit for the product; of the others the rows.
+        const unsigned good = any_of & ~bad_of, at_word = (lane << shift) >> 5 & 7;
+        const unsigned bits = __shfl_sync(0xffffffffu, good, at_word) >> ((lane << shift) & 31), ones = (1u << grain) - 1;
+        live = __ballot_sync(0xffffffffu, mine.x >= 0 && lane < kRows >> shift && (bits & ones) == ones);
+        const unsigned in_word = (1u << (32 >> shift)) - 1;
+#pragma unroll 1
+        for (int w = 0; w < kRows / 32; ++w) {
+          if (((parts >> (w >> 1)) & 1u) == 0 || ((live >> (w << (5 - shift))) & in_word) == in_word) continue;
+          const int x = 32 * w + lane;
+          const int2 b = make_int2(__shfl_sync(0xffffffffu, mine.x, x >> shift), __shfl_sync(0xffffffffu, mine.y, x >> shift));
+          const bool use = (__shfl_sync(0xffffffffu, good, w) >> lane) & 1u;
+          ms.row[buf][x] = use ? address(b, x & (grain - 1)) : pad_row;
+        }
+      } else {
+#pragma unroll 1
+        for (int w = 0; w < kRows / 32; ++w)
+          if ((__shfl_sync(0xffffffffu, bad_of, w) >> lane) & 1u) ms.row[buf][32 * w + lane] |= kNoValue;
+      }
     }
+    if (FP8) {
+#pragma unroll
+      for (int k = 0; k < (FP8 ? 8 : 1); ++k) {
+        const int x = 32 * k + lane;
+        const float kk = p.grain > 0 ? ks[k] : ms.ksc[buf][x], vv = p.grain > 0 ? vs[k] : ms.lvs[buf][x];
+        ms.ksc[buf][x] = p.scale_log2 * kk;
+        const float lv = fmaxf(__log2f(vv), kLeastLog2ScaleT);
+        ms.lvs[buf][x] = lv;
+        ms.ivs[buf][x] = exp2f(-lv);
+      }
+    }
+    if (p.grain > 0) ms.box[buf][lane] = mine;
     const bool head = g == 0 || j == 0, last = j == r.tiles - 1 || left == 1;
     if (head) first_j = j;
     if (lane == 0) {
+      ms.held[buf] = held;
+      ms.live[buf] = live;
       ms.flags[buf] = (head ? TF_FIRST : 0) | (last ? TF_LAST : 0) | (last && first_j == 0 && j == r.tiles - 1 ? TF_WHOLE : 0) |
-                      (first_j == 0 ? TF_HEAD : 0) | (tma ? 0 : TF_GATHERED) | (spoiled ? TF_SPOILED : 0);
+                      (first_j == 0 ? TF_HEAD : 0) | (p.grain == 0 ? TF_GATHERED : 0) | (full ? TF_FULL : 0) |
+                      (spoiled ? TF_SPOILED : 0) | (int)parts << TF_PARTS;
       ms.tok[buf] = rank == 0 ? r.tok : r.two ? r.tok + 1 : -1;
       ms.q_tok[buf] = rank == 0 || !r.two ? r.tok : r.tok + 1;
     }
@@ -484,13 +536,14 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
 
 // ------------------------------------------------------------------ loaders
 
-// The warps of K, or of V, load part after part into their ring: by TMA, a run per lane
-// (warps in turn), or by 16-byte copies.  E4M3: one warp for both, K one tile ahead.
+// The warps of K, or of V, load part after part into their ring: by TMA, a run or a
+// grain per lane (warps in turn), or by 16-byte copies.  E4M3: one warp for both, K one
+// tile ahead.
 template <bool FP8>
 __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, uint32_t rank, uint32_t sbase, TMisc &ms,
                                                bool v_warp, int tid) {
   if (nt <= 0) return;
-  const int n_warps = v_warp ? kVLoadWarps<FP8> : kKLoadWarps<FP8>, n_threads = 32 * n_warps;
+  const int n_warps = v_warp ? kVLoadWarps<FP8> : kKLoadWarps<FP8>;
   const int lane = tid & 31, warp = tid >> 5;
   const long long vdelta0 = p.seg[0].v - p.seg[0].k, vdelta1 = p.seg[1].v - p.seg[1].k;
   uint32_t st_k = 0, ph_k = 1, st_v = 0, ph_v = 1;  // next stage of either ring and the parity to wait for
@@ -520,11 +573,15 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
       ++n_item;
       __syncwarp();
     }
-    const bool tma = !(flags & TF_GATHERED);
-    const int runs = (is_v ? 64 : 128) >> p.run_shift;
+    // Grains that TMA brings (by runs of several where all are whole).
+    const bool full = flags & TF_FULL, gathered = flags & TF_GATHERED, by_rows = is_v ? !full : gathered;
+    const uint32_t grains = is_v ? ms.live[buf] : ms.held[buf];
+    const int shift = p.grain_shift, unit = full ? p.run_shift : shift;  // log2 of the rows of a copy
+    const int rows = is_v ? 64 : 128;                                    // of a part
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
       // Part c of K is dims 64 c .. of this CTA's rows; of V (nb, kq) dims 256 nb + 128 rank .. of rows 64 kq ..
+      if (is_v && ((flags >> (TF_PARTS + (c & 3))) & 1) == 0) continue;
       const int row0 = is_v ? 64 * (c & 3) : 128 * (int)rank;
       const int dim0 = is_v ? 256 * (c >> 2) + 128 * (int)rank : 64 * c;
       const uint32_t st = is_v ? (FP8 ? kCodeSlots : kKStages<false>) + st_v : st_k, ph = is_v ? ph_v : ph_k;
@@ -535,40 +592,50 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
         ok = false;
         break;
       }
-      if (tma) {
-        // fp16: the bytes of both CTAs count at rank 0's barrier; rank 1's has the issue only.
-        if (lane == 0) {
-          const bool expects = warp == 0 && (FP8 || rank == 0);
-          if (expects) mbar_arrive_expect_tx(b_full, FP8 ? kCodePart : 2 * kPart);
-          mbar_arrive_cnt(b_full, expects ? 31 : 32);
+      if (!gathered) {
+        // Rows that TMA brings here; fp16: the bytes of both CTAs count at rank 0's
+        // barrier (of K, each has rows of its own), rank 1's has the issue only.
+        const uint32_t first = (uint32_t)row0 >> shift, n = (uint32_t)rows >> shift;
+        const uint32_t here = (grains >> first) & ((1u << n) - 1);
+        if (tid == 0 && (FP8 || rank == 0)) {
+          const uint32_t count = FP8 ? __popc(here) : is_v ? 2 * __popc(here) : __popc(grains);
+          if (count != 0) mbar_expect_tx(b_full, (count << shift) * (is_v ? 256u : 128u) / (FP8 ? 2u : 1u));
         }
-        const int turn = warp - c % n_warps, run = (turn < 0 ? turn + n_warps : turn) + lane * n_warps;
-        if (run < runs) {
-          const uint32_t dst = slot + (run << p.run_shift) * (is_v ? (FP8 ? 128u : 256u) : (FP8 ? 64u : 128u));
-          const CUtensorMap *m = is_v ? &p.tm_v : &p.tm_k;
-          const int2 x = ms.box[buf][(row0 >> p.run_shift) + run];
+        __syncwarp();
+        const int turn = warp - c % n_warps, i_copy = (turn < 0 ? turn + n_warps : turn) + lane * n_warps;
+        const int row = i_copy << unit;  // within the part
+        if (row < rows && ((here >> (row >> shift)) & 1u)) {
+          const uint32_t dst = slot + row * (is_v ? (FP8 ? 128u : 256u) : (FP8 ? 64u : 128u));
+          const int2 x = ms.box[buf][(row0 + row) >> shift];
+          const CUtensorMap *m = full ? (is_v ? &p.tm_v : &p.tm_k)
+                                      : (x.y & 1) ? (is_v ? &p.tm_vg[1] : &p.tm_kg[1]) : (is_v ? &p.tm_vg[0] : &p.tm_kg[0]);
           filled |= 1u << st;
           last_par = ph ? last_par & ~(1u << st) : last_par | 1u << st;
           if (FP8)
-            tma_load_3d(dst, m, b_full, dim0, x.y, x.x);
+            tma_load_3d(dst, m, b_full, dim0, x.y >> 1, x.x);
           else
-            tma_load_5d_pair(dst, m, cluster_addr(b_full, 0), 0, 0, dim0 >> 6, x.y >> 3, x.x);
+            tma_load_5d_pair(dst, m, cluster_addr(b_full, 0), 0, 0, dim0 >> 6, x.y >> 4, x.x);
         }
-      } else {
-        // 16-byte copies, eight lanes to a row (E4M3 codes of K: four).
+      }
+      if (by_rows) {
+        // 16-byte copies, eight lanes to a row (E4M3 codes of K: four), of the rows in
+        // grains that TMA does not bring.
         const unsigned long long *list = ms.row[buf] + row0;
-        auto src_of = [&](int row, int byte, unsigned long long skip, uint32_t &bytes) {
+        const uint32_t done = grains >> ((uint32_t)row0 >> shift & 31);
+        auto src_of = [&](int row, int byte, uint32_t &bytes) {
           const unsigned long long e = list[row];
           const long long to_v = (e & kSegBitT) ? vdelta1 : vdelta0;
-          bytes = (e & skip) ? 0u : 16u;
+          bytes = (e & (is_v ? kNoRowT | kNoValue : kNoRowT)) ? 0u : 16u;
           return reinterpret_cast<const uint8_t *>(e & ~15ull) + (is_v ? to_v : 0) + byte;
         };
         uint32_t n;
         if (FP8) {
-          const int shift = is_v ? 3 : 2;
-#pragma unroll 8
+          const int per_row = is_v ? 3 : 2;
+#pragma unroll 4
           for (int k = lane; k < 512; k += 32) {
-            const uint8_t *src = src_of(k >> shift, dim0 + 16 * (k & ((1 << shift) - 1)), is_v ? kNoRowT | kNoValue : kNoRowT, n);
+            const int row = k >> per_row;
+            if (!gathered && ((done >> (row >> shift)) & 1u)) continue;
+            const uint8_t *src = src_of(row, dim0 + 16 * (k & ((1 << per_row) - 1)), n);
             cp_async16z(slot + 16 * k, src, n);
           }
         } else if (!is_v) {
@@ -578,24 +645,27 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
           for (int k = 0; k < kTurns; ++k) {
             const int row = kRowsAtOnce * k + (tid >> 3);
             if (row < 128) {
-              const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, kNoRowT, n);
+              const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
               cp_async16z(slot + row * 128 + ((c8 ^ (row & 7)) << 4), src, n);
             }
           }
         } else {
           constexpr int kRowsAtOnce = 4 * kVLoadWarps<false>, kTurns = 64 / kRowsAtOnce;
-          static_assert(64 % kRowsAtOnce == 0, "rows of a V part");
+          static_assert(kRowsAtOnce == 8, "a turn lies within a grain");
           const int c8 = tid & 7;
 #pragma unroll
           for (int k = 0; k < kTurns; ++k) {
+            if (!gathered && ((done >> ((kRowsAtOnce * k) >> shift)) & 1u)) continue;
             const int row = kRowsAtOnce * k + (tid >> 3);
-            const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, kNoRowT | kNoValue, n);
+            const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
             const uint32_t dst = slot + (row >> 3) * 2048 + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4);
             cp_async16z(dst, src, n);
             cp_async16z(dst + 1024, src + 128, n);
           }
         }
         cp_async_arrive(b_full);
+      } else if (lane == 0) {
+        mbar_arrive_cnt(b_full, 32);
       }
       if (is_v) {
         if (++st_v == (FP8 ? kCodeSlots : kVStages<false>)) st_v = 0, ph_v ^= 1;
@@ -626,8 +696,17 @@ __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &m
   static_assert(kKStages<true> == kVStages<true>, "one ring length for both");
   Ring<kCodeSlots> codes;
   Ring<kKStages<true>> ring;
+  int parts = 15, buf = 0;
 #pragma unroll 1
   for (int i = 0; i < 8 * nt; ++i) {
+    if (is_v && (i & 7) == 0) {
+      const int g = i >> 3;
+      buf = g % kListsT;
+      if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait))) return;
+      parts = ms.flags[buf] >> TF_PARTS;
+      warp_arrive(smem_u32(&ms.list_empty[buf]));
+    }
+    if (((parts >> (i & 3)) & 1) == 0) continue;
     if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[slot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait))) return;
     const uint32_t src = sbase + kOffRing + 4 * kPart + (slot0 + codes.st) * kCodePart;
     const uint32_t dst = sbase + kOffRing + (stage0 + ring.st) * kPart;
@@ -673,18 +752,17 @@ __device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v) {
 #pragma unroll 1
   for (int g = 0; g < nt; ++g) {
     const int buf = g % kListsT;
-    if (!is_v) {
-      if (!wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait)) return;
-      const int flags = ms.flags[buf];
-      mbar_arrive(smem_u32(&ms.list_empty[buf]));
-      if (flags & TF_FIRST) {
-        if (!wait_phase(smem_u32(&ms.q_full), item & 1, TSITE_Q_FULL, &ms.wait)) return;
-        mbar_arrive_cluster(cluster_addr(smem_u32(&ms.peer_q_full), 0));
-        ++item;
-      }
+    if (!wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait)) return;
+    const int flags = ms.flags[buf];
+    mbar_arrive(smem_u32(&ms.list_empty[buf]));
+    if (!is_v && (flags & TF_FIRST)) {
+      if (!wait_phase(smem_u32(&ms.q_full), item & 1, TSITE_Q_FULL, &ms.wait)) return;
+      mbar_arrive_cluster(cluster_addr(smem_u32(&ms.peer_q_full), 0));
+      ++item;
     }
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
+      if (is_v && ((flags >> (TF_PARTS + (c & 3))) & 1) == 0) continue;
       const uint32_t bar = smem_u32(&ms.kv_full[stage0 + st]);
       if (!wait_phase(bar, ph, TSITE_KV_FULL, &ms.wait)) return;
       fence_proxy_async_smem();
@@ -710,6 +788,8 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
                                : sdesc_sw128(sbase + kOffRing, 16, 1024);
   Ring<IS_V ? kVStages<FP8> : kKStages<FP8>> ring;
   uint32_t item = 0;
+  bool ready = false;  // the next stage had landed when it was asked for
+  bool empty = true;   // no product has gone into this item's O
   auto wait = [&](uint64_t &bar, uint32_t parity, uint32_t site) -> bool {
     return __all_sync(0xffffffffu, wait_phase(smem_u32(&bar), parity, site, &ms.wait));
   };
@@ -719,7 +799,8 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
     if (!wait(ms.list_full[buf], (g / kListsT) & 1, TSITE_LIST_FULL)) return;
     const int flags = ms.flags[buf];
     warp_arrive(smem_u32(&ms.list_empty[buf]));
-    const bool first = flags & TF_FIRST, last = flags & TF_LAST, fence = FP8 || (flags & TF_GATHERED);
+    const bool first = flags & TF_FIRST, last = flags & TF_LAST, fence = FP8 || !(flags & TF_FULL);
+    const int parts = IS_V ? flags >> TF_PARTS : 15, lowest = __ffs(parts) - 1;
     const uint32_t sb = g & 1;
     if (IS_V) {
       if (first && !wait(ms.o_empty, (item & 1) ^ 1, TSITE_O_EMPTY)) return;
@@ -729,20 +810,21 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
       if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, TSITE_S_EMPTY)) return;
     }
     if (first) ++item;
+    empty = empty || first;
     tc_fence_after();
-    bool ready = false;
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
+      if (IS_V && ((parts >> (c & 3)) & 1) == 0) continue;
       const uint32_t st = ring.st;
       if (!__all_sync(0xffffffffu, ready) && !wait(ms.kv_full[kStage0 + st], ring.ph, TSITE_KV_FULL)) return;
       ring.advance();
       // The next stage is asked for before this one's products are issued.
-      ready = c < 7 && mbar_test(smem_u32(&ms.kv_full[kStage0 + ring.st]), ring.ph);
+      ready = mbar_test(smem_u32(&ms.kv_full[kStage0 + ring.st]), ring.ph);
       if (fence) fence_proxy_async_smem();
       const uint64_t a0 = sdesc_add(a_desc, (IS_V ? c & 3 : c) * 8192);
       const uint64_t b0 = sdesc_add(b_desc, st * kPart);
       const uint32_t d = IS_V ? tmem + 128 * (c >> 2) : tmem + kTmemTS + 128 * sb;
-      const bool fresh = IS_V ? first && (c & 3) == 0 : c == 0;
+      const bool fresh = IS_V ? empty && (c & 3) == lowest : c == 0;
       if (elect_lane()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
@@ -752,16 +834,21 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
             umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * (IS_V ? 4096 : 32)), kIdesc);
         }
         umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + st]));
-        if (IS_V) {
-          if ((c & 3) == 3 && last) umma_pair_commit(smem_u32(&ms.o_full[c >> 2]));
-          if (c == 7) umma_pair_commit(smem_u32(&ms.p_empty));
-        } else if (c == 7) {
+        if (!IS_V && c == 7) {
           umma_pair_commit(smem_u32(&ms.s_full[sb]));
           if (last) umma_pair_commit(smem_u32(&ms.q_empty));
         }
+        if (IS_V && last && c < 4 && (parts & 15) >> (c + 1) == 0) umma_pair_commit(smem_u32(&ms.o_full[0]));
       }
       __syncwarp();
     }
+    if (parts != 0) empty = false;
+    if (IS_V && elect_lane()) {
+      if (last && (parts & 15) == 0) umma_pair_commit(smem_u32(&ms.o_full[0]));
+      if (last) umma_pair_commit(smem_u32(&ms.o_full[1]));
+      umma_pair_commit(smem_u32(&ms.p_empty));
+    }
+    __syncwarp();
   }
 }
 
@@ -958,7 +1045,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
           uint32_t x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const __half2 v = __floats2half2_rn(o[16 * k + 2 * i] * inv, o[16 * k + 2 * i + 1] * inv);
+            const __half2 v = none ? __half2{} : __floats2half2_rn(o[16 * k + 2 * i] * inv, o[16 * k + 2 * i + 1] * inv);
             x[i] = *reinterpret_cast<const uint32_t *>(&v);
           }
           if (p.o_wide) {
@@ -974,7 +1061,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
         for (int k = 0; k < 4; ++k) {
           uint32_t x[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(o[8 * k + i] * inv);
+          for (int i = 0; i < 8; ++i) x[i] = none ? 0u : __float_as_uint(o[8 * k + i] * inv);
           stg32(at + 8 * k, x);
         }
       }
@@ -1013,8 +1100,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     }
     for (int s = 0; s < kListsT; ++s) {
       mbar_init(smem_u32(&ms.list_full[s]), 1);
-      mbar_init(smem_u32(&ms.list_empty[s]), kComputeWarps + (rank == 0 ? 2 : 1) +
-                                                 (FP8 ? 1 : kKLoadWarps<false> + kVLoadWarps<false>));
+      // Softmax, the last two warps, loaders and those that widen V.
+      mbar_init(smem_u32(&ms.list_empty[s]), kComputeWarps + 2 + (FP8 ? 3 : kKLoadWarps<false> + kVLoadWarps<false>));
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ms.s_full[s]), 1);
@@ -1030,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     ms.wait.abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.tm_q);
-    if (p.run_rows > 0) {
+    if (p.grain > 0 && p.seg[1].max_rows > 0) {
       tma_prefetch_desc(&p.tm_k);
       tma_prefetch_desc(&p.tm_v);
     }

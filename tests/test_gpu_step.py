@@ -257,6 +257,10 @@ TREES = [
     ([5, 4], [1024, 2000], 4, 128, False, False, False, 1),
     ([17] * 20, list(range(0, 400, 20)), 4, 16, False, True, False, 128),
     ([2] * 90, [30] * 90, 128, 7, True, True, True, 128),
+    ([30, 9], [530, 300], 4, 12, False, False, False, 128),
+    ([64, 100], [900, 511], 4, 20, True, False, False, 50),
+    ([64, 100], [900, 511], 4, 40, True, False, True, 50),
+    ([31, 128], [1500, 256], 2, 56, False, True, False, 128),
 ]
 
 
@@ -381,6 +385,21 @@ def test_tree_bad_rows_spoil_their_tokens_only(torch, ds4a, f8, chain):
                 assert np.isnan(o[hit]).all() and np.isnan(lse[hit]).all()
             else:
                 assert np.isfinite(lse[hit]).all()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("page", [16, 7])
+def test_tree_first_tile_without_rows(torch, ds4a, f8, page):
+    """The pages of a sequence's first compressed rows are absent, so that nothing is seen there; then of all."""
+    rng = np.random.default_rng(31)
+    geom, first, parent, q, raw, comp = tree_case(rng, [5, 4, 2], [700, 600, 40], 4, page, f8, False)
+    for b, gone in ((0, 560 // page), (1, 100000), (2, 100000)):
+        comp["table"][b, :gone] = -1
+    raw["table"][2] = 1 << 20
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    assert (want[4][9:] == 0).all() and (want[4][:9] > 100).all()
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
 
 
 def test_tree_pages_past_32_bit_offsets(torch, ds4a):
