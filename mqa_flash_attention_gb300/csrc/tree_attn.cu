@@ -62,12 +62,13 @@ template <bool FP8>
 constexpr int kVStages = FP8 ? 2 : 3;
 constexpr int kCodeSlots = 3;
 static_assert(7 * kPart <= kRingBytes && 4 * kPart + 2 * kCodeSlots * kCodePart <= kRingBytes, "shared memory of the rings");
-// Warps 0-7 softmax and epilogue; 8-10 load K and 11-12 V (E4M3: 8 loads both, 9-10
-// widen K and 11-12 V); 13 finds the rows of the tiles; 14 issues P . V, 15 Q . K (in
+// Warps 0-7 softmax and epilogue; 8-10 load K and 11-12 V (E4M3: 8 loads K and 11 V,
+// 9-10 widen K and 12 V); 13 finds the rows of the tiles; 14 issues P . V, 15 Q . K (in
 // the CTA of rank 1 they report what has landed).  Every role is a loop over the
 // tiles that meets the others at mbarriers only, and its code is kept small: what
 // all roles run through in a tile has to stay in the instruction cache.
-constexpr int kKLoadWarp0 = 8, kVLoadWarp0 = 11, kWidenWarp0 = 9, kListWarp = 13, kPvWarp = 14, kQkWarp = 15;
+constexpr int kKLoadWarp0 = 8, kVLoadWarp0 = 11, kListWarp = 13, kPvWarp = 14, kQkWarp = 15;
+constexpr int kWidenK0 = 9, kWidenV0 = 12, kWidenKWarps = 2, kWidenVWarps = 1;
 template <bool FP8>
 constexpr int kKLoadWarps = FP8 ? 1 : 3;
 template <bool FP8>
@@ -537,26 +538,26 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
 // ------------------------------------------------------------------ loaders
 
 // The warps of K, or of V, load part after part into their ring: by TMA, a run or a
-// grain per lane (warps in turn), or by 16-byte copies.  E4M3: one warp for both, K one
-// tile ahead.
+// grain per lane, or by 16-byte copies.  A warp stands some 600 cycles at a bulk copy,
+// so the warps take the parts that TMA brings in turn; parts with gathered rows
+// are loaded by all.  (A warp that waits for a stage has waited for one at most
+// as many parts before as there are warps, and there are more stages than
+// warps, so it is never two phases behind.)
 template <bool FP8>
 __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, uint32_t rank, uint32_t sbase, TMisc &ms,
-                                               bool v_warp, int tid) {
+                                               bool is_v, int tid) {
   if (nt <= 0) return;
-  const int n_warps = v_warp ? kVLoadWarps<FP8> : kKLoadWarps<FP8>;
+  static_assert(kKLoadWarps<FP8> <= kKStages<false> && kVLoadWarps<FP8> <= kVStages<false>, "no more warps than stages");
+  const int n_warps = is_v ? kVLoadWarps<FP8> : kKLoadWarps<FP8>;
   const int lane = tid & 31, warp = tid >> 5;
   const long long vdelta0 = p.seg[0].v - p.seg[0].k, vdelta1 = p.seg[1].v - p.seg[1].k;
-  uint32_t st_k = 0, ph_k = 1, st_v = 0, ph_v = 1;  // next stage of either ring and the parity to wait for
+  const uint32_t st0 = is_v ? (FP8 ? kCodeSlots : kKStages<false>) : 0;
+  const uint32_t stages = FP8 ? kCodeSlots : is_v ? kVStages<false> : kKStages<false>;
+  uint32_t at = 0, ph = 1, turn = 0;  // next stage of the ring and the parity to wait for; the warp whose turn is next
   uint32_t filled = 0, last_par = 0, n_item = 0;
   bool ok = true, q_issued = false;
-  // Step i loads K of tile i / 2 (even) or V of the tile before (odd): warps of
-  // one kind have every other step.
-  const int steps = 2 * nt + 2;
 #pragma unroll 1
-  for (int i = FP8 ? 0 : v_warp ? 3 : 0; i < steps && ok; i += FP8 ? 1 : 2) {
-    const bool is_v = i & 1;
-    const int g = is_v ? (i >> 1) - 1 : i >> 1;
-    if (g < 0 || g >= nt) continue;
+  for (int g = 0; g < nt && ok; ++g) {
     const int buf = g % kListsT;
     if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait))) break;
     const int flags = ms.flags[buf];
@@ -582,40 +583,44 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
     for (int c = 0; c < 8; ++c) {
       // Part c of K is dims 64 c .. of this CTA's rows; of V (nb, kq) dims 256 nb + 128 rank .. of rows 64 kq ..
       if (is_v && ((flags >> (TF_PARTS + (c & 3))) & 1) == 0) continue;
+      const bool mine = (int)turn == warp;
+      const uint32_t st = st0 + at, par = ph;
+      if ((int)++turn == n_warps) turn = 0;
+      if (++at == stages) at = 0, ph ^= 1;
+      if (!mine && !by_rows) continue;
       const int row0 = is_v ? 64 * (c & 3) : 128 * (int)rank;
       const int dim0 = is_v ? 256 * (c >> 2) + 128 * (int)rank : 64 * c;
-      const uint32_t st = is_v ? (FP8 ? kCodeSlots : kKStages<false>) + st_v : st_k, ph = is_v ? ph_v : ph_k;
       const uint32_t slot = sbase + kOffRing + (FP8 ? 4 * kPart + st * kCodePart : st * kPart);
       const uint32_t b_full = smem_u32(FP8 ? &ms.code_full[st] : &ms.kv_full[st]);
-      if (!__all_sync(0xffffffffu, wait_phase(smem_u32(FP8 ? &ms.code_empty[st] : &ms.kv_empty[st]), ph,
+      if (!__all_sync(0xffffffffu, wait_phase(smem_u32(FP8 ? &ms.code_empty[st] : &ms.kv_empty[st]), par,
                                               FP8 ? TSITE_CODE_EMPTY : TSITE_KV_EMPTY, &ms.wait))) {
         ok = false;
         break;
       }
-      if (!gathered) {
+      if (!gathered && mine) {
         // Rows that TMA brings here; fp16: the bytes of both CTAs count at rank 0's
         // barrier (of K, each has rows of its own), rank 1's has the issue only.
         const uint32_t first = (uint32_t)row0 >> shift, n = (uint32_t)rows >> shift;
         const uint32_t here = (grains >> first) & ((1u << n) - 1);
-        if (tid == 0 && (FP8 || rank == 0)) {
+        if (lane == 0) {
           const uint32_t count = FP8 ? __popc(here) : is_v ? 2 * __popc(here) : __popc(grains);
-          if (count != 0) mbar_expect_tx(b_full, (count << shift) * (is_v ? 256u : 128u) / (FP8 ? 2u : 1u));
+          if (count != 0 && (FP8 || rank == 0)) mbar_expect_tx(b_full, (count << shift) * (is_v ? 256u : 128u) / (FP8 ? 2u : 1u));
+          if (!by_rows) mbar_arrive_cnt(b_full, 32 * n_warps);
         }
-        __syncwarp();
-        const int turn = warp - c % n_warps, i_copy = (turn < 0 ? turn + n_warps : turn) + lane * n_warps;
-        const int row = i_copy << unit;  // within the part
+        const int row = lane << unit;  // within the part
         if (row < rows && ((here >> (row >> shift)) & 1u)) {
           const uint32_t dst = slot + row * (is_v ? (FP8 ? 128u : 256u) : (FP8 ? 64u : 128u));
           const int2 x = ms.box[buf][(row0 + row) >> shift];
           const CUtensorMap *m = full ? (is_v ? &p.tm_v : &p.tm_k)
                                       : (x.y & 1) ? (is_v ? &p.tm_vg[1] : &p.tm_kg[1]) : (is_v ? &p.tm_vg[0] : &p.tm_kg[0]);
           filled |= 1u << st;
-          last_par = ph ? last_par & ~(1u << st) : last_par | 1u << st;
+          last_par = par ? last_par & ~(1u << st) : last_par | 1u << st;
           if (FP8)
             tma_load_3d(dst, m, b_full, dim0, x.y >> 1, x.x);
           else
             tma_load_5d_pair(dst, m, cluster_addr(b_full, 0), 0, 0, dim0 >> 6, x.y >> 4, x.x);
         }
+        __syncwarp();
       }
       if (by_rows) {
         // 16-byte copies, eight lanes to a row (E4M3 codes of K: four), of the rows in
@@ -664,17 +669,10 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
           }
         }
         cp_async_arrive(b_full);
-      } else if (lane == 0) {
-        mbar_arrive_cnt(b_full, 32);
-      }
-      if (is_v) {
-        if (++st_v == (FP8 ? kCodeSlots : kVStages<false>)) st_v = 0, ph_v ^= 1;
-      } else {
-        if (++st_k == (FP8 ? kCodeSlots : kKStages<false>)) st_k = 0, ph_k ^= 1;
       }
     }
     __syncwarp();
-    if (ok && (!FP8 || is_v)) warp_arrive(smem_u32(&ms.list_empty[buf]));
+    if (ok) warp_arrive(smem_u32(&ms.list_empty[buf]));
   }
   // No copy may still be landing at exit.  (When every wait succeeded the MMA
   // warps have seen all stages land.)
@@ -689,52 +687,56 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
   }
 }
 
-// Warps 9 and 10 (K) or 11 and 12 (V) with E4M3 rows: a slot's codes, 128 a thread,
-// widened exactly into the next stage in the layout that the fp16 kernel's copies have.
+// With E4M3 rows: a slot's codes widened exactly into the next stage, in the layout
+// that the fp16 kernel's copies have; 64 threads for K, 32 for V (twice 128 codes each).
 __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &ms, bool is_v, int ct) {
   const uint32_t slot0 = is_v ? kCodeSlots : 0, stage0 = is_v ? kKStages<true> : 0;
   static_assert(kKStages<true> == kVStages<true>, "one ring length for both");
+  const int threads = 32 * (is_v ? kWidenVWarps : kWidenKWarps);
   Ring<kCodeSlots> codes;
   Ring<kKStages<true>> ring;
-  int parts = 15, buf = 0;
+  int parts = 15;
 #pragma unroll 1
   for (int i = 0; i < 8 * nt; ++i) {
     if (is_v && (i & 7) == 0) {
-      const int g = i >> 3;
-      buf = g % kListsT;
+      const int g = i >> 3, buf = g % kListsT;
       if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait))) return;
       parts = ms.flags[buf] >> TF_PARTS;
       warp_arrive(smem_u32(&ms.list_empty[buf]));
     }
     if (((parts >> (i & 3)) & 1) == 0) continue;
-    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[slot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait))) return;
     const uint32_t src = sbase + kOffRing + 4 * kPart + (slot0 + codes.st) * kCodePart;
     const uint32_t dst = sbase + kOffRing + (stage0 + ring.st) * kPart;
-    uint4 raw[8];
+    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[slot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait) &&
+                                     wait_phase(smem_u32(&ms.kv_empty[stage0 + ring.st]), ring.ph ^ 1, TSITE_KV_EMPTY, &ms.wait)))
+      return;
+#pragma unroll 1
+    for (int n0 = ct; n0 < 512; n0 += 8 * threads) {
+      uint4 raw[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(raw[k].x), "=r"(raw[k].y), "=r"(raw[k].z), "=r"(raw[k].w)
-                   : "r"(src + 16 * (ct + 64 * k)));
-    warp_arrive(smem_u32(&ms.code_empty[slot0 + codes.st]));
-    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.kv_empty[stage0 + ring.st]), ring.ph ^ 1, TSITE_KV_EMPTY, &ms.wait))) return;
+      for (int k = 0; k < 8; ++k)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(raw[k].x), "=r"(raw[k].y), "=r"(raw[k].z), "=r"(raw[k].w)
+                     : "r"(src + 16 * (n0 + threads * k)));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int n = ct + 64 * k;
-      const int row = is_v ? n >> 3 : n >> 2, c = is_v ? n & 7 : n & 3;  // 16 codes: chunks 2c, 2c + 1 of 8 values
-      const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-      uint32_t h[8];
+      for (int k = 0; k < 8; ++k) {
+        const int n = n0 + threads * k;
+        const int row = is_v ? n >> 3 : n >> 2, c = is_v ? n & 7 : n & 3;  // 16 codes: chunks 2c, 2c + 1 of 8 values
+        const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        uint32_t h[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] & 0xFFFFu));
-        h[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] >> 16));
+        for (int e = 0; e < 4; ++e) {
+          h[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] & 0xFFFFu));
+          h[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] >> 16));
+        }
+        const uint32_t drow = dst + (row & 7) * 128 + (is_v ? (row >> 3) * 2048 + (c >> 2) * 1024 : (row >> 3) * 1024);
+        const int col = 2 * (c & 3);
+        sts_v4(drow + ((col ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+        sts_v4(drow + (((col + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
       }
-      const uint32_t drow = dst + (row & 7) * 128 + (is_v ? (row >> 3) * 2048 + (c >> 2) * 1024 : (row >> 3) * 1024);
-      const int col = 2 * (c & 3);
-      sts_v4(drow + ((col ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-      sts_v4(drow + (((col + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
     }
-    warp_arrive(smem_u32(&ms.kv_full[stage0 + ring.st]));
+    warp_arrive(smem_u32(&ms.code_empty[slot0 + codes.st]));
+    if ((ct & 31) == 0) mbar_arrive(smem_u32(&ms.kv_full[stage0 + ring.st]));
     codes.advance();
     ring.advance();
   }
@@ -1089,19 +1091,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     mbar_init(smem_u32(&ms.q_empty), 1);
     mbar_init(smem_u32(&ms.peer_q_full), 1);
     for (int s = 0; s < 7; ++s) {
-      // Loader threads, or the two warps that widen; and the other CTA's report.
+      // Loader threads, or the warps that widen; and the other CTA's report.
       const int loaders = 32 * (s < kKStages<false> ? kKLoadWarps<false> : kVLoadWarps<false>);
-      mbar_init(smem_u32(&ms.kv_full[s]), (FP8 ? 2 : loaders) + (rank == 0 ? 1 : 0));
+      const int widen = s < kKStages<true> ? kWidenKWarps : kWidenVWarps;
+      mbar_init(smem_u32(&ms.kv_full[s]), (FP8 ? widen : loaders) + (rank == 0 ? 1 : 0));
       mbar_init(smem_u32(&ms.kv_empty[s]), 1);
     }
     for (int s = 0; s < 2 * kCodeSlots; ++s) {
       mbar_init(smem_u32(&ms.code_full[s]), 32);
-      mbar_init(smem_u32(&ms.code_empty[s]), 2);
+      mbar_init(smem_u32(&ms.code_empty[s]), s < kCodeSlots ? kWidenKWarps : kWidenVWarps);
     }
     for (int s = 0; s < kListsT; ++s) {
       mbar_init(smem_u32(&ms.list_full[s]), 1);
       // Softmax, the last two warps, loaders and those that widen V.
-      mbar_init(smem_u32(&ms.list_empty[s]), kComputeWarps + 2 + (FP8 ? 3 : kKLoadWarps<false> + kVLoadWarps<false>));
+      mbar_init(smem_u32(&ms.list_empty[s]), kComputeWarps + 2 + kKLoadWarps<FP8> + kVLoadWarps<FP8> +
+                                                 (FP8 ? kWidenVWarps : 0));
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ms.s_full[s]), 1);
@@ -1153,11 +1157,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     __syncwarp();
   } else if (warp == kListWarp) {
     tree_list_role<FP8>(p, nt, cluster, rank, ms, threadIdx.x & 31);
-  } else if (FP8 && warp >= kWidenWarp0) {
-    const bool is_v = warp >= kWidenWarp0 + 2;
-    tree_widen_role(nt, sbase, ms, is_v, (threadIdx.x - 32 * kWidenWarp0) & 63);
+  } else if (FP8 && warp != kKLoadWarp0 && warp != kVLoadWarp0) {
+    const bool is_v = warp >= kWidenV0;
+    tree_widen_role(nt, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kWidenV0 : kWidenK0));
   } else {
-    const bool is_v = !FP8 && warp >= kVLoadWarp0;
+    const bool is_v = warp >= kVLoadWarp0;
     tree_load_role<FP8>(p, nt, rank, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kVLoadWarp0 : kKLoadWarp0));
   }
   tc_fence_before();
