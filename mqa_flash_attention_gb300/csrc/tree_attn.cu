@@ -117,9 +117,10 @@ struct TMisc {
   uint64_t code_full[2 * kCodeSlots], code_empty[2 * kCodeSlots];
   uint64_t list_full[kListsT], list_empty[kListsT];
   uint64_t s_full[2], s_empty[2], o_full[2];
-  uint64_t p_full, p_empty, o_empty, mma_done;
+  uint64_t p_full[4], p_empty[4], o_empty, mma_done;  // (P: by boxes of 64 rows)
   WaitBox wait;
   UnitRec unit;   // of the tile that is listed
+  uint8_t odd_row[kRows];  // its rows that one token sees and the other does not
   uint32_t tmem_base;
 };
 constexpr uint32_t kTreeSmem = kOffTMisc + ((sizeof(TMisc) + 127) / 128) * 128 + 1024;
@@ -339,14 +340,28 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
             ((b.y >> 1) + more) * (sg ? p.seg[1].row_stride : p.seg[0].row_stride)) |
            (sg ? kSegBitT : 0);
   };
-  // Who sees the list's place x (1: the first token, 2: the second).
-  auto seen_by = [&](int x) -> unsigned {
-    if (x < r.raw_at) return (x < r.nc_of[0] ? 1 : 0) | (x < r.nc_of[1] ? 2 : 0);
-    if (x >= r.len) return 0;
-    const int row = r.raw0 + (x - r.raw_at), d = row - r.n_raw;
-    if (d < 0) return (row >= r.ra[0] && row < r.rb[0] ? 1 : 0) | (row >= r.ra[1] && row < r.rb[1] ? 2 : 0);
-    if (chain) return (d >= r.da[0] && d < r.db[0] ? 1 : 0) | (d >= r.da[1] && d < r.db[1] ? 2 : 0);
-    return ((r.anc[0][d >> 5] >> (d & 31)) & 1u) | (((r.anc[1][d >> 5] >> (d & 31)) & 1u) << 1);
+  // Bits lo .. hi - 1 of a word (either may lie outside).
+  auto range = [](int lo, int hi) -> unsigned {
+    lo = max(lo, 0);
+    hi = min(hi, 32);
+    return lo < hi ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0;
+  };
+  // Which of places x .. x + 31 of the list token i sees.
+  auto seen_word = [&](int i, int x) -> unsigned {
+    const int to_row = r.raw0 - r.raw_at;  // from a place to a raw row
+    unsigned m = range(-x, r.nc_of[i] - x);
+    const int row = x + to_row;            // of the word's first bit, were it a raw one
+    unsigned raw = range(r.ra[i] - row, r.rb[i] - row);
+    const int d = r.n_raw - row;           // bit of the first new row
+    if (chain) {
+      raw |= range(r.da[i] + d, r.db[i] + d);
+    } else if (d < 32 && d > -kTreeTokens) {
+      // Bits d .. of the word are nodes 0 .. : two words of the ancestors, shifted.
+      const int k = d >= 0 ? 0 : -d >> 5, off = d + 32 * k;  // 0 .. 31, or -31 .. 0
+      const unsigned a0 = r.anc[i][k], a1 = k < 3 ? r.anc[i][k + 1] : 0;
+      raw |= off >= 0 ? a0 << off : (a0 >> -off) | (a1 << (32 + off));
+    }
+    return m | (raw & range(r.raw_at - x, r.len - x));
   };
 #pragma unroll 1
   for (int g = 0; g < nt; ++g) {
@@ -372,15 +387,29 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
       live = held;
       full = full && held == (kRows >> shift == 32 ? 0xffffffffu : (1u << (kRows >> shift)) - 1);
     }
+    // Lane k: what either token sees of rows 32 k .. that have a page.
+    unsigned see0 = 0xffffffffu, see1 = 0xffffffffu;
+    if (!full && lane < kRows / 32) {
+      unsigned there = 0xffffffffu;
+      if (p.grain > 0) {
+        there = 0;
+#pragma unroll 1
+        for (int k = 0; k < 32 >> shift; ++k)
+          if ((held >> ((lane << (5 - shift)) + k)) & 1u) there |= ((1u << grain) - 1) << (k << shift);
+      }
+      see0 = seen_word(0, base + 32 * lane) & there;
+      see1 = seen_word(1, base + 32 * lane) & there;
+    }
     float ks[FP8 ? 8 : 1], vs[FP8 ? 8 : 1];
     if (FP8 && p.grain > 0) {
 #pragma unroll
       for (int k = 0; k < (FP8 ? 8 : 1); ++k) {
         const int x = 32 * k + lane;
         const int page = __shfl_sync(0xffffffffu, mine.x, x >> shift), at = __shfl_sync(0xffffffffu, mine.y, x >> shift);
+        const unsigned some = __shfl_sync(0xffffffffu, see0 | see1, k);
         ks[k] = 0.f;
         vs[k] = 1.f;
-        if (page >= 0 && (full || seen_by(base + x) != 0)) {
+        if ((some >> lane) & 1u) {
           const bool sg = at & 1;
           const long long sr = (long long)page * (sg ? p.seg[1].page_rows : p.seg[0].page_rows) + (at >> 1) + (x & (grain - 1));
           ks[k] = (sg ? p.seg[1].k_scale : p.seg[0].k_scale)[sr];
@@ -391,116 +420,100 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
     if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_empty[buf]), ((g / kListsT) & 1) ^ 1, TSITE_LIST_EMPTY,
                                             &ms.wait)))
       return;
-    unsigned parts = 15;
-    if (full) {
-      if (lane < kRows / 32) ms.mask[buf][lane] = 0xFFFFFFFFu;
-    } else {
-      parts = 0;
-      unsigned any_of = 0, one_of = 0, one_any = 0;  // lane k, rows 32 k ..: seen by some token, by one; words of the latter
+    if (p.grain > 0) ms.box[buf][lane] = mine;
+    if (p.grain == 0) {
+      // Every row by itself.
 #pragma unroll 1
       for (int k = 0; k < kRows / 32; ++k) {
         const int x = 32 * k + lane;
-        int2 at = mine;
-        if (p.grain > 0) {
-          at.x = __shfl_sync(0xffffffffu, mine.x, x >> shift);
-        } else {
-          at = place(base + x);
-          ms.row[buf][x] = pad_row;
-        }
-        const unsigned seen = at.x >= 0 ? seen_by(base + x) : 0;
-        if (p.grain == 0 && seen != 0) {
-          ms.row[buf][x] = address(at, 0);
-          if (FP8) {
-            const bool sg = at.y & 1;
-            const long long sr = (long long)at.x * (sg ? p.seg[1].page_rows : p.seg[0].page_rows) + (at.y >> 1);
-            const float kk = (sg ? p.seg[1].k_scale : p.seg[0].k_scale)[sr], vv = (sg ? p.seg[1].v_scale : p.seg[0].v_scale)[sr];
-            ms.ksc[buf][x] = kk;
-            ms.lvs[buf][x] = vv;
-          }
-        } else if (FP8 && p.grain == 0) {
-          ms.ksc[buf][x] = 0.f;
-          ms.lvs[buf][x] = 1.f;
-        }
-        const unsigned own = __ballot_sync(0xffffffffu, (seen >> rank) & 1), some = __ballot_sync(0xffffffffu, seen != 0);
-        const unsigned one = __ballot_sync(0xffffffffu, seen == 1 || seen == 2);
+        const int2 b = place(base + x);
+        const unsigned there = __ballot_sync(0xffffffffu, b.x >= 0);
         if (lane == k) {
-          ms.mask[buf][k] = own;
-          any_of = some;
-          one_of = one;
+          see0 &= there;
+          see1 &= there;
         }
-        if (one != 0) one_any |= 1u << k;
-        if (some != 0) parts |= 1u << (k >> 1);
+        const bool use = (__shfl_sync(0xffffffffu, see0 | see1, k) >> lane) & 1u;
+        ms.row[buf][x] = use ? address(b, 0) : pad_row;
+        if (FP8) {
+          const bool sg = b.y & 1;
+          const long long sr = (long long)b.x * (sg ? p.seg[1].page_rows : p.seg[0].page_rows) + (b.y >> 1);
+          ms.ksc[buf][x] = use ? (sg ? p.seg[1].k_scale : p.seg[0].k_scale)[sr] : 0.f;
+          ms.lvs[buf][x] = use ? (sg ? p.seg[1].v_scale : p.seg[0].v_scale)[sr] : 1.f;
+        }
       }
+    }
+    if (lane < kRows / 32) ms.mask[buf][lane] = rank == 0 ? see0 : see1;
+    unsigned parts = 15;
+    if (!full) {
+      const unsigned some = __ballot_sync(0xffffffffu, lane < kRows / 32 && (see0 | see1) != 0);
+      parts = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) parts |= (some >> (2 * k)) & 3 ? 1u << k : 0;
       // A V row that one token sees and the other does not must be finite, because
       // its weight of 0 multiplies it all the same: the warp looks these few rows
-      // through (new rows, edges of a window).  One that is not finite is left out
-      // of the product, and the token that sees it is marked.
-      __syncwarp();
-      unsigned bad_of = 0, who = 0;
-      int k = 0;
+      // through (new rows, edges of a window), eight lanes to a row.  One that is
+      // not finite is left out of the product, and the token that sees it is marked.
+      unsigned one = lane < kRows / 32 ? see0 ^ see1 : 0, bad_of = 0;
+      int n_one = 0;
 #pragma unroll 1
-      while (one_any != 0 || who != 0) {
-        constexpr int kAhead = 8, kWords = FP8 ? 1 : 2;
-        uint4 v[kAhead][kWords];
-        int x[kAhead];
+      for (unsigned words = __ballot_sync(0xffffffffu, one != 0); words != 0; words &= words - 1) {
+        const int k = __ffs(words) - 1;
+        const unsigned bits = __shfl_sync(0xffffffffu, one, k);
+        if ((bits >> lane) & 1u) ms.odd_row[n_one + __popc(bits & ((1u << lane) - 1))] = (uint8_t)(32 * k + lane);
+        n_one += __popc(bits);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int i0 = 0; i0 < n_one; i0 += 4) {
+        const int i = i0 + (lane >> 3), x = ms.odd_row[min(i, n_one - 1)];
+        const unsigned long long e = p.grain > 0 ? address(ms.box[buf][x >> shift], x & (grain - 1)) : ms.row[buf][x];
+        const uint4 *src = reinterpret_cast<const uint4 *>(e & ~15ull) + (lane & 7);
+        src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(src) + ((e & kSegBitT) ? vdelta1 : vdelta0));
+        constexpr int kWords = FP8 ? 4 : 8;
+        uint4 v[kWords];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          if (who == 0 && one_any != 0) {
-            k = __ffs(one_any) - 1;
-            one_any &= one_any - 1;
-            who = __shfl_sync(0xffffffffu, one_of, k);
-          }
-          x[a] = who != 0 ? 32 * k + __ffs(who) - 1 : -1;
-          who &= who - 1;
-          unsigned long long e = 0;
-          if (x[a] >= 0) {
-            if (p.grain > 0) {
-              const int2 b = make_int2(__shfl_sync(0xffffffffu, mine.x, x[a] >> shift), __shfl_sync(0xffffffffu, mine.y, x[a] >> shift));
-              e = address(b, x[a] & (grain - 1));
-            } else {
-              e = ms.row[buf][x[a]];
-            }
-          }
-          const uint8_t *src = reinterpret_cast<const uint8_t *>(e & ~15ull) + ((e & kSegBitT) ? vdelta1 : vdelta0);
+        for (int w = 0; w < kWords; ++w) v[w] = src[8 * w];
+        uint32_t odd = 0;
 #pragma unroll
-          for (int w = 0; w < kWords; ++w)
-            v[a][w] = x[a] >= 0 ? reinterpret_cast<const uint4 *>(src)[32 * w + lane] : make_uint4(0, 0, 0, 0);
+        for (int w = 0; w < kWords; ++w) {
+          const uint32_t y[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            odd |= FP8 ? ((y[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u   // a code of NaN: seven ones
+                       : ((y[k] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;  // an exponent of five ones
         }
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          uint32_t odd = 0;
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            const uint32_t y[4] = {v[a][w].x, v[a][w].y, v[a][w].z, v[a][w].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              odd |= FP8 ? ((y[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u   // a code of NaN: seven ones
-                         : ((y[i] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;  // an exponent of five ones
-          }
-          if (__any_sync(0xffffffffu, odd != 0)) {
-            spoiled = spoiled || ((ms.mask[buf][x[a] >> 5] >> (x[a] & 31)) & 1u) != 0;
-            if (lane == x[a] >> 5) bad_of |= 1u << (x[a] & 31);
+        const unsigned who = __ballot_sync(0xffffffffu, odd != 0);
+        if (who == 0) continue;
+#pragma unroll 1
+        for (int k = 0; k < 4 && i0 + k < n_one; ++k) {
+          if (((who >> (8 * k)) & 255u) == 0) continue;
+          const int y = ms.odd_row[i0 + k];
+          if (lane == y >> 5) {
+            bad_of |= 1u << (y & 31);
+            spoiled = spoiled || (((rank == 0 ? see0 : see1) >> (y & 31)) & 1u) != 0;
           }
         }
       }
+      spoiled = __any_sync(0xffffffffu, spoiled);
       if (p.grain > 0) {
         // Grains of which every row is seen and fit for the product; of the others the rows.
-        const unsigned good = any_of & ~bad_of, at_word = (lane << shift) >> 5 & 7;
-        const unsigned bits = __shfl_sync(0xffffffffu, good, at_word) >> ((lane << shift) & 31), ones = (1u << grain) - 1;
+        const unsigned good = (see0 | see1) & ~bad_of;
+        const unsigned bits = __shfl_sync(0xffffffffu, good, ((lane << shift) >> 5) & 7) >> ((lane << shift) & 31);
+        const unsigned ones = (1u << grain) - 1, in_word = (1u << (32 >> shift)) - 1;
         live = __ballot_sync(0xffffffffu, mine.x >= 0 && lane < kRows >> shift && (bits & ones) == ones);
-        const unsigned in_word = (1u << (32 >> shift)) - 1;
 #pragma unroll 1
         for (int w = 0; w < kRows / 32; ++w) {
           if (((parts >> (w >> 1)) & 1u) == 0 || ((live >> (w << (5 - shift))) & in_word) == in_word) continue;
           const int x = 32 * w + lane;
-          const int2 b = make_int2(__shfl_sync(0xffffffffu, mine.x, x >> shift), __shfl_sync(0xffffffffu, mine.y, x >> shift));
           const bool use = (__shfl_sync(0xffffffffu, good, w) >> lane) & 1u;
-          ms.row[buf][x] = use ? address(b, x & (grain - 1)) : pad_row;
+          ms.row[buf][x] = use ? address(ms.box[buf][x >> shift], x & (grain - 1)) : pad_row;
         }
       } else {
 #pragma unroll 1
-        for (int w = 0; w < kRows / 32; ++w)
-          if ((__shfl_sync(0xffffffffu, bad_of, w) >> lane) & 1u) ms.row[buf][32 * w + lane] |= kNoValue;
+        for (unsigned words = __ballot_sync(0xffffffffu, bad_of != 0); words != 0; words &= words - 1) {
+          const int k = __ffs(words) - 1;
+          if ((__shfl_sync(0xffffffffu, bad_of, k) >> lane) & 1u) ms.row[buf][32 * k + lane] |= kNoValue;
+        }
       }
     }
     if (FP8) {
@@ -514,7 +527,6 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
         ms.ivs[buf][x] = exp2f(-lv);
       }
     }
-    if (p.grain > 0) ms.box[buf][lane] = mine;
     const bool head = g == 0 || j == 0, last = j == r.tiles - 1 || left == 1;
     if (head) first_j = j;
     if (lane == 0) {
@@ -581,15 +593,15 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
     const int rows = is_v ? 64 : 128;                                    // of a part
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
-      // Part c of K is dims 64 c .. of this CTA's rows; of V (nb, kq) dims 256 nb + 128 rank .. of rows 64 kq ..
-      if (is_v && ((flags >> (TF_PARTS + (c & 3))) & 1) == 0) continue;
+      // Part c of K is dims 64 c .. of this CTA's rows; of V (kq, nb) dims 256 nb + 128 rank .. of rows 64 kq ..
+      if (is_v && ((flags >> (TF_PARTS + (c >> 1))) & 1) == 0) continue;
       const bool mine = (int)turn == warp;
       const uint32_t st = st0 + at, par = ph;
       if ((int)++turn == n_warps) turn = 0;
       if (++at == stages) at = 0, ph ^= 1;
       if (!mine && !by_rows) continue;
-      const int row0 = is_v ? 64 * (c & 3) : 128 * (int)rank;
-      const int dim0 = is_v ? 256 * (c >> 2) + 128 * (int)rank : 64 * c;
+      const int row0 = is_v ? 64 * (c >> 1) : 128 * (int)rank;
+      const int dim0 = is_v ? 256 * (c & 1) + 128 * (int)rank : 64 * c;
       const uint32_t slot = sbase + kOffRing + (FP8 ? 4 * kPart + st * kCodePart : st * kPart);
       const uint32_t b_full = smem_u32(FP8 ? &ms.code_full[st] : &ms.kv_full[st]);
       if (!__all_sync(0xffffffffu, wait_phase(smem_u32(FP8 ? &ms.code_empty[st] : &ms.kv_empty[st]), par,
@@ -704,7 +716,7 @@ __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &m
       parts = ms.flags[buf] >> TF_PARTS;
       warp_arrive(smem_u32(&ms.list_empty[buf]));
     }
-    if (((parts >> (i & 3)) & 1) == 0) continue;
+    if (((parts >> ((i & 7) >> 1)) & 1) == 0) continue;
     const uint32_t src = sbase + kOffRing + 4 * kPart + (slot0 + codes.st) * kCodePart;
     const uint32_t dst = sbase + kOffRing + (stage0 + ring.st) * kPart;
     if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[slot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait) &&
@@ -764,7 +776,7 @@ __device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v) {
     }
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
-      if (is_v && ((flags >> (TF_PARTS + (c & 3))) & 1) == 0) continue;
+      if (is_v && ((flags >> (TF_PARTS + (c >> 1))) & 1) == 0) continue;
       const uint32_t bar = smem_u32(&ms.kv_full[stage0 + st]);
       if (!wait_phase(bar, ph, TSITE_KV_FULL, &ms.wait)) return;
       fence_proxy_async_smem();
@@ -806,7 +818,6 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
     const uint32_t sb = g & 1;
     if (IS_V) {
       if (first && !wait(ms.o_empty, (item & 1) ^ 1, TSITE_O_EMPTY)) return;
-      if (!wait(ms.p_full, g & 1, TSITE_P_FULL)) return;
     } else {
       if (first && (!wait(ms.q_full, item & 1, TSITE_Q_FULL) || !wait(ms.peer_q_full, item & 1, TSITE_Q_FULL))) return;
       if (!wait(ms.s_empty[sb], ((g >> 1) & 1) ^ 1, TSITE_S_EMPTY)) return;
@@ -816,41 +827,45 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
     tc_fence_after();
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
-      if (IS_V && ((parts >> (c & 3)) & 1) == 0) continue;
-      const uint32_t st = ring.st;
-      if (!__all_sync(0xffffffffu, ready) && !wait(ms.kv_full[kStage0 + st], ring.ph, TSITE_KV_FULL)) return;
-      ring.advance();
-      // The next stage is asked for before this one's products are issued.
-      ready = mbar_test(smem_u32(&ms.kv_full[kStage0 + ring.st]), ring.ph);
-      if (fence) fence_proxy_async_smem();
-      const uint64_t a0 = sdesc_add(a_desc, (IS_V ? c & 3 : c) * 8192);
+      // (Also of a box whose rows nobody sees: its barriers go through every tile.)
+      if (IS_V && (c & 1) == 0 && !wait(ms.p_full[c >> 1], g & 1, TSITE_P_FULL)) return;
+      const bool live = !IS_V || ((parts >> (c >> 1)) & 1) != 0;
+      uint32_t st = 0;
+      if (live) {
+        st = ring.st;
+        if (!__all_sync(0xffffffffu, ready) && !wait(ms.kv_full[kStage0 + st], ring.ph, TSITE_KV_FULL)) return;
+        ring.advance();
+        // The next stage is asked for before this one's products are issued.
+        ready = mbar_test(smem_u32(&ms.kv_full[kStage0 + ring.st]), ring.ph);
+        if (fence) fence_proxy_async_smem();
+      }
+      if (IS_V) tc_fence_after();
+      const uint64_t a0 = sdesc_add(a_desc, (IS_V ? c >> 1 : c) * 8192);
       const uint64_t b0 = sdesc_add(b_desc, st * kPart);
-      const uint32_t d = IS_V ? tmem + 128 * (c >> 2) : tmem + kTmemTS + 128 * sb;
-      const bool fresh = IS_V ? empty && (c & 3) == lowest : c == 0;
+      const uint32_t d = IS_V ? tmem + 128 * (c & 1) : tmem + kTmemTS + 128 * sb;
+      const bool fresh = IS_V ? empty && (c >> 1) == lowest : c == 0;
       if (elect_lane()) {
+        if (live) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (ks == 0)
-            umma_pair_f16(d, a0, b0, kIdesc, fresh ? 0u : 1u);
-          else
-            umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * (IS_V ? 4096 : 32)), kIdesc);
+          for (int ks = 0; ks < 4; ++ks) {
+            if (ks == 0)
+              umma_pair_f16(d, a0, b0, kIdesc, fresh ? 0u : 1u);
+            else
+              umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * (IS_V ? 4096 : 32)), kIdesc);
+          }
+          umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + st]));
         }
-        umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + st]));
-        if (!IS_V && c == 7) {
+        if (IS_V) {
+          if (c & 1) umma_pair_commit(smem_u32(&ms.p_empty[c >> 1]));
+          if (c >= 6 && last) umma_pair_commit(smem_u32(&ms.o_full[c & 1]));
+        } else if (c == 7) {
           umma_pair_commit(smem_u32(&ms.s_full[sb]));
           if (last) umma_pair_commit(smem_u32(&ms.q_empty));
         }
-        if (IS_V && last && c < 4 && (parts & 15) >> (c + 1) == 0) umma_pair_commit(smem_u32(&ms.o_full[0]));
       }
       __syncwarp();
     }
     if (parts != 0) empty = false;
-    if (IS_V && elect_lane()) {
-      if (last && (parts & 15) == 0) umma_pair_commit(smem_u32(&ms.o_full[0]));
-      if (last) umma_pair_commit(smem_u32(&ms.o_full[1]));
-      umma_pair_commit(smem_u32(&ms.p_empty));
-    }
-    __syncwarp();
   }
 }
 
@@ -891,147 +906,16 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
   uint32_t n_item = 0;
   float m_ref = kNoRefT, m_lim = kNoRefT, lsum = 0.f;
   uint8_t *prow = smem + kOffTP + box * kPBox + (h >> 3) * 1024 + (h & 7) * 128;
-#pragma unroll 1
-  for (int g = 0; g < nt; ++g) {
-    const int buf = g % kListsT;
-    const uint32_t sb = g & 1, s_at = tmem + kTmemTS + 128 * sb + 64 * hh + lanes;
-    wait(ms.list_full[buf], (g / kListsT) & 1, TSITE_LIST_FULL);
-    const int flags = ms.flags[buf], tok = ms.tok[buf];
-    const uint32_t see0 = ms.mask[buf][2 * box], see1 = ms.mask[buf][2 * box + 1];
-    if (flags & TF_FIRST) {
-      m_ref = m_lim = kNoRefT;
-      lsum = 0.f;
-      spoiled = false;
-    }
-    spoiled = spoiled || (flags & TF_SPOILED);
-    if (!FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
-    wait(ms.s_full[sb], (g >> 1) & 1, TSITE_S_FULL);
-    tc_fence_after();
-    // 32 scores a time, twice over: for their maximum, then for the weights.  (Held in
-    // registers for both, the code is twice as long.)
-    auto scores = [&](int c0, float (&s)[32]) {
-      tmem_ld32(s_at + c0, s);
-      tmem_wait_ld();
-      if (FP8) {
-        const float4 *ks = reinterpret_cast<const float4 *>(ms.ksc[buf] + 64 * box + c0);
-        const float4 *lv = reinterpret_cast<const float4 *>(ms.lvs[buf] + 64 * box + c0);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float4 k = ks[c], v = lv[c];
-          s[4 * c] = fmaf(s[4 * c], k.x, v.x);
-          s[4 * c + 1] = fmaf(s[4 * c + 1], k.y, v.y);
-          s[4 * c + 2] = fmaf(s[4 * c + 2], k.z, v.z);
-          s[4 * c + 3] = fmaf(s[4 * c + 3], k.w, v.w);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] *= p.scale_log2;
-      }
-      const uint32_t see = c0 == 0 ? see0 : see1;
-      if (see != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = (see >> c) & 1u ? s[c] : -INFINITY;
-      }
-    };
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int c0 = 0; c0 < 64; c0 += 32) {
-      float s[32];
-      scores(c0, s);
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-    }
-    bool moved = false;
-    float alpha = 1.f;
-    if (bar_red_or(group, 128, top > m_lim || bad)) {
-      // Some head's reference moves: the tile's maximum over a head's four threads.
-      ms.red[box][h] = top;
-      if (bar_red_or(group, 128, bad)) break;
-      const float tmax = fmaxf(fmaxf(ms.red[0][h], ms.red[1][h]), fmaxf(ms.red[2][h], ms.red[3][h]));
-      if (tmax > m_lim) {
-        // Rounded so that P stays within 2^15 where scores are 16 and more apart.
-        const float next = __fsub_ru(tmax, kLiftT);
-        alpha = exp2f(m_ref - next);  // 0 while there was none
-        m_ref = next;
-        m_lim = __fadd_rd(m_ref, kLiftT + kHoldT);
-      }
-      moved = true;
-      lsum *= alpha;
-    }
-    // This head's 64 weights, rounded once to fp16 for the product; the sums add them
-    // unrounded, eight at a time, so that lse keeps fp32 precision over long rows.
-    // They wait in registers for P's buffer: the next P . V waits for no more than
-    // their stores.
-    uint32_t weights[32];
-#pragma unroll
-    for (int c0 = 0; c0 < 64; c0 += 32) {
-      float s[32];
-      scores(c0, s);
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int x = 2 * i;
-        const float e0 = exp2f(s[x] - m_ref), e1 = exp2f(s[x + 1] - m_ref);
-        __half2 hp = __floats2half2_rn(e0, e1);
-        if (FP8) {
-          const float2 iv = *reinterpret_cast<const float2 *>(&ms.ivs[buf][64 * box + c0 + x]);
-          part[i & 3] = fmaf(e0, iv.x, fmaf(e1, iv.y, part[i & 3]));
-          // A V scale of 0: weight, but no value.
-          if (iv.x >= kMostScaleInv || iv.y >= kMostScaleInv)
-            hp = __floats2half2_rn(iv.x >= kMostScaleInv ? 0.f : e0, iv.y >= kMostScaleInv ? 0.f : e1);
-        } else {
-          part[i & 3] += e0 + e1;
-        }
-        weights[c0 / 2 + i] = *reinterpret_cast<const uint32_t *>(&hp);
-      }
-      lsum += (part[0] + part[1]) + (part[2] + part[3]);
-    }
-    tc_fence_before();
-    tell(ms.s_empty[sb]);
-    wait(ms.p_empty, (g & 1) ^ 1, TSITE_P_EMPTY);
-    // 16-byte chunk c of the head's 128 bytes at c ^ (h & 7).
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<uint4 *>(prow + ((c ^ (h & 7)) << 4)) =
-          make_uint4(weights[4 * c], weights[4 * c + 1], weights[4 * c + 2], weights[4 * c + 3]);
-    if (FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
-    if (moved && !(flags & TF_FIRST)) {
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        tmem_ld32(tmem + 128 * hh + 32 * c + lanes, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= alpha;
-        tmem_st32(tmem + 128 * hh + 32 * c + lanes, o);
-      }
-      tmem_wait_st();
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    tell(ms.p_full);
-    if (!(flags & TF_LAST)) continue;
-
-    // End of an item: the sum over a head's four threads, then this thread's 128
-    // dims of o (dims 256 hh + 128 half ..) once the last PV has finished them.
-    const bool whole = flags & TF_WHOLE;
-    ms.red[box][h] = lsum;
-    if (bar_red_or(group, 128, bad)) break;
-    const float sum = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
-    // No weight at all: o = 0.  (A sum that is NaN is not that: it stays.)
-    const bool none = sum == 0.f;
-    const float inv = spoiled ? __int_as_float(0x7FC00000) : none ? 0.f : 1.f / sum;
-    const long long slot = 2ll * (2 * cluster + (flags & TF_HEAD ? 1 : 0)) + rank;
-    if (box == 0 && tok >= 0) {
-      if (!whole)
-        p.ws_ml[slot * kH + h] = make_float2(none ? -INFINITY : m_ref, sum);
-      else if (p.lse != nullptr)
-        p.lse[(long long)tok * kH + h] = none ? -INFINITY : (m_ref + log2f(sum)) * kLn2;
-    }
+  // The output of an item that has ended: this thread's 128 dims of o (dims 256 hh +
+  // 128 half ..) once the last products have gone into them.
+  bool pending = false, none = false, whole = false;
+  float inv = 0.f;
+  int out_tok = -1;
+  long long slot = 0;
+  auto drain = [&]() {
+    pending = false;
     wait(ms.o_full[hh], n_item & 1, TSITE_O_FULL);
+    ++n_item;
     tc_fence_after();
     const int dim0 = 256 * hh + 128 * half;
 #pragma unroll 1
@@ -1039,9 +923,9 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       float o[32];
       tmem_ld32(tmem + 128 * hh + 32 * c + lanes, o);
       tmem_wait_ld();
-      if (tok < 0) continue;
+      if (out_tok < 0 || bad) continue;
       if (whole) {
-        __half *at = p.o + tok * p.o_stride + (long long)h * kD + dim0 + 32 * c;
+        __half *at = p.o + out_tok * p.o_stride + (long long)h * kD + dim0 + 32 * c;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t x[8];
@@ -1070,9 +954,143 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     }
     tc_fence_before();
     tell(ms.o_empty);
-    ++n_item;
-    if (bar_red_or(group, 128, bad)) break;  // (and the sums have been read)
+  };
+#pragma unroll 1
+  for (int g = 0; g < nt; ++g) {
+    const int buf = g % kListsT;
+    const uint32_t sb = g & 1, s_at = tmem + kTmemTS + 128 * sb + 64 * hh + lanes;
+    wait(ms.list_full[buf], (g / kListsT) & 1, TSITE_LIST_FULL);
+    const int flags = ms.flags[buf], tok = ms.tok[buf];
+    const uint32_t see0 = ms.mask[buf][2 * box], see1 = ms.mask[buf][2 * box + 1];
+    if (flags & TF_FIRST) {
+      m_ref = m_lim = kNoRefT;
+      lsum = 0.f;
+      spoiled = false;
+    }
+    spoiled = spoiled || (flags & TF_SPOILED);
+    if (!FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
+    wait(ms.s_full[sb], (g >> 1) & 1, TSITE_S_FULL);
+    tc_fence_after();
+    float s[64];
+    tmem_ld64(s_at, s);
+    tmem_wait_ld();
+    tc_fence_before();
+    tell(ms.s_empty[sb]);
+    if (FP8) {
+      const float4 *ks = reinterpret_cast<const float4 *>(ms.ksc[buf] + 64 * box);
+      const float4 *lv = reinterpret_cast<const float4 *>(ms.lvs[buf] + 64 * box);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float4 k = ks[c], v = lv[c];
+        s[4 * c] = fmaf(s[4 * c], k.x, v.x);
+        s[4 * c + 1] = fmaf(s[4 * c + 1], k.y, v.y);
+        s[4 * c + 2] = fmaf(s[4 * c + 2], k.z, v.z);
+        s[4 * c + 3] = fmaf(s[4 * c + 3], k.w, v.w);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) s[c] *= p.scale_log2;
+    }
+    if ((see0 & see1) != 0xFFFFFFFFu) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        s[c] = (see0 >> c) & 1u ? s[c] : -INFINITY;
+        s[c + 32] = (see1 >> c) & 1u ? s[c + 32] : -INFINITY;
+      }
+    }
+    float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    bool moved = false;
+    float alpha = 1.f;
+    if (bar_red_or(group, 128, top > m_lim || bad)) {
+      // Some head's reference moves: the tile's maximum over a head's four threads.
+      ms.red[box][h] = top;
+      if (bar_red_or(group, 128, bad)) break;
+      const float tmax = fmaxf(fmaxf(ms.red[0][h], ms.red[1][h]), fmaxf(ms.red[2][h], ms.red[3][h]));
+      if (tmax > m_lim) {
+        // Rounded so that P stays within 2^15 where scores are 16 and more apart.
+        const float next = __fsub_ru(tmax, kLiftT);
+        alpha = exp2f(m_ref - next);  // 0 while there was none
+        m_ref = next;
+        m_lim = __fadd_rd(m_ref, kLiftT + kHoldT);
+      }
+      moved = true;
+      lsum *= alpha;
+    }
+    // This head's 64 weights, rounded once to fp16 for the product; the sums add them
+    // unrounded, sixteen at a time, so that lse keeps fp32 precision over long rows.
+    uint32_t weights[32];
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float e0 = exp2f(s[2 * i] - m_ref), e1 = exp2f(s[2 * i + 1] - m_ref);
+      __half2 hp = __floats2half2_rn(e0, e1);
+      if (FP8) {
+        const float2 iv = *reinterpret_cast<const float2 *>(&ms.ivs[buf][64 * box + 2 * i]);
+        part[i & 3] = fmaf(e0, iv.x, fmaf(e1, iv.y, part[i & 3]));
+        // A V scale of 0: weight, but no value.
+        if (iv.x >= kMostScaleInv || iv.y >= kMostScaleInv)
+          hp = __floats2half2_rn(iv.x >= kMostScaleInv ? 0.f : e0, iv.y >= kMostScaleInv ? 0.f : e1);
+      } else {
+        part[i & 3] += e0 + e1;
+      }
+      weights[i] = *reinterpret_cast<const uint32_t *>(&hp);
+    }
+    lsum += (part[0] + part[1]) + (part[2] + part[3]);
+    if (FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
+    if (pending) drain();
+    if (moved && !(flags & TF_FIRST)) {
+      // O under the new reference, once the products so far have gone into it (those
+      // of the last box complete last), and before any of this tile does.
+      wait(ms.p_empty[3], (g & 1) ^ 1, TSITE_P_EMPTY);
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld32(tmem + 128 * hh + 32 * c + lanes, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+        tmem_st32(tmem + 128 * hh + 32 * c + lanes, o);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      bar_sync_id(group, 128);
+    }
+    wait(ms.p_empty[box], (g & 1) ^ 1, TSITE_P_EMPTY);
+    // 16-byte chunk c of the head's 128 bytes at c ^ (h & 7).
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4 *>(prow + ((c ^ (h & 7)) << 4)) =
+          make_uint4(weights[4 * c], weights[4 * c + 1], weights[4 * c + 2], weights[4 * c + 3]);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    tell(ms.p_full[box]);
+    if (!(flags & TF_LAST)) continue;
+
+    // End of an item: the sum over a head's four threads.  Its output is taken from
+    // TMEM behind the next tile's weights, while the last products run.
+    ms.red[box][h] = lsum;
+    if (bar_red_or(group, 128, bad)) break;
+    const float sum = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
+    // No weight at all: o = 0.  (A sum that is NaN is not that: it stays.)
+    none = sum == 0.f;
+    inv = spoiled ? __int_as_float(0x7FC00000) : none ? 0.f : 1.f / sum;
+    whole = flags & TF_WHOLE;
+    out_tok = tok;
+    slot = 2ll * (2 * cluster + (flags & TF_HEAD ? 1 : 0)) + rank;
+    if (box == 0 && tok >= 0) {
+      if (!whole)
+        p.ws_ml[slot * kH + h] = make_float2(none ? -INFINITY : m_ref, sum);
+      else if (p.lse != nullptr)
+        p.lse[(long long)tok * kH + h] = none ? -INFINITY : (m_ref + log2f(sum)) * kLn2;
+    }
+    pending = true;
+    bar_sync_id(group, 128);  // the sums have been read
   }
+  if (pending && !bad) drain();
 }
 
 // ------------------------------------------------------------------ kernel
@@ -1112,8 +1130,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mbar_init(smem_u32(&ms.s_empty[s]), 2 * kComputeWarps);
       mbar_init(smem_u32(&ms.o_full[s]), 1);
     }
-    mbar_init(smem_u32(&ms.p_full), 2 * kComputeWarps);
-    mbar_init(smem_u32(&ms.p_empty), 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(smem_u32(&ms.p_full[s]), 2 * kComputeWarps / 4);
+      mbar_init(smem_u32(&ms.p_empty[s]), 1);
+    }
     mbar_init(smem_u32(&ms.o_empty), 2 * kComputeWarps);
     mbar_init(smem_u32(&ms.mma_done), 2);
     ms.wait.timeout_ns = p.timeout_ns;
