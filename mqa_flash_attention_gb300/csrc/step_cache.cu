@@ -23,6 +23,8 @@ namespace {
 
 constexpr int kListThreads = 1024;
 constexpr int kListWarps = kListThreads / 32;
+constexpr int kByWarps = 128;  // up to here, more than kFewPages / 8 pages are a warp's work
+constexpr int kFewPages = 64;  // given back by a sequence: beyond, always a warp's
 constexpr int kFillThreads = 128;
 constexpr int kFillSlots = 8;  // padding slots of a thread
 
@@ -44,87 +46,127 @@ __device__ __forceinline__ Pages pages_of(const PageTablesParams &p, int b) {
   return x;
 }
 
-// The pages that a sequence gives back, 32 entries a step: calls f(valid, page,
-// how many valid ones came before in this sequence) with the whole warp.
+// The pages that sequence b gives back, by one lane, eight loads in flight, or by a
+// whole warp: f(page, how many came before in this sequence); returns how many.
+// A round trip to L2 is what a step costs.  All of n_seq sequences by lanes take
+// n / 8 of them, by 32 warps n_seq / 32 * n / 32: lanes are ahead from 128
+// sequences on (a call that takes and one that gives back, 1,024 sequences of up to
+// 50 pages: 31 us by lanes, 34 by warps; 64 of up to 64 pages: 17.5 and 15.9).
 template <class F>
-__device__ __forceinline__ void given_back(const PageTablesParams &p, int b, int gone, int need, int held, int lane,
-                                           F f) {
+__device__ __forceinline__ int given_back_lane(const PageTablesParams &p, int b, int gone, int need, int held, F f) {
   const int32_t *row = p.table + b * p.table_stride;
-  const int tail = max(0, held - need), n = gone + tail;
+  const int n = gone + max(0, held - need);
+  int before = 0;
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    int page[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k;
+      page[k] = i < n ? row[i < gone ? i : need + i - gone] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if ((unsigned)page[k] < (unsigned)p.n_pages) f(page[k], before++);
+    }
+  }
+  return before;
+}
+
+template <class F>
+__device__ __forceinline__ int given_back_warp(const PageTablesParams &p, int b, int gone, int need, int held,
+                                               int lane, F f) {
+  const int32_t *row = p.table + b * p.table_stride;
+  const int n = gone + max(0, held - need);
   int before = 0;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
     const int page = i < n ? row[i < gone ? i : need + i - gone] : -1;
     const bool valid = (unsigned)page < (unsigned)p.n_pages;
     const unsigned who = __ballot_sync(0xffffffffu, valid);
-    f(valid, page, before + __popc(who & ((1u << lane) - 1)));
+    if (valid) f(page, before + __popc(who & ((1u << lane) - 1)));
     before += __popc(who);
   }
+  return before;
+}
+
+// Sum over a warp's lanes up to this one, in 64 bits (new rows of many sequences may
+// pass 32).
+__device__ __forceinline__ long long scan_lanes(long long v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
 }
 
 __global__ void __launch_bounds__(kListThreads, 1) page_lists_kernel(const PageTablesParams p) {
-  __shared__ long long warp_sum[3][kListWarps];
+  __shared__ long long warp_sum[3][kListWarps], at_of[kListThreads];
+  __shared__ int3 warp_job[kListThreads];  // gone, need, held; zeros: a lane does it
+  __shared__ int back_of[kListThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_launch_dependents();
   grid_dependency_wait();
   const int start = min(max(p.n_free[0], 0), p.n_pages);
   long long top = start, need_all = 0, rows_all = 0;  // before this round
   for (int b0 = 0; b0 < p.n_seq; b0 += kListThreads) {
-    const int b = b0 + tid;
+    const int b = b0 + tid, n_here = min(kListThreads, p.n_seq - b0);
     const bool live = b < p.n_seq;
     Pages x = {0, 0, 0, 0, 0};
     if (live) x = pages_of(p, b);
-    // Pages that are given back: the warp counts each of its 32 sequences in turn.
+    // A lane counts what its sequence gives back where that is little; the warps
+    // take the other sequences in turn.
     const int n_back = x.gone + max(0, x.held - x.need);
-    unsigned who = __ballot_sync(0xffffffffu, n_back > 0);
-    int back = 0;
-    while (who != 0) {
-      const int l = __ffs(who) - 1;
-      who &= who - 1;
-      int n = 0;
-      given_back(p, b0 + 32 * warp + l, __shfl_sync(0xffffffffu, x.gone, l), __shfl_sync(0xffffffffu, x.need, l),
-                 __shfl_sync(0xffffffffu, x.held, l), lane, [&](bool valid, int, int) { n += valid; });
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == l) back = n;
-    }
-    // Sums over the sequences before this one: given back, taken, new rows.
-    // (A warp's new rows may pass 32 bits: 64-bit sums there.)
-    long long at[3] = {back, live ? x.grow() : 0, live ? x.rows() : 0}, inc[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      long long v = at[k];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += t;
+    const bool few = n_back <= (n_here > kByWarps ? kFewPages : kFewPages / 8);
+    warp_job[tid] = few ? make_int3(0, 0, 0) : make_int3(x.gone, x.need, x.held);
+    back_of[tid] = few ? given_back_lane(p, b, x.gone, x.need, x.held, [](int, int) {}) : 0;
+    const bool any_many = __syncthreads_or(!few);
+    if (any_many) {
+      for (int s = warp; s < n_here; s += kListWarps) {
+        const int3 j = warp_job[s];
+        const int n = given_back_warp(p, b0 + s, j.x, j.y, j.z, lane, [](int, int) {});
+        if (lane == 0 && n > 0) back_of[s] = n;
       }
-      inc[k] = v;
-      if (lane == 31) warp_sum[k][warp] = v;
+      __syncthreads();
     }
-    __syncthreads();
+    const int back = back_of[tid];
+    // Sums over the sequences before this one: given back, taken, new rows.
+    const long long own[3] = {back, live ? x.grow() : 0, live ? x.rows() : 0};
     long long before[3], all[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      before[k] = inc[k] - at[k];
-      all[k] = 0;
-      for (int w = 0; w < kListWarps; ++w) {
-        if (w < warp) before[k] += warp_sum[k][w];
-        all[k] += warp_sum[k][w];
-      }
+      before[k] = scan_lanes(own[k], lane);
+      if (lane == 31) warp_sum[k][warp] = before[k];
+      before[k] -= own[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const long long v = scan_lanes(warp_sum[k][lane], lane);
+      all[k] = __shfl_sync(0xffffffffu, v, 31);
+      const long long w = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
+      if (warp > 0) before[k] += w;
     }
     if (live) {
       p.plan[b] = PagePlan{need_all + before[1], rows_all + before[2]};
       p.first[b] = (int)min(rows_all + before[2], (long long)p.n_slots);
     }
-    who = __ballot_sync(0xffffffffu, back > 0);
-    while (who != 0) {
-      const int l = __ffs(who) - 1;
-      who &= who - 1;
-      const long long at0 = top + __shfl_sync(0xffffffffu, before[0], l);
-      given_back(p, b0 + 32 * warp + l, __shfl_sync(0xffffffffu, x.gone, l), __shfl_sync(0xffffffffu, x.need, l),
-                 __shfl_sync(0xffffffffu, x.held, l), lane, [&](bool valid, int page, int i) {
-                   if (valid && at0 + i < p.n_pages) p.free_pages[at0 + i] = page;
-                 });
+    const long long at = top + before[0];
+    if (few) {
+      given_back_lane(p, b, x.gone, x.need, x.held, [&](int page, int i) {
+        if (at + i < p.n_pages) p.free_pages[at + i] = page;
+      });
+    }
+    if (any_many) {
+      at_of[tid] = at;
+      __syncthreads();
+      for (int s = warp; s < n_here; s += kListWarps) {
+        const int3 j = warp_job[s];
+        const long long at_s = at_of[s];
+        given_back_warp(p, b0 + s, j.x, j.y, j.z, lane, [&](int page, int i) {
+          if (at_s + i < p.n_pages) p.free_pages[at_s + i] = page;
+        });
+      }
     }
     top += all[0];
     need_all += all[1];

@@ -55,7 +55,8 @@ def run_pages(torch, ds4a, c, page, n_slots, stream=None):
 
 @pytest.mark.parametrize("n_seq,page,rows,grow,spare", [
     (1, 64, 0, 1, 4), (1, 1, 5, 9, 20), (3, 64, 300, 40, 0), (64, 16, 200, 20, 90), (31, 7, 50, 60, 3),
-    (1024, 16, 90, 40, 2000), (1025, 8, 30, 20, 100), (2500, 24, 60, 100, 20000), (2, 128, 5000, 9000, 200)])
+    (1024, 16, 90, 40, 2000), (1025, 8, 30, 20, 100), (2500, 24, 60, 100, 20000), (2, 128, 5000, 9000, 200),
+    (1100, 4, 500, 20, 100), (200, 4, 500, 20, 100)])
 @pytest.mark.parametrize("dropped", [False, True])
 def test_page_tables_match_the_oracle(torch, ds4a, n_seq, page, rows, grow, spare, dropped):
     rng = np.random.default_rng(n_seq * 1000 + page + dropped)
