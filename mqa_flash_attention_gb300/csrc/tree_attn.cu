@@ -700,40 +700,47 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
 }
 
 // With E4M3 rows: a slot's codes widened exactly into the next stage, in the layout
-// that the fp16 kernel's copies have; 64 threads for K, 32 for V (twice 128 codes each).
-__device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &ms, bool is_v, int ct) {
-  const uint32_t slot0 = is_v ? kCodeSlots : 0, stage0 = is_v ? kKStages<true> : 0;
-  static_assert(kKStages<true> == kVStages<true>, "one ring length for both");
-  const int threads = 32 * (is_v ? kWidenVWarps : kWidenKWarps);
+// that the fp16 kernel's copies have; 64 threads for K, 32 for V.  A thread takes 16
+// codes, 8 times a part of K and 16 times one of V, at addresses that differ by
+// constants; eight neighbouring threads meet every bank once, in codes and in values.
+template <bool IS_V>
+__device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &ms, int ct) {
+  constexpr uint32_t kSlot0 = IS_V ? kCodeSlots : 0, kStage0 = IS_V ? kKStages<true> : 0;
+  static_assert(kWidenKWarps == 2 && kWidenVWarps == 1, "a turn is 16 rows of K, 4 of V");
+  // K: 4 threads to a row, rows 16 apart.  V: 8 threads to a row, of which the first four
+  // take the left half in even rows and the right half in odd ones.
+  const int row = IS_V ? 2 * (ct >> 4) + ((ct >> 2) & 1) : ct >> 2;
+  const int c = IS_V ? (ct & 3) | ((((ct >> 2) ^ (ct >> 3)) & 1) << 2) : ct & 3;  // chunks 2 c, 2 c + 1 of 8 values
+  const uint32_t from = row * (IS_V ? 128 : 64) + 16 * c;
+  const uint32_t to = IS_V ? row * 128 + (c >> 2) * 1024 : (row >> 3) * 1024 + (row & 7) * 128;
+  const uint32_t col0 = ((2 * (c & 3)) ^ (row & 7)) << 4, col1 = ((2 * (c & 3) + 1) ^ (row & 7)) << 4;
   Ring<kCodeSlots> codes;
   Ring<kKStages<true>> ring;
   int parts = 15;
 #pragma unroll 1
   for (int i = 0; i < 8 * nt; ++i) {
-    if (is_v && (i & 7) == 0) {
+    if (IS_V && (i & 7) == 0) {
       const int g = i >> 3, buf = g % kListsT;
       if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait))) return;
       parts = ms.flags[buf] >> TF_PARTS;
       warp_arrive(smem_u32(&ms.list_empty[buf]));
     }
     if (((parts >> ((i & 7) >> 1)) & 1) == 0) continue;
-    const uint32_t src = sbase + kOffRing + 4 * kPart + (slot0 + codes.st) * kCodePart;
-    const uint32_t dst = sbase + kOffRing + (stage0 + ring.st) * kPart;
-    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[slot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait) &&
-                                     wait_phase(smem_u32(&ms.kv_empty[stage0 + ring.st]), ring.ph ^ 1, TSITE_KV_EMPTY, &ms.wait)))
+    const uint32_t src = sbase + kOffRing + 4 * kPart + (kSlot0 + codes.st) * kCodePart + from;
+    const uint32_t dst = sbase + kOffRing + (kStage0 + ring.st) * kPart + to;
+    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[kSlot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait) &&
+                                     wait_phase(smem_u32(&ms.kv_empty[kStage0 + ring.st]), ring.ph ^ 1, TSITE_KV_EMPTY, &ms.wait)))
       return;
 #pragma unroll 1
-    for (int n0 = ct; n0 < 512; n0 += 8 * threads) {
+    for (int k0 = 0; k0 < (IS_V ? 16 : 8); k0 += 8) {
       uint4 raw[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(raw[k].x), "=r"(raw[k].y), "=r"(raw[k].z), "=r"(raw[k].w)
-                     : "r"(src + 16 * (n0 + threads * k)));
+                     : "r"(src + k0 * 512 + k * (IS_V ? 512 : 1024)));
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int n = n0 + threads * k;
-        const int row = is_v ? n >> 3 : n >> 2, c = is_v ? n & 7 : n & 3;  // 16 codes: chunks 2c, 2c + 1 of 8 values
         const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
         uint32_t h[8];
 #pragma unroll
@@ -741,14 +748,15 @@ __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &m
           h[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] & 0xFFFFu));
           h[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] >> 16));
         }
-        const uint32_t drow = dst + (row & 7) * 128 + (is_v ? (row >> 3) * 2048 + (c >> 2) * 1024 : (row >> 3) * 1024);
-        const int col = 2 * (c & 3);
-        sts_v4(drow + ((col ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-        sts_v4(drow + (((col + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+        // V: 4 rows further every turn, 8 every other one.
+        const uint32_t drow = dst + (IS_V ? k0 * 1024 + (k >> 1) * 2048 + (k & 1) * 512 : k * 2048);
+        const uint32_t flip = IS_V && (k & 1) ? 64 : 0;  // chunk ^ 4
+        sts_v4(drow + (col0 ^ flip), h[0], h[1], h[2], h[3]);
+        sts_v4(drow + (col1 ^ flip), h[4], h[5], h[6], h[7]);
       }
     }
-    warp_arrive(smem_u32(&ms.code_empty[slot0 + codes.st]));
-    if ((ct & 31) == 0) mbar_arrive(smem_u32(&ms.kv_full[stage0 + ring.st]));
+    warp_arrive(smem_u32(&ms.code_empty[kSlot0 + codes.st]));
+    if ((ct & 31) == 0) mbar_arrive(smem_u32(&ms.kv_full[kStage0 + ring.st]));
     codes.advance();
     ring.advance();
   }
@@ -1178,8 +1186,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   } else if (warp == kListWarp) {
     tree_list_role<FP8>(p, nt, cluster, rank, ms, threadIdx.x & 31);
   } else if (FP8 && warp != kKLoadWarp0 && warp != kVLoadWarp0) {
-    const bool is_v = warp >= kWidenV0;
-    tree_widen_role(nt, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kWidenV0 : kWidenK0));
+    if (warp >= kWidenV0)
+      tree_widen_role<true>(nt, sbase, ms, threadIdx.x - 32 * kWidenV0);
+    else
+      tree_widen_role<false>(nt, sbase, ms, threadIdx.x - 32 * kWidenK0);
   } else {
     const bool is_v = warp >= kVLoadWarp0;
     tree_load_role<FP8>(p, nt, rank, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kVLoadWarp0 : kKLoadWarp0));
