@@ -68,11 +68,13 @@ static_assert(7 * kPart <= kRingBytes && 4 * kPart + 2 * kCodeSlots * kCodePart 
 // tiles that meets the others at mbarriers only, and its code is kept small: what
 // all roles run through in a tile has to stay in the instruction cache.
 constexpr int kKLoadWarp0 = 8, kVLoadWarp0 = 11, kListWarp = 13, kPvWarp = 14, kQkWarp = 15;
-constexpr int kWidenK0 = 9, kWidenV0 = 12, kWidenKWarps = 2, kWidenVWarps = 1;
+constexpr int kWidenK0 = 9, kWidenV0 = 16, kWidenKWarps = 2, kWidenVWarps = 4;
 template <bool FP8>
 constexpr int kKLoadWarps = FP8 ? 1 : 3;
 template <bool FP8>
 constexpr int kVLoadWarps = FP8 ? 1 : 2;
+template <bool FP8>
+constexpr int kTreeThreads = 32 * (FP8 ? kWidenV0 + kWidenVWarps : kQkWarp + 1);
 
 constexpr float kLeastLog2ScaleT = -40.f;   // V scales below 2^-40 count as 0: such rows round to 0 in fp16
 constexpr float kMostScaleInv = 1.0995e12f;      // just below 2^40
@@ -700,19 +702,20 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
 }
 
 // With E4M3 rows: a slot's codes widened exactly into the next stage, in the layout
-// that the fp16 kernel's copies have; 64 threads for K, 32 for V.  A thread takes 16
-// codes, 8 times a part of K and 16 times one of V, at addresses that differ by
-// constants; eight neighbouring threads meet every bank once, in codes and in values.
+// that the fp16 kernel's copies have.  A thread takes 16 codes at a time, at addresses
+// that differ by constants; eight neighbouring threads meet every bank once, in codes
+// and in values.
 template <bool IS_V>
 __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &ms, int ct) {
   constexpr uint32_t kSlot0 = IS_V ? kCodeSlots : 0, kStage0 = IS_V ? kKStages<true> : 0;
-  static_assert(kWidenKWarps == 2 && kWidenVWarps == 1, "a turn is 16 rows of K, 4 of V");
-  // K: 4 threads to a row, rows 16 apart.  V: 8 threads to a row, of which the first four
-  // take the left half in even rows and the right half in odd ones.
+  constexpr int kWarps = IS_V ? kWidenVWarps : kWidenKWarps, kTurns = 16 / kWarps;
+  static_assert(kWidenVWarps % 2 == 0, "a turn is whole groups of eight rows");
+  // K: 4 threads to a row.  V: 8 threads to a row, of which the first four take the left
+  // half in even rows and the right half in odd ones.
   const int row = IS_V ? 2 * (ct >> 4) + ((ct >> 2) & 1) : ct >> 2;
   const int c = IS_V ? (ct & 3) | ((((ct >> 2) ^ (ct >> 3)) & 1) << 2) : ct & 3;  // chunks 2 c, 2 c + 1 of 8 values
   const uint32_t from = row * (IS_V ? 128 : 64) + 16 * c;
-  const uint32_t to = IS_V ? row * 128 + (c >> 2) * 1024 : (row >> 3) * 1024 + (row & 7) * 128;
+  const uint32_t to = (row >> 3) * (IS_V ? 2048 : 1024) + (row & 7) * 128 + (IS_V ? (c >> 2) * 1024 : 0);
   const uint32_t col0 = ((2 * (c & 3)) ^ (row & 7)) << 4, col1 = ((2 * (c & 3) + 1) ^ (row & 7)) << 4;
   Ring<kCodeSlots> codes;
   Ring<kKStages<true>> ring;
@@ -731,29 +734,23 @@ __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &m
     if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.code_full[kSlot0 + codes.st]), codes.ph, TSITE_CODE_FULL, &ms.wait) &&
                                      wait_phase(smem_u32(&ms.kv_empty[kStage0 + ring.st]), ring.ph ^ 1, TSITE_KV_EMPTY, &ms.wait)))
       return;
-#pragma unroll 1
-    for (int k0 = 0; k0 < (IS_V ? 16 : 8); k0 += 8) {
-      uint4 raw[8];
+    uint4 raw[kTurns];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(raw[k].x), "=r"(raw[k].y), "=r"(raw[k].z), "=r"(raw[k].w)
-                     : "r"(src + k0 * 512 + k * (IS_V ? 512 : 1024)));
+    for (int k = 0; k < kTurns; ++k)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(raw[k].x), "=r"(raw[k].y), "=r"(raw[k].z), "=r"(raw[k].w)
+                   : "r"(src + k * 512 * kWarps));
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-        uint32_t h[8];
+    for (int k = 0; k < kTurns; ++k) {
+      const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      uint32_t h[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] & 0xFFFFu));
-          h[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] >> 16));
-        }
-        // V: 4 rows further every turn, 8 every other one.
-        const uint32_t drow = dst + (IS_V ? k0 * 1024 + (k >> 1) * 2048 + (k & 1) * 512 : k * 2048);
-        const uint32_t flip = IS_V && (k & 1) ? 64 : 0;  // chunk ^ 4
-        sts_v4(drow + (col0 ^ flip), h[0], h[1], h[2], h[3]);
-        sts_v4(drow + (col1 ^ flip), h[4], h[5], h[6], h[7]);
+      for (int e = 0; e < 4; ++e) {
+        h[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] & 0xFFFFu));
+        h[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] >> 16));
       }
+      sts_v4(dst + k * 1024 * kWarps + col0, h[0], h[1], h[2], h[3]);
+      sts_v4(dst + k * 1024 * kWarps + col1, h[4], h[5], h[6], h[7]);
     }
     warp_arrive(smem_u32(&ms.code_empty[kSlot0 + codes.st]));
     if ((ct & 31) == 0) mbar_arrive(smem_u32(&ms.kv_full[kStage0 + ring.st]));
@@ -1104,7 +1101,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
 // ------------------------------------------------------------------ kernel
 
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
+__global__ void __launch_bounds__(kTreeThreads<FP8>, 1) tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -1167,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const int nt = (int)max(0ll, min((long long)head.y, head.x - before));
   if (warp < kComputeWarps) {
     tree_softmax_role<FP8>(p, nt, cluster, rank, smem, tmem, ms, threadIdx.x);
-  } else if (warp >= kPvWarp) {
+  } else if (warp == kPvWarp || warp == kQkWarp) {
     const bool is_v = warp == kPvWarp, lane0 = (threadIdx.x & 31) == 0;
     if (rank == 0) {
       if (is_v)
@@ -1185,12 +1182,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     __syncwarp();
   } else if (warp == kListWarp) {
     tree_list_role<FP8>(p, nt, cluster, rank, ms, threadIdx.x & 31);
-  } else if (FP8 && warp != kKLoadWarp0 && warp != kVLoadWarp0) {
-    if (warp >= kWidenV0)
-      tree_widen_role<true>(nt, sbase, ms, threadIdx.x - 32 * kWidenV0);
-    else
-      tree_widen_role<false>(nt, sbase, ms, threadIdx.x - 32 * kWidenK0);
-  } else {
+  } else if (FP8 && warp >= kWidenV0) {
+    tree_widen_role<true>(nt, sbase, ms, threadIdx.x - 32 * kWidenV0);
+  } else if (FP8 && warp >= kWidenK0 && warp < kWidenK0 + kWidenKWarps) {
+    tree_widen_role<false>(nt, sbase, ms, threadIdx.x - 32 * kWidenK0);
+  } else if (warp < kVLoadWarp0 + kVLoadWarps<FP8>) {
     const bool is_v = warp >= kVLoadWarp0;
     tree_load_role<FP8>(p, nt, rank, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kVLoadWarp0 : kKLoadWarp0));
   }
@@ -1301,7 +1297,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams &p, bool e4m3, cudaStream_t s)
   cudaError_t e = launch((const void *)tree_plan_kernel, p, 1, kPlanThreads, 0, 1, s);
   if (e == cudaSuccess)
     e = launch(e4m3 ? (const void *)tree_attn_kernel<true> : (const void *)tree_attn_kernel<false>, p, 2 * p.clusters,
-               kThreads, kTreeSmem, 2, s);
+               e4m3 ? kTreeThreads<true> : kTreeThreads<false>, kTreeSmem, 2, s);
   if (e == cudaSuccess && p.clusters > 1)
     e = launch((const void *)tree_merge_kernel, p, (p.clusters - 1) * 2 * (kH / kMergeHeads), 32 * kMergeHeads, 0, 1, s);
   return e;
