@@ -54,27 +54,29 @@ constexpr uint32_t kTmemTS = 256;           // S buffers at columns 256 and 384
 constexpr int kListsT = 3;
 
 // K and V come through rings of their own, because their products are issued by
-// warps of their own.  fp16 rows: four stages of K and three of V.  E4M3 rows:
+// warps of their own.  fp16 rows: three stages of K and four of V.  E4M3 rows:
 // codes land in three slots for each and are widened into two stages for each.
 template <bool FP8>
-constexpr int kKStages = FP8 ? 2 : 4;
+constexpr int kKStages = FP8 ? 2 : 3;
 template <bool FP8>
-constexpr int kVStages = FP8 ? 2 : 3;
+constexpr int kVStages = FP8 ? 2 : 4;
 constexpr int kCodeSlots = 3;
 static_assert(7 * kPart <= kRingBytes && 4 * kPart + 2 * kCodeSlots * kCodePart <= kRingBytes, "shared memory of the rings");
-// Warps 0-7 softmax and epilogue; 8-10 load K and 11-12 V (E4M3: 8 loads K and 11 V,
-// 9-10 widen K and 12 V); 13 finds the rows of the tiles; 14 issues P . V, 15 Q . K (in
-// the CTA of rank 1 they report what has landed).  Every role is a loop over the
-// tiles that meets the others at mbarriers only, and its code is kept small: what
-// all roles run through in a tile has to stay in the instruction cache.
-constexpr int kKLoadWarp0 = 8, kVLoadWarp0 = 11, kListWarp = 13, kPvWarp = 14, kQkWarp = 15;
+// Warps 0-7 softmax and epilogue; 13 finds the rows of the tiles; 14 issues P . V, 15
+// Q . K (in the CTA of rank 1 they report what has landed).  8-9 load K and 16-19 V
+// (E4M3: 8 loads K and 11 V, 9-10 widen K and 16-19 V); 10-12 (12) are idle, because
+// registers go to four warps at a time.  Every role is a loop over the tiles that
+// meets the others at mbarriers only, and its code is kept small: what all roles run
+// through in a tile has to stay in the instruction cache.
+constexpr int kTreeThreads = 640;
+constexpr int kKLoadWarp0 = 8, kListWarp = 13, kPvWarp = 14, kQkWarp = 15;
 constexpr int kWidenK0 = 9, kWidenV0 = 16, kWidenKWarps = 2, kWidenVWarps = 4;
 template <bool FP8>
-constexpr int kKLoadWarps = FP8 ? 1 : 3;
+constexpr int kVLoadWarp0 = FP8 ? 11 : 16;
 template <bool FP8>
-constexpr int kVLoadWarps = FP8 ? 1 : 2;
+constexpr int kKLoadWarps = FP8 ? 1 : 2;
 template <bool FP8>
-constexpr int kTreeThreads = 32 * (FP8 ? kWidenV0 + kWidenVWarps : kQkWarp + 1);
+constexpr int kVLoadWarps = FP8 ? 1 : 4;
 
 constexpr float kLeastLog2ScaleT = -40.f;   // V scales below 2^-40 count as 0: such rows round to 0 in fp16
 constexpr float kMostScaleInv = 1.0995e12f;      // just below 2^40
@@ -658,24 +660,23 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
             cp_async16z(slot + 16 * k, src, n);
           }
         } else if (!is_v) {
-          constexpr int kRowsAtOnce = 4 * kKLoadWarps<false>, kTurns = (128 + kRowsAtOnce - 1) / kRowsAtOnce;
+          constexpr int kRowsAtOnce = 4 * kKLoadWarps<false>, kTurns = 128 / kRowsAtOnce;
+          static_assert(128 % kRowsAtOnce == 0, "whole turns");
           const int c8 = tid & 7;
 #pragma unroll
           for (int k = 0; k < kTurns; ++k) {
             const int row = kRowsAtOnce * k + (tid >> 3);
-            if (row < 128) {
-              const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
-              cp_async16z(slot + row * 128 + ((c8 ^ (row & 7)) << 4), src, n);
-            }
+            const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
+            cp_async16z(slot + row * 128 + ((c8 ^ (row & 7)) << 4), src, n);
           }
         } else {
           constexpr int kRowsAtOnce = 4 * kVLoadWarps<false>, kTurns = 64 / kRowsAtOnce;
-          static_assert(kRowsAtOnce == 8, "a turn lies within a grain");
-          const int c8 = tid & 7;
+          static_assert(64 % kRowsAtOnce == 0, "whole turns");
+                  const int c8 = tid & 7;
 #pragma unroll
           for (int k = 0; k < kTurns; ++k) {
-            if (!gathered && ((done >> ((kRowsAtOnce * k) >> shift)) & 1u)) continue;
             const int row = kRowsAtOnce * k + (tid >> 3);
+            if (!gathered && ((done >> (row >> shift)) & 1u)) continue;
             const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
             const uint32_t dst = slot + (row >> 3) * 2048 + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4);
             cp_async16z(dst, src, n);
@@ -1101,7 +1102,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
 // ------------------------------------------------------------------ kernel
 
 template <bool FP8>
-__global__ void __launch_bounds__(kTreeThreads<FP8>, 1) tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -1186,9 +1187,9 @@ __global__ void __launch_bounds__(kTreeThreads<FP8>, 1) tree_attn_kernel(const _
     tree_widen_role<true>(nt, sbase, ms, threadIdx.x - 32 * kWidenV0);
   } else if (FP8 && warp >= kWidenK0 && warp < kWidenK0 + kWidenKWarps) {
     tree_widen_role<false>(nt, sbase, ms, threadIdx.x - 32 * kWidenK0);
-  } else if (warp < kVLoadWarp0 + kVLoadWarps<FP8>) {
-    const bool is_v = warp >= kVLoadWarp0;
-    tree_load_role<FP8>(p, nt, rank, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kVLoadWarp0 : kKLoadWarp0));
+  } else if (warp < kKLoadWarp0 + kKLoadWarps<FP8> || (warp >= kVLoadWarp0<FP8> && warp < kVLoadWarp0<FP8> + kVLoadWarps<FP8>)) {
+    const bool is_v = warp >= kVLoadWarp0<FP8>;
+    tree_load_role<FP8>(p, nt, rank, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kVLoadWarp0<FP8> : kKLoadWarp0));
   }
   tc_fence_before();
   __syncthreads();
@@ -1297,7 +1298,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams &p, bool e4m3, cudaStream_t s)
   cudaError_t e = launch((const void *)tree_plan_kernel, p, 1, kPlanThreads, 0, 1, s);
   if (e == cudaSuccess)
     e = launch(e4m3 ? (const void *)tree_attn_kernel<true> : (const void *)tree_attn_kernel<false>, p, 2 * p.clusters,
-               e4m3 ? kTreeThreads<true> : kTreeThreads<false>, kTreeSmem, 2, s);
+               kTreeThreads, kTreeSmem, 2, s);
   if (e == cudaSuccess && p.clusters > 1)
     e = launch((const void *)tree_merge_kernel, p, (p.clusters - 1) * 2 * (kH / kMergeHeads), 32 * kMergeHeads, 0, 1, s);
   return e;
