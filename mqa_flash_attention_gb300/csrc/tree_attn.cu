@@ -252,8 +252,9 @@ __device__ __forceinline__ void unit_record(const TreeAttnParams &p, int seq, in
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAttnParams p) {
-  __shared__ int warp_sum[32];
+  __shared__ int warp_sum[32], near[kPlanThreads];
   const int tid = threadIdx.x;
+  int *units_before = p.n_seq <= kPlanThreads ? near : p.ws_seq;  // of each sequence
   UnitRec *recs = static_cast<UnitRec *>(p.ws_unit);
   grid_launch_dependents();
   grid_dependency_wait();
@@ -262,12 +263,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
     const int b = b0 + tid, n = b < p.n_seq ? (tokens_of(p, b).n + 1) / 2 : 0;
     int all;
     const int inc = block_scan(n, warp_sum, all);
-    if (b < p.n_seq) p.ws_seq[b] = units + inc - n;
+    if (b < p.n_seq) units_before[b] = units + inc - n;
     units = min(units + all, 1 << 30);  // (only ranges that overlap name as many)
   }
   units = min(units, p.max_units);  // more than there is room for
   __syncthreads();
-  int tiles = 0;
+  int tiles = 0, at = 0, n = 0;
   for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int u = u0 + tid;
     UnitRec rec;
@@ -276,14 +277,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
       int lo = 0, hi = p.n_seq;  // the last sequence whose units begin at or before u
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (p.ws_seq[mid] <= u) lo = mid; else hi = mid;
+        if (units_before[mid] <= u) lo = mid; else hi = mid;
       }
-      unit_record(p, lo, 2 * (u - p.ws_seq[lo]), rec);
+      unit_record(p, lo, 2 * (u - units_before[lo]), rec);
     }
     int all;
     const int inc = block_scan(rec.tiles, warp_sum, all);
     if (u < units) {
-      rec.before = tiles + inc - rec.tiles;
+      rec.before = at = tiles + inc - rec.tiles;
+      n = rec.tiles;
       rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
       recs[u] = rec;
     }
@@ -294,7 +296,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
   __syncthreads();
   // The unit of each cluster's first tile.
   for (int u = tid; u < units; u += kPlanThreads) {
-    const int at = recs[u].before, n = recs[u].tiles;
+    if (units > kPlanThreads) {
+      at = recs[u].before;
+      n = recs[u].tiles;
+    }
     for (int i = (at + per - 1) / per; (long long)i * per < at + n; ++i) p.ws_start[i] = u;
   }
 }
@@ -1215,9 +1220,10 @@ __global__ void __launch_bounds__(32 * kMergeHeads) tree_merge_kernel(const Tree
   const int group = blockIdx.x % (kH / kMergeHeads), rest = blockIdx.x / (kH / kMergeHeads);
   const int i = rest & 1, edge = 1 + (rest >> 1), h = group * kMergeHeads + (threadIdx.x >> 5);
   const int4 head = p.ws_head[0];
+  const int unit = p.ws_start[edge];  // (anything where there is no such tile)
   const long long at = (long long)edge * head.y;
   if (at >= head.x) return;
-  const UnitRec &rec = static_cast<const UnitRec *>(p.ws_unit)[p.ws_start[edge]];
+  const UnitRec &rec = static_cast<const UnitRec *>(p.ws_unit)[unit];
   const int before = rec.before;
   if (before >= at || at - before > head.y) return;  // no cut here, or not the unit's first
   if (i > rec.two) return;
