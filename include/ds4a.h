@@ -767,6 +767,11 @@ ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *work
  *               row.  Runs are as long as the tables allow.
  *   X->raw, X->comp  as in ds4a_attn_decode_paged.
  *   X->q, X->o  fp16 [n_tok][64][512]; X->lse fp32 [n_tok][64] or NULL.
+ *               o, lse and the workspace must not overlap one another or an
+ *               input.
+ *   At most 2^20 tokens and 2^20 sequences; at most 2^30 rows in a sequence's
+ *   two tables, and 2^30 tiles of 256 rows over all pairs of tokens
+ *   (((n_tok + n_seq) / 2 + 1) * (table rows / 256 + 1)).
  *   workspace   256-byte aligned, at least ds4a_attn_tree_paged_workspace_size()
  *               bytes (which depends on the current device's SM count); need not
  *               be initialised; not shared by calls in flight at the same time.
@@ -905,7 +910,12 @@ ds4a_status ds4a_device_status(ds4a_stream_t stream, int clear);
  * attention: 0x60 Q buffer free, 0x61 K/V stage free, 0x62 Q loaded, 0x63 S
  * buffer free, 0x64 K/V stage loaded, 0x65 P written, 0x66 O read, 0x67 S
  * computed, 0x68 P consumed, 0x69 O complete, 0x6A draining copies, 0x6B E4M3
- * codes loaded, 0x6C row list written, 0x6D row list read.
+ * codes loaded, 0x6C row list written, 0x6D row list read.  Attention of
+ * several new tokens: 0x80 Q buffer free, 0x81 K/V stage free, 0x82 Q loaded,
+ * 0x83 S buffer free, 0x84 K/V stage loaded, 0x85 P written, 0x86 O read, 0x87
+ * S computed, 0x88 P consumed, 0x89 O complete, 0x8A draining copies and
+ * products, 0x8B E4M3 codes loaded, 0x8C row list written, 0x8D row list read,
+ * 0x8E E4M3 code slot free.
  * clear != 0 resets the word.
  */
 ds4a_status ds4a_device_error_word(ds4a_stream_t stream, uint32_t *word, int clear);

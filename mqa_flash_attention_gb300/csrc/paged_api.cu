@@ -491,6 +491,13 @@ ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout
     most += (int64_t)r->max_pages * r->page_rows;
   }
   if (most > kMostRows) return DS4A_ERR_INVALID_ARG;
+  // Other units still read q, and the merge the plan, when a unit's output is written.
+  const Span out[3] = {span(X->o, n_tok, X->o_tok_stride, (int64_t)DS4A_HEADS * DS4A_ROW_BYTES),
+                       span(X->lse, n_tok, 4 * DS4A_HEADS, 4 * DS4A_HEADS),
+                       span(workspace, 1, 0, (int64_t)ds4a_attn_tree_paged_workspace_size(n_seq, n_tok))};
+  const Span in[4] = {span(X->q, n_tok, X->q_tok_stride, (int64_t)DS4A_HEADS * DS4A_ROW_BYTES),
+                      ints(X->first, (int64_t)n_seq + 1), ints(X->parent, n_tok), ints(seq_geom, 4LL * n_seq)};
+  if (!apart(out, 3, in, 4)) return DS4A_ERR_INVALID_ARG;
   // Tiles of 256 rows, of pairs of tokens.
   if ((((int64_t)n_tok + n_seq) / 2 + 1) * ((most + 255) / 256 + 1) > (1 << 30)) return DS4A_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256) ||

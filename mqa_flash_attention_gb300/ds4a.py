@@ -1199,12 +1199,12 @@ def page_tables(table, free_pages, n_free, have, want, page_rows, *, drop=None, 
     sequence's begin, int32 [B + 1]; how many pages were lacking, int32 [1]."""
     import torch
     dev = table.device
-    if slots is None:
-        slots = _new(stream, torch.empty, (int(n_slots),), dtype=torch.int32, device=dev)
+    if slots is None:  # (filled: a call without sequences writes nothing)
+        slots = _new(stream, torch.full, (int(n_slots),), -1, dtype=torch.int32, device=dev)
     if first is None:
-        first = _new(stream, torch.empty, (have.shape[0] + 1,), dtype=torch.int32, device=dev)
+        first = _new(stream, torch.zeros, (have.shape[0] + 1,), dtype=torch.int32, device=dev)
     if n_short is None:
-        n_short = _new(stream, torch.empty, (1,), dtype=torch.int32, device=dev)
+        n_short = _new(stream, torch.zeros, (1,), dtype=torch.int32, device=dev)
     prepare_page_tables(table, free_pages, n_free, have, want, page_rows, drop=drop, slots=slots, first=first,
                         n_short=n_short, workspace=workspace, stream=stream)()
     return slots, first, n_short

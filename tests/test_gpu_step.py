@@ -6,7 +6,7 @@ Page tables, accepted paths and moved rows are whole numbers and copies: bit for
 import numpy as np
 import pytest
 
-from oracle import paged, step
+from oracle import fp8, paged, step
 from test_gpu_paged import (check_decode, device_error_word_stays_clear, ds4a, host, poison, rows_on, shape_of,  # noqa: F401
                             torch, up)
 from test_paged_oracle import make
@@ -487,3 +487,198 @@ def test_tree_of_single_tokens_is_the_decode(torch, ds4a):
     i32 = up(torch, np.array(one, dtype=np.int32))
     o, lse = ds4a.attn_decode_paged(shape_of(4), i32, up(torch, q), r, c, want_lse=True)
     check_decode(host(o), host(lse), want, [n + 129 for n in rows])
+
+
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_nan_in_a_query_stays_with_its_head(torch, ds4a, chain):
+    rng = np.random.default_rng(32)
+    geom, first, parent, q, raw, comp = tree_case(rng, [5, 6], [300, 20], 4, 16, chain=chain)
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    q[4, 33, 100] = np.nan
+    q[7, 0, 511] = np.inf
+    o, lse = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    assert np.isnan(o[4, 33]).all() and np.isnan(lse[4, 33])
+    assert not np.isfinite(o[7, 0]).any() or np.isnan(o[7, 0]).all()
+    o[4, 33], lse[4, 33], o[7, 0], lse[7, 0] = want[0][4, 33], want[1][4, 33], want[0][7, 0], want[1][7, 0]
+    check_tree(o, lse, want)
+
+
+# ------------------------------------------------------------------ the step as a whole
+
+def same_pool(rows, seg):
+    for name in ("k", "v"):
+        assert np.array_equal(host(getattr(rows, name)).view(np.uint8), np.ascontiguousarray(seg[name]).view(np.uint8)), name
+        if seg.get(name + "_scale") is not None:
+            assert np.array_equal(host(getattr(rows, name + "_scale")), seg[name + "_scale"]), name
+
+
+def write_rows(seg, slots, new, page):
+    """New rows (fp16 [n, 512] for K and V) into the pool, as the append writes them."""
+    for name, x in zip(("k",) if seg["v"] is seg["k"] else ("k", "v"), new):
+        for s, row in zip(slots, x):
+            if s < 0:
+                continue
+            if seg.get(name + "_scale") is not None:
+                c, sc = fp8.quantize_rows(row[None])
+                seg[name][s // page, s % page], seg[name + "_scale"][s // page, s % page] = c[0], sc[0]
+            else:
+                seg[name][s // page, s % page] = row
+
+
+@pytest.mark.parametrize("recorded", [False, True])
+@pytest.mark.parametrize("f8,shared,chain", [(False, True, False), (True, False, False), (False, False, True)])
+def test_the_step_from_page_tables_to_page_tables(torch, ds4a, f8, shared, chain, recorded):
+    """Several steps of one batch: pages for the new rows, the rows appended, attention, acceptance, the accepted rows
+    moved, the pages of the others given back; as direct calls, and as two graphs that share the workspaces."""
+    rng = np.random.default_rng(60 + f8 + 2 * chain)
+    n, page, width, n_pages, ratio, window, T = 5, 16, 14, 60, 4, 64, 48
+    shape = shape_of(ratio, window)
+    comp_rows = [400, 3, 0, 77, 250]
+    comp = make(rng, n, comp_rows, page, f8, shared)
+    raw = make(rng, 1, [n_pages * page], page, f8, shared)  # a pool whose pages no sequence holds yet
+    raw["table"] = np.full((n, width), -1, dtype=np.int32)
+    c, r = rows_on(torch, ds4a, comp), rows_on(torch, ds4a, raw)
+    free, n_free = rng.permutation(n_pages).astype(np.int32).tolist(), n_pages
+    pos = np.array([x * ratio + 2 for x in comp_rows])
+    raw0, n_raw = pos.copy(), np.zeros(n, dtype=int)
+    prev = rng.integers(0, 2, n).astype(np.int32)
+
+    stream = torch.cuda.Stream()
+    zeros = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    d = dict(have=zeros(n), want=zeros(n), drop=zeros(n), slots=zeros(T), first=zeros(n + 1), short=zeros(1),
+             geom=zeros(n, 4), parent=zeros(T), token=zeros(T), target=zeros(T), prev=up(torch, prev), path=zeros(n, T),
+             count=zeros(n), next=zeros(n), have2=zeros(n), want2=zeros(n), first2=zeros(n + 1), short2=zeros(1),
+             k=zeros(T, D, dtype=torch.float16), v=zeros(T, D, dtype=torch.float16),
+             q=zeros(T, H, D, dtype=torch.float16), o=zeros(T, H, D, dtype=torch.float16), lse=zeros(T, H, dtype=torch.float32),
+             free=up(torch, np.array(free, dtype=np.int32)), n_free=up(torch, np.array([n_free], dtype=np.int32)))
+    wp = torch.empty(ds4a.page_tables_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+    wt = torch.empty(ds4a.tree_paged_workspace_bytes(n, T), dtype=torch.uint8, device="cuda")
+    par = None if chain else d["parent"]
+    forward = [
+        ds4a.prepare_page_tables(r.table, d["free"], d["n_free"], d["have"], d["want"], page, drop=d["drop"],
+                                 slots=d["slots"], first=d["first"], n_short=d["short"], workspace=wp, stream=stream),
+        ds4a.prepare_append_paged(r, d["k"], None if shared else d["v"], d["slots"], stream=stream),
+        ds4a.prepare_tree_paged(shape, d["geom"], d["first"], d["q"], r, c, parent=par, workspace=wt, out=d["o"],
+                                lse=d["lse"], stream=stream),
+        ds4a.prepare_tree_accept(d["first"], d["token"], d["target"], parent=par, prev=d["prev"], path=d["path"],
+                                 n_accepted=d["count"], next_token=d["next"], stream=stream),
+        ds4a.prepare_commit_paged(r, d["geom"], d["path"], d["count"], stream=stream)]
+    back = [ds4a.prepare_page_tables(r.table, d["free"], d["n_free"], d["have2"], d["want2"], page, slots=None,
+                                     first=d["first2"], n_short=d["short2"], workspace=wp, stream=stream)]
+
+    def run(calls):
+        for f in calls:
+            f()
+    torch.cuda.synchronize()
+    graphs = []
+    if recorded:
+        for calls in (forward, back):
+            with ds4a.Graph(stream) as g:
+                run(calls)
+            graphs.append(g)
+    accepted_some = accepted_none = 0
+    for i in range(7):
+        counts = rng.integers(0, 10, n)
+        new = int(counts.sum())
+        first = np.concatenate([[0], np.cumsum(counts)])
+        drop = np.minimum(np.maximum(pos - window + 1 - raw0, 0), n_raw)
+        gone = drop // page
+        parent = None if chain else np.concatenate([tree_of(rng, m, False) for m in counts] + [np.zeros(T - new, int)])
+        token, target = rng.integers(0, 2, T), rng.integers(0, 2, T)
+        q, k, v = (rng.standard_normal(s).astype(np.float16) for s in ((T, H, D), (T, D), (T, D)))
+        n_comp = np.array(comp_rows)
+        # counted as after the dropped pages: the attention comes behind the page tables
+        geom = np.stack([pos, n_raw - gone * page, raw0 + gone * page, n_comp], 1)
+        for name, x in dict(have=n_raw, want=n_raw + counts, drop=drop, geom=geom, token=token, target=target,
+                            have2=n_raw - gone * page + counts).items():
+            d[name].copy_(up(torch, x.astype(np.int32)))
+        if not chain:
+            d["parent"].copy_(up(torch, parent.astype(np.int32)))
+        for name, x in dict(q=q, k=k, v=v).items():
+            d[name].copy_(up(torch, x))
+        d["o"].fill_(7.0)
+        torch.cuda.synchronize()
+        graphs[0]() if recorded else run(forward)
+        torch.cuda.synchronize()
+
+        n_free, slots, first_, short = step.page_tables(raw["table"], free, n_free, n_raw, n_raw + counts, drop, page,
+                                                        n_pages, T)
+        assert np.array_equal(host(r.table), raw["table"]) and int(d["n_free"]) == n_free and int(d["short"]) == short == 0
+        assert np.array_equal(host(d["slots"]), slots) and np.array_equal(host(d["first"]), first_)
+        assert np.array_equal(first_, first)
+        write_rows(raw, slots, (k, v), page)
+        want = step.attention(shape, geom, first, parent, q, raw, comp)
+        check_tree(host(d["o"])[:new], host(d["lse"])[:new], tuple(x[:new] for x in want))
+        assert (host(d["o"])[new:] == 7).all()
+        paths, nxt = step.accept(first, parent, token, target, host(d["prev"]), T)
+        assert host(d["count"]).tolist() == [len(p) for p in paths] and host(d["next"]).tolist() == nxt
+        step.commit(raw, geom, paths)
+        same_pool(r, raw)
+
+        taken = np.array([len(p) for p in paths])
+        accepted_some += (taken > 1).sum()
+        accepted_none += (taken == 0).sum()
+        n_raw = n_raw - gone * page
+        d["want2"].copy_(up(torch, (n_raw + taken).astype(np.int32)))
+        torch.cuda.synchronize()
+        graphs[1]() if recorded else run(back)
+        torch.cuda.synchronize()
+        n_free, *_ = step.page_tables(raw["table"], free, n_free, n_raw + counts, n_raw + taken, None, page, n_pages, 0)
+        assert np.array_equal(host(r.table), raw["table"]) and int(d["n_free"]) == n_free
+        assert np.array_equal(host(d["free"]), np.array(free, dtype=np.int32))
+        pos, n_raw, raw0 = pos + taken, n_raw + taken, raw0 + gone * page
+        d["prev"].copy_(d["next"])
+    assert accepted_some and accepted_none
+    assert n_pages == n_free + sum(-(-x // page) for x in n_raw)
+    for g in graphs:
+        g.close()
+
+
+def test_steps_on_two_streams_at_once(torch, ds4a):
+    """Attention, acceptance and commits in flight on two streams, outputs and workspaces made by the calls: a job's
+    results are the same bits every time."""
+    rng = np.random.default_rng(70)
+    jobs = []
+    for k in range(2):
+        geom, first, parent, q, raw, comp = tree_case(rng, [9 + k, 30, 2], [2000, 700 + k, 5], 4, 16, bool(k), True)
+        i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+        token, target = rng.integers(0, 2, len(q)), rng.integers(0, 2, len(q))
+        jobs.append(dict(geom=i32(geom), first=i32(first), parent=i32(parent), q=up(torch, q), raw=rows_on(torch, ds4a, raw),
+                         comp=rows_on(torch, ds4a, comp), token=i32(token), target=i32(target), stream=torch.cuda.Stream(),
+                         want=step.attention(shape_of(4), geom, first, parent, q, raw, comp),
+                         paths=step.accept(first, parent, token, target, None, len(q))))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(12):
+        for j in jobs:
+            o, lse = ds4a.attn_tree_paged(shape_of(4), j["geom"], j["first"], j["q"], j["raw"], j["comp"],
+                                          parent=j["parent"], want_lse=True, stream=j["stream"])
+            outs.append((o, lse, *ds4a.tree_accept(j["first"], j["token"], j["target"], parent=j["parent"],
+                                                   stream=j["stream"])))
+    torch.cuda.synchronize()
+    for k, j in enumerate(jobs):
+        check_tree(host(outs[k][0]), host(outs[k][1]), j["want"])
+        assert host(outs[k][3]).tolist() == [len(p) for p in j["paths"][0]] and host(outs[k][4]).tolist() == j["paths"][1]
+        for again in outs[k + 2::2]:
+            assert all(torch.equal(a, b) for a, b in zip(again, outs[k]))
+
+
+def test_step_calls_of_empty_batches(torch, ds4a):
+    """No sequence, or no new token: nothing is written, and nothing fails."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    rows = ds4a.PagedRows(torch.zeros((4, 16, D), dtype=torch.float16, device="cuda"), None, i32(2, 3))
+    o = ds4a.attn_tree_paged(shape_of(4), i32(2, 4), i32(3), torch.zeros((0, H, D), dtype=torch.float16, device="cuda"), rows)
+    assert o.shape == (0, H, D)
+    none = ds4a.PagedRows(rows.k, None, i32(0, 3))
+    q = torch.zeros((3, H, D), dtype=torch.float16, device="cuda")
+    out = torch.full_like(q, 5)
+    ds4a.attn_tree_paged(shape_of(4), i32(0, 4), i32(1), q, none, out=out)
+    assert (out == 5).all()
+    path, count, nxt = ds4a.tree_accept(i32(3), i32(0), i32(0), width=4)
+    assert (path == -1).all() and count.tolist() == [0, 0] and nxt.tolist() == [-1, -1]
+    assert ds4a.tree_accept(i32(1), i32(0), i32(0), width=4)[0].shape == (0, 4)
+    ds4a.commit_paged(rows, i32(2, 4), i32(2, 0), i32(2))
+    ds4a.commit_paged(none, i32(0, 4), i32(0, 4), i32(0))
+    slots, first, short = ds4a.page_tables(i32(0, 3), i32(4), i32(1), i32(0), i32(0), 16, n_slots=3)
+    assert slots.tolist() == [-1] * 3 and first.tolist() == [0] and short.tolist() == [0]
+    torch.cuda.synchronize()

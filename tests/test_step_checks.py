@@ -83,8 +83,8 @@ def test_commit_arguments_are_checked(lib):
 
 
 def tree(lib, n=3, n_tok=20, shape=None, geom=5 * AT, ws=1 << 30, nbytes=None, **kw):
-    base = dict(q=4 * AT, q_tok_stride=65536, first=6 * AT, parent=7 * AT, raw=seg(), comp=seg(), o=8 * AT,
-                o_tok_stride=65536, lse=9 * AT)
+    base = dict(q=1 << 35, q_tok_stride=65536, first=6 * AT, parent=7 * AT, raw=seg(), comp=seg(), o=1 << 36,
+                o_tok_stride=65536, lse=1 << 37)
     base.update(kw)
     X = ds4a.PagedTree(*[base[n] for n, _ in ds4a.PagedTree._fields_])
     S = ds4a.make_layout(dict(SHAPE, **(shape or {})))
@@ -110,11 +110,14 @@ def test_tree_arguments_are_checked(lib):
                 dict(geom=AT + 8), dict(shape=dict(window=0)), dict(shape=dict(ratio=0)), dict(shape=dict(scale=math.inf)),
                 dict(shape=dict(scale=math.nan)), dict(shape=dict(scale=3e38)), dict(comp=seg(**f8)), dict(raw=seg(k=None)),
                 dict(comp=seg(v=None)), dict(raw=seg(page_rows=0)), dict(comp=seg(table=None)), dict(raw=seg(max_pages=-1)),
-                dict(raw=seg(**big), comp=seg())):
+                dict(raw=seg(**big), comp=seg()),
+                # ranges that overlap
+                dict(o=(1 << 35) + 65536), dict(o=(1 << 35) - 19 * 65536), dict(lse=(1 << 36) + 16), dict(lse=7 * AT + 76),
+                dict(lse=6 * AT - 5116), dict(o=5 * AT), dict(ws=1 << 35), dict(ws=(1 << 36) - 256), dict(lse=1 << 30)):
         assert tree(lib, **bad) == ds4a.ERR_INVALID_ARG, bad
     need = lib.ds4a_attn_tree_paged_workspace_size(3, 20)
     assert need > 0 and lib.ds4a_attn_tree_paged_workspace_size(0, 5) == 0
-    for bad in (dict(ws=None), dict(ws=AT + 128), dict(nbytes=need - 1)):
+    for bad in (dict(ws=None), dict(ws=(1 << 30) + 128), dict(nbytes=need - 1)):
         assert tree(lib, **bad) == ds4a.ERR_WORKSPACE, bad
 
 
