@@ -3,6 +3,9 @@
 Page tables, accepted paths and moved rows are whole numbers and copies: bit for bit.
 """
 
+import os
+import re
+
 import numpy as np
 import pytest
 
@@ -632,6 +635,46 @@ def test_the_step_from_page_tables_to_page_tables(torch, ds4a, f8, shared, chain
     assert n_pages == n_free + sum(-(-x // page) for x in n_raw)
     for g in graphs:
         g.close()
+
+
+def test_the_documented_step_of_drafted_tokens(torch, ds4a):
+    """The README's step, run as it stands: three steps of two sequences."""
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        (block,) = re.findall(r"```py\n(.*?)```", f.read(), re.S)
+    rng = np.random.default_rng(71)
+    n, page, n_pages, ratio = 2, 64, 9, 4
+    comp = make(rng, n, [300, 40], page, False, True)
+    raw = make(rng, 1, [n_pages * page], page, False, True)
+    raw["table"] = np.full((n, 4), -1, dtype=np.int32)
+    r, c = rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp)
+    free, n_free = rng.permutation(n_pages).astype(np.int32).tolist(), n_pages
+    i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    geom = np.array([(1201, 0, 1201, 300), (163, 0, 163, 40)], dtype=np.int32)
+    names = dict(torch=torch, ds4a=ds4a, geom=i32(geom), raw_table=r.table, raw=r, comp=c, free_pages=i32(free),
+                 n_free=i32([n_free]), shape=shape_of(ratio), prev=i32([1, 0]))
+    for counts in ([9, 70], [1, 5], [60, 60]):
+        T = sum(counts)
+        first = np.concatenate([[0], np.cumsum(counts)])
+        parent = np.concatenate([tree_of(rng, m, False) for m in counts])
+        token, target = rng.integers(0, 2, T), rng.integers(0, 2, T)
+        q, k = rng.standard_normal((T, H, D)).astype(np.float16), rng.standard_normal((T, D)).astype(np.float16)
+        names.update(first=i32(first), n_new=i32(counts), parent=i32(parent), token=i32(token), q=up(torch, q),
+                     new_k=up(torch, k), choose=lambda o, t=target: i32(t))
+        prev, have = host(names["prev"]), geom[:, 1].copy()
+        exec(block, names)
+        n_free, slots, *_ = step.page_tables(raw["table"], free, n_free, have, have + counts, None, page, n_pages, T)
+        write_rows(raw, slots, (k,), page)
+        want = step.attention(shape_of(ratio), geom, first, parent, q, raw, comp)
+        check_tree(host(names["o"]), None, want)
+        paths, nxt = step.accept(first, parent, token, target, prev, T)
+        taken = np.array([len(p) for p in paths])
+        step.commit(raw, geom, paths)
+        same_pool(r, raw)
+        n_free, *_ = step.page_tables(raw["table"], free, n_free, have + counts, have + taken, None, page, n_pages, 0)
+        geom[:, :2] += taken[:, None].astype(np.int32)
+        assert np.array_equal(host(names["geom"]), geom) and np.array_equal(host(r.table), raw["table"])
+        assert int(names["n_free"]) == n_free and host(names["next_token"]).tolist() == nxt
+        names["prev"] = names["next_token"]
 
 
 def test_steps_on_two_streams_at_once(torch, ds4a):
