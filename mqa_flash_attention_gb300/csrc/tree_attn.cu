@@ -69,7 +69,7 @@ static_assert(7 * kPart <= kRingBytes && 4 * kPart + 2 * kCodeSlots * kCodePart 
 // meets the others at mbarriers only, and its code is kept small: what all roles run
 // through in a tile has to stay in the instruction cache.
 constexpr int kTreeThreads = 640;
-constexpr int kKLoadWarp0 = 8, kListWarp = 13, kPvWarp = 14, kQkWarp = 15;
+constexpr int kKLoadWarp0 = 8, kPvWarp1 = 12, kListWarp = 13, kPvWarp0 = 14, kQkWarp = 15;
 constexpr int kWidenK0 = 9, kWidenV0 = 16, kWidenKWarps = 2, kWidenVWarps = 4;
 template <bool FP8>
 constexpr int kVLoadWarp0 = FP8 ? 11 : 16;
@@ -560,15 +560,18 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
 
 // The warps of K, or of V, load part after part into their ring: by TMA, a run or a
 // grain per lane, or by 16-byte copies.  A warp stands some 600 cycles at a bulk copy,
-// so the warps take the parts that TMA brings in turn; parts with gathered rows
-// are loaded by all.  (A warp that waits for a stage has waited for one at most
-// as many parts before as there are warps, and there are more stages than
-// warps, so it is never two phases behind.)
+// so the warps take the parts in turn, and nobody but a part's warp waits for its stage.
+// (A parity tells a phase from the next one only.  Stages of K are freed in order, and
+// a warp that waits for one has waited for another at most as many parts before as
+// there are warps, fewer than stages.  V's halves are consumed by warps of their own,
+// one up to a tile ahead of the other: there a stage is always the same warp's.)
 template <bool FP8>
 __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, uint32_t rank, uint32_t sbase, TMisc &ms,
                                                bool is_v, int tid) {
   if (nt <= 0) return;
-  static_assert(kKLoadWarps<FP8> <= kKStages<false> && kVLoadWarps<FP8> <= kVStages<false>, "no more warps than stages");
+  static_assert(kKLoadWarps<false> < kKStages<false> && kVLoadWarps<false> == kVStages<false> && kKLoadWarps<true> == 1 &&
+                    kVLoadWarps<true> == 1,
+                "whose turn a stage is");
   const int n_warps = is_v ? kVLoadWarps<FP8> : kKLoadWarps<FP8>;
   const int lane = tid & 31, warp = tid >> 5;
   const long long vdelta0 = p.seg[0].v - p.seg[0].k, vdelta1 = p.seg[1].v - p.seg[1].k;
@@ -596,7 +599,7 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
       __syncwarp();
     }
     // Grains that TMA brings (by runs of several where all are whole).
-    const bool full = flags & TF_FULL, gathered = flags & TF_GATHERED, by_rows = is_v ? !full : gathered;
+    const bool full = flags & TF_FULL, gathered = flags & TF_GATHERED;
     const uint32_t grains = is_v ? ms.live[buf] : ms.held[buf];
     const int shift = p.grain_shift, unit = full ? p.run_shift : shift;  // log2 of the rows of a copy
     const int rows = is_v ? 64 : 128;                                    // of a part
@@ -608,7 +611,7 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
       const uint32_t st = st0 + at, par = ph;
       if ((int)++turn == n_warps) turn = 0;
       if (++at == stages) at = 0, ph ^= 1;
-      if (!mine && !by_rows) continue;
+      if (!mine) continue;
       const int row0 = is_v ? 64 * (c >> 1) : 128 * (int)rank;
       const int dim0 = is_v ? 256 * (c & 1) + 128 * (int)rank : 64 * c;
       const uint32_t slot = sbase + kOffRing + (FP8 ? 4 * kPart + st * kCodePart : st * kPart);
@@ -618,15 +621,17 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
         ok = false;
         break;
       }
-      if (!gathered && mine) {
+      // Grains of the part that TMA brings; of V, rows of the others are copied one by one.
+      const uint32_t all = gathered ? 0 : 0xffffffffu >> (32 - (rows >> shift));
+      const uint32_t here = gathered ? 0 : (grains >> (row0 >> shift)) & all;
+      const bool by_rows = gathered || (is_v && here != all);
+      if (!gathered) {
         // Rows that TMA brings here; fp16: the bytes of both CTAs count at rank 0's
         // barrier (of K, each has rows of its own), rank 1's has the issue only.
-        const uint32_t first = (uint32_t)row0 >> shift, n = (uint32_t)rows >> shift;
-        const uint32_t here = (grains >> first) & ((1u << n) - 1);
         if (lane == 0) {
           const uint32_t count = FP8 ? __popc(here) : is_v ? 2 * __popc(here) : __popc(grains);
           if (count != 0 && (FP8 || rank == 0)) mbar_expect_tx(b_full, (count << shift) * (is_v ? 256u : 128u) / (FP8 ? 2u : 1u));
-          if (!by_rows) mbar_arrive_cnt(b_full, 32 * n_warps);
+          if (!by_rows) mbar_arrive_cnt(b_full, 32);
         }
         const int row = lane << unit;  // within the part
         if (row < rows && ((here >> (row >> shift)) & 1u)) {
@@ -647,45 +652,32 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
         // 16-byte copies, eight lanes to a row (E4M3 codes of K: four), of the rows in
         // grains that TMA does not bring.
         const unsigned long long *list = ms.row[buf] + row0;
-        const uint32_t done = grains >> ((uint32_t)row0 >> shift & 31);
         auto src_of = [&](int row, int byte, uint32_t &bytes) {
           const unsigned long long e = list[row];
           const long long to_v = (e & kSegBitT) ? vdelta1 : vdelta0;
           bytes = (e & (is_v ? kNoRowT | kNoValue : kNoRowT)) ? 0u : 16u;
           return reinterpret_cast<const uint8_t *>(e & ~15ull) + (is_v ? to_v : 0) + byte;
         };
+        auto by_tma = [&](int row) { return ((here >> ((row >> shift) & 31)) & 1u) != 0; };
         uint32_t n;
         if (FP8) {
           const int per_row = is_v ? 3 : 2;
 #pragma unroll 4
           for (int k = lane; k < 512; k += 32) {
             const int row = k >> per_row;
-            if (!gathered && ((done >> (row >> shift)) & 1u)) continue;
+            if (by_tma(row)) continue;
             const uint8_t *src = src_of(row, dim0 + 16 * (k & ((1 << per_row) - 1)), n);
             cp_async16z(slot + 16 * k, src, n);
           }
-        } else if (!is_v) {
-          constexpr int kRowsAtOnce = 4 * kKLoadWarps<false>, kTurns = 128 / kRowsAtOnce;
-          static_assert(128 % kRowsAtOnce == 0, "whole turns");
-          const int c8 = tid & 7;
-#pragma unroll
-          for (int k = 0; k < kTurns; ++k) {
-            const int row = kRowsAtOnce * k + (tid >> 3);
-            const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
-            cp_async16z(slot + row * 128 + ((c8 ^ (row & 7)) << 4), src, n);
-          }
         } else {
-          constexpr int kRowsAtOnce = 4 * kVLoadWarps<false>, kTurns = 64 / kRowsAtOnce;
-          static_assert(64 % kRowsAtOnce == 0, "whole turns");
-                  const int c8 = tid & 7;
-#pragma unroll
-          for (int k = 0; k < kTurns; ++k) {
-            const int row = kRowsAtOnce * k + (tid >> 3);
-            if (!gathered && ((done >> (row >> shift)) & 1u)) continue;
+          const int c8 = lane & 7;
+#pragma unroll 4
+          for (int row = lane >> 3; row < rows; row += 4) {
+            if (by_tma(row)) continue;
             const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
-            const uint32_t dst = slot + (row >> 3) * 2048 + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4);
+            const uint32_t dst = slot + (row >> 3) * (is_v ? 2048 : 1024) + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4);
             cp_async16z(dst, src, n);
-            cp_async16z(dst + 1024, src + 128, n);
+            if (is_v) cp_async16z(dst + 1024, src + 128, n);
           }
         }
         cp_async_arrive(b_full);
@@ -771,9 +763,9 @@ __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &m
 // what has landed here, stage by stage.  Gathered and widened rows are generic-proxy
 // writes: the fence makes them visible to the tensor core before the news goes out.
 template <bool FP8>
-__device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v) {
-  const uint32_t stage0 = is_v ? kKStages<FP8> : 0, stages = is_v ? kVStages<FP8> : kKStages<FP8>;
-  uint32_t st = 0, ph = 0, item = 0;
+__device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v, uint32_t half) {
+  const uint32_t stage0 = is_v ? kKStages<FP8> : 0, stages = is_v ? kVStages<FP8> : kKStages<FP8>, step = is_v ? 2 : 1;
+  uint32_t st = half, ph = 0, item = 0;
 #pragma unroll 1
   for (int g = 0; g < nt; ++g) {
     const int buf = g % kListsT;
@@ -786,13 +778,13 @@ __device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v) {
       ++item;
     }
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
+    for (uint32_t c = half; c < 8; c += step) {
       if (is_v && ((flags >> (TF_PARTS + (c >> 1))) & 1) == 0) continue;
       const uint32_t bar = smem_u32(&ms.kv_full[stage0 + st]);
       if (!wait_phase(bar, ph, TSITE_KV_FULL, &ms.wait)) return;
       fence_proxy_async_smem();
       mbar_arrive_cluster(cluster_addr(bar, 0));
-      if (++st == stages) st = 0, ph ^= 1;
+      if ((st += step) >= stages) st = half, ph ^= 1;
     }
   }
 }
@@ -803,7 +795,7 @@ __device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v) {
 // descriptors are warp-uniform values, and one elected lane issues.  Waits are
 // joined over the warp: all lanes go on or none.
 template <bool FP8, bool IS_V>
-__device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t tmem, TMisc &ms) {
+__device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t tmem, TMisc &ms, uint32_t half) {
   constexpr uint32_t kIdesc = idesc_f16_f32(128, 256, false, IS_V);
   constexpr int kStage0 = IS_V ? kKStages<FP8> : 0;
   // Q, K and P: K-major.  V: MN-major, LBO = distance of the 64-dim blocks, SBO =
@@ -811,8 +803,9 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
   const uint64_t a_desc = IS_V ? sdesc_sw128(sbase + kOffTP, 16, 1024) : sdesc_sw128(sbase, 16, 1024);
   const uint64_t b_desc = IS_V ? sdesc_sw128(sbase + kOffRing + kStage0 * kPart, 1024, 2048)
                                : sdesc_sw128(sbase + kOffRing, 16, 1024);
-  Ring<IS_V ? kVStages<FP8> : kKStages<FP8>> ring;
-  uint32_t item = 0;
+  constexpr uint32_t kStages = IS_V ? kVStages<FP8> : kKStages<FP8>, kStep = IS_V ? 2 : 1;
+  static_assert(kVStages<FP8> % 2 == 0, "a stage of V is always the same half's");
+  uint32_t st = half, ph = 0, item = 0;
   bool ready = false;  // the next stage had landed when it was asked for
   bool empty = true;   // no product has gone into this item's O
   auto wait = [&](uint64_t &bar, uint32_t parity, uint32_t site) -> bool {
@@ -837,24 +830,23 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
     empty = empty || first;
     tc_fence_after();
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
+    for (uint32_t c = half; c < 8; c += kStep) {
       // (Also of a box whose rows nobody sees: its barriers go through every tile.)
-      if (IS_V && (c & 1) == 0 && !wait(ms.p_full[c >> 1], g & 1, TSITE_P_FULL)) return;
+      if (IS_V && !wait(ms.p_full[c >> 1], g & 1, TSITE_P_FULL)) return;
       const bool live = !IS_V || ((parts >> (c >> 1)) & 1) != 0;
-      uint32_t st = 0;
+      const uint32_t at = st;
       if (live) {
-        st = ring.st;
-        if (!__all_sync(0xffffffffu, ready) && !wait(ms.kv_full[kStage0 + st], ring.ph, TSITE_KV_FULL)) return;
-        ring.advance();
+        if (!__all_sync(0xffffffffu, ready) && !wait(ms.kv_full[kStage0 + st], ph, TSITE_KV_FULL)) return;
+        if ((st += kStep) >= kStages) st = half, ph ^= 1;
         // The next stage is asked for before this one's products are issued.
-        ready = mbar_test(smem_u32(&ms.kv_full[kStage0 + ring.st]), ring.ph);
+        ready = mbar_test(smem_u32(&ms.kv_full[kStage0 + st]), ph);
         if (fence) fence_proxy_async_smem();
       }
       if (IS_V) tc_fence_after();
       const uint64_t a0 = sdesc_add(a_desc, (IS_V ? c >> 1 : c) * 8192);
-      const uint64_t b0 = sdesc_add(b_desc, st * kPart);
-      const uint32_t d = IS_V ? tmem + 128 * (c & 1) : tmem + kTmemTS + 128 * sb;
-      const bool fresh = IS_V ? empty && (c >> 1) == lowest : c == 0;
+      const uint64_t b0 = sdesc_add(b_desc, at * kPart);
+      const uint32_t d = IS_V ? tmem + 128 * half : tmem + kTmemTS + 128 * sb;
+      const bool fresh = IS_V ? empty && (int)(c >> 1) == lowest : c == 0;
       if (elect_lane()) {
         if (live) {
 #pragma unroll
@@ -864,11 +856,11 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
             else
               umma_pair_f16_acc(d, sdesc_add(a0, ks * 32), sdesc_add(b0, ks * (IS_V ? 4096 : 32)), kIdesc);
           }
-          umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + st]));
+          umma_pair_commit(smem_u32(&ms.kv_empty[kStage0 + at]));
         }
         if (IS_V) {
-          if (c & 1) umma_pair_commit(smem_u32(&ms.p_empty[c >> 1]));
-          if (c >= 6 && last) umma_pair_commit(smem_u32(&ms.o_full[c & 1]));
+          umma_pair_commit(smem_u32(&ms.p_empty[c >> 1]));
+          if (c >= 6 && last) umma_pair_commit(smem_u32(&ms.o_full[half]));
         } else if (c == 7) {
           umma_pair_commit(smem_u32(&ms.s_full[sb]));
           if (last) umma_pair_commit(smem_u32(&ms.q_empty));
@@ -1120,10 +1112,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     mbar_init(smem_u32(&ms.q_empty), 1);
     mbar_init(smem_u32(&ms.peer_q_full), 1);
     for (int s = 0; s < 7; ++s) {
-      // Loader threads, or the warps that widen; and the other CTA's report.
-      const int loaders = 32 * (s < kKStages<false> ? kKLoadWarps<false> : kVLoadWarps<false>);
+      // The threads of the warp that loads, or the warps that widen; and the other CTA's report.
       const int widen = s < kKStages<true> ? kWidenKWarps : kWidenVWarps;
-      mbar_init(smem_u32(&ms.kv_full[s]), (FP8 ? widen : loaders) + (rank == 0 ? 1 : 0));
+      mbar_init(smem_u32(&ms.kv_full[s]), (FP8 ? widen : 32) + (rank == 0 ? 1 : 0));
       mbar_init(smem_u32(&ms.kv_empty[s]), 1);
     }
     for (int s = 0; s < 2 * kCodeSlots; ++s) {
@@ -1132,8 +1123,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     }
     for (int s = 0; s < kListsT; ++s) {
       mbar_init(smem_u32(&ms.list_full[s]), 1);
-      // Softmax, the last two warps, loaders and those that widen V.
-      mbar_init(smem_u32(&ms.list_empty[s]), kComputeWarps + 2 + kKLoadWarps<FP8> + kVLoadWarps<FP8> +
+      // Softmax, the MMA warps, loaders and those that widen V.
+      mbar_init(smem_u32(&ms.list_empty[s]), kComputeWarps + 3 + kKLoadWarps<FP8> + kVLoadWarps<FP8> +
                                                  (FP8 ? kWidenVWarps : 0));
     }
     for (int s = 0; s < 2; ++s) {
@@ -1143,10 +1134,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(smem_u32(&ms.p_full[s]), 2 * kComputeWarps / 4);
-      mbar_init(smem_u32(&ms.p_empty[s]), 1);
+      mbar_init(smem_u32(&ms.p_empty[s]), 2);
     }
     mbar_init(smem_u32(&ms.o_empty), 2 * kComputeWarps);
-    mbar_init(smem_u32(&ms.mma_done), 2);
+    mbar_init(smem_u32(&ms.mma_done), 3);
     ms.wait.timeout_ns = p.timeout_ns;
     ms.wait.err = p.err;
     ms.wait.abort_flag = 0;
@@ -1170,17 +1161,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   const int nt = (int)max(0ll, min((long long)head.y, head.x - before));
   if (warp < kComputeWarps) {
     tree_softmax_role<FP8>(p, nt, cluster, rank, smem, tmem, ms, threadIdx.x);
-  } else if (warp == kPvWarp || warp == kQkWarp) {
-    const bool is_v = warp == kPvWarp, lane0 = (threadIdx.x & 31) == 0;
+  } else if (warp == kPvWarp0 || warp == kPvWarp1 || warp == kQkWarp) {
+    const bool is_v = warp != kQkWarp, lane0 = (threadIdx.x & 31) == 0;
+    const uint32_t half = warp == kPvWarp1 ? 1 : 0;
     if (rank == 0) {
       if (is_v)
-        tree_mma_role<FP8, true>(nt, sbase, tmem, ms);
+        tree_mma_role<FP8, true>(nt, sbase, tmem, ms, half);
       else
-        tree_mma_role<FP8, false>(nt, sbase, tmem, ms);
+        tree_mma_role<FP8, false>(nt, sbase, tmem, ms, 0);
       __syncwarp();
       if (elect_lane()) umma_pair_commit(smem_u32(&ms.mma_done));
     } else if (lane0) {
-      tree_relay_role<FP8>(nt, ms, is_v);
+      tree_relay_role<FP8>(nt, ms, is_v, half);
     }
     __syncwarp();
     volatile int never = 0;
