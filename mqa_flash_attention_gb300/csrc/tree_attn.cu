@@ -204,12 +204,10 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sum, int &all) {
   return v;
 }
 
-__device__ __forceinline__ void unit_record(const TreeAttnParams &p, int seq, int t0, UnitRec &r) {
+__device__ __forceinline__ void unit_record(const TreeAttnParams &p, int seq, Span2 s, int4 g, int t0,
+                                            const UnitRows &rows, UnitRec &r) {
   const bool chain = p.parent == nullptr;
-  const Span2 s = tokens_of(p, seq);
-  const int4 g = p.geom[seq];
   const int t1 = min(t0 + 1, s.n - 1);
-  const UnitRows rows = unit_rows(p, g, s.n, t0, t1);
   const long long pos = max(g.x, 0), raw_pos0 = max(g.z, 0);
   r.seq = seq;
   r.t0 = t0;
@@ -251,10 +249,16 @@ __device__ __forceinline__ void unit_record(const TreeAttnParams &p, int seq, in
   }
 }
 
+// Every block counts all tiles, which is quick, and writes the records of its share of
+// the units, which is not (a tree's nodes climb to their roots): in one block, 1,470
+// units took 31 us.
+constexpr int kPlanUnits = 32;  // of a block, at least
+constexpr int kPlanBlocks = 32;
+
 __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAttnParams p) {
   __shared__ int warp_sum[32], near[kPlanThreads];
   const int tid = threadIdx.x;
-  int *units_before = p.n_seq <= kPlanThreads ? near : p.ws_seq;  // of each sequence
+  int *units_before = p.n_seq <= kPlanThreads ? near : p.ws_seq;  // of each sequence (all blocks write the same)
   UnitRec *recs = static_cast<UnitRec *>(p.ws_unit);
   grid_launch_dependents();
   grid_dependency_wait();
@@ -268,35 +272,46 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
   }
   units = min(units, p.max_units);  // more than there is room for
   __syncthreads();
+  const int share = (units + (int)gridDim.x - 1) / (int)gridDim.x, u_lo = (int)blockIdx.x * share;
+  const int u_hi = min(u_lo + share, units);
   int tiles = 0, at = 0, n = 0;
   for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int u = u0 + tid;
-    UnitRec rec;
-    rec.tiles = 0;
+    int here = 0, seq = 0, t0 = 0;
+    Span2 toks = {0, 0};
+    int4 g = make_int4(0, 0, 0, 0);
+    UnitRows rows = {0, 0, 0, 0, 0};
     if (u < units) {
-      int lo = 0, hi = p.n_seq;  // the last sequence whose units begin at or before u
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (units_before[mid] <= u) lo = mid; else hi = mid;
+      int hi = p.n_seq;  // the last sequence whose units begin at or before u
+      while (hi - seq > 1) {
+        const int mid = (seq + hi) / 2;
+        if (units_before[mid] <= u) seq = mid; else hi = mid;
       }
-      unit_record(p, lo, 2 * (u - units_before[lo]), rec);
+      t0 = 2 * (u - units_before[seq]);
+      toks = tokens_of(p, seq);
+      g = p.geom[seq];
+      rows = unit_rows(p, g, toks.n, t0, min(t0 + 1, toks.n - 1));
+      here = rows.tiles();
     }
     int all;
-    const int inc = block_scan(rec.tiles, warp_sum, all);
-    if (u < units) {
-      rec.before = at = tiles + inc - rec.tiles;
-      n = rec.tiles;
+    const int inc = block_scan(here, warp_sum, all);
+    if (u >= u_lo && u < u_hi) {
+      UnitRec rec;
+      unit_record(p, seq, toks, g, t0, rows, rec);
+      rec.before = at = tiles + inc - here;
+      n = here;
       rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
       recs[u] = rec;
     }
     tiles += all;
   }
   const int per = max(1, (tiles + p.clusters - 1) / p.clusters);
-  if (tid == 0) p.ws_head[0] = make_int4(tiles, per, units, 0);
+  if (blockIdx.x == 0 && tid == 0) p.ws_head[0] = make_int4(tiles, per, units, 0);
   __syncthreads();
   // The unit of each cluster's first tile.
-  for (int u = tid; u < units; u += kPlanThreads) {
-    if (units > kPlanThreads) {
+  for (int u = tid; u < u_hi; u += kPlanThreads) {
+    if (u < u_lo) continue;
+    if (share > kPlanThreads) {  // (else this thread's only unit)
       at = recs[u].before;
       n = recs[u].tiles;
     }
@@ -1203,7 +1218,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 //   o = sum_s W_s o_s / L,  L = sum_s W_s,  lse = (M + log2 L) ln 2.
 
 constexpr int kMergeHeads = 8;
-constexpr int kMergeAhead = 4;
+constexpr int kMergeAhead = 2;
 
 __global__ void __launch_bounds__(32 * kMergeHeads) tree_merge_kernel(const TreeAttnParams p) {
   grid_launch_dependents();
@@ -1293,7 +1308,8 @@ cudaError_t launch(const void *f, const TreeAttnParams &p, int grid, int threads
 }  // namespace
 
 cudaError_t launch_tree_attn(const TreeAttnParams &p, bool e4m3, cudaStream_t s) {
-  cudaError_t e = launch((const void *)tree_plan_kernel, p, 1, kPlanThreads, 0, 1, s);
+  const int plan_blocks = p.max_units <= kPlanUnits * kPlanBlocks ? (p.max_units + kPlanUnits - 1) / kPlanUnits : kPlanBlocks;
+  cudaError_t e = launch((const void *)tree_plan_kernel, p, plan_blocks, kPlanThreads, 0, 1, s);
   if (e == cudaSuccess)
     e = launch(e4m3 ? (const void *)tree_attn_kernel<true> : (const void *)tree_attn_kernel<false>, p, 2 * p.clusters,
                kTreeThreads, kTreeSmem, 2, s);
