@@ -673,24 +673,36 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
           bytes = (e & (is_v ? kNoRowT | kNoValue : kNoRowT)) ? 0u : 16u;
           return reinterpret_cast<const uint8_t *>(e & ~15ull) + (is_v ? to_v : 0) + byte;
         };
-        auto by_tma = [&](int row) { return ((here >> ((row >> shift) & 31)) & 1u) != 0; };
-        uint32_t n;
-        if (FP8) {
-          const int per_row = is_v ? 3 : 2;
-#pragma unroll 4
-          for (int k = lane; k < 512; k += 32) {
-            const int row = k >> per_row;
-            if (by_tma(row)) continue;
-            const uint8_t *src = src_of(row, dim0 + 16 * (k & ((1 << per_row) - 1)), n);
-            cp_async16z(slot + 16 * k, src, n);
+        // By eight rows, bit u: rows 8 u ..
+        uint32_t todo = ~here & all;
+        if (gathered) {
+          todo = 0xffffffffu >> (32 - rows / 8);
+        } else if (shift == 4) {  // 16 rows a grain
+          todo = (todo | todo << 4) & 0x0f0f;
+          todo = (todo | todo << 2) & 0x3333;
+          todo = (todo | todo << 1) & 0x5555;
+          todo |= todo << 1;
+        }
+        const int c8 = lane & 7;
+#pragma unroll 1
+        for (; todo != 0; todo &= todo - 1) {
+          const int row = 8 * (__ffs(todo) - 1) + (lane >> 3);
+          uint32_t n;
+          if (FP8 && !is_v) {
+            const int at_row = row - (lane >> 3) + (lane >> 2), byte = 16 * (lane & 3);
+            const uint8_t *src = src_of(at_row, dim0 + byte, n);
+            cp_async16z(slot + 64 * at_row + byte, src, n);
+            continue;
           }
-        } else {
-          const int c8 = lane & 7;
-#pragma unroll 4
-          for (int row = lane >> 3; row < rows; row += 4) {
-            if (by_tma(row)) continue;
-            const uint8_t *src = src_of(row, 2 * dim0 + 16 * c8, n);
-            const uint32_t dst = slot + (row >> 3) * (is_v ? 2048 : 1024) + (row & 7) * 128 + ((c8 ^ (row & 7)) << 4);
+#pragma unroll
+          for (int k = 0; k < 8; k += 4) {
+            const uint8_t *src = src_of(row + k, (FP8 ? 1 : 2) * dim0 + 16 * c8, n);
+            if (FP8) {
+              cp_async16z(slot + 128 * (row + k) + 16 * c8, src, n);
+              continue;
+            }
+            const int in8 = (row + k) & 7;
+            const uint32_t dst = slot + (row >> 3) * (is_v ? 2048 : 1024) + in8 * 128 + ((c8 ^ in8) << 4);
             cp_async16z(dst, src, n);
             if (is_v) cp_async16z(dst + 1024, src + 128, n);
           }
