@@ -520,7 +520,6 @@ ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout
   p.scale_log2 = shape->scale * kLog2e;
   p.o = static_cast<__half *>(X->o);
   p.o_stride = X->o_tok_stride / 2;
-  p.o_wide = aligned(X->o, 32) && X->o_tok_stride % 32 == 0;
   p.lse = X->lse;
   st = ds4a::host_encode_q(&p.tm_q, X->q, n_tok, X->q_tok_stride);
   if (st != DS4A_OK) return st;

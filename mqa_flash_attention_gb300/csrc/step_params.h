@@ -63,7 +63,6 @@ struct TreeAttnParams {
   float scale_log2;
   __half *o;
   long long o_stride;      // elements
-  int o_wide;              // o and its stride are 32-byte aligned: 32-byte stores
   float *lse;
   int clusters, max_units;
   // Workspace.

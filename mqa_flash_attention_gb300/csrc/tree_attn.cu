@@ -907,10 +907,58 @@ __device__ __forceinline__ void tree_mma_role(int nt, uint32_t sbase, uint32_t t
 constexpr float kLiftT = 10.f, kHoldT = 5.f;
 constexpr float kNoRefT = -3e38f;
 
-__device__ __forceinline__ void stg32(void *at, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// This lane's 128 columns of TMEM, times inv (none: zeros), as fp16 (whole) or fp32 to
+// the output: 128 bytes of every head at a time, turned in the warp's own rows of P,
+// which is free then, so that eight lanes store a head's (`at`: the lane's first).
+// Stores of a head per lane took 3,500 cycles. 
+__device__ __forceinline__ void take_output(uint32_t cols, uint32_t prow, float inv, bool none, bool whole, uint8_t *at) {
+  int l = threadIdx.x & 31;
+  asm volatile("" : "+r"(l), "+r"(prow), "+r"(cols));  // nothing of this is kept in registers from tile to tile
+  const uint32_t wrow = prow - (l >> 3) * 1024 - (l & 7) * 128;  // of the warp's first head
+  const int n = whole ? 4 : 2;                                   // times 16 dims in 128 bytes
+#pragma unroll 1
+  for (int c = 0; c < 8 / n; ++c) {
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+      float o[16];
+      tmem_ld16(cols + 16 * (n * c + k), o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = none ? 0.f : o[i] * inv;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 v = __floats2half2_rn(o[8 * i + 2 * e], o[8 * i + 2 * e + 1]);
+            y[e] = *reinterpret_cast<const uint32_t *>(&v);
+          }
+          sts_v4(prow + (((2 * k + i) ^ (l & 7)) << 4), y[0], y[1], y[2], y[3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sts_v4(prow + (((4 * k + i) ^ (l & 7)) << 4), __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                 __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+      }
+    }
+    __syncwarp();
+    if (at != nullptr) {
+      uint4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int in8 = 4 * (k & 1) + (l >> 3);  // row within eight heads
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
+                     : "r"(wrow + (k >> 1) * 1024 + in8 * 128 + (((l & 7) ^ in8) << 4)));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4 *>(at + 128 * c + 16 * (l & 7) + k * 4 * kD * (whole ? 2 : 4)) = x[k];
+    }
+    __syncwarp();
+  }
 }
 
 // Warp w: TMEM lanes 32 (w & 3) .., that is heads 32 (w & 1) .. and rows 128 of
@@ -941,47 +989,19 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
   bool pending = false, none = false, whole = false;
   float inv = 0.f;
   int out_tok = -1;
-  long long slot = 0;
-  auto drain = [&]() {
+  int slot = 0;
+  auto drain = [&](uint32_t tile) {  // ahead of this tile's P
     pending = false;
     wait(ms.o_full[hh], n_item & 1, TSITE_O_FULL);
+    wait(ms.p_empty[box], (tile & 1) ^ 1, TSITE_P_EMPTY);
     ++n_item;
     tc_fence_after();
-    const int dim0 = 256 * hh + 128 * half;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      float o[32];
-      tmem_ld32(tmem + 128 * hh + 32 * c + lanes, o);
-      tmem_wait_ld();
-      if (out_tok < 0 || bad) continue;
-      if (whole) {
-        __half *at = p.o + out_tok * p.o_stride + (long long)h * kD + dim0 + 32 * c;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const __half2 v = none ? __half2{} : __floats2half2_rn(o[16 * k + 2 * i] * inv, o[16 * k + 2 * i + 1] * inv);
-            x[i] = *reinterpret_cast<const uint32_t *>(&v);
-          }
-          if (p.o_wide) {
-            stg32(at + 16 * k, x);
-          } else {
-            reinterpret_cast<uint4 *>(at + 16 * k)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-            reinterpret_cast<uint4 *>(at + 16 * k)[1] = make_uint4(x[4], x[5], x[6], x[7]);
-          }
-        }
-      } else {
-        float *at = p.ws_o + (slot * kH + h) * kD + dim0 + 32 * c;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = none ? 0u : __float_as_uint(o[8 * k + i] * inv);
-          stg32(at + 8 * k, x);
-        }
-      }
-    }
+    const int dim0 = 256 * hh + 128 * half, row0 = 32 * (q & 1) + (l >> 3);
+    uint8_t *at = nullptr;
+    if (out_tok >= 0 && !bad)
+      at = whole ? reinterpret_cast<uint8_t *>(p.o + out_tok * p.o_stride + (long long)row0 * kD + dim0)
+                 : reinterpret_cast<uint8_t *>(p.ws_o + ((long long)slot * kH + row0) * kD + dim0);
+    take_output(tmem + 128 * hh + lanes, smem_u32(prow), inv, none, whole, at);
     tc_fence_before();
     tell(ms.o_empty);
   };
@@ -1070,7 +1090,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     }
     lsum += (part[0] + part[1]) + (part[2] + part[3]);
     if (FP8) warp_arrive(smem_u32(&ms.list_empty[buf]));
-    if (pending) drain();
+    if (pending) drain(g);
     if (moved && !(flags & TF_FIRST)) {
       // O under the new reference, once the products so far have gone into it (those
       // of the last box complete last), and before any of this tile does.
@@ -1110,7 +1130,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     inv = spoiled ? __int_as_float(0x7FC00000) : none ? 0.f : 1.f / sum;
     whole = flags & TF_WHOLE;
     out_tok = tok;
-    slot = 2ll * (2 * cluster + (flags & TF_HEAD ? 1 : 0)) + rank;
+    slot = 2 * (2 * cluster + (flags & TF_HEAD ? 1 : 0)) + rank;
     if (box == 0 && tok >= 0) {
       if (!whole)
         p.ws_ml[slot * kH + h] = make_float2(none ? -INFINITY : m_ref, sum);
@@ -1120,7 +1140,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     pending = true;
     bar_sync_id(group, 128);  // the sums have been read
   }
-  if (pending && !bad) drain();
+  if (pending && !bad) drain(nt);
 }
 
 // ------------------------------------------------------------------ kernel
