@@ -27,11 +27,26 @@
 // The tiles of all units are numbered through, and each cluster takes the same
 // number of them in a row: whole units, and parts of the first and the last.  A
 // part leaves its normalised output (fp32) and (m, l) in one of its cluster's two
-// slots; a merge joins them.  Lengths are only known on the device: a one-block
-// kernel counts the tiles first.
+// slots; a merge joins them.  Lengths are only known on the device: a small kernel
+// counts the tiles first and writes down what each unit sees.
 //
-// Rows are found through the page tables.  Rows of a tile that neither token
-// sees are zero-filled, those that one sees are masked for the other.
+// Rows are found through the page tables.  Where all pages are whole grains of 8 or
+// 16 rows, TMA brings K by grains and V by the grains of which every row is seen (in
+// runs of up to 64 rows where a tile is seen in full); other rows of V, and all rows
+// of other page sizes, are copied one by one, zeros in place of those that neither
+// token sees.  What one of the two sees is masked for the other.
+//
+// What bounds it (GB300; the rates are this card's own, a cuBLAS product of bf16 at
+// 1,878 TFLOP/s, at 1,702 where it runs for seconds under the power cap).  2,048 new
+// tokens over 7,680 compressed rows: 1,325 us, 1,633 TFLOP/s, and 1,500 us under the
+// power cap (clocks fall from 2,070 to 1,630 MHz).  A tile takes 6,200 cycles, of
+// which the tensor core works 4,096, shared memory 5,100, and the warp that issues
+// Q . K with its three stages all 6,200 (690 a part).  E4M3 rows: 9,500 cycles, 7,250 of
+// them shared memory (each row is read as codes and written as values again); a slot
+// of codes comes round in 3,300 and there is room for three.  Short lists (2,900
+// tokens of 330 rows each in two tiles): 211 us; a tile takes 11,000 cycles, because
+// an item's output has to leave TMEM before the next one's products.  Few tokens (8
+// over 386 rows): 23 us, three launches and their round trips.
 #include "attn_params.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -54,20 +69,26 @@ constexpr uint32_t kTmemTS = 256;           // S buffers at columns 256 and 384
 constexpr int kListsT = 3;
 
 // K and V come through rings of their own, because their products are issued by
-// warps of their own.  fp16 rows: three stages of K and four of V.  E4M3 rows:
-// codes land in three slots for each and are widened into two stages for each.
+// warps of their own.  fp16 rows: three stages of K and four of V (four and three: 1,530
+// against 1,449 us for 2,048 tokens when it was measured).  E4M3 rows: codes land in three
+// slots for each and are widened into two stages for each (two slots and a third
+// stage for K or V: 303 to 306 us against 301).
 template <bool FP8>
 constexpr int kKStages = FP8 ? 2 : 3;
 template <bool FP8>
 constexpr int kVStages = FP8 ? 2 : 4;
 constexpr int kCodeSlots = 3;
 static_assert(7 * kPart <= kRingBytes && 4 * kPart + 2 * kCodeSlots * kCodePart <= kRingBytes, "shared memory of the rings");
-// Warps 0-7 softmax and epilogue; 13 finds the rows of the tiles; 14 issues P . V, 15
-// Q . K (in the CTA of rank 1 they report what has landed).  8-9 load K and 16-19 V
-// (E4M3: 8 loads K and 11 V, 9-10 widen K and 16-19 V); 10-12 (12) are idle, because
-// registers go to four warps at a time.  Every role is a loop over the tiles that
-// meets the others at mbarriers only, and its code is kept small: what all roles run
-// through in a tile has to stay in the instruction cache.
+// Warps 0-7 softmax and epilogue; 13 finds the rows of the tiles; 12 and 14 issue P . V,
+// a half of each 256 dims each, and 15 Q . K (in the CTA of rank 1 they report what has
+// landed).  8-9 load K and 16-19 V (E4M3: 8 loads K and 11 V, 9-10 widen K and 16-19 V);
+// 10-11 are idle with fp16 rows, because registers go to four warps at a time.  Every
+// role is a loop over the tiles that meets the others at mbarriers only, and its code is
+// kept small: what all roles run through in a tile has to stay in the instruction cache
+// (128 KB on an SM).  What the numbers of warps are worth: two
+// that issue P . V instead of one 1,446 -> 1,355 us (2,048 tokens), a third for K 1,449 ->
+// 1,480; four that load V instead of two 329 -> 276 us (short lists); four that widen V
+// instead of one 326 -> 301 us (E4M3).
 constexpr int kTreeThreads = 640;
 constexpr int kKLoadWarp0 = 8, kPvWarp1 = 12, kListWarp = 13, kPvWarp0 = 14, kQkWarp = 15;
 constexpr int kWidenK0 = 9, kWidenV0 = 16, kWidenKWarps = 2, kWidenVWarps = 4;
@@ -816,9 +837,10 @@ __device__ __forceinline__ void tree_relay_role(int nt, TMisc &ms, bool is_v, ui
   }
 }
 
-// Two warps issue, Q . K and P . V, each the products of its own ring: the wait for a
-// stage, the issue and the commits take a warp some 400 cycles a stage, its MMAs
-// 256; one warp for both took 6,400 cycles a tile.  The whole warp walks the tiles, so that
+// Three warps issue, Q . K and the halves of P . V, each from its own stages: the wait for
+// a stage, the issue and the commits take a warp some 650 cycles a part, its MMAs 256.
+// (The halves go to columns of their own, so that their order does not matter; all parts
+// of Q . K go into one sum.)  The whole warp walks the tiles, so that
 // descriptors are warp-uniform values, and one elected lane issues.  Waits are
 // joined over the warp: all lanes go on or none.
 template <bool FP8, bool IS_V>
