@@ -562,14 +562,28 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
       }
     }
     if (FP8) {
+      uint32_t odd = 0;  // V scales that are not finite, by k
 #pragma unroll
       for (int k = 0; k < (FP8 ? 8 : 1); ++k) {
         const int x = 32 * k + lane;
         const float kk = p.grain > 0 ? ks[k] : ms.ksc[buf][x], vv = p.grain > 0 ? vs[k] : ms.lvs[buf][x];
+        odd |= (__float_as_uint(vv) & 0x7F800000u) == 0x7F800000u ? 1u << k : 0;
         ms.ksc[buf][x] = p.scale_log2 * kk;
         const float lv = fmaxf(__log2f(vv), kLeastLog2ScaleT);
         ms.lvs[buf][x] = lv;
         ms.ivs[buf][x] = exp2f(-lv);
+      }
+      if (__any_sync(0xffffffffu, odd != 0)) {
+        // Such a row spoils who sees it; its weight counts all the same.
+#pragma unroll 1
+        for (int k = 0; k < kRows / 32; ++k) {
+          const unsigned see = __shfl_sync(0xffffffffu, rank == 0 ? see0 : see1, k);
+          if (((odd >> k) & 1u) == 0) continue;
+          spoiled = spoiled || ((see >> lane) & 1u) != 0;
+          ms.lvs[buf][32 * k + lane] = 0.f;
+          ms.ivs[buf][32 * k + lane] = 1.f;
+        }
+        spoiled = __any_sync(0xffffffffu, spoiled);
       }
     }
     const bool head = g == 0 || j == 0, last = j == r.tiles - 1 || left == 1;

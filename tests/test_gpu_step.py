@@ -391,6 +391,38 @@ def test_tree_bad_rows_spoil_their_tokens_only(torch, ds4a, f8, chain):
                 assert np.isfinite(lse[hit]).all()
 
 
+@pytest.mark.parametrize("page", [16, 7])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_tree_bad_scales_spoil_their_tokens_only(torch, ds4a, page, value):
+    """A scale that is not finite: of K, of V, of a new row that some see, of a compressed row that all see."""
+    rng = np.random.default_rng(33)
+    counts, ratio = [12, 40], 128
+    geom, first, parent, q, raw, comp = tree_case(rng, counts, [150, 300], ratio, page, True, False)
+    shape = shape_of(ratio)
+    want = step.attention(shape, geom, first, parent, q, raw, comp)
+    for which, b, node in (("v", 0, 4), ("v", 1, 9), ("v", 1, None), ("k", 0, 5)):
+        mine = {n: {k: (None if x is None else x.copy()) for k, x in s.items()} for n, s in (("raw", raw), ("comp", comp))}
+        row = 30 if node is None else geom[b][1] + node
+        seg = mine["comp" if node is None else "raw"]
+        seg[which + "_scale"][seg["table"][b, row // page], row % page] = value
+        o, lse = run_tree(torch, ds4a, shape, geom, first, parent, q, rows_on(torch, ds4a, mine["raw"]),
+                          rows_on(torch, ds4a, mine["comp"]))
+        views = step.seen(shape, geom[b], parent, int(first[b]), counts[b], 1 << 20, 1 << 20)
+        hit = np.zeros(len(q), dtype=bool)
+        hit[first[b]:first[b + 1]] = [row in v[1 if node is None else 0] for v in views]
+        assert hit.any() and not hit.all()
+        check_tree(o[~hit], lse[~hit], tuple(x[~hit] for x in want))
+        if which == "k" and value == np.inf:  # a score of -inf is a weight of 0
+            dots = q[hit].astype(np.float64) @ fp8.decode_table()[seg["k"][seg["table"][b, row // page], row % page]]
+            assert (np.isnan(o[hit]).all(2) == (dots > 0)).all() and (dots > 0).any()
+            continue
+        assert np.isnan(o[hit]).all()
+        if which == "v":  # the weights are what they were
+            lse_ = lse.copy()
+            o[hit] = want[0][hit]
+            check_tree(o, lse_, want)
+
+
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("page", [16, 7])
 def test_tree_first_tile_without_rows(torch, ds4a, f8, page):
