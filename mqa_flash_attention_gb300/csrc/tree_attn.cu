@@ -99,8 +99,7 @@ constexpr int kKLoadWarps = FP8 ? 1 : 2;
 template <bool FP8>
 constexpr int kVLoadWarps = FP8 ? 1 : 4;
 
-constexpr float kLeastLog2ScaleT = -40.f;   // V scales below 2^-40 count as 0: such rows round to 0 in fp16
-constexpr float kMostScaleInv = 1.0995e12f;      // just below 2^40
+constexpr float kLeastLog2ScaleT = -40.f;  // V rows of a scale of 2^-40 or less count as 0: they round to 0 in fp16
 constexpr unsigned long long kSegBitT = 1, kNoRowT = 2, kNoValue = 4;  // low bits of a list entry
 
 // Of a tile within its item (the cluster's tiles of one unit); how its rows come; and
@@ -488,7 +487,16 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
       }
     }
     if (lane < kRows / 32) ms.mask[buf][lane] = rank == 0 ? see0 : see1;
-    unsigned parts = 15;
+    unsigned parts = 15, bad_of = 0;  // rows whose V is left out of the product
+    if (FP8) {
+#pragma unroll
+      for (int k = 0; k < (FP8 ? 8 : 1); ++k) {
+        const float vv = p.grain > 0 ? vs[k] : ms.lvs[buf][32 * k + lane];
+        const unsigned tiny = __ballot_sync(0xffffffffu, !(__log2f(vv) > kLeastLog2ScaleT));
+        if (lane == k) bad_of = tiny;
+        full = full && tiny == 0;
+      }
+    }
     if (!full) {
       const unsigned some = __ballot_sync(0xffffffffu, lane < kRows / 32 && (see0 | see1) != 0);
       parts = 0;
@@ -498,7 +506,7 @@ __device__ __forceinline__ void tree_list_role(const TreeAttnParams &p, int nt, 
       // its weight of 0 multiplies it all the same: the warp looks these few rows
       // through (new rows, edges of a window), eight lanes to a row.  One that is
       // not finite is left out of the product, and the token that sees it is marked.
-      unsigned one = lane < kRows / 32 ? see0 ^ see1 : 0, bad_of = 0;
+      unsigned one = lane < kRows / 32 ? see0 ^ see1 : 0;
       int n_one = 0;
 #pragma unroll 1
       for (unsigned words = __ballot_sync(0xffffffffu, one != 0); words != 0; words &= words - 1) {
@@ -1112,13 +1120,10 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       const float e0 = exp2f(s[2 * i] - m_ref), e1 = exp2f(s[2 * i + 1] - m_ref);
-      __half2 hp = __floats2half2_rn(e0, e1);
+      const __half2 hp = __floats2half2_rn(e0, e1);
       if (FP8) {
         const float2 iv = *reinterpret_cast<const float2 *>(&ms.ivs[buf][64 * box + 2 * i]);
-        part[i & 3] = fmaf(e0, iv.x, fmaf(e1, iv.y, part[i & 3]));
-        // A V scale of 0: weight, but no value.
-        if (iv.x >= kMostScaleInv || iv.y >= kMostScaleInv)
-          hp = __floats2half2_rn(iv.x >= kMostScaleInv ? 0.f : e0, iv.y >= kMostScaleInv ? 0.f : e1);
+        part[i & 3] = fmaf(e0, iv.x, fmaf(e1, iv.y, part[i & 3]));  // (a V scale of 0: weight, but no value)
       } else {
         part[i & 3] += e0 + e1;
       }

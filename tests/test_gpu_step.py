@@ -467,6 +467,22 @@ def test_tree_e4m3_scales_of_any_size(torch, ds4a, exponent):
     check_tree(*got, want)
 
 
+@pytest.mark.parametrize("page", [64, 8, 12])
+def test_tree_e4m3_value_scales_of_zero(torch, ds4a, page):
+    """Rows with weight and no value, whatever their codes, in tiles that are seen in full and at their edges."""
+    rng = np.random.default_rng(34)
+    geom, first, parent, q, raw, comp = tree_case(rng, [7, 12], [1100, 300], 4, page, True, False)
+    for seg, rows in ((raw, [g[1] + n for g, n in zip(geom, (7, 12))]), (comp, [1100, 300])):
+        for b, n in enumerate(rows):
+            gone = rng.random(n) < 0.1
+            gone[n // 2:n // 2 + 70] = True
+            for i in np.flatnonzero(gone):
+                seg["v_scale"][seg["table"][b, i // page], i % page] = rng.choice([0.0, 2.0 ** -60])
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
 @pytest.mark.parametrize("f8", [False, True])
 def test_tree_large_scores_move_the_reference(torch, ds4a, f8):
     """Scores that grow along the rows, by far more than an exponent holds."""
