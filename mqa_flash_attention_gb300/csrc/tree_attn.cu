@@ -38,15 +38,15 @@
 //
 // What bounds it (GB300; the rates are this card's own, a cuBLAS product of bf16 at
 // 1,878 TFLOP/s, at 1,702 where it runs for seconds under the power cap).  2,048 new
-// tokens over 7,680 compressed rows: 1,325 us, 1,633 TFLOP/s, and 1,500 us under the
+// tokens over 7,680 compressed rows: 1,320 us, 1,640 TFLOP/s, and 1,500 us under the
 // power cap (clocks fall from 2,070 to 1,630 MHz).  A tile takes 6,200 cycles, of
 // which the tensor core works 4,096, shared memory 5,100, and the warp that issues
-// Q . K with its three stages all 6,200 (690 a part).  E4M3 rows: 9,500 cycles, 7,250 of
+// Q . K with its three stages all 6,200 (690 a part).  E4M3 rows: 9,100 cycles, 7,250 of
 // them shared memory (each row is read as codes and written as values again); a slot
 // of codes comes round in 3,300 and there is room for three.  Short lists (2,900
 // tokens of 330 rows each in two tiles): 211 us; a tile takes 11,000 cycles, because
-// an item's output has to leave TMEM before the next one's products.  Few tokens (8
-// over 386 rows): 23 us, three launches and their round trips.
+// an item's output has to leave TMEM before the next one's products, all clusters' at
+// once (9.7 MB).  Few tokens (8 over 386 rows): 22.8 us, two launches and their round trips.
 #include "attn_params.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -337,6 +337,47 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tree_plan_kernel(const TreeAt
     }
     for (int i = (at + per - 1) / per; (long long)i * per < at + n; ++i) p.ws_start[i] = u;
   }
+}
+
+// Few sequences and units (one a lane of a warp): every CTA of the attention plans for
+// itself, which is a launch less (8 tokens of one sequence: 23.4 us with the kernel above,
+// 22.8 with this).  All write the same numbers to the workspace, each reads its own.
+// (Not inlined: where its code lay among the roles', E4M3 rows took 277 us, not 270.)
+__host__ __device__ __forceinline__ bool plans_itself(const TreeAttnParams &p) { return p.n_seq <= 32 && p.max_units <= 32; }
+
+static __device__ __noinline__ void plan_by_warp(const TreeAttnParams &p, int lane) {
+  auto sum_to = [&](int v) {  // over the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    return v;
+  };
+  const int ends = sum_to(lane < p.n_seq ? (tokens_of(p, lane).n + 1) / 2 : 0);  // units up to this sequence's last
+  const int units = min(__shfl_sync(0xffffffffu, ends, 31), p.max_units);
+  int seq = 0;  // the first whose units end behind this lane's
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1)
+    if (__shfl_sync(0xffffffffu, ends, seq + step - 1) <= lane) seq += step;
+  const int before = __shfl_sync(0xffffffffu, ends, max(seq - 1, 0));
+  UnitRec rec;
+  rec.tiles = 0;
+  if (lane < units) {
+    const Span2 toks = tokens_of(p, seq);
+    const int4 g = p.geom[seq];
+    const int t0 = 2 * (lane - (seq > 0 ? before : 0));
+    unit_record(p, seq, toks, g, t0, unit_rows(p, g, toks.n, t0, min(t0 + 1, toks.n - 1)), rec);
+  }
+  const int end = sum_to(rec.tiles), tiles = __shfl_sync(0xffffffffu, end, 31);
+  const int per = max(1, (tiles + p.clusters - 1) / p.clusters);
+  if (lane < units) {
+    rec.before = end - rec.tiles;
+    rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
+    static_cast<UnitRec *>(p.ws_unit)[lane] = rec;
+    for (int i = (rec.before + per - 1) / per; (long long)i * per < end; ++i) p.ws_start[i] = lane;
+  }
+  if (lane == 0) p.ws_head[0] = make_int4(tiles, per, units, 0);
 }
 
 // ------------------------------------------------------------------ lists
@@ -1243,7 +1284,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
   grid_launch_dependents();
-  grid_dependency_wait();  // the plan
+  grid_dependency_wait();  // the plan, or what the plan is made from
+  if (plans_itself(p)) {
+    if (warp == kListWarp) plan_by_warp(p, threadIdx.x & 31);
+    __syncthreads();
+  }
   const int4 head = p.ws_head[0];
   const long long before = (long long)cluster * head.y;
   const int nt = (int)max(0ll, min((long long)head.y, head.x - before));
@@ -1382,7 +1427,8 @@ cudaError_t launch(const void *f, const TreeAttnParams &p, int grid, int threads
 
 cudaError_t launch_tree_attn(const TreeAttnParams &p, bool e4m3, cudaStream_t s) {
   const int plan_blocks = p.max_units <= kPlanUnits * kPlanBlocks ? (p.max_units + kPlanUnits - 1) / kPlanUnits : kPlanBlocks;
-  cudaError_t e = launch((const void *)tree_plan_kernel, p, plan_blocks, kPlanThreads, 0, 1, s);
+  cudaError_t e = cudaSuccess;
+  if (!plans_itself(p)) e = launch((const void *)tree_plan_kernel, p, plan_blocks, kPlanThreads, 0, 1, s);
   if (e == cudaSuccess)
     e = launch(e4m3 ? (const void *)tree_attn_kernel<true> : (const void *)tree_attn_kernel<false>, p, 2 * p.clusters,
                kTreeThreads, kTreeSmem, 2, s);
