@@ -58,7 +58,8 @@ namespace ds4a {
 namespace {
 
 constexpr int kRows = 256;                  // of a tile
-constexpr uint32_t kPart = 16384;           // a stage (a tile has 8 of K, 8 of V): 64 dims of 128 K rows, or 128 dims of 64 V rows
+// A stage (a tile has 8 of K, 8 of V): 64 dims of 128 K rows, or 128 dims of 64 V rows.
+constexpr uint32_t kPart = 16384;
 constexpr uint32_t kCodePart = kPart / 2;
 constexpr uint32_t kOffTP = kQBytes;        // P: 4 boxes [64 heads][64 rows]
 constexpr uint32_t kPBox = 8192;
@@ -729,7 +730,8 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
         // barrier (of K, each has rows of its own), rank 1's has the issue only.
         if (lane == 0) {
           const uint32_t count = FP8 ? __popc(here) : is_v ? 2 * __popc(here) : __popc(grains);
-          if (count != 0 && (FP8 || rank == 0)) mbar_expect_tx(b_full, (count << shift) * (is_v ? 256u : 128u) / (FP8 ? 2u : 1u));
+          if (count != 0 && (FP8 || rank == 0))
+            mbar_expect_tx(b_full, (count << shift) * (is_v ? 256u : 128u) / (FP8 ? 2u : 1u));
           if (!by_rows) mbar_arrive_cnt(b_full, 32);
         }
         const int row = lane << unit;  // within the part
@@ -833,7 +835,8 @@ __device__ __forceinline__ void tree_widen_role(int nt, uint32_t sbase, TMisc &m
   for (int i = 0; i < 8 * nt; ++i) {
     if (IS_V && (i & 7) == 0) {
       const int g = i >> 3, buf = g % kListsT;
-      if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait))) return;
+      if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ms.list_full[buf]), (g / kListsT) & 1, TSITE_LIST_FULL, &ms.wait)))
+        return;
       parts = ms.flags[buf] >> TF_PARTS;
       warp_arrive(smem_u32(&ms.list_empty[buf]));
     }
@@ -995,7 +998,7 @@ constexpr float kNoRefT = -3e38f;
 // This lane's 128 columns of TMEM, times inv (none: zeros), as fp16 (whole) or fp32 to
 // the output: 128 bytes of every head at a time, turned in the warp's own rows of P,
 // which is free then, so that eight lanes store a head's (`at`: the lane's first).
-// Stores of a head per lane took 3,500 cycles. 
+// (Stores of a head per lane: short lists took 229.6 us, so 211.6.)
 __device__ __forceinline__ void take_output(uint32_t cols, uint32_t prow, float inv, bool none, bool whole, uint8_t *at) {
   int l = threadIdx.x & 31;
   asm volatile("" : "+r"(l), "+r"(prow), "+r"(cols));  // nothing of this is kept in registers from tile to tile
@@ -1317,7 +1320,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     tree_widen_role<true>(nt, sbase, ms, threadIdx.x - 32 * kWidenV0);
   } else if (FP8 && warp >= kWidenK0 && warp < kWidenK0 + kWidenKWarps) {
     tree_widen_role<false>(nt, sbase, ms, threadIdx.x - 32 * kWidenK0);
-  } else if (warp < kKLoadWarp0 + kKLoadWarps<FP8> || (warp >= kVLoadWarp0<FP8> && warp < kVLoadWarp0<FP8> + kVLoadWarps<FP8>)) {
+  } else if (warp < kKLoadWarp0 + kKLoadWarps<FP8> ||
+             (warp >= kVLoadWarp0<FP8> && warp < kVLoadWarp0<FP8> + kVLoadWarps<FP8>)) {
     const bool is_v = warp >= kVLoadWarp0<FP8>;
     tree_load_role<FP8>(p, nt, rank, sbase, ms, is_v, threadIdx.x - 32 * (is_v ? kVLoadWarp0<FP8> : kKLoadWarp0));
   }
