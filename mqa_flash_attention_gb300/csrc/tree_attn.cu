@@ -1207,6 +1207,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
 
     // End of an item: the sum over a head's four threads.  Its output is taken from
     // TMEM behind the next tile's weights, while the last products run.
+    if (moved && (flags & TF_FIRST)) bar_sync_id(group, 128);  // the maxima have been read: nothing since then met
     ms.red[box][h] = lsum;
     if (bar_red_or(group, 128, bad)) break;
     const float sum = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);

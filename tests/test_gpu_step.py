@@ -524,6 +524,27 @@ def test_tree_of_a_long_tail_under_one_row(torch, ds4a, below):
     check_tree(*got, want)
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_tree_units_of_a_single_tile(torch, ds4a, f8):
+    """Items that are one tile each, many to a pair of SMs: a head's maximum and its sum, of sizes far apart between
+    heads, pass between the same four warps with nothing else in between.  Every call gives the oracle's values."""
+    rng = np.random.default_rng(34)
+    counts = [int(x) for x in rng.integers(1, 5, 260)]
+    rows = [int(x) for x in rng.integers(0, 100, 260)]
+    geom, first, parent, q, raw, comp = tree_case(rng, counts, rows, 128, 16, f8, True, window=64)
+    q = (q.astype(np.float32) * np.geomspace(0.1, 10, H)[rng.permutation(H)][None, :, None]).astype(np.float16)
+    shape = shape_of(128, 64)
+    want = step.attention(shape, geom, first, parent, q, raw, comp)
+    assert (want[4] + 64 <= 256).all()  # one tile to a unit
+    i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    args = (shape, i32(geom), i32(first), up(torch, q), rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    o, lse = ds4a.attn_tree_paged(*args, parent=i32(parent), want_lse=True)
+    check_tree(host(o), host(lse), want)
+    for _ in range(200):
+        again = ds4a.attn_tree_paged(*args, parent=i32(parent), want_lse=True)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
 def test_tree_of_single_tokens_is_the_decode(torch, ds4a):
     """One new token per sequence: the decode's result, its own row counted among the raw ones."""
     rng = np.random.default_rng(30)
