@@ -77,7 +77,7 @@ def branch(text, at):
 def holds(cond, first, last, moved):
     if "top > m_lim" in cond:
         return moved
-    if EVENTS.search(cond):
+    if cond == "bad" or EVENTS.search(cond):
         return False  # a vote that some wait ran out
     code = re.sub(r"\(?flags & TF_(FIRST|LAST)\)?", lambda m: m.group(1).lower(), cond)
     code = code.replace("&&", " and ").replace("||", " or ").replace("!", " not ")
@@ -131,3 +131,13 @@ def test_shared_numbers_are_read_before_they_are_written_again():
                     assert not unread, f"a warp may read what another has not written: {tiles}"
                     unmet = True
                 assert e != "leave"
+
+
+def test_threads_leave_the_tiles_together():
+    """When a wait has run out in some threads, all of the group have to know before they leave: those that did not
+    would go on to take an output, in steps that need whole warps, and wait there without end."""
+    body = tile_body()
+    ways_out = [m.start() for m in re.finditer(r"\bbreak;", body)]
+    assert len(ways_out) == 2
+    for at in ways_out:
+        assert re.search(r"bad = bar_red_or\(group, 128, bad\);\s*if \(bad\) $", body[:at]), body[at - 80:at]
