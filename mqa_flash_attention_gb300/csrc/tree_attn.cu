@@ -1145,8 +1145,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     if (bar_red_or(group, 128, top > m_lim || bad)) {
       // Some head's reference moves: the tile's maximum over a head's four threads.
       ms.red[box][h] = top;
-      bad = bar_red_or(group, 128, bad);  // of any thread: all leave, and none takes an output behind the loop
-      if (bad) break;
+      if (bar_red_or(group, 128, bad)) break;
       const float tmax = fmaxf(fmaxf(ms.red[0][h], ms.red[1][h]), fmaxf(ms.red[2][h], ms.red[3][h]));
       if (tmax > m_lim) {
         // Rounded so that P stays within 2^15 where scores are 16 and more apart.
@@ -1210,8 +1209,7 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     // TMEM behind the next tile's weights, while the last products run.
     if (moved && (flags & TF_FIRST)) bar_sync_id(group, 128);  // the maxima have been read: nothing since then met
     ms.red[box][h] = lsum;
-    bad = bar_red_or(group, 128, bad);
-    if (bad) break;
+    if (bar_red_or(group, 128, bad)) break;
     const float sum = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
     // No weight at all: o = 0.  (A sum that is NaN is not that: it stays.)
     none = sum == 0.f;
@@ -1228,7 +1226,8 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
     pending = true;
     bar_sync_id(group, 128);  // the sums have been read
   }
-  if (pending && !bad) drain(nt);
+  // All or none: an output is taken in steps that need whole warps.
+  if (pending && !bar_red_or(group, 128, bad)) drain(nt);
 }
 
 // ------------------------------------------------------------------ kernel

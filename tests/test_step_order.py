@@ -134,10 +134,12 @@ def test_shared_numbers_are_read_before_they_are_written_again():
 
 
 def test_threads_leave_the_tiles_together():
-    """When a wait has run out in some threads, all of the group have to know before they leave: those that did not
-    would go on to take an output, in steps that need whole warps, and wait there without end."""
-    body = tile_body()
-    ways_out = [m.start() for m in re.finditer(r"\bbreak;", body)]
-    assert len(ways_out) == 2
-    for at in ways_out:
-        assert re.search(r"bad = bar_red_or\(group, 128, bad\);\s*if \(bad\) $", body[:at]), body[at - 80:at]
+    """When a wait has run out in some threads, all of the group have to know before an output is taken behind the
+    loop: those that did not would do so in steps that need whole warps, and wait there without end."""
+    with open(SOURCE) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    body, role = tile_body(), text[text.index("void tree_softmax_role("):]
+    for m in re.finditer(r"\bbreak;", body):  # all leave the loop at once
+        assert body[:m.start()].endswith("if (bar_red_or(group, 128, bad)) ")
+    behind = role[role.index(body) + len(body):]
+    assert re.match(r"\s*\}\s*if \(pending && !bar_red_or\(group, 128, bad\)\) drain\(nt\);\s*\}", behind)
