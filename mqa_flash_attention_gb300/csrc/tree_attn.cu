@@ -696,7 +696,7 @@ __device__ __forceinline__ void tree_load_role(const TreeAttnParams &p, int nt, 
         }
       }
       ++n_item;
-      __syncwarp();
+      if (__any_sync(0xffffffffu, !ok)) break;  // all lanes leave, or the votes below would miss one
     }
     // Grains that TMA brings (by runs of several where all are whole).
     const bool full = flags & TF_FULL, gathered = flags & TF_GATHERED;

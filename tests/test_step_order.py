@@ -143,3 +143,18 @@ def test_threads_leave_the_tiles_together():
         assert body[:m.start()].endswith("if (bar_red_or(group, 128, bad)) ")
     behind = role[role.index(body) + len(body):]
     assert re.match(r"\s*\}\s*if \(pending && !bar_red_or\(group, 128, bad\)\) drain\(nt\);\s*\}", behind)
+
+
+def test_a_loader_leaves_with_all_its_lanes():
+    """One lane of a loader waits for Q's buffer.  Its warp votes in every later wait: if that lane gave up alone, the
+    others would wait for it without end."""
+    with open(SOURCE) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    role = text[text.index("void tree_load_role("):text.index("void tree_widen_role(")]
+    loop = role[role.index("for (int g = 0; g < nt && ok; ++g) {"):]
+    alone = [m.start() for m in re.finditer(r"ok = false;", loop[:closing(loop, loop.index("{"), "{}")])]
+    assert len(alone) == 2
+    q_wait, kv_wait = alone
+    assert re.match(r"[^$]*?if \(__any_sync\(0xffffffffu, !ok\)\) break;", loop[q_wait:loop.index("for (int c = 0;")])
+    # Already a vote's result.
+    assert re.search(r"if \(!__all_sync\(0xffffffffu, wait_phase\([^{]*\{\s*$", loop[:kv_wait])
