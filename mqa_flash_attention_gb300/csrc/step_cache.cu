@@ -413,7 +413,7 @@ cudaError_t launch_page_tables(const PageTablesParams &p, cudaStream_t s) {
   const cudaError_t e = launch_pdl(page_lists_kernel, 1, kListThreads, s, p);
   if (e != cudaSuccess) return e;
   const int per = kFillThreads * kFillSlots;
-  return launch_pdl(page_fill_kernel, (unsigned)(p.n_seq + (p.n_slots + per - 1) / per), kFillThreads, s, p);
+  return launch_pdl(page_fill_kernel, (unsigned)(p.n_seq + ((long long)p.n_slots + per - 1) / per), kFillThreads, s, p);
 }
 
 cudaError_t launch_accept(const AcceptParams &p, cudaStream_t s) {

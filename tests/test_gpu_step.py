@@ -111,6 +111,22 @@ def test_page_tables_take_and_give_back(torch, ds4a):
         assert np.array_equal(np.sort(np.concatenate([held, f])), np.arange(n_pages))
 
 
+def test_page_tables_of_the_most_slots(torch, ds4a):
+    """As many slots as a 32-bit count names (8.6 GB of them): the blocks that fill them are counted in 64 bits."""
+    c = (np.array([3, 0]), np.array([20, 5]), None, np.array([[0, -1, -1], [-1, -1, -1]], dtype=np.int32),
+         np.array([1, 2, 3, 4, 0], dtype=np.int32), 4, 5)
+    table, free = c[3].copy(), c[4].tolist()
+    want = step.page_tables(table, free, c[5], c[0], c[1], None, 8, c[6], 30)
+    i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    slots = torch.empty(2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    slots[-2000:] = 7
+    t, f, nf = i32(c[3]), i32(c[4]), i32([c[5]])
+    _, first, short = ds4a.page_tables(t, f, nf, i32(c[0]), i32(c[1]), 8, slots=slots)
+    assert np.array_equal(host(t), table) and np.array_equal(host(f), free) and int(nf) == want[0]
+    assert np.array_equal(host(slots[:30]), want[1]) and host(first).tolist() == want[2].tolist() and int(short) == want[3]
+    assert all(bool((part == -1).all()) for part in slots[22:].split(1 << 28))
+
+
 # ------------------------------------------------------------------ acceptance
 
 def tree_of(rng, n, chain, wide=8):
