@@ -81,6 +81,20 @@ bool table_ok(const ds4a_paged_rows *r) {
   return (int64_t)r->max_pages * r->page_rows <= kMostRows;
 }
 
+// The pools, scales and table of a segment with rows.
+constexpr int kSegSpans = 5;
+int seg_spans(const ds4a_paged_rows *r, int32_t n_seq, Span *out) {
+  const bool e4m3 = r->k_scale != nullptr;
+  const int64_t page = (int64_t)(r->page_rows - 1) * r->row_stride + (e4m3 ? DS4A_HEAD_DIM : DS4A_ROW_BYTES);
+  const int64_t scales = 4LL * r->page_rows;
+  int n = 0;
+  for (const void *pool : {r->k, r->v}) out[n++] = span(pool, r->n_pages, r->page_stride, page);
+  if (e4m3)
+    for (const float *scale : {r->k_scale, r->v_scale}) out[n++] = span(scale, r->n_pages, scales, scales);
+  out[n++] = span(r->table, n_seq, r->table_stride, 4LL * r->max_pages);
+  return n;
+}
+
 // The exponent of a power of two, -1 otherwise.
 int log2_of(int n) {
   for (int i = 0; i < 31; ++i)
@@ -491,13 +505,16 @@ ds4a_status ds4a_attn_tree_paged(int32_t n_seq, int32_t n_tok, const ds4a_layout
     most += (int64_t)r->max_pages * r->page_rows;
   }
   if (most > kMostRows) return DS4A_ERR_INVALID_ARG;
-  // Other units still read q, and the merge the plan, when a unit's output is written.
+  // Other units still read q and the rows, and the merge the plan, when a unit's output is written.
   const Span out[3] = {span(X->o, n_tok, X->o_tok_stride, (int64_t)DS4A_HEADS * DS4A_ROW_BYTES),
                        span(X->lse, n_tok, 4 * DS4A_HEADS, 4 * DS4A_HEADS),
                        span(workspace, 1, 0, (int64_t)ds4a_attn_tree_paged_workspace_size(n_seq, n_tok))};
-  const Span in[4] = {span(X->q, n_tok, X->q_tok_stride, (int64_t)DS4A_HEADS * DS4A_ROW_BYTES),
-                      ints(X->first, (int64_t)n_seq + 1), ints(X->parent, n_tok), ints(seq_geom, 4LL * n_seq)};
-  if (!apart(out, 3, in, 4)) return DS4A_ERR_INVALID_ARG;
+  Span in[4 + 2 * kSegSpans] = {span(X->q, n_tok, X->q_tok_stride, (int64_t)DS4A_HEADS * DS4A_ROW_BYTES),
+                                ints(X->first, (int64_t)n_seq + 1), ints(X->parent, n_tok), ints(seq_geom, 4LL * n_seq)};
+  int n_in = 4;
+  for (const ds4a_paged_rows *r : {&X->raw, &X->comp})
+    if (has_rows(r)) n_in += seg_spans(r, n_seq, in + n_in);
+  if (!apart(out, 3, in, n_in)) return DS4A_ERR_INVALID_ARG;
   // Tiles of 256 rows, of pairs of tokens.
   if ((((int64_t)n_tok + n_seq) / 2 + 1) * ((most + 255) / 256 + 1) > (1 << 30)) return DS4A_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256) ||

@@ -121,6 +121,36 @@ def test_tree_arguments_are_checked(lib):
         assert tree(lib, **bad) == ds4a.ERR_WORKSPACE, bad
 
 
+@needs_no_gpu
+def test_tree_outputs_apart_from_the_rows(lib):
+    """o, lse and the workspace against pools, scales and tables of both segments; a segment without rows has none."""
+    need = lib.ds4a_attn_tree_paged_workspace_size(3, 20)
+    far = {n: (72 + i) << 30 for i, n in enumerate(("k", "v", "k_scale", "v_scale", "table"))}
+    for which in ("raw", "comp"):
+        for f8 in (False, True):
+            row = 512 if f8 else 1024
+            kw = dict(far, row_stride=row, page_stride=16 * row)
+            if not f8:
+                kw.update(k_scale=None, v_scale=None)
+            other = dict(raw=seg(max_pages=0, k=None), comp=seg(max_pages=0, k=None))
+            rows = dict(other, **{which: seg(**kw)})
+            assert passes(tree(lib, **rows))
+            ends = dict(k=8 * 16 * row, v=8 * 16 * row, k_scale=8 * 64, v_scale=8 * 64, table=2 * 32 + 32)
+            for name, size in ends.items():
+                if kw[name] is None:
+                    continue
+                at = kw[name]
+                for bad in (dict(o=at + size - 16), dict(o=at - 20 * 65536 + 16), dict(lse=at + size - 4),
+                            dict(lse=at - 20 * 256 + 4), dict(ws=at), dict(ws=at - (need - 1) // 256 * 256)):
+                    assert tree(lib, **rows, **bad) == ds4a.ERR_INVALID_ARG, (which, name, bad)
+                for good in (dict(o=at + (size + 15) // 16 * 16), dict(o=at - 20 * 65536), dict(lse=at + size),
+                             dict(lse=at - 20 * 256), dict(ws=at + (size + 255) // 256 * 256)):
+                    assert passes(tree(lib, **rows, **good)), (which, name, good)
+            if which == "raw":
+                empty = dict(raw=seg(max_pages=0, **{k: v for k, v in kw.items()}), comp=other["comp"])
+                assert passes(tree(lib, **empty, o=far["k"], lse=far["v"]))
+
+
 # ------------------------------------------------------------------ binding
 
 def i32(*shape):
