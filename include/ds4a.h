@@ -725,7 +725,7 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
  * No two of these ranges may overlap, but have, want and drop one another.
  *   workspace    256-byte aligned, at least ds4a_page_tables_workspace_size()
  *                bytes; need not be initialised; not shared by calls in flight
- *                at the same time.
+ *                at the same time; overlaps none of these ranges.
  * All results are whole numbers and exact.  n_seq == 0 does nothing.
  */
 typedef struct {

@@ -450,9 +450,11 @@ ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *work
                        ints(X->n_short, 1)};
   const Span in[3] = {ints(X->have, n_seq), ints(X->want, n_seq), ints(X->drop, n_seq)};
   if (!apart(out, 6, in, 3)) return DS4A_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned(workspace, 256) ||
-      workspace_bytes < ds4a_page_tables_workspace_size(n_seq))
-    return DS4A_ERR_WORKSPACE;
+  const int64_t need = (int64_t)ds4a_page_tables_workspace_size(n_seq);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < (size_t)need) return DS4A_ERR_WORKSPACE;
+  // The second kernel reads the counts again, and the plan that the first left.
+  const Span ws = span(workspace, 1, 0, need);
+  if (!apart(&ws, 1, in, 3) || !apart(&ws, 1, out, 6)) return DS4A_ERR_INVALID_ARG;
   HostDevice d;
   const ds4a_status st = ds4a::host_device(&d);
   if (st != DS4A_OK) return st;

@@ -45,6 +45,20 @@ def test_page_tables_arguments_are_checked(lib):
         assert pages(lib, **bad) == ds4a.ERR_WORKSPACE, bad
 
 
+@needs_no_gpu
+def test_page_tables_workspace_apart_from_the_lists(lib):
+    need = lib.ds4a_page_tables_workspace_size(3)
+    base = lists(drop=9 * AT)
+    sizes = dict(table=2 * 32 + 32, free_pages=400, n_free=4, have=12, want=12, drop=12, slots=200, first=16, n_short=4)
+    for name, size in sizes.items():
+        at = getattr(base, name)
+        assert pages(lib, drop=9 * AT, ws=at) == ds4a.ERR_INVALID_ARG, name
+        assert passes(pages(lib, drop=9 * AT, ws=at + (size + 255) // 256 * 256)), name
+        assert passes(pages(lib, drop=9 * AT, ws=at - 256)), name  # (64 bytes are used)
+        assert pages(lib, **dict(dict(drop=9 * AT), **{name: (1 << 30) + need - 4})) == ds4a.ERR_INVALID_ARG, name
+        assert passes(pages(lib, **dict(dict(drop=9 * AT), **{name: (1 << 30) + need}))), name
+
+
 def accept(lib, n=3, n_tok=20, first=AT, parent=2 * AT, token=3 * AT, target=4 * AT, prev=5 * AT, path=6 * AT, stride=40,
            width=10, count=7 * AT, nxt=8 * AT):
     return elsewhere(lib.ds4a_tree_accept, n, n_tok, first, parent, token, target, prev, path, stride, width, count, nxt,
