@@ -23,6 +23,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "li
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = range(6)
 BLOCK_ROWS = 32
 ROW_BYTES = 1024
+TREE_TOKENS = 128  # nodes of a tree that attn_tree_paged looks at
 
 
 class Ds4aError(RuntimeError):
@@ -1278,12 +1279,18 @@ def tree_accept(first, token, target, *, parent=None, prev=None, width=None, pat
     hold ``token`` int32 [n_tok], ``target`` is what the model chose after each,
     ``parent`` (None: chains) counts within the sequence, ``prev`` int32 [B] is
     what it chose after the cached rows.  Returns (path int32 [B, width], -1
-    behind it; n_accepted int32 [B]; next_token int32 [B])."""
+    behind it; n_accepted int32 [B]; next_token int32 [B]).  ``width`` bounds a
+    path: the most nodes of a sequence is enough.  Without it a tree's has 128
+    (``TREE_TOKENS``: nodes behind them see nothing), and a chain's all
+    ``n_tok``, which only the caller of few sequences wants: each row of ``path`` is
+    written whole."""
     import torch
     B, dev = first.shape[0] - 1, first.device
     if path is None:
-        path = _new(stream, torch.empty, (B, int(token.shape[0] if width is None else width)), dtype=torch.int32,
-                    device=dev)
+        n = token.shape[0]
+        if width is None:
+            width = n if parent is None else min(n, TREE_TOKENS)
+        path = _new(stream, torch.empty, (B, int(width)), dtype=torch.int32, device=dev)
     if n_accepted is None:
         n_accepted = _new(stream, torch.empty, (B,), dtype=torch.int32, device=dev)
     if next_token is None:

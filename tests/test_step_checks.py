@@ -216,6 +216,16 @@ def test_whole_numbers_of_the_wrong_kind_are_refused(name, bad, monkeypatch):
     raises(match, ds4a.prepare_page_tables, **dict(good, **{name: bad}))
 
 
+@pytest.mark.parametrize("n,tree,width,cols", [(5, True, None, 5), (32768, True, None, 128), (32768, False, None, 32768),
+                                               (32768, True, 64, 64), (32768, False, 7, 7), (0, True, None, 0)])
+def test_accept_makes_a_path_as_wide_as_a_tree(monkeypatch, n, tree, width, cols):
+    """Not of all sequences' nodes: 512 trees of 64 would write 64 MB."""
+    made = []
+    monkeypatch.setattr(ds4a, "prepare_tree_accept", lambda *a, path, **kw: made.append(path) or (lambda: None))
+    path, count, _ = ds4a.tree_accept(i32(513), i32(n), i32(n), parent=i32(n) if tree else None, width=width)
+    assert made[0] is path and path.shape == (512, cols) and count.shape == (512,)
+
+
 # ------------------------------------------------------------------ the oracle by hand
 
 def test_page_tables_by_hand():
