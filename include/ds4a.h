@@ -690,8 +690,11 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
  * first[b + 1] - 1 of n_tok (device int32 [n_seq + 1], ascending; clamped to
  * 0 .. n_tok).  The calls of a step, in order: ds4a_page_tables (room for the new
  * rows, and their slots), ds4a_append_paged, ds4a_attn_tree_paged,
- * ds4a_tree_accept, ds4a_commit_paged, ds4a_page_tables (gives back).  The
- * sources define no such step: the readings are the library's own.
+ * ds4a_tree_accept, ds4a_commit_paged, ds4a_page_tables (gives back).  None of
+ * them adds compressed rows: ds4a_compress_append pools those of the accepted tokens
+ * and ds4a_append_paged puts them into their slots, after the step (or before it, see
+ * ds4a_attn_tree_paged), and n_comp counts them from then on.  The sources define
+ * no such step: the readings are the library's own.
  */
 
 /*
@@ -711,7 +714,11 @@ ds4a_status ds4a_append_paged(const ds4a_paged_rows *rows, int32_t n, const void
  *   Slots: the new rows have .. want-1 of all sequences, packed: row j of
  *   sequence b's is slots[first[b] + j] = page * page_rows + row in page, or -1
  *   where it has no page; slots from first[n_seq] on are -1 (a padded batch).
- *   New rows beyond n_slots get no slot, and first is clamped to n_slots.
+ *   New rows beyond n_slots get no slot, and first is clamped to n_slots (0: to
+ *   0).  Nothing reports that: a caller that hands first on to the other calls gives
+ *   as many slots as all sequences have new rows, and one that packs tokens by
+ *   ranges of its own wants no more rows than the table holds, because slots are
+ *   packed by the clamped counts.
  *   X->table     device int32 [n_seq][max_pages], at table_stride bytes
  *                (a multiple of 4, >= 4 * max_pages), read and written.
  *   page_rows, n_pages  of the pool; page_rows * max_pages <= 2^30 and
@@ -756,6 +763,15 @@ ds4a_status ds4a_page_tables(int32_t n_seq, const ds4a_page_lists *X, void *work
  *   - compressed row c < n_comp when (c + 1) * ratio <= p + 1.
  * Rows of absent pages, and raw rows behind the table, are left out.  A token
  * that sees no row gets o = 0 and lse = -inf.
+ * This is what decoding token by token gives (ds4a_attn_decode_paged at position
+ * p, its own row counted among the raw ones) while n_comp counts the spans that
+ * have ended on the token's path: (p + 1) / ratio <= n_comp.  The rows of spans that
+ * new tokens end are in the cache only where the caller has put them there: those
+ * of a run, or of the part of a tree that all deeper nodes descend from, may be
+ * appended and counted in n_comp before the call, and tokens see them from the
+ * span's last position on.  A span that ends on one branch of a tree has no row:
+ * nodes from there on see fewer compressed rows than decode would, and the model's
+ * choice after them may be another.  Where that matters, trees end before it.
  *   n_tok       tokens of all sequences; those that first gives to no sequence
  *               keep what o and lse held.
  *   shape, seq_geom  as in ds4a_attn_decode_paged; q_pos is the position of a

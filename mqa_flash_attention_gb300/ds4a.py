@@ -1197,7 +1197,8 @@ def page_tables(table, free_pages, n_free, have, want, page_rows, *, drop=None, 
     first ``drop`` rows leave the ``table`` int32 [B, max_pages].  All four are
     updated in place.  Returns (slots, first, n_short): the slots of the new
     rows, packed, -1 behind them (``n_slots`` of them when made here); where each
-    sequence's begin, int32 [B + 1]; how many pages were lacking, int32 [1]."""
+    sequence's begin, int32 [B + 1], clamped to the number of slots (so to 0 without
+    them); how many pages were lacking, int32 [1]."""
     import torch
     dev = table.device
     if slots is None:  # (filled: a call without sequences writes nothing)
@@ -1249,7 +1250,11 @@ def attn_tree_paged(shape, seq_geom, first, q, raw, comp=None, *, parent=None, w
     (int32 [B + 1]); ``parent`` int32 [n_tok] within the sequence, negative for
     a root, or None: runs of tokens, causal.  Token t's own row is raw row
     ``n_raw + t``; seq_geom int32 [B, 4]: (position of the first new token,
-    cached raw rows, raw_pos0, n_comp)."""
+    cached raw rows, raw_pos0, n_comp).  Compressed rows that new tokens complete
+    are seen only if they were appended and counted before the call, which a
+    tree's branches cannot have: nodes whose path ends a span beyond ``n_comp``
+    see fewer rows than token-by-token decode would.  Tokens of no sequence
+    keep what ``out`` and ``lse`` held (anything, when made here)."""
     out, lse = _outputs(q, out, lse, want_lse, stream)
     prepare_tree_paged(shape, seq_geom, first, q, raw, comp, parent=parent, workspace=workspace, out=out, lse=lse,
                        stream=stream)()

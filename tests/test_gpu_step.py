@@ -9,8 +9,8 @@ import re
 import numpy as np
 import pytest
 
-from oracle import fp8, paged, step
-from test_gpu_paged import (check_decode, device_error_word_stays_clear, ds4a, host, poison, rows_on, shape_of,  # noqa: F401
+from oracle import compressor, fp8, paged, step
+from test_gpu_paged import (F16, check_decode, device_error_word_stays_clear, ds4a, host, poison, rows_on, shape_of,  # noqa: F401
                             torch, up)
 from test_paged_oracle import make
 
@@ -760,6 +760,109 @@ def test_the_documented_step_of_drafted_tokens(torch, ds4a):
         assert np.array_equal(host(names["geom"]), geom) and np.array_equal(host(r.table), raw["table"])
         assert int(names["n_free"]) == n_free and host(names["next_token"]).tolist() == nxt
         names["prev"] = names["next_token"]
+
+
+def test_the_documented_step_on_a_layer_with_compressed_rows(torch, ds4a):
+    """The README's three blocks as they stand, until the windows have left their first pages and dozens of spans
+    have ended: every node's result is that of decoding token by token along its path."""
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        before, block, behind = re.findall(r"```py(?:thon3)?\n(.*?)```", f.read(), re.S)
+    rng = np.random.default_rng(72)
+    n, page, n_pages, ratio, start = 2, 64, 11, 4, [21, 8]
+    shape = shape_of(ratio)
+    pos = np.array(start)
+    i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    comp = make(rng, n, [300, 300], page, False, True)
+    comp["k"][:] = 0
+    raw = make(rng, 1, [n_pages * page], page, False, True)
+    raw["table"] = np.full((n, 4), -1, dtype=np.int32)
+    r, c = rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp)
+    # What stands in the caches: positions from 0 on, in the state those of the span in progress.
+    rows = [rng.standard_normal((int(x), D)).astype(np.float16) for x in pos]  # K = V of every position
+    kvs, scores = ([rng.standard_normal((int(x), D)).astype(np.float32) for x in pos] for _ in range(2))
+    geom = np.array([(x, x, 0, x // ratio) for x in pos], dtype=np.int32)
+    free = rng.permutation(n_pages).tolist()
+    for b in range(n):
+        raw["table"][b, 0] = free.pop()
+        raw["k"][raw["table"][b, 0], :pos[b]] = rows[b]
+        pooled = compressor.pool(kvs[b][:pos[b] // ratio * ratio], scores[b][:pos[b] // ratio * ratio], ratio)
+        comp["k"][comp["table"][b, 0], :len(pooled)] = pooled
+    for seg, dev in ((raw, r), (comp, c)):
+        dev.k.copy_(up(torch, seg["k"]))
+    r.table.copy_(up(torch, raw["table"]))
+    state = torch.zeros((2, n, ratio - 1, D), device="cuda")
+    for b in range(n):
+        for s, x in zip(state, (kvs, scores)):
+            if pos[b] % ratio:
+                s[b, :pos[b] % ratio] = up(torch, x[b][pos[b] // ratio * ratio:])
+    names = dict(torch=torch, ds4a=ds4a, n_seq=n, geom=i32(geom), raw_table=r.table, raw=r, comp=c, comp_table=c.table,
+                 free_pages=i32(free + [-1] * (n_pages - len(free))), n_free=i32([len(free)]), shape=shape,
+                 prev=i32(rng.integers(0, 2, n)), state_kv=state[0], state_score=state[1],
+                 n_state=[int(x) % ratio for x in pos])
+    compared = 0
+    for turn in range(200):
+        # Trees of one root that end with the span: up to two more nodes in a generation.
+        prev, parents, tokens, depths = host(names["prev"]), [], [], []
+        for b in range(n):
+            parent, depth = [-1], [0]
+            for d in range(1, ratio - (int(pos[b]) + 1) % ratio):
+                above = [t for t, x in enumerate(depth) if x == d - 1]
+                for _ in range(int(rng.integers(1, 3))):
+                    parent.append(int(rng.choice(above)))
+                    depth.append(d)
+            parents.append(parent)
+            depths.append(depth)
+            tokens.append([int(prev[b])] + rng.integers(0, 2, len(parent) - 1).tolist())
+        counts = [len(x) for x in parents]
+        T, first = sum(counts), np.concatenate([[0], np.cumsum(counts)])
+        target = rng.integers(0, 2, T)
+        q, k = rng.standard_normal((T, H, D)).astype(np.float16), rng.standard_normal((T, D)).astype(np.float16)
+        kv, score = (rng.standard_normal((T, D)).astype(np.float32) for _ in range(2))
+        names.update(first=i32(first), n_new=i32(counts), parent=i32(np.concatenate(parents)), q=up(torch, q),
+                     token=i32(np.concatenate(tokens)), new_k=up(torch, k), kv=up(torch, kv), score=up(torch, score),
+                     choose=lambda o, t=target: i32(t))
+        exec(before, names)
+        exec(block, names)
+        path, taken = host(names["path"]), host(names["n_accepted"])
+        paths, nxt = step.accept(first, np.concatenate(parents), np.concatenate(tokens), target, prev, 128)
+        assert [path[b, :taken[b]].tolist() for b in range(n)] == paths and (taken >= 1).all()
+        assert host(names["next_token"]).tolist() == nxt and int(names["n_short"]) == 0
+        if turn % 8 == 0 or turn > 190:
+            cache, c_table = host(c.k), host(c.table)
+            for b in range(n):
+                ways = []
+                for t, u in enumerate(parents[b]):
+                    ways.append((ways[u] if u >= 0 else []) + [t])
+                    at = first[b] + t
+                    seq_rows = np.concatenate([rows[b], k[first[b] + np.array(ways[t])]])
+                    p, ended = len(seq_rows) - 1, len(seq_rows) // ratio
+                    pooled = cache[c_table[b, np.arange(ended) // page], np.arange(ended) % page]
+                    segs = []
+                    for x in (seq_rows, pooled):
+                        x = np.concatenate([x, np.zeros((-len(x) % page, D), dtype=np.float16)]).reshape(-1, page, D)
+                        segs.append(dict(k=x, v=x, table=np.arange(len(x), dtype=np.int32)[None]))
+                    want = paged.decode(shape, [(p, len(seq_rows), 0, ended)], q[at:at + 1], *segs)
+                    check_decode(host(names["o"])[at:at + 1], None, want, [min(128, p + 1) + ended])
+                    compared += 1
+        exec(behind, names)
+        for b in range(n):
+            took = first[b] + np.array(paths[b])
+            rows[b], kvs[b], scores[b] = (np.concatenate([x, y[took]]) for x, y in
+                                          ((rows[b], k), (kvs[b], kv), (scores[b], score)))
+        pos = pos + taken
+        g = host(names["geom"])
+        assert g[:, 0].tolist() == pos.tolist() and (g[:, 1] + g[:, 2] == pos).all() and (g[:, 3] == pos // ratio).all()
+        names["prev"] = names["next_token"]
+    assert compared > 100 and (host(names["geom"])[:, 2] >= page).all()
+    assert int(names["n_free"]) == n_pages - sum(-(-int(x) // page) for x in host(names["geom"])[:, 1])
+    # The compressed rows, by the compressor's definition.  (Weights from scores up to 10 apart: an exponent is off by
+    # 10 log2(e) 2^-24, a weight and a quotient by another 2^-22 each: under 2^-18 of the span's largest row; then fp16.)
+    for b in range(n):
+        ended = pos[b] // ratio
+        got = host(c.k)[c_table[b, np.arange(ended) // page], np.arange(ended) % page].astype(np.float64)
+        most = np.abs(kvs[b][:ended * ratio]).reshape(ended, ratio, D).max(1)
+        want = compressor.pool(kvs[b][:ended * ratio], scores[b][:ended * ratio], ratio)
+        assert (np.abs(got - want) <= F16 * np.abs(want) + 2.0 ** -18 * most + 2.0 ** -25).all()
 
 
 def test_steps_on_two_streams_at_once(torch, ds4a):

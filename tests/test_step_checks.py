@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from mqa_flash_attention_gb300 import ds4a
-from oracle import step
+from oracle import paged, step
 from test_paged_checks import AT, I32, SHAPE, elsewhere, lib, needs_no_gpu, passes, raises, seg  # noqa: F401
 
 
@@ -255,3 +255,64 @@ def test_seen_by_hand():
     shape = dict(window=3, ratio=2, scale=1.0)
     got = step.seen(shape, (6, 2, 4, 9), np.array([-1, 0, 0, 2]), 0, 4, 100, 100)
     assert got == [([0, 1, 2], [0, 1, 2]), ([1, 2, 3], [0, 1, 2, 3]), ([1, 2, 4], [0, 1, 2, 3]), ([2, 4, 5], [0, 1, 2, 3])]
+
+
+def whole_history(rng, n_rows, n_spans):
+    """Rows of one sequence from position 0 on, in pages, and its compressed rows."""
+    def rows(n):
+        k = rng.standard_normal((-(-n // 8), 8, 512)).astype(np.float16)
+        return dict(k=k, v=k, table=np.arange(len(k), dtype=np.int32)[None])
+    return rows(n_rows), rows(n_spans)
+
+
+def decoded(shape, raw, comp, q, p, path, n_raw):
+    """Token-by-token decode at position p: the cached rows 0 .. n_raw - 1, then those of ``path``, and every
+    compressed row whose span has ended."""
+    at = list(range(n_raw)) + [n_raw + t for t in path]
+    k = raw["k"].reshape(-1, 512)[at]
+    k = np.concatenate([k, np.zeros((-len(k) % 8, 512), dtype=np.float16)]).reshape(-1, 8, 512)
+    own = dict(k=k, v=k, table=np.arange(len(k), dtype=np.int32)[None])
+    o, lse, *_ = paged.decode(shape, [(p, len(at), 0, 1 << 20)], q[None], own, comp)
+    return o[0], lse[0]
+
+
+@pytest.mark.parametrize("ratio,pos", [(4, 11), (4, 12), (2, 9), (16, 40)])
+def test_a_run_is_decode_token_by_token(ratio, pos):
+    """With the compressed rows of its own tokens in the cache and counted."""
+    rng = np.random.default_rng(ratio)
+    n, shape = 13, dict(ratio=ratio, window=9, scale=1 / math.sqrt(512))
+    raw, comp = whole_history(rng, pos + n, (pos + n) // ratio)
+    q = rng.standard_normal((n, 64, 512)).astype(np.float16)
+    o, lse, *_ = step.attention(shape, [(pos, pos, 0, (pos + n) // ratio)], [0, n], None, q, raw, comp)
+    for t in range(n):
+        want = decoded(shape, raw, comp, q[t], pos + t, range(t + 1), pos)
+        assert np.allclose(o[t], want[0], rtol=0, atol=1e-12) and np.allclose(lse[t], want[1], rtol=0, atol=1e-12)
+
+
+@pytest.mark.parametrize("pos", [8, 9, 10, 11])
+def test_a_tree_is_decode_until_a_span_ends_on_a_branch(pos):
+    """A root, two branches of three: equal to decode along each node's path while n_comp counts the spans that
+    have ended on it (the root's row may have been appended), and short of the branch's compressed row behind that."""
+    rng = np.random.default_rng(pos)
+    ratio, parent = 4, np.array([-1, 0, 0, 1, 2, 3, 4])
+    paths = [[0], [0, 1], [0, 2], [0, 1, 3], [0, 2, 4], [0, 1, 3, 5], [0, 2, 4, 6]]
+    shape = dict(ratio=ratio, window=128, scale=1 / math.sqrt(512))
+    raw, comp = whole_history(rng, pos + 7, 8)  # (branches' rows differ: those of one of them)
+    n_comp = (pos + 1) // ratio                 # the root's among them
+    q = rng.standard_normal((7, 64, 512)).astype(np.float16)
+    o, lse, *_ = step.attention(shape, [(pos, pos, 0, n_comp)], [0, 7], parent, q, raw, comp)
+    same = 0
+    for t, path in enumerate(paths):
+        p = pos + len(path) - 1
+        want = decoded(shape, raw, comp, q[t], p, path, pos)
+        equal = np.allclose(o[t], want[0], rtol=0, atol=1e-12) and np.allclose(lse[t], want[1], rtol=0, atol=1e-12)
+        assert equal == ((p + 1) // ratio <= n_comp)
+        same += equal
+    assert same == {8: 5, 9: 3, 10: 1, 11: 7}[pos]
+
+
+def test_the_header_names_a_tree_s_tokens():
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(__file__), "..", "include", "ds4a.h")) as f:
+        assert re.search(r"#define DS4A_TREE_TOKENS (\d+)", f.read()).group(1) == str(ds4a.TREE_TOKENS)
