@@ -561,6 +561,37 @@ def test_tree_units_of_a_single_tile(torch, ds4a, f8):
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
 
 
+def test_tree_of_more_sequences_than_a_plan_holds(torch, ds4a):
+    """1,300 trees: where units begin is kept in the workspace, and units are counted in several rounds."""
+    rng = np.random.default_rng(35)
+    counts = [int(x) for x in rng.integers(0, 5, 1300)]
+    rows = [int(x) for x in rng.integers(0, 9, 1300)]
+    geom, first, parent, q, raw, comp = tree_case(rng, counts, rows, 4, 8, window=6)
+    assert sum((n + 1) // 2 for n in counts) > 1024
+    want = step.attention(shape_of(4, 6), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(4, 6), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_of_more_units_than_blocks_have_threads(torch, ds4a, chain):
+    """66,000 tokens in 33,000 pairs, over 1,024 to a block of the plan: 600 sequences alike, whose results have the same
+    bits, since a pair's rows are one tile that no border cuts."""
+    rng = np.random.default_rng(36)
+    n_seq, n = 600, 110
+    geom, _, parent, q, raw, comp = tree_case(rng, [n], [9], 4, 16, window=24, chain=chain)
+    want = step.attention(shape_of(4, 24), geom, [0, n], parent, q, raw, comp)
+    assert n_seq * (n // 2) > 32 * 1024 and want[4].max() + n < 256
+    for seg in (raw, comp):
+        seg["table"] = np.repeat(seg["table"], n_seq, axis=0)
+    i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    o, lse = ds4a.attn_tree_paged(shape_of(4, 24), i32(geom * n_seq), i32(np.arange(n_seq + 1) * n),
+                                  up(torch, q).repeat(n_seq, 1, 1), rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp),
+                                  parent=None if chain else i32(np.tile(parent, n_seq)), want_lse=True)
+    check_tree(host(o[:n]), host(lse[:n]), want)
+    assert all(torch.equal(o[i:i + n], o[:n]) and torch.equal(lse[i:i + n], lse[:n]) for i in range(0, n_seq * n, n))
+
+
 def test_tree_of_single_tokens_is_the_decode(torch, ds4a):
     """One new token per sequence: the decode's result, its own row counted among the raw ones."""
     rng = np.random.default_rng(30)
@@ -892,6 +923,61 @@ def test_steps_on_two_streams_at_once(torch, ds4a):
         assert host(outs[k][3]).tolist() == [len(p) for p in j["paths"][0]] and host(outs[k][4]).tolist() == j["paths"][1]
         for again in outs[k + 2::2]:
             assert all(torch.equal(a, b) for a, b in zip(again, outs[k]))
+
+
+def test_all_calls_of_the_step_on_two_streams_at_once(torch, ds4a):
+    """Page tables, attention, acceptance and commits in flight on two streams, each job with pools, tables and lists
+    of its own, outputs and workspaces made by the calls: every round's results, and what all rounds leave behind."""
+    rng = np.random.default_rng(73)
+    i32 = lambda a: up(torch, np.asarray(a, dtype=np.int32))  # noqa: E731
+    rounds, jobs = 8, []
+    for k in range(2):
+        counts = [9 + k, 30, 2]
+        geom, first, parent, q, raw, comp = tree_case(rng, counts, [600, 300 + k, 5], 4, 16, bool(k), True)
+        if k:
+            raw["k_scale"][np.isnan(raw["k_scale"])] = 3.0  # (to be compared; of rows that nobody sees)
+        token, target = rng.integers(0, 2, len(q)), rng.integers(0, 2, len(q))
+        prev = token[first[:-1]]
+        have, want, _, table, free, n_free, n_pages = page_case(rng, 40 + k, 16, 90, 60, False, 150)
+        jobs.append(dict(
+            host=dict(geom=geom, first=first, parent=parent, q=q, raw=raw, comp=comp, have=have, want=want, table=table,
+                      free=free.tolist(), n_free=n_free, n_pages=n_pages, slots=int(np.maximum(want - have, 0).sum()),
+                      paths=step.accept(first, parent, token, target, prev, 128)),
+            geom=i32(geom), first=i32(first), parent=i32(parent), q=up(torch, q), raw=rows_on(torch, ds4a, raw),
+            comp=rows_on(torch, ds4a, comp), token=i32(token), target=i32(target), prev=i32(prev), have=i32(have),
+            want=i32(want), table=i32(table), free=i32(free), n_free=i32([n_free]), stream=torch.cuda.Stream()))
+    assert any(len(p) > 2 for j in jobs for p in j["host"]["paths"][0])
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(rounds):
+        for j, out in zip(jobs, outs):
+            s, h = j["stream"], j["host"]
+            there = ds4a.page_tables(j["table"], j["free"], j["n_free"], j["have"], j["want"], 16, n_slots=h["slots"],
+                                     stream=s)
+            o = ds4a.attn_tree_paged(shape_of(4), j["geom"], j["first"], j["q"], j["raw"], j["comp"], parent=j["parent"],
+                                     stream=s)
+            taken = ds4a.tree_accept(j["first"], j["token"], j["target"], parent=j["parent"], prev=j["prev"], stream=s)
+            ds4a.commit_paged(j["raw"], j["geom"], taken[0], taken[1], stream=s)
+            ds4a.page_tables(j["table"], j["free"], j["n_free"], j["want"], j["have"], 16, stream=s)
+            out.append((there, o, taken))
+    torch.cuda.synchronize()
+    for j, out in zip(jobs, outs):
+        h = j["host"]
+        for i, (there, o, taken) in enumerate(out):
+            h["n_free"], slots, first, short = step.page_tables(h["table"], h["free"], h["n_free"], h["have"], h["want"], None,
+                                                                16, h["n_pages"], h["slots"])
+            assert np.array_equal(host(there[0]), slots) and np.array_equal(host(there[1]), first) and int(there[2]) == short
+            if i in (0, rounds - 1):
+                want = step.attention(shape_of(4), h["geom"], h["first"], h["parent"], h["q"], h["raw"], h["comp"])
+                check_tree(host(o), None, want)
+            paths, nxt = h["paths"]
+            assert [p[:n] for p, n in zip(host(taken[0]).tolist(), host(taken[1]).tolist())] == paths
+            assert (host(taken[0]) >= 0).sum() == sum(map(len, paths)) and host(taken[2]).tolist() == nxt
+            step.commit(h["raw"], h["geom"], paths)
+            h["n_free"], *_ = step.page_tables(h["table"], h["free"], h["n_free"], h["want"], h["have"], None, 16, h["n_pages"], 0)
+        same_pool(j["raw"], h["raw"])
+        assert np.array_equal(host(j["table"]), h["table"]) and np.array_equal(host(j["free"]), h["free"])
+        assert int(j["n_free"]) == h["n_free"]
 
 
 def test_step_calls_of_empty_batches(torch, ds4a):
