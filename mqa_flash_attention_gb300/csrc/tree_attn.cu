@@ -12,8 +12,9 @@
 // reads 6 KB of operands from shared memory for 48 cycles' work that the tensor
 // core could do in 32: shared memory bounds it, and the rows have to come in for
 // each token anew.  Two CTAs of a cluster hold a token each and run every product
-// as one MMA of M = 128 (2 x 64 heads) and N = 256 at the full rate (64 cycles of
-// 8192 multiply-adds per SM; measured), each SM bringing half of the rows' operand:
+// as one MMA of M = 128 (2 x 64 heads) and N = 256 at the full rate (64 cycles for 16
+// dims, 4096 multiply-adds per SM and cycle; measured), each SM bringing half of the
+// rows' operand:
 //   S[2 x 64 heads][256 rows]  = Q . K_tile^T     a CTA has rows 128c .. 128c+127 of K
 //   O[2 x 64 heads][512 dims] += P . V_tile       and dims 128c .. +127 of each 256 of V
 // so a row's K and V enter each SM half, and serve two tokens.  In such an MMA a CTA
@@ -34,7 +35,9 @@
 // 16 rows, TMA brings K by grains and V by the grains of which every row is seen (in
 // runs of up to 64 rows where a tile is seen in full); other rows of V, and all rows
 // of other page sizes, are copied one by one, zeros in place of those that neither
-// token sees.  What one of the two sees is masked for the other.
+// token sees.  What one of the two sees is masked for the other.  (Where the pages of
+// either segment are no multiple of 8 rows, all rows of both are copied one by one: 2.2 to
+// 2.7 times as long for trees and short lists, 3.3 times for 2,048 tokens over 7,680 rows.)
 //
 // What bounds it (GB300; the rates are this card's own, a cuBLAS product of bf16 at
 // 1,878 TFLOP/s, at 1,702 where it runs for seconds under the power cap).  2,048 new
@@ -1157,8 +1160,10 @@ __device__ __forceinline__ void tree_softmax_role(const TreeAttnParams &p, int n
       moved = true;
       lsum *= alpha;
     }
-    // This head's 64 weights, rounded once to fp16 for the product; the sums add them
-    // unrounded, sixteen at a time, so that lse keeps fp32 precision over long rows.
+    // This head's 64 weights, rounded once to fp16, V's type, because both operands of a
+    // product have one (2^-11 of each at most: outputs are 2.3e-4 to 2.9e-4 from those in 64
+    // bits, 2.1e-4 of it their own rounding); the sums add them unrounded, sixteen at a
+    // time, so that lse keeps fp32 precision over long rows.
     uint32_t weights[32];
     float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
