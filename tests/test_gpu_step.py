@@ -344,6 +344,20 @@ def test_tree_strides_and_untouched_tokens(torch, ds4a, f8):
     assert (host(big_o)[n:] == 7).all() and (host(big_o)[:, H * D:] == 7).all() and (host(lse)[n:] == 5).all()
 
 
+@pytest.mark.parametrize("raw_page,comp_page", [(8, 64), (64, 8), (16, 24), (256, 16), (7, 64), (64, 7), (40, 128), (1, 1)])
+@pytest.mark.parametrize("f8", [False, True])
+def test_tree_pages_of_two_sizes(torch, ds4a, raw_page, comp_page, f8):
+    """Raw and compressed rows in pages of sizes of their own; K and V one pool in one segment and two in the other."""
+    rng = np.random.default_rng(raw_page + comp_page)
+    geom, first, parent, q, raw, _ = tree_case(rng, [5, 40, 1], [530, 70, 0], 4, raw_page, f8, True)
+    counts = [g[3] for g in geom]
+    comp = make(rng, 3, counts, comp_page, f8, False)
+    poison(comp, counts)
+    want = step.attention(shape_of(4), geom, first, parent, q, raw, comp)
+    got = run_tree(torch, ds4a, shape_of(4), geom, first, parent, q, rows_on(torch, ds4a, raw), rows_on(torch, ds4a, comp))
+    check_tree(*got, want)
+
+
 def test_tree_of_more_nodes_than_are_seen(torch, ds4a):
     """Nodes behind the 128th see no row; a chain of as many does."""
     rng = np.random.default_rng(23)
@@ -793,12 +807,17 @@ def test_the_documented_step_of_drafted_tokens(torch, ds4a):
         names["prev"] = names["next_token"]
 
 
-def test_the_documented_step_on_a_layer_with_compressed_rows(torch, ds4a):
+@pytest.mark.parametrize("runs", [False, True])
+def test_the_documented_step_on_a_layer_with_compressed_rows(torch, ds4a, runs):
     """The README's three blocks as they stand, until the windows have left their first pages and dozens of spans
-    have ended: every node's result is that of decoding token by token along its path."""
+    have ended: every node's result is that of decoding token by token along its path.  Or runs of drafts, as the text
+    behind them says: the compressed rows of all their tokens first, and taken back to those of the accepted ones."""
     with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
         before, block, behind = re.findall(r"```py(?:thon3)?\n(.*?)```", f.read(), re.S)
     rng = np.random.default_rng(72)
+    if runs:
+        before, roots = before.split("\nfor b in range(n_seq):")
+        assert "append_compressed" in roots
     n, page, n_pages, ratio, start = 2, 64, 11, 4, [21, 8]
     shape = shape_of(ratio)
     pos = np.array(start)
@@ -836,9 +855,9 @@ def test_the_documented_step_on_a_layer_with_compressed_rows(torch, ds4a):
         prev, parents, tokens, depths = host(names["prev"]), [], [], []
         for b in range(n):
             parent, depth = [-1], [0]
-            for d in range(1, ratio - (int(pos[b]) + 1) % ratio):
+            for d in range(1, int(rng.integers(1, 10)) if runs else ratio - (int(pos[b]) + 1) % ratio):
                 above = [t for t, x in enumerate(depth) if x == d - 1]
-                for _ in range(int(rng.integers(1, 3))):
+                for _ in range(1 if runs else int(rng.integers(1, 3))):
                     parent.append(int(rng.choice(above)))
                     depth.append(d)
             parents.append(parent)
@@ -849,10 +868,14 @@ def test_the_documented_step_on_a_layer_with_compressed_rows(torch, ds4a):
         target = rng.integers(0, 2, T)
         q, k = rng.standard_normal((T, H, D)).astype(np.float16), rng.standard_normal((T, D)).astype(np.float16)
         kv, score = (rng.standard_normal((T, D)).astype(np.float32) for _ in range(2))
-        names.update(first=i32(first), n_new=i32(counts), parent=i32(np.concatenate(parents)), q=up(torch, q),
-                     token=i32(np.concatenate(tokens)), new_k=up(torch, k), kv=up(torch, kv), score=up(torch, score),
-                     choose=lambda o, t=target: i32(t))
+        names.update(first=i32(first), n_new=i32(counts), parent=None if runs else i32(np.concatenate(parents)),
+                     q=up(torch, q), token=i32(np.concatenate(tokens)), new_k=up(torch, k), kv=up(torch, kv),
+                     score=up(torch, score), choose=lambda o, t=target: i32(t))
+        kept = (names["geom"][:, 3].clone(), state.clone(), list(names["n_state"]))
         exec(before, names)
+        if runs:
+            for b in range(n):
+                names["append_compressed"](b, torch.arange(first[b], first[b + 1], device="cuda"))
         exec(block, names)
         path, taken = host(names["path"]), host(names["n_accepted"])
         paths, nxt = step.accept(first, np.concatenate(parents), np.concatenate(tokens), target, prev, 128)
@@ -875,7 +898,13 @@ def test_the_documented_step_on_a_layer_with_compressed_rows(torch, ds4a):
                     want = paged.decode(shape, [(p, len(seq_rows), 0, ended)], q[at:at + 1], *segs)
                     check_decode(host(names["o"])[at:at + 1], None, want, [min(128, p + 1) + ended])
                     compared += 1
-        exec(behind, names)
+        if runs:
+            names["geom"][:, 3], names["n_state"] = kept[0], kept[2]
+            state.copy_(kept[1])
+            for b in range(n):
+                names["append_compressed"](b, (names["first"][b] + names["path"][b, :taken[b]]).long())
+        else:
+            exec(behind, names)
         for b in range(n):
             took = first[b] + np.array(paths[b])
             rows[b], kvs[b], scores[b] = (np.concatenate([x, y[took]]) for x, y in
