@@ -19,10 +19,11 @@ namespace {
 // that no order of execution changes.  The list's top has to be known before the
 // first page is taken, so one CTA adds up and gives back first; taking pages,
 // closing the gap of the dropped ones and naming the slots of new rows is a CTA's
-// work for each sequence, in a second kernel because there are many.  Bounded by two launches and their round trips
-// to L2 (the bytes would take less than 1 us): 15.6 us for a call that takes 8 rows'
-// room for each of 64 sequences and one that gives it back, 31 us for two of 1,024
-// sequences of which each takes 500 rows in pages of 16.
+// work for each sequence, in a second kernel because there are many.  Bounded by
+// two launches and their round trips to L2 (the bytes would take less than 1 us):
+// 15.6 us for a call that takes 8 rows' room for each of 64 sequences and one that
+// gives it back, 31 us for two of 1,024 sequences of which each takes 500 rows in
+// pages of 16.
 
 constexpr int kListThreads = 1024;
 constexpr int kListWarps = kListThreads / 32;
